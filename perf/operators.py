@@ -275,8 +275,9 @@ def _own(st):
         kda.kda_kv_gather(st["pool"], st["fmt"], c["pt"], st["cu_out"], st["begin"], st["table"], st["k_out"],
                           st["v_out"], st["status"])
         return {"q": st["q_out"], "k": st["k_out"], "v": st["v_out"]}
-    kda.kda_attn_paged(st["pool"], st["fmt"], c["pt"], st["cu"], st["kv_len"], st["table"], st["maxq"], st["q"],
-                       st["o"], st["ws"], st["status"], window=c["window"], sinks=c["sinks"], lse=st["lse"])
+    kda.kda_attn_paged(st["pool"], c["Hkv"], st["fmt"], c["pt"], st["cu"], st["kv_len"], st["table"], st["maxq"],
+                       st["q"], st["o"], st["ws"], st["status"], window=c["window"], sinks=c["sinks"],
+                       lse=st["lse"])
     return {"o": st["o"], "lse": st["lse"]}
 
 
