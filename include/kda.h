@@ -416,6 +416,101 @@ int kda_ckpt_restore_q8(kda_pool *pool, int32_t H, int32_t d, int32_t dtype, int
                         const int32_t *ckpt_pages, const int32_t *active_pages, void *pool_base,
                         void *workspace, int64_t ws_bytes, int32_t *status_dev, void *stream);
 
+/* ---------------------------------------------------------------- key/value cache ----- */
+
+/* The other layers of a hybrid model attend over cached keys and values.  Their cache lives in
+ * the same pool of pages as the recurrent states ("Cache de préfixe hybride KDA–MLA", §La mise en
+ * page unifiée: one page size, one allocator for every kind), one page table row a sequence:
+ * table[s][b] is the page of the sequence's tokens [b * page_tokens, (b + 1) * page_tokens).
+ *
+ * A page is one block of page_tokens tokens (a multiple of 16, 16 to 128) of all Hkv heads of one
+ * layer: Hkv records in head order, each
+ *     K tile | V tile | KDA_KV_I8 only: float K scale, float V scale, 8 zero bytes
+ * A tile is page_tokens rows of d elements (bf16, or int8 codes), cut into lines of 128 bytes (64
+ * where a row has only 64): line block c holds bytes [128 c, 128 c + 128) of every row, row after
+ * row, and the 16-byte unit u of token slot t's line lies at place u ^ (t % 8) (64-byte lines:
+ * u ^ ((t / 2) % 4)).  A record is thus shared-memory ready: copied as it is, eight tokens' units
+ * of one column fall into different banks.
+ *
+ * Formats: KDA_KV_BF16, values rounded to bf16; KDA_KV_I8, value = code * scale with one scale
+ * for the keys and one for the values of each (block, head).  Appending to a block sets
+ * scale = max(max |x| over the new tokens / 127, the block's scale if it holds older tokens) and
+ * code = round-to-nearest-even(x / scale), both divisions IEEE fp32; when the scale grows, older
+ * codes c become rne(c * old scale / scale).  A block with an infinity or a NaN in it reads as NaN
+ * (that head's K or V); a scale of 0 reads as zeros.
+ *
+ * Batches: cu_q (device int32 [nseq + 1], ascending) cuts the call's T_tot packed token rows into
+ * sequences; kv_len (device int32 [nseq]) is each sequence's length in the cache with the call's
+ * own tokens in it, so that its n new tokens stand at positions kv_len - n .. kv_len - 1.  The
+ * same arrays serve kda_kv_append and kda_attn_paged.  max_q bounds the new tokens of any one
+ * sequence (host).  Nothing is read back to the host, so the calls can be captured in a graph and
+ * replayed on new lengths.  Metadata out of range (n > max_q, kv_len beyond the table, cu_q beyond
+ * T_tot) sets KDA_DEV_BAD_META and that sequence is skipped; a page id outside the pool sets
+ * KDA_DEV_BAD_PAGE and that block is skipped.
+ *
+ * Token tensors q, k, v are [T_tot][H][d] in dtype with token rows `stride` elements apart (at
+ * least H * d: the parts of one fused projection will do); pointers are 16-byte aligned and
+ * strides multiples of 16 bytes.  d is 64 or 128. */
+#define KDA_KV_BF16 0
+#define KDA_KV_I8 1
+
+/* Bytes of one page of such a cache, rounded up to a valid pool page size (a multiple of 256); a
+ * pool with larger pages holds it too.  KDA_EINVAL for a bad shape. */
+int64_t kda_kv_page_bytes(int32_t Hkv, int32_t d, int32_t fmt, int32_t page_tokens);
+
+/* Append the call's keys and values to their blocks, keys rotated by position on the way, and
+ * write the rotated queries.
+ *   q, q_out      queries [T_tot][Hq][d] and their rotated copy (contiguous, dtype; may be q
+ *                 itself when q is contiguous).  Both NULL: keys and values only
+ *   k, v          new keys and values [T_tot][Hkv][d]
+ *   cos_sin       device fp32 [max_pos][rot_dim]: row p holds the rot_dim / 2 cosines, then the
+ *                 sines, of position p.  NULL (rot_dim 0): no rotation.  A sequence that
+ *                 reaches past max_pos sets KDA_DEV_BAD_META and is skipped
+ *   rot_dim       leading elements of a head that rotate: a multiple of 16, at most d
+ *   interleaved   0: element i turns with i + rot_dim / 2; else 2 i with 2 i + 1
+ * The pages written must be private to their sequence (a shared prefix ends on a block's end, or
+ * its last block is copied first).  A call whose kv_len < n for a sequence skips it
+ * (KDA_DEV_BAD_META).  One launch. */
+int kda_kv_append(const kda_pool *pool, int32_t Hq, int32_t Hkv, int32_t d, int32_t dtype, int32_t fmt,
+                  int32_t page_tokens, int32_t nseq, int64_t T_tot, int32_t max_q, const int32_t *cu_q,
+                  const int32_t *kv_len, const int32_t *page_table, int32_t max_pages, const void *q,
+                  int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                  const float *cos_sin, int32_t max_pos, int32_t rot_dim, int32_t interleaved, void *q_out,
+                  void *pool_base, int32_t *status_dev, void *stream);
+
+/* Read cached ranges back as values: row cu_out[s] + i of k_out and v_out ([T_out][Hkv][d], dtype)
+ * is sequence s's token begin[s] + i (cu_out device int32 [nseq + 1], begin device int32 [nseq]).
+ * For handing a prefix on, or checking what a cache stands for. */
+int kda_kv_gather(const kda_pool *pool, int32_t Hkv, int32_t d, int32_t dtype, int32_t fmt, int32_t page_tokens,
+                  int32_t nseq, int64_t T_out, const int32_t *cu_out, const int32_t *begin,
+                  const int32_t *page_table, int32_t max_pages, void *k_out, void *v_out, const void *pool_base,
+                  int32_t *status_dev, void *stream);
+
+/* Workspace bytes of kda_attn_paged for such a batch (partial results of sequences that several
+ * CTAs share; nothing in it outlives a call).  KDA_EINVAL for a bad shape. */
+int64_t kda_attn_workspace_bytes(int32_t Hq, int32_t Hkv, int32_t d, int32_t dtype, int32_t nseq, int64_t T_tot,
+                                 int32_t max_q);
+
+/* Attention of the call's queries over the cache: query head h reads key/value head
+ * h / (Hq / Hkv), and a query at position p sees the cached tokens j <= p with
+ *     window == 0  or  j > p - window  or  j < sinks
+ * (causal; with a window, the last `window` tokens and the first `sinks` ones).
+ *   q             [T_tot][Hq][d] as rotated by kda_kv_append, its tokens already in the cache
+ *   scale         factor of q . k, commonly 1 / sqrt(d)
+ *   o             [T_tot][Hq][d] contiguous, dtype: softmax(scale q k) v
+ *   lse           device fp32 [T_tot][Hq] or NULL: the log of the sum of the exponentials
+ *   workspace     device, 16-byte aligned, kda_attn_workspace_bytes(); one call at a time uses it
+ * A query that sees nothing (kv_len < n puts it before the first token) gets o = 0 and
+ * lse = -infinity.  What a query does not see never changes its result, a NaN or an infinity
+ * included; pages that no query of the call sees are not read, and their table entries may hold
+ * anything.  Sums, maxima and accumulators are fp32; KDA_F32 calls keep fp32 accuracy throughout.
+ * Results do not depend on timing: the same call gives the same bits. */
+int kda_attn_paged(const kda_pool *pool, int32_t Hq, int32_t Hkv, int32_t d, int32_t dtype, int32_t fmt,
+                   int32_t page_tokens, int32_t nseq, int64_t T_tot, int32_t max_q, const int32_t *cu_q,
+                   const int32_t *kv_len, const int32_t *page_table, int32_t max_pages, const void *q,
+                   int64_t q_stride, float scale, int32_t window, int32_t sinks, void *o, float *lse,
+                   const void *pool_base, void *workspace, int64_t ws_bytes, int32_t *status_dev, void *stream);
+
 /* ---------------------------------------------------------------- status -------------- */
 
 /* Wait for `stream`, read and clear *status_dev.  Returns KDA_OK, KDA_EDEVICE (bits in

@@ -25,6 +25,7 @@ _lib = None
 KDA_OK, KDA_EINVAL, KDA_ENOPAGES, KDA_EREF, KDA_ECUDA, KDA_EDEVICE = 0, -1, -2, -3, -4, -5
 KDA_F32, KDA_BF16 = 0, 1
 KDA_DEV_BAD_PAGE, KDA_DEV_BAD_META, KDA_DEV_TIMEOUT, KDA_DEV_RANGE = 1, 2, 4, 8
+KDA_KV_BF16, KDA_KV_I8 = 0, 1
 DTYPES = {"f32": KDA_F32, "bf16": KDA_BF16}
 
 # Every symbol include/kda.h declares, with (restype, argtypes).
@@ -74,6 +75,14 @@ _SIGS = {
     "kda_object_pages_q8": (_I32, [_P, _I32, _I32, _I32]),
     "kda_ckpt_write_q8": (ctypes.c_int, [_P, _I32, _I32, _I32, _I32, _P, _P, _P, _P, _I64, _P, _P]),
     "kda_ckpt_restore_q8": (ctypes.c_int, [_P, _I32, _I32, _I32, _I32, _P, _P, _P, _P, _I64, _P, _P]),
+    "kda_kv_page_bytes": (_I64, [_I32, _I32, _I32, _I32]),
+    "kda_kv_append": (ctypes.c_int, [_P, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _I64, _I32, _P, _P, _P, _I32, _P,
+                                     _I64, _P, _I64, _P, _I64, _P, _I32, _I32, _I32, _P, _P, _P, _P]),
+    "kda_kv_gather": (ctypes.c_int, [_P, _I32, _I32, _I32, _I32, _I32, _I32, _I64, _P, _P, _P, _I32, _P, _P, _P, _P,
+                                     _P]),
+    "kda_attn_workspace_bytes": (_I64, [_I32, _I32, _I32, _I32, _I32, _I64, _I32]),
+    "kda_attn_paged": (ctypes.c_int, [_P, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _I64, _I32, _P, _P, _P, _I32, _P,
+                                      _I64, ctypes.c_float, _I32, _I32, _P, _P, _P, _P, _I64, _P, _P]),
     "kda_sync_status": (ctypes.c_int, [_P, _P, _P]),
     "kda_status_string": (ctypes.c_char_p, [ctypes.c_int]),
 }
@@ -522,6 +531,103 @@ def kda_ckpt_restore_q8(pool: Pool, H: int, d: int, dtype: int, ckpt_pages, acti
                                    _dev(workspace), workspace.numel() * workspace.element_size(),
                                    _dev(status), _stream(stream))
     _check(rc, "kda_ckpt_restore_q8")
+
+
+# ------------------------------------------------------------------------------ key/value cache
+def _rows(t, H: int, d: int):
+    """(device address, token stride) of a [T, H, d] CUDA tensor whose token rows are whole: the
+    parts of a fused projection qualify."""
+    T, h, w = t.shape
+    if not t.is_cuda or h != H or w != d or (T and (t.stride(2) != 1 or (h > 1 and t.stride(1) != d))):
+        raise ValueError("expected a [T, H, d] CUDA tensor with contiguous heads")
+    return t.data_ptr(), (t.stride(0) if T > 1 else H * d)
+
+
+def _table(cu, lens, page_table):
+    """(nseq, max_pages) of a batch's device int32 arrays."""
+    import torch
+    nseq, max_pages = page_table.shape
+    for t, n in ((cu, nseq + 1), (lens, nseq), (page_table, nseq * max_pages)):
+        if t.dtype != torch.int32 or t.numel() != n:
+            raise ValueError("expected int32 [nseq + 1], [nseq] and [nseq, max_pages] CUDA tensors")
+    return nseq, max_pages
+
+
+def kda_kv_page_bytes(Hkv: int, d: int, fmt: int, page_tokens: int) -> int:
+    return _check(lib().kda_kv_page_bytes(Hkv, d, fmt, page_tokens), "kda_kv_page_bytes")
+
+
+def kda_kv_append(pool: Pool, fmt: int, page_tokens: int, cu_q, kv_len, page_table, max_q: int, q, k, v, cos_sin,
+                  q_out, status, interleaved: bool = False, stream=None) -> None:
+    """k, v: [T, Hkv, d] and q: [T, Hq, d] (or None, with q_out None), token rows any stride
+    apart; cu_q, kv_len, page_table: int32 CUDA [nseq + 1], [nseq], [nseq, max_pages]; cos_sin:
+    fp32 CUDA [max_pos, rot_dim] or None; q_out: [T, Hq, d] contiguous."""
+    T, Hkv, d = k.shape
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    nseq, max_pages = _table(cu_q, kv_len, page_table)
+    kp, ks = _rows(k, Hkv, d)
+    vp, vs = _rows(v, Hkv, d)
+    Hq, qp, qs = 0, None, 0
+    if q is not None:
+        Hq = q.shape[1]
+        qp, qs = _rows(q, Hq, d)
+        if q.shape[0] != T or q_out.shape != q.shape or not q.dtype == q_out.dtype == k.dtype:
+            raise ValueError("q, q_out and k differ in tokens or type")
+    if v.shape[0] != T or v.dtype != k.dtype:
+        raise ValueError("k and v differ in tokens or type")
+    pos, rot = (0, 0) if cos_sin is None else cos_sin.shape
+    if cos_sin is not None and cos_sin.element_size() != 4:
+        raise ValueError("cos_sin must be float32")
+    rc = lib().kda_kv_append(pool.handle, Hq, Hkv, d, dtype_of(k), fmt, page_tokens, nseq, T, max_q, _dev(cu_q),
+                             _dev(kv_len), _dev(page_table), max_pages, qp, qs, kp, ks, vp, vs, _dev(cos_sin), pos,
+                             rot, int(interleaved), _dev(q_out), _dev(pool.base), _dev(status), _stream(stream))
+    _check(rc, "kda_kv_append")
+
+
+def kda_kv_gather(pool: Pool, fmt: int, page_tokens: int, cu_out, begin, page_table, k_out, v_out, status,
+                  stream=None) -> None:
+    """Rows cu_out[s] + i of k_out, v_out [T, Hkv, d] become sequence s's cached token
+    begin[s] + i (cu_out, begin: int32 CUDA [nseq + 1], [nseq])."""
+    T, Hkv, d = k_out.shape
+    if v_out.shape != k_out.shape or v_out.dtype != k_out.dtype:
+        raise ValueError("k_out and v_out differ")
+    nseq, max_pages = _table(cu_out, begin, page_table)
+    rc = lib().kda_kv_gather(pool.handle, Hkv, d, dtype_of(k_out), fmt, page_tokens, nseq, T, _dev(cu_out),
+                             _dev(begin), _dev(page_table), max_pages, _dev(k_out), _dev(v_out), _dev(pool.base),
+                             _dev(status), _stream(stream))
+    _check(rc, "kda_kv_gather")
+
+
+def kda_attn_workspace_bytes(Hq: int, Hkv: int, d: int, dtype: int, nseq: int, T_tot: int, max_q: int) -> int:
+    return _check(lib().kda_attn_workspace_bytes(Hq, Hkv, d, dtype, nseq, T_tot, max_q), "kda_attn_workspace_bytes")
+
+
+def attn_workspace(q, Hkv: int, nseq: int, max_q: int):
+    """A device byte tensor sized for kda_attn_paged on queries q [T, Hq, d]."""
+    import torch
+    T, Hq, d = q.shape
+    nb = kda_attn_workspace_bytes(Hq, Hkv, d, dtype_of(q), nseq, T, max_q)
+    return torch.empty(nb, dtype=torch.uint8, device=q.device)
+
+
+def kda_attn_paged(pool: Pool, Hkv: int, fmt: int, page_tokens: int, cu_q, kv_len, page_table, max_q: int, q, o,
+                   workspace, status, scale: float | None = None, window: int = 0, sinks: int = 0, lse=None,
+                   stream=None) -> None:
+    """q: [T, Hq, d], token rows any stride apart; o: [T, Hq, d] contiguous; lse: fp32 CUDA
+    [T, Hq] or None.  scale defaults to d ** -0.5."""
+    T, Hq, d = q.shape
+    if o.shape != q.shape or o.dtype != q.dtype:
+        raise ValueError("q and o differ in shape or type")
+    if lse is not None and (lse.element_size() != 4 or lse.numel() != T * Hq):
+        raise ValueError("lse must be float32 [T, Hq]")
+    nseq, max_pages = _table(cu_q, kv_len, page_table)
+    qp, qs = _rows(q, Hq, d)
+    rc = lib().kda_attn_paged(pool.handle, Hq, Hkv, d, dtype_of(q), fmt, page_tokens, nseq, T, max_q, _dev(cu_q),
+                              _dev(kv_len), _dev(page_table), max_pages, qp, qs, d ** -0.5 if scale is None else scale,
+                              window, sinks, _dev(o), _dev(lse), _dev(pool.base), _dev(workspace),
+                              workspace.numel() * workspace.element_size(), _dev(status), _stream(stream))
+    _check(rc, "kda_attn_paged")
 
 
 # ------------------------------------------------------------------------------ status

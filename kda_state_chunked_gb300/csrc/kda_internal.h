@@ -153,6 +153,77 @@ struct Q8Args {
     int32_t *status;
 };
 
+// Geometry of a key/value cache inside the paged pool: a page is one block of page_tokens
+// tokens of all Hkv heads, one record per head (K tile | V tile | scales of the 8-bit form).
+struct KvView {
+    uint8_t *base;
+    int64_t page_bytes;
+    int32_t num_pages;
+    int32_t page_tokens;
+    int32_t Hkv, d, fmt;
+    int32_t rec_bytes;            // bytes of one head's record
+    const int32_t *table;         // [nseq][max_pages]
+    int32_t max_pages;
+    int32_t *status;
+};
+constexpr int kKvMaxPageTokens = 128;
+
+struct KvAppendArgs {
+    KvView kv;
+    int32_t Hq, dtype, nseq, max_q;
+    int64_t T_tot;
+    const int32_t *cu_q, *kv_len;
+    const void *q, *k, *v;        // token rows q_stride / k_stride / v_stride elements apart
+    int64_t q_stride, k_stride, v_stride;
+    const float *cos_sin;         // [max_pos][rot_dim]: cosines, then sines; null for no rotation
+    int32_t max_pos, rot_dim, interleaved;
+    void *q_out;                  // [T_tot][Hq][d]
+};
+
+struct KvGatherArgs {
+    KvView kv;
+    int32_t dtype, nseq;
+    int64_t T_out;
+    const int32_t *cu_out, *begin;
+    void *k_out, *v_out;          // [T_out][Hkv][d]
+};
+
+// Attention over a paged cache.  A row tile is a run of (token, head of the group) query rows of
+// one sequence and one key/value head; an item is a row tile's work over the tokens it sees, cut
+// into units of kAttnUnit cached tokens.  The units of all items, in order, are shared out evenly
+// over the CTAs; an item that several CTAs touch is joined afterwards from their partial results.
+constexpr int kAttnUnit = 128;
+constexpr int kAttnDecodeRows = 16;    // rows of a tile of the register kernel
+constexpr int kAttnPrefillRows = 128;  // rows of a tile of the tensor-memory kernel
+
+// An item that starts in a CTA and ends in a later one (one per CTA at most).
+struct AttnSplit {
+    int32_t last_cta;             // CTA that holds its last unit; < 0: none
+    int32_t row_tok;              // packed token of the tile's first row
+    int32_t head;                 // key/value head
+    int32_t row0, nrows;          // first row of the tile in its sequence, rows in use
+    int32_t pad[3];
+};
+
+struct AttnArgs {
+    KvView kv;
+    int32_t Hq, G, dtype, nseq, max_q;
+    int64_t T_tot;
+    const int32_t *cu_q, *kv_len;
+    const void *q;
+    int64_t q_stride;
+    float scale;
+    int32_t window, sinks;
+    void *o;                      // [T_tot][Hq][d]
+    float *lse;                   // [T_tot][Hq] or null
+    int32_t ctas;                 // CTAs the units are shared out over
+    float *part;                  // [ctas][2][rows][d + 2]: m, l and unnormalised o of partial items
+    AttnSplit *split;             // [ctas]
+    int64_t *plan;                // prefill: units before each row tile, of all heads
+};
+// CTAs of the attention kernels: one per SM.
+constexpr int kAttnMaxCtas = 152;
+
 // Kernel launchers (defined in the .cu files).
 cudaError_t launch_prefill_split(const SplitArgs &a, const SplitPlan &plan, cudaStream_t s);
 cudaError_t launch_prefill_simt(const PrefillArgs &a, cudaStream_t s);
@@ -173,5 +244,8 @@ cudaError_t launch_copy_objects(const CopyArgs &a, cudaStream_t s);
 cudaError_t launch_host_copy(const HostCopyArgs &a, cudaStream_t s);
 cudaError_t launch_ckpt_quantize(const Q8Args &a, cudaStream_t s);
 cudaError_t launch_ckpt_dequantize(const Q8Args &a, cudaStream_t s);
+cudaError_t launch_kv_append(const KvAppendArgs &a, cudaStream_t s);
+cudaError_t launch_kv_gather(const KvGatherArgs &a, cudaStream_t s);
+cudaError_t launch_attn_decode(const AttnArgs &a, cudaStream_t s);
 
 }  // namespace kda

@@ -1,0 +1,698 @@
+// Attention of few query rows over the paged cache (decoding, drafts; every float32 call).
+//
+//   o_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = exp(scale q_i . k_j - m_i), j over the visible tokens
+//
+// in one pass over the cache with a running maximum and sum per row.  Bound: the cache's bytes.
+// The rows of a group (query heads that share a key/value head, times the call's tokens) fill the
+// M = 16 of a warp-level matrix product, so a cached byte is read once for all of them; wider
+// tensor-memory tiles would stand empty here.
+//
+// One CTA of 8 warps an SM.  A unit is 128 tokens; warp w takes tokens 16 w .. 16 w + 15 of it, which
+// lie in one page, and runs alone: it copies its own tokens of later units into its own ring of
+// shared-memory stages (bulk copies: a page's rows are contiguous) and keeps its own maxima, sums
+// and 16 x D accumulators.  The warps meet only at an item's end.
+//
+// 8-bit cache: codes c become fp16 exactly (the byte under the exponent of 1024, less 1152), a
+// query row is scaled by a power of two into fp16's range, so q . c carries no rounding beyond
+// fp32 sums, and the block's key scale multiplies the score.  The value scale goes into the
+// probabilities: p (vs / ref) 2^13 in fp16, ref the largest value scale so far.  float32 queries
+// are split into 2 fp16 terms (3 bf16 terms over the 16-bit cache), and so are the probabilities:
+// the products then keep 22 to 24 bits.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "attn_common.cuh"
+
+namespace kda {
+namespace {
+
+using namespace attn;
+
+constexpr int kWarps = 8, kStep = 16;
+constexpr float kPScale = 8192.f;                     // probabilities' scale in fp16
+constexpr float kMinRef = 0x1p-100f;
+
+template <int FMT, int D>
+struct Shape {
+    static constexpr int row = kKvRow<FMT, D>;
+    static constexpr int tile = row * kStep;          // K or V bytes of a step
+    static constexpr int stage = 2 * tile + 128;
+    static constexpr int stages = FMT == KDA_KV_I8 ? (D == 128 ? 4 : 6) : (D == 128 ? 2 : 4);
+};
+
+template <int FMT, int D, int NT>
+struct Smem {
+    static constexpr int ring = kWarps * Shape<FMT, D>::stages * Shape<FMT, D>::stage;
+    static constexpr int o_acc = ring;                                   // [8][16][D] fp32
+    static constexpr int o_ml = o_acc + kWarps * 16 * D * 4;             // [2][8][16][2] fp32
+    static constexpr int o_q = o_ml + 2 * kWarps * 16 * 8;               // fragments of split queries
+    static constexpr int o_bar = o_q + (NT > 1 ? NT * (D / 16) * 512 : 0);
+    static constexpr int o_tok = o_bar + kWarps * Shape<FMT, D>::stages * 8;
+    static constexpr int o_misc = o_tok + kWarps * Shape<FMT, D>::stages * 4;
+    static constexpr int total = o_misc + 128;
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+// D (16x8) += A (16x16) B (16x8), fp32 sums.
+template <int FMT>
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (FMT == KDA_KV_I8)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                     "{%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                     "{%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Two biased bytes (selected by SEL, under the exponent byte 0x64) as fp16: 1024 + b - 1152 = code.
+template <uint32_t SEL>
+__device__ __forceinline__ uint32_t half2_of(uint32_t biased) {
+    const uint32_t u = __byte_perm(biased, 0x64646464u, SEL);
+    const uint32_t k = 0x64806480u;   // 1152, 1152
+    const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&u), *reinterpret_cast<const __half2 *>(&k));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+// x (already in range) as NT packed terms of the product's type whose sum is x to NT times its bits.
+template <int FMT, int NT>
+__device__ __forceinline__ void split2(float x, float y, uint32_t (&out)[NT]) {
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+        if constexpr (FMT == KDA_KV_I8) {
+            const __half2 h = __floats2half2_rn(x, y);
+            out[i] = *reinterpret_cast<const uint32_t *>(&h);
+            if (i + 1 < NT) x -= __low2float(h), y -= __high2float(h);
+        } else {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+            out[i] = *reinterpret_cast<const uint32_t *>(&h);
+            if (i + 1 < NT) x -= __low2float(h), y -= __high2float(h);
+        }
+    }
+}
+
+// Place of the 4-float unit u of a row of the warps' accumulators in shared memory, so that the
+// fragment stores of a warp fall into different banks.
+template <int FMT, int D>
+__device__ __forceinline__ int acc_unit(int row, int u) {
+    if constexpr (FMT == KDA_KV_BF16) return u ^ ((row & (D / 8 - 1) & 7) << 1);
+    else if constexpr (D == 128) return u ^ (((u >> 3) & 3) + 4 * (row & 1));
+    else return u ^ (((u >> 3) & 1) + 2 * (row & 1));
+}
+
+// Where a warp's loads stand: the unit whose copy comes next, its page id already on the way.
+struct Cursor {
+    Tile t;
+    int32_t h, u;
+    int32_t tok;                  // first token of this warp's step, -1: no row sees any of them
+    int32_t page, slot;
+};
+
+template <int FMT, int D, int NT>
+__global__ void __launch_bounds__(kWarps * 32, 1) attn_decode_kernel(const __grid_constant__ AttnArgs a) {
+    using S = Shape<FMT, D>;
+    using M = Smem<FMT, D, NT>;
+    constexpr int kKs = D / 16;   // 16-wide slices of a row
+    constexpr int kNt = D / 8;    // 8-wide output tiles
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = ptx::smem_align1024(smem_raw);
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane >> 2, t = lane & 3;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + M::o_bar) + warp * S::stages;
+    int32_t *toks = reinterpret_cast<int32_t *>(sm + M::o_tok) + warp * S::stages;
+    uint8_t *ring = sm + warp * S::stages * S::stage;
+    float *ml = reinterpret_cast<float *>(sm + M::o_ml);   // of this item; the last one's may still be read
+    int ml_next = kWarps * 32;
+    float *acc = reinterpret_cast<float *>(sm + M::o_acc);
+    uint32_t *qfrag = reinterpret_cast<uint32_t *>(sm + M::o_q);
+    volatile int *err = reinterpret_cast<int *>(sm + M::o_misc);
+    int64_t *share = reinterpret_cast<int64_t *>(sm + M::o_misc + 16);   // [8] warp sums, then the start
+
+    if (lane == 0)
+        for (int i = 0; i < S::stages; ++i) ptx::mbar_init(&bars[i], 1);
+    if (tid == 0) *err = 0;
+    ptx::fence_mbar_init();
+    ptx::grid_dep_wait();
+
+    // ---- this CTA's units: sum the units of every sequence, then find where its share begins
+    const int32_t Hkv = a.kv.Hkv;
+    auto seq = [&](int s) { return kv_seq(a.cu_q, a.kv_len, s, a.T_tot, a.max_q, a.kv); };
+    auto seq_units = [&](int s) {
+        const KvSeq q = seq(s);
+        const int n = tiles_of<kAttnDecodeRows>(a, q);
+        int64_t w = 0;
+        for (int i = 0; i < n; ++i) w += make_tile<kAttnDecodeRows>(a, s, q, i).units;
+        return w * Hkv;
+    };
+    auto block_sum = [&](int64_t v, int64_t &before) {   // exclusive prefix over threads; returns the sum
+        int64_t x = v;
+        for (int i = 1; i < 32; i <<= 1) {
+            const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, i);
+            if (lane >= i) x += y;
+        }
+        __syncthreads();
+        if (lane == 31) share[warp] = x;
+        __syncthreads();
+        int64_t base = 0, all = 0;
+        for (int i = 0; i < kWarps; ++i) {
+            if (i < warp) base += share[i];
+            all += share[i];
+        }
+        before = base + x - v;
+        return all;
+    };
+    int64_t mine0 = 0, mine = 0, before, W;
+    for (int s = tid; s < a.nseq; s += kWarps * 32) {
+        const int64_t w = seq_units(s);
+        if (s == tid) mine0 = w;
+        mine += w;
+    }
+    W = block_sum(mine, before);
+    if (tid == 0) a.split[blockIdx.x].last_cta = -1;
+    const int32_t C = (int32_t)min((int64_t)a.ctas, W);   // no CTA that takes part is without a unit
+    if ((int32_t)blockIdx.x >= C) return;
+    const int64_t begin = (int64_t)blockIdx.x * W / C, end = (int64_t)(blockIdx.x + 1) * W / C;
+    int32_t s0 = 0;
+    int64_t left0 = 0;   // units before `begin` in sequence s0
+    {
+        int64_t *found = share + 8;
+        int64_t base = 0;
+        for (int s = 0; s < a.nseq; s += kWarps * 32) {
+            const int64_t w = s == 0 ? mine0 : (s + tid < a.nseq ? seq_units(s + tid) : 0);
+            const int64_t all = block_sum(w, before);
+            if (begin >= base + before && begin < base + before + w) {
+                found[0] = s + tid;
+                found[1] = begin - base - before;
+            }
+            base += all;
+            if (begin < base) break;
+        }
+        __syncthreads();
+        s0 = (int32_t)found[0];
+        left0 = found[1];
+    }
+    Tile t0;
+    int32_t h0, u0;
+    {
+        const KvSeq q = seq(s0);
+        int rt = 0;
+        for (;; ++rt) {
+            t0 = make_tile<kAttnDecodeRows>(a, s0, q, rt);
+            if (left0 < (int64_t)t0.units * Hkv) break;
+            left0 -= (int64_t)t0.units * Hkv;
+        }
+        h0 = (int32_t)(left0 / t0.units);
+        u0 = (int32_t)(left0 % t0.units);
+    }
+
+    // the next item after (tile, head)
+    auto next_item = [&](Tile &x, int32_t &h) {
+        if (++h < Hkv) return;
+        h = 0;
+        if (x.rt + 1 < x.tiles) {
+            x = make_tile<kAttnDecodeRows>(a, x.s, x.q, x.rt + 1);
+            return;
+        }
+        int s = x.s + 1;
+        KvSeq q = seq(s);
+        while (q.n == 0 && s + 1 < a.nseq) q = seq(++s);
+        x = make_tile<kAttnDecodeRows>(a, s, q, 0);
+    };
+
+    // ---- loads
+    const int pt = a.kv.page_tokens;
+    auto aim = [&](Cursor &c) {   // this warp's step of the cursor's unit
+        const int32_t j = unit_token(c.t, c.u) + warp * kStep;
+        c.tok = -1;
+        if (!any_sees(a, c.t, j, kStep)) return;
+        c.tok = j;
+        const int32_t b = j / pt;
+        c.slot = j - b * pt;
+        c.page = __ldg(a.kv.table + (int64_t)c.t.s * a.kv.max_pages + b);
+    };
+    auto load = [&](const Cursor &c, int stage) {
+        if (lane != 0) return;
+        const uint8_t *rec = c.tok < 0 ? nullptr : kv_record(a.kv, c.page, c.h);
+        toks[stage] = rec ? c.tok : -1;
+        if (!rec) {
+            ptx::mbar_arrive(&bars[stage]);
+            return;
+        }
+        uint8_t *dst = ring + stage * S::stage;
+        constexpr uint32_t kLine = S::row < 128 ? S::row : 128, kRun = kLine * kStep;
+        ptx::mbar_arrive_expect_tx(&bars[stage], 2 * S::tile + (FMT == KDA_KV_I8 ? 16 : 0));
+#pragma unroll
+        for (int v = 0; v < 2; ++v)
+#pragma unroll
+            for (int b = 0; b < S::tile / (int)kRun; ++b)
+                ptx::bulk_load(dst + v * S::tile + b * kRun, rec + v * pt * S::row + b * pt * 128 + c.slot * kLine, kRun,
+                               &bars[stage]);
+        if (FMT == KDA_KV_I8) ptx::bulk_load(dst + 2 * S::tile, rec + 2 * pt * S::row, 16, &bars[stage]);
+    };
+    Cursor cur;
+    cur.t = t0;
+    cur.h = h0;
+    cur.u = u0;
+    int64_t to_load = end - begin;
+    aim(cur);
+    auto load_next = [&](int stage) {
+        if (to_load == 0) return;
+        load(cur, stage);
+        if (--to_load == 0) return;
+        if (++cur.u == cur.t.units) {
+            cur.u = 0;
+            next_item(cur.t, cur.h);
+        }
+        aim(cur);
+    };
+    for (int i = 0; i < S::stages; ++i) load_next(i);
+
+    // ---- items
+    Tile tile = t0;
+    int32_t head = h0, u = u0, stage = 0;
+    uint32_t phase = 0;
+    int64_t left = end - begin;
+    while (left > 0) {
+        const int32_t u_first = u, u_last = (int32_t)min((int64_t)tile.units, u + left);
+
+        // query fragments, rows g and g + 8
+        uint32_t qa[NT == 1 ? kKs : 1][4];
+        float rs[2];
+        int32_t pos[2];
+        {
+            float x[2][kKs * 4];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int row = g + 8 * r, at = tile.row0 + row;
+                const bool in = row < tile.nrows;
+                pos[r] = in ? tile.q.len - tile.q.n + at / a.G : -1;
+                const int64_t off = (int64_t)(tile.q.tok0 + at / a.G) * a.q_stride + (int64_t)(head * a.G + at % a.G) * D;
+#pragma unroll
+                for (int k = 0; k < kKs; ++k) {
+                    // the four columns of slice k that this lane feeds: neighbours for the 8-bit
+                    // cache (a lane's four bytes of a key), the fragment's own for the 16-bit one
+                    const int c0 = 16 * k + (FMT == KDA_KV_I8 ? 4 * t : 2 * t);
+                    const int c1 = FMT == KDA_KV_I8 ? c0 + 2 : c0 + 8;
+                    float2 lo = make_float2(0.f, 0.f), hi = lo;
+                    if (in) {
+                        if (NT > 1) {
+                            const float *p = static_cast<const float *>(a.q) + off;
+                            lo = *reinterpret_cast<const float2 *>(p + c0);
+                            hi = *reinterpret_cast<const float2 *>(p + c1);
+                        } else {
+                            const __nv_bfloat16 *p = static_cast<const __nv_bfloat16 *>(a.q) + off;
+                            lo = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(p + c0));
+                            hi = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(p + c1));
+                        }
+                    }
+                    x[r][4 * k] = lo.x, x[r][4 * k + 1] = lo.y, x[r][4 * k + 2] = hi.x, x[r][4 * k + 3] = hi.y;
+                }
+                rs[r] = a.scale * kLog2e;
+                if (FMT == KDA_KV_I8) {
+                    // a power of two that brings the row's largest magnitude to [2^10, 2^11)
+                    float top = 0.f;
+#pragma unroll
+                    for (int i = 0; i < kKs * 4; ++i) top = fmaxf(top, fabsf(x[r][i]));
+                    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+                    const int e = (int)(__float_as_uint(top) >> 23);
+                    const int shift = e == 0 || e == 255 ? 0 : min(max(137 - e, -120), 120);
+                    const float up = __uint_as_float((uint32_t)(127 + shift) << 23);
+#pragma unroll
+                    for (int i = 0; i < kKs * 4; ++i) x[r][i] *= up;
+                    rs[r] *= __uint_as_float((uint32_t)(127 - shift) << 23);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kKs; ++k) {
+                uint32_t f[4][NT];
+                split2<FMT, NT>(x[0][4 * k], x[0][4 * k + 1], f[0]);
+                split2<FMT, NT>(x[1][4 * k], x[1][4 * k + 1], f[1]);
+                split2<FMT, NT>(x[0][4 * k + 2], x[0][4 * k + 3], f[2]);
+                split2<FMT, NT>(x[1][4 * k + 2], x[1][4 * k + 3], f[3]);
+                if constexpr (NT == 1) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) qa[k][i] = f[i][0];
+                } else if (k % kWarps == warp) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        *reinterpret_cast<uint4 *>(qfrag + ((n * kKs + k) * 32 + lane) * 4) =
+                            make_uint4(f[0][n], f[1][n], f[2][n], f[3][n]);
+                }
+            }
+            if constexpr (NT > 1) __syncthreads();
+        }
+
+        float o[kNt][4];
+#pragma unroll
+        for (int j = 0; j < kNt; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+        float ref = 0.f, inv_ref = 0.f;   // 8-bit: largest value scale so far
+
+        for (; u < u_last; ++u, --left) {
+            const bool ok = __all_sync(0xFFFFFFFFu, ptx::mbar_wait(&bars[stage], phase, err));
+            if (!ok) flag_status(a.kv.status, KDA_DEV_TIMEOUT);
+            const int32_t j0 = ok ? toks[stage] : -1;
+            if (j0 >= 0) {
+                const uint8_t *buf = ring + stage * S::stage;
+                const uint32_t kb = ptx::smem_u32(buf), vb = kb + S::tile;
+                float sc[2] = {rs[0], rs[1]}, vs = 1.f;
+                if (FMT == KDA_KV_I8) {
+                    const float2 f = *reinterpret_cast<const float2 *>(buf + 2 * S::tile);
+                    sc[0] *= f.x, sc[1] *= f.x, vs = f.y;
+                }
+                // ---- scores: c[n-tile][..], even and odd slices apart for shorter chains
+                float c[2][2][4] = {};
+                const int mr = lane & 7, mm = lane >> 3;   // row and matrix whose address this lane gives
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    if constexpr (FMT == KDA_KV_I8) {
+#pragma unroll
+                        for (int i = 0; i < kKs / 4; ++i) {
+                            uint32_t w[4];
+                            ldsm4(w, kb + kv_tile_off<S::row>(kStep, 8 * n + mr, 16 * (4 * i + mm)));
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const uint32_t b = w[k] ^ 0x80808080u;
+                                const uint32_t b0 = half2_of<0x4140>(b), b1 = half2_of<0x4342>(b);
+                                if constexpr (NT == 1) {
+                                    mma<FMT>(c[n][k & 1], qa[4 * i + k], b0, b1);
+                                } else {
+#pragma unroll
+                                    for (int z = NT - 1; z >= 0; --z) {
+                                        const uint4 f = *reinterpret_cast<const uint4 *>(
+                                            qfrag + ((z * kKs + 4 * i + k) * 32 + lane) * 4);
+                                        const uint32_t qf[4] = {f.x, f.y, f.z, f.w};
+                                        mma<FMT>(c[n][k & 1], qf, b0, b1);
+                                    }
+                                }
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < kKs / 2; ++i) {
+                            uint32_t w[4];
+                            ldsm4(w, kb + kv_tile_off<S::row>(kStep, 8 * n + mr, 16 * (4 * i + mm)));
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                if constexpr (NT == 1) {
+                                    mma<FMT>(c[n][k], qa[2 * i + k], w[2 * k], w[2 * k + 1]);
+                                } else {
+#pragma unroll
+                                    for (int z = NT - 1; z >= 0; --z) {
+                                        const uint4 f = *reinterpret_cast<const uint4 *>(
+                                            qfrag + ((z * kKs + 2 * i + k) * 32 + lane) * 4);
+                                        const uint32_t qf[4] = {f.x, f.y, f.z, f.w};
+                                        mma<FMT>(c[n][k], qf, w[2 * k], w[2 * k + 1]);
+                                    }
+                                }
+                            }
+                        }
+                    }
+                }
+                // ---- softmax: element (n, e) is row g + 8 (e / 2), token j0 + 8 n + 2 t + e % 2
+                const bool whole = all_see(a, tile, j0, kStep);   // rows not in use may see what they like
+                float p[2][4], top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        p[n][e] = (c[n][0][e] + c[n][1][e]) * sc[e >> 1];
+                        if (!whole && !sees(a, pos[e >> 1], j0 + 8 * n + 2 * t + (e & 1))) p[n][e] = -INFINITY;
+                        top[e >> 1] = fmaxf(top[e >> 1], p[n][e]);
+                    }
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    top[r] = fmaxf(top[r], __shfl_xor_sync(0xFFFFFFFFu, top[r], 1));
+                    top[r] = fmaxf(top[r], __shfl_xor_sync(0xFFFFFFFFu, top[r], 2));
+                }
+                const bool scaled = FMT == KDA_KV_I8 && vs > ref && vs < INFINITY;
+                if (__any_sync(0xFFFFFFFFu, top[0] > m[0] || top[1] > m[1] || scaled)) {
+                    float f[2];
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const float mn = fmaxf(m[r], top[r]);
+                        f[r] = mn == -INFINITY ? 1.f : exp2f(m[r] - mn);
+                        l[r] *= f[r];
+                        m[r] = mn;
+                    }
+                    if (scaled) {
+                        const float rn = fmaxf(vs, kMinRef), k = ref / rn;
+                        f[0] *= k, f[1] *= k;
+                        ref = rn;
+                        inv_ref = 1.f / rn;
+                    }
+#pragma unroll
+                    for (int j = 0; j < kNt; ++j) o[j][0] *= f[0], o[j][1] *= f[0], o[j][2] *= f[1], o[j][3] *= f[1];
+                }
+                const float mx[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+                float pv = 1.f;   // what a probability is multiplied by before it is rounded
+                if (FMT == KDA_KV_I8) pv = isfinite(vs) ? vs * inv_ref * kPScale : NAN;
+                uint32_t pa[4][NT];
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        p[n][e] = exp2f(p[n][e] - mx[e >> 1]);
+                        l[e >> 1] += p[n][e];
+                        if (FMT == KDA_KV_I8) p[n][e] = p[n][e] == 0.f ? 0.f : p[n][e] * pv;
+                    }
+                    split2<FMT, NT>(p[n][0], p[n][1], pa[2 * n]);
+                    split2<FMT, NT>(p[n][2], p[n][3], pa[2 * n + 1]);
+                }
+                // ---- values
+                auto values = [&](const uint32_t (&pf)[4][NT]) {
+                    if constexpr (FMT == KDA_KV_I8) {
+                        // a lane reads kNt neighbouring columns of its four tokens; output tile j
+                        // then stands for columns kNt n + j
+                        uint32_t w[4][kNt / 4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int row = 2 * t + (i & 1) + 8 * (i >> 1);
+                            const uint8_t *at = buf + S::tile + kv_tile_off<S::row>(kStep, row, kNt * g);
+                            if constexpr (kNt == 16) {
+                                const uint4 x = *reinterpret_cast<const uint4 *>(at);
+                                w[i][0] = x.x, w[i][1] = x.y, w[i][2] = x.z, w[i][3] = x.w;
+                            } else {
+                                const uint2 x = *reinterpret_cast<const uint2 *>(at);
+                                w[i][0] = x.x, w[i][1] = x.y;
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < kNt / 4; ++i) {
+                            uint32_t b[4][2];
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                const uint32_t lo = __byte_perm(w[2 * y][i], w[2 * y + 1][i], 0x5140) ^ 0x80808080u;
+                                const uint32_t hi = __byte_perm(w[2 * y][i], w[2 * y + 1][i], 0x7362) ^ 0x80808080u;
+                                b[0][y] = half2_of<0x4140>(lo);
+                                b[1][y] = half2_of<0x4342>(lo);
+                                b[2][y] = half2_of<0x4140>(hi);
+                                b[3][y] = half2_of<0x4342>(hi);
+                            }
+#pragma unroll
+                            for (int z = NT - 1; z >= 0; --z) {
+                                const uint32_t f[4] = {pf[0][z], pf[1][z], pf[2][z], pf[3][z]};
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) mma<FMT>(o[4 * i + j], f, b[j][0], b[j][1]);
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < kNt / 2; ++i) {
+                            uint32_t w[4];   // (tokens 0-7, 8-15) of output tiles 2 i and 2 i + 1
+                            ldsm4t(w, vb + kv_tile_off<S::row>(kStep, 8 * (mm & 1) + mr, 16 * (2 * i + (mm >> 1))));
+#pragma unroll
+                            for (int z = NT - 1; z >= 0; --z) {
+                                const uint32_t f[4] = {pf[0][z], pf[1][z], pf[2][z], pf[3][z]};
+                                mma<FMT>(o[2 * i], f, w[0], w[1]);
+                                mma<FMT>(o[2 * i + 1], f, w[2], w[3]);
+                            }
+                        }
+                    }
+                };
+                bool odd = false;
+                if constexpr (FMT == KDA_KV_BF16) {
+                    // A token that a row does not see has probability 0, but 0 times an infinity or a
+                    // NaN is not 0 (stale slots past the end, or a value the row must not know of).
+                    // Where a step is not seen whole, look for such a value first.
+                    if (!whole) {
+                        uint32_t bad = 0;
+                        for (int i = lane; i < S::tile / 16; i += 32) {
+                            const uint4 x = *reinterpret_cast<const uint4 *>(buf + S::tile + 16 * i);
+                            for (uint32_t y : {x.x, x.y, x.z, x.w})
+                                bad |= (uint32_t)((y & 0x7F80u) == 0x7F80u) | (uint32_t)((y & 0x7F800000u) == 0x7F800000u);
+                        }
+                        odd = __any_sync(0xFFFFFFFFu, bad != 0);
+                    }
+                }
+                if (!odd) {
+                    values(pa);
+                } else if constexpr (FMT == KDA_KV_BF16) {
+                    // one product for each query token, without the tokens it does not see, of which
+                    // only that token's rows are kept
+                    for (int32_t q = tile.pmin; q <= tile.pmax; ++q) {
+                        uint32_t keep[2];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int j = j0 + 8 * i + 2 * t;
+                            keep[i] = (sees(a, q, j) ? 0xFFFFu : 0u) | (sees(a, q, j + 1) ? 0xFFFF0000u : 0u);
+                        }
+#pragma unroll
+                        for (int i = 0; i < kNt; ++i) {
+                            uint32_t w[4];
+                            ldsm4t(w, vb + kv_tile_off<S::row>(kStep, 8 * (mm & 1) + mr, 16 * i));
+                            float d[4] = {};
+#pragma unroll
+                            for (int z = NT - 1; z >= 0; --z) {
+                                const uint32_t f[4] = {pa[0][z], pa[1][z], pa[2][z], pa[3][z]};
+                                mma<FMT>(d, f, w[0] & keep[0], w[1] & keep[1]);
+                            }
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (pos[e >> 1] == q) o[i][e] += d[e];
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+            load_next(stage);
+            if (++stage == S::stages) stage = 0, phase ^= 1;
+        }
+
+        // ---- the warps' results together
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], 1);
+            l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], 2);
+            if (t == 0) {
+                ml[(warp * 16 + g + 8 * r) * 2] = m[r];
+                ml[(warp * 16 + g + 8 * r) * 2 + 1] = l[r];
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int row = g + 8 * r;
+            if (row >= tile.nrows) continue;
+            float mt = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) mt = fmaxf(mt, ml[(i * 16 + row) * 2]);
+            float f = mt == -INFINITY ? 1.f : exp2f(m[r] - mt);
+            if (FMT == KDA_KV_I8) f *= ref * (1.f / kPScale);
+            float *dst = acc + (warp * 16 + row) * D;
+            if constexpr (FMT == KDA_KV_I8) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int i = 0; i < kNt / 4; ++i) {
+                        const int unit = (kNt / 4) * (2 * t + e) + i;
+                        *reinterpret_cast<float4 *>(dst + 4 * acc_unit<FMT, D>(row, unit)) =
+                            make_float4(o[4 * i][2 * r + e] * f, o[4 * i + 1][2 * r + e] * f, o[4 * i + 2][2 * r + e] * f,
+                                        o[4 * i + 3][2 * r + e] * f);
+                    }
+            } else {
+#pragma unroll
+                for (int j = 0; j < kNt; ++j)
+                    *reinterpret_cast<float2 *>(dst + 4 * acc_unit<FMT, D>(row, 2 * j + (t >> 1)) + 2 * (t & 1)) =
+                        make_float2(o[j][2 * r] * f, o[j][2 * r + 1] * f);
+            }
+        }
+        __syncthreads();
+        const bool starts = u_first == 0, ends = u_last == tile.units;
+        const int part_slot = starts ? 1 : 0;
+        for (int i = tid; i < tile.nrows * (D / 4); i += kWarps * 32) {
+            const int row = i / (D / 4), unit = i % (D / 4);
+            float mt = -INFINITY, lt = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) mt = fmaxf(mt, ml[(w * 16 + row) * 2]);
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float lw = ml[(w * 16 + row) * 2 + 1];
+                lt += mt == -INFINITY ? lw : lw * exp2f(ml[(w * 16 + row) * 2] - mt);
+                const float4 x = *reinterpret_cast<const float4 *>(acc + (w * 16 + row) * D + 4 * acc_unit<FMT, D>(row, unit));
+                v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+            }
+            if (starts && ends) {
+                const int at_row = tile.row0 + row;
+                const int64_t at = (int64_t)(tile.q.tok0 + at_row / a.G) * a.Hq + head * a.G + at_row % a.G;
+                const float inv = 1.f / lt;
+                if (lt == 0.f) v = make_float4(0.f, 0.f, 0.f, 0.f);
+                else v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
+                store_row4(a.o, a.dtype, at * D + 4 * unit, v);
+                if (a.lse && unit == 0) a.lse[at] = lse_of(mt, lt);
+            } else {
+                float *dst = a.part + ((int64_t)(blockIdx.x * 2 + part_slot) * 16 + row) * kPartRow<D>;
+                *reinterpret_cast<float4 *>(dst + 4 * unit) = v;
+                if (unit == 0) dst[D] = mt, dst[D + 1] = lt;
+            }
+        }
+        if (tid == 0 && starts && !ends) {
+            AttnSplit sp{};
+            sp.last_cta = cta_of(end - 1 + (tile.units - u_last) , W, C);
+            sp.row_tok = tile.q.tok0;
+            sp.head = head;
+            sp.row0 = tile.row0;
+            sp.nrows = tile.nrows;
+            a.split[blockIdx.x] = sp;
+        }
+        ml += ml_next;
+        ml_next = -ml_next;
+        if (left > 0) {
+            u = 0;
+            next_item(tile, head);
+        }
+    }
+}
+
+template <int FMT, int D, int NT>
+cudaError_t run(const AttnArgs &a, cudaStream_t st) {
+    using M = Smem<FMT, D, NT>;
+    static_assert(M::total + 1024 <= 227 * 1024, "shared memory");
+    auto kern = attn_decode_kernel<FMT, D, NT>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, M::total + 1024);
+    if (e != cudaSuccess) return e;
+    kern<<<a.ctas, kWarps * 32, M::total + 1024, st>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    // the join is placed while the last CTAs run and waits for them in hardware
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(a.ctas, 4);
+    cfg.blockDim = dim3(128);
+    cfg.stream = st;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_join_kernel<D, kAttnDecodeRows>, a);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_decode(const AttnArgs &a, cudaStream_t s) {
+    const bool i8 = a.kv.fmt == KDA_KV_I8, f32 = a.dtype == KDA_F32;
+    if (a.kv.d == 128) {
+        if (i8) return f32 ? run<KDA_KV_I8, 128, 2>(a, s) : run<KDA_KV_I8, 128, 1>(a, s);
+        return f32 ? run<KDA_KV_BF16, 128, 3>(a, s) : run<KDA_KV_BF16, 128, 1>(a, s);
+    }
+    if (i8) return f32 ? run<KDA_KV_I8, 64, 2>(a, s) : run<KDA_KV_I8, 64, 1>(a, s);
+    return f32 ? run<KDA_KV_BF16, 64, 3>(a, s) : run<KDA_KV_BF16, 64, 1>(a, s);
+}
+
+}  // namespace kda

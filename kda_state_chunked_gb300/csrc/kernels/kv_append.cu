@@ -1,0 +1,345 @@
+// Filling and reading the paged key/value cache.
+//
+// kv_append_kernel writes the call's new keys and values into their blocks and rotates queries and
+// keys by position on the way:
+//   halves  y_i = x_i c_i - x_{i+R/2} s_i,  y_{i+R/2} = x_{i+R/2} c_i + x_i s_i   (i < R/2)
+//   pairs   the same for (x_{2i}, x_{2i+1})
+// Products and sums are rounded one by one in fp32, never contracted, so a code does not depend on
+// how the compiler orders them.  In the 8-bit form a block's scale for a head is
+//   s = max(max |x| over its new tokens / 127, s_old if it holds older tokens)
+// and a code is rne(x / s), both divisions IEEE fp32 (the rule of the 8-bit checkpoints).  When s
+// grows, the older codes c become rne(c s_old / s): the values they stood for, rounded again.
+//
+// Bound: bytes.  A CTA takes one (block, head, K or V): the block's new rows stay in registers
+// between the maximum and the codes, so every input is read once and every code written once.  A
+// thread holds 8 + 8 elements of a row, the two places that rotate together, and so needs no
+// exchange with another thread.  Query rows are handled by CTAs of their own in the same launch.
+#include <cuda_bf16.h>
+
+#include "kv_common.cuh"
+
+namespace kda {
+namespace {
+
+__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float *x) {
+    const uint4 u = *reinterpret_cast<const uint4 *>(p);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+__device__ __forceinline__ void load8(const float *p, float *x) {
+    const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+__device__ __forceinline__ uint4 pack8(const float *x) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float *x) { *reinterpret_cast<uint4 *>(p) = pack8(x); }
+__device__ __forceinline__ void store8(float *p, const float *x) {
+    *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
+    *reinterpret_cast<float4 *>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+}
+
+// Places of the two groups of eight that thread c of a row holds: the halves that rotate
+// together, or sixteen neighbours (pairs, and what is not rotated).
+struct Place {
+    int a, b;
+    bool turned;
+};
+__device__ __forceinline__ Place place(int c, int rot, bool interleaved) {
+    const bool turned = 16 * c < rot;
+    if (turned && !interleaved) return {8 * c, rot / 2 + 8 * c, true};
+    return {16 * c, 16 * c + 8, turned};
+}
+
+__device__ __forceinline__ void turn(float &u, float &w, float co, float si) {
+    const float a = __fsub_rn(__fmul_rn(u, co), __fmul_rn(w, si));
+    w = __fadd_rn(__fmul_rn(w, co), __fmul_rn(u, si));
+    u = a;
+}
+
+// Rotate x (8 + 8 elements of thread c) by the table row cs of the token's position.
+__device__ __forceinline__ void rotate(float (&x)[16], const float *cs, int c, int rot, bool interleaved) {
+    float co[8], si[8];
+    load8(cs + 8 * c, co);
+    load8(cs + rot / 2 + 8 * c, si);
+    if (interleaved) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) turn(x[2 * j], x[2 * j + 1], co[j], si[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) turn(x[j], x[j + 8], co[j], si[j]);
+    }
+}
+
+__device__ __forceinline__ int8_t code_of(float x, float s) {
+    const int c = __float2int_rn(__fdiv_rn(x, s));
+    return (int8_t)max(-127, min(127, c));
+}
+// Eight codes of values x at scale s; all zero where the scale is (nothing but zeros, or so small
+// that a 127th of it is not a number of its own).
+__device__ __forceinline__ uint2 codes8(const float *x, float s) {
+    uint32_t w[2] = {0, 0};
+    if (s != 0.f)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i >> 2] |= (uint32_t)(uint8_t)code_of(x[i], s) << (8 * (i & 3));
+    return make_uint2(w[0], w[1]);
+}
+
+// NT threads; ROWS: new rows of a block that one thread may hold.
+template <int FMT, int D, class TIN, int NT, int ROWS>
+__global__ void __launch_bounds__(NT) kv_append_kernel(KvAppendArgs a, int32_t q_ctas, int32_t q_toks, int64_t items) {
+    constexpr int kTpr = D / 16;          // threads a row
+    constexpr int kRpp = NT / kTpr;       // rows a pass
+    constexpr int kRow = kKvRow<FMT, D>;
+    const int tid = threadIdx.x;
+    const bool il = a.interleaved != 0;
+    const int rot = a.rot_dim;
+
+    if ((int)blockIdx.x < q_ctas) {
+        const int64_t t_lo = (int64_t)blockIdx.x * q_toks;
+        const int per_tok = a.Hq * kTpr;
+        for (int i = tid; i < q_toks * per_tok; i += NT) {
+            const int64_t tok = t_lo + i / per_tok;
+            if (tok >= a.T_tot) break;
+            const int h = (i % per_tok) / kTpr, c = i % kTpr;
+            const Place p = place(c, rot, il);
+            const TIN *src = static_cast<const TIN *>(a.q) + tok * a.q_stride + h * D;
+            float x[16];
+            load8(src + p.a, x);
+            load8(src + p.b, x + 8);
+            if (p.turned) {
+                const int s = kv_find(a.nseq, tok, [&](int m) { return (int64_t)__ldg(a.cu_q + m); });
+                const KvSeq q = kv_seq(a.cu_q, a.kv_len, s, a.T_tot, a.max_q, a.kv);
+                const int64_t pos = (int64_t)q.len - q.n + (tok - q.tok0);
+                if (tok < q.tok0 || tok >= (int64_t)q.tok0 + q.n) continue;
+                if (pos < 0 || pos >= a.max_pos) {
+                    flag_status(a.kv.status, KDA_DEV_BAD_META);
+                    continue;
+                }
+                rotate(x, a.cos_sin + pos * rot, c, rot, il);
+            }
+            TIN *dst = static_cast<TIN *>(a.q_out) + (tok * a.Hq + h) * D;
+            store8(dst + p.a, x);
+            store8(dst + p.b, x + 8);
+        }
+        return;
+    }
+
+    // (block slot, head, K or V); the heads of a block side by side
+    const uint32_t w = blockIdx.x - q_ctas;
+    const bool is_v = (w & 1u) != 0;
+    const int head = (int)((w >> 1) % (uint32_t)a.kv.Hkv);
+    const int64_t item = (w >> 1) / (uint32_t)a.kv.Hkv;
+    const int pt = a.kv.page_tokens;
+    int s, block;
+    KvSeq q;
+    if (a.max_q == 1) {
+        // a token is a block's only new one
+        s = kv_find(a.nseq, item, [&](int m) { return (int64_t)__ldg(a.cu_q + m); });
+        q = kv_seq(a.cu_q, a.kv_len, s, a.T_tot, a.max_q, a.kv);
+        if (item < q.tok0 || item >= (int64_t)q.tok0 + q.n) return;
+        block = (q.len - q.n) / pt;
+    } else {
+        // sequence m owns block slots cu[m] / pt + 2 m and up: as many as n tokens can touch
+        auto start = [&](int m) { return (int64_t)(__ldg(a.cu_q + m) / pt) + 2 * (int64_t)m; };
+        s = kv_find(a.nseq, item, start);
+        q = kv_seq(a.cu_q, a.kv_len, s, a.T_tot, a.max_q, a.kv);
+        if (q.n == 0) return;
+        const int64_t b = (int64_t)((q.len - q.n) / pt) + (item - start(s));
+        if (item < start(s) || b * pt >= q.len) return;
+        block = (int)b;
+    }
+    const int old = q.len - q.n;
+    if (old < 0 || (rot > 0 && q.len > a.max_pos)) {   // no place, or no angle, for such a token
+        if (tid == 0) flag_status(a.kv.status, KDA_DEV_BAD_META);
+        return;
+    }
+    uint8_t *rec = kv_record(a.kv, __ldg(a.kv.table + (int64_t)s * a.kv.max_pages + block), head);
+    if (!rec) return;
+    uint8_t *tile = rec + (is_v ? pt * kRow : 0);
+    const int lo = max(old - block * pt, 0), hi = min(q.len - block * pt, pt);   // slots of the new rows
+    const int64_t tok_of_slot0 = (int64_t)q.tok0 + (int64_t)block * pt - old;
+
+    const int c = tid % kTpr, r0 = tid / kTpr;
+    const Place p = is_v ? Place{16 * c, 16 * c + 8, false} : place(c, rot, il);
+    const TIN *src = is_v ? static_cast<const TIN *>(a.v) : static_cast<const TIN *>(a.k);
+    const int64_t stride = is_v ? a.v_stride : a.k_stride;
+    float x[ROWS][16];
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        const int slot = lo + i * kRpp + r0;
+        if (slot < hi) {
+            const TIN *row = src + (tok_of_slot0 + slot) * stride + head * D;
+            load8(row + p.a, x[i]);
+            load8(row + p.b, x[i] + 8);
+        }
+    }
+    if (p.turned) {
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            const int slot = lo + i * kRpp + r0;
+            if (slot < hi) rotate(x[i], a.cos_sin + ((int64_t)block * pt + slot) * rot, c, rot, il);
+        }
+    }
+    if constexpr (FMT == KDA_KV_BF16) {
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            const int slot = lo + i * kRpp + r0;
+            if (slot < hi) {
+                *reinterpret_cast<uint4 *>(tile + kv_tile_off<kRow>(pt, slot, 2 * p.a)) = pack8(x[i]);
+                *reinterpret_cast<uint4 *>(tile + kv_tile_off<kRow>(pt, slot, 2 * p.b)) = pack8(x[i] + 8);
+            }
+        }
+    } else {
+        // The maximum goes by the bits of |x|: an infinity or a NaN wins, so that a block that holds
+        // one reads as NaN instead of losing it.
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i)
+            if (lo + i * kRpp + r0 < hi)
+#pragma unroll
+                for (int j = 0; j < 16; ++j) top = max(top, __float_as_uint(x[i][j]) & 0x7FFFFFFFu);
+        top = __reduce_max_sync(0xFFFFFFFFu, top);
+        __shared__ uint32_t tops[NT / 32];
+        if (tid % 32 == 0) tops[tid / 32] = top;
+        float *scale_at = reinterpret_cast<float *>(rec + 2 * pt * kRow) + (is_v ? 1 : 0);
+        const uint32_t s_old = lo > 0 ? __float_as_uint(*scale_at) & 0x7FFFFFFFu : 0u;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < NT / 32; ++i) top = max(top, tops[i]);
+        const uint32_t s_bits = max(__float_as_uint(__fdiv_rn(__uint_as_float(top), 127.f)) & 0x7FFFFFFFu, s_old);
+        const float sc = __uint_as_float(s_bits);
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            const int slot = lo + i * kRpp + r0;
+            if (slot < hi) {
+                *reinterpret_cast<uint2 *>(tile + kv_tile_off<kRow>(pt, slot, p.a)) = codes8(x[i], sc);
+                *reinterpret_cast<uint2 *>(tile + kv_tile_off<kRow>(pt, slot, p.b)) = codes8(x[i] + 8, sc);
+            }
+        }
+        if (lo > 0 && s_bits != s_old) {
+            const float so = __uint_as_float(s_old);
+            for (int i = tid; i < lo * (kRow / 8); i += NT) {   // rows below lo: whole, in any order of units
+                const int slot = i / (kRow / 8);
+                uint2 *at = reinterpret_cast<uint2 *>(tile + kv_tile_off<kRow>(pt, slot, 8 * (i % (kRow / 8))));
+                const uint2 u = *at;
+                float v[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = __fmul_rn((float)(int8_t)((j < 4 ? u.x : u.y) >> (8 * (j & 3))), so);
+                *at = codes8(v, sc);
+            }
+        }
+        if (tid == 0) *scale_at = sc;
+    }
+}
+
+// 16 values of a cache row as fp32: unit c of 16 elements.
+template <int FMT, int D>
+__device__ __forceinline__ void read16(const uint8_t *tile, int pt, int slot, int c, float sc, float (&x)[16]) {
+    constexpr int kRow = kKvRow<FMT, D>;
+    if constexpr (FMT == KDA_KV_I8) {
+        const uint4 u = *reinterpret_cast<const uint4 *>(tile + kv_tile_off<kRow>(pt, slot, 16 * c));
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int j = 0; j < 16; ++j) x[j] = __fmul_rn((float)(int8_t)(w[j >> 2] >> (8 * (j & 3))), sc);
+    } else {
+        load8(reinterpret_cast<const __nv_bfloat16 *>(tile + kv_tile_off<kRow>(pt, slot, 32 * c)), x);
+        load8(reinterpret_cast<const __nv_bfloat16 *>(tile + kv_tile_off<kRow>(pt, slot, 32 * c + 16)), x + 8);
+    }
+}
+
+// Cached ranges as values: one thread takes 16 elements of K and of V of one (row, head), so that a
+// warp writes whole lines of both outputs.
+template <int FMT, int D, class TOUT>
+__global__ void __launch_bounds__(256) kv_gather_kernel(KvGatherArgs a) {
+    constexpr int kTpr = D / 16, kRow = kKvRow<FMT, D>;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int c = (int)(i % kTpr);
+    const int64_t rh = i / kTpr, row = rh / a.kv.Hkv;
+    const int head = (int)(rh % a.kv.Hkv);
+    if (row >= a.T_out) return;
+    const int pt = a.kv.page_tokens;
+    const int s = kv_find(a.nseq, row, [&](int m) { return (int64_t)__ldg(a.cu_out + m); });
+    const int64_t at = __ldg(a.cu_out + s), end = __ldg(a.cu_out + s + 1), first = __ldg(a.begin + s);
+    if (row < at || row >= end) return;                 // rows that no sequence owns stay as they are
+    const int64_t tok = first + (row - at);
+    if (first < 0 || tok >= (int64_t)a.kv.max_pages * pt) {
+        flag_status(a.kv.status, KDA_DEV_BAD_META);
+        return;
+    }
+    const int block = (int)(tok / pt), slot = (int)(tok % pt);
+    const uint8_t *rec = kv_record(a.kv, __ldg(a.kv.table + (int64_t)s * a.kv.max_pages + block), head);
+    if (!rec) return;
+    float ks = 1.f, vs = 1.f;
+    if constexpr (FMT == KDA_KV_I8) {
+        const float2 sc = *reinterpret_cast<const float2 *>(rec + 2 * pt * kRow);
+        ks = sc.x, vs = sc.y;
+    }
+    float x[16], y[16];
+    read16<FMT, D>(rec, pt, slot, c, ks, x);
+    read16<FMT, D>(rec + pt * kRow, pt, slot, c, vs, y);
+    TOUT *ko = static_cast<TOUT *>(a.k_out) + rh * D + 16 * c, *vo = static_cast<TOUT *>(a.v_out) + rh * D + 16 * c;
+    store8(ko, x);
+    store8(ko + 8, x + 8);
+    store8(vo, y);
+    store8(vo + 8, y + 8);
+}
+
+template <int FMT, int D, class TIN, int NT, int ROWS>
+cudaError_t append(const KvAppendArgs &a, cudaStream_t st) {
+    // about four pairs of eights a thread for the queries' CTAs
+    const int32_t q_toks = a.q ? max(1, 4 * NT / (a.Hq * (D / 16))) : 1;
+    const int64_t q_ctas = a.q ? (a.T_tot + q_toks - 1) / q_toks : 0;
+    const int64_t items = a.max_q == 1 ? a.T_tot : a.T_tot / a.kv.page_tokens + 2 * (int64_t)a.nseq;
+    const int64_t grid = q_ctas + 2 * items * a.kv.Hkv;
+    if (grid > INT32_MAX) return cudaErrorInvalidValue;
+    kv_append_kernel<FMT, D, TIN, NT, ROWS><<<(unsigned)grid, NT, 0, st>>>(a, (int32_t)q_ctas, q_toks, items);
+    return cudaGetLastError();
+}
+
+// Few new tokens a sequence leave all but one row of a block's threads idle, so small CTAs take
+// them; a CTA of 256 holds a whole block of 128 new rows.
+template <int FMT, int D, class TIN>
+cudaError_t append_sized(const KvAppendArgs &a, cudaStream_t st) {
+    if (a.max_q <= 8) return append<FMT, D, TIN, 64, 1>(a, st);
+    return append<FMT, D, TIN, 256, kKvMaxPageTokens * (D / 16) / 256>(a, st);
+}
+
+template <int FMT, int D>
+cudaError_t gather(const KvGatherArgs &a, cudaStream_t st) {
+    const int64_t n = a.T_out * a.kv.Hkv * (D / 16), grid = (n + 255) / 256;
+    if (grid > INT32_MAX) return cudaErrorInvalidValue;
+    if (a.dtype == KDA_F32) kv_gather_kernel<FMT, D, float><<<(unsigned)grid, 256, 0, st>>>(a);
+    else kv_gather_kernel<FMT, D, __nv_bfloat16><<<(unsigned)grid, 256, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_kv_append(const KvAppendArgs &a, cudaStream_t s) {
+    const bool i8 = a.kv.fmt == KDA_KV_I8, f32 = a.dtype == KDA_F32;
+    if (a.kv.d == 128) {
+        if (i8) return f32 ? append_sized<KDA_KV_I8, 128, float>(a, s) : append_sized<KDA_KV_I8, 128, __nv_bfloat16>(a, s);
+        return f32 ? append_sized<KDA_KV_BF16, 128, float>(a, s) : append_sized<KDA_KV_BF16, 128, __nv_bfloat16>(a, s);
+    }
+    if (i8) return f32 ? append_sized<KDA_KV_I8, 64, float>(a, s) : append_sized<KDA_KV_I8, 64, __nv_bfloat16>(a, s);
+    return f32 ? append_sized<KDA_KV_BF16, 64, float>(a, s) : append_sized<KDA_KV_BF16, 64, __nv_bfloat16>(a, s);
+}
+
+cudaError_t launch_kv_gather(const KvGatherArgs &a, cudaStream_t s) {
+    if (a.kv.d == 128) return a.kv.fmt == KDA_KV_I8 ? gather<KDA_KV_I8, 128>(a, s) : gather<KDA_KV_BF16, 128>(a, s);
+    return a.kv.fmt == KDA_KV_I8 ? gather<KDA_KV_I8, 64>(a, s) : gather<KDA_KV_BF16, 64>(a, s);
+}
+
+}  // namespace kda
