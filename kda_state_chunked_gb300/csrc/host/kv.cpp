@@ -9,6 +9,8 @@
 
 namespace {
 
+constexpr int64_t kMaxTokens = 1 << 30;   // of a sequence: the kernels' positions and their differences fit int32
+
 int64_t elem_size(int32_t dtype) { return dtype == KDA_BF16 ? 2 : 4; }
 int64_t align_up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -31,7 +33,7 @@ bool valid_rows(const void *p, int64_t stride, int32_t H, int32_t d, int32_t dty
 bool cache_view(const kda_pool *pool, int32_t Hkv, int32_t d, int32_t fmt, int32_t page_tokens, void *pool_base,
                 const int32_t *table, int32_t max_pages, int32_t *status, kda::KvView &v) {
     if (!pool || !valid_cache(Hkv, d, fmt, page_tokens) || !pool_base || !aligned16(pool_base) || max_pages < 0 ||
-        (max_pages > 0 && !table) || !status || (int64_t)max_pages * page_tokens > INT32_MAX - 1024)
+        (max_pages > 0 && !table) || !status || (int64_t)max_pages * page_tokens > kMaxTokens)
         return false;
     const int64_t rec = record_bytes(d, fmt, page_tokens);
     if (pool->page_bytes < rec * Hkv) return false;
@@ -54,6 +56,13 @@ bool valid_batch(int32_t nseq, int64_t T_tot, int32_t max_q, int32_t dtype) {
 }
 
 int status_of(cudaError_t e) { return e == cudaSuccess ? KDA_OK : KDA_ECUDA; }
+
+// Rows of a tile.  The register kernel holds 16 rows and is bound by the cache's bytes; with more
+// rows a sequence it would read the cache again for every 16, so the tensor-memory kernel takes
+// them.  float32 calls stay on the register kernel: its products split an operand into terms.
+int32_t attn_rows(int32_t dtype, int32_t max_q, int32_t G) {
+    return dtype == KDA_F32 || (int64_t)max_q * G <= kda::kAttnDecodeRows ? kda::kAttnDecodeRows : kda::kAttnPrefillRows;
+}
 
 // Workspace of an attention call: [AttnSplit per CTA][partial results].
 struct AttnWs {
@@ -122,7 +131,7 @@ int64_t kda_attn_workspace_bytes(int32_t Hq, int32_t Hkv, int32_t d, int32_t dty
                                  int32_t max_q) {
     if (Hkv <= 0 || Hq <= 0 || Hq > 4096 || Hq % Hkv || (d != 64 && d != 128) || !valid_batch(nseq, T_tot, max_q, dtype))
         return KDA_EINVAL;
-    return attn_ws(d, kda::kAttnDecodeRows).total;
+    return attn_ws(d, attn_rows(dtype, max_q, Hq / Hkv)).total;
 }
 
 int kda_attn_paged(const kda_pool *pool, int32_t Hq, int32_t Hkv, int32_t d, int32_t dtype, int32_t fmt,
@@ -144,9 +153,11 @@ int kda_attn_paged(const kda_pool *pool, int32_t Hq, int32_t Hkv, int32_t d, int
     a.Hq = Hq; a.G = Hq / Hkv; a.dtype = dtype; a.nseq = nseq; a.max_q = max_q; a.T_tot = T_tot;
     a.cu_q = cu_q; a.kv_len = kv_len;
     a.q = q; a.q_stride = q_stride;
-    a.scale = scale; a.window = window; a.sinks = sinks;
+    // a window (or sinks) as long as a sequence can be is none (are all of it)
+    const int32_t longest = max_pages * page_tokens;
+    a.scale = scale; a.window = window >= longest ? 0 : window; a.sinks = std::min(sinks, longest);
     a.o = o; a.lse = lse;
-    const int32_t rows = kda::kAttnDecodeRows;
+    const int32_t rows = attn_rows(dtype, max_q, a.G);
     const AttnWs w = attn_ws(d, rows);
     // the most units that the call can have bounds the CTAs worth launching
     const int64_t tiles = T_tot * a.G / rows + nseq;
@@ -154,7 +165,8 @@ int kda_attn_paged(const kda_pool *pool, int32_t Hq, int32_t Hkv, int32_t d, int
     a.ctas = (int32_t)std::min<int64_t>(kda::kAttnMaxCtas, std::max<int64_t>(1, tiles * Hkv * std::max<int64_t>(1, units)));
     a.split = static_cast<kda::AttnSplit *>(workspace);
     a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + w.o_part);
-    return status_of(kda::launch_attn_decode(a, static_cast<cudaStream_t>(stream)));
+    return status_of(rows == kda::kAttnDecodeRows ? kda::launch_attn_decode(a, static_cast<cudaStream_t>(stream))
+                                                  : kda::launch_attn_prefill(a, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -194,7 +194,7 @@ struct KvGatherArgs {
 // over the CTAs; an item that several CTAs touch is joined afterwards from their partial results.
 constexpr int kAttnUnit = 128;
 constexpr int kAttnDecodeRows = 16;    // rows of a tile of the register kernel
-constexpr int kAttnPrefillRows = 128;  // rows of a tile of the tensor-memory kernel
+constexpr int kAttnPrefillRows = 256;  // rows of a tile of the tensor-memory kernel
 
 // An item that starts in a CTA and ends in a later one (one per CTA at most).
 struct AttnSplit {
@@ -219,7 +219,6 @@ struct AttnArgs {
     int32_t ctas;                 // CTAs the units are shared out over
     float *part;                  // [ctas][2][rows][d + 2]: m, l and unnormalised o of partial items
     AttnSplit *split;             // [ctas]
-    int64_t *plan;                // prefill: units before each row tile, of all heads
 };
 // CTAs of the attention kernels: one per SM.
 constexpr int kAttnMaxCtas = 152;
@@ -247,5 +246,6 @@ cudaError_t launch_ckpt_dequantize(const Q8Args &a, cudaStream_t s);
 cudaError_t launch_kv_append(const KvAppendArgs &a, cudaStream_t s);
 cudaError_t launch_kv_gather(const KvGatherArgs &a, cudaStream_t s);
 cudaError_t launch_attn_decode(const AttnArgs &a, cudaStream_t s);
+cudaError_t launch_attn_prefill(const AttnArgs &a, cudaStream_t s);
 
 }  // namespace kda
