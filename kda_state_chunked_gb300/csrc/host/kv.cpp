@@ -68,10 +68,11 @@ int32_t attn_rows(int32_t dtype, int32_t max_q, int32_t G) {
 struct AttnWs {
     int64_t o_part, total;
 };
+int32_t attn_ctas(int32_t rows) { return rows == kda::kAttnDecodeRows ? kda::kAttnMaxCtas : kda::kAttnSms; }
 AttnWs attn_ws(int32_t d, int32_t rows) {
     AttnWs w;
-    w.o_part = align_up(kda::kAttnMaxCtas * (int64_t)sizeof(kda::AttnSplit), 256);
-    w.total = w.o_part + (int64_t)kda::kAttnMaxCtas * 2 * rows * (d + 4) * 4;
+    w.o_part = align_up(attn_ctas(rows) * (int64_t)sizeof(kda::AttnSplit), 256);
+    w.total = w.o_part + (int64_t)attn_ctas(rows) * 2 * rows * (d + 4) * 4;
     return w;
 }
 
@@ -161,8 +162,8 @@ int kda_attn_paged(const kda_pool *pool, int32_t Hq, int32_t Hkv, int32_t d, int
     const AttnWs w = attn_ws(d, rows);
     // the most units that the call can have bounds the CTAs worth launching
     const int64_t tiles = T_tot * a.G / rows + nseq;
-    const int64_t units = ((int64_t)max_pages * page_tokens + kda::kAttnUnit - 1) / kda::kAttnUnit;
-    a.ctas = (int32_t)std::min<int64_t>(kda::kAttnMaxCtas, std::max<int64_t>(1, tiles * Hkv * std::max<int64_t>(1, units)));
+    const int64_t units = ((int64_t)max_pages * page_tokens + kda::kAttnMinUnit - 1) / kda::kAttnMinUnit;
+    a.ctas = (int32_t)std::min<int64_t>(attn_ctas(rows), std::max<int64_t>(1, tiles * Hkv * std::max<int64_t>(1, units)));
     a.split = static_cast<kda::AttnSplit *>(workspace);
     a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + w.o_part);
     return status_of(rows == kda::kAttnDecodeRows ? kda::launch_attn_decode(a, static_cast<cudaStream_t>(stream))

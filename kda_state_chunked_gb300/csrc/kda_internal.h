@@ -190,9 +190,9 @@ struct KvGatherArgs {
 
 // Attention over a paged cache.  A row tile is a run of (token, head of the group) query rows of
 // one sequence and one key/value head; an item is a row tile's work over the tokens it sees, cut
-// into units of kAttnUnit cached tokens.  The units of all items, in order, are shared out evenly
+// into units of 64 or 128 cached tokens.  The units of all items, in order, are shared out evenly
 // over the CTAs; an item that several CTAs touch is joined afterwards from their partial results.
-constexpr int kAttnUnit = 128;
+constexpr int kAttnMinUnit = 64;
 constexpr int kAttnDecodeRows = 16;    // rows of a tile of the register kernel
 constexpr int kAttnPrefillRows = 256;  // rows of a tile of the tensor-memory kernel
 
@@ -220,8 +220,9 @@ struct AttnArgs {
     float *part;                  // [ctas][2][rows][d + 2]: m, l and unnormalised o of partial items
     AttnSplit *split;             // [ctas]
 };
-// CTAs of the attention kernels: one per SM.
-constexpr int kAttnMaxCtas = 152;
+// CTAs of the attention kernels: two an SM for the register kernel, one for the other.
+constexpr int kAttnSms = 152;
+constexpr int kAttnMaxCtas = 2 * kAttnSms;
 
 // Kernel launchers (defined in the .cu files).
 cudaError_t launch_prefill_split(const SplitArgs &a, const SplitPlan &plan, cudaStream_t s);

@@ -1,8 +1,8 @@
 // What the two attention kernels share: row tiles, the tokens each sees, the even split of all
 // their units over the CTAs, and the joining of partial results.
 //
-// The split: every row tile of every sequence and head is an item of >= 1 units of kAttnUnit
-// cached tokens (an item that sees nothing has one, which writes its zeros).  With W units in all,
+// The split: every row tile of every sequence and head is an item of >= 1 units of UNIT cached
+// tokens (an item that sees nothing has one, which writes its zeros).  With W units in all,
 // CTA c takes units [c W / C, (c + 1) W / C) of the list ordered by sequence, row tile, head: each
 // CTA has the same work however ragged the lengths are, and the lengths stay on the device.
 #pragma once
@@ -23,7 +23,7 @@ struct Tile {
     KvSeq q;
     int32_t row0, nrows;
     int32_t pmin, pmax;           // positions of its first and last row's token
-    int32_t first, sinks, units;  // tile of 128 tokens where its window begins, sink tiles before it, units
+    int32_t first, sinks, units;  // unit where its window begins, sink units before that, units in all
 };
 
 template <int ROWS>
@@ -31,7 +31,7 @@ __device__ __forceinline__ int32_t tiles_of(const AttnArgs &a, const KvSeq &q) {
     return (int32_t)(((int64_t)q.n * a.G + ROWS - 1) / ROWS);
 }
 
-template <int ROWS>
+template <int ROWS, int UNIT>
 __device__ __forceinline__ Tile make_tile(const AttnArgs &a, int32_t s, const KvSeq &q, int32_t rt) {
     Tile t;
     t.s = s;
@@ -49,16 +49,17 @@ __device__ __forceinline__ Tile make_tile(const AttnArgs &a, int32_t s, const Kv
         return t;
     }
     if (a.window > 0) {
-        t.first = max(0, t.pmin - a.window + 1) / kAttnUnit;
-        t.sinks = min(t.first, (int32_t)(((int64_t)a.sinks + kAttnUnit - 1) / kAttnUnit));
+        t.first = max(0, t.pmin - a.window + 1) / UNIT;
+        t.sinks = min(t.first, (a.sinks + UNIT - 1) / UNIT);
     }
-    t.units = t.sinks + t.pmax / kAttnUnit - t.first + 1;
+    t.units = t.sinks + t.pmax / UNIT - t.first + 1;
     return t;
 }
 
 // First token of the tile's unit u.
+template <int UNIT>
 __device__ __forceinline__ int32_t unit_token(const Tile &t, int32_t u) {
-    return (u < t.sinks ? u : t.first + u - t.sinks) * kAttnUnit;
+    return (u < t.sinks ? u : t.first + u - t.sinks) * UNIT;
 }
 
 // Whether position p sees token j.
@@ -76,6 +77,12 @@ __device__ __forceinline__ bool all_see(const AttnArgs &a, const Tile &t, int32_
 // CTA that holds unit u of W.
 __device__ __forceinline__ int32_t cta_of(int64_t u, int64_t W, int32_t C) {
     return (int32_t)(((u + 1) * C - 1) / W);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 template <int D>

@@ -7,10 +7,11 @@
 // M = 16 of a warp-level matrix product, so a cached byte is read once for all of them; wider
 // tensor-memory tiles would stand empty here.
 //
-// One CTA of 8 warps an SM.  A unit is 128 tokens; warp w takes tokens 16 w .. 16 w + 15 of it, which
-// lie in one page, and runs alone: it copies its own tokens of later units into its own ring of
-// shared-memory stages (bulk copies: a page's rows are contiguous) and keeps its own maxima, sums
-// and 16 x D accumulators.  The warps meet only at an item's end.
+// Two CTAs of 4 warps an SM, so that one streams while the other joins its warps or starts an item.
+// A warp takes a step of a unit's tokens (32 of the 8-bit cache, 16 of the 16-bit one: groups of 16
+// tokens, each in one page) and runs alone: it copies its own tokens of later units into its own
+// ring of shared-memory stages (bulk copies: a page's rows are contiguous) and keeps its own
+// maxima, sums and 16 x D accumulators.  The warps meet only at an item's end.
 //
 // 8-bit cache: codes c become fp16 exactly (the byte under the exponent of 1024, less 1152), a
 // query row is scaled by a power of two into fp16's range, so q . c carries no rounding beyond
@@ -28,27 +29,29 @@ namespace {
 
 using namespace attn;
 
-constexpr int kWarps = 8, kStep = 16;
+constexpr int kWarps = 4;
 constexpr float kPScale = 8192.f;                     // probabilities' scale in fp16
 constexpr float kMinRef = 0x1p-100f;
 
 template <int FMT, int D>
 struct Shape {
     static constexpr int row = kKvRow<FMT, D>;
-    static constexpr int tile = row * kStep;          // K or V bytes of a step
-    static constexpr int stage = 2 * tile + 128;
-    static constexpr int stages = FMT == KDA_KV_I8 ? (D == 128 ? 4 : 6) : (D == 128 ? 2 : 4);
+    static constexpr int step = FMT == KDA_KV_I8 ? 32 : 16, groups = step / 16, unit = kWarps * step;
+    static constexpr int group = row * 16;            // K or V bytes of 16 tokens
+    static constexpr int tile = groups * group;
+    static constexpr int stage = 2 * tile + 128;      // keys, values, 16 bytes of scales a group
+    static constexpr int stages = D == 128 ? 2 : 4;
 };
 
 template <int FMT, int D, int NT>
 struct Smem {
     static constexpr int ring = kWarps * Shape<FMT, D>::stages * Shape<FMT, D>::stage;
-    static constexpr int o_acc = ring;                                   // [8][16][D] fp32
-    static constexpr int o_ml = o_acc + kWarps * 16 * D * 4;             // [2][8][16][2] fp32
+    static constexpr int o_acc = ring;                                   // [kWarps][16][D] fp32
+    static constexpr int o_ml = o_acc + kWarps * 16 * D * 4;             // [2][kWarps][16][2] fp32
     static constexpr int o_q = o_ml + 2 * kWarps * 16 * 8;               // fragments of split queries
     static constexpr int o_bar = o_q + (NT > 1 ? NT * (D / 16) * 512 : 0);
-    static constexpr int o_tok = o_bar + kWarps * Shape<FMT, D>::stages * 8;
-    static constexpr int o_misc = o_tok + kWarps * Shape<FMT, D>::stages * 4;
+    static constexpr int o_live = o_bar + kWarps * Shape<FMT, D>::stages * 8;
+    static constexpr int o_misc = o_live + kWarps * Shape<FMT, D>::stages * 4;
     static constexpr int total = o_misc + 128;
 };
 
@@ -110,37 +113,37 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t (&out)[NT]) {
 // fragment stores of a warp fall into different banks.
 template <int FMT, int D>
 __device__ __forceinline__ int acc_unit(int row, int u) {
-    if constexpr (FMT == KDA_KV_BF16) return u ^ ((row & (D / 8 - 1) & 7) << 1);
-    else if constexpr (D == 128) return u ^ (((u >> 3) & 3) + 4 * (row & 1));
-    else return u ^ (((u >> 3) & 1) + 2 * (row & 1));
+    return FMT == KDA_KV_BF16 ? u ^ ((row & 7) << 1) : u ^ ((row & 1) << 2);
 }
 
-// Where a warp's loads stand: the unit whose copy comes next, its page id already on the way.
+// Where a warp's loads stand: the unit whose copy comes next; lane i's group i of it, its page id
+// already on the way.
 struct Cursor {
     Tile t;
     int32_t h, u;
-    int32_t tok;                  // first token of this warp's step, -1: no row sees any of them
+    bool want;
     int32_t page, slot;
 };
 
 template <int FMT, int D, int NT>
-__global__ void __launch_bounds__(kWarps * 32, 1) attn_decode_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, 2) attn_decode_kernel(const __grid_constant__ AttnArgs a) {
     using S = Shape<FMT, D>;
     using M = Smem<FMT, D, NT>;
     constexpr int kKs = D / 16;   // 16-wide slices of a row
     constexpr int kNt = D / 8;    // 8-wide output tiles
+    constexpr int kGr = S::groups;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = ptx::smem_align1024(smem_raw);
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane >> 2, t = lane & 3;
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + M::o_bar) + warp * S::stages;
-    int32_t *toks = reinterpret_cast<int32_t *>(sm + M::o_tok) + warp * S::stages;
+    volatile uint32_t *live = reinterpret_cast<uint32_t *>(sm + M::o_live) + warp * S::stages;
     uint8_t *ring = sm + warp * S::stages * S::stage;
     float *ml = reinterpret_cast<float *>(sm + M::o_ml);   // of this item; the last one's may still be read
     int ml_next = kWarps * 32;
     float *acc = reinterpret_cast<float *>(sm + M::o_acc);
     uint32_t *qfrag = reinterpret_cast<uint32_t *>(sm + M::o_q);
     volatile int *err = reinterpret_cast<int *>(sm + M::o_misc);
-    int64_t *share = reinterpret_cast<int64_t *>(sm + M::o_misc + 16);   // [8] warp sums, then the start
+    int64_t *share = reinterpret_cast<int64_t *>(sm + M::o_misc + 16);   // warps' sums, then the start
 
     if (lane == 0)
         for (int i = 0; i < S::stages; ++i) ptx::mbar_init(&bars[i], 1);
@@ -155,7 +158,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attn_decode_kernel(const __gri
         const KvSeq q = seq(s);
         const int n = tiles_of<kAttnDecodeRows>(a, q);
         int64_t w = 0;
-        for (int i = 0; i < n; ++i) w += make_tile<kAttnDecodeRows>(a, s, q, i).units;
+        for (int i = 0; i < n; ++i) w += make_tile<kAttnDecodeRows, S::unit>(a, s, q, i).units;
         return w * Hkv;
     };
     auto block_sum = [&](int64_t v, int64_t &before) {   // exclusive prefix over threads; returns the sum
@@ -189,7 +192,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attn_decode_kernel(const __gri
     int32_t s0 = 0;
     int64_t left0 = 0;   // units before `begin` in sequence s0
     {
-        int64_t *found = share + 8;
+        int64_t *found = share + kWarps;
         int64_t base = 0;
         for (int s = 0; s < a.nseq; s += kWarps * 32) {
             const int64_t w = s == 0 ? mine0 : (s + tid < a.nseq ? seq_units(s + tid) : 0);
@@ -211,7 +214,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attn_decode_kernel(const __gri
         const KvSeq q = seq(s0);
         int rt = 0;
         for (;; ++rt) {
-            t0 = make_tile<kAttnDecodeRows>(a, s0, q, rt);
+            t0 = make_tile<kAttnDecodeRows, S::unit>(a, s0, q, rt);
             if (left0 < (int64_t)t0.units * Hkv) break;
             left0 -= (int64_t)t0.units * Hkv;
         }
@@ -224,44 +227,45 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attn_decode_kernel(const __gri
         if (++h < Hkv) return;
         h = 0;
         if (x.rt + 1 < x.tiles) {
-            x = make_tile<kAttnDecodeRows>(a, x.s, x.q, x.rt + 1);
+            x = make_tile<kAttnDecodeRows, S::unit>(a, x.s, x.q, x.rt + 1);
             return;
         }
         int s = x.s + 1;
         KvSeq q = seq(s);
         while (q.n == 0 && s + 1 < a.nseq) q = seq(++s);
-        x = make_tile<kAttnDecodeRows>(a, s, q, 0);
+        x = make_tile<kAttnDecodeRows, S::unit>(a, s, q, 0);
     };
 
     // ---- loads
     const int pt = a.kv.page_tokens;
     auto aim = [&](Cursor &c) {   // this warp's step of the cursor's unit
-        const int32_t j = unit_token(c.t, c.u) + warp * kStep;
-        c.tok = -1;
-        if (!any_sees(a, c.t, j, kStep)) return;
-        c.tok = j;
+        const int32_t j = unit_token<S::unit>(c.t, c.u) + warp * S::step + lane * 16;
+        c.want = lane < kGr && any_sees(a, c.t, j, 16);
+        if (!c.want) return;
         const int32_t b = j / pt;
         c.slot = j - b * pt;
         c.page = __ldg(a.kv.table + (int64_t)c.t.s * a.kv.max_pages + b);
     };
     auto load = [&](const Cursor &c, int stage) {
-        if (lane != 0) return;
-        const uint8_t *rec = c.tok < 0 ? nullptr : kv_record(a.kv, c.page, c.h);
-        toks[stage] = rec ? c.tok : -1;
-        if (!rec) {
-            ptx::mbar_arrive(&bars[stage]);
-            return;
+        const uint8_t *rec = c.want ? kv_record(a.kv, c.page, c.h) : nullptr;
+        const uint32_t there = __ballot_sync(0xFFFFFFFFu, rec != nullptr);
+        if (lane == 0) {
+            live[stage] = there;
+            ptx::mbar_arrive_expect_tx(&bars[stage], __popc(there) * (2 * S::group + (FMT == KDA_KV_I8 ? 16 : 0)));
         }
-        uint8_t *dst = ring + stage * S::stage;
-        constexpr uint32_t kLine = S::row < 128 ? S::row : 128, kRun = kLine * kStep;
-        ptx::mbar_arrive_expect_tx(&bars[stage], 2 * S::tile + (FMT == KDA_KV_I8 ? 16 : 0));
+        __syncwarp();
+        if (!rec) return;
+        // a group's lines follow one another in the page; a stage has them by line block, like a page
+        constexpr uint32_t kLine = S::row < 128 ? S::row : 128, kRun = kLine * 16;
+        uint8_t *dst = ring + stage * S::stage + lane * kRun;
 #pragma unroll
         for (int v = 0; v < 2; ++v)
 #pragma unroll
-            for (int b = 0; b < S::tile / (int)kRun; ++b)
-                ptx::bulk_load(dst + v * S::tile + b * kRun, rec + v * pt * S::row + b * pt * 128 + c.slot * kLine, kRun,
+            for (int b = 0; b < S::group / (int)kRun; ++b)
+                ptx::bulk_load(dst + v * S::tile + b * kGr * kRun, rec + v * pt * S::row + b * pt * 128 + c.slot * kLine, kRun,
                                &bars[stage]);
-        if (FMT == KDA_KV_I8) ptx::bulk_load(dst + 2 * S::tile, rec + 2 * pt * S::row, 16, &bars[stage]);
+        if (FMT == KDA_KV_I8)
+            ptx::bulk_load(ring + stage * S::stage + 2 * S::tile + 16 * lane, rec + 2 * pt * S::row, 16, &bars[stage]);
     };
     Cursor cur;
     cur.t = t0;
@@ -366,161 +370,162 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attn_decode_kernel(const __gri
         for (; u < u_last; ++u, --left) {
             const bool ok = __all_sync(0xFFFFFFFFu, ptx::mbar_wait(&bars[stage], phase, err));
             if (!ok) flag_status(a.kv.status, KDA_DEV_TIMEOUT);
-            const int32_t j0 = ok ? toks[stage] : -1;
-            if (j0 >= 0) {
+            const uint32_t there = ok ? live[stage] : 0u;
+            if (there) {
+                const int32_t j0 = unit_token<S::unit>(tile, u) + warp * S::step;
                 const uint8_t *buf = ring + stage * S::stage;
                 const uint32_t kb = ptx::smem_u32(buf), vb = kb + S::tile;
-                float sc[2] = {rs[0], rs[1]}, vs = 1.f;
-                if (FMT == KDA_KV_I8) {
-                    const float2 f = *reinterpret_cast<const float2 *>(buf + 2 * S::tile);
-                    sc[0] *= f.x, sc[1] *= f.x, vs = f.y;
+                float sc[kGr][2], vs[kGr];   // a group's score factors (by row half) and value scale
+#pragma unroll
+                for (int y = 0; y < kGr; ++y) {
+                    sc[y][0] = rs[0], sc[y][1] = rs[1], vs[y] = 0.f;
+                    if (FMT == KDA_KV_I8) {
+                        const float2 f = *reinterpret_cast<const float2 *>(buf + 2 * S::tile + 16 * y);
+                        if (there >> y & 1u) sc[y][0] *= fabsf(f.x), sc[y][1] *= fabsf(f.x), vs[y] = fabsf(f.y);
+                    }
                 }
-                // ---- scores: c[n-tile][..], even and odd slices apart for shorter chains
-                float c[2][2][4] = {};
+                // ---- scores: c[n] of tokens j0 + 8 n ..
+                float c[2 * kGr][4] = {};
                 const int mr = lane & 7, mm = lane >> 3;   // row and matrix whose address this lane gives
+                auto slice = [&](float (&d)[4], int k, uint32_t b0, uint32_t b1) {
+                    if constexpr (NT == 1) {
+                        mma<FMT>(d, qa[k], b0, b1);
+                    } else {
 #pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    if constexpr (FMT == KDA_KV_I8) {
+                        for (int z = NT - 1; z >= 0; --z) {
+                            const uint4 f = *reinterpret_cast<const uint4 *>(qfrag + ((z * kKs + k) * 32 + lane) * 4);
+                            const uint32_t qf[4] = {f.x, f.y, f.z, f.w};
+                            mma<FMT>(d, qf, b0, b1);
+                        }
+                    }
+                };
+                if constexpr (FMT == KDA_KV_I8) {
 #pragma unroll
-                        for (int i = 0; i < kKs / 4; ++i) {
+                    for (int i = 0; i < kKs / 4; ++i)
+#pragma unroll
+                        for (int n = 0; n < 2 * kGr; ++n) {
                             uint32_t w[4];
-                            ldsm4(w, kb + kv_tile_off<S::row>(kStep, 8 * n + mr, 16 * (4 * i + mm)));
+                            ldsm4(w, kb + kv_tile_off<S::row>(S::step, 8 * n + mr, 16 * (4 * i + mm)));
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
                                 const uint32_t b = w[k] ^ 0x80808080u;
-                                const uint32_t b0 = half2_of<0x4140>(b), b1 = half2_of<0x4342>(b);
-                                if constexpr (NT == 1) {
-                                    mma<FMT>(c[n][k & 1], qa[4 * i + k], b0, b1);
-                                } else {
-#pragma unroll
-                                    for (int z = NT - 1; z >= 0; --z) {
-                                        const uint4 f = *reinterpret_cast<const uint4 *>(
-                                            qfrag + ((z * kKs + 4 * i + k) * 32 + lane) * 4);
-                                        const uint32_t qf[4] = {f.x, f.y, f.z, f.w};
-                                        mma<FMT>(c[n][k & 1], qf, b0, b1);
-                                    }
-                                }
+                                slice(c[n], 4 * i + k, half2_of<0x4140>(b), half2_of<0x4342>(b));
                             }
                         }
-                    } else {
+                } else {
 #pragma unroll
-                        for (int i = 0; i < kKs / 2; ++i) {
+                    for (int i = 0; i < kKs / 2; ++i)
+#pragma unroll
+                        for (int n = 0; n < 2 * kGr; ++n) {
                             uint32_t w[4];
-                            ldsm4(w, kb + kv_tile_off<S::row>(kStep, 8 * n + mr, 16 * (4 * i + mm)));
+                            ldsm4(w, kb + kv_tile_off<S::row>(S::step, 8 * n + mr, 16 * (4 * i + mm)));
 #pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                if constexpr (NT == 1) {
-                                    mma<FMT>(c[n][k], qa[2 * i + k], w[2 * k], w[2 * k + 1]);
-                                } else {
-#pragma unroll
-                                    for (int z = NT - 1; z >= 0; --z) {
-                                        const uint4 f = *reinterpret_cast<const uint4 *>(
-                                            qfrag + ((z * kKs + 2 * i + k) * 32 + lane) * 4);
-                                        const uint32_t qf[4] = {f.x, f.y, f.z, f.w};
-                                        mma<FMT>(c[n][k], qf, w[2 * k], w[2 * k + 1]);
-                                    }
-                                }
-                            }
+                            for (int k = 0; k < 2; ++k) slice(c[n], 2 * i + k, w[2 * k], w[2 * k + 1]);
                         }
-                    }
                 }
                 // ---- softmax: element (n, e) is row g + 8 (e / 2), token j0 + 8 n + 2 t + e % 2
-                const bool whole = all_see(a, tile, j0, kStep);   // rows not in use may see what they like
-                float p[2][4], top[2] = {-INFINITY, -INFINITY};
+                const bool whole = there == (1u << kGr) - 1u && all_see(a, tile, j0, S::step);
+                float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
+                for (int n = 0; n < 2 * kGr; ++n)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        p[n][e] = (c[n][0][e] + c[n][1][e]) * sc[e >> 1];
-                        if (!whole && !sees(a, pos[e >> 1], j0 + 8 * n + 2 * t + (e & 1))) p[n][e] = -INFINITY;
-                        top[e >> 1] = fmaxf(top[e >> 1], p[n][e]);
-                    }
+                    for (int e = 0; e < 4; ++e) c[n][e] *= sc[n >> 1][e >> 1];
+                if (!whole)   // rows not in use may see what they like
+#pragma unroll
+                    for (int n = 0; n < 2 * kGr; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (!(there >> (n >> 1) & 1u) || !sees(a, pos[e >> 1], j0 + 8 * n + 2 * t + (e & 1)))
+                                c[n][e] = -INFINITY;
+#pragma unroll
+                for (int n = 0; n < 2 * kGr; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) top[e >> 1] = fmaxf(top[e >> 1], c[n][e]);
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     top[r] = fmaxf(top[r], __shfl_xor_sync(0xFFFFFFFFu, top[r], 1));
                     top[r] = fmaxf(top[r], __shfl_xor_sync(0xFFFFFFFFu, top[r], 2));
                 }
-                const bool scaled = FMT == KDA_KV_I8 && vs > ref && vs < INFINITY;
+                float vmax = 0.f;
+                if (FMT == KDA_KV_I8)
+#pragma unroll
+                    for (int y = 0; y < kGr; ++y) vmax = vs[y] < INFINITY ? fmaxf(vmax, vs[y]) : vmax;
+                const bool scaled = FMT == KDA_KV_I8 && vmax > ref;
                 if (__any_sync(0xFFFFFFFFu, top[0] > m[0] || top[1] > m[1] || scaled)) {
                     float f[2];
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
                         const float mn = fmaxf(m[r], top[r]);
-                        f[r] = mn == -INFINITY ? 1.f : exp2f(m[r] - mn);
+                        f[r] = mn == -INFINITY ? 1.f : ex2(m[r] - mn);
                         l[r] *= f[r];
                         m[r] = mn;
                     }
                     if (scaled) {
-                        const float rn = fmaxf(vs, kMinRef), k = ref / rn;
+                        const float rn = fmaxf(vmax, kMinRef), k = ref / rn;
                         f[0] *= k, f[1] *= k;
                         ref = rn;
-                        inv_ref = 1.f / rn;
+                        inv_ref = kPScale / rn;
                     }
 #pragma unroll
                     for (int j = 0; j < kNt; ++j) o[j][0] *= f[0], o[j][1] *= f[0], o[j][2] *= f[1], o[j][3] *= f[1];
                 }
                 const float mx[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
-                float pv = 1.f;   // what a probability is multiplied by before it is rounded
-                if (FMT == KDA_KV_I8) pv = isfinite(vs) ? vs * inv_ref * kPScale : NAN;
-                uint32_t pa[4][NT];
+                bool strange = false;   // a value scale that is no number: 0 times it must stay 0
+                float pv[kGr];          // what a group's probabilities are multiplied by before rounding
 #pragma unroll
-                for (int n = 0; n < 2; ++n) {
+                for (int y = 0; y < kGr; ++y) {
+                    pv[y] = 1.f;
+                    if (FMT == KDA_KV_I8) {
+                        pv[y] = vs[y] * inv_ref;
+                        if (!(vs[y] < INFINITY)) strange = true, pv[y] = NAN;
+                    }
+                }
+                uint32_t pa[kGr][4][NT];
+#pragma unroll
+                for (int n = 0; n < 2 * kGr; ++n) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        p[n][e] = exp2f(p[n][e] - mx[e >> 1]);
-                        l[e >> 1] += p[n][e];
-                        if (FMT == KDA_KV_I8) p[n][e] = p[n][e] == 0.f ? 0.f : p[n][e] * pv;
+                        c[n][e] = ex2(c[n][e] - mx[e >> 1]);
+                        l[e >> 1] += c[n][e];
                     }
-                    split2<FMT, NT>(p[n][0], p[n][1], pa[2 * n]);
-                    split2<FMT, NT>(p[n][2], p[n][3], pa[2 * n + 1]);
+                    if (FMT == KDA_KV_I8) {
+                        if (strange)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) c[n][e] = c[n][e] == 0.f ? 0.f : c[n][e] * pv[n >> 1];
+                        else
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) c[n][e] *= pv[n >> 1];
+                    }
+                    split2<FMT, NT>(c[n][0], c[n][1], pa[n >> 1][2 * (n & 1)]);
+                    split2<FMT, NT>(c[n][2], c[n][3], pa[n >> 1][2 * (n & 1) + 1]);
                 }
                 // ---- values
-                auto values = [&](const uint32_t (&pf)[4][NT]) {
-                    if constexpr (FMT == KDA_KV_I8) {
-                        // a lane reads kNt neighbouring columns of its four tokens; output tile j
-                        // then stands for columns kNt n + j
-                        uint32_t w[4][kNt / 4];
+                auto values = [&]() {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int row = 2 * t + (i & 1) + 8 * (i >> 1);
-                            const uint8_t *at = buf + S::tile + kv_tile_off<S::row>(kStep, row, kNt * g);
-                            if constexpr (kNt == 16) {
-                                const uint4 x = *reinterpret_cast<const uint4 *>(at);
-                                w[i][0] = x.x, w[i][1] = x.y, w[i][2] = x.z, w[i][3] = x.w;
-                            } else {
-                                const uint2 x = *reinterpret_cast<const uint2 *>(at);
-                                w[i][0] = x.x, w[i][1] = x.y;
-                            }
-                        }
+                    for (int y = 0; y < kGr; ++y) {
 #pragma unroll
-                        for (int i = 0; i < kNt / 4; ++i) {
-                            uint32_t b[4][2];
+                        for (int i = 0; i < S::row / 32; ++i) {
+                            uint32_t w[4];   // (tokens 0-7, 8-15) of 16-byte units 2 i and 2 i + 1
+                            ldsm4t(w, vb + kv_tile_off<S::row>(S::step, 16 * y + 8 * (mm & 1) + mr, 16 * (2 * i + (mm >> 1))));
 #pragma unroll
-                            for (int y = 0; y < 2; ++y) {
-                                const uint32_t lo = __byte_perm(w[2 * y][i], w[2 * y + 1][i], 0x5140) ^ 0x80808080u;
-                                const uint32_t hi = __byte_perm(w[2 * y][i], w[2 * y + 1][i], 0x7362) ^ 0x80808080u;
-                                b[0][y] = half2_of<0x4140>(lo);
-                                b[1][y] = half2_of<0x4342>(lo);
-                                b[2][y] = half2_of<0x4140>(hi);
-                                b[3][y] = half2_of<0x4342>(hi);
-                            }
+                            for (int x = 0; x < 2; ++x) {
+                                if constexpr (FMT == KDA_KV_I8) {
+                                    // a register holds columns 2 g, 2 g + 1 of two tokens: the even ones
+                                    // make one output tile, the odd ones the next
+                                    const uint32_t b0 = w[2 * x] ^ 0x80808080u, b1 = w[2 * x + 1] ^ 0x80808080u;
 #pragma unroll
-                            for (int z = NT - 1; z >= 0; --z) {
-                                const uint32_t f[4] = {pf[0][z], pf[1][z], pf[2][z], pf[3][z]};
+                                    for (int z = NT - 1; z >= 0; --z) {
+                                        const uint32_t f[4] = {pa[y][0][z], pa[y][1][z], pa[y][2][z], pa[y][3][z]};
+                                        mma<FMT>(o[2 * (2 * i + x)], f, half2_of<0x4240>(b0), half2_of<0x4240>(b1));
+                                        mma<FMT>(o[2 * (2 * i + x) + 1], f, half2_of<0x4341>(b0), half2_of<0x4341>(b1));
+                                    }
+                                } else {
 #pragma unroll
-                                for (int j = 0; j < 4; ++j) mma<FMT>(o[4 * i + j], f, b[j][0], b[j][1]);
-                            }
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < kNt / 2; ++i) {
-                            uint32_t w[4];   // (tokens 0-7, 8-15) of output tiles 2 i and 2 i + 1
-                            ldsm4t(w, vb + kv_tile_off<S::row>(kStep, 8 * (mm & 1) + mr, 16 * (2 * i + (mm >> 1))));
-#pragma unroll
-                            for (int z = NT - 1; z >= 0; --z) {
-                                const uint32_t f[4] = {pf[0][z], pf[1][z], pf[2][z], pf[3][z]};
-                                mma<FMT>(o[2 * i], f, w[0], w[1]);
-                                mma<FMT>(o[2 * i + 1], f, w[2], w[3]);
+                                    for (int z = NT - 1; z >= 0; --z) {
+                                        const uint32_t f[4] = {pa[y][0][z], pa[y][1][z], pa[y][2][z], pa[y][3][z]};
+                                        mma<FMT>(o[2 * i + x], f, w[2 * x], w[2 * x + 1]);
+                                    }
+                                }
                             }
                         }
                     }
@@ -541,7 +546,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attn_decode_kernel(const __gri
                     }
                 }
                 if (!odd) {
-                    values(pa);
+                    values();
                 } else if constexpr (FMT == KDA_KV_BF16) {
                     // one product for each query token, without the tokens it does not see, of which
                     // only that token's rows are kept
@@ -555,11 +560,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attn_decode_kernel(const __gri
 #pragma unroll
                         for (int i = 0; i < kNt; ++i) {
                             uint32_t w[4];
-                            ldsm4t(w, vb + kv_tile_off<S::row>(kStep, 8 * (mm & 1) + mr, 16 * i));
+                            ldsm4t(w, vb + kv_tile_off<S::row>(S::step, 8 * (mm & 1) + mr, 16 * i));
                             float d[4] = {};
 #pragma unroll
                             for (int z = NT - 1; z >= 0; --z) {
-                                const uint32_t f[4] = {pa[0][z], pa[1][z], pa[2][z], pa[3][z]};
+                                const uint32_t f[4] = {pa[0][0][z], pa[0][1][z], pa[0][2][z], pa[0][3][z]};
                                 mma<FMT>(d, f, w[0] & keep[0], w[1] & keep[1]);
                             }
 #pragma unroll
@@ -597,14 +602,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1) attn_decode_kernel(const __gri
             float *dst = acc + (warp * 16 + row) * D;
             if constexpr (FMT == KDA_KV_I8) {
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-#pragma unroll
-                    for (int i = 0; i < kNt / 4; ++i) {
-                        const int unit = (kNt / 4) * (2 * t + e) + i;
-                        *reinterpret_cast<float4 *>(dst + 4 * acc_unit<FMT, D>(row, unit)) =
-                            make_float4(o[4 * i][2 * r + e] * f, o[4 * i + 1][2 * r + e] * f, o[4 * i + 2][2 * r + e] * f,
-                                        o[4 * i + 3][2 * r + e] * f);
-                    }
+                for (int i = 0; i < kNt / 2; ++i)   // columns 16 i + 4 t ..: even and odd ones from two tiles
+                    *reinterpret_cast<float4 *>(dst + 4 * acc_unit<FMT, D>(row, 4 * i + t)) =
+                        make_float4(o[2 * i][2 * r] * f, o[2 * i + 1][2 * r] * f, o[2 * i][2 * r + 1] * f,
+                                    o[2 * i + 1][2 * r + 1] * f);
             } else {
 #pragma unroll
                 for (int j = 0; j < kNt; ++j)

@@ -35,7 +35,7 @@ namespace {
 
 using namespace attn;
 
-constexpr int kRows = kAttnPrefillRows, kHalf = 128, kUnit = kAttnUnit;
+constexpr int kRows = kAttnPrefillRows, kHalf = 128, kUnit = 128;
 constexpr int kSoftWarps = 8, kLoadWarps = 4, kMmaWarp = 12, kThreads = 14 * 32;
 constexpr float kGrow = 8.f;            // bits that a row's maximum may grow before O is rescaled
 constexpr float kPBits = 6.f;           // 8-bit: bits that a probability is scaled up in fp16
@@ -63,12 +63,6 @@ template <int FMT>
 __host__ __device__ constexpr uint32_t idesc(int M, int N, int b_mn) {
     const uint32_t d = ptx::idesc_bf16(M, N, 0, b_mn);
     return FMT == KDA_KV_I8 ? d & ~((1u << 7) | (1u << 10)) : d;   // fp16 operands instead of bf16
-}
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
 }
 
 template <int FMT>
@@ -128,13 +122,13 @@ __device__ __forceinline__ void next_item(const AttnArgs &a, Walk &w) {
     if (++w.h < a.kv.Hkv) return;
     w.h = 0;
     if (w.t.rt + 1 < w.t.tiles) {
-        w.t = make_tile<kRows>(a, w.t.s, w.t.q, w.t.rt + 1);
+        w.t = make_tile<kRows, kUnit>(a, w.t.s, w.t.q, w.t.rt + 1);
         return;
     }
     int s = w.t.s + 1;
     KvSeq q = seq_of(a, s);
     while (q.n == 0 && s + 1 < a.nseq) q = seq_of(a, ++s);
-    w.t = make_tile<kRows>(a, s, q, 0);
+    w.t = make_tile<kRows, kUnit>(a, s, q, 0);
 }
 
 // Units of sequence s over all heads, summed by a warp.
@@ -142,7 +136,7 @@ __device__ __forceinline__ int64_t seq_units(const AttnArgs &a, int s, int lane)
     const KvSeq q = seq_of(a, s);
     const int n = tiles_of<kRows>(a, q);
     int64_t w = 0;
-    for (int i = lane; i < n; i += 32) w += make_tile<kRows>(a, s, q, i).units;
+    for (int i = lane; i < n; i += 32) w += make_tile<kRows, kUnit>(a, s, q, i).units;
     for (int i = 16; i; i >>= 1) w += __shfl_xor_sync(0xFFFFFFFFu, w, i);
     return w * a.kv.Hkv;
 }
@@ -174,7 +168,7 @@ __device__ __forceinline__ Walk find_share(const AttnArgs &a, int64_t *sums, Wal
             const KvSeq q = seq_of(a, s);
             for (int base = 0;; base += 32) {           // the tile: prefix sums over 32 tiles at a time
                 const int rt = base + lane, n = tiles_of<kRows>(a, q);
-                const int64_t mine = rt < n ? (int64_t)make_tile<kRows>(a, s, q, rt).units * a.kv.Hkv : 0;
+                const int64_t mine = rt < n ? (int64_t)make_tile<kRows, kUnit>(a, s, q, rt).units * a.kv.Hkv : 0;
                 int64_t x = mine;
                 for (int j = 1; j < 32; j <<= 1) {
                     const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, j);
@@ -184,7 +178,7 @@ __device__ __forceinline__ Walk find_share(const AttnArgs &a, int64_t *sums, Wal
                 if (hit) {
                     const int f = __ffs(hit) - 1;
                     at -= __shfl_sync(0xFFFFFFFFu, x - mine, f);
-                    w.t = make_tile<kRows>(a, s, q, base + f);
+                    w.t = make_tile<kRows, kUnit>(a, s, q, base + f);
                     break;
                 }
                 at -= __shfl_sync(0xFFFFFFFFu, x, 31);
@@ -286,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                     for (int c = 0; c < kChunks; ++c) ptx::tmem_st32(tO + 32 * c, z);
                 }
                 for (int32_t u = u_first; u < u_last; ++u, ++n_s, ++n_unit) {
-                    const int32_t j0 = unit_token(t, u);
+                    const int32_t j0 = unit_token<kUnit>(t, u);
                     ok = __all_sync(0xFFFFFFFFu, wait(SFULL + half, n_s & 1));
                     if (!ok) break;
                     ptx::tc_fence_after();
@@ -526,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
             auto look = [&]() {
                 f_any = far.left > 0;
                 if (!f_any) return;
-                f_tok = unit_token(far.t, far.u);
+                f_tok = unit_token<kUnit>(far.t, far.u);
                 f_head = far.h;
                 const int32_t j = f_tok + 16 * lane;
                 const bool want = lane < 8 && any_sees(a, far.t, j, 16);
@@ -665,7 +659,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                         // taken out and left to the rows that see it
                         ok = __all_sync(0xFFFFFFFFu, wait(VRAW + st, n_unit >> 1 & 1));
                         if (!ok) break;
-                        const int32_t j0 = unit_token(w.t, u);
+                        const int32_t j0 = unit_token<kUnit>(w.t, u);
                         const uint32_t groups = live[n_unit % kRing];
                         if (!all_see(a, w.t, j0, kUnit) || groups != 0xFFu) {
                             uint8_t *line = sm + L::v + st * L::tile + lt * 128;
@@ -766,7 +760,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
             uint32_t n_k = 0, n_v = 0;                                // tiles asked for
             bool want;                                                // lanes 0-7: this group of 16 tokens is needed
             auto look = [&]() -> int32_t {                            // and its page
-                const int32_t j = unit_token(w.t, w.u) + 16 * lane;
+                const int32_t j = unit_token<kUnit>(w.t, w.u) + 16 * lane;
                 want = lane < 8 && any_sees(a, w.t, j, 16);
                 return want ? __ldg(a.kv.table + (int64_t)w.t.s * a.kv.max_pages + j / pt) : 0;
             };
@@ -774,7 +768,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
             while (w.left > 0) {
                 const int st = n_k & 1;
                 const uint32_t par = (n_k >> 1 & 1) ^ 1;
-                const int32_t slot = (unit_token(w.t, w.u) + 16 * lane) % pt;
+                const int32_t slot = (unit_token<kUnit>(w.t, w.u) + 16 * lane) % pt;
                 const uint8_t *rec = want ? kv_record(a.kv, page, w.h) : nullptr;
                 const uint32_t there = __ballot_sync(0xFFFFFFFFu, rec != nullptr);
                 if (--w.left > 0) {
