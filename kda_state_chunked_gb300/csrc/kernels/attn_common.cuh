@@ -85,6 +85,18 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// ptx::mbar_wait with its loop kept rolled: these kernels wait in many places, and the unrolled
+// loops alone came to 85 KB of code.
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatile int *err) {
+#pragma unroll 1
+    for (uint32_t i = 0; i < ptx::kSpinLimit; ++i) {
+        if (ptx::mbar_try_wait(bar, parity)) return true;
+        if (err && *err) return false;
+    }
+    if (err) *err = 1;
+    return false;
+}
+
 template <int D>
 constexpr int kPartRow = D + 4;   // floats of a partial row: o, m, l, 2 free (rows stay 16-byte aligned)
 

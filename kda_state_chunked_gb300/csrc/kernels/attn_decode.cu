@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_decode_kernel(const __gri
         float ref = 0.f, inv_ref = 0.f;   // 8-bit: largest value scale so far
 
         for (; u < u_last; ++u, --left) {
-            const bool ok = __all_sync(0xFFFFFFFFu, ptx::mbar_wait(&bars[stage], phase, err));
+            const bool ok = __all_sync(0xFFFFFFFFu, wait_bar(&bars[stage], phase, err));
             if (!ok) flag_status(a.kv.status, KDA_DEV_TIMEOUT);
             const uint32_t there = ok ? live[stage] : 0u;
             if (there) {

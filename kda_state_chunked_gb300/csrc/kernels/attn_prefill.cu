@@ -9,21 +9,28 @@
 // other.  Tensor memory holds S of both halves (128 columns each, P over its first half) and O of
 // both: 512 columns.  Keys and values of a unit of 128 tokens are read once for both halves.
 //
-// One CTA of 14 warps an SM:
+// One CTA of 16 warps an SM:
 //   warps 0-3, 4-7   softmax of a half, a thread a row: scores from tensor memory, probabilities
-//                    back into it, at the end the output.  O is only rescaled when a row's maximum
-//                    has grown by more than 2^8 (fp16 and bf16 have the room).
+//                    back into it, at the end the output.  A unit's probabilities are taken
+//                    against the row's maximum of the units before; only when it has grown by
+//                    more than 2^8 (fp16 and bf16 have the room) are they taken again and O rescaled.
 //   warps 8-11       queries into shared memory; 8-bit cache: codes from global memory through
 //                    registers to fp16 tiles (a page's bytes never lie in shared memory);
 //                    16-bit cache: a look at values that not every row sees
 //   warp 12          issues the products
 //   warp 13          16-bit cache: bulk copies of pages, whose lines already lie as the matrix
 //                    unit's 128-byte swizzle wants them
+//   warp 14          walks the list of units and hands each on as a job: its tokens, records, scales
+// The walk's divisions and table reads are in one place, up to eight units ahead: with a copy of it
+// in every role the kernel was 220 KB of code and stood waiting for instructions (9,700 cycles a
+// unit).
 //
 // 8-bit cache: as in the register kernel codes are exact in fp16 and query rows scaled by a power
 // of two; the key scale of each 16 tokens multiplies f, the value scale goes into the exponent:
 // p' = 2^(f S - m + log2(vs / ref 2^6)), and a group's sum of p' divided by that factor is its sum
 // of p.  ref is the largest value scale so far, to within a factor of two.
+#include <type_traits>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -36,28 +43,45 @@ namespace {
 using namespace attn;
 
 constexpr int kRows = kAttnPrefillRows, kHalf = 128, kUnit = 128;
-constexpr int kSoftWarps = 8, kLoadWarps = 4, kMmaWarp = 12, kThreads = 14 * 32;
+constexpr int kSoftWarps = 8, kLoadWarps = 4, kMmaWarp = 12, kCopyWarp = 13, kWalkWarp = 14, kThreads = 16 * 32;
 constexpr float kGrow = 8.f;            // bits that a row's maximum may grow before O is rescaled
 constexpr float kPBits = 6.f;           // 8-bit: bits that a probability is scaled up in fp16
-constexpr float kMinRef = 0x1p-100f;
-constexpr int kRing = 4;                // units whose scales and live groups are kept
+constexpr int kJobs = 8;                // units handed out and not yet done with
+
+enum : int32_t { kBegin = 1, kEnd = 2, kWhole = 4, kStop = 8, kStarts = 16, kEnds = 32 };
+
+// A unit of work.
+struct __align__(16) Job {
+    int32_t j0;                         // its first token
+    int32_t flags;                      // kBegin, kEnd: first, last unit of its item in this CTA; kWhole: every
+                                        // row sees every token; kStarts, kEnds: the item's own first, last unit
+                                        // is in this CTA; kStop: no unit, the end
+    int32_t base;                       // position of the sequence's first query
+    int32_t row0, nrows, tok0, head;    // the row tile
+    uint32_t live;                      // groups of 16 tokens that are there
+    int32_t s, last_cta, pmin, pmax;
+    int32_t slot[8];                    // of each group: first token's slot in its page,
+    int64_t rec[8];                     // its record's place in the pool,
+    float ks[8], vs[8];                 // 8-bit: key scale, log2 of the value scale
+    float vtop;                         // log2 of the largest value scale
+    int32_t pad[3];
+};
 
 template <int D>
 struct Lay {
     static constexpr int half_q = kHalf * D * 2, tile = kUnit * D * 2, blk = kUnit * 128;   // 64-column blocks
     static constexpr int q = 0, k = 2 * half_q, v = k + 2 * tile, misc = v + 2 * tile;
     static constexpr int qs = misc;                        // [2][256] row factors
-    static constexpr int ks = qs + 2 * kRows * 4;          // [kRing][8] key scales, then value scales
-    static constexpr int vs = ks + kRing * 8 * 4;
-    static constexpr int live = vs + kRing * 8 * 4;        // [kRing] groups of 16 tokens that are there
-    static constexpr int bad = live + kRing * 4;           // [2][4] tokens taken out of a value tile
+    static constexpr int jobs = qs + 2 * kRows * 4;        // [kJobs]
+    static constexpr int bad = jobs + kJobs * (int)sizeof(Job);   // [2][4] tokens taken out of a value tile
     static constexpr int plan = bad + 2 * 16;              // the split's scratch
-    static constexpr int bar = plan + 4096 + 64;
-    static constexpr int total = bar + 256;
+    static constexpr int bar = plan + 4096;
+    static constexpr int total = bar + 512;
 };
 
 enum Bar { QFULL, QEMPTY, KFULL, KEMPTY = KFULL + 2, VFULL = KEMPTY + 2, VEMPTY = VFULL + 2, VRAW = VEMPTY + 2,
-           SFULL = VRAW + 2, PFULL = SFULL + 2, OFULL = PFULL + 2, DRAIN = OFULL + 2, NBAR };
+           SFULL = VRAW + 2, PFULL = SFULL + 2, OFULL = PFULL + 2, DRAIN = OFULL + 2, JFULL, JEMPTY = JFULL + kJobs,
+           NBAR = JEMPTY + kJobs };
 
 template <int FMT>
 __host__ __device__ constexpr uint32_t idesc(int M, int N, int b_mn) {
@@ -75,16 +99,28 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     }
 }
 
+// Wait for the loads of v from tensor memory; naming the registers keeps their uses behind it.
+__device__ __forceinline__ void wait_ld(float (&v)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                   "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]),
+                   "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]),
+                   "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27])
+                 :
+                 : "memory");
+    asm volatile("" : "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31])::"memory");
+}
 __device__ __forceinline__ float tmem_ld1(uint32_t addr) {
     uint32_t r;
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(addr) : "memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r)::"memory");
     return __uint_as_float(r);
 }
-__device__ __forceinline__ void tmem_st16u(uint32_t addr, const uint32_t (&v)[16]) {
-    float f[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(v[i]);
-    ptx::tmem_st16(addr, f);
+// The larger of two numbers; NaN if either is.
+__device__ __forceinline__ float max_nan(float x, float y) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+    return r;
 }
 
 // Sixteen codes as fp16, in two 16-byte units.
@@ -106,7 +142,7 @@ __device__ __forceinline__ void codes_to_half(uint4 c, uint4 &lo, uint4 &hi) {
     hi = make_uint4(r[4], r[5], r[6], r[7]);
 }
 
-// A CTA's place in the list of units, walked by every role on its own.
+// A place in the list of units.
 struct Walk {
     Tile t;
     int32_t h, u;
@@ -141,9 +177,9 @@ __device__ __forceinline__ int64_t seq_units(const AttnArgs &a, int s, int lane)
     return w * a.kv.Hkv;
 }
 
-// This CTA's share of the units (left = 0: none).  W and the number of CTAs that take part come
-// back too.  All warps call it; sums[512] and start are shared scratch.
-__device__ __forceinline__ Walk find_share(const AttnArgs &a, int64_t *sums, Walk *start, int64_t &W, int32_t &C) {
+// This CTA's share of the units, into *start (left = 0: none).  W and the number of CTAs that take
+// part come back too.  All warps call it; sums[512] is shared scratch.
+__device__ __forceinline__ void find_share(const AttnArgs &a, int64_t *sums, Walk *start, int64_t &W, int32_t &C) {
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int per = (a.nseq + 511) / 512, groups = (a.nseq + per - 1) / per;   // sequences a sum
     for (int i = warp; i < groups; i += kThreads / 32) {
@@ -196,13 +232,13 @@ __device__ __forceinline__ Walk find_share(const AttnArgs &a, int64_t *sums, Wal
     __syncthreads();
     W = sums[0];
     C = (int32_t)min((int64_t)a.ctas, W);
-    return *start;
 }
 
 template <int FMT, int D>
 __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_constant__ AttnArgs a) {
     using L = Lay<D>;
     constexpr int kBlks = D / 64, kChunks = D / 32, kRow = kKvRow<FMT, D>;
+    static_assert(NBAR * 8 <= 512, "barriers");
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = ptx::smem_align1024(smem_raw);
     __shared__ uint32_t tmem_at;
@@ -210,8 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
     __shared__ Walk start;
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::bar);
     float *qs = reinterpret_cast<float *>(sm + L::qs);
-    float *ks = reinterpret_cast<float *>(sm + L::ks), *vs = reinterpret_cast<float *>(sm + L::vs);
-    volatile uint32_t *live = reinterpret_cast<uint32_t *>(sm + L::live);
+    Job *jobs = reinterpret_cast<Job *>(sm + L::jobs);
     volatile uint32_t *bad = reinterpret_cast<uint32_t *>(sm + L::bad);
     volatile int *err = &err_flag;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -231,6 +266,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
             ptx::mbar_init(&bars[OFULL + i], 1);
         }
         ptx::mbar_init(&bars[DRAIN], 1);
+        for (int i = 0; i < kJobs; ++i) {
+            ptx::mbar_init(&bars[JFULL + i], 1);
+            ptx::mbar_init(&bars[JEMPTY + i], kSoftWarps + kLoadWarps + 1 + (FMT == KDA_KV_BF16 ? 1 : 0));
+        }
     }
     ptx::fence_mbar_init();
     if (warp == kMmaWarp) {
@@ -241,568 +280,566 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
     ptx::grid_dep_wait();
     int64_t W;
     int32_t C;
-    const Walk mine = find_share(a, reinterpret_cast<int64_t *>(sm + L::plan), &start, W, C);
+    find_share(a, reinterpret_cast<int64_t *>(sm + L::plan), &start, W, C);
     ptx::tc_fence_after();
     const uint32_t tm = tmem_at;
-    const int64_t end = C > 0 ? (int64_t)(blockIdx.x + 1) * W / C : 0;
-    if (tid == 0) a.split[blockIdx.x].last_cta = -1;
     const int pt = a.kv.page_tokens;
-    auto wait = [&](int b, uint32_t parity) { return ptx::mbar_wait(&bars[b], parity, err); };
+    // Waits of a whole warp, of one thread; the next job, and being done with one.
+    auto wait1 = [&](int b, uint32_t parity) { return wait_bar(&bars[b], parity, err); };
+    auto wait = [&](int b, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait1(b, parity)) != 0; };
+    auto job = [&](uint32_t n) -> const Job & { return jobs[n % kJobs]; };
+    auto wait_job = [&](uint32_t n) { return wait(JFULL + n % kJobs, n / kJobs & 1); };
+    auto done = [&](uint32_t n) { tcx::warp_arrive(&bars[JEMPTY + n % kJobs]); };
 
-    if (mine.left > 0) {
-        if (warp < kSoftWarps) {
-            // ================================================== softmax and output
-            const int half = warp / 4, row = half * kHalf + (warp % 4) * 32 + lane;
-            const uint32_t lanes = (uint32_t)((warp % 4) * 32) << 16;
-            const uint32_t tS = tm + lanes + half * 128, tO = tm + lanes + 256 + half * 128;
-            Walk w = mine;
-            uint32_t n_s = 0;              // units of this half so far: the parity of its barriers
-            uint32_t n_unit = 0, n_item = 0;
-            bool ok = true;
-            while (w.left > 0 && ok) {
-                const Tile &t = w.t;
-                const int32_t u_first = w.u, u_last = (int32_t)min((int64_t)t.units, w.u + w.left);
-                if (half * kHalf >= t.nrows) {           // nothing in this half
-                    n_unit += u_last - u_first;
-                    w.left -= u_last - u_first;
-                    ++n_item;
-                    if (w.left > 0) next_item(a, w);
-                    continue;
-                }
-                const bool in = row < t.nrows;
-                const int32_t at = t.row0 + row, pos = in ? t.q.len - t.q.n + at / a.G : -1;
-                float m = -INFINITY, l = 0.f, ref = 0.f, f_row = 0.f;
-                {
-                    float z[32];
+    // Registers go to where the scores are: 168 + 168 + 112 + 64 a thread of the four warpgroups are
+    // the 4 x 128 that the block was launched with.
+    if (warp < kSoftWarps) {
+        // ====================================================== softmax and output
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+        const int half = warp / 4, row = half * kHalf + (warp % 4) * 32 + lane;
+        const uint32_t lanes = (uint32_t)((warp % 4) * 32) << 16;
+        const uint32_t tS = tm + lanes + half * 128, tO = tm + lanes + 256 + half * 128;
+        uint32_t n_s = 0, n_item = 0;   // units of this half, items so far: the barriers' parities
+        int32_t pos = -1;
+        bool in = false, ok = true;
+        float m = -INFINITY, l = 0.f, lref = -INFINITY, f_row = 0.f;   // lref: log2 of ref
+        for (uint32_t n = 0;; ++n) {
+            ok = wait_job(n);
+            if (!ok) break;
+            const Job &jb = job(n);
+            const int32_t flags = jb.flags, nrows = jb.nrows, j0 = jb.j0;
+            if (flags & kStop) break;
+            if (half * kHalf >= nrows) {           // nothing in this half
+                n_item += (flags & kEnd) != 0;
+                done(n);
+                continue;
+            }
+            const int32_t at = jb.row0 + row;
+            if (flags & kBegin) {
+                in = row < nrows;
+                pos = in ? jb.base + at / a.G : -1;
+                m = -INFINITY, l = 0.f, lref = -INFINITY;
+                float z[32];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) z[i] = 0.f;
+                for (int i = 0; i < 32; ++i) z[i] = 0.f;
 #pragma unroll
-                    for (int c = 0; c < kChunks; ++c) ptx::tmem_st32(tO + 32 * c, z);
+                for (int c = 0; c < kChunks; ++c) ptx::tmem_st32(tO + 32 * c, z);
+            }
+            ok = wait(SFULL + half, n_s & 1);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            if (flags & kBegin) f_row = qs[(n_item & 1) * kRows + row];
+            const uint32_t live = jb.live;
+            // columns that this row sees, 32 at a time
+            auto seen = [&](int c) -> uint32_t {
+                auto low = [](int32_t k) -> uint32_t { return k <= 0 ? 0u : k >= 32 ? ~0u : (1u << k) - 1u; };
+                const int32_t b = j0 + 32 * c;
+                uint32_t x = low(pos + 1 - b);
+                if (a.window > 0) x &= ~low(pos - a.window + 1 - b) | low(a.sinks - b);
+                if (!(live >> (2 * c) & 1u)) x &= 0xFFFF0000u;
+                if (!(live >> (2 * c + 1) & 1u)) x &= 0x0000FFFFu;
+                return x;
+            };
+            // ---- scores to probabilities in one pass, against the row's reference m of the units
+            // before.  Should its maximum have outgrown that by more than the types hold, once more
+            // against the new one: the scores still stand, as nothing is written before.
+            float grown = 1.f, sum;       // what O is to be multiplied by; this unit's sum
+            if (FMT == KDA_KV_I8 && jb.vtop > lref + 1.f) {
+                grown = ex2(lref - jb.vtop);
+                lref = jb.vtop;
+            }
+            uint32_t p[64];
+            auto pass = [&](auto all) -> float {
+                constexpr bool kAll = decltype(all)::value;
+                const float ms = m == -INFINITY ? 0.f : m;
+                float top = -INFINITY, s[2][32];
+                sum = 0.f;
+                ptx::tmem_ld32(tS, s[0]);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    float(&x)[32] = s[c & 1];
+                    wait_ld(x);
+                    if (c < 3) ptx::tmem_ld32(tS + 32 * (c + 1), s[(c + 1) & 1]);
+                    const uint32_t see = kAll ? ~0u : seen(c);
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        float fk = f_row, bias = -ms, back = 1.f;
+                        if (FMT == KDA_KV_I8) {
+                            fk *= jb.ks[2 * c + g];
+                            const float lg = max_nan(jb.vs[2 * c + g] - lref, -100.f) + kPBits;
+                            bias += lg;
+                            back = ex2(-lg);
+                        }
+                        const float2 ff = make_float2(fk, fk), bb = make_float2(bias, bias);
+                        float2 part = make_float2(0.f, 0.f);
+                        float gt = -INFINITY;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int e = 16 * g + 2 * i;
+                            const bool v0 = kAll || (see >> e & 1u), v1 = kAll || (see >> (e + 1) & 1u);
+                            gt = fmaxf(gt, fmaxf(v0 ? x[e] : -INFINITY, v1 ? x[e + 1] : -INFINITY));
+                            float2 y = tcx::ffma2(make_float2(x[e], x[e + 1]), ff, bb);
+                            y.x = v0 ? ex2(y.x) : 0.f;
+                            y.y = v1 ? ex2(y.y) : 0.f;
+                            part = tcx::fadd2(part, y);
+                            p[16 * c + 8 * g + i] = pack2<FMT>(y.x, y.y);
+                        }
+                        top = fmaxf(top, gt == -INFINITY ? gt : gt * fk);   // f >= 0: the product keeps the order
+                        sum += (part.x + part.y) * back;
+                    }
                 }
-                for (int32_t u = u_first; u < u_last; ++u, ++n_s, ++n_unit) {
-                    const int32_t j0 = unit_token<kUnit>(t, u);
-                    ok = __all_sync(0xFFFFFFFFu, wait(SFULL + half, n_s & 1));
+                return top;
+            };
+            for (;;) {
+                const float top = flags & kWhole ? pass(std::true_type{}) : pass(std::false_type{});
+                const bool grow = top > m + kGrow;   // also where m is still -infinity
+                if (!__any_sync(0xFFFFFFFFu, grow)) break;
+                if (grow) {
+                    const float f = m == -INFINITY ? 0.f : ex2(m - top);
+                    grown *= f;
+                    l *= f;
+                    m = top;
+                }
+            }
+            l += sum;
+            // ---- tokens whose values were taken out of the product (16-bit cache)
+            bool odd = false;
+            if (FMT == KDA_KV_BF16 && !(flags & kWhole)) {
+                ok = wait(VFULL + (n & 1), n >> 1 & 1);
+                if (!ok) break;
+                const volatile uint32_t *out = bad + (n & 1) * 4;
+                odd = (out[0] | out[1] | out[2] | out[3]) != 0;
+            }
+            // ---- O to the new references
+            if (__any_sync(0xFFFFFFFFu, grown != 1.f || odd)) {
+                if (!(flags & kBegin)) {
+                    ok = wait(OFULL + half, (n_s - 1) & 1);
                     if (!ok) break;
                     ptx::tc_fence_after();
-                    if (u == u_first) f_row = qs[(n_item & 1) * kRows + row];
-                    const uint32_t there = live[n_unit % kRing];
-                    const bool whole = all_see(a, t, j0, kUnit) && there == 0xFFu;
-                    // columns that this row sees, 32 at a time
-                    auto seen = [&](int c) -> uint32_t {
-                        auto low = [](int32_t n) -> uint32_t { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
-                        const int32_t b = j0 + 32 * c;
-                        uint32_t s = low(pos + 1 - b);
-                        if (a.window > 0) s &= ~low(pos - a.window + 1 - b) | low(a.sinks - b);
-                        if (!(there >> (2 * c) & 1u)) s &= 0xFFFF0000u;
-                        if (!(there >> (2 * c + 1) & 1u)) s &= 0x0000FFFFu;
-                        return s;
-                    };
-                    float fk[8];
-#pragma unroll
-                    for (int g = 0; g < 8; ++g) fk[g] = FMT == KDA_KV_I8 ? f_row * ks[(n_unit % kRing) * 8 + g] : f_row;
-                    // ---- the row's maximum (f >= 0, so it may be taken before the product)
-                    float top = -INFINITY;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        float s[32];
-                        ptx::tmem_ld32(tS + 32 * c, s);
-                        ptx::tmem_wait_ld();
-                        if (!whole) {
-                            const uint32_t see = seen(c);
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) s[i] = see >> i & 1u ? s[i] : -INFINITY;
-                        }
-#pragma unroll
-                        for (int g = 0; g < 2; ++g) {
-                            float x = s[16 * g];
-#pragma unroll
-                            for (int i = 1; i < 16; ++i) x = fmaxf(x, s[16 * g + i]);
-                            x = x == -INFINITY ? x : x * fk[2 * c + g];
-                            top = fmaxf(top, x);
-                        }
-                    }
-                    // ---- value scales
-                    float vmax = 0.f;
-                    if (FMT == KDA_KV_I8) {
-#pragma unroll
-                        for (int g = 0; g < 8; ++g) {
-                            const float x = vs[(n_unit % kRing) * 8 + g];
-                            if (x < INFINITY) vmax = fmaxf(vmax, x);
-                        }
-                    }
-                    // ---- tokens whose values were taken out of the product (16-bit cache)
-                    uint32_t out_of[4] = {0, 0, 0, 0};
-                    bool odd = false;
-                    if (FMT == KDA_KV_BF16 && !whole) {
-                        ok = __all_sync(0xFFFFFFFFu, wait(VFULL + (n_unit & 1), n_unit >> 1 & 1));
-                        if (!ok) break;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            out_of[i] = bad[(n_unit & 1) * 4 + i];
-                            odd |= out_of[i] != 0;
-                        }
-                    }
-                    // ---- O, where the row's reference moves
-                    const bool grow = top > m + kGrow || (m == -INFINITY && top > -INFINITY);
-                    const bool scaled = FMT == KDA_KV_I8 && vmax > 2.f * ref;
-                    if (__any_sync(0xFFFFFFFFu, grow || scaled || odd)) {
-                        float f = 1.f;
-                        if (grow) {
-                            f = m == -INFINITY ? 0.f : ex2(m - top);
-                            l *= f;
-                            m = top;
-                        }
-                        if (scaled) {
-                            const float r = fmaxf(vmax, kMinRef);
-                            f *= ref / r;
-                            ref = r;
-                        }
-                        if (u > u_first || odd) {
-                            if (u > u_first) {
-                                ok = __all_sync(0xFFFFFFFFu, wait(OFULL + half, (n_s - 1) & 1));
-                                if (!ok) break;
-                                ptx::tc_fence_after();
-                            } else {
-                                ptx::tmem_wait_st();
-                            }
-#pragma unroll
-                            for (int c = 0; c < kChunks; ++c) {
-                                float o[32];
-                                ptx::tmem_ld32(tO + 32 * c, o);
-                                ptx::tmem_wait_ld();
-#pragma unroll
-                                for (int i = 0; i < 32; ++i) o[i] *= f;
-                                if (FMT == KDA_KV_BF16 && odd) {
-                                    for (int j = 0; j < kUnit; ++j) {
-                                        if (!(out_of[j >> 5] >> (j & 31) & 1u)) continue;   // the same for all rows
-                                        const float s = tmem_ld1(tS + j);
-                                        ptx::tmem_wait_ld();
-                                        if (sees(a, pos, j0 + j)) {
-                                            const float p = ex2(s * f_row - (m == -INFINITY ? 0.f : m));
-                                            const int b = (j0 + j) / pt, slot = (j0 + j) % pt;
-                                            const uint8_t *rec = kv_record(
-                                                a.kv, __ldg(a.kv.table + (int64_t)t.s * a.kv.max_pages + b), w.h);
-                                            if (rec)
-#pragma unroll
-                                                for (int i = 0; i < 32; ++i)
-                                                    o[i] += p * __bfloat162float(*reinterpret_cast<const __nv_bfloat16 *>(
-                                                                    rec + pt * kRow +
-                                                                    kv_tile_off<kRow>(pt, slot, 64 * c + 2 * i)));
-                                        }
-                                        __syncwarp();
-                                    }
-                                }
-                                ptx::tmem_st32(tO + 32 * c, o);
-                            }
-                        }
-                    }
-                    // ---- probabilities, over the scores that they come from
-                    const float ms = m == -INFINITY ? 0.f : m;
-                    float bias[8], back[8];
-#pragma unroll
-                    for (int g = 0; g < 8; ++g) {
-                        bias[g] = -ms;
-                        back[g] = 1.f;
-                        if (FMT == KDA_KV_I8) {
-                            const float x = vs[(n_unit % kRing) * 8 + g];
-                            const float lg = x == 0.f ? 0.f : x < INFINITY ? fmaxf(log2f(x / ref), -100.f) + kPBits : NAN;
-                            bias[g] += lg;
-                            back[g] = ex2(-lg);
-                        }
-                    }
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        float s[32];
-                        ptx::tmem_ld32(tS + 32 * c, s);
-                        ptx::tmem_wait_ld();
-                        const uint32_t see = whole ? ~0u : seen(c);
-                        uint32_t p[16];
-#pragma unroll
-                        for (int g = 0; g < 2; ++g) {
-                            float2 sum = make_float2(0.f, 0.f);
-                            const float2 ff = make_float2(fk[2 * c + g], fk[2 * c + g]);
-                            const float2 bb = make_float2(bias[2 * c + g], bias[2 * c + g]);
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const int e = 16 * g + 2 * i;
-                                float2 y = tcx::ffma2(make_float2(s[e], s[e + 1]), ff, bb);
-                                y.x = ex2(y.x), y.y = ex2(y.y);
-                                if (!whole) {
-                                    y.x = see >> e & 1u ? y.x : 0.f;
-                                    y.y = see >> (e + 1) & 1u ? y.y : 0.f;
-                                }
-                                sum = tcx::fadd2(sum, y);
-                                p[8 * g + i] = pack2<FMT>(y.x, y.y);
-                            }
-                            l += (sum.x + sum.y) * back[2 * c + g];
-                        }
-                        tmem_st16u(tS + 16 * c, p);
-                    }
+                } else {
                     ptx::tmem_wait_st();
-                    ptx::tc_fence_before();
-                    tcx::warp_arrive(&bars[PFULL + half]);
                 }
-                if (!ok) break;
-                // ---- the item's output, or this CTA's part of it
-                ok = __all_sync(0xFFFFFFFFu, wait(OFULL + half, (n_s - 1) & 1));
-                if (!ok) break;
-                ptx::tc_fence_after();
-                const bool starts = u_first == 0, ends = u_last == t.units;
-                const int64_t tok = (int64_t)t.q.tok0 + at / a.G, orow = tok * a.Hq + w.h * a.G + at % a.G;
-                const float unscale = FMT == KDA_KV_I8 ? ref * 0x1p-6f : 1.f;
-                const float f = starts && ends ? (l == 0.f ? 0.f : unscale / l) : unscale;
-                float *part = a.part + ((int64_t)(blockIdx.x * 2 + (starts ? 1 : 0)) * kRows + row) * kPartRow<D>;
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < kChunks; ++c) {
                     float o[32];
                     ptx::tmem_ld32(tO + 32 * c, o);
-                    ptx::tmem_wait_ld();
-                    if (in && starts && ends) {
+                    wait_ld(o);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] *= grown;
+                    if (FMT == KDA_KV_BF16 && odd) {
+#pragma unroll 1
+                        for (int j = 0; j < kUnit; ++j) {
+                            if (!(bad[(n & 1) * 4 + (j >> 5)] >> (j & 31) & 1u)) continue;   // the same for all rows
+                            const float x = tmem_ld1(tS + j);
+                            if (sees(a, pos, j0 + j)) {
+                                const float pj = ex2(x * f_row - (m == -INFINITY ? 0.f : m));
+                                const uint8_t *line = a.kv.base + jb.rec[j >> 4] + pt * kRow;
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    const uint4 v = *reinterpret_cast<const uint4 *>(
+                                        line + kv_tile_off<kRow>(pt, jb.slot[j >> 4] + (j & 15), 64 * c + 16 * i));
+                                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                                    for (int y = 0; y < 4; ++y) {
+                                        const float2 z = tcx::bf2_to_f2(w[y]);
+                                        o[8 * i + 2 * y] += pj * z.x;
+                                        o[8 * i + 2 * y + 1] += pj * z.y;
+                                    }
+                                }
+                            }
+                            __syncwarp();
+                        }
+                    }
+                    ptx::tmem_st32(tO + 32 * c, o);
+                }
+            }
+            // ---- the probabilities, over the scores' first half
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                float x[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(p[16 * c + i]);
+                ptx::tmem_st16(tS + 16 * c, x);
+            }
+            ptx::tmem_wait_st();
+            ptx::tc_fence_before();
+            tcx::warp_arrive(&bars[PFULL + half]);
+            ++n_s;
+            if (flags & kEnd) {
+                // ---- the item's output, or this CTA's part of it
+                ok = wait(OFULL + half, (n_s - 1) & 1);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                const bool all = (flags & kStarts) && (flags & kEnds);
+                const int64_t orow = ((int64_t)jb.tok0 + at / a.G) * a.Hq + jb.head * a.G + at % a.G;
+                const float unscale = FMT == KDA_KV_I8 ? exp2f(lref - kPBits) : 1.f;
+                const float f = all ? (l == 0.f ? 0.f : unscale / l) : unscale;
+                float *part = a.part + ((int64_t)(blockIdx.x * 2 + (flags & kStarts ? 1 : 0)) * kRows + row) * kPartRow<D>;
+#pragma unroll 1
+                for (int c = 0; c < kChunks; ++c) {
+                    float o[32];
+                    ptx::tmem_ld32(tO + 32 * c, o);
+                    wait_ld(o);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = all && l == 0.f ? 0.f : o[i] * f;
+                    if (in && all) {
                         uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o) + orow * D + 32 * c);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint32_t x[4];
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const float p0 = l == 0.f ? 0.f : o[8 * i + 2 * j] * f, p1 = l == 0.f ? 0.f : o[8 * i + 2 * j + 1] * f;
-                                x[j] = tcx::f2_to_bf2(p0, p1);
-                            }
-                            dst[i] = make_uint4(x[0], x[1], x[2], x[3]);
-                        }
+                        for (int i = 0; i < 4; ++i)
+                            dst[i] = make_uint4(tcx::f2_to_bf2(o[8 * i], o[8 * i + 1]), tcx::f2_to_bf2(o[8 * i + 2], o[8 * i + 3]),
+                                                tcx::f2_to_bf2(o[8 * i + 4], o[8 * i + 5]), tcx::f2_to_bf2(o[8 * i + 6], o[8 * i + 7]));
                     } else if (in) {
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
                             reinterpret_cast<float4 *>(part + 32 * c)[i] =
-                                make_float4(o[4 * i] * f, o[4 * i + 1] * f, o[4 * i + 2] * f, o[4 * i + 3] * f);
+                                make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                     }
                     __syncwarp();
                 }
                 ptx::tc_fence_before();
                 if (in) {
-                    if (!(starts && ends)) part[D] = m, part[D + 1] = l;
+                    if (!all) part[D] = m, part[D + 1] = l;
                     else if (a.lse) a.lse[orow] = lse_of(m, l);
                 }
-                if (tid == 0 && starts && !ends) {
+                if (tid == 0 && (flags & kStarts) && !(flags & kEnds)) {
                     AttnSplit sp{};
-                    sp.last_cta = cta_of(end - 1 + (t.units - u_last), W, C);
-                    sp.row_tok = t.q.tok0;
-                    sp.head = w.h;
-                    sp.row0 = t.row0;
-                    sp.nrows = t.nrows;
+                    sp.last_cta = jb.last_cta;
+                    sp.row_tok = jb.tok0;
+                    sp.head = jb.head;
+                    sp.row0 = jb.row0;
+                    sp.nrows = nrows;
                     a.split[blockIdx.x] = sp;
                 }
-                w.left -= u_last - u_first;
                 ++n_item;
-                if (w.left > 0) next_item(a, w);
             }
-            if (!ok && lane == 0) flag_status(a.kv.status, KDA_DEV_TIMEOUT);
-        } else if (warp < kSoftWarps + kLoadWarps) {
-            // ================================================== queries, and keys and values
-            const int lw = warp - kSoftWarps, lt = tid - kSoftWarps * 32;
-            Walk w = mine;
-            uint32_t n_unit = 0, n_item = 0;
-            bool ok = true;
-            // 8-bit: the units' codes are read one unit ahead into registers.  A warp takes 32 tokens;
-            // eight lanes take four units of token r and of token r ^ 5, which keeps both their reads
-            // and their writes in different banks.
-            constexpr int kRegs = kRow / 16;
-            constexpr int kQuads = kRow / 64;                         // groups of four 16-byte units a row
-            uint4 kc[kRegs], vc[kRegs];
-            const int r8 = (lane >> 3) ^ ((lane >> 2 & 1) * 5), ul = lane & 3;
-            float2 sc = make_float2(0.f, 0.f);                        // lanes 0-7: scales of the unit's groups
-            uint32_t there = 0;                                       // groups that are in the pool
-            // the unit whose codes are fetched next, looked up one more unit ahead: its tokens, its
-            // head and, in lanes 0-7, the pages of its groups
-            Walk far = mine;
-            int32_t f_tok = 0, f_head = 0, f_page = 0;
-            uint32_t f_want = 0;
-            bool f_any = false;
-            auto look = [&]() {
-                f_any = far.left > 0;
-                if (!f_any) return;
-                f_tok = unit_token<kUnit>(far.t, far.u);
-                f_head = far.h;
-                const int32_t j = f_tok + 16 * lane;
-                const bool want = lane < 8 && any_sees(a, far.t, j, 16);
-                if (want) f_page = __ldg(a.kv.table + (int64_t)far.t.s * a.kv.max_pages + j / pt);
-                f_want = __ballot_sync(0xFFFFFFFFu, want);
-                if (--far.left > 0 && ++far.u == far.t.units) next_item(a, far);
-            };
-            auto fetch = [&](bool values, uint4 (&c)[kRegs]) {
+            done(n);
+        }
+        if (!ok && lane == 0) flag_status(a.kv.status, KDA_DEV_TIMEOUT);
+    } else if (warp < kSoftWarps + kLoadWarps) {
+        // ====================================================== queries, and keys and values
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
+        const int lw = warp - kSoftWarps, lt = tid - kSoftWarps * 32;
+        uint32_t n_item = 0;
+        // 8-bit: the units' codes are read one unit ahead into registers.  A warp takes 32 tokens;
+        // eight lanes take four units of token r and of token r ^ 5, which keeps both their reads
+        // and their writes in different banks.
+        constexpr int kRegs = kRow / 16;
+        constexpr int kQuads = kRow / 64;                         // groups of four 16-byte units a row
+        uint4 kc[kRegs], vc[kRegs];
+        const int r8 = (lane >> 3) ^ ((lane >> 2 & 1) * 5), ul = lane & 3;
+        auto fetch = [&](const Job &jb, bool values, uint4 (&c)[kRegs]) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {                         // eight tokens
-                    const int32_t id = __shfl_sync(0xFFFFFFFFu, f_page, 2 * lw + (i >> 1));
-                    const int32_t slot = (f_tok + 32 * lw + 8 * i) % pt + r8;
-                    const bool real = (f_want >> (2 * lw + (i >> 1)) & 1u) && (uint32_t)id < (uint32_t)a.kv.num_pages;
-                    const uint8_t *tile = a.kv.base + (int64_t)id * a.kv.page_bytes + (int64_t)f_head * a.kv.rec_bytes +
-                                          (values ? pt * kRow : 0);
+            for (int y = 0; y < 2; ++y) {                         // a group of 16 tokens
+                const bool there = jb.live >> (2 * lw + y) & 1u;
+                const uint8_t *tile = a.kv.base + jb.rec[2 * lw + y] + (values ? pt * kRow : 0);
+                const int slot = jb.slot[2 * lw + y] + r8;
 #pragma unroll
-                    for (int y = 0; y < kQuads; ++y) {
-                        c[i * kQuads + y] = make_uint4(0, 0, 0, 0);
-                        if (real)
-                            c[i * kQuads + y] = __ldg(reinterpret_cast<const uint4 *>(
-                                tile + kv_tile_off<kRow>(pt, slot, 16 * (4 * y + ul))));
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int x = 0; x < kQuads; ++x) {
+                        uint4 &z = c[(2 * y + i) * kQuads + x];
+                        z = make_uint4(0, 0, 0, 0);
+                        if (there)
+                            z = __ldg(reinterpret_cast<const uint4 *>(
+                                tile + kv_tile_off<kRow>(pt, slot + 8 * i, 16 * (4 * x + ul))));
                     }
+            }
+        };
+        auto put = [&](const uint4 (&c)[kRegs], uint8_t *tile) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int x = 0; x < kQuads; ++x) {
+                    uint4 lo, hi;
+                    codes_to_half(c[i * kQuads + x], lo, hi);
+                    const int r = 32 * lw + 8 * i + r8, unit = 4 * x + ul;      // columns 16 unit ..
+                    uint8_t *line = tile + (unit >> 2) * L::blk + r * 128;
+                    *reinterpret_cast<uint4 *>(line + (((2 * unit) & 7) ^ (r & 7)) * 16) = lo;
+                    *reinterpret_cast<uint4 *>(line + (((2 * unit + 1) & 7) ^ (r & 7)) * 16) = hi;
                 }
-            };
-            auto scales = [&]() {                                     // lanes 0-7 of the first warp
-                if (lw != 0) return;
-                sc = make_float2(0.f, 0.f);
-                const uint8_t *rec = lane < 8 && (f_want >> lane & 1u) ? kv_record(a.kv, f_page, f_head) : nullptr;
-                if (rec) sc = __ldg(reinterpret_cast<const float2 *>(rec + 2 * pt * kRow));
-                there = __ballot_sync(0xFFFFFFFFu, rec != nullptr);
-            };
-            auto put = [&](const uint4 (&c)[kRegs], uint8_t *tile) {
+        };
+        auto queries = [&](const Job &jb) {
+            constexpr int kTpr = D / 16, kRpp = kLoadWarps * 32 / kTpr;
+            const float sign = a.scale < 0.f ? -1.f : 1.f;
+            const int nrows = jb.nrows, rows = nrows > kHalf ? kRows : kHalf, c = lt % kTpr;
+#pragma unroll 2
+            for (int r = lt / kTpr; r < rows; r += kRpp) {
+                const int at = jb.row0 + r;
+                uint4 x[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+                if (r < nrows) {
+                    const uint4 *src = reinterpret_cast<const uint4 *>(
+                        static_cast<const __nv_bfloat16 *>(a.q) + ((int64_t)jb.tok0 + at / a.G) * a.q_stride +
+                        (int64_t)(jb.head * a.G + at % a.G) * D + 16 * c);
+                    x[0] = src[0], x[1] = src[1];
+                }
+                float f = a.scale * sign * kLog2e;
+                float e[16];
+                const uint32_t xw[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < 8; ++i) {
+                    const float2 p = tcx::bf2_to_f2(xw[i]);
+                    e[2 * i] = p.x * sign, e[2 * i + 1] = p.y * sign;
+                }
+                if (FMT == KDA_KV_I8) {
+                    // a power of two that brings the row's largest magnitude to [2^10, 2^11)
+                    float top = 0.f;
 #pragma unroll
-                    for (int y = 0; y < kQuads; ++y) {
-                        uint4 lo, hi;
-                        codes_to_half(c[i * kQuads + y], lo, hi);
-                        const int r = 32 * lw + 8 * i + r8, unit = 4 * y + ul;      // columns 16 unit ..
-                        uint8_t *line = tile + (unit >> 2) * L::blk + r * 128;
-                        *reinterpret_cast<uint4 *>(line + (((2 * unit) & 7) ^ (r & 7)) * 16) = lo;
-                        *reinterpret_cast<uint4 *>(line + (((2 * unit + 1) & 7) ^ (r & 7)) * 16) = hi;
-                    }
-            };
-            if (FMT == KDA_KV_I8) {
-                look();
-                scales();
-                fetch(false, kc);
-                fetch(true, vc);
-                look();
+                    for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(e[i]));
+#pragma unroll
+                    for (int i = 1; i < kTpr; i <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, i));
+                    const int b = (int)(__float_as_uint(top) >> 23);
+                    const int shift = b == 0 || b == 255 ? 0 : min(max(137 - b, -120), 120);
+                    const float up = __uint_as_float((uint32_t)(127 + shift) << 23);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) e[i] *= up;
+                    f *= __uint_as_float((uint32_t)(127 - shift) << 23);
+                }
+                uint32_t y[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[i] = pack2<FMT>(e[2 * i], e[2 * i + 1]);
+                uint8_t *dst = sm + L::q + (r / kHalf) * L::half_q + (c >> 2) * (kHalf * 128);
+                const int rr = r % kHalf;
+                *reinterpret_cast<uint4 *>(dst + ptx::sw128_off(rr, 32 * (c & 3))) = make_uint4(y[0], y[1], y[2], y[3]);
+                *reinterpret_cast<uint4 *>(dst + ptx::sw128_off(rr, 32 * (c & 3) + 16)) = make_uint4(y[4], y[5], y[6], y[7]);
+                if (c == 0) qs[(n_item & 1) * kRows + r] = f;
             }
-            while (w.left > 0 && ok) {
-                const int32_t u_first = w.u, u_last = (int32_t)min((int64_t)w.t.units, w.u + w.left);
-                // ---- queries
-                ok = __all_sync(0xFFFFFFFFu, wait(QEMPTY, (n_item & 1) ^ 1));
+            ptx::fence_proxy_async_smem();
+            tcx::warp_arrive(&bars[QFULL]);
+        };
+        bool ok = wait_job(0), stop = ok && (job(0).flags & kStop);
+        if (FMT == KDA_KV_I8 && ok && !stop) {
+            fetch(job(0), false, kc);
+            fetch(job(0), true, vc);
+        }
+        for (uint32_t n = 0; ok && !stop; ++n) {
+            const Job &jb = job(n);
+            const int st = n & 1;
+            const uint32_t par = (n >> 1 & 1) ^ 1;
+            if (jb.flags & kBegin) {
+                ok = wait(QEMPTY, (n_item & 1) ^ 1);
                 if (!ok) break;
-                {
-                    constexpr int kTpr = D / 16, kRpp = kLoadWarps * 32 / kTpr;
-                    const float sign = a.scale < 0.f ? -1.f : 1.f;
-                    const int rows = w.t.nrows > kHalf ? kRows : kHalf, c = lt % kTpr;
-                    for (int r = lt / kTpr; r < rows; r += kRpp) {
-                        const int at = w.t.row0 + r;
-                        uint4 x[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-                        if (r < w.t.nrows) {
-                            const uint4 *src = reinterpret_cast<const uint4 *>(
-                                static_cast<const __nv_bfloat16 *>(a.q) + (int64_t)(w.t.q.tok0 + at / a.G) * a.q_stride +
-                                (int64_t)(w.h * a.G + at % a.G) * D + 16 * c);
-                            x[0] = src[0], x[1] = src[1];
-                        }
-                        float f = a.scale * sign * kLog2e;
-                        float e[16];
-                        const uint32_t xw[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float2 p = tcx::bf2_to_f2(xw[i]);
-                            e[2 * i] = p.x * sign, e[2 * i + 1] = p.y * sign;
-                        }
-                        if (FMT == KDA_KV_I8) {
-                            // a power of two that brings the row's largest magnitude to [2^10, 2^11)
-                            float top = 0.f;
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(e[i]));
-#pragma unroll
-                            for (int i = 1; i < kTpr; i <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, i));
-                            const int b = (int)(__float_as_uint(top) >> 23);
-                            const int shift = b == 0 || b == 255 ? 0 : min(max(137 - b, -120), 120);
-                            const float up = __uint_as_float((uint32_t)(127 + shift) << 23);
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) e[i] *= up;
-                            f *= __uint_as_float((uint32_t)(127 - shift) << 23);
-                        }
-                        uint32_t y[8];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) y[i] = pack2<FMT>(e[2 * i], e[2 * i + 1]);
-                        uint8_t *dst = sm + L::q + (r / kHalf) * L::half_q + (c >> 2) * (kHalf * 128);
-                        const int rr = r % kHalf;
-                        *reinterpret_cast<uint4 *>(dst + ptx::sw128_off(rr, 32 * (c & 3))) = make_uint4(y[0], y[1], y[2], y[3]);
-                        *reinterpret_cast<uint4 *>(dst + ptx::sw128_off(rr, 32 * (c & 3) + 16)) = make_uint4(y[4], y[5], y[6], y[7]);
-                        if (c == 0) qs[(n_item & 1) * kRows + r] = f;
-                    }
-                    ptx::fence_proxy_async_smem();
-                    tcx::warp_arrive(&bars[QFULL]);
-                }
-                for (int32_t u = u_first; u < u_last; ++u, ++n_unit) {
-                    const int st = n_unit & 1;
-                    const uint32_t par = (n_unit >> 1 & 1) ^ 1;
-                    if (FMT == KDA_KV_I8) {
-                        ok = __all_sync(0xFFFFFFFFu, wait(KEMPTY + st, par));
-                        if (!ok) break;
-                        put(kc, sm + L::k + st * L::tile);
-                        if (lw == 0) {
-                            if (lane < 8) {
-                                ks[(n_unit % kRing) * 8 + lane] = fabsf(sc.x);
-                                vs[(n_unit % kRing) * 8 + lane] = fabsf(sc.y);
-                            }
-                            if (lane == 0) live[n_unit % kRing] = there;
-                        }
-                        ptx::fence_proxy_async_smem();
-                        tcx::warp_arrive(&bars[KFULL + st]);
-                        if (f_any) {
-                            fetch(false, kc);
-                            scales();
-                        }
-                        ok = __all_sync(0xFFFFFFFFu, wait(VEMPTY + st, par));
-                        if (!ok) break;
-                        put(vc, sm + L::v + st * L::tile);
-                        ptx::fence_proxy_async_smem();
-                        tcx::warp_arrive(&bars[VFULL + st]);
-                        if (f_any) {
-                            fetch(true, vc);
-                            look();
-                        }
-                    } else {
-                        // values that not every row sees: a token that no row sees is cleared (0 times
-                        // what a stale slot holds need not be 0), and one with an infinity or a NaN is
-                        // taken out and left to the rows that see it
-                        ok = __all_sync(0xFFFFFFFFu, wait(VRAW + st, n_unit >> 1 & 1));
-                        if (!ok) break;
-                        const int32_t j0 = unit_token<kUnit>(w.t, u);
-                        const uint32_t groups = live[n_unit % kRing];
-                        if (!all_see(a, w.t, j0, kUnit) || groups != 0xFFu) {
-                            uint8_t *line = sm + L::v + st * L::tile + lt * 128;
-                            const bool any = (groups >> (lt >> 4) & 1u) && any_sees(a, w.t, j0 + lt, 1);
-                            bool strange = false;
-                            if (any) {
-#pragma unroll
-                                for (int b = 0; b < kBlks; ++b)
-                                    for (int i = 0; i < 8; ++i) {
-                                        const uint4 x = *reinterpret_cast<const uint4 *>(line + b * L::blk + ((i ^ (lt & 7)) << 4));
-                                        for (uint32_t y : {x.x, x.y, x.z, x.w})
-                                            strange |= (y & 0x7F80u) == 0x7F80u || (y & 0x7F800000u) == 0x7F800000u;
-                                    }
-                            }
-                            if (!any || strange)
-#pragma unroll
-                                for (int b = 0; b < kBlks; ++b)
-                                    for (int i = 0; i < 8; ++i)
-                                        *reinterpret_cast<uint4 *>(line + b * L::blk + ((i ^ (lt & 7)) << 4)) = make_uint4(0, 0, 0, 0);
-                            const uint32_t mask = __ballot_sync(0xFFFFFFFFu, strange);
-                            if (lane == 0) bad[st * 4 + lw] = mask;
-                            ptx::fence_proxy_async_smem();
-                        }
-                        tcx::warp_arrive(&bars[VFULL + st]);
-                    }
-                }
-                w.left -= u_last - u_first;
+                queries(jb);
                 ++n_item;
-                if (w.left > 0 && ok) next_item(a, w);
             }
-        } else if (warp == kMmaWarp) {
+            if (FMT == KDA_KV_I8) {
+                ok = wait(KEMPTY + st, par);
+                if (!ok) break;
+                put(kc, sm + L::k + st * L::tile);
+                ptx::fence_proxy_async_smem();
+                tcx::warp_arrive(&bars[KFULL + st]);
+                ok = wait_job(n + 1);
+                if (!ok) break;
+                stop = job(n + 1).flags & kStop;
+                if (!stop) fetch(job(n + 1), false, kc);
+                ok = wait(VEMPTY + st, par);
+                if (!ok) break;
+                put(vc, sm + L::v + st * L::tile);
+                ptx::fence_proxy_async_smem();
+                tcx::warp_arrive(&bars[VFULL + st]);
+                if (!stop) fetch(job(n + 1), true, vc);
+            } else {
+                // values that not every row sees: a token that no row sees is cleared (0 times what a
+                // stale slot holds need not be 0), and one with an infinity or a NaN is taken out and
+                // left to the rows that see it
+                ok = wait(VRAW + st, n >> 1 & 1);
+                if (!ok) break;
+                if (!(jb.flags & kWhole)) {
+                    uint8_t *line = sm + L::v + st * L::tile + lt * 128;
+                    const int32_t j = jb.j0 + lt;
+                    const bool any = (jb.live >> (lt >> 4) & 1u) && j <= jb.pmax &&
+                                     (a.window <= 0 || j > jb.pmin - a.window || j < a.sinks);
+                    bool strange = false;
+                    if (any) {
+#pragma unroll 1
+                        for (int b = 0; b < kBlks; ++b)
+#pragma unroll 2
+                            for (int i = 0; i < 8; ++i) {
+                                const uint4 x = *reinterpret_cast<const uint4 *>(line + b * L::blk + ((i ^ (lt & 7)) << 4));
+                                for (uint32_t y : {x.x, x.y, x.z, x.w})
+                                    strange |= (y & 0x7F80u) == 0x7F80u || (y & 0x7F800000u) == 0x7F800000u;
+                            }
+                    }
+                    if (!any || strange)
+#pragma unroll 1
+                        for (int b = 0; b < kBlks; ++b)
+#pragma unroll 2
+                            for (int i = 0; i < 8; ++i)
+                                *reinterpret_cast<uint4 *>(line + b * L::blk + ((i ^ (lt & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+                    const uint32_t mask = __ballot_sync(0xFFFFFFFFu, strange);
+                    if (lane == 0) bad[st * 4 + lw] = mask;
+                    ptx::fence_proxy_async_smem();
+                }
+                tcx::warp_arrive(&bars[VFULL + st]);
+                ok = wait_job(n + 1);
+                stop = ok && (job(n + 1).flags & kStop);
+            }
+            done(n);
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        if (warp == kMmaWarp) {
             // ================================================== products
             if (lane == 0) {
                 const uint32_t sb = ptx::smem_u32(sm);
-                Walk w = mine;
-                uint32_t n_unit = 0, n_item = 0, n_p[2] = {0, 0};
-                bool ok = true;
+                uint32_t n_item = 0, n_p[2] = {0, 0};
+                // Descriptors of one operand differ in their low word only, by an address that a step adds
+                // to; the empty statement keeps the compiler from holding them all in registers.
+                const uint32_t hi = (uint32_t)(ptx::sdesc_sw128(0, 16, 1024) >> 32);
+                auto low = [&](uint32_t at, uint32_t lbo) {
+                    uint32_t x = (at >> 4) | (lbo >> 4) << 16;
+                    asm volatile("" : "+r"(x));
+                    return x;
+                };
+                auto desc = [&](uint32_t lo) { return (uint64_t)hi << 32 | lo; };
                 auto scores = [&](int half, int st) {
+                    const uint32_t ql = low(sb + L::q + half * L::half_q, 16), kl = low(sb + L::k + st * L::tile, 16);
 #pragma unroll
                     for (int s = 0; s < D / 16; ++s) {
-                        const uint32_t off = (s >> 2) * L::blk + (s & 3) * 32;
-                        ptx::mma_bf16(tm + half * 128, ptx::sdesc_sw128(sb + L::q + half * L::half_q + off, 16, 1024),
-                                      ptx::sdesc_sw128(sb + L::k + st * L::tile + off, 16, 1024), idesc<FMT>(128, 128, 0),
-                                      s > 0 ? 1u : 0u);
+                        const uint32_t off = ((s >> 2) * L::blk + (s & 3) * 32) >> 4;
+                        ptx::mma_bf16(tm + half * 128, desc(ql + off), desc(kl + off), idesc<FMT>(128, 128, 0), s > 0 ? 1u : 0u);
                     }
                     ptx::mma_commit(&bars[SFULL + half]);
                 };
                 auto outputs = [&](int half, int st) {
+                    const uint32_t vl = low(sb + L::v + st * L::tile, L::blk);
 #pragma unroll
                     for (int s = 0; s < kUnit / 16; ++s)
-                        ptx::mma_bf16_ta(tm + 256 + half * 128, tm + half * 128 + s * 8,
-                                         ptx::sdesc_sw128(sb + L::v + st * L::tile + s * 2048, L::blk, 1024),
+                        ptx::mma_bf16_ta(tm + 256 + half * 128, tm + half * 128 + s * 8, desc(vl + (s * 2048 >> 4)),
                                          idesc<FMT>(128, D, 1), 1u);
                     ptx::mma_commit(&bars[OFULL + half]);
                 };
-                while (w.left > 0 && ok) {
-                    const int32_t n = (int32_t)min((int64_t)w.t.units - w.u, w.left);
-                    const int halves = w.t.nrows > kHalf ? 2 : 1;
-                    ok = wait(QFULL, n_item & 1) && wait(KFULL + (n_unit & 1), n_unit >> 1 & 1);
+                bool ok = true;
+                for (uint32_t n = 0; ok; ++n) {
+                    ok = wait1(JFULL + n % kJobs, n / kJobs & 1);
                     if (!ok) break;
-                    ptx::tc_fence_after();
-                    for (int h = 0; h < halves; ++h) scores(h, n_unit & 1);
-                    ptx::mma_commit(&bars[KEMPTY + (n_unit & 1)]);
-                    if (n == 1) ptx::mma_commit(&bars[QEMPTY]);
-                    for (int32_t i = 0; i < n && ok; ++i, ++n_unit) {
-                        const int st = n_unit & 1, nx = st ^ 1;
-                        for (int h = 0; h < halves; ++h) {
-                            ok = wait(PFULL + h, n_p[h] & 1) && (h || wait(VFULL + st, n_unit >> 1 & 1));
+                    const int32_t flags = job(n).flags;
+                    if (flags & kStop) break;
+                    const int halves = job(n).nrows > kHalf ? 2 : 1, st = n & 1, nx = st ^ 1;
+                    ptx::mbar_arrive(&bars[JEMPTY + n % kJobs]);
+                    // the scores of an item's first unit; those of the next come between the outputs
+                    if (flags & kBegin) {
+                        ok = wait1(QFULL, n_item & 1) && wait1(KFULL + st, n >> 1 & 1);
+                        if (!ok) break;
+                        ptx::tc_fence_after();
+                        for (int h = 0; h < halves; ++h) scores(h, st);
+                        ptx::mma_commit(&bars[KEMPTY + st]);
+                        if (flags & kEnd) ptx::mma_commit(&bars[QEMPTY]);
+                        ++n_item;
+                    }
+                    for (int h = 0; h < halves; ++h) {
+                        ok = wait1(PFULL + h, n_p[h] & 1) && (h || wait1(VFULL + st, n >> 1 & 1));
+                        if (!ok) break;
+                        ++n_p[h];
+                        ptx::tc_fence_after();
+                        outputs(h, st);
+                        if (h + 1 == halves) ptx::mma_commit(&bars[VEMPTY + st]);
+                        if (!(flags & kEnd)) {
+                            ok = h || wait1(KFULL + nx, (n + 1) >> 1 & 1);
                             if (!ok) break;
-                            ++n_p[h];
                             ptx::tc_fence_after();
-                            outputs(h, st);
-                            if (h + 1 == halves) ptx::mma_commit(&bars[VEMPTY + st]);
-                            if (i + 1 < n) {
-                                ok = h || wait(KFULL + nx, (n_unit + 1) >> 1 & 1);
-                                if (!ok) break;
-                                ptx::tc_fence_after();
-                                scores(h, nx);
-                                if (h + 1 == halves) {
-                                    ptx::mma_commit(&bars[KEMPTY + nx]);
-                                    if (i + 2 == n) ptx::mma_commit(&bars[QEMPTY]);
-                                }
+                            scores(h, nx);
+                            if (h + 1 == halves) {
+                                ptx::mma_commit(&bars[KEMPTY + nx]);
+                                // the item's last scores are under way: its queries may go
+                                if (wait1(JFULL + (n + 1) % kJobs, (n + 1) / kJobs & 1) && (job(n + 1).flags & kEnd))
+                                    ptx::mma_commit(&bars[QEMPTY]);
                             }
                         }
                     }
-                    w.left -= n;
-                    ++n_item;
-                    if (w.left > 0) next_item(a, w);
                 }
                 ptx::mma_commit(&bars[DRAIN]);
-                ptx::mbar_wait(&bars[DRAIN], 0, nullptr);
+                wait_bar(&bars[DRAIN], 0, nullptr);
             }
             __syncwarp();
-        } else if (FMT == KDA_KV_BF16) {
+        } else if (FMT == KDA_KV_BF16 && warp == kCopyWarp) {
             // ================================================== copies (16-bit cache)
-            Walk w = mine;
-            bool ok = true;
-            uint32_t n_k = 0, n_v = 0;                                // tiles asked for
-            bool want;                                                // lanes 0-7: this group of 16 tokens is needed
-            auto look = [&]() -> int32_t {                            // and its page
-                const int32_t j = unit_token<kUnit>(w.t, w.u) + 16 * lane;
-                want = lane < 8 && any_sees(a, w.t, j, 16);
-                return want ? __ldg(a.kv.table + (int64_t)w.t.s * a.kv.max_pages + j / pt) : 0;
-            };
-            int32_t page = look();
-            while (w.left > 0) {
-                const int st = n_k & 1;
-                const uint32_t par = (n_k >> 1 & 1) ^ 1;
-                const int32_t slot = (unit_token<kUnit>(w.t, w.u) + 16 * lane) % pt;
-                const uint8_t *rec = want ? kv_record(a.kv, page, w.h) : nullptr;
-                const uint32_t there = __ballot_sync(0xFFFFFFFFu, rec != nullptr);
-                if (--w.left > 0) {
-                    if (++w.u == w.t.units) next_item(a, w);
-                    page = look();                                    // the next unit's, while this one waits
-                }
-                ok = __all_sync(0xFFFFFFFFu, wait(KEMPTY + st, par));
-                if (!ok) break;
-                if (lane == 0) {
-                    live[n_k % kRing] = there;
-                    ptx::mbar_arrive_expect_tx(&bars[KFULL + st], __popc(there) * 16 * kRow);
-                }
-                __syncwarp();
-                if (rec)
+            uint32_t n_k = 0, n_v = 0;                            // tiles asked for
+            for (uint32_t n = 0; wait_job(n); ++n) {
+                const Job &jb = job(n);
+                if (jb.flags & kStop) break;
+                const int st = n & 1;
+                const uint32_t par = (n >> 1 & 1) ^ 1, bytes = __popc(jb.live) * 16 * kRow;
+                const bool there = lane < 8 && (jb.live >> lane & 1u);
+                const uint8_t *src = there ? a.kv.base + jb.rec[lane] + jb.slot[lane] * 128 : nullptr;
+                done(n);
+                auto copy = [&](int bar, uint8_t *dst, const uint8_t *from) {
+                    if (lane == 0) ptx::mbar_arrive_expect_tx(&bars[bar], bytes);
+                    __syncwarp();
+                    if (there)
 #pragma unroll
-                    for (int b = 0; b < kBlks; ++b)
-                        ptx::bulk_load(sm + L::k + st * L::tile + b * L::blk + lane * 2048, rec + b * pt * 128 + slot * 128, 2048,
-                                       &bars[KFULL + st]);
+                        for (int b = 0; b < kBlks; ++b)
+                            ptx::bulk_load(dst + b * L::blk + lane * 2048, from + b * pt * 128, 2048, &bars[bar]);
+                };
+                if (!wait(KEMPTY + st, par)) break;
+                copy(KFULL + st, sm + L::k + st * L::tile, src);
                 ++n_k;
-                ok = __all_sync(0xFFFFFFFFu, wait(VEMPTY + st, par));
-                if (!ok) break;
-                if (lane == 0) ptx::mbar_arrive_expect_tx(&bars[VRAW + st], __popc(there) * 16 * kRow);
-                __syncwarp();
-                if (rec)
-#pragma unroll
-                    for (int b = 0; b < kBlks; ++b)
-                        ptx::bulk_load(sm + L::v + st * L::tile + b * L::blk + lane * 2048,
-                                       rec + pt * kRow + b * pt * 128 + slot * 128, 2048, &bars[VRAW + st]);
+                if (!wait(VEMPTY + st, par)) break;
+                copy(VRAW + st, sm + L::v + st * L::tile, src + pt * kRow);
                 ++n_v;
             }
             // the last copies land before the block ends, whatever became of their readers
             __syncwarp();
-            for (uint32_t i = n_k > 2 ? n_k - 2 : 0; i < n_k; ++i) ptx::mbar_wait(&bars[KFULL + (i & 1)], i >> 1 & 1, nullptr);
-            for (uint32_t i = n_v > 2 ? n_v - 2 : 0; i < n_v; ++i) ptx::mbar_wait(&bars[VRAW + (i & 1)], i >> 1 & 1, nullptr);
+            for (uint32_t i = n_k > 2 ? n_k - 2 : 0; i < n_k; ++i) wait_bar(&bars[KFULL + (i & 1)], i >> 1 & 1, nullptr);
+            for (uint32_t i = n_v > 2 ? n_v - 2 : 0; i < n_v; ++i) wait_bar(&bars[VRAW + (i & 1)], i >> 1 & 1, nullptr);
+        } else if (warp == kWalkWarp) {
+            // ================================================== the list of units
+            Walk w = start;
+            if (lane == 0) a.split[blockIdx.x].last_cta = -1;
+            const int64_t end = C > 0 ? (int64_t)(blockIdx.x + 1) * W / C : 0;
+            int32_t u_first = w.u;
+            for (uint32_t n = 0;; ++n) {
+                if (!wait(JEMPTY + n % kJobs, (n / kJobs & 1) ^ 1)) break;
+                Job &jb = jobs[n % kJobs];
+                if (w.left <= 0) {
+                    if (lane == 0) {
+                        jb.flags = kStop;
+                        ptx::mbar_arrive(&bars[JFULL + n % kJobs]);
+                    }
+                    break;
+                }
+                const Tile &t = w.t;
+                const int32_t j0 = unit_token<kUnit>(t, w.u), j = j0 + 16 * lane;
+                const uint8_t *rec = nullptr;
+                if (lane < 8 && any_sees(a, t, j, 16))
+                    rec = kv_record(a.kv, __ldg(a.kv.table + (int64_t)t.s * a.kv.max_pages + j / pt), w.h);
+                const uint32_t live = __ballot_sync(0xFFFFFFFFu, rec != nullptr);
+                if (lane < 8) {
+                    jb.slot[lane] = j % pt;
+                    jb.rec[lane] = rec ? rec - a.kv.base : 0;
+                }
+                if (FMT == KDA_KV_I8) {
+                    // a value scale of 0 stands for codes of 0: any factor does, so the largest other
+                    const float2 sc = rec ? __ldg(reinterpret_cast<const float2 *>(rec + 2 * pt * kRow)) : make_float2(0.f, 0.f);
+                    const float x = fabsf(sc.y);
+                    float lg = x > 0.f && x < INFINITY ? log2f(x) : -INFINITY, top = lg;
+#pragma unroll
+                    for (int i = 1; i < 8; i <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, i));
+                    top = fmaxf(top, -100.f);
+                    if (x == 0.f) lg = top;
+                    if (!(x < INFINITY)) lg = NAN;
+                    if (lane < 8) jb.ks[lane] = fabsf(sc.x), jb.vs[lane] = lg;
+                    if (lane == 0) jb.vtop = top;
+                }
+                if (lane == 0) {
+                    const bool ends = w.left >= t.units - w.u;   // the item's last unit is in this share
+                    jb.j0 = j0;
+                    jb.flags = (w.u == u_first ? kBegin : 0) | (w.u + 1 == t.units || w.left == 1 ? kEnd : 0) |
+                               (all_see(a, t, j0, kUnit) && live == 0xFFu ? kWhole : 0) | (u_first == 0 ? kStarts : 0) |
+                               (ends ? kEnds : 0);
+                    jb.base = t.q.len - t.q.n;
+                    jb.row0 = t.row0, jb.nrows = t.nrows, jb.tok0 = t.q.tok0, jb.head = w.h;
+                    jb.live = live;
+                    jb.s = t.s;
+                    jb.last_cta = ends ? (int32_t)blockIdx.x : cta_of(end - w.left + (t.units - 1 - w.u), W, C);
+                    jb.pmin = t.pmin, jb.pmax = t.pmax;
+                }
+                tcx::warp_arrive(&bars[JFULL + n % kJobs]);
+                --w.left;
+                if (++w.u == w.t.units) {
+                    if (w.left > 0) next_item(a, w);
+                    u_first = 0;
+                }
+            }
         }
     }
     __syncthreads();
