@@ -11,9 +11,9 @@
 //
 // One CTA of 16 warps an SM:
 //   warps 0-3, 4-7   softmax of a half, a thread a row: scores from tensor memory, probabilities
-//                    back into it, at the end the output.  A unit's probabilities are taken
-//                    against the row's maximum of the units before; only when it has grown by
-//                    more than 2^8 (fp16 and bf16 have the room) are they taken again and O rescaled.
+//                    back into it, at the end the output.  The probabilities are taken against
+//                    a reference that follows the row's maximum only once that has grown by more
+//                    than 2^8 (fp16 and bf16 have the room), so O is seldom rescaled.
 //   warps 8-11       queries into shared memory; 8-bit cache: codes from global memory through
 //                    registers to fp16 tiles (a page's bytes never lie in shared memory);
 //                    16-bit cache: a look at values that not every row sees
@@ -172,6 +172,7 @@ __device__ __forceinline__ int64_t seq_units(const AttnArgs &a, int s, int lane)
     const KvSeq q = seq_of(a, s);
     const int n = tiles_of<kRows>(a, q);
     int64_t w = 0;
+#pragma unroll 1
     for (int i = lane; i < n; i += 32) w += make_tile<kRows, kUnit>(a, s, q, i).units;
     for (int i = 16; i; i >>= 1) w += __shfl_xor_sync(0xFFFFFFFFu, w, i);
     return w * a.kv.Hkv;
@@ -182,8 +183,10 @@ __device__ __forceinline__ int64_t seq_units(const AttnArgs &a, int s, int lane)
 __device__ __forceinline__ void find_share(const AttnArgs &a, int64_t *sums, Walk *start, int64_t &W, int32_t &C) {
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int per = (a.nseq + 511) / 512, groups = (a.nseq + per - 1) / per;   // sequences a sum
+#pragma unroll 1
     for (int i = warp; i < groups; i += kThreads / 32) {
         int64_t w = 0;
+#pragma unroll 1
         for (int s = i * per; s < min(a.nseq, (i + 1) * per); ++s) w += seq_units(a, s, lane);
         if (lane == 0) sums[i] = w;
     }
@@ -200,8 +203,10 @@ __device__ __forceinline__ void find_share(const AttnArgs &a, int64_t *sums, Wal
             int i = 0;
             while (at >= sums[i]) at -= sums[i++];
             int s = i * per;
+#pragma unroll 1
             for (int64_t n; at >= (n = seq_units(a, s, lane)); ++s) at -= n;
             const KvSeq q = seq_of(a, s);
+#pragma unroll 1
             for (int base = 0;; base += 32) {           // the tile: prefix sums over 32 tiles at a time
                 const int rt = base + lane, n = tiles_of<kRows>(a, q);
                 const int64_t mine = rt < n ? (int64_t)make_tile<kRows, kUnit>(a, s, q, rt).units * a.kv.Hkv : 0;
@@ -291,11 +296,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
     auto wait_job = [&](uint32_t n) { return wait(JFULL + n % kJobs, n / kJobs & 1); };
     auto done = [&](uint32_t n) { tcx::warp_arrive(&bars[JEMPTY + n % kJobs]); };
 
-    // Registers go to where the scores are: 168 + 168 + 112 + 64 a thread of the four warpgroups are
-    // the 4 x 128 that the block was launched with.
+    // The roles run side by side out of one instruction cache, so their loops are kept small: rolled
+    // where their register arrays allow it.
     if (warp < kSoftWarps) {
         // ====================================================== softmax and output
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
         const int half = warp / 4, row = half * kHalf + (warp % 4) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp % 4) * 32) << 16;
         const uint32_t tS = tm + lanes + half * 128, tO = tm + lanes + 256 + half * 128;
@@ -340,68 +344,54 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                 if (!(live >> (2 * c + 1) & 1u)) x &= 0x0000FFFFu;
                 return x;
             };
-            // ---- scores to probabilities in one pass, against the row's reference m of the units
-            // before.  Should its maximum have outgrown that by more than the types hold, once more
-            // against the new one: the scores still stand, as nothing is written before.
-            float grown = 1.f, sum;       // what O is to be multiplied by; this unit's sum
+            // 32 scores at a time, the next 32 on their way from tensor memory
+            auto chunks = [&](auto step) {
+                float x[2][32];
+                ptx::tmem_ld32(tS, x[0]);
+#pragma unroll 1
+                for (int c = 0; c < 4; c += 2) {
+                    wait_ld(x[0]);
+                    ptx::tmem_ld32(tS + 32 * (c + 1), x[1]);
+                    step(x[0], c);
+                    wait_ld(x[1]);
+                    if (c == 0) ptx::tmem_ld32(tS + 64, x[0]);
+                    step(x[1], c + 1);
+                }
+            };
+            // ---- the row's maximum
+            float top = -INFINITY;
+            auto most = [&](auto all) {
+                chunks([&](const float (&x)[32], int c) {
+                    constexpr bool kAll = decltype(all)::value;
+                    const uint32_t see = kAll ? ~0u : seen(c);
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        float gt = -INFINITY;
+#pragma unroll
+                        for (int i = 16 * g; i < 16 * g + 16; i += 2)
+                            gt = fmaxf(gt, fmaxf(kAll || (see >> i & 1u) ? x[i] : -INFINITY,
+                                                 kAll || (see >> (i + 1) & 1u) ? x[i + 1] : -INFINITY));
+                        // f >= 0: the product keeps the order
+                        const float fk = FMT == KDA_KV_I8 ? f_row * jb.ks[2 * c + g] : f_row;
+                        top = fmaxf(top, gt == -INFINITY ? gt : gt * fk);
+                    }
+                });
+            };
+            if (flags & kWhole) most(std::true_type{});
+            else most(std::false_type{});
+            // ---- the references: m lags behind the maximum, ref behind the value scales
+            float grown = 1.f;            // what O is to be multiplied by
             if (FMT == KDA_KV_I8 && jb.vtop > lref + 1.f) {
                 grown = ex2(lref - jb.vtop);
                 lref = jb.vtop;
             }
-            uint32_t p[64];
-            auto pass = [&](auto all) -> float {
-                constexpr bool kAll = decltype(all)::value;
-                const float ms = m == -INFINITY ? 0.f : m;
-                float top = -INFINITY, s[2][32];
-                sum = 0.f;
-                ptx::tmem_ld32(tS, s[0]);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    float(&x)[32] = s[c & 1];
-                    wait_ld(x);
-                    if (c < 3) ptx::tmem_ld32(tS + 32 * (c + 1), s[(c + 1) & 1]);
-                    const uint32_t see = kAll ? ~0u : seen(c);
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        float fk = f_row, bias = -ms, back = 1.f;
-                        if (FMT == KDA_KV_I8) {
-                            fk *= jb.ks[2 * c + g];
-                            const float lg = max_nan(jb.vs[2 * c + g] - lref, -100.f) + kPBits;
-                            bias += lg;
-                            back = ex2(-lg);
-                        }
-                        const float2 ff = make_float2(fk, fk), bb = make_float2(bias, bias);
-                        float2 part = make_float2(0.f, 0.f);
-                        float gt = -INFINITY;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int e = 16 * g + 2 * i;
-                            const bool v0 = kAll || (see >> e & 1u), v1 = kAll || (see >> (e + 1) & 1u);
-                            gt = fmaxf(gt, fmaxf(v0 ? x[e] : -INFINITY, v1 ? x[e + 1] : -INFINITY));
-                            float2 y = tcx::ffma2(make_float2(x[e], x[e + 1]), ff, bb);
-                            y.x = v0 ? ex2(y.x) : 0.f;
-                            y.y = v1 ? ex2(y.y) : 0.f;
-                            part = tcx::fadd2(part, y);
-                            p[16 * c + 8 * g + i] = pack2<FMT>(y.x, y.y);
-                        }
-                        top = fmaxf(top, gt == -INFINITY ? gt : gt * fk);   // f >= 0: the product keeps the order
-                        sum += (part.x + part.y) * back;
-                    }
-                }
-                return top;
-            };
-            for (;;) {
-                const float top = flags & kWhole ? pass(std::true_type{}) : pass(std::false_type{});
-                const bool grow = top > m + kGrow;   // also where m is still -infinity
-                if (!__any_sync(0xFFFFFFFFu, grow)) break;
-                if (grow) {
-                    const float f = m == -INFINITY ? 0.f : ex2(m - top);
-                    grown *= f;
-                    l *= f;
-                    m = top;
-                }
+            if (top > m + kGrow) {        // also where m is still -infinity
+                const float f = m == -INFINITY ? 0.f : ex2(m - top);
+                grown *= f;
+                l *= f;
+                m = top;
             }
-            l += sum;
+            const float ms = m == -INFINITY ? 0.f : m;
             // ---- tokens whose values were taken out of the product (16-bit cache)
             bool odd = false;
             if (FMT == KDA_KV_BF16 && !(flags & kWhole)) {
@@ -432,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                             if (!(bad[(n & 1) * 4 + (j >> 5)] >> (j & 31) & 1u)) continue;   // the same for all rows
                             const float x = tmem_ld1(tS + j);
                             if (sees(a, pos, j0 + j)) {
-                                const float pj = ex2(x * f_row - (m == -INFINITY ? 0.f : m));
+                                const float pj = ex2(x * f_row - ms);
                                 const uint8_t *line = a.kv.base + jb.rec[j >> 4] + pt * kRow;
 #pragma unroll
                                 for (int i = 0; i < 4; ++i) {
@@ -453,14 +443,43 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                     ptx::tmem_st32(tO + 32 * c, o);
                 }
             }
-            // ---- the probabilities, over the scores' first half
+            // ---- the probabilities, over the scores' first half: a chunk's 16 columns lie in what an
+            // earlier chunk has read
+            auto weigh = [&](auto all) {
+                chunks([&](const float (&x)[32], int c) {
+                    constexpr bool kAll = decltype(all)::value;
+                    const uint32_t see = kAll ? ~0u : seen(c);
+                    float p[16];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                float x[16];
+                    for (int g = 0; g < 2; ++g) {
+                        float fk = f_row, bias = -ms, back = 1.f;
+                        if (FMT == KDA_KV_I8) {
+                            fk *= jb.ks[2 * c + g];
+                            const float lg = max_nan(jb.vs[2 * c + g] - lref, -100.f) + kPBits;
+                            bias += lg;
+                            back = ex2(-lg);
+                        }
+                        const float2 ff = make_float2(fk, fk), bb = make_float2(bias, bias);
+                        float2 part = make_float2(0.f, 0.f);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(p[16 * c + i]);
-                ptx::tmem_st16(tS + 16 * c, x);
-            }
+                        for (int i = 0; i < 8; ++i) {
+                            const int e = 16 * g + 2 * i;
+                            float2 y = tcx::ffma2(make_float2(x[e], x[e + 1]), ff, bb);
+                            y.x = ex2(y.x), y.y = ex2(y.y);
+                            if (!kAll) {
+                                y.x = see >> e & 1u ? y.x : 0.f;
+                                y.y = see >> (e + 1) & 1u ? y.y : 0.f;
+                            }
+                            part = tcx::fadd2(part, y);
+                            p[8 * g + i] = __uint_as_float(pack2<FMT>(y.x, y.y));
+                        }
+                        l += (part.x + part.y) * back;
+                    }
+                    ptx::tmem_st16(tS + 16 * c, p);
+                });
+            };
+            if (flags & kWhole) weigh(std::true_type{});
+            else weigh(std::false_type{});
             ptx::tmem_wait_st();
             ptx::tc_fence_before();
             tcx::warp_arrive(&bars[PFULL + half]);
@@ -517,7 +536,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
         if (!ok && lane == 0) flag_status(a.kv.status, KDA_DEV_TIMEOUT);
     } else if (warp < kSoftWarps + kLoadWarps) {
         // ====================================================== queries, and keys and values
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
         const int lw = warp - kSoftWarps, lt = tid - kSoftWarps * 32;
         uint32_t n_item = 0;
         // 8-bit: the units' codes are read one unit ahead into registers.  A warp takes 32 tokens;
@@ -525,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
         // and their writes in different banks.
         constexpr int kRegs = kRow / 16;
         constexpr int kQuads = kRow / 64;                         // groups of four 16-byte units a row
-        uint4 kc[kRegs], vc[kRegs];
+        uint4 kc[kRegs] = {}, vc[kRegs] = {};
         const int r8 = (lane >> 3) ^ ((lane >> 2 & 1) * 5), ul = lane & 3;
         auto fetch = [&](const Job &jb, bool values, uint4 (&c)[kRegs]) {
 #pragma unroll
@@ -558,85 +576,104 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                     *reinterpret_cast<uint4 *>(line + (((2 * unit + 1) & 7) ^ (r & 7)) * 16) = hi;
                 }
         };
-        auto queries = [&](const Job &jb) {
-            constexpr int kTpr = D / 16, kRpp = kLoadWarps * 32 / kTpr;
+        // An item's queries: a thread takes 16 columns of every kRpp-th row, kBatch rows' loads under way
+        // at a time; the first batch is read while the last item's queries are still in use.
+        auto queries = [&](const Job &jb) -> bool {
+            constexpr int kTpr = D / 16, kRpp = kLoadWarps * 32 / kTpr, kBatch = FMT == KDA_KV_I8 ? 4 : 8;
             const float sign = a.scale < 0.f ? -1.f : 1.f;
             const int nrows = jb.nrows, rows = nrows > kHalf ? kRows : kHalf, c = lt % kTpr;
-#pragma unroll 2
-            for (int r = lt / kTpr; r < rows; r += kRpp) {
-                const int at = jb.row0 + r;
-                uint4 x[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-                if (r < nrows) {
-                    const uint4 *src = reinterpret_cast<const uint4 *>(
-                        static_cast<const __nv_bfloat16 *>(a.q) + ((int64_t)jb.tok0 + at / a.G) * a.q_stride +
-                        (int64_t)(jb.head * a.G + at % a.G) * D + 16 * c);
-                    x[0] = src[0], x[1] = src[1];
+            uint4 x[kBatch][2];
+#pragma unroll 1
+            for (int r0 = lt / kTpr; r0 < rows; r0 += kBatch * kRpp) {
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    const int r = r0 + i * kRpp, at = jb.row0 + r;
+                    x[i][0] = x[i][1] = make_uint4(0, 0, 0, 0);
+                    if (r < nrows) {
+                        const uint4 *src = reinterpret_cast<const uint4 *>(
+                            static_cast<const __nv_bfloat16 *>(a.q) + ((int64_t)jb.tok0 + at / a.G) * a.q_stride +
+                            (int64_t)(jb.head * a.G + at % a.G) * D + 16 * c);
+                        x[i][0] = src[0], x[i][1] = src[1];
+                    }
                 }
-                float f = a.scale * sign * kLog2e;
-                float e[16];
-                const uint32_t xw[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
+                if (r0 == lt / kTpr && !wait(QEMPTY, (n_item & 1) ^ 1)) return false;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float2 p = tcx::bf2_to_f2(xw[i]);
-                    e[2 * i] = p.x * sign, e[2 * i + 1] = p.y * sign;
+                for (int i = 0; i < kBatch; ++i) {
+                    const int r = r0 + i * kRpp;
+                    if (r >= rows) break;
+                    float f = a.scale * sign * kLog2e;
+                    float e[16];
+                    const uint32_t xw[8] = {x[i][0].x, x[i][0].y, x[i][0].z, x[i][0].w, x[i][1].x, x[i][1].y, x[i][1].z, x[i][1].w};
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float2 p = tcx::bf2_to_f2(xw[j]);
+                        e[2 * j] = p.x * sign, e[2 * j + 1] = p.y * sign;
+                    }
+                    if (FMT == KDA_KV_I8) {
+                        // a power of two that brings the row's largest magnitude to [2^10, 2^11)
+                        float top = 0.f;
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) top = fmaxf(top, fabsf(e[j]));
+#pragma unroll
+                        for (int j = 1; j < kTpr; j <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, j));
+                        const int b = (int)(__float_as_uint(top) >> 23);
+                        const int shift = b == 0 || b == 255 ? 0 : min(max(137 - b, -120), 120);
+                        const float up = __uint_as_float((uint32_t)(127 + shift) << 23);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) e[j] *= up;
+                        f *= __uint_as_float((uint32_t)(127 - shift) << 23);
+                    }
+                    uint32_t y[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) y[j] = pack2<FMT>(e[2 * j], e[2 * j + 1]);
+                    uint8_t *dst = sm + L::q + (r / kHalf) * L::half_q + (c >> 2) * (kHalf * 128);
+                    const int rr = r % kHalf;
+                    *reinterpret_cast<uint4 *>(dst + ptx::sw128_off(rr, 32 * (c & 3))) = make_uint4(y[0], y[1], y[2], y[3]);
+                    *reinterpret_cast<uint4 *>(dst + ptx::sw128_off(rr, 32 * (c & 3) + 16)) = make_uint4(y[4], y[5], y[6], y[7]);
+                    if (c == 0) qs[(n_item & 1) * kRows + r] = f;
                 }
-                if (FMT == KDA_KV_I8) {
-                    // a power of two that brings the row's largest magnitude to [2^10, 2^11)
-                    float top = 0.f;
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(e[i]));
-#pragma unroll
-                    for (int i = 1; i < kTpr; i <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, i));
-                    const int b = (int)(__float_as_uint(top) >> 23);
-                    const int shift = b == 0 || b == 255 ? 0 : min(max(137 - b, -120), 120);
-                    const float up = __uint_as_float((uint32_t)(127 + shift) << 23);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) e[i] *= up;
-                    f *= __uint_as_float((uint32_t)(127 - shift) << 23);
-                }
-                uint32_t y[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] = pack2<FMT>(e[2 * i], e[2 * i + 1]);
-                uint8_t *dst = sm + L::q + (r / kHalf) * L::half_q + (c >> 2) * (kHalf * 128);
-                const int rr = r % kHalf;
-                *reinterpret_cast<uint4 *>(dst + ptx::sw128_off(rr, 32 * (c & 3))) = make_uint4(y[0], y[1], y[2], y[3]);
-                *reinterpret_cast<uint4 *>(dst + ptx::sw128_off(rr, 32 * (c & 3) + 16)) = make_uint4(y[4], y[5], y[6], y[7]);
-                if (c == 0) qs[(n_item & 1) * kRows + r] = f;
             }
             ptx::fence_proxy_async_smem();
             tcx::warp_arrive(&bars[QFULL]);
+            return true;
         };
         bool ok = wait_job(0), stop = ok && (job(0).flags & kStop);
         if (FMT == KDA_KV_I8 && ok && !stop) {
-            fetch(job(0), false, kc);
-            fetch(job(0), true, vc);
+#pragma unroll 1
+            for (int v = 0; v < 2; ++v) {
+#pragma unroll
+                for (int i = 0; i < kRegs; ++i) kc[i] = vc[i];
+                fetch(job(0), v, vc);
+            }
         }
         for (uint32_t n = 0; ok && !stop; ++n) {
             const Job &jb = job(n);
             const int st = n & 1;
             const uint32_t par = (n >> 1 & 1) ^ 1;
             if (jb.flags & kBegin) {
-                ok = wait(QEMPTY, (n_item & 1) ^ 1);
+                ok = queries(jb);
                 if (!ok) break;
-                queries(jb);
                 ++n_item;
             }
             if (FMT == KDA_KV_I8) {
-                ok = wait(KEMPTY + st, par);
+                // keys, then values: kc goes out, vc moves up, the same of the next unit is fetched
+#pragma unroll 1
+                for (int v = 0; v < 2; ++v) {
+                    ok = wait((v ? VEMPTY : KEMPTY) + st, par);
+                    if (!ok) break;
+                    put(kc, sm + (v ? L::v : L::k) + st * L::tile);
+                    ptx::fence_proxy_async_smem();
+                    tcx::warp_arrive(&bars[(v ? VFULL : KFULL) + st]);
+                    if (v == 0) {
+                        ok = wait_job(n + 1);
+                        if (!ok) break;
+                        stop = job(n + 1).flags & kStop;
+                    }
+#pragma unroll
+                    for (int i = 0; i < kRegs; ++i) kc[i] = vc[i];
+                    if (!stop) fetch(job(n + 1), v, vc);
+                }
                 if (!ok) break;
-                put(kc, sm + L::k + st * L::tile);
-                ptx::fence_proxy_async_smem();
-                tcx::warp_arrive(&bars[KFULL + st]);
-                ok = wait_job(n + 1);
-                if (!ok) break;
-                stop = job(n + 1).flags & kStop;
-                if (!stop) fetch(job(n + 1), false, kc);
-                ok = wait(VEMPTY + st, par);
-                if (!ok) break;
-                put(vc, sm + L::v + st * L::tile);
-                ptx::fence_proxy_async_smem();
-                tcx::warp_arrive(&bars[VFULL + st]);
-                if (!stop) fetch(job(n + 1), true, vc);
             } else {
                 // values that not every row sees: a token that no row sees is cleared (0 times what a
                 // stale slot holds need not be 0), and one with an infinity or a NaN is taken out and
@@ -676,7 +713,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
             done(n);
         }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         if (warp == kMmaWarp) {
             // ================================================== products
             if (lane == 0) {
@@ -693,7 +729,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                 auto desc = [&](uint32_t lo) { return (uint64_t)hi << 32 | lo; };
                 auto scores = [&](int half, int st) {
                     const uint32_t ql = low(sb + L::q + half * L::half_q, 16), kl = low(sb + L::k + st * L::tile, 16);
-#pragma unroll
+#pragma unroll 4
                     for (int s = 0; s < D / 16; ++s) {
                         const uint32_t off = ((s >> 2) * L::blk + (s & 3) * 32) >> 4;
                         ptx::mma_bf16(tm + half * 128, desc(ql + off), desc(kl + off), idesc<FMT>(128, 128, 0), s > 0 ? 1u : 0u);
@@ -702,7 +738,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                 };
                 auto outputs = [&](int half, int st) {
                     const uint32_t vl = low(sb + L::v + st * L::tile, L::blk);
-#pragma unroll
+#pragma unroll 4
                     for (int s = 0; s < kUnit / 16; ++s)
                         ptx::mma_bf16_ta(tm + 256 + half * 128, tm + half * 128 + s * 8, desc(vl + (s * 2048 >> 4)),
                                          idesc<FMT>(128, D, 1), 1u);
