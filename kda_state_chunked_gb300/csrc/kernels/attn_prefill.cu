@@ -62,9 +62,10 @@ struct __align__(16) Job {
     int32_t s, last_cta, pmin, pmax;
     int32_t slot[8];                    // of each group: first token's slot in its page,
     int64_t rec[8];                     // its record's place in the pool,
-    float ks[8], vs[8];                 // 8-bit: key scale, log2 of the value scale
-    float vtop;                         // log2 of the largest value scale
-    int32_t pad[3];
+    float ks[8];                        // 8-bit: key scale, log2 of what the probabilities are scaled by,
+    float lg[8], back[8];               // and the inverse of that
+    float lref, shift;                  // log2 of ref, and by what O follows its last move
+    int32_t pad[2];
 };
 
 template <int D>
@@ -116,11 +117,11 @@ __device__ __forceinline__ float tmem_ld1(uint32_t addr) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r)::"memory");
     return __uint_as_float(r);
 }
-// The larger of two numbers; NaN if either is.
-__device__ __forceinline__ float max_nan(float x, float y) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
-    return r;
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 // Sixteen codes as fp16, in two 16-byte units.
@@ -306,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
         uint32_t n_s = 0, n_item = 0;   // units of this half, items so far: the barriers' parities
         int32_t pos = -1;
         bool in = false, ok = true;
-        float m = -INFINITY, l = 0.f, lref = -INFINITY, f_row = 0.f;   // lref: log2 of ref
+        float m = -INFINITY, l = 0.f, f_row = 0.f;
         for (uint32_t n = 0;; ++n) {
             ok = wait_job(n);
             if (!ok) break;
@@ -322,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
             if (flags & kBegin) {
                 in = row < nrows;
                 pos = in ? jb.base + at / a.G : -1;
-                m = -INFINITY, l = 0.f, lref = -INFINITY;
+                m = -INFINITY, l = 0.f;
                 float z[32];
 #pragma unroll
                 for (int i = 0; i < 32; ++i) z[i] = 0.f;
@@ -379,12 +380,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
             };
             if (flags & kWhole) most(std::true_type{});
             else most(std::false_type{});
-            // ---- the references: m lags behind the maximum, ref behind the value scales
-            float grown = 1.f;            // what O is to be multiplied by
-            if (FMT == KDA_KV_I8 && jb.vtop > lref + 1.f) {
-                grown = ex2(lref - jb.vtop);
-                lref = jb.vtop;
-            }
+            // ---- the row's reference, which lags behind its maximum
+            float grown = FMT == KDA_KV_I8 ? jb.shift : 1.f;   // what O is to be multiplied by
             if (top > m + kGrow) {        // also where m is still -infinity
                 const float f = m == -INFINITY ? 0.f : ex2(m - top);
                 grown *= f;
@@ -455,9 +452,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                         float fk = f_row, bias = -ms, back = 1.f;
                         if (FMT == KDA_KV_I8) {
                             fk *= jb.ks[2 * c + g];
-                            const float lg = max_nan(jb.vs[2 * c + g] - lref, -100.f) + kPBits;
-                            bias += lg;
-                            back = ex2(-lg);
+                            bias += jb.lg[2 * c + g];
+                            back = jb.back[2 * c + g];
                         }
                         const float2 ff = make_float2(fk, fk), bb = make_float2(bias, bias);
                         float2 part = make_float2(0.f, 0.f);
@@ -491,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                 ptx::tc_fence_after();
                 const bool all = (flags & kStarts) && (flags & kEnds);
                 const int64_t orow = ((int64_t)jb.tok0 + at / a.G) * a.Hq + jb.head * a.G + at % a.G;
-                const float unscale = FMT == KDA_KV_I8 ? exp2f(lref - kPBits) : 1.f;
+                const float unscale = FMT == KDA_KV_I8 ? exp2f(jb.lref - kPBits) : 1.f;
                 const float f = all ? (l == 0.f ? 0.f : unscale / l) : unscale;
                 float *part = a.part + ((int64_t)(blockIdx.x * 2 + (flags & kStarts ? 1 : 0)) * kRows + row) * kPartRow<D>;
 #pragma unroll 1
@@ -715,78 +711,82 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
     } else {
         if (warp == kMmaWarp) {
             // ================================================== products
-            if (lane == 0) {
-                const uint32_t sb = ptx::smem_u32(sm);
-                uint32_t n_item = 0, n_p[2] = {0, 0};
-                // Descriptors of one operand differ in their low word only, by an address that a step adds
-                // to; the empty statement keeps the compiler from holding them all in registers.
-                const uint32_t hi = (uint32_t)(ptx::sdesc_sw128(0, 16, 1024) >> 32);
-                auto low = [&](uint32_t at, uint32_t lbo) {
-                    uint32_t x = (at >> 4) | (lbo >> 4) << 16;
-                    asm volatile("" : "+r"(x));
-                    return x;
-                };
-                auto desc = [&](uint32_t lo) { return (uint64_t)hi << 32 | lo; };
-                auto scores = [&](int half, int st) {
-                    const uint32_t ql = low(sb + L::q + half * L::half_q, 16), kl = low(sb + L::k + st * L::tile, 16);
-#pragma unroll 4
+            // The whole warp walks along and one lane issues: addresses then stay in uniform registers,
+            // and a product takes the 64 cycles that the pipe needs (about 100 from a lone lane).
+            const uint32_t sb = ptx::smem_u32(sm);
+            const uint32_t tu = __shfl_sync(0xFFFFFFFFu, tm, 0);
+            uint32_t n_item = 0, n_p[2] = {0, 0};
+            auto scores = [&](int half, int st) {
+                const uint64_t qd = ptx::sdesc_sw128(sb + L::q + half * L::half_q, 16, 1024);
+                const uint64_t kd = ptx::sdesc_sw128(sb + L::k + st * L::tile, 16, 1024);
+                if (elect()) {
+#pragma unroll
                     for (int s = 0; s < D / 16; ++s) {
                         const uint32_t off = ((s >> 2) * L::blk + (s & 3) * 32) >> 4;
-                        ptx::mma_bf16(tm + half * 128, desc(ql + off), desc(kl + off), idesc<FMT>(128, 128, 0), s > 0 ? 1u : 0u);
+                        ptx::mma_bf16(tu + half * 128, qd + off, kd + off, idesc<FMT>(128, 128, 0), s > 0 ? 1u : 0u);
                     }
                     ptx::mma_commit(&bars[SFULL + half]);
-                };
-                auto outputs = [&](int half, int st) {
-                    const uint32_t vl = low(sb + L::v + st * L::tile, L::blk);
-#pragma unroll 4
+                }
+                __syncwarp();
+            };
+            auto outputs = [&](int half, int st) {
+                const uint64_t vd = ptx::sdesc_sw128(sb + L::v + st * L::tile, L::blk, 1024);
+                if (elect()) {
+#pragma unroll
                     for (int s = 0; s < kUnit / 16; ++s)
-                        ptx::mma_bf16_ta(tm + 256 + half * 128, tm + half * 128 + s * 8, desc(vl + (s * 2048 >> 4)),
+                        ptx::mma_bf16_ta(tu + 256 + half * 128, tu + half * 128 + s * 8, vd + (s * 2048 >> 4),
                                          idesc<FMT>(128, D, 1), 1u);
                     ptx::mma_commit(&bars[OFULL + half]);
-                };
-                bool ok = true;
-                for (uint32_t n = 0; ok; ++n) {
-                    ok = wait1(JFULL + n % kJobs, n / kJobs & 1);
+                }
+                __syncwarp();
+            };
+            auto commit = [&](int b) {
+                if (elect()) ptx::mma_commit(&bars[b]);
+                __syncwarp();
+            };
+            bool ok = true;
+            for (uint32_t n = 0; ok; ++n) {
+                ok = wait_job(n);
+                if (!ok) break;
+                const int32_t flags = job(n).flags;
+                if (flags & kStop) break;
+                const int halves = job(n).nrows > kHalf ? 2 : 1, st = n & 1, nx = st ^ 1;
+                done(n);
+                // the scores of an item's first unit; those of the next come between the outputs
+                if (flags & kBegin) {
+                    ok = wait(QFULL, n_item & 1) && wait(KFULL + st, n >> 1 & 1);
                     if (!ok) break;
-                    const int32_t flags = job(n).flags;
-                    if (flags & kStop) break;
-                    const int halves = job(n).nrows > kHalf ? 2 : 1, st = n & 1, nx = st ^ 1;
-                    ptx::mbar_arrive(&bars[JEMPTY + n % kJobs]);
-                    // the scores of an item's first unit; those of the next come between the outputs
-                    if (flags & kBegin) {
-                        ok = wait1(QFULL, n_item & 1) && wait1(KFULL + st, n >> 1 & 1);
+                    ptx::tc_fence_after();
+#pragma unroll 1
+                    for (int h = 0; h < halves; ++h) scores(h, st);
+                    commit(KEMPTY + st);
+                    if (flags & kEnd) commit(QEMPTY);
+                    ++n_item;
+                }
+#pragma unroll 1
+                for (int h = 0; h < halves; ++h) {
+                    ok = wait(PFULL + h, n_p[h] & 1) && (h || wait(VFULL + st, n >> 1 & 1));
+                    if (!ok) break;
+                    if (h) ++n_p[1];
+                    else ++n_p[0];
+                    ptx::tc_fence_after();
+                    outputs(h, st);
+                    if (h + 1 == halves) commit(VEMPTY + st);
+                    if (!(flags & kEnd)) {
+                        ok = h || wait(KFULL + nx, (n + 1) >> 1 & 1);
                         if (!ok) break;
                         ptx::tc_fence_after();
-                        for (int h = 0; h < halves; ++h) scores(h, st);
-                        ptx::mma_commit(&bars[KEMPTY + st]);
-                        if (flags & kEnd) ptx::mma_commit(&bars[QEMPTY]);
-                        ++n_item;
-                    }
-                    for (int h = 0; h < halves; ++h) {
-                        ok = wait1(PFULL + h, n_p[h] & 1) && (h || wait1(VFULL + st, n >> 1 & 1));
-                        if (!ok) break;
-                        ++n_p[h];
-                        ptx::tc_fence_after();
-                        outputs(h, st);
-                        if (h + 1 == halves) ptx::mma_commit(&bars[VEMPTY + st]);
-                        if (!(flags & kEnd)) {
-                            ok = h || wait1(KFULL + nx, (n + 1) >> 1 & 1);
-                            if (!ok) break;
-                            ptx::tc_fence_after();
-                            scores(h, nx);
-                            if (h + 1 == halves) {
-                                ptx::mma_commit(&bars[KEMPTY + nx]);
-                                // the item's last scores are under way: its queries may go
-                                if (wait1(JFULL + (n + 1) % kJobs, (n + 1) / kJobs & 1) && (job(n + 1).flags & kEnd))
-                                    ptx::mma_commit(&bars[QEMPTY]);
-                            }
+                        scores(h, nx);
+                        if (h + 1 == halves) {
+                            commit(KEMPTY + nx);
+                            // the item's last scores are under way: its queries may go
+                            if (wait_job(n + 1) && (job(n + 1).flags & kEnd)) commit(QEMPTY);
                         }
                     }
                 }
-                ptx::mma_commit(&bars[DRAIN]);
-                wait_bar(&bars[DRAIN], 0, nullptr);
             }
-            __syncwarp();
+            commit(DRAIN);
+            wait_bar(&bars[DRAIN], 0, nullptr);
         } else if (FMT == KDA_KV_BF16 && warp == kCopyWarp) {
             // ================================================== copies (16-bit cache)
             uint32_t n_k = 0, n_v = 0;                            // tiles asked for
@@ -823,6 +823,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
             if (lane == 0) a.split[blockIdx.x].last_cta = -1;
             const int64_t end = C > 0 ? (int64_t)(blockIdx.x + 1) * W / C : 0;
             int32_t u_first = w.u;
+            float lref = -INFINITY;
             for (uint32_t n = 0;; ++n) {
                 if (!wait(JEMPTY + n % kJobs, (n / kJobs & 1) ^ 1)) break;
                 Job &jb = jobs[n % kJobs];
@@ -844,17 +845,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                     jb.rec[lane] = rec ? rec - a.kv.base : 0;
                 }
                 if (FMT == KDA_KV_I8) {
-                    // a value scale of 0 stands for codes of 0: any factor does, so the largest other
+                    // ref moves up to the unit's largest value scale when that has doubled.  A scale of 0
+                    // stands for codes of 0: any factor does, so the largest other.
                     const float2 sc = rec ? __ldg(reinterpret_cast<const float2 *>(rec + 2 * pt * kRow)) : make_float2(0.f, 0.f);
                     const float x = fabsf(sc.y);
                     float lg = x > 0.f && x < INFINITY ? log2f(x) : -INFINITY, top = lg;
 #pragma unroll
                     for (int i = 1; i < 8; i <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, i));
-                    top = fmaxf(top, -100.f);
-                    if (x == 0.f) lg = top;
-                    if (!(x < INFINITY)) lg = NAN;
-                    if (lane < 8) jb.ks[lane] = fabsf(sc.x), jb.vs[lane] = lg;
-                    if (lane == 0) jb.vtop = top;
+                    top = fmaxf(__shfl_sync(0xFFFFFFFFu, top, 0), -100.f);
+                    if (w.u == u_first) lref = -INFINITY;
+                    float shift = 1.f;
+                    if (top > lref + 1.f) {
+                        shift = exp2f(lref - top);
+                        lref = top;
+                    }
+                    lg = x == 0.f ? kPBits : x < INFINITY ? fmaxf(lg - lref, -100.f) + kPBits : NAN;
+                    if (lane < 8) jb.ks[lane] = fabsf(sc.x), jb.lg[lane] = lg, jb.back[lane] = exp2f(-lg);
+                    if (lane == 0) jb.lref = lref, jb.shift = shift;
                 }
                 if (lane == 0) {
                     const bool ends = w.left >= t.units - w.u;   // the item's last unit is in this share
