@@ -61,7 +61,7 @@ struct __align__(16) Job {
     uint32_t live;                      // groups of 16 tokens that are there
     int32_t s, last_cta, pmin, pmax;
     int32_t slot[8];                    // of each group: first token's slot in its page,
-    int64_t rec[8];                     // its record's place in the pool,
+    int64_t rec[8];                     // its record's place in the pool (the pool's first where it is not there),
     float ks[8];                        // 8-bit: key scale, log2 of what the probabilities are scaled by,
     float lg[8], back[8];               // and the inverse of that
     float lref, shift;                  // log2 of ref, and by what O follows its last move
@@ -541,35 +541,33 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
         constexpr int kQuads = kRow / 64;                         // groups of four 16-byte units a row
         uint4 kc[kRegs] = {}, vc[kRegs] = {};
         const int r8 = (lane >> 3) ^ ((lane >> 2 & 1) * 5), ul = lane & 3;
+        // A lane's places: its units' in a page's lines (rows 8 apart lie 1024 bytes apart, the upper
+        // four units of a line opposite the lower), and those of their two halves in a tile.
+        const uint32_t from = kv_tile_off<kRow>(pt, r8, 16 * ul), from4 = from ^ 64u;
+        const uint32_t to = (32 * lw + r8) * 128 + (((2 * ul) ^ (r8 & 7)) << 4);
         auto fetch = [&](const Job &jb, bool values, uint4 (&c)[kRegs]) {
 #pragma unroll
             for (int y = 0; y < 2; ++y) {                         // a group of 16 tokens
-                const bool there = jb.live >> (2 * lw + y) & 1u;
-                const uint8_t *tile = a.kv.base + jb.rec[2 * lw + y] + (values ? pt * kRow : 0);
-                const int slot = jb.slot[2 * lw + y] + r8;
+                const uint8_t *src = a.kv.base + (jb.rec[2 * lw + y] + (values ? pt * kRow : 0) +
+                                                  jb.slot[2 * lw + y] * (kRow < 128 ? kRow : 128));
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
 #pragma unroll
-                    for (int x = 0; x < kQuads; ++x) {
-                        uint4 &z = c[(2 * y + i) * kQuads + x];
-                        z = make_uint4(0, 0, 0, 0);
-                        if (there)
-                            z = __ldg(reinterpret_cast<const uint4 *>(
-                                tile + kv_tile_off<kRow>(pt, slot + 8 * i, 16 * (4 * x + ul))));
-                    }
+                    for (int x = 0; x < kQuads; ++x)
+                        c[(2 * y + i) * kQuads + x] =
+                            __ldg(reinterpret_cast<const uint4 *>(src + (x ? from4 : from) + i * 8 * (kRow < 128 ? kRow : 128)));
             }
         };
         auto put = [&](const uint4 (&c)[kRegs], uint8_t *tile) {
+            uint8_t *lo_at = tile + to, *hi_at = tile + (to ^ 16u);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int x = 0; x < kQuads; ++x) {
                     uint4 lo, hi;
                     codes_to_half(c[i * kQuads + x], lo, hi);
-                    const int r = 32 * lw + 8 * i + r8, unit = 4 * x + ul;      // columns 16 unit ..
-                    uint8_t *line = tile + (unit >> 2) * L::blk + r * 128;
-                    *reinterpret_cast<uint4 *>(line + (((2 * unit) & 7) ^ (r & 7)) * 16) = lo;
-                    *reinterpret_cast<uint4 *>(line + (((2 * unit + 1) & 7) ^ (r & 7)) * 16) = hi;
+                    *reinterpret_cast<uint4 *>(lo_at + x * L::blk + i * 1024) = lo;
+                    *reinterpret_cast<uint4 *>(hi_at + x * L::blk + i * 1024) = hi;
                 }
         };
         // An item's queries: a thread takes 16 columns of every kRpp-th row, kBatch rows' loads under way
