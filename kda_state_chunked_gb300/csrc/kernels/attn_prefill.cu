@@ -9,18 +9,20 @@
 // other.  Tensor memory holds S of both halves (128 columns each, P over its first half) and O of
 // both: 512 columns.  Keys and values of a unit of 128 tokens are read once for both halves.
 //
-// One CTA of 16 warps an SM:
-//   warps 0-3, 4-7   softmax of a half, a thread a row: scores from tensor memory, probabilities
-//                    back into it, at the end the output.  The probabilities are taken against
-//                    a reference that follows the row's maximum only once that has grown by more
-//                    than 2^8 (fp16 and bf16 have the room), so O is seldom rescaled.
-//   warps 8-11       queries into shared memory; 8-bit cache: codes from global memory through
+// One CTA of 28 warps an SM:
+//   warps 0-15       softmax, eight to a half, two threads a row (64 tokens each): scores from tensor
+//                    memory, probabilities back into it, at the end the output.  The probabilities
+//                    are taken against a reference that follows the row's maximum only once that
+//                    has grown by more than 2^8 (fp16 and bf16 have the room), so O is seldom
+//                    rescaled.  With a thread a row a half took 3,300 cycles from its scores to its
+//                    last probability, and the pipe stood idle for most of that.
+//   warps 16-23      queries into shared memory; 8-bit cache: codes from global memory through
 //                    registers to fp16 tiles (a page's bytes never lie in shared memory);
 //                    16-bit cache: a look at values that not every row sees
-//   warp 12          issues the products
-//   warp 13          16-bit cache: bulk copies of pages, whose lines already lie as the matrix
+//   warp 24          issues the products
+//   warp 25          16-bit cache: bulk copies of pages, whose lines already lie as the matrix
 //                    unit's 128-byte swizzle wants them
-//   warp 14          walks the list of units and hands each on as a job: its tokens, records, scales
+//   warp 26          walks the list of units and hands each on as a job: its tokens, records, scales
 // The walk's divisions and table reads are in one place, up to eight units ahead: with a copy of it
 // in every role the kernel was 220 KB of code and stood waiting for instructions (9,700 cycles a
 // unit).
@@ -43,7 +45,7 @@ namespace {
 using namespace attn;
 
 constexpr int kRows = kAttnPrefillRows, kHalf = 128, kUnit = 128;
-constexpr int kSoftWarps = 8, kLoadWarps = 4, kMmaWarp = 12, kCopyWarp = 13, kWalkWarp = 14, kThreads = 16 * 32;
+constexpr int kSoftWarps = 16, kLoadWarps = 8, kMmaWarp = 24, kCopyWarp = 25, kWalkWarp = 26, kThreads = 28 * 32;
 constexpr float kGrow = 8.f;            // bits that a row's maximum may grow before O is rescaled
 constexpr float kPBits = 6.f;           // 8-bit: bits that a probability is scaled up in fp16
 constexpr int kJobs = 8;                // units handed out and not yet done with
@@ -74,7 +76,8 @@ struct Lay {
     static constexpr int q = 0, k = 2 * half_q, v = k + 2 * tile, misc = v + 2 * tile;
     static constexpr int qs = misc;                        // [2][256] row factors
     static constexpr int jobs = qs + 2 * kRows * 4;        // [kJobs]
-    static constexpr int bad = jobs + kJobs * (int)sizeof(Job);   // [2][4] tokens taken out of a value tile
+    static constexpr int pair = jobs + kJobs * (int)sizeof(Job);  // [2][2][256] what a row's two threads tell each other
+    static constexpr int bad = pair + 2 * 2 * kRows * 4;   // [2][4] tokens taken out of a value tile
     static constexpr int plan = bad + 2 * 16;              // the split's scratch
     static constexpr int bar = plan + 4096;
     static constexpr int total = bar + 512;
@@ -100,16 +103,21 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     }
 }
 
+// 32 lanes x 16 columns, a lane a thread.
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&v)[16]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+                   "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+                 : "r"(addr)
+                 : "memory");
+}
 // Wait for the loads of v from tensor memory; naming the registers keeps their uses behind it.
-__device__ __forceinline__ void wait_ld(float (&v)[32]) {
+__device__ __forceinline__ void wait_ld(float (&v)[16]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
-                   "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]),
-                   "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]),
-                   "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27])
+                   "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
                  :
                  : "memory");
-    asm volatile("" : "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31])::"memory");
 }
 __device__ __forceinline__ float tmem_ld1(uint32_t addr) {
     uint32_t r;
@@ -243,7 +251,7 @@ __device__ __forceinline__ void find_share(const AttnArgs &a, int64_t *sums, Wal
 template <int FMT, int D>
 __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_constant__ AttnArgs a) {
     using L = Lay<D>;
-    constexpr int kBlks = D / 64, kChunks = D / 32, kRow = kKvRow<FMT, D>;
+    constexpr int kBlks = D / 64, kRow = kKvRow<FMT, D>;
     static_assert(NBAR * 8 <= 512, "barriers");
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = ptx::smem_align1024(smem_raw);
@@ -268,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
             ptx::mbar_init(&bars[VEMPTY + i], 1);
             ptx::mbar_init(&bars[VRAW + i], 1);
             ptx::mbar_init(&bars[SFULL + i], 1);
-            ptx::mbar_init(&bars[PFULL + i], 4);
+            ptx::mbar_init(&bars[PFULL + i], kSoftWarps / 2);
             ptx::mbar_init(&bars[OFULL + i], 1);
         }
         ptx::mbar_init(&bars[DRAIN], 1);
@@ -301,9 +309,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
     // where their register arrays allow it.
     if (warp < kSoftWarps) {
         // ====================================================== softmax and output
-        const int half = warp / 4, row = half * kHalf + (warp % 4) * 32 + lane;
+        const int half = warp / 8, side = warp / 4 % 2, row = half * kHalf + (warp % 4) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp % 4) * 32) << 16;
-        const uint32_t tS = tm + lanes + half * 128, tO = tm + lanes + 256 + half * 128;
+        const uint32_t tS = tm + lanes + half * 128 + side * 64;           // this thread's 64 scores
+        const uint32_t tO = tm + lanes + 256 + half * 128 + side * (D / 2);   // and its half of the output
+        float *pair = reinterpret_cast<float *>(sm + L::pair);
+        auto meet = [&]() { tcx::named_bar(1 + half * 4 + warp % 4, 64); };    // the two warps of these rows
         uint32_t n_s = 0, n_item = 0;   // units of this half, items so far: the barriers' parities
         int32_t pos = -1;
         bool in = false, ok = true;
@@ -324,62 +335,62 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                 in = row < nrows;
                 pos = in ? jb.base + at / a.G : -1;
                 m = -INFINITY, l = 0.f;
-                float z[32];
+                float z[16];
 #pragma unroll
-                for (int i = 0; i < 32; ++i) z[i] = 0.f;
+                for (int i = 0; i < 16; ++i) z[i] = 0.f;
 #pragma unroll
-                for (int c = 0; c < kChunks; ++c) ptx::tmem_st32(tO + 32 * c, z);
+                for (int c = 0; c < D / 32; ++c) ptx::tmem_st16(tO + 16 * c, z);
             }
             ok = wait(SFULL + half, n_s & 1);
             if (!ok) break;
             ptx::tc_fence_after();
             if (flags & kBegin) f_row = qs[(n_item & 1) * kRows + row];
-            const uint32_t live = jb.live;
-            // columns that this row sees, 32 at a time
+            // columns of group c (16 tokens) that this row sees
             auto seen = [&](int c) -> uint32_t {
-                auto low = [](int32_t k) -> uint32_t { return k <= 0 ? 0u : k >= 32 ? ~0u : (1u << k) - 1u; };
-                const int32_t b = j0 + 32 * c;
+                auto low = [](int32_t k) -> uint32_t { return k <= 0 ? 0u : k >= 16 ? 0xFFFFu : (1u << k) - 1u; };
+                const int32_t b = j0 + 64 * side + 16 * c;
                 uint32_t x = low(pos + 1 - b);
                 if (a.window > 0) x &= ~low(pos - a.window + 1 - b) | low(a.sinks - b);
-                if (!(live >> (2 * c) & 1u)) x &= 0xFFFF0000u;
-                if (!(live >> (2 * c + 1) & 1u)) x &= 0x0000FFFFu;
-                return x;
+                return jb.live >> (4 * side + c) & 1u ? x : 0u;
             };
-            // 32 scores at a time, the next 32 on their way from tensor memory
-            auto chunks = [&](auto step) {
-                float x[2][32];
-                ptx::tmem_ld32(tS, x[0]);
+            // 16 scores at a time, the next on their way from tensor memory
+            auto groups = [&](auto step) {
+                float x[2][16];
+                tmem_ld16(tS, x[0]);
 #pragma unroll 1
                 for (int c = 0; c < 4; c += 2) {
                     wait_ld(x[0]);
-                    ptx::tmem_ld32(tS + 32 * (c + 1), x[1]);
+                    tmem_ld16(tS + 16 * (c + 1), x[1]);
                     step(x[0], c);
                     wait_ld(x[1]);
-                    if (c == 0) ptx::tmem_ld32(tS + 64, x[0]);
+                    if (c == 0) tmem_ld16(tS + 32, x[0]);
                     step(x[1], c + 1);
                 }
             };
             // ---- the row's maximum
             float top = -INFINITY;
             auto most = [&](auto all) {
-                chunks([&](const float (&x)[32], int c) {
+                groups([&](const float (&x)[16], int c) {
                     constexpr bool kAll = decltype(all)::value;
                     const uint32_t see = kAll ? ~0u : seen(c);
+                    float gt = -INFINITY;
 #pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        float gt = -INFINITY;
-#pragma unroll
-                        for (int i = 16 * g; i < 16 * g + 16; i += 2)
-                            gt = fmaxf(gt, fmaxf(kAll || (see >> i & 1u) ? x[i] : -INFINITY,
-                                                 kAll || (see >> (i + 1) & 1u) ? x[i + 1] : -INFINITY));
-                        // f >= 0: the product keeps the order
-                        const float fk = FMT == KDA_KV_I8 ? f_row * jb.ks[2 * c + g] : f_row;
-                        top = fmaxf(top, gt == -INFINITY ? gt : gt * fk);
-                    }
+                    for (int i = 0; i < 16; i += 2)
+                        gt = fmaxf(gt, fmaxf(kAll || (see >> i & 1u) ? x[i] : -INFINITY,
+                                             kAll || (see >> (i + 1) & 1u) ? x[i + 1] : -INFINITY));
+                    // f >= 0: the product keeps the order
+                    const float fk = FMT == KDA_KV_I8 ? f_row * jb.ks[4 * side + c] : f_row;
+                    top = fmaxf(top, gt == -INFINITY ? gt : gt * fk);
                 });
             };
             if (flags & kWhole) most(std::true_type{});
             else most(std::false_type{});
+            {
+                float *mine = pair + ((n_s & 1) * 2 + side) * kRows, *other = pair + ((n_s & 1) * 2 + (side ^ 1)) * kRows;
+                mine[row] = top;
+                meet();
+                top = fmaxf(top, other[row]);
+            }
             // ---- the row's reference, which lags behind its maximum
             float grown = FMT == KDA_KV_I8 ? jb.shift : 1.f;   // what O is to be multiplied by
             if (top > m + kGrow) {        // also where m is still -infinity
@@ -407,24 +418,24 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                     ptx::tmem_wait_st();
                 }
 #pragma unroll 1
-                for (int c = 0; c < kChunks; ++c) {
-                    float o[32];
-                    ptx::tmem_ld32(tO + 32 * c, o);
+                for (int c = 0; c < D / 32; ++c) {
+                    float o[16];
+                    tmem_ld16(tO + 16 * c, o);
                     wait_ld(o);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] *= grown;
+                    for (int i = 0; i < 16; ++i) o[i] *= grown;
                     if (FMT == KDA_KV_BF16 && odd) {
 #pragma unroll 1
                         for (int j = 0; j < kUnit; ++j) {
                             if (!(bad[(n & 1) * 4 + (j >> 5)] >> (j & 31) & 1u)) continue;   // the same for all rows
-                            const float x = tmem_ld1(tS + j);
+                            const float x = tmem_ld1(tS - side * 64 + j);
                             if (sees(a, pos, j0 + j)) {
                                 const float pj = ex2(x * f_row - ms);
                                 const uint8_t *line = a.kv.base + jb.rec[j >> 4] + pt * kRow;
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) {
+                                for (int i = 0; i < 2; ++i) {
                                     const uint4 v = *reinterpret_cast<const uint4 *>(
-                                        line + kv_tile_off<kRow>(pt, jb.slot[j >> 4] + (j & 15), 64 * c + 16 * i));
+                                        line + kv_tile_off<kRow>(pt, jb.slot[j >> 4] + (j & 15), side * D + 32 * c + 16 * i));
                                     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                                     for (int y = 0; y < 4; ++y) {
@@ -437,41 +448,38 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                             __syncwarp();
                         }
                     }
-                    ptx::tmem_st32(tO + 32 * c, o);
+                    ptx::tmem_st16(tO + 16 * c, o);
                 }
             }
-            // ---- the probabilities, over the scores' first half: a chunk's 16 columns lie in what an
-            // earlier chunk has read
+            if (FMT == KDA_KV_BF16 && odd) meet();   // the other warp is done with these scores too
+            // ---- the probabilities, over the scores that they come from: a group's 8 columns lie in
+            // what an earlier group has read
             auto weigh = [&](auto all) {
-                chunks([&](const float (&x)[32], int c) {
+                groups([&](const float (&x)[16], int c) {
                     constexpr bool kAll = decltype(all)::value;
                     const uint32_t see = kAll ? ~0u : seen(c);
-                    float p[16];
-#pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        float fk = f_row, bias = -ms, back = 1.f;
-                        if (FMT == KDA_KV_I8) {
-                            fk *= jb.ks[2 * c + g];
-                            bias += jb.lg[2 * c + g];
-                            back = jb.back[2 * c + g];
-                        }
-                        const float2 ff = make_float2(fk, fk), bb = make_float2(bias, bias);
-                        float2 part = make_float2(0.f, 0.f);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int e = 16 * g + 2 * i;
-                            float2 y = tcx::ffma2(make_float2(x[e], x[e + 1]), ff, bb);
-                            y.x = ex2(y.x), y.y = ex2(y.y);
-                            if (!kAll) {
-                                y.x = see >> e & 1u ? y.x : 0.f;
-                                y.y = see >> (e + 1) & 1u ? y.y : 0.f;
-                            }
-                            part = tcx::fadd2(part, y);
-                            p[8 * g + i] = __uint_as_float(pack2<FMT>(y.x, y.y));
-                        }
-                        l += (part.x + part.y) * back;
+                    float p[8];
+                    float fk = f_row, bias = -ms, back = 1.f;
+                    if (FMT == KDA_KV_I8) {
+                        fk *= jb.ks[4 * side + c];
+                        bias += jb.lg[4 * side + c];
+                        back = jb.back[4 * side + c];
                     }
-                    ptx::tmem_st16(tS + 16 * c, p);
+                    const float2 ff = make_float2(fk, fk), bb = make_float2(bias, bias);
+                    float2 part = make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        float2 y = tcx::ffma2(make_float2(x[2 * i], x[2 * i + 1]), ff, bb);
+                        y.x = ex2(y.x), y.y = ex2(y.y);
+                        if (!kAll) {
+                            y.x = see >> (2 * i) & 1u ? y.x : 0.f;
+                            y.y = see >> (2 * i + 1) & 1u ? y.y : 0.f;
+                        }
+                        part = tcx::fadd2(part, y);
+                        p[i] = __uint_as_float(pack2<FMT>(y.x, y.y));
+                    }
+                    l += (part.x + part.y) * back;
+                    ptx::tmem_st8(tS + 8 * c, p);
                 });
             };
             if (flags & kWhole) weigh(std::true_type{});
@@ -482,6 +490,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
             ++n_s;
             if (flags & kEnd) {
                 // ---- the item's output, or this CTA's part of it
+                {
+                    float *mine = pair + ((n_s & 1) * 2 + side) * kRows, *other = pair + ((n_s & 1) * 2 + (side ^ 1)) * kRows;
+                    mine[row] = l;
+                    meet();
+                    l += other[row];
+                    meet();              // the next item's first maxima go to the same place
+                }
                 ok = wait(OFULL + half, (n_s - 1) & 1);
                 if (!ok) break;
                 ptx::tc_fence_after();
@@ -491,28 +506,29 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                 const float f = all ? (l == 0.f ? 0.f : unscale / l) : unscale;
                 float *part = a.part + ((int64_t)(blockIdx.x * 2 + (flags & kStarts ? 1 : 0)) * kRows + row) * kPartRow<D>;
 #pragma unroll 1
-                for (int c = 0; c < kChunks; ++c) {
-                    float o[32];
-                    ptx::tmem_ld32(tO + 32 * c, o);
+                for (int c = 0; c < D / 32; ++c) {
+                    float o[16];
+                    tmem_ld16(tO + 16 * c, o);
                     wait_ld(o);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = all && l == 0.f ? 0.f : o[i] * f;
+                    for (int i = 0; i < 16; ++i) o[i] = all && l == 0.f ? 0.f : o[i] * f;
+                    const int col = side * (D / 2) + 16 * c;
                     if (in && all) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o) + orow * D + 32 * c);
+                        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o) + orow * D + col);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
+                        for (int i = 0; i < 2; ++i)
                             dst[i] = make_uint4(tcx::f2_to_bf2(o[8 * i], o[8 * i + 1]), tcx::f2_to_bf2(o[8 * i + 2], o[8 * i + 3]),
                                                 tcx::f2_to_bf2(o[8 * i + 4], o[8 * i + 5]), tcx::f2_to_bf2(o[8 * i + 6], o[8 * i + 7]));
                     } else if (in) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            reinterpret_cast<float4 *>(part + 32 * c)[i] =
+                        for (int i = 0; i < 4; ++i)
+                            reinterpret_cast<float4 *>(part + col)[i] =
                                 make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                     }
                     __syncwarp();
                 }
                 ptx::tc_fence_before();
-                if (in) {
+                if (in && side == 0) {
                     if (!all) part[D] = m, part[D + 1] = l;
                     else if (a.lse) a.lse[orow] = lse_of(m, l);
                 }
@@ -534,34 +550,30 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
         // ====================================================== queries, and keys and values
         const int lw = warp - kSoftWarps, lt = tid - kSoftWarps * 32;
         uint32_t n_item = 0;
-        // 8-bit: the units' codes are read one unit ahead into registers.  A warp takes 32 tokens;
+        // 8-bit: the units' codes are read one unit ahead into registers.  A warp takes 16 tokens;
         // eight lanes take four units of token r and of token r ^ 5, which keeps both their reads
         // and their writes in different banks.
-        constexpr int kRegs = kRow / 16;
+        constexpr int kRegs = kRow / 32;
         constexpr int kQuads = kRow / 64;                         // groups of four 16-byte units a row
         uint4 kc[kRegs] = {}, vc[kRegs] = {};
         const int r8 = (lane >> 3) ^ ((lane >> 2 & 1) * 5), ul = lane & 3;
         // A lane's places: its units' in a page's lines (rows 8 apart lie 1024 bytes apart, the upper
         // four units of a line opposite the lower), and those of their two halves in a tile.
         const uint32_t from = kv_tile_off<kRow>(pt, r8, 16 * ul), from4 = from ^ 64u;
-        const uint32_t to = (32 * lw + r8) * 128 + (((2 * ul) ^ (r8 & 7)) << 4);
+        const uint32_t to = (16 * lw + r8) * 128 + (((2 * ul) ^ (r8 & 7)) << 4);
         auto fetch = [&](const Job &jb, bool values, uint4 (&c)[kRegs]) {
+            const uint8_t *src = a.kv.base + (jb.rec[lw] + (values ? pt * kRow : 0) + jb.slot[lw] * (kRow < 128 ? kRow : 128));
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {                         // a group of 16 tokens
-                const uint8_t *src = a.kv.base + (jb.rec[2 * lw + y] + (values ? pt * kRow : 0) +
-                                                  jb.slot[2 * lw + y] * (kRow < 128 ? kRow : 128));
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int x = 0; x < kQuads; ++x)
-                        c[(2 * y + i) * kQuads + x] =
-                            __ldg(reinterpret_cast<const uint4 *>(src + (x ? from4 : from) + i * 8 * (kRow < 128 ? kRow : 128)));
-            }
+                for (int x = 0; x < kQuads; ++x)
+                    c[i * kQuads + x] =
+                        __ldg(reinterpret_cast<const uint4 *>(src + (x ? from4 : from) + i * 8 * (kRow < 128 ? kRow : 128)));
         };
         auto put = [&](const uint4 (&c)[kRegs], uint8_t *tile) {
             uint8_t *lo_at = tile + to, *hi_at = tile + (to ^ 16u);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int x = 0; x < kQuads; ++x) {
                     uint4 lo, hi;
@@ -573,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
         // An item's queries: a thread takes 16 columns of every kRpp-th row, kBatch rows' loads under way
         // at a time; the first batch is read while the last item's queries are still in use.
         auto queries = [&](const Job &jb) -> bool {
-            constexpr int kTpr = D / 16, kRpp = kLoadWarps * 32 / kTpr, kBatch = FMT == KDA_KV_I8 ? 4 : 8;
+            constexpr int kTpr = D / 16, kRpp = kLoadWarps * 32 / kTpr, kBatch = FMT == KDA_KV_I8 ? 2 : 4;
             const float sign = a.scale < 0.f ? -1.f : 1.f;
             const int nrows = jb.nrows, rows = nrows > kHalf ? kRows : kHalf, c = lt % kTpr;
             uint4 x[kBatch][2];
@@ -674,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                 // left to the rows that see it
                 ok = wait(VRAW + st, n >> 1 & 1);
                 if (!ok) break;
-                if (!(jb.flags & kWhole)) {
+                if (!(jb.flags & kWhole) && lt < kUnit) {
                     uint8_t *line = sm + L::v + st * L::tile + lt * 128;
                     const int32_t j = jb.j0 + lt;
                     const bool any = (jb.live >> (lt >> 4) & 1u) && j <= jb.pmax &&
@@ -714,29 +726,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
             const uint32_t sb = ptx::smem_u32(sm);
             const uint32_t tu = __shfl_sync(0xFFFFFFFFu, tm, 0);
             uint32_t n_item = 0, n_p[2] = {0, 0};
-            auto scores = [&](int half, int st) {
+            auto scores = [&](int half, int st) {                     // one lane
                 const uint64_t qd = ptx::sdesc_sw128(sb + L::q + half * L::half_q, 16, 1024);
                 const uint64_t kd = ptx::sdesc_sw128(sb + L::k + st * L::tile, 16, 1024);
-                if (elect()) {
 #pragma unroll
-                    for (int s = 0; s < D / 16; ++s) {
-                        const uint32_t off = ((s >> 2) * L::blk + (s & 3) * 32) >> 4;
-                        ptx::mma_bf16(tu + half * 128, qd + off, kd + off, idesc<FMT>(128, 128, 0), s > 0 ? 1u : 0u);
-                    }
-                    ptx::mma_commit(&bars[SFULL + half]);
+                for (int s = 0; s < D / 16; ++s) {
+                    const uint32_t off = ((s >> 2) * L::blk + (s & 3) * 32) >> 4;
+                    ptx::mma_bf16(tu + half * 128, qd + off, kd + off, idesc<FMT>(128, 128, 0), s > 0 ? 1u : 0u);
                 }
-                __syncwarp();
+                ptx::mma_commit(&bars[SFULL + half]);
             };
             auto outputs = [&](int half, int st) {
                 const uint64_t vd = ptx::sdesc_sw128(sb + L::v + st * L::tile, L::blk, 1024);
-                if (elect()) {
 #pragma unroll
-                    for (int s = 0; s < kUnit / 16; ++s)
-                        ptx::mma_bf16_ta(tu + 256 + half * 128, tu + half * 128 + s * 8, vd + (s * 2048 >> 4),
-                                         idesc<FMT>(128, D, 1), 1u);
-                    ptx::mma_commit(&bars[OFULL + half]);
-                }
-                __syncwarp();
+                for (int s = 0; s < kUnit / 16; ++s)   // probabilities: 32 columns in each half of the scores
+                    ptx::mma_bf16_ta(tu + 256 + half * 128, tu + half * 128 + (s >> 2) * 64 + (s & 3) * 8, vd + (s * 2048 >> 4),
+                                     idesc<FMT>(128, D, 1), 1u);
+                ptx::mma_commit(&bars[OFULL + half]);
             };
             auto commit = [&](int b) {
                 if (elect()) ptx::mma_commit(&bars[b]);
@@ -750,37 +756,41 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                 if (flags & kStop) break;
                 const int halves = job(n).nrows > kHalf ? 2 : 1, st = n & 1, nx = st ^ 1;
                 done(n);
-                // the scores of an item's first unit; those of the next come between the outputs
+                // the scores of an item's first unit; those of the next follow each half's outputs
                 if (flags & kBegin) {
                     ok = wait(QFULL, n_item & 1) && wait(KFULL + st, n >> 1 & 1);
                     if (!ok) break;
                     ptx::tc_fence_after();
-#pragma unroll 1
-                    for (int h = 0; h < halves; ++h) scores(h, st);
-                    commit(KEMPTY + st);
-                    if (flags & kEnd) commit(QEMPTY);
+                    if (elect()) {
+                        for (int h = 0; h < halves; ++h) scores(h, st);
+                        ptx::mma_commit(&bars[KEMPTY + st]);
+                        if (flags & kEnd) ptx::mma_commit(&bars[QEMPTY]);
+                    }
+                    __syncwarp();
                     ++n_item;
                 }
+                const bool more = !(flags & kEnd);
+                ok = wait(VFULL + st, n >> 1 & 1) && (!more || (wait(KFULL + nx, (n + 1) >> 1 & 1) && wait_job(n + 1)));
+                if (!ok) break;
+                // the item's last scores: its queries may go when they are done
+                const bool last = more && (job(n + 1).flags & kEnd);
 #pragma unroll 1
                 for (int h = 0; h < halves; ++h) {
-                    ok = wait(PFULL + h, n_p[h] & 1) && (h || wait(VFULL + st, n >> 1 & 1));
+                    ok = wait(PFULL + h, n_p[h] & 1);
                     if (!ok) break;
                     if (h) ++n_p[1];
                     else ++n_p[0];
                     ptx::tc_fence_after();
-                    outputs(h, st);
-                    if (h + 1 == halves) commit(VEMPTY + st);
-                    if (!(flags & kEnd)) {
-                        ok = h || wait(KFULL + nx, (n + 1) >> 1 & 1);
-                        if (!ok) break;
-                        ptx::tc_fence_after();
-                        scores(h, nx);
+                    if (elect()) {
+                        outputs(h, st);
+                        if (more) scores(h, nx);
                         if (h + 1 == halves) {
-                            commit(KEMPTY + nx);
-                            // the item's last scores are under way: its queries may go
-                            if (wait_job(n + 1) && (job(n + 1).flags & kEnd)) commit(QEMPTY);
+                            ptx::mma_commit(&bars[VEMPTY + st]);
+                            if (more) ptx::mma_commit(&bars[KEMPTY + nx]);
+                            if (last) ptx::mma_commit(&bars[QEMPTY]);
                         }
                     }
+                    __syncwarp();
                 }
             }
             commit(DRAIN);
