@@ -534,23 +534,45 @@ def kda_ckpt_restore_q8(pool: Pool, H: int, d: int, dtype: int, ckpt_pages, acti
 
 
 # ------------------------------------------------------------------------------ key/value cache
+# A decode step makes these calls once a layer and runs for microseconds on the GPU, so their host
+# side is kept short: addresses go as plain integers, the library and the current stream are looked
+# up without locks or wrapper objects.
+def _address(t):
+    """Device address of a contiguous CUDA tensor (None: NULL)."""
+    if t is None:
+        return None
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError("expected a contiguous CUDA tensor")
+    return t.data_ptr()
+
+
 def _rows(t, H: int, d: int):
     """(device address, token stride) of a [T, H, d] CUDA tensor whose token rows are whole: the
     parts of a fused projection qualify."""
     T, h, w = t.shape
-    if not t.is_cuda or h != H or w != d or (T and (t.stride(2) != 1 or (h > 1 and t.stride(1) != d))):
+    row, head, elem = t.stride()
+    if not t.is_cuda or h != H or w != d or (T and (elem != 1 or (h > 1 and head != d))):
         raise ValueError("expected a [T, H, d] CUDA tensor with contiguous heads")
-    return t.data_ptr(), (t.stride(0) if T > 1 else H * d)
+    return t.data_ptr(), (row if T > 1 else H * d)
 
 
-def _table(cu, lens, page_table):
-    """(nseq, max_pages) of a batch's device int32 arrays."""
+def _batch(cu, lens, page_table):
+    """(nseq, max_pages, addresses) of a batch's device int32 arrays."""
     import torch
     nseq, max_pages = page_table.shape
-    for t, n in ((cu, nseq + 1), (lens, nseq), (page_table, nseq * max_pages)):
-        if t.dtype != torch.int32 or t.numel() != n:
-            raise ValueError("expected int32 [nseq + 1], [nseq] and [nseq, max_pages] CUDA tensors")
-    return nseq, max_pages
+    i32 = torch.int32
+    if (cu.dtype != i32 or lens.dtype != i32 or page_table.dtype != i32 or cu.numel() != nseq + 1
+            or lens.numel() != nseq):
+        raise ValueError("expected int32 [nseq + 1], [nseq] and [nseq, max_pages] CUDA tensors")
+    return nseq, max_pages, _address(cu), _address(lens), _address(page_table)
+
+
+def _raw_stream(t, stream) -> int:
+    """The given stream, or the current one of t's device, as an integer."""
+    if stream is not None:
+        return stream.cuda_stream
+    import torch
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def kda_kv_page_bytes(Hkv: int, d: int, fmt: int, page_tokens: int) -> int:
@@ -563,26 +585,31 @@ def kda_kv_append(pool: Pool, fmt: int, page_tokens: int, cu_q, kv_len, page_tab
     apart; cu_q, kv_len, page_table: int32 CUDA [nseq + 1], [nseq], [nseq, max_pages]; cos_sin:
     fp32 CUDA [max_pos, rot_dim] or None; q_out: [T, Hq, d] contiguous."""
     T, Hkv, d = k.shape
-    if (q is None) != (q_out is None):
-        raise ValueError("q and q_out go together")
-    nseq, max_pages = _table(cu_q, kv_len, page_table)
+    dtype = k.dtype
+    nseq, max_pages, cu, lens, table = _batch(cu_q, kv_len, page_table)
     kp, ks = _rows(k, Hkv, d)
     vp, vs = _rows(v, Hkv, d)
+    if v.shape[0] != T or v.dtype != dtype:
+        raise ValueError("k and v differ in tokens or type")
     Hq, qp, qs = 0, None, 0
-    if q is not None:
+    if q is not None and q_out is not None:
         Hq = q.shape[1]
         qp, qs = _rows(q, Hq, d)
-        if q.shape[0] != T or q_out.shape != q.shape or not q.dtype == q_out.dtype == k.dtype:
+        if q.shape[0] != T or q_out.shape != q.shape or q.dtype != dtype or q_out.dtype != dtype:
             raise ValueError("q, q_out and k differ in tokens or type")
-    if v.shape[0] != T or v.dtype != k.dtype:
-        raise ValueError("k and v differ in tokens or type")
-    pos, rot = (0, 0) if cos_sin is None else cos_sin.shape
-    if cos_sin is not None and cos_sin.element_size() != 4:
-        raise ValueError("cos_sin must be float32")
-    rc = lib().kda_kv_append(pool.handle, Hq, Hkv, d, dtype_of(k), fmt, page_tokens, nseq, T, max_q, _dev(cu_q),
-                             _dev(kv_len), _dev(page_table), max_pages, qp, qs, kp, ks, vp, vs, _dev(cos_sin), pos,
-                             rot, int(interleaved), _dev(q_out), _dev(pool.base), _dev(status), _stream(stream))
-    _check(rc, "kda_kv_append")
+    elif q is not None or q_out is not None:
+        raise ValueError("q and q_out go together")
+    pos, rot = 0, 0
+    if cos_sin is not None:
+        pos, rot = cos_sin.shape
+        if cos_sin.element_size() != 4:
+            raise ValueError("cos_sin must be float32")
+    rc = (_lib or lib()).kda_kv_append(
+        pool.handle, Hq, Hkv, d, dtype_of(k), fmt, page_tokens, nseq, T, max_q, cu, lens, table, max_pages, qp, qs, kp,
+        ks, vp, vs, _address(cos_sin), pos, rot, bool(interleaved), _address(q_out), _address(pool.base),
+        _address(status), _raw_stream(k, stream))
+    if rc < 0:
+        raise KdaError(rc, "kda_kv_append")
 
 
 def kda_kv_gather(pool: Pool, fmt: int, page_tokens: int, cu_out, begin, page_table, k_out, v_out, status,
@@ -592,11 +619,12 @@ def kda_kv_gather(pool: Pool, fmt: int, page_tokens: int, cu_out, begin, page_ta
     T, Hkv, d = k_out.shape
     if v_out.shape != k_out.shape or v_out.dtype != k_out.dtype:
         raise ValueError("k_out and v_out differ")
-    nseq, max_pages = _table(cu_out, begin, page_table)
-    rc = lib().kda_kv_gather(pool.handle, Hkv, d, dtype_of(k_out), fmt, page_tokens, nseq, T, _dev(cu_out),
-                             _dev(begin), _dev(page_table), max_pages, _dev(k_out), _dev(v_out), _dev(pool.base),
-                             _dev(status), _stream(stream))
-    _check(rc, "kda_kv_gather")
+    nseq, max_pages, cu, lens, table = _batch(cu_out, begin, page_table)
+    rc = (_lib or lib()).kda_kv_gather(
+        pool.handle, Hkv, d, dtype_of(k_out), fmt, page_tokens, nseq, T, cu, lens, table, max_pages, _address(k_out),
+        _address(v_out), _address(pool.base), _address(status), _raw_stream(k_out, stream))
+    if rc < 0:
+        raise KdaError(rc, "kda_kv_gather")
 
 
 def kda_attn_workspace_bytes(Hq: int, Hkv: int, d: int, dtype: int, nseq: int, T_tot: int, max_q: int) -> int:
@@ -621,13 +649,14 @@ def kda_attn_paged(pool: Pool, Hkv: int, fmt: int, page_tokens: int, cu_q, kv_le
         raise ValueError("q and o differ in shape or type")
     if lse is not None and (lse.element_size() != 4 or lse.numel() != T * Hq):
         raise ValueError("lse must be float32 [T, Hq]")
-    nseq, max_pages = _table(cu_q, kv_len, page_table)
+    nseq, max_pages, cu, lens, table = _batch(cu_q, kv_len, page_table)
     qp, qs = _rows(q, Hq, d)
-    rc = lib().kda_attn_paged(pool.handle, Hq, Hkv, d, dtype_of(q), fmt, page_tokens, nseq, T, max_q, _dev(cu_q),
-                              _dev(kv_len), _dev(page_table), max_pages, qp, qs, d ** -0.5 if scale is None else scale,
-                              window, sinks, _dev(o), _dev(lse), _dev(pool.base), _dev(workspace),
-                              workspace.numel() * workspace.element_size(), _dev(status), _stream(stream))
-    _check(rc, "kda_attn_paged")
+    rc = (_lib or lib()).kda_attn_paged(
+        pool.handle, Hq, Hkv, d, dtype_of(q), fmt, page_tokens, nseq, T, max_q, cu, lens, table, max_pages, qp, qs,
+        d ** -0.5 if scale is None else scale, window, sinks, _address(o), _address(lse), _address(pool.base),
+        _address(workspace), workspace.numel() * workspace.element_size(), _address(status), _raw_stream(q, stream))
+    if rc < 0:
+        raise KdaError(rc, "kda_attn_paged")
 
 
 # ------------------------------------------------------------------------------ status

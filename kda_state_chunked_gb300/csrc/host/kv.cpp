@@ -9,6 +9,7 @@
 
 namespace {
 
+constexpr int64_t kWholeTokens = 1024;     // visible tokens up to which an item is not split
 constexpr int64_t kMaxTokens = 1 << 30;   // of a sequence: the kernels' positions and their differences fit int32
 
 int64_t elem_size(int32_t dtype) { return dtype == KDA_BF16 ? 2 : 4; }
@@ -162,8 +163,16 @@ int kda_attn_paged(const kda_pool *pool, int32_t Hq, int32_t Hkv, int32_t d, int
     const AttnWs w = attn_ws(d, rows);
     // the most units that the call can have bounds the CTAs worth launching
     const int64_t tiles = T_tot * a.G / rows + nseq;
-    const int64_t units = ((int64_t)max_pages * page_tokens + kda::kAttnMinUnit - 1) / kda::kAttnMinUnit;
-    a.ctas = (int32_t)std::min<int64_t>(attn_ctas(rows), std::max<int64_t>(1, tiles * Hkv * std::max<int64_t>(1, units)));
+    int64_t tokens = (int64_t)max_pages * page_tokens;   // that a row tile can see: window, sinks, a unit cut at both ends
+    if (a.window) tokens = std::min<int64_t>(tokens, (int64_t)a.window + a.sinks + max_q + 3 * kda::kAttnMinUnit);
+    const int64_t units = std::max<int64_t>(1, (tokens + kda::kAttnMinUnit - 1) / kda::kAttnMinUnit);
+    a.ctas = (int32_t)std::min<int64_t>(attn_ctas(rows), std::max<int64_t>(1, tiles * Hkv * units));
+    // Few, short items: a CTA each, which then takes all of its loads ahead; splitting them would cost
+    // another launch to join the parts.
+    a.whole = rows == kda::kAttnDecodeRows && (int64_t)max_q * a.G <= rows && (int64_t)nseq * Hkv <= kda::kAttnSms &&
+              tokens <= kWholeTokens;
+    if (a.whole) a.ctas = nseq * Hkv;
+    a.deep = rows == kda::kAttnDecodeRows && a.ctas <= kda::kAttnSms;
     a.split = static_cast<kda::AttnSplit *>(workspace);
     a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + w.o_part);
     return status_of(rows == kda::kAttnDecodeRows ? kda::launch_attn_decode(a, static_cast<cudaStream_t>(stream))

@@ -40,19 +40,20 @@ struct Shape {
     static constexpr int group = row * 16;            // K or V bytes of 16 tokens
     static constexpr int tile = groups * group;
     static constexpr int stage = 2 * tile + 128;      // keys, values, 16 bytes of scales a group
-    static constexpr int stages = D == 128 ? 2 : 4;
+    static constexpr int stages = D == 128 ? 2 : 4;        // of a warp's ring, two CTAs an SM
+    static constexpr int deep_stages = D == 128 ? 5 : 8;   // one CTA an SM
 };
 
 template <int FMT, int D, int NT>
 struct Smem {
-    static constexpr int ring = kWarps * Shape<FMT, D>::stages * Shape<FMT, D>::stage;
-    static constexpr int o_acc = ring;                                   // [kWarps][16][D] fp32
+    // behind the rings
+    static constexpr int o_acc = 0;                                      // [kWarps][16][D] fp32
     static constexpr int o_ml = o_acc + kWarps * 16 * D * 4;             // [2][kWarps][16][2] fp32
     static constexpr int o_q = o_ml + 2 * kWarps * 16 * 8;               // fragments of split queries
     static constexpr int o_bar = o_q + (NT > 1 ? NT * (D / 16) * 512 : 0);
-    static constexpr int o_live = o_bar + kWarps * Shape<FMT, D>::stages * 8;
-    static constexpr int o_misc = o_live + kWarps * Shape<FMT, D>::stages * 4;
-    static constexpr int total = o_misc + 128;
+    static constexpr int o_live = o_bar + kWarps * Shape<FMT, D>::deep_stages * 8;
+    static constexpr int o_misc = o_live + kWarps * Shape<FMT, D>::deep_stages * 4;
+    static constexpr int total(int stages) { return kWarps * stages * Shape<FMT, D>::stage + o_misc + 128; }
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
@@ -133,11 +134,13 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_decode_kernel(const __gri
     constexpr int kNt = D / 8;    // 8-wide output tiles
     constexpr int kGr = S::groups;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t *sm = ptx::smem_align1024(smem_raw);
+    uint8_t *rings = ptx::smem_align1024(smem_raw);
+    const int stages = a.deep ? S::deep_stages : S::stages;
+    uint8_t *sm = rings + kWarps * stages * S::stage;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane >> 2, t = lane & 3;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + M::o_bar) + warp * S::stages;
-    volatile uint32_t *live = reinterpret_cast<uint32_t *>(sm + M::o_live) + warp * S::stages;
-    uint8_t *ring = sm + warp * S::stages * S::stage;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + M::o_bar) + warp * stages;
+    volatile uint32_t *live = reinterpret_cast<uint32_t *>(sm + M::o_live) + warp * stages;
+    uint8_t *ring = rings + warp * stages * S::stage;
     float *ml = reinterpret_cast<float *>(sm + M::o_ml);   // of this item; the last one's may still be read
     int ml_next = kWarps * 32;
     float *acc = reinterpret_cast<float *>(sm + M::o_acc);
@@ -146,7 +149,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_decode_kernel(const __gri
     int64_t *share = reinterpret_cast<int64_t *>(sm + M::o_misc + 16);   // warps' sums, then the start
 
     if (lane == 0)
-        for (int i = 0; i < S::stages; ++i) ptx::mbar_init(&bars[i], 1);
+        for (int i = 0; i < stages; ++i) ptx::mbar_init(&bars[i], 1);
     if (tid == 0) *err = 0;
     ptx::fence_mbar_init();
     ptx::grid_dep_wait();
@@ -178,20 +181,28 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_decode_kernel(const __gri
         before = base + x - v;
         return all;
     };
-    int64_t mine0 = 0, mine = 0, before, W;
-    for (int s = tid; s < a.nseq; s += kWarps * 32) {
-        const int64_t w = seq_units(s);
-        if (s == tid) mine0 = w;
-        mine += w;
-    }
-    W = block_sum(mine, before);
-    if (tid == 0) a.split[blockIdx.x].last_cta = -1;
-    const int32_t C = (int32_t)min((int64_t)a.ctas, W);   // no CTA that takes part is without a unit
-    if ((int32_t)blockIdx.x >= C) return;
-    const int64_t begin = (int64_t)blockIdx.x * W / C, end = (int64_t)(blockIdx.x + 1) * W / C;
-    int32_t s0 = 0;
-    int64_t left0 = 0;   // units before `begin` in sequence s0
-    {
+    int64_t W = 0, begin = 0, end;
+    int32_t C = 0, h0, u0 = 0;
+    Tile t0;
+    if (a.whole) {
+        // CTA i is item i: key/value head i % Hkv of sequence i / Hkv (one row tile a sequence)
+        const KvSeq q = seq(blockIdx.x / Hkv);
+        if (q.n == 0) return;
+        h0 = blockIdx.x % Hkv;
+        t0 = make_tile<kAttnDecodeRows, S::unit>(a, blockIdx.x / Hkv, q, 0);
+        end = t0.units;
+    } else {
+        int64_t mine0 = 0, mine = 0, before;
+        for (int s = tid; s < a.nseq; s += kWarps * 32) {
+            const int64_t w = seq_units(s);
+            if (s == tid) mine0 = w;
+            mine += w;
+        }
+        W = block_sum(mine, before);
+        if (tid == 0) a.split[blockIdx.x].last_cta = -1;
+        C = (int32_t)min((int64_t)a.ctas, W);   // no CTA that takes part is without a unit
+        if ((int32_t)blockIdx.x >= C) return;
+        begin = (int64_t)blockIdx.x * W / C, end = (int64_t)(blockIdx.x + 1) * W / C;
         int64_t *found = share + kWarps;
         int64_t base = 0;
         for (int s = 0; s < a.nseq; s += kWarps * 32) {
@@ -205,15 +216,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_decode_kernel(const __gri
             if (begin < base) break;
         }
         __syncthreads();
-        s0 = (int32_t)found[0];
-        left0 = found[1];
-    }
-    Tile t0;
-    int32_t h0, u0;
-    {
+        const int32_t s0 = (int32_t)found[0];
+        int64_t left0 = found[1];   // units before `begin` in sequence s0
         const KvSeq q = seq(s0);
-        int rt = 0;
-        for (;; ++rt) {
+        for (int rt = 0;; ++rt) {
             t0 = make_tile<kAttnDecodeRows, S::unit>(a, s0, q, rt);
             if (left0 < (int64_t)t0.units * Hkv) break;
             left0 -= (int64_t)t0.units * Hkv;
@@ -283,7 +289,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_decode_kernel(const __gri
         }
         aim(cur);
     };
-    for (int i = 0; i < S::stages; ++i) load_next(i);
+    for (int i = 0; i < stages; ++i) load_next(i);
 
     // ---- items
     Tile tile = t0;
@@ -576,7 +582,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_decode_kernel(const __gri
             }
             __syncwarp();
             load_next(stage);
-            if (++stage == S::stages) stage = 0, phase ^= 1;
+            if (++stage == stages) stage = 0, phase ^= 1;
         }
 
         // ---- the warps' results together
@@ -664,13 +670,15 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_decode_kernel(const __gri
 template <int FMT, int D, int NT>
 cudaError_t run(const AttnArgs &a, cudaStream_t st) {
     using M = Smem<FMT, D, NT>;
-    static_assert(M::total + 1024 <= 227 * 1024, "shared memory");
+    static_assert(M::total(Shape<FMT, D>::deep_stages) + 1024 <= 227 * 1024, "shared memory");
+    static_assert(M::total(Shape<FMT, D>::stages) <= 113 * 1024, "two CTAs an SM");
+    const int smem = M::total(a.deep ? Shape<FMT, D>::deep_stages : Shape<FMT, D>::stages) + 1024;
     auto kern = attn_decode_kernel<FMT, D, NT>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, M::total + 1024);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kern<<<a.ctas, kWarps * 32, M::total + 1024, st>>>(a);
+    kern<<<a.ctas, kWarps * 32, smem, st>>>(a);
     e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || a.whole) return e;
     // the join is placed while the last CTAs run and waits for them in hardware
     cudaLaunchAttribute at{};
     at.id = cudaLaunchAttributeProgrammaticStreamSerialization;

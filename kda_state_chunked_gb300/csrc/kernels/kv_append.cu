@@ -21,8 +21,7 @@
 namespace kda {
 namespace {
 
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float *x) {
-    const uint4 u = *reinterpret_cast<const uint4 *>(p);
+__device__ __forceinline__ void unpack8(const uint4 &u, float *x) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -30,6 +29,7 @@ __device__ __forceinline__ void load8(const __nv_bfloat16 *p, float *x) {
         x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
     }
 }
+__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float *x) { unpack8(*reinterpret_cast<const uint4 *>(p), x); }
 __device__ __forceinline__ void load8(const float *p, float *x) {
     const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
     x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
@@ -96,6 +96,8 @@ __device__ __forceinline__ uint2 codes8(const float *x, float s) {
     return make_uint2(w[0], w[1]);
 }
 
+constexpr int kMaxToks = 128;   // tokens of a CTA that rotates queries
+
 // NT threads; ROWS: new rows of a block that one thread may hold.
 template <int FMT, int D, class TIN, int NT, int ROWS>
 __global__ void __launch_bounds__(NT) kv_append_kernel(KvAppendArgs a, int32_t q_ctas, int32_t q_toks, int64_t items) {
@@ -107,8 +109,26 @@ __global__ void __launch_bounds__(NT) kv_append_kernel(KvAppendArgs a, int32_t q
     const int rot = a.rot_dim;
 
     if ((int)blockIdx.x < q_ctas) {
+        // a token's place in its sequence, by one warp a token
+        __shared__ int64_t place_of[kMaxToks];
         const int64_t t_lo = (int64_t)blockIdx.x * q_toks;
         const int per_tok = a.Hq * kTpr;
+        if (rot > 0) {
+            for (int i = tid / 32; i < q_toks; i += NT / 32) {
+                const int64_t tok = t_lo + i;
+                if (tok >= a.T_tot) break;
+                const int s = kv_find(a.nseq, tok, [&](int m) { return (int64_t)__ldg(a.cu_q + m); });
+                const KvSeq q = kv_seq(a.cu_q, a.kv_len, s, a.T_tot, a.max_q, a.kv);
+                int64_t pos = (int64_t)q.len - q.n + (tok - q.tok0);
+                if (tok < q.tok0 || tok >= (int64_t)q.tok0 + q.n) pos = -1;
+                else if (pos < 0 || pos >= a.max_pos) {
+                    flag_status(a.kv.status, KDA_DEV_BAD_META);
+                    pos = -1;
+                }
+                if (tid % 32 == 0) place_of[i] = pos;
+            }
+            __syncthreads();
+        }
         for (int i = tid; i < q_toks * per_tok; i += NT) {
             const int64_t tok = t_lo + i / per_tok;
             if (tok >= a.T_tot) break;
@@ -119,14 +139,8 @@ __global__ void __launch_bounds__(NT) kv_append_kernel(KvAppendArgs a, int32_t q
             load8(src + p.a, x);
             load8(src + p.b, x + 8);
             if (p.turned) {
-                const int s = kv_find(a.nseq, tok, [&](int m) { return (int64_t)__ldg(a.cu_q + m); });
-                const KvSeq q = kv_seq(a.cu_q, a.kv_len, s, a.T_tot, a.max_q, a.kv);
-                const int64_t pos = (int64_t)q.len - q.n + (tok - q.tok0);
-                if (tok < q.tok0 || tok >= (int64_t)q.tok0 + q.n) continue;
-                if (pos < 0 || pos >= a.max_pos) {
-                    flag_status(a.kv.status, KDA_DEV_BAD_META);
-                    continue;
-                }
+                const int64_t pos = place_of[i / per_tok];
+                if (pos < 0) continue;
                 rotate(x, a.cos_sin + pos * rot, c, rot, il);
             }
             TIN *dst = static_cast<TIN *>(a.q_out) + (tok * a.Hq + h) * D;
@@ -165,9 +179,7 @@ __global__ void __launch_bounds__(NT) kv_append_kernel(KvAppendArgs a, int32_t q
         if (tid == 0) flag_status(a.kv.status, KDA_DEV_BAD_META);
         return;
     }
-    uint8_t *rec = kv_record(a.kv, __ldg(a.kv.table + (int64_t)s * a.kv.max_pages + block), head);
-    if (!rec) return;
-    uint8_t *tile = rec + (is_v ? pt * kRow : 0);
+    const int32_t page = __ldg(a.kv.table + (int64_t)s * a.kv.max_pages + block);   // used when the rows are under way
     const int lo = max(old - block * pt, 0), hi = min(q.len - block * pt, pt);   // slots of the new rows
     const int64_t tok_of_slot0 = (int64_t)q.tok0 + (int64_t)block * pt - old;
 
@@ -185,6 +197,12 @@ __global__ void __launch_bounds__(NT) kv_append_kernel(KvAppendArgs a, int32_t q
             load8(row + p.b, x[i] + 8);
         }
     }
+    uint8_t *rec = kv_record(a.kv, page, head);
+    if (!rec) return;
+    uint8_t *tile = rec + (is_v ? pt * kRow : 0);
+    float *scale_at = reinterpret_cast<float *>(rec + 2 * pt * kRow) + (is_v ? 1 : 0);
+    uint32_t s_old = 0;
+    if (FMT == KDA_KV_I8 && lo > 0) s_old = __float_as_uint(*scale_at) & 0x7FFFFFFFu;
     if (p.turned) {
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) {
@@ -213,9 +231,7 @@ __global__ void __launch_bounds__(NT) kv_append_kernel(KvAppendArgs a, int32_t q
         top = __reduce_max_sync(0xFFFFFFFFu, top);
         __shared__ uint32_t tops[NT / 32];
         if (tid % 32 == 0) tops[tid / 32] = top;
-        float *scale_at = reinterpret_cast<float *>(rec + 2 * pt * kRow) + (is_v ? 1 : 0);
-        const uint32_t s_old = lo > 0 ? __float_as_uint(*scale_at) & 0x7FFFFFFFu : 0u;
-        __syncthreads();
+        __syncthreads();   // behind it every thread has read the old scale
 #pragma unroll
         for (int i = 0; i < NT / 32; ++i) top = max(top, tops[i]);
         const uint32_t s_bits = max(__float_as_uint(__fdiv_rn(__uint_as_float(top), 127.f)) & 0x7FFFFFFFu, s_old);
@@ -244,62 +260,89 @@ __global__ void __launch_bounds__(NT) kv_append_kernel(KvAppendArgs a, int32_t q
     }
 }
 
-// 16 values of a cache row as fp32: unit c of 16 elements.
-template <int FMT, int D>
-__device__ __forceinline__ void read16(const uint8_t *tile, int pt, int slot, int c, float sc, float (&x)[16]) {
-    constexpr int kRow = kKvRow<FMT, D>;
-    if constexpr (FMT == KDA_KV_I8) {
-        const uint4 u = *reinterpret_cast<const uint4 *>(tile + kv_tile_off<kRow>(pt, slot, 16 * c));
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int j = 0; j < 16; ++j) x[j] = __fmul_rn((float)(int8_t)(w[j >> 2] >> (8 * (j & 3))), sc);
-    } else {
-        load8(reinterpret_cast<const __nv_bfloat16 *>(tile + kv_tile_off<kRow>(pt, slot, 32 * c)), x);
-        load8(reinterpret_cast<const __nv_bfloat16 *>(tile + kv_tile_off<kRow>(pt, slot, 32 * c + 16)), x + 8);
-    }
-}
-
-// Cached ranges as values: one thread takes 16 elements of K and of V of one (row, head), so that a
-// warp writes whole lines of both outputs.
+// Cached ranges as values.  A thread takes 16 elements of K and of V of one head, in kGatherRows rows
+// whose loads are under way together; neighbours take the next elements and heads, so a warp writes
+// whole lines of both outputs.
+constexpr int kGatherRows = 4;
 template <int FMT, int D, class TOUT>
 __global__ void __launch_bounds__(256) kv_gather_kernel(KvGatherArgs a) {
     constexpr int kTpr = D / 16, kRow = kKvRow<FMT, D>;
+    const int per_row = a.kv.Hkv * kTpr;
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int c = (int)(i % kTpr);
-    const int64_t rh = i / kTpr, row = rh / a.kv.Hkv;
-    const int head = (int)(rh % a.kv.Hkv);
-    if (row >= a.T_out) return;
-    const int pt = a.kv.page_tokens;
-    const int s = kv_find(a.nseq, row, [&](int m) { return (int64_t)__ldg(a.cu_out + m); });
-    const int64_t at = __ldg(a.cu_out + s), end = __ldg(a.cu_out + s + 1), first = __ldg(a.begin + s);
-    if (row < at || row >= end) return;                 // rows that no sequence owns stay as they are
-    const int64_t tok = first + (row - at);
-    if (first < 0 || tok >= (int64_t)a.kv.max_pages * pt) {
-        flag_status(a.kv.status, KDA_DEV_BAD_META);
-        return;
+    const int64_t row0 = i / per_row * kGatherRows;
+    const int c = (int)(i % kTpr), head = (int)(i % per_row) / kTpr, pt = a.kv.page_tokens;
+    // the warp's first row's sequence; a thread steps on from there
+    int s = kv_find(a.nseq, __shfl_sync(0xFFFFFFFFu, row0, 0), [&](int m) { return (int64_t)__ldg(a.cu_out + m); });
+    int32_t page[kGatherRows], slot[kGatherRows], wrong = 0;
+    bool mine[kGatherRows];
+#pragma unroll
+    for (int r = 0; r < kGatherRows; ++r) {
+        const int64_t row = row0 + r;
+        mine[r] = row < a.T_out;
+        page[r] = slot[r] = 0;
+        if (!mine[r]) continue;
+        while (s + 1 < a.nseq && __ldg(a.cu_out + s + 1) <= row) ++s;
+        const int64_t at = __ldg(a.cu_out + s), end = __ldg(a.cu_out + s + 1), first = __ldg(a.begin + s);
+        mine[r] = row >= at && row < end;               // rows that no sequence owns stay as they are
+        const int64_t tok = first + (row - at);
+        if (mine[r] && (first < 0 || tok >= (int64_t)a.kv.max_pages * pt)) {
+            wrong |= KDA_DEV_BAD_META;
+            mine[r] = false;
+        }
+        if (!mine[r]) continue;
+        const int block = (int)tok / pt;
+        slot[r] = (int)tok - block * pt;
+        page[r] = __ldg(a.kv.table + (int64_t)s * a.kv.max_pages + block);
     }
-    const int block = (int)(tok / pt), slot = (int)(tok % pt);
-    const uint8_t *rec = kv_record(a.kv, __ldg(a.kv.table + (int64_t)s * a.kv.max_pages + block), head);
-    if (!rec) return;
-    float ks = 1.f, vs = 1.f;
-    if constexpr (FMT == KDA_KV_I8) {
-        const float2 sc = *reinterpret_cast<const float2 *>(rec + 2 * pt * kRow);
-        ks = sc.x, vs = sc.y;
+    const uint8_t *rec[kGatherRows];
+#pragma unroll
+    for (int r = 0; r < kGatherRows; ++r) {
+        const bool there = (uint32_t)page[r] < (uint32_t)a.kv.num_pages;
+        if (mine[r] && !there) wrong |= KDA_DEV_BAD_PAGE;
+        rec[r] = mine[r] && there ? a.kv.base + (int64_t)page[r] * a.kv.page_bytes + (int64_t)head * a.kv.rec_bytes : nullptr;
     }
-    float x[16], y[16];
-    read16<FMT, D>(rec, pt, slot, c, ks, x);
-    read16<FMT, D>(rec + pt * kRow, pt, slot, c, vs, y);
-    TOUT *ko = static_cast<TOUT *>(a.k_out) + rh * D + 16 * c, *vo = static_cast<TOUT *>(a.v_out) + rh * D + 16 * c;
-    store8(ko, x);
-    store8(ko + 8, x + 8);
-    store8(vo, y);
-    store8(vo + 8, y + 8);
+    if (wrong) flag_status(a.kv.status, wrong);
+    constexpr int kUnits = FMT == KDA_KV_I8 ? 1 : 2;    // 16-byte units of 16 elements
+    uint4 u[kGatherRows][2][kUnits];
+    float2 sc[kGatherRows];
+#pragma unroll
+    for (int r = 0; r < kGatherRows; ++r) {
+        if (!rec[r]) continue;
+#pragma unroll
+        for (int v = 0; v < 2; ++v)
+#pragma unroll
+            for (int y = 0; y < kUnits; ++y)
+                u[r][v][y] = *reinterpret_cast<const uint4 *>(rec[r] + v * pt * kRow +
+                                                              kv_tile_off<kRow>(pt, slot[r], 16 * (kUnits * c + y)));
+        if (FMT == KDA_KV_I8) sc[r] = *reinterpret_cast<const float2 *>(rec[r] + 2 * pt * kRow);
+    }
+#pragma unroll
+    for (int r = 0; r < kGatherRows; ++r) {
+        if (!rec[r]) continue;
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+            TOUT *out = static_cast<TOUT *>(v ? a.v_out : a.k_out) + ((row0 + r) * a.kv.Hkv + head) * D + 16 * c;
+            float x[16];
+            if constexpr (FMT == KDA_KV_I8) {
+                const uint4 z = u[r][v][0];
+                const uint32_t w[4] = {z.x, z.y, z.z, z.w};
+                const float f = v ? sc[r].y : sc[r].x;
+#pragma unroll
+                for (int j = 0; j < 16; ++j) x[j] = __fmul_rn((float)(int8_t)(w[j >> 2] >> (8 * (j & 3))), f);
+            } else {
+#pragma unroll
+                for (int y = 0; y < kUnits; ++y) unpack8(u[r][v][y], x + 8 * y);
+            }
+            store8(out, x);
+            store8(out + 8, x + 8);
+        }
+    }
 }
 
 template <int FMT, int D, class TIN, int NT, int ROWS>
 cudaError_t append(const KvAppendArgs &a, cudaStream_t st) {
     // about four pairs of eights a thread for the queries' CTAs
-    const int32_t q_toks = a.q ? max(1, 4 * NT / (a.Hq * (D / 16))) : 1;
+    const int32_t q_toks = a.q ? min(kMaxToks, max(1, 4 * NT / (a.Hq * (D / 16)))) : 1;
     const int64_t q_ctas = a.q ? (a.T_tot + q_toks - 1) / q_toks : 0;
     const int64_t items = a.max_q == 1 ? a.T_tot : a.T_tot / a.kv.page_tokens + 2 * (int64_t)a.nseq;
     const int64_t grid = q_ctas + 2 * items * a.kv.Hkv;
@@ -318,7 +361,7 @@ cudaError_t append_sized(const KvAppendArgs &a, cudaStream_t st) {
 
 template <int FMT, int D>
 cudaError_t gather(const KvGatherArgs &a, cudaStream_t st) {
-    const int64_t n = a.T_out * a.kv.Hkv * (D / 16), grid = (n + 255) / 256;
+    const int64_t n = (a.T_out + kGatherRows - 1) / kGatherRows * a.kv.Hkv * (D / 16), grid = (n + 255) / 256;
     if (grid > INT32_MAX) return cudaErrorInvalidValue;
     if (a.dtype == KDA_F32) kv_gather_kernel<FMT, D, float><<<(unsigned)grid, 256, 0, st>>>(a);
     else kv_gather_kernel<FMT, D, __nv_bfloat16><<<(unsigned)grid, 256, 0, st>>>(a);

@@ -47,13 +47,19 @@ __device__ __forceinline__ KvSeq kv_seq(const int32_t *cu, const int32_t *kv_len
 }
 
 // The last s in [0, nseq) with start(s) <= x, for a start() that does not fall; 0 if there is none.
+// The whole warp calls it with one x: 32 places are looked at a time, so that 1,024 sequences take
+// two reads one behind the other and not ten.
 template <class F>
 __device__ __forceinline__ int32_t kv_find(int32_t nseq, int64_t x, F start) {
-    int32_t lo = 0, hi = nseq;
-    while (hi - lo > 1) {
-        const int32_t mid = (lo + hi) >> 1;
-        if (start(mid) <= x) lo = mid;
-        else hi = mid;
+    int32_t lo = 0, n = nseq;   // start(lo) <= x, or lo = 0; the answer is in [lo, lo + n)
+    const int lane = threadIdx.x % 32;
+    while (n > 1) {
+        const int32_t step = (n + 31) / 32, at = lo + lane * step;
+        const bool below = at < lo + n && (at == lo || start(at) <= x);
+        const int32_t k = 31 - __clz(__ballot_sync(0xFFFFFFFFu, below));
+        const int32_t end = lo + n;
+        lo += k * step;
+        n = min(step, end - lo);
     }
     return lo;
 }
