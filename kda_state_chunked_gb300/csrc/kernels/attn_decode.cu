@@ -56,32 +56,40 @@ struct Smem {
     static constexpr int total(int stages) { return kWarps * stages * Shape<FMT, D>::stage + o_misc + 128; }
 };
 
+// Fragment loads and products are plain functions of their operands to the compiler, which may so
+// place them as their latencies want.  What keeps the loads between a stage's arrival and its release
+// is the address (pinned behind the wait) and the accumulators (pinned before the release).
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
+    asm("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+        : "r"(addr));
 }
 __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
+    asm("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+        : "r"(addr));
+}
+template <int N>
+__device__ __forceinline__ void pin(float (&o)[N][4]) {
+#pragma unroll
+    for (int j = 0; j < N; j += 2)
+        asm volatile("" : "+f"(o[j][0]), "+f"(o[j][1]), "+f"(o[j][2]), "+f"(o[j][3]), "+f"(o[j + 1][0]), "+f"(o[j + 1][1]),
+                     "+f"(o[j + 1][2]), "+f"(o[j + 1][3])::"memory");
 }
 
 // D (16x8) += A (16x16) B (16x8), fp32 sums.
 template <int FMT>
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     if constexpr (FMT == KDA_KV_I8)
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-                     "{%0,%1,%2,%3};"
-                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+            "{%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
     else
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-                     "{%0,%1,%2,%3};"
-                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+            "{%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 // Two biased bytes (selected by SEL, under the exponent byte 0x64) as fp16: 1024 + b - 1152 = code.
@@ -380,7 +388,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_decode_kernel(const __gri
             if (there) {
                 const int32_t j0 = unit_token<S::unit>(tile, u) + warp * S::step;
                 const uint8_t *buf = ring + stage * S::stage;
-                const uint32_t kb = ptx::smem_u32(buf), vb = kb + S::tile;
+                uint32_t kb = ptx::smem_u32(buf);
+                asm volatile("" : "+r"(kb)::"memory");
+                const uint32_t vb = kb + S::tile;
                 float sc[kGr][2], vs[kGr];   // a group's score factors (by row half) and value scale
 #pragma unroll
                 for (int y = 0; y < kGr; ++y) {
@@ -580,6 +590,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_decode_kernel(const __gri
                     }
                 }
             }
+            pin(o);
             __syncwarp();
             load_next(stage);
             if (++stage == stages) stage = 0, phase ^= 1;
