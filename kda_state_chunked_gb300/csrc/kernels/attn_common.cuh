@@ -97,6 +97,37 @@ __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatil
     return false;
 }
 
+// What a warp that walks the list of units says of each (bits of a job's flags): first, last unit of
+// its item in this CTA; every row sees every token; the item's own first, last unit is in this CTA;
+// no unit, the end.
+enum : int32_t { kBegin = 1, kEnd = 2, kWhole = 4, kStop = 8, kStarts = 16, kEnds = 32 };
+
+// A place in the list of units.
+struct Walk {
+    Tile t;
+    int32_t h, u;
+    int64_t left;
+};
+
+__device__ __forceinline__ KvSeq seq_of(const AttnArgs &a, int s) {
+    return kv_seq(a.cu_q, a.kv_len, s, a.T_tot, a.max_q, a.kv);
+}
+
+template <int ROWS, int UNIT>
+__device__ __forceinline__ void next_item(const AttnArgs &a, Walk &w) {
+    w.u = 0;
+    if (++w.h < a.kv.Hkv) return;
+    w.h = 0;
+    int s = w.t.s, rt = w.t.rt + 1;
+    KvSeq q = w.t.q;
+    if (rt >= w.t.tiles) {
+        rt = 0;
+        do q = seq_of(a, ++s);
+        while (q.n == 0 && s + 1 < a.nseq);
+    }
+    w.t = make_tile<ROWS, UNIT>(a, s, q, rt);
+}
+
 template <int D>
 constexpr int kPartRow = D + 4;   // floats of a partial row: o, m, l, 2 free (rows stay 16-byte aligned)
 

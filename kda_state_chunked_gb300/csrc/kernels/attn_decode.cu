@@ -7,11 +7,12 @@
 // M = 16 of a warp-level matrix product, so a cached byte is read once for all of them; wider
 // tensor-memory tiles would stand empty here.
 //
-// Two CTAs of 4 warps an SM, so that one streams while the other joins its warps or starts an item.
-// A warp takes a step of a unit's tokens (32 of the 8-bit cache, 16 of the 16-bit one: groups of 16
-// tokens, each in one page) and runs alone: it copies its own tokens of later units into its own
-// ring of shared-memory stages (bulk copies: a page's rows are contiguous) and keeps its own
-// maxima, sums and 16 x D accumulators.  The warps meet only at an item's end.
+// Two CTAs an SM, so that one streams while the other joins its warps or starts an item.  A fifth
+// warp walks the list of units and copies them into a ring of stages (bulk copies: 16 tokens lie in
+// one page, and a page's rows are contiguous); with each warp aiming its own copies the bookkeeping
+// was 40% of the instructions.  The other four take a step of a unit's tokens each (32 of the 8-bit
+// cache, 16 of the 16-bit one) and run alone, with their own maxima, sums and 16 x D accumulators.
+// They meet only at an item's beginning, to split its queries, and at its end.
 //
 // 8-bit cache: codes c become fp16 exactly (the byte under the exponent of 1024, less 1152), a
 // query row is scaled by a power of two into fp16's range, so q . c carries no rounding beyond
@@ -29,7 +30,7 @@ namespace {
 
 using namespace attn;
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 4;                             // that compute; one more walks and copies
 constexpr float kPScale = 8192.f;                     // probabilities' scale in fp16
 constexpr float kMinRef = 0x1p-100f;
 
@@ -39,21 +40,30 @@ struct Shape {
     static constexpr int step = FMT == KDA_KV_I8 ? 32 : 16, groups = step / 16, unit = kWarps * step;
     static constexpr int group = row * 16;            // K or V bytes of 16 tokens
     static constexpr int tile = groups * group;
-    static constexpr int stage = 2 * tile + 128;      // keys, values, 16 bytes of scales a group
-    static constexpr int stages = D == 128 ? 2 : 4;        // of a warp's ring, two CTAs an SM
+    static constexpr int part = 2 * tile + 128;       // a warp's keys, values, 16 bytes of scales a group
+    static constexpr int stage = kWarps * part;
+    static constexpr int stages = D == 128 ? 2 : 4;        // of the ring, two CTAs an SM
     static constexpr int deep_stages = D == 128 ? 5 : 8;   // one CTA an SM
+};
+
+// A unit of work.
+struct Job {
+    int32_t j0, flags, base, row0, nrows, tok0, head;   // first token; the row tile
+    uint32_t live, whole;                               // groups that are there; warps whose rows see all of theirs
+    int32_t pmin, pmax, pad;
 };
 
 template <int FMT, int D, int NT>
 struct Smem {
-    // behind the rings
+    // behind the ring
     static constexpr int o_acc = 0;                                      // [kWarps][16][D] fp32
     static constexpr int o_ml = o_acc + kWarps * 16 * D * 4;             // [2][kWarps][16][2] fp32
-    static constexpr int o_q = o_ml + 2 * kWarps * 16 * 8;               // fragments of split queries
-    static constexpr int o_bar = o_q + (NT > 1 ? NT * (D / 16) * 512 : 0);
-    static constexpr int o_live = o_bar + kWarps * Shape<FMT, D>::deep_stages * 8;
-    static constexpr int o_misc = o_live + kWarps * Shape<FMT, D>::deep_stages * 4;
-    static constexpr int total(int stages) { return kWarps * stages * Shape<FMT, D>::stage + o_misc + 128; }
+    static constexpr int o_q = o_ml + 2 * kWarps * 16 * 8;               // fragments of the queries
+    static constexpr int o_qs = o_q + NT * (D / 16) * 512;               // [16] row factors
+    static constexpr int o_job = o_qs + 64;
+    static constexpr int o_bar = o_job + Shape<FMT, D>::deep_stages * (int)sizeof(Job);   // full, empty
+    static constexpr int o_err = o_bar + 2 * Shape<FMT, D>::deep_stages * 8;
+    static constexpr int total(int stages) { return stages * Shape<FMT, D>::stage + o_err + 64; }
 };
 
 // Fragment loads and products are plain functions of their operands to the compiler, which may so
@@ -125,476 +135,496 @@ __device__ __forceinline__ int acc_unit(int row, int u) {
     return FMT == KDA_KV_BF16 ? u ^ ((row & 7) << 1) : u ^ ((row & 1) << 2);
 }
 
-// Where a warp's loads stand: the unit whose copy comes next; lane i's group i of it, its page id
-// already on the way.
-struct Cursor {
-    Tile t;
-    int32_t h, u;
-    bool want;
-    int32_t page, slot;
-};
+// The share of this CTA (left = 0: none), found by one warp: the units of all sequences summed, then
+// the sequence, row tile, head and unit where the share begins.
+template <int UNIT>
+__device__ __forceinline__ Walk find_share(const AttnArgs &a, int lane, int64_t &W, int32_t &C) {
+    constexpr int R = kAttnDecodeRows;
+    auto seq_units = [&](int s) {
+        const KvSeq q = seq_of(a, s);
+        const int n = tiles_of<R>(a, q);
+        int64_t w = 0;
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) w += make_tile<R, UNIT>(a, s, q, i).units;
+        return w * a.kv.Hkv;
+    };
+    Walk w{};
+    W = 0;
+#pragma unroll 1
+    for (int s = lane; s < a.nseq; s += 32) W += seq_units(s);
+    for (int i = 16; i; i >>= 1) W += __shfl_xor_sync(0xFFFFFFFFu, W, i);
+    C = (int32_t)min((int64_t)a.ctas, W);   // no CTA that takes part is without a unit
+    if ((int32_t)blockIdx.x >= C) return w;
+    const int64_t begin = (int64_t)blockIdx.x * W / C, end = (int64_t)(blockIdx.x + 1) * W / C;
+    w.left = end - begin;
+    int64_t at = begin;
+    int s0 = 0;
+#pragma unroll 1
+    for (int base = 0;; base += 32) {
+        const int64_t mine = base + lane < a.nseq ? seq_units(base + lane) : 0;
+        int64_t x = mine;
+        for (int i = 1; i < 32; i <<= 1) {
+            const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, i);
+            if (lane >= i) x += y;
+        }
+        const uint32_t hit = __ballot_sync(0xFFFFFFFFu, at < x);
+        const int f = hit ? __ffs(hit) - 1 : 31;
+        at -= __shfl_sync(0xFFFFFFFFu, hit ? x - mine : x, f);
+        s0 = base + f;
+        if (hit) break;
+    }
+    const KvSeq q = seq_of(a, s0);
+#pragma unroll 1
+    for (int rt = 0;; ++rt) {
+        w.t = make_tile<R, UNIT>(a, s0, q, rt);
+        if (at < (int64_t)w.t.units * a.kv.Hkv) break;
+        at -= (int64_t)w.t.units * a.kv.Hkv;
+    }
+    w.h = (int32_t)(at / w.t.units);
+    w.u = (int32_t)(at % w.t.units);
+    return w;
+}
 
 template <int FMT, int D, int NT>
-__global__ void __launch_bounds__(kWarps * 32, 2) attn_decode_kernel(const __grid_constant__ AttnArgs a) {
+__global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const __grid_constant__ AttnArgs a) {
     using S = Shape<FMT, D>;
     using M = Smem<FMT, D, NT>;
     constexpr int kKs = D / 16;   // 16-wide slices of a row
     constexpr int kNt = D / 8;    // 8-wide output tiles
     constexpr int kGr = S::groups;
     extern __shared__ uint8_t smem_raw[];
-    uint8_t *rings = ptx::smem_align1024(smem_raw);
+    uint8_t *ring = ptx::smem_align1024(smem_raw);
     const int stages = a.deep ? S::deep_stages : S::stages;
-    uint8_t *sm = rings + kWarps * stages * S::stage;
+    uint8_t *sm = ring + stages * S::stage;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane >> 2, t = lane & 3;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + M::o_bar) + warp * stages;
-    volatile uint32_t *live = reinterpret_cast<uint32_t *>(sm + M::o_live) + warp * stages;
-    uint8_t *ring = rings + warp * stages * S::stage;
+    uint64_t *full = reinterpret_cast<uint64_t *>(sm + M::o_bar), *empty = full + S::deep_stages;
+    Job *jobs = reinterpret_cast<Job *>(sm + M::o_job);
+    volatile int *err = reinterpret_cast<int *>(sm + M::o_err);
+    if (tid == 0) {
+        for (int i = 0; i < stages; ++i) {
+            ptx::mbar_init(&full[i], 1);
+            ptx::mbar_init(&empty[i], kWarps);
+        }
+        *err = 0;
+    }
+    ptx::fence_mbar_init();
+    __syncthreads();
+    ptx::grid_dep_wait();
+
+    if (warp == kWarps) {
+        // ====================================================== the list of units, and their copies
+        constexpr int kGroups = kWarps * kGr;
+        const int pt = a.kv.page_tokens;
+        Walk w{};
+        int64_t W = 0;
+        int32_t C = 0;
+        if (a.whole) {
+            // CTA i is item i: key/value head i % Hkv of sequence i / Hkv (one row tile a sequence)
+            const KvSeq q = seq_of(a, blockIdx.x / a.kv.Hkv);
+            if (q.n > 0) {
+                w.h = blockIdx.x % a.kv.Hkv;
+                w.t = make_tile<kAttnDecodeRows, S::unit>(a, blockIdx.x / a.kv.Hkv, q, 0);
+                w.left = w.t.units;
+            }
+        } else {
+            w = find_share<S::unit>(a, lane, W, C);
+            if (lane == 0) a.split[blockIdx.x].last_cta = -1;
+        }
+        // Units go in batches of up to kBatch of one item: lane i looks up the page of group i % kGroups of
+        // the batch's unit i / kGroups, and the next batch is looked up while this one is copied.
+        constexpr int kBatch = 32 / kGroups;
+        struct Look {
+            int32_t n, page, slot;
+            bool want;
+        };
+        auto look = [&](const Walk &x) {
+            Look r{0, 0, 0, false};
+            if (x.left <= 0) return r;
+            r.n = (int32_t)min((int64_t)min(kBatch, x.t.units - x.u), x.left);
+            const int32_t j = unit_token<S::unit>(x.t, x.u + lane / kGroups) + lane % kGroups * 16, b = j / pt;
+            r.slot = j - b * pt;
+            r.want = lane / kGroups < r.n && any_sees(a, x.t, j, 16);
+            if (r.want) r.page = __ldg(a.kv.table + (int64_t)x.t.s * a.kv.max_pages + b);
+            return r;
+        };
+        int32_t u_first = w.u;
+        Look now = look(w);
+        int stage = 0;
+        uint32_t phase = 1;
+        bool ok = true;
+        while (ok && now.n > 0) {
+            Walk next = w;
+            next.left -= now.n;
+            next.u += now.n;
+            if (next.left > 0 && next.u == w.t.units) next_item<kAttnDecodeRows, S::unit>(a, next);
+            const Look then = look(next);
+            const Tile &x = w.t;
+#pragma unroll 1
+            for (int k = 0; k < now.n; ++k) {
+                ok = __all_sync(0xFFFFFFFFu, wait_bar(&empty[stage], phase, err));
+                if (!ok) break;
+                const int32_t u = w.u + k, j0 = unit_token<S::unit>(x, u), from = k * kGroups + lane;
+                const int64_t left = w.left - k;
+                const int32_t page = __shfl_sync(0xFFFFFFFFu, now.page, from), slot = __shfl_sync(0xFFFFFFFFu, now.slot, from);
+                const bool want = __shfl_sync(0xFFFFFFFFu, (int)now.want, from) && lane < kGroups;
+                const uint8_t *rec = want ? kv_record(a.kv, page, w.h) : nullptr;
+                const uint32_t live = __ballot_sync(0xFFFFFFFFu, rec != nullptr);
+                const uint32_t whole = __ballot_sync(0xFFFFFFFFu, lane < kWarps && all_see(a, x, j0 + lane * S::step, S::step));
+                if (lane == 0) {
+                    Job &jb = jobs[stage];
+                    const bool ends = left >= x.units - u;   // the item's last unit is in this share
+                    jb.j0 = j0;
+                    jb.flags = (u == u_first ? kBegin : 0) | (u + 1 == x.units || left == 1 ? kEnd : 0) |
+                               (u_first == 0 ? kStarts : 0) | (ends ? kEnds : 0);
+                    jb.base = x.q.len - x.q.n;
+                    jb.row0 = x.row0, jb.nrows = x.nrows, jb.tok0 = x.q.tok0, jb.head = w.h;
+                    jb.live = live, jb.whole = whole;
+                    jb.pmin = x.pmin, jb.pmax = x.pmax;
+                    if (u_first == 0 && !ends && left == 1) {
+                        AttnSplit sp{};
+                        sp.last_cta = cta_of((int64_t)(blockIdx.x + 1) * W / C - 1 + (x.units - 1 - u), W, C);
+                        sp.row_tok = x.q.tok0;
+                        sp.head = w.h;
+                        sp.row0 = x.row0;
+                        sp.nrows = x.nrows;
+                        a.split[blockIdx.x] = sp;
+                    }
+                    ptx::mbar_arrive_expect_tx(&full[stage], __popc(live) * (2 * S::group + (FMT == KDA_KV_I8 ? 16 : 0)));
+                }
+                __syncwarp();
+                if (rec) {
+                    // 16 tokens' lines follow one another in the page; a warp's part has them by line block, too
+                    constexpr uint32_t kLine = S::row < 128 ? S::row : 128, kRun = kLine * 16;
+                    uint8_t *dst = ring + stage * S::stage + lane / kGr * S::part + lane % kGr * kRun;
+                    const uint8_t *src = rec + slot * kLine;
+#pragma unroll
+                    for (int v = 0; v < 2; ++v)
+#pragma unroll
+                        for (int b = 0; b < S::group / (int)kRun; ++b)
+                            ptx::bulk_load(dst + v * S::tile + b * kGr * kRun, src + v * pt * S::row + b * pt * 128, kRun,
+                                           &full[stage]);
+                    if (FMT == KDA_KV_I8)
+                        ptx::bulk_load(ring + stage * S::stage + lane / kGr * S::part + 2 * S::tile + 16 * (lane % kGr),
+                                       rec + 2 * pt * S::row, 16, &full[stage]);
+                }
+                if (++stage == stages) stage = 0, phase ^= 1;
+            }
+            if (next.u == 0) u_first = 0;
+            w = next;
+            now = then;
+        }
+        if (ok && __all_sync(0xFFFFFFFFu, wait_bar(&empty[stage], phase, err)) && lane == 0) {
+            jobs[stage].flags = kStop;
+            ptx::mbar_arrive(&full[stage]);
+        }
+        return;
+    }
+
+    // ========================================================== the warps that compute
     float *ml = reinterpret_cast<float *>(sm + M::o_ml);   // of this item; the last one's may still be read
     int ml_next = kWarps * 32;
     float *acc = reinterpret_cast<float *>(sm + M::o_acc);
     uint32_t *qfrag = reinterpret_cast<uint32_t *>(sm + M::o_q);
-    volatile int *err = reinterpret_cast<int *>(sm + M::o_misc);
-    int64_t *share = reinterpret_cast<int64_t *>(sm + M::o_misc + 16);   // warps' sums, then the start
-
-    if (lane == 0)
-        for (int i = 0; i < stages; ++i) ptx::mbar_init(&bars[i], 1);
-    if (tid == 0) *err = 0;
-    ptx::fence_mbar_init();
-    ptx::grid_dep_wait();
-
-    // ---- this CTA's units: sum the units of every sequence, then find where its share begins
-    const int32_t Hkv = a.kv.Hkv;
-    auto seq = [&](int s) { return kv_seq(a.cu_q, a.kv_len, s, a.T_tot, a.max_q, a.kv); };
-    auto seq_units = [&](int s) {
-        const KvSeq q = seq(s);
-        const int n = tiles_of<kAttnDecodeRows>(a, q);
-        int64_t w = 0;
-        for (int i = 0; i < n; ++i) w += make_tile<kAttnDecodeRows, S::unit>(a, s, q, i).units;
-        return w * Hkv;
-    };
-    auto block_sum = [&](int64_t v, int64_t &before) {   // exclusive prefix over threads; returns the sum
-        int64_t x = v;
-        for (int i = 1; i < 32; i <<= 1) {
-            const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, i);
-            if (lane >= i) x += y;
-        }
-        __syncthreads();
-        if (lane == 31) share[warp] = x;
-        __syncthreads();
-        int64_t base = 0, all = 0;
-        for (int i = 0; i < kWarps; ++i) {
-            if (i < warp) base += share[i];
-            all += share[i];
-        }
-        before = base + x - v;
-        return all;
-    };
-    int64_t W = 0, begin = 0, end;
-    int32_t C = 0, h0, u0 = 0;
-    Tile t0;
-    if (a.whole) {
-        // CTA i is item i: key/value head i % Hkv of sequence i / Hkv (one row tile a sequence)
-        const KvSeq q = seq(blockIdx.x / Hkv);
-        if (q.n == 0) return;
-        h0 = blockIdx.x % Hkv;
-        t0 = make_tile<kAttnDecodeRows, S::unit>(a, blockIdx.x / Hkv, q, 0);
-        end = t0.units;
-    } else {
-        int64_t mine0 = 0, mine = 0, before;
-        for (int s = tid; s < a.nseq; s += kWarps * 32) {
-            const int64_t w = seq_units(s);
-            if (s == tid) mine0 = w;
-            mine += w;
-        }
-        W = block_sum(mine, before);
-        if (tid == 0) a.split[blockIdx.x].last_cta = -1;
-        C = (int32_t)min((int64_t)a.ctas, W);   // no CTA that takes part is without a unit
-        if ((int32_t)blockIdx.x >= C) return;
-        begin = (int64_t)blockIdx.x * W / C, end = (int64_t)(blockIdx.x + 1) * W / C;
-        int64_t *found = share + kWarps;
-        int64_t base = 0;
-        for (int s = 0; s < a.nseq; s += kWarps * 32) {
-            const int64_t w = s == 0 ? mine0 : (s + tid < a.nseq ? seq_units(s + tid) : 0);
-            const int64_t all = block_sum(w, before);
-            if (begin >= base + before && begin < base + before + w) {
-                found[0] = s + tid;
-                found[1] = begin - base - before;
-            }
-            base += all;
-            if (begin < base) break;
-        }
-        __syncthreads();
-        const int32_t s0 = (int32_t)found[0];
-        int64_t left0 = found[1];   // units before `begin` in sequence s0
-        const KvSeq q = seq(s0);
-        for (int rt = 0;; ++rt) {
-            t0 = make_tile<kAttnDecodeRows, S::unit>(a, s0, q, rt);
-            if (left0 < (int64_t)t0.units * Hkv) break;
-            left0 -= (int64_t)t0.units * Hkv;
-        }
-        h0 = (int32_t)(left0 / t0.units);
-        u0 = (int32_t)(left0 % t0.units);
-    }
-
-    // the next item after (tile, head)
-    auto next_item = [&](Tile &x, int32_t &h) {
-        if (++h < Hkv) return;
-        h = 0;
-        if (x.rt + 1 < x.tiles) {
-            x = make_tile<kAttnDecodeRows, S::unit>(a, x.s, x.q, x.rt + 1);
-            return;
-        }
-        int s = x.s + 1;
-        KvSeq q = seq(s);
-        while (q.n == 0 && s + 1 < a.nseq) q = seq(++s);
-        x = make_tile<kAttnDecodeRows, S::unit>(a, s, q, 0);
-    };
-
-    // ---- loads
-    const int pt = a.kv.page_tokens;
-    auto aim = [&](Cursor &c) {   // this warp's step of the cursor's unit
-        const int32_t j = unit_token<S::unit>(c.t, c.u) + warp * S::step + lane * 16;
-        c.want = lane < kGr && any_sees(a, c.t, j, 16);
-        if (!c.want) return;
-        const int32_t b = j / pt;
-        c.slot = j - b * pt;
-        c.page = __ldg(a.kv.table + (int64_t)c.t.s * a.kv.max_pages + b);
-    };
-    auto load = [&](const Cursor &c, int stage) {
-        const uint8_t *rec = c.want ? kv_record(a.kv, c.page, c.h) : nullptr;
-        const uint32_t there = __ballot_sync(0xFFFFFFFFu, rec != nullptr);
-        if (lane == 0) {
-            live[stage] = there;
-            ptx::mbar_arrive_expect_tx(&bars[stage], __popc(there) * (2 * S::group + (FMT == KDA_KV_I8 ? 16 : 0)));
-        }
-        __syncwarp();
-        if (!rec) return;
-        // a group's lines follow one another in the page; a stage has them by line block, like a page
-        constexpr uint32_t kLine = S::row < 128 ? S::row : 128, kRun = kLine * 16;
-        uint8_t *dst = ring + stage * S::stage + lane * kRun;
-#pragma unroll
-        for (int v = 0; v < 2; ++v)
-#pragma unroll
-            for (int b = 0; b < S::group / (int)kRun; ++b)
-                ptx::bulk_load(dst + v * S::tile + b * kGr * kRun, rec + v * pt * S::row + b * pt * 128 + c.slot * kLine, kRun,
-                               &bars[stage]);
-        if (FMT == KDA_KV_I8)
-            ptx::bulk_load(ring + stage * S::stage + 2 * S::tile + 16 * lane, rec + 2 * pt * S::row, 16, &bars[stage]);
-    };
-    Cursor cur;
-    cur.t = t0;
-    cur.h = h0;
-    cur.u = u0;
-    int64_t to_load = end - begin;
-    aim(cur);
-    auto load_next = [&](int stage) {
-        if (to_load == 0) return;
-        load(cur, stage);
-        if (--to_load == 0) return;
-        if (++cur.u == cur.t.units) {
-            cur.u = 0;
-            next_item(cur.t, cur.h);
-        }
-        aim(cur);
-    };
-    for (int i = 0; i < stages; ++i) load_next(i);
-
-    // ---- items
-    Tile tile = t0;
-    int32_t head = h0, u = u0, stage = 0;
+    float *qs = reinterpret_cast<float *>(sm + M::o_qs);
+    auto meet = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory"); };
+    int stage = 0;
     uint32_t phase = 0;
-    int64_t left = end - begin;
-    while (left > 0) {
-        const int32_t u_first = u, u_last = (int32_t)min((int64_t)tile.units, u + left);
-
-        // query fragments, rows g and g + 8
-        uint32_t qa[NT == 1 ? kKs : 1][4];
-        float rs[2];
-        int32_t pos[2];
-        {
-            float x[2][kKs * 4];
+    uint32_t qa[NT == 1 ? kKs : 1][4];
+    float rs[2] = {0.f, 0.f};
+    int32_t pos[2] = {-1, -1}, nrows = 0, row0 = 0, tok0 = 0, head = 0;   // the item
+    float o[kNt][4], m[2], l[2], ref = 0.f, inv_ref = 0.f;   // ref: 8-bit, the largest value scale so far
+    for (;;) {
+        const bool ok = __all_sync(0xFFFFFFFFu, wait_bar(&full[stage], phase, err));
+        if (!ok) {
+            if (lane == 0) flag_status(a.kv.status, KDA_DEV_TIMEOUT);
+            break;
+        }
+        const Job &jb = jobs[stage];
+        const int32_t flags = jb.flags;
+        if (flags & kStop) break;
+        if (flags & kBegin) {
+            nrows = jb.nrows, row0 = jb.row0, tok0 = jb.tok0, head = jb.head;
+            // The item's queries as fragments: eight threads a row, who agree on its factor.  Columns go
+            // where the fragment wants them: pairs of a lane's four bytes of a key for the 8-bit cache.
+            constexpr int kCols = D / 8;
+            const int row = tid / 8, c0 = tid % 8 * kCols, at = row0 + row;
+            float x[kCols];
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const int row = g + 8 * r, at = tile.row0 + row;
-                const bool in = row < tile.nrows;
-                pos[r] = in ? tile.q.len - tile.q.n + at / a.G : -1;
-                const int64_t off = (int64_t)(tile.q.tok0 + at / a.G) * a.q_stride + (int64_t)(head * a.G + at % a.G) * D;
+            for (int i = 0; i < kCols; ++i) x[i] = 0.f;
+            if (row < nrows) {
+                const int64_t off = (int64_t)(tok0 + at / a.G) * a.q_stride + (int64_t)(head * a.G + at % a.G) * D + c0;
+#pragma unroll
+                for (int i = 0; i < kCols; i += 8) {
+                    if (NT > 1) {
+                        const float4 u = *reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) + off + i);
+                        const float4 v = *reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) + off + i + 4);
+                        x[i] = u.x, x[i + 1] = u.y, x[i + 2] = u.z, x[i + 3] = u.w;
+                        x[i + 4] = v.x, x[i + 5] = v.y, x[i + 6] = v.z, x[i + 7] = v.w;
+                    } else {
+                        const uint4 u = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) + off + i);
+                        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            x[i + 2 * y] = __uint_as_float(w[y] << 16);
+                            x[i + 2 * y + 1] = __uint_as_float(w[y] & 0xFFFF0000u);
+                        }
+                    }
+                }
+            }
+            float f = a.scale * kLog2e;
+            if (FMT == KDA_KV_I8) {
+                // a power of two that brings the row's largest magnitude to [2^10, 2^11)
+                float top = 0.f;
+#pragma unroll
+                for (int i = 0; i < kCols; ++i) top = fmaxf(top, fabsf(x[i]));
+#pragma unroll
+                for (int i = 1; i < 8; i <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, i));
+                const int e = (int)(__float_as_uint(top) >> 23);
+                const int shift = e == 0 || e == 255 ? 0 : min(max(137 - e, -120), 120);
+                const float up = __uint_as_float((uint32_t)(127 + shift) << 23);
+#pragma unroll
+                for (int i = 0; i < kCols; ++i) x[i] *= up;
+                f *= __uint_as_float((uint32_t)(127 - shift) << 23);
+            }
+            if (tid % 8 == 0) qs[row] = f;
+#pragma unroll
+            for (int i = 0; i < kCols; i += 2) {
+                const int c = (c0 + i) % 16, k = (c0 + i) / 16;
+                const int tt = FMT == KDA_KV_I8 ? c / 4 : c % 8 / 2, half = FMT == KDA_KV_I8 ? c / 2 % 2 : c / 8;
+                uint32_t z[NT];
+                split2<FMT, NT>(x[i], x[i + 1], z);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) qfrag[((n * kKs + k) * 32 + row % 8 * 4 + tt) * 4 + row / 8 + 2 * half] = z[n];
+            }
+            meet();
+            if constexpr (NT == 1) {
 #pragma unroll
                 for (int k = 0; k < kKs; ++k) {
-                    // the four columns of slice k that this lane feeds: neighbours for the 8-bit
-                    // cache (a lane's four bytes of a key), the fragment's own for the 16-bit one
-                    const int c0 = 16 * k + (FMT == KDA_KV_I8 ? 4 * t : 2 * t);
-                    const int c1 = FMT == KDA_KV_I8 ? c0 + 2 : c0 + 8;
-                    float2 lo = make_float2(0.f, 0.f), hi = lo;
-                    if (in) {
-                        if (NT > 1) {
-                            const float *p = static_cast<const float *>(a.q) + off;
-                            lo = *reinterpret_cast<const float2 *>(p + c0);
-                            hi = *reinterpret_cast<const float2 *>(p + c1);
-                        } else {
-                            const __nv_bfloat16 *p = static_cast<const __nv_bfloat16 *>(a.q) + off;
-                            lo = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(p + c0));
-                            hi = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(p + c1));
-                        }
-                    }
-                    x[r][4 * k] = lo.x, x[r][4 * k + 1] = lo.y, x[r][4 * k + 2] = hi.x, x[r][4 * k + 3] = hi.y;
-                }
-                rs[r] = a.scale * kLog2e;
-                if (FMT == KDA_KV_I8) {
-                    // a power of two that brings the row's largest magnitude to [2^10, 2^11)
-                    float top = 0.f;
-#pragma unroll
-                    for (int i = 0; i < kKs * 4; ++i) top = fmaxf(top, fabsf(x[r][i]));
-                    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-                    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-                    const int e = (int)(__float_as_uint(top) >> 23);
-                    const int shift = e == 0 || e == 255 ? 0 : min(max(137 - e, -120), 120);
-                    const float up = __uint_as_float((uint32_t)(127 + shift) << 23);
-#pragma unroll
-                    for (int i = 0; i < kKs * 4; ++i) x[r][i] *= up;
-                    rs[r] *= __uint_as_float((uint32_t)(127 - shift) << 23);
+                    const uint4 u = *reinterpret_cast<const uint4 *>(qfrag + (k * 32 + lane) * 4);
+                    qa[k][0] = u.x, qa[k][1] = u.y, qa[k][2] = u.z, qa[k][3] = u.w;
                 }
             }
 #pragma unroll
-            for (int k = 0; k < kKs; ++k) {
-                uint32_t f[4][NT];
-                split2<FMT, NT>(x[0][4 * k], x[0][4 * k + 1], f[0]);
-                split2<FMT, NT>(x[1][4 * k], x[1][4 * k + 1], f[1]);
-                split2<FMT, NT>(x[0][4 * k + 2], x[0][4 * k + 3], f[2]);
-                split2<FMT, NT>(x[1][4 * k + 2], x[1][4 * k + 3], f[3]);
-                if constexpr (NT == 1) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) qa[k][i] = f[i][0];
-                } else if (k % kWarps == warp) {
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-                        *reinterpret_cast<uint4 *>(qfrag + ((n * kKs + k) * 32 + lane) * 4) =
-                            make_uint4(f[0][n], f[1][n], f[2][n], f[3][n]);
-                }
+            for (int r = 0; r < 2; ++r) {
+                rs[r] = qs[g + 8 * r];
+                pos[r] = g + 8 * r < nrows ? jb.base + (row0 + g + 8 * r) / a.G : -1;
+                m[r] = -INFINITY, l[r] = 0.f;
             }
-            if constexpr (NT > 1) __syncthreads();
+            ref = inv_ref = 0.f;
+#pragma unroll
+            for (int j = 0; j < kNt; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
         }
-
-        float o[kNt][4];
+        const uint32_t there = jb.live >> (warp * kGr) & ((1u << kGr) - 1u);
+        if (there) {
+            const int32_t j0 = jb.j0 + warp * S::step;
+            const uint8_t *buf = ring + stage * S::stage + warp * S::part;
+            uint32_t kb = ptx::smem_u32(buf);
+            asm volatile("" : "+r"(kb)::"memory");
+            const uint32_t vb = kb + S::tile;
+            float sc[kGr][2], vs[kGr];   // a group's score factors (by row half) and value scale
 #pragma unroll
-        for (int j = 0; j < kNt; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-        float ref = 0.f, inv_ref = 0.f;   // 8-bit: largest value scale so far
-
-        for (; u < u_last; ++u, --left) {
-            const bool ok = __all_sync(0xFFFFFFFFu, wait_bar(&bars[stage], phase, err));
-            if (!ok) flag_status(a.kv.status, KDA_DEV_TIMEOUT);
-            const uint32_t there = ok ? live[stage] : 0u;
-            if (there) {
-                const int32_t j0 = unit_token<S::unit>(tile, u) + warp * S::step;
-                const uint8_t *buf = ring + stage * S::stage;
-                uint32_t kb = ptx::smem_u32(buf);
-                asm volatile("" : "+r"(kb)::"memory");
-                const uint32_t vb = kb + S::tile;
-                float sc[kGr][2], vs[kGr];   // a group's score factors (by row half) and value scale
-#pragma unroll
-                for (int y = 0; y < kGr; ++y) {
-                    sc[y][0] = rs[0], sc[y][1] = rs[1], vs[y] = 0.f;
-                    if (FMT == KDA_KV_I8) {
-                        const float2 f = *reinterpret_cast<const float2 *>(buf + 2 * S::tile + 16 * y);
-                        if (there >> y & 1u) sc[y][0] *= fabsf(f.x), sc[y][1] *= fabsf(f.x), vs[y] = fabsf(f.y);
-                    }
+            for (int y = 0; y < kGr; ++y) {
+                sc[y][0] = rs[0], sc[y][1] = rs[1], vs[y] = 0.f;
+                if (FMT == KDA_KV_I8) {
+                    const float2 f = *reinterpret_cast<const float2 *>(buf + 2 * S::tile + 16 * y);
+                    if (there >> y & 1u) sc[y][0] *= fabsf(f.x), sc[y][1] *= fabsf(f.x), vs[y] = fabsf(f.y);
                 }
-                // ---- scores: c[n] of tokens j0 + 8 n ..
-                float c[2 * kGr][4] = {};
-                const int mr = lane & 7, mm = lane >> 3;   // row and matrix whose address this lane gives
-                auto slice = [&](float (&d)[4], int k, uint32_t b0, uint32_t b1) {
-                    if constexpr (NT == 1) {
-                        mma<FMT>(d, qa[k], b0, b1);
-                    } else {
-#pragma unroll
-                        for (int z = NT - 1; z >= 0; --z) {
-                            const uint4 f = *reinterpret_cast<const uint4 *>(qfrag + ((z * kKs + k) * 32 + lane) * 4);
-                            const uint32_t qf[4] = {f.x, f.y, f.z, f.w};
-                            mma<FMT>(d, qf, b0, b1);
-                        }
-                    }
-                };
-                if constexpr (FMT == KDA_KV_I8) {
-#pragma unroll
-                    for (int i = 0; i < kKs / 4; ++i)
-#pragma unroll
-                        for (int n = 0; n < 2 * kGr; ++n) {
-                            uint32_t w[4];
-                            ldsm4(w, kb + kv_tile_off<S::row>(S::step, 8 * n + mr, 16 * (4 * i + mm)));
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const uint32_t b = w[k] ^ 0x80808080u;
-                                slice(c[n], 4 * i + k, half2_of<0x4140>(b), half2_of<0x4342>(b));
-                            }
-                        }
+            }
+            // ---- scores: c[n] of tokens j0 + 8 n ..
+            float c[2 * kGr][4] = {};
+            const int mr = lane & 7, mm = lane >> 3;   // row and matrix whose address this lane gives
+            auto slice = [&](float (&d)[4], int k, uint32_t b0, uint32_t b1) {
+                if constexpr (NT == 1) {
+                    mma<FMT>(d, qa[k], b0, b1);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < kKs / 2; ++i)
-#pragma unroll
-                        for (int n = 0; n < 2 * kGr; ++n) {
-                            uint32_t w[4];
-                            ldsm4(w, kb + kv_tile_off<S::row>(S::step, 8 * n + mr, 16 * (4 * i + mm)));
-#pragma unroll
-                            for (int k = 0; k < 2; ++k) slice(c[n], 2 * i + k, w[2 * k], w[2 * k + 1]);
-                        }
+                    for (int z = NT - 1; z >= 0; --z) {
+                        const uint4 f = *reinterpret_cast<const uint4 *>(qfrag + ((z * kKs + k) * 32 + lane) * 4);
+                        const uint32_t qf[4] = {f.x, f.y, f.z, f.w};
+                        mma<FMT>(d, qf, b0, b1);
+                    }
                 }
-                // ---- softmax: element (n, e) is row g + 8 (e / 2), token j0 + 8 n + 2 t + e % 2
-                const bool whole = there == (1u << kGr) - 1u && all_see(a, tile, j0, S::step);
-                float top[2] = {-INFINITY, -INFINITY};
+            };
+            if constexpr (FMT == KDA_KV_I8) {
+#pragma unroll
+                for (int i = 0; i < kKs / 4; ++i)
+#pragma unroll
+                    for (int n = 0; n < 2 * kGr; ++n) {
+                        uint32_t w[4];
+                        ldsm4(w, kb + kv_tile_off<S::row>(S::step, 8 * n + mr, 16 * (4 * i + mm)));
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t b = w[k] ^ 0x80808080u;
+                            slice(c[n], 4 * i + k, half2_of<0x4140>(b), half2_of<0x4342>(b));
+                        }
+                    }
+            } else {
+#pragma unroll
+                for (int i = 0; i < kKs / 2; ++i)
+#pragma unroll
+                    for (int n = 0; n < 2 * kGr; ++n) {
+                        uint32_t w[4];
+                        ldsm4(w, kb + kv_tile_off<S::row>(S::step, 8 * n + mr, 16 * (4 * i + mm)));
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) slice(c[n], 2 * i + k, w[2 * k], w[2 * k + 1]);
+                    }
+            }
+            // ---- softmax: element (n, e) is row g + 8 (e / 2), token j0 + 8 n + 2 t + e % 2
+            const bool whole = there == (1u << kGr) - 1u && (jb.whole >> warp & 1u);
+            float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int n = 0; n < 2 * kGr; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) c[n][e] *= sc[n >> 1][e >> 1];
+            if (!whole)   // rows not in use may see what they like
 #pragma unroll
                 for (int n = 0; n < 2 * kGr; ++n)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) c[n][e] *= sc[n >> 1][e >> 1];
-                if (!whole)   // rows not in use may see what they like
+                    for (int e = 0; e < 4; ++e)
+                        if (!(there >> (n >> 1) & 1u) || !sees(a, pos[e >> 1], j0 + 8 * n + 2 * t + (e & 1)))
+                            c[n][e] = -INFINITY;
 #pragma unroll
-                    for (int n = 0; n < 2 * kGr; ++n)
+            for (int n = 0; n < 2 * kGr; ++n)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (!(there >> (n >> 1) & 1u) || !sees(a, pos[e >> 1], j0 + 8 * n + 2 * t + (e & 1)))
-                                c[n][e] = -INFINITY;
+                for (int e = 0; e < 4; ++e) top[e >> 1] = fmaxf(top[e >> 1], c[n][e]);
 #pragma unroll
-                for (int n = 0; n < 2 * kGr; ++n)
+            for (int r = 0; r < 2; ++r) {
+                top[r] = fmaxf(top[r], __shfl_xor_sync(0xFFFFFFFFu, top[r], 1));
+                top[r] = fmaxf(top[r], __shfl_xor_sync(0xFFFFFFFFu, top[r], 2));
+            }
+            float vmax = 0.f;
+            if (FMT == KDA_KV_I8)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) top[e >> 1] = fmaxf(top[e >> 1], c[n][e]);
+                for (int y = 0; y < kGr; ++y) vmax = vs[y] < INFINITY ? fmaxf(vmax, vs[y]) : vmax;
+            const bool scaled = FMT == KDA_KV_I8 && vmax > ref;
+            if (__any_sync(0xFFFFFFFFu, top[0] > m[0] || top[1] > m[1] || scaled)) {
+                float f[2];
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    top[r] = fmaxf(top[r], __shfl_xor_sync(0xFFFFFFFFu, top[r], 1));
-                    top[r] = fmaxf(top[r], __shfl_xor_sync(0xFFFFFFFFu, top[r], 2));
+                    const float mn = fmaxf(m[r], top[r]);
+                    f[r] = mn == -INFINITY ? 1.f : ex2(m[r] - mn);
+                    l[r] *= f[r];
+                    m[r] = mn;
                 }
-                float vmax = 0.f;
-                if (FMT == KDA_KV_I8)
-#pragma unroll
-                    for (int y = 0; y < kGr; ++y) vmax = vs[y] < INFINITY ? fmaxf(vmax, vs[y]) : vmax;
-                const bool scaled = FMT == KDA_KV_I8 && vmax > ref;
-                if (__any_sync(0xFFFFFFFFu, top[0] > m[0] || top[1] > m[1] || scaled)) {
-                    float f[2];
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const float mn = fmaxf(m[r], top[r]);
-                        f[r] = mn == -INFINITY ? 1.f : ex2(m[r] - mn);
-                        l[r] *= f[r];
-                        m[r] = mn;
-                    }
-                    if (scaled) {
-                        const float rn = fmaxf(vmax, kMinRef), k = ref / rn;
-                        f[0] *= k, f[1] *= k;
-                        ref = rn;
-                        inv_ref = kPScale / rn;
-                    }
-#pragma unroll
-                    for (int j = 0; j < kNt; ++j) o[j][0] *= f[0], o[j][1] *= f[0], o[j][2] *= f[1], o[j][3] *= f[1];
+                if (scaled) {
+                    const float rn = fmaxf(vmax, kMinRef), k = ref / rn;
+                    f[0] *= k, f[1] *= k;
+                    ref = rn;
+                    inv_ref = kPScale / rn;
                 }
-                const float mx[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
-                bool strange = false;   // a value scale that is no number: 0 times it must stay 0
-                float pv[kGr];          // what a group's probabilities are multiplied by before rounding
+#pragma unroll
+                for (int j = 0; j < kNt; ++j) o[j][0] *= f[0], o[j][1] *= f[0], o[j][2] *= f[1], o[j][3] *= f[1];
+            }
+            const float mx[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+            bool strange = false;   // a value scale that is no number: 0 times it must stay 0
+            float pv[kGr];          // what a group's probabilities are multiplied by before rounding
+#pragma unroll
+            for (int y = 0; y < kGr; ++y) {
+                pv[y] = 1.f;
+                if (FMT == KDA_KV_I8) {
+                    pv[y] = vs[y] * inv_ref;
+                    if (!(vs[y] < INFINITY)) strange = true, pv[y] = NAN;
+                }
+            }
+            uint32_t pa[kGr][4][NT];
+#pragma unroll
+            for (int n = 0; n < 2 * kGr; ++n) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    c[n][e] = ex2(c[n][e] - mx[e >> 1]);
+                    l[e >> 1] += c[n][e];
+                }
+                if (FMT == KDA_KV_I8) {
+                    if (strange)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) c[n][e] = c[n][e] == 0.f ? 0.f : c[n][e] * pv[n >> 1];
+                    else
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) c[n][e] *= pv[n >> 1];
+                }
+                split2<FMT, NT>(c[n][0], c[n][1], pa[n >> 1][2 * (n & 1)]);
+                split2<FMT, NT>(c[n][2], c[n][3], pa[n >> 1][2 * (n & 1) + 1]);
+            }
+            // ---- values
+            auto values = [&]() {
 #pragma unroll
                 for (int y = 0; y < kGr; ++y) {
-                    pv[y] = 1.f;
-                    if (FMT == KDA_KV_I8) {
-                        pv[y] = vs[y] * inv_ref;
-                        if (!(vs[y] < INFINITY)) strange = true, pv[y] = NAN;
-                    }
-                }
-                uint32_t pa[kGr][4][NT];
 #pragma unroll
-                for (int n = 0; n < 2 * kGr; ++n) {
+                    for (int i = 0; i < S::row / 32; ++i) {
+                        uint32_t w[4];   // (tokens 0-7, 8-15) of 16-byte units 2 i and 2 i + 1
+                        ldsm4t(w, vb + kv_tile_off<S::row>(S::step, 16 * y + 8 * (mm & 1) + mr, 16 * (2 * i + (mm >> 1))));
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        c[n][e] = ex2(c[n][e] - mx[e >> 1]);
-                        l[e >> 1] += c[n][e];
-                    }
-                    if (FMT == KDA_KV_I8) {
-                        if (strange)
+                        for (int x = 0; x < 2; ++x) {
+                            if constexpr (FMT == KDA_KV_I8) {
+                                // a register holds columns 2 g, 2 g + 1 of two tokens: the even ones
+                                // make one output tile, the odd ones the next
+                                const uint32_t b0 = w[2 * x] ^ 0x80808080u, b1 = w[2 * x + 1] ^ 0x80808080u;
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) c[n][e] = c[n][e] == 0.f ? 0.f : c[n][e] * pv[n >> 1];
-                        else
+                                for (int z = NT - 1; z >= 0; --z) {
+                                    const uint32_t f[4] = {pa[y][0][z], pa[y][1][z], pa[y][2][z], pa[y][3][z]};
+                                    mma<FMT>(o[2 * (2 * i + x)], f, half2_of<0x4240>(b0), half2_of<0x4240>(b1));
+                                    mma<FMT>(o[2 * (2 * i + x) + 1], f, half2_of<0x4341>(b0), half2_of<0x4341>(b1));
+                                }
+                            } else {
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) c[n][e] *= pv[n >> 1];
-                    }
-                    split2<FMT, NT>(c[n][0], c[n][1], pa[n >> 1][2 * (n & 1)]);
-                    split2<FMT, NT>(c[n][2], c[n][3], pa[n >> 1][2 * (n & 1) + 1]);
-                }
-                // ---- values
-                auto values = [&]() {
-#pragma unroll
-                    for (int y = 0; y < kGr; ++y) {
-#pragma unroll
-                        for (int i = 0; i < S::row / 32; ++i) {
-                            uint32_t w[4];   // (tokens 0-7, 8-15) of 16-byte units 2 i and 2 i + 1
-                            ldsm4t(w, vb + kv_tile_off<S::row>(S::step, 16 * y + 8 * (mm & 1) + mr, 16 * (2 * i + (mm >> 1))));
-#pragma unroll
-                            for (int x = 0; x < 2; ++x) {
-                                if constexpr (FMT == KDA_KV_I8) {
-                                    // a register holds columns 2 g, 2 g + 1 of two tokens: the even ones
-                                    // make one output tile, the odd ones the next
-                                    const uint32_t b0 = w[2 * x] ^ 0x80808080u, b1 = w[2 * x + 1] ^ 0x80808080u;
-#pragma unroll
-                                    for (int z = NT - 1; z >= 0; --z) {
-                                        const uint32_t f[4] = {pa[y][0][z], pa[y][1][z], pa[y][2][z], pa[y][3][z]};
-                                        mma<FMT>(o[2 * (2 * i + x)], f, half2_of<0x4240>(b0), half2_of<0x4240>(b1));
-                                        mma<FMT>(o[2 * (2 * i + x) + 1], f, half2_of<0x4341>(b0), half2_of<0x4341>(b1));
-                                    }
-                                } else {
-#pragma unroll
-                                    for (int z = NT - 1; z >= 0; --z) {
-                                        const uint32_t f[4] = {pa[y][0][z], pa[y][1][z], pa[y][2][z], pa[y][3][z]};
-                                        mma<FMT>(o[2 * i + x], f, w[2 * x], w[2 * x + 1]);
-                                    }
+                                for (int z = NT - 1; z >= 0; --z) {
+                                    const uint32_t f[4] = {pa[y][0][z], pa[y][1][z], pa[y][2][z], pa[y][3][z]};
+                                    mma<FMT>(o[2 * i + x], f, w[2 * x], w[2 * x + 1]);
                                 }
                             }
                         }
                     }
-                };
-                bool odd = false;
-                if constexpr (FMT == KDA_KV_BF16) {
-                    // A token that a row does not see has probability 0, but 0 times an infinity or a
-                    // NaN is not 0 (stale slots past the end, or a value the row must not know of).
-                    // Where a step is not seen whole, look for such a value first.
-                    if (!whole) {
-                        uint32_t bad = 0;
-                        for (int i = lane; i < S::tile / 16; i += 32) {
-                            const uint4 x = *reinterpret_cast<const uint4 *>(buf + S::tile + 16 * i);
-                            for (uint32_t y : {x.x, x.y, x.z, x.w})
-                                bad |= (uint32_t)((y & 0x7F80u) == 0x7F80u) | (uint32_t)((y & 0x7F800000u) == 0x7F800000u);
-                        }
-                        odd = __any_sync(0xFFFFFFFFu, bad != 0);
-                    }
                 }
-                if (!odd) {
-                    values();
-                } else if constexpr (FMT == KDA_KV_BF16) {
-                    // one product for each query token, without the tokens it does not see, of which
-                    // only that token's rows are kept
-                    for (int32_t q = tile.pmin; q <= tile.pmax; ++q) {
-                        uint32_t keep[2];
+            };
+            bool odd = false;
+            if constexpr (FMT == KDA_KV_BF16) {
+                // A token that a row does not see has probability 0, but 0 times an infinity or a
+                // NaN is not 0 (stale slots past the end, or a value the row must not know of).
+                // Where a step is not seen whole, look for such a value first.
+                if (!whole) {
+                    uint32_t bad = 0;
+                    for (int i = lane; i < S::tile / 16; i += 32) {
+                        const uint4 x = *reinterpret_cast<const uint4 *>(buf + S::tile + 16 * i);
+                        for (uint32_t y : {x.x, x.y, x.z, x.w})
+                            bad |= (uint32_t)((y & 0x7F80u) == 0x7F80u) | (uint32_t)((y & 0x7F800000u) == 0x7F800000u);
+                    }
+                    odd = __any_sync(0xFFFFFFFFu, bad != 0);
+                }
+            }
+            if (!odd) {
+                values();
+            } else if constexpr (FMT == KDA_KV_BF16) {
+                // one product for each query token, without the tokens it does not see, of which
+                // only that token's rows are kept
+                for (int32_t q = jb.pmin; q <= jb.pmax; ++q) {
+                    uint32_t keep[2];
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const int j = j0 + 8 * i + 2 * t;
-                            keep[i] = (sees(a, q, j) ? 0xFFFFu : 0u) | (sees(a, q, j + 1) ? 0xFFFF0000u : 0u);
+                    for (int i = 0; i < 2; ++i) {
+                        const int j = j0 + 8 * i + 2 * t;
+                        keep[i] = (sees(a, q, j) ? 0xFFFFu : 0u) | (sees(a, q, j + 1) ? 0xFFFF0000u : 0u);
+                    }
+#pragma unroll
+                    for (int i = 0; i < kNt; ++i) {
+                        uint32_t w[4];
+                        ldsm4t(w, vb + kv_tile_off<S::row>(S::step, 8 * (mm & 1) + mr, 16 * i));
+                        float d[4] = {};
+#pragma unroll
+                        for (int z = NT - 1; z >= 0; --z) {
+                            const uint32_t f[4] = {pa[0][0][z], pa[0][1][z], pa[0][2][z], pa[0][3][z]};
+                            mma<FMT>(d, f, w[0] & keep[0], w[1] & keep[1]);
                         }
 #pragma unroll
-                        for (int i = 0; i < kNt; ++i) {
-                            uint32_t w[4];
-                            ldsm4t(w, vb + kv_tile_off<S::row>(S::step, 8 * (mm & 1) + mr, 16 * i));
-                            float d[4] = {};
-#pragma unroll
-                            for (int z = NT - 1; z >= 0; --z) {
-                                const uint32_t f[4] = {pa[0][0][z], pa[0][1][z], pa[0][2][z], pa[0][3][z]};
-                                mma<FMT>(d, f, w[0] & keep[0], w[1] & keep[1]);
-                            }
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                if (pos[e >> 1] == q) o[i][e] += d[e];
-                        }
+                        for (int e = 0; e < 4; ++e)
+                            if (pos[e >> 1] == q) o[i][e] += d[e];
                     }
                 }
             }
-            pin(o);
-            __syncwarp();
-            load_next(stage);
-            if (++stage == stages) stage = 0, phase ^= 1;
-        }
+            }
+        pin(o);
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&empty[stage]);
+        if (++stage == stages) stage = 0, phase ^= 1;
+        if (!(flags & kEnd)) continue;
 
         // ---- the warps' results together
 #pragma unroll
@@ -606,11 +636,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_decode_kernel(const __gri
                 ml[(warp * 16 + g + 8 * r) * 2 + 1] = l[r];
             }
         }
-        __syncthreads();
+        meet();
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             const int row = g + 8 * r;
-            if (row >= tile.nrows) continue;
+            if (row >= nrows) continue;
             float mt = -INFINITY;
 #pragma unroll
             for (int i = 0; i < kWarps; ++i) mt = fmaxf(mt, ml[(i * 16 + row) * 2]);
@@ -630,10 +660,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_decode_kernel(const __gri
                         make_float2(o[j][2 * r] * f, o[j][2 * r + 1] * f);
             }
         }
-        __syncthreads();
-        const bool starts = u_first == 0, ends = u_last == tile.units;
+        meet();
+        const bool starts = flags & kStarts, ends = flags & kEnds;
         const int part_slot = starts ? 1 : 0;
-        for (int i = tid; i < tile.nrows * (D / 4); i += kWarps * 32) {
+        for (int i = tid; i < nrows * (D / 4); i += kWarps * 32) {
             const int row = i / (D / 4), unit = i % (D / 4);
             float mt = -INFINITY, lt = 0.f;
 #pragma unroll
@@ -647,8 +677,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_decode_kernel(const __gri
                 v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
             }
             if (starts && ends) {
-                const int at_row = tile.row0 + row;
-                const int64_t at = (int64_t)(tile.q.tok0 + at_row / a.G) * a.Hq + head * a.G + at_row % a.G;
+                const int at_row = row0 + row;
+                const int64_t at = (int64_t)(tok0 + at_row / a.G) * a.Hq + head * a.G + at_row % a.G;
                 const float inv = 1.f / lt;
                 if (lt == 0.f) v = make_float4(0.f, 0.f, 0.f, 0.f);
                 else v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
@@ -660,21 +690,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) attn_decode_kernel(const __gri
                 if (unit == 0) dst[D] = mt, dst[D + 1] = lt;
             }
         }
-        if (tid == 0 && starts && !ends) {
-            AttnSplit sp{};
-            sp.last_cta = cta_of(end - 1 + (tile.units - u_last) , W, C);
-            sp.row_tok = tile.q.tok0;
-            sp.head = head;
-            sp.row0 = tile.row0;
-            sp.nrows = tile.nrows;
-            a.split[blockIdx.x] = sp;
-        }
         ml += ml_next;
         ml_next = -ml_next;
-        if (left > 0) {
-            u = 0;
-            next_item(tile, head);
-        }
     }
 }
 
@@ -687,7 +704,7 @@ cudaError_t run(const AttnArgs &a, cudaStream_t st) {
     auto kern = attn_decode_kernel<FMT, D, NT>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kern<<<a.ctas, kWarps * 32, smem, st>>>(a);
+    kern<<<a.ctas, (kWarps + 1) * 32, smem, st>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess || a.whole) return e;
     // the join is placed while the last CTAs run and waits for them in hardware

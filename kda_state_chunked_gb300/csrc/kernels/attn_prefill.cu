@@ -50,14 +50,10 @@ constexpr float kGrow = 8.f;            // bits that a row's maximum may grow be
 constexpr float kPBits = 6.f;           // 8-bit: bits that a probability is scaled up in fp16
 constexpr int kJobs = 8;                // units handed out and not yet done with
 
-enum : int32_t { kBegin = 1, kEnd = 2, kWhole = 4, kStop = 8, kStarts = 16, kEnds = 32 };
-
 // A unit of work.
 struct __align__(16) Job {
     int32_t j0;                         // its first token
-    int32_t flags;                      // kBegin, kEnd: first, last unit of its item in this CTA; kWhole: every
-                                        // row sees every token; kStarts, kEnds: the item's own first, last unit
-                                        // is in this CTA; kStop: no unit, the end
+    int32_t flags;
     int32_t base;                       // position of the sequence's first query
     int32_t row0, nrows, tok0, head;    // the row tile
     uint32_t live;                      // groups of 16 tokens that are there
@@ -149,31 +145,6 @@ __device__ __forceinline__ void codes_to_half(uint4 c, uint4 &lo, uint4 &hi) {
     }
     lo = make_uint4(r[0], r[1], r[2], r[3]);
     hi = make_uint4(r[4], r[5], r[6], r[7]);
-}
-
-// A place in the list of units.
-struct Walk {
-    Tile t;
-    int32_t h, u;
-    int64_t left;
-};
-
-__device__ __forceinline__ KvSeq seq_of(const AttnArgs &a, int s) {
-    return kv_seq(a.cu_q, a.kv_len, s, a.T_tot, a.max_q, a.kv);
-}
-
-__device__ __forceinline__ void next_item(const AttnArgs &a, Walk &w) {
-    w.u = 0;
-    if (++w.h < a.kv.Hkv) return;
-    w.h = 0;
-    if (w.t.rt + 1 < w.t.tiles) {
-        w.t = make_tile<kRows, kUnit>(a, w.t.s, w.t.q, w.t.rt + 1);
-        return;
-    }
-    int s = w.t.s + 1;
-    KvSeq q = seq_of(a, s);
-    while (q.n == 0 && s + 1 < a.nseq) q = seq_of(a, ++s);
-    w.t = make_tile<kRows, kUnit>(a, s, q, 0);
 }
 
 // Units of sequence s over all heads, summed by a warp.
@@ -887,7 +858,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                 tcx::warp_arrive(&bars[JFULL + n % kJobs]);
                 --w.left;
                 if (++w.u == w.t.units) {
-                    if (w.left > 0) next_item(a, w);
+                    if (w.left > 0) next_item<kRows, kUnit>(a, w);
                     u_first = 0;
                 }
             }
