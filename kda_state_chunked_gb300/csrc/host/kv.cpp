@@ -9,7 +9,7 @@
 
 namespace {
 
-constexpr int64_t kWholeTokens = 1024;     // visible tokens up to which an item is not split
+constexpr int64_t kWholeTokens = 384;      // visible tokens up to which an item is not split
 constexpr int64_t kMaxTokens = 1 << 30;   // of a sequence: the kernels' positions and their differences fit int32
 
 int64_t elem_size(int32_t dtype) { return dtype == KDA_BF16 ? 2 : 4; }

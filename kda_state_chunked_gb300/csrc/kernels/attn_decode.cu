@@ -192,6 +192,8 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
     constexpr int kKs = D / 16;   // 16-wide slices of a row
     constexpr int kNt = D / 8;    // 8-wide output tiles
     constexpr int kGr = S::groups;
+    // query fragments stay in registers where the accumulators leave room for them
+    constexpr bool kRegQ = NT == 1 && !(FMT == KDA_KV_BF16 && D == 128);
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = ptx::smem_align1024(smem_raw);
     const int stages = a.deep ? S::deep_stages : S::stages;
@@ -329,7 +331,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
     auto meet = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory"); };
     int stage = 0;
     uint32_t phase = 0;
-    uint32_t qa[NT == 1 ? kKs : 1][4];
+    uint32_t qa[kRegQ ? kKs : 1][4];
     float rs[2] = {0.f, 0.f};
     int32_t pos[2] = {-1, -1}, nrows = 0, row0 = 0, tok0 = 0, head = 0;   // the item
     float o[kNt][4], m[2], l[2], ref = 0.f, inv_ref = 0.f;   // ref: 8-bit, the largest value scale so far
@@ -397,7 +399,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
                 for (int n = 0; n < NT; ++n) qfrag[((n * kKs + k) * 32 + row % 8 * 4 + tt) * 4 + row / 8 + 2 * half] = z[n];
             }
             meet();
-            if constexpr (NT == 1) {
+            if constexpr (kRegQ) {
 #pragma unroll
                 for (int k = 0; k < kKs; ++k) {
                     const uint4 u = *reinterpret_cast<const uint4 *>(qfrag + (k * 32 + lane) * 4);
@@ -434,7 +436,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
             float c[2 * kGr][4] = {};
             const int mr = lane & 7, mm = lane >> 3;   // row and matrix whose address this lane gives
             auto slice = [&](float (&d)[4], int k, uint32_t b0, uint32_t b1) {
-                if constexpr (NT == 1) {
+                if constexpr (kRegQ) {
                     mma<FMT>(d, qa[k], b0, b1);
                 } else {
 #pragma unroll
