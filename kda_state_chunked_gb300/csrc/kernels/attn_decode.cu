@@ -17,7 +17,7 @@
 // 8-bit cache: codes c become fp16 exactly (the byte under the exponent of 1024, less 1152), a
 // query row is scaled by a power of two into fp16's range, so q . c carries no rounding beyond
 // fp32 sums, and the block's key scale multiplies the score.  The value scale goes into the
-// probabilities: p (vs / ref) 2^13 in fp16, ref the largest value scale so far.  float32 queries
+// probabilities: p (vs / ref) 2^6 in fp16, ref the largest value scale so far to within a factor of two.  float32 queries
 // are split into 2 fp16 terms (3 bf16 terms over the 16-bit cache), and so are the probabilities:
 // the products then keep 22 to 24 bits.
 #include <cuda_bf16.h>
@@ -31,7 +31,8 @@ namespace {
 using namespace attn;
 
 constexpr int kWarps = 4;                             // that compute; one more walks and copies
-constexpr float kPScale = 8192.f;                     // probabilities' scale in fp16
+constexpr float kPScale = 64.f;                       // probabilities' scale in fp16
+constexpr float kGrow = 8.f;                          // bits that a row's maximum may grow before O is rescaled
 constexpr float kMinRef = 0x1p-100f;
 
 template <int FMT, int D>
@@ -42,8 +43,8 @@ struct Shape {
     static constexpr int tile = groups * group;
     static constexpr int part = 2 * tile + 128;       // a warp's keys, values, 16 bytes of scales a group
     static constexpr int stage = kWarps * part;
-    static constexpr int stages = D == 128 ? 2 : 4;        // of the ring, two CTAs an SM
-    static constexpr int deep_stages = D == 128 ? 5 : 8;   // one CTA an SM
+    static constexpr int stages = D == 128 ? 3 : 6;        // of the ring, two CTAs an SM
+    static constexpr int deep_stages = D == 128 ? 6 : 8;   // one CTA an SM
 };
 
 // A unit of work.
@@ -56,8 +57,8 @@ struct Job {
 template <int FMT, int D, int NT>
 struct Smem {
     // behind the ring
-    static constexpr int o_acc = 0;                                      // [kWarps][16][D] fp32
-    static constexpr int o_ml = o_acc + kWarps * 16 * D * 4;             // [2][kWarps][16][2] fp32
+    static constexpr int o_acc = 0;                                      // [kWarps][4][D] fp32
+    static constexpr int o_ml = o_acc + kWarps * 4 * D * 4;             // [2][kWarps][16][2] fp32
     static constexpr int o_q = o_ml + 2 * kWarps * 16 * 8;               // fragments of the queries
     static constexpr int o_qs = o_q + NT * (D / 16) * 512;               // [16] row factors
     static constexpr int o_job = o_qs + 64;
@@ -196,7 +197,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
     constexpr bool kRegQ = NT == 1 && !(FMT == KDA_KV_BF16 && D == 128);
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = ptx::smem_align1024(smem_raw);
-    const int stages = a.deep ? S::deep_stages : S::stages;
+    const int stages = a.deep ? S::deep_stages : S::stages - (NT > 1);
     uint8_t *sm = ring + stages * S::stage;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane >> 2, t = lane & 3;
     uint64_t *full = reinterpret_cast<uint64_t *>(sm + M::o_bar), *empty = full + S::deep_stages;
@@ -329,6 +330,13 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
     uint32_t *qfrag = reinterpret_cast<uint32_t *>(sm + M::o_q);
     float *qs = reinterpret_cast<float *>(sm + M::o_qs);
     auto meet = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory"); };
+    // Where a lane's addresses for the fragment loads lie in a part: key row mr of unit mm, value row
+    // 8 (mm % 2) + mr of unit mm / 2; other units are an exclusive-or away, other rows a sum.
+    const int mr = lane & 7, mm = lane >> 3;
+    const uint32_t k_at = kv_tile_off<S::row>(S::step, mr, 16 * mm);
+    const uint32_t v_at = S::tile + kv_tile_off<S::row>(S::step, 8 * (mm & 1) + mr, 16 * (mm >> 1));
+    constexpr uint32_t kLine = S::row < 128 ? S::row : 128;
+    auto unit = [](uint32_t at, int u) { return (at ^ (u & 7) << 4) + (u >> 3) * S::step * 128; };   // u even or a multiple of 4
     int stage = 0;
     uint32_t phase = 0;
     uint32_t qa[kRegQ ? kKs : 1][4];
@@ -373,7 +381,10 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
                     }
                 }
             }
-            float f = a.scale * kLog2e;
+            const float sign = a.scale < 0.f ? -1.f : 1.f;   // goes to the query: factors are positive
+            float f = fmaxf(a.scale * sign * kLog2e, 1e-30f);
+#pragma unroll
+            for (int i = 0; i < kCols; ++i) x[i] *= sign;
             if (FMT == KDA_KV_I8) {
                 // a power of two that brings the row's largest magnitude to [2^10, 2^11)
                 float top = 0.f;
@@ -422,19 +433,22 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
             const uint8_t *buf = ring + stage * S::stage + warp * S::part;
             uint32_t kb = ptx::smem_u32(buf);
             asm volatile("" : "+r"(kb)::"memory");
-            const uint32_t vb = kb + S::tile;
-            float sc[kGr][2], vs[kGr];   // a group's score factors (by row half) and value scale
+            float sc[kGr][2], vs[kGr];   // a group's score factors (by row half, all > 0) and value scale
+            bool strange = false;        // a scale that is no number: what a row does not see must stay 0
 #pragma unroll
             for (int y = 0; y < kGr; ++y) {
                 sc[y][0] = rs[0], sc[y][1] = rs[1], vs[y] = 0.f;
                 if (FMT == KDA_KV_I8) {
                     const float2 f = *reinterpret_cast<const float2 *>(buf + 2 * S::tile + 16 * y);
-                    if (there >> y & 1u) sc[y][0] *= fabsf(f.x), sc[y][1] *= fabsf(f.x), vs[y] = fabsf(f.y);
+                    if (there >> y & 1u) {
+                        const float ks = f.x == 0.f ? 1e-30f : fabsf(f.x);   // 0: the codes are 0, too
+                        sc[y][0] *= ks, sc[y][1] *= ks, vs[y] = fabsf(f.y);
+                        strange |= !(ks < INFINITY && vs[y] < INFINITY);
+                    }
                 }
             }
             // ---- scores: c[n] of tokens j0 + 8 n ..
             float c[2 * kGr][4] = {};
-            const int mr = lane & 7, mm = lane >> 3;   // row and matrix whose address this lane gives
             auto slice = [&](float (&d)[4], int k, uint32_t b0, uint32_t b1) {
                 if constexpr (kRegQ) {
                     mma<FMT>(d, qa[k], b0, b1);
@@ -453,7 +467,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
 #pragma unroll
                     for (int n = 0; n < 2 * kGr; ++n) {
                         uint32_t w[4];
-                        ldsm4(w, kb + kv_tile_off<S::row>(S::step, 8 * n + mr, 16 * (4 * i + mm)));
+                        ldsm4(w, kb + unit(k_at, 4 * i) + n * 8 * kLine);
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             const uint32_t b = w[k] ^ 0x80808080u;
@@ -466,18 +480,13 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
 #pragma unroll
                     for (int n = 0; n < 2 * kGr; ++n) {
                         uint32_t w[4];
-                        ldsm4(w, kb + kv_tile_off<S::row>(S::step, 8 * n + mr, 16 * (4 * i + mm)));
+                        ldsm4(w, kb + unit(k_at, 4 * i) + n * 8 * kLine);
 #pragma unroll
                         for (int k = 0; k < 2; ++k) slice(c[n], 2 * i + k, w[2 * k], w[2 * k + 1]);
                     }
             }
             // ---- softmax: element (n, e) is row g + 8 (e / 2), token j0 + 8 n + 2 t + e % 2
             const bool whole = there == (1u << kGr) - 1u && (jb.whole >> warp & 1u);
-            float top[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-            for (int n = 0; n < 2 * kGr; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) c[n][e] *= sc[n >> 1][e >> 1];
             if (!whole)   // rows not in use may see what they like
 #pragma unroll
                 for (int n = 0; n < 2 * kGr; ++n)
@@ -485,24 +494,25 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
                     for (int e = 0; e < 4; ++e)
                         if (!(there >> (n >> 1) & 1u) || !sees(a, pos[e >> 1], j0 + 8 * n + 2 * t + (e & 1)))
                             c[n][e] = -INFINITY;
+            // m lags: it only follows a row's maximum when that has grown by more than 2^8, which this
+            // lane's own scores tell well enough; so do ref and the value scales, by a factor of two.
+            float top[2] = {-INFINITY, -INFINITY}, vmax = 0.f;
 #pragma unroll
-            for (int n = 0; n < 2 * kGr; ++n)
+            for (int y = 0; y < kGr; ++y) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) top[e >> 1] = fmaxf(top[e >> 1], c[n][e]);
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                top[r] = fmaxf(top[r], __shfl_xor_sync(0xFFFFFFFFu, top[r], 1));
-                top[r] = fmaxf(top[r], __shfl_xor_sync(0xFFFFFFFFu, top[r], 2));
+                for (int r = 0; r < 2; ++r) {
+                    const float x = fmaxf(fmaxf(c[2 * y][2 * r], c[2 * y][2 * r + 1]), fmaxf(c[2 * y + 1][2 * r], c[2 * y + 1][2 * r + 1]));
+                    top[r] = fmaxf(top[r], x * sc[y][r]);
+                }
+                if (FMT == KDA_KV_I8 && vs[y] < INFINITY) vmax = fmaxf(vmax, vs[y]);
             }
-            float vmax = 0.f;
-            if (FMT == KDA_KV_I8)
-#pragma unroll
-                for (int y = 0; y < kGr; ++y) vmax = vs[y] < INFINITY ? fmaxf(vmax, vs[y]) : vmax;
-            const bool scaled = FMT == KDA_KV_I8 && vmax > ref;
-            if (__any_sync(0xFFFFFFFFu, top[0] > m[0] || top[1] > m[1] || scaled)) {
+            const bool scaled = FMT == KDA_KV_I8 && vmax > 2.f * ref;
+            if (__any_sync(0xFFFFFFFFu, top[0] > m[0] + kGrow || top[1] > m[1] + kGrow || scaled)) {
                 float f[2];
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
+                    top[r] = fmaxf(top[r], __shfl_xor_sync(0xFFFFFFFFu, top[r], 1));
+                    top[r] = fmaxf(top[r], __shfl_xor_sync(0xFFFFFFFFu, top[r], 2));
                     const float mn = fmaxf(m[r], top[r]);
                     f[r] = mn == -INFINITY ? 1.f : ex2(m[r] - mn);
                     l[r] *= f[r];
@@ -518,34 +528,21 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
                 for (int j = 0; j < kNt; ++j) o[j][0] *= f[0], o[j][1] *= f[0], o[j][2] *= f[1], o[j][3] *= f[1];
             }
             const float mx[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
-            bool strange = false;   // a value scale that is no number: 0 times it must stay 0
-            float pv[kGr];          // what a group's probabilities are multiplied by before rounding
-#pragma unroll
-            for (int y = 0; y < kGr; ++y) {
-                pv[y] = 1.f;
-                if (FMT == KDA_KV_I8) {
-                    pv[y] = vs[y] * inv_ref;
-                    if (!(vs[y] < INFINITY)) strange = true, pv[y] = NAN;
-                }
-            }
             uint32_t pa[kGr][4][NT];
 #pragma unroll
             for (int n = 0; n < 2 * kGr; ++n) {
+                // probabilities, and what of them is rounded: 8-bit, p vs / ref 2^6
+                const float pv = FMT == KDA_KV_I8 ? (vs[n >> 1] < INFINITY ? vs[n >> 1] * inv_ref : NAN) : 1.f;
+                float p[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    c[n][e] = ex2(c[n][e] - mx[e >> 1]);
-                    l[e >> 1] += c[n][e];
+                    p[e] = ex2(fmaf(c[n][e], sc[n >> 1][e >> 1], -mx[e >> 1]));
+                    if (FMT == KDA_KV_I8 && strange && c[n][e] == -INFINITY) p[e] = 0.f;
+                    l[e >> 1] += p[e];
+                    if (FMT == KDA_KV_I8) p[e] = strange && p[e] == 0.f ? 0.f : p[e] * pv;
                 }
-                if (FMT == KDA_KV_I8) {
-                    if (strange)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) c[n][e] = c[n][e] == 0.f ? 0.f : c[n][e] * pv[n >> 1];
-                    else
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) c[n][e] *= pv[n >> 1];
-                }
-                split2<FMT, NT>(c[n][0], c[n][1], pa[n >> 1][2 * (n & 1)]);
-                split2<FMT, NT>(c[n][2], c[n][3], pa[n >> 1][2 * (n & 1) + 1]);
+                split2<FMT, NT>(p[0], p[1], pa[n >> 1][2 * (n & 1)]);
+                split2<FMT, NT>(p[2], p[3], pa[n >> 1][2 * (n & 1) + 1]);
             }
             // ---- values
             auto values = [&]() {
@@ -554,7 +551,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
 #pragma unroll
                     for (int i = 0; i < S::row / 32; ++i) {
                         uint32_t w[4];   // (tokens 0-7, 8-15) of 16-byte units 2 i and 2 i + 1
-                        ldsm4t(w, vb + kv_tile_off<S::row>(S::step, 16 * y + 8 * (mm & 1) + mr, 16 * (2 * i + (mm >> 1))));
+                        ldsm4t(w, kb + unit(v_at, 2 * i) + y * 16 * kLine);
 #pragma unroll
                         for (int x = 0; x < 2; ++x) {
                             if constexpr (FMT == KDA_KV_I8) {
@@ -608,7 +605,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
 #pragma unroll
                     for (int i = 0; i < kNt; ++i) {
                         uint32_t w[4];
-                        ldsm4t(w, vb + kv_tile_off<S::row>(S::step, 8 * (mm & 1) + mr, 16 * i));
+                        ldsm4t(w, kb + S::tile + kv_tile_off<S::row>(S::step, 8 * (mm & 1) + mr, 16 * i));
                         float d[4] = {};
 #pragma unroll
                         for (int z = NT - 1; z >= 0; --z) {
@@ -639,57 +636,66 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
             }
         }
         meet();
+        // four rows at a time, so that the ring has the room
+        const bool starts = flags & kStarts, ends = flags & kEnds;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-            const int row = g + 8 * r;
-            if (row >= nrows) continue;
+            const int my_row = g + 8 * r;
             float mt = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < kWarps; ++i) mt = fmaxf(mt, ml[(i * 16 + row) * 2]);
-            float f = mt == -INFINITY ? 1.f : exp2f(m[r] - mt);
+            for (int i = 0; i < kWarps; ++i) mt = fmaxf(mt, ml[(i * 16 + my_row) * 2]);
+            float f = mt == -INFINITY ? 1.f : ex2(m[r] - mt);
             if (FMT == KDA_KV_I8) f *= ref * (1.f / kPScale);
-            float *dst = acc + (warp * 16 + row) * D;
-            if constexpr (FMT == KDA_KV_I8) {
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+                const int base = 8 * r + 4 * half;
+                if (base >= nrows) break;
+                if (g >> 2 == half) {
+                    float *dst = acc + (warp * 4 + (my_row & 3)) * D;
+                    if constexpr (FMT == KDA_KV_I8) {
 #pragma unroll
-                for (int i = 0; i < kNt / 2; ++i)   // columns 16 i + 4 t ..: even and odd ones from two tiles
-                    *reinterpret_cast<float4 *>(dst + 4 * acc_unit<FMT, D>(row, 4 * i + t)) =
-                        make_float4(o[2 * i][2 * r] * f, o[2 * i + 1][2 * r] * f, o[2 * i][2 * r + 1] * f,
-                                    o[2 * i + 1][2 * r + 1] * f);
-            } else {
+                        for (int i = 0; i < kNt / 2; ++i)   // columns 16 i + 4 t ..: even and odd ones from two tiles
+                            *reinterpret_cast<float4 *>(dst + 4 * acc_unit<FMT, D>(my_row, 4 * i + t)) =
+                                make_float4(o[2 * i][2 * r] * f, o[2 * i + 1][2 * r] * f, o[2 * i][2 * r + 1] * f,
+                                            o[2 * i + 1][2 * r + 1] * f);
+                    } else {
 #pragma unroll
-                for (int j = 0; j < kNt; ++j)
-                    *reinterpret_cast<float2 *>(dst + 4 * acc_unit<FMT, D>(row, 2 * j + (t >> 1)) + 2 * (t & 1)) =
-                        make_float2(o[j][2 * r] * f, o[j][2 * r + 1] * f);
-            }
-        }
-        meet();
-        const bool starts = flags & kStarts, ends = flags & kEnds;
-        const int part_slot = starts ? 1 : 0;
-        for (int i = tid; i < nrows * (D / 4); i += kWarps * 32) {
-            const int row = i / (D / 4), unit = i % (D / 4);
-            float mt = -INFINITY, lt = 0.f;
+                        for (int j = 0; j < kNt; ++j)
+                            *reinterpret_cast<float2 *>(dst + 4 * acc_unit<FMT, D>(my_row, 2 * j + (t >> 1)) + 2 * (t & 1)) =
+                                make_float2(o[j][2 * r] * f, o[j][2 * r + 1] * f);
+                    }
+                }
+                meet();
+                // a thread sums 4 columns of a row: D / 4 threads a row
+                const int sum_row = base + tid / (D / 4), unit4 = tid % (D / 4);
+                if (sum_row < min(nrows, base + 4)) {
+                    float top = -INFINITY, lt = 0.f;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) mt = fmaxf(mt, ml[(w * 16 + row) * 2]);
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[(w * 16 + sum_row) * 2]);
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float lw = ml[(w * 16 + row) * 2 + 1];
-                lt += mt == -INFINITY ? lw : lw * exp2f(ml[(w * 16 + row) * 2] - mt);
-                const float4 x = *reinterpret_cast<const float4 *>(acc + (w * 16 + row) * D + 4 * acc_unit<FMT, D>(row, unit));
-                v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
-            }
-            if (starts && ends) {
-                const int at_row = row0 + row;
-                const int64_t at = (int64_t)(tok0 + at_row / a.G) * a.Hq + head * a.G + at_row % a.G;
-                const float inv = 1.f / lt;
-                if (lt == 0.f) v = make_float4(0.f, 0.f, 0.f, 0.f);
-                else v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
-                store_row4(a.o, a.dtype, at * D + 4 * unit, v);
-                if (a.lse && unit == 0) a.lse[at] = lse_of(mt, lt);
-            } else {
-                float *dst = a.part + ((int64_t)(blockIdx.x * 2 + part_slot) * 16 + row) * kPartRow<D>;
-                *reinterpret_cast<float4 *>(dst + 4 * unit) = v;
-                if (unit == 0) dst[D] = mt, dst[D + 1] = lt;
+                    for (int w = 0; w < kWarps; ++w) {
+                        const float lw = ml[(w * 16 + sum_row) * 2 + 1];
+                        lt += top == -INFINITY ? lw : lw * ex2(ml[(w * 16 + sum_row) * 2] - top);
+                        const float4 x = *reinterpret_cast<const float4 *>(acc + (w * 4 + (sum_row & 3)) * D +
+                                                                           4 * acc_unit<FMT, D>(sum_row, unit4));
+                        v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+                    }
+                    if (starts && ends) {
+                        const int at_row = row0 + sum_row;
+                        const int64_t at = (int64_t)(tok0 + at_row / a.G) * a.Hq + head * a.G + at_row % a.G;
+                        const float inv = 1.f / lt;
+                        if (lt == 0.f) v = make_float4(0.f, 0.f, 0.f, 0.f);
+                        else v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;
+                        store_row4(a.o, a.dtype, at * D + 4 * unit4, v);
+                        if (a.lse && unit4 == 0) a.lse[at] = lse_of(top, lt);
+                    } else {
+                        float *dst = a.part + ((int64_t)(blockIdx.x * 2 + (starts ? 1 : 0)) * 16 + sum_row) * kPartRow<D>;
+                        *reinterpret_cast<float4 *>(dst + 4 * unit4) = v;
+                        if (unit4 == 0) dst[D] = top, dst[D + 1] = lt;
+                    }
+                }
+                if (base + 4 < nrows) meet();
             }
         }
         ml += ml_next;
@@ -701,8 +707,9 @@ template <int FMT, int D, int NT>
 cudaError_t run(const AttnArgs &a, cudaStream_t st) {
     using M = Smem<FMT, D, NT>;
     static_assert(M::total(Shape<FMT, D>::deep_stages) + 1024 <= 227 * 1024, "shared memory");
-    static_assert(M::total(Shape<FMT, D>::stages) <= 113 * 1024, "two CTAs an SM");
-    const int smem = M::total(a.deep ? Shape<FMT, D>::deep_stages : Shape<FMT, D>::stages) + 1024;
+    // (the split terms of float32 queries leave room for one stage less beside another CTA)
+    static_assert(NT > 1 || 2 * (M::total(Shape<FMT, D>::stages) + 2048) <= 228 * 1024, "two CTAs an SM");
+    const int smem = M::total(a.deep ? Shape<FMT, D>::deep_stages : Shape<FMT, D>::stages - (NT > 1)) + 1024;
     auto kern = attn_decode_kernel<FMT, D, NT>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
