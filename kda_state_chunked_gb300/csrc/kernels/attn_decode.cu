@@ -38,11 +38,10 @@ constexpr float kMinRef = 0x1p-100f;
 template <int FMT, int D>
 struct Shape {
     static constexpr int row = kKvRow<FMT, D>;
+    static constexpr int line = row < 128 ? row : 128, blocks = row / line;
     static constexpr int step = FMT == KDA_KV_I8 ? 32 : 16, groups = step / 16, unit = kWarps * step;
-    static constexpr int group = row * 16;            // K or V bytes of 16 tokens
-    static constexpr int tile = groups * group;
-    static constexpr int part = 2 * tile + 128;       // a warp's keys, values, 16 bytes of scales a group
-    static constexpr int stage = kWarps * part;
+    static constexpr int tile = row * unit;           // keys or values of a unit, by line block as in a page
+    static constexpr int stage = 2 * tile + 128;      // and 16 bytes of scales for each 16 tokens
     static constexpr int stages = D == 128 ? 3 : 6;        // of the ring, two CTAs an SM
     static constexpr int deep_stages = D == 128 ? 6 : 8;   // one CTA an SM
 };
@@ -51,7 +50,8 @@ struct Shape {
 struct Job {
     int32_t j0, flags, base, row0, nrows, tok0, head;   // first token; the row tile
     uint32_t live, whole;                               // groups that are there; warps whose rows see all of theirs
-    int32_t pmin, pmax, pad;
+    uint32_t lead;                                      // 4 bits a group: the group that its scales came with
+    int32_t pmin, pmax;
 };
 
 template <int FMT, int D, int NT>
@@ -272,6 +272,15 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
                 const bool want = __shfl_sync(0xFFFFFFFFu, (int)now.want, from) && lane < kGroups;
                 const uint8_t *rec = want ? kv_record(a.kv, page, w.h) : nullptr;
                 const uint32_t live = __ballot_sync(0xFFFFFFFFu, rec != nullptr);
+                // A page's groups that follow one another go in one copy, which the first of them starts: a
+                // copy costs some 100 cycles to start, whatever its size.
+                const bool leads = rec && (lane == 0 || slot == 0 || !(live >> (lane - 1) & 1u));
+                const uint32_t leaders = __ballot_sync(0xFFFFFFFFu, leads);
+                const int first = 31 - __clz(leaders & (2u << lane) - 1u | 1u);   // this group's leader
+                const uint32_t stop = (leaders | ~live) & ~((2u << lane) - 1u) | 1u << kGroups;
+                const uint32_t run = __ffs(stop) - 1 - lane;                      // a leader's groups
+                uint32_t lead = lane < kGroups ? (uint32_t)first << (4 * lane) : 0u;
+                lead = __reduce_or_sync(0xFFFFFFFFu, lead);
                 const uint32_t whole = __ballot_sync(0xFFFFFFFFu, lane < kWarps && all_see(a, x, j0 + lane * S::step, S::step));
                 if (lane == 0) {
                     Job &jb = jobs[stage];
@@ -281,7 +290,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
                                (u_first == 0 ? kStarts : 0) | (ends ? kEnds : 0);
                     jb.base = x.q.len - x.q.n;
                     jb.row0 = x.row0, jb.nrows = x.nrows, jb.tok0 = x.q.tok0, jb.head = w.h;
-                    jb.live = live, jb.whole = whole;
+                    jb.live = live, jb.whole = whole, jb.lead = lead;
                     jb.pmin = x.pmin, jb.pmax = x.pmax;
                     if (u_first == 0 && !ends && left == 1) {
                         AttnSplit sp{};
@@ -292,23 +301,20 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
                         sp.nrows = x.nrows;
                         a.split[blockIdx.x] = sp;
                     }
-                    ptx::mbar_arrive_expect_tx(&full[stage], __popc(live) * (2 * S::group + (FMT == KDA_KV_I8 ? 16 : 0)));
+                    ptx::mbar_arrive_expect_tx(&full[stage], __popc(live) * 2 * 16 * S::row + (FMT == KDA_KV_I8 ? __popc(leaders) * 16 : 0));
                 }
                 __syncwarp();
-                if (rec) {
-                    // 16 tokens' lines follow one another in the page; a warp's part has them by line block, too
-                    constexpr uint32_t kLine = S::row < 128 ? S::row : 128, kRun = kLine * 16;
-                    uint8_t *dst = ring + stage * S::stage + lane / kGr * S::part + lane % kGr * kRun;
-                    const uint8_t *src = rec + slot * kLine;
+                if (leads) {
+                    uint8_t *dst = ring + stage * S::stage + lane * 16 * S::line;
+                    const uint8_t *src = rec + slot * S::line;
 #pragma unroll
                     for (int v = 0; v < 2; ++v)
 #pragma unroll
-                        for (int b = 0; b < S::group / (int)kRun; ++b)
-                            ptx::bulk_load(dst + v * S::tile + b * kGr * kRun, src + v * pt * S::row + b * pt * 128, kRun,
-                                           &full[stage]);
+                        for (int b = 0; b < S::blocks; ++b)
+                            ptx::bulk_load(dst + v * S::tile + b * S::unit * S::line, src + v * pt * S::row + b * pt * S::line,
+                                           run * 16 * S::line, &full[stage]);
                     if (FMT == KDA_KV_I8)
-                        ptx::bulk_load(ring + stage * S::stage + lane / kGr * S::part + 2 * S::tile + 16 * (lane % kGr),
-                                       rec + 2 * pt * S::row, 16, &full[stage]);
+                        ptx::bulk_load(ring + stage * S::stage + 2 * S::tile + 16 * lane, rec + 2 * pt * S::row, 16, &full[stage]);
                 }
                 if (++stage == stages) stage = 0, phase ^= 1;
             }
@@ -333,10 +339,10 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
     // Where a lane's addresses for the fragment loads lie in a part: key row mr of unit mm, value row
     // 8 (mm % 2) + mr of unit mm / 2; other units are an exclusive-or away, other rows a sum.
     const int mr = lane & 7, mm = lane >> 3;
-    const uint32_t k_at = kv_tile_off<S::row>(S::step, mr, 16 * mm);
-    const uint32_t v_at = S::tile + kv_tile_off<S::row>(S::step, 8 * (mm & 1) + mr, 16 * (mm >> 1));
-    constexpr uint32_t kLine = S::row < 128 ? S::row : 128;
-    auto unit = [](uint32_t at, int u) { return (at ^ (u & 7) << 4) + (u >> 3) * S::step * 128; };   // u even or a multiple of 4
+    const uint32_t k_at = kv_tile_off<S::row>(S::unit, warp * S::step + mr, 16 * mm);
+    const uint32_t v_at = S::tile + kv_tile_off<S::row>(S::unit, warp * S::step + 8 * (mm & 1) + mr, 16 * (mm >> 1));
+    constexpr uint32_t kLine = S::line;
+    auto unit = [](uint32_t at, int u) { return (at ^ (u & 7) << 4) + (u >> 3) * S::unit * 128; };   // u even or a multiple of 4
     int stage = 0;
     uint32_t phase = 0;
     uint32_t qa[kRegQ ? kKs : 1][4];
@@ -430,7 +436,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
         const uint32_t there = jb.live >> (warp * kGr) & ((1u << kGr) - 1u);
         if (there) {
             const int32_t j0 = jb.j0 + warp * S::step;
-            const uint8_t *buf = ring + stage * S::stage + warp * S::part;
+            const uint8_t *buf = ring + stage * S::stage;
             uint32_t kb = ptx::smem_u32(buf);
             asm volatile("" : "+r"(kb)::"memory");
             float sc[kGr][2], vs[kGr];   // a group's score factors (by row half, all > 0) and value scale
@@ -439,7 +445,8 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
             for (int y = 0; y < kGr; ++y) {
                 sc[y][0] = rs[0], sc[y][1] = rs[1], vs[y] = 0.f;
                 if (FMT == KDA_KV_I8) {
-                    const float2 f = *reinterpret_cast<const float2 *>(buf + 2 * S::tile + 16 * y);
+                    const float2 f = *reinterpret_cast<const float2 *>(buf + 2 * S::tile +
+                                                                       16 * (jb.lead >> (4 * (warp * kGr + y)) & 15u));
                     if (there >> y & 1u) {
                         const float ks = f.x == 0.f ? 1e-30f : fabsf(f.x);   // 0: the codes are 0, too
                         sc[y][0] *= ks, sc[y][1] *= ks, vs[y] = fabsf(f.y);
@@ -461,29 +468,26 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
                     }
                 }
             };
-            if constexpr (FMT == KDA_KV_I8) {
+            // a slice of every tile in turn, so that products that follow one another add to different sums
 #pragma unroll
-                for (int i = 0; i < kKs / 4; ++i)
+            for (int i = 0; i < S::row / 64; ++i) {
+                uint32_t w[2 * kGr][4];   // 16-byte units 4 i .. of each tile's keys
 #pragma unroll
-                    for (int n = 0; n < 2 * kGr; ++n) {
-                        uint32_t w[4];
-                        ldsm4(w, kb + unit(k_at, 4 * i) + n * 8 * kLine);
+                for (int n = 0; n < 2 * kGr; ++n) ldsm4(w[n], kb + unit(k_at, 4 * i) + n * 8 * kLine);
+                if constexpr (FMT == KDA_KV_I8) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const uint32_t b = w[k] ^ 0x80808080u;
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int n = 0; n < 2 * kGr; ++n) {
+                            const uint32_t b = w[n][k] ^ 0x80808080u;
                             slice(c[n], 4 * i + k, half2_of<0x4140>(b), half2_of<0x4342>(b));
                         }
-                    }
-            } else {
+                } else {
 #pragma unroll
-                for (int i = 0; i < kKs / 2; ++i)
+                    for (int k = 0; k < 2; ++k)
 #pragma unroll
-                    for (int n = 0; n < 2 * kGr; ++n) {
-                        uint32_t w[4];
-                        ldsm4(w, kb + unit(k_at, 4 * i) + n * 8 * kLine);
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) slice(c[n], 2 * i + k, w[2 * k], w[2 * k + 1]);
-                    }
+                        for (int n = 0; n < 2 * kGr; ++n) slice(c[n], 2 * i + k, w[n][2 * k], w[n][2 * k + 1]);
+                }
             }
             // ---- softmax: element (n, e) is row g + 8 (e / 2), token j0 + 8 n + 2 t + e % 2
             const bool whole = there == (1u << kGr) - 1u && (jb.whole >> warp & 1u);
@@ -582,8 +586,10 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
                 // Where a step is not seen whole, look for such a value first.
                 if (!whole) {
                     uint32_t bad = 0;
-                    for (int i = lane; i < S::tile / 16; i += 32) {
-                        const uint4 x = *reinterpret_cast<const uint4 *>(buf + S::tile + 16 * i);
+                    for (int i = lane; i < S::step * S::blocks * 8; i += 32) {   // 16-byte units of the warp's rows
+                        const int b = i / (S::step * 8);
+                        const uint4 x = *reinterpret_cast<const uint4 *>(buf + S::tile + b * S::unit * 128 + warp * S::step * 128 +
+                                                                         16 * (i % (S::step * 8)));
                         for (uint32_t y : {x.x, x.y, x.z, x.w})
                             bad |= (uint32_t)((y & 0x7F80u) == 0x7F80u) | (uint32_t)((y & 0x7F800000u) == 0x7F800000u);
                     }
@@ -605,7 +611,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
 #pragma unroll
                     for (int i = 0; i < kNt; ++i) {
                         uint32_t w[4];
-                        ldsm4t(w, kb + S::tile + kv_tile_off<S::row>(S::step, 8 * (mm & 1) + mr, 16 * i));
+                        ldsm4t(w, kb + S::tile + kv_tile_off<S::row>(S::unit, warp * S::step + 8 * (mm & 1) + mr, 16 * i));
                         float d[4] = {};
 #pragma unroll
                         for (int z = NT - 1; z >= 0; --z) {
