@@ -3,9 +3,12 @@
 //   o_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = exp(scale q_i . k_j - m_i), j over the visible tokens
 //
 // in one pass over the cache with a running maximum and sum per row.  Bound: the cache's bytes.
-// The rows of a group (query heads that share a key/value head, times the call's tokens) fill the
-// M = 16 of a warp-level matrix product, so a cached byte is read once for all of them; wider
-// tensor-memory tiles would stand empty here.
+// The rows of a group (query heads that share a key/value head, times the call's tokens) are the
+// N = 8 of a warp-level matrix product (twice, for up to 16 rows), tokens and columns its M = 16:
+//   S^T = K Q^T,  O^T += V^T P^T
+// so a cached byte is read once for all rows; wider tensor-memory tiles would stand empty here.  With
+// the rows as M, eight of them left half of every product empty, and 64 products a step at 11
+// cycles each (measured, saturated) took half of the time that the bytes take.
 //
 // Two CTAs an SM, so that one streams while the other joins its warps or starts an item.  A fifth
 // warp walks the list of units and copies them into a ring of stages (bulk copies: 16 tokens lie in
@@ -54,13 +57,13 @@ struct Job {
     int32_t pmin, pmax;
 };
 
-template <int FMT, int D, int NT>
+template <int FMT, int D, int NT, int NR>
 struct Smem {
     // behind the ring
     static constexpr int o_acc = 0;                                      // [kWarps][4][D] fp32
     static constexpr int o_ml = o_acc + kWarps * 4 * D * 4;             // [2][kWarps][16][2] fp32
     static constexpr int o_q = o_ml + 2 * kWarps * 16 * 8;               // fragments of the queries
-    static constexpr int o_qs = o_q + NT * (D / 16) * 512;               // [16] row factors
+    static constexpr int o_qs = o_q + NT * NR * (D / 16) * 256;          // [16] row factors
     static constexpr int o_job = o_qs + 64;
     static constexpr int o_bar = o_job + Shape<FMT, D>::deep_stages * (int)sizeof(Job);   // full, empty
     static constexpr int o_err = o_bar + 2 * Shape<FMT, D>::deep_stages * 8;
@@ -129,11 +132,15 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t (&out)[NT]) {
     }
 }
 
-// Place of the 4-float unit u of a row of the warps' accumulators in shared memory, so that the
-// fragment stores of a warp fall into different banks.
-template <int FMT, int D>
-__device__ __forceinline__ int acc_unit(int row, int u) {
-    return FMT == KDA_KV_BF16 ? u ^ ((row & 7) << 1) : u ^ ((row & 1) << 2);
+// Place of the 4-float unit u of a row of the warps' accumulators in shared memory: a warp stores 64
+// bytes of four pairs of rows at a time, which so fall into different banks.
+__device__ __forceinline__ int acc_unit(int row, int u) { return u ^ (row >> 1 & 3) << 2; }
+
+// The transpose of an 8 x 8 tile of 16-bit values, held as a product's fragment.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
 }
 
 // The share of this CTA (left = 0: none), found by one warp: the units of all sequences summed, then
@@ -186,15 +193,15 @@ __device__ __forceinline__ Walk find_share(const AttnArgs &a, int lane, int64_t 
     return w;
 }
 
-template <int FMT, int D, int NT>
+// NT: terms of a split operand; NR: tiles of eight rows.
+template <int FMT, int D, int NT, int NR>
 __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const __grid_constant__ AttnArgs a) {
     using S = Shape<FMT, D>;
-    using M = Smem<FMT, D, NT>;
+    using M = Smem<FMT, D, NT, NR>;
     constexpr int kKs = D / 16;   // 16-wide slices of a row
-    constexpr int kNt = D / 8;    // 8-wide output tiles
+    constexpr int kDt = D / 16;   // 16-column output tiles
     constexpr int kGr = S::groups;
-    // query fragments stay in registers where the accumulators leave room for them
-    constexpr bool kRegQ = NT == 1 && !(FMT == KDA_KV_BF16 && D == 128);
+    constexpr bool kRegQ = NT == 1;   // query fragments stay in registers
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = ptx::smem_align1024(smem_raw);
     const int stages = a.deep ? S::deep_stages : S::stages - (NT > 1);
@@ -336,19 +343,22 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
     uint32_t *qfrag = reinterpret_cast<uint32_t *>(sm + M::o_q);
     float *qs = reinterpret_cast<float *>(sm + M::o_qs);
     auto meet = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory"); };
-    // Where a lane's addresses for the fragment loads lie in a part: key row mr of unit mm, value row
-    // 8 (mm % 2) + mr of unit mm / 2; other units are an exclusive-or away, other rows a sum.
+    // Where a lane's addresses for the fragment loads lie in a stage.  Row mr of matrix mm: for the keys
+    // of the 8-bit cache, tokens 8 (mm % 2) + mr and unit mm / 2 (two slices); of the 16-bit one, the
+    // same (a slice is two units); for its values, tokens 8 (mm / 2) + mr and unit mm % 2; for those of
+    // the 8-bit cache, tokens 8 (mm % 2) + mr and unit mm / 2.  Other units are an exclusive-or away.
     const int mr = lane & 7, mm = lane >> 3;
-    const uint32_t k_at = kv_tile_off<S::row>(S::unit, warp * S::step + mr, 16 * mm);
-    const uint32_t v_at = S::tile + kv_tile_off<S::row>(S::unit, warp * S::step + 8 * (mm & 1) + mr, 16 * (mm >> 1));
+    const uint32_t k_at = kv_tile_off<S::row>(S::unit, warp * S::step + 8 * (mm & 1) + mr, 16 * (mm >> 1));
+    const uint32_t v_at = S::tile + (FMT == KDA_KV_I8 ? k_at : kv_tile_off<S::row>(S::unit, warp * S::step + 8 * (mm >> 1) + mr, 16 * (mm & 1)));
     constexpr uint32_t kLine = S::line;
     auto unit = [](uint32_t at, int u) { return (at ^ (u & 7) << 4) + (u >> 3) * S::unit * 128; };   // u even or a multiple of 4
     int stage = 0;
     uint32_t phase = 0;
-    uint32_t qa[kRegQ ? kKs : 1][4];
-    float rs[2] = {0.f, 0.f};
-    int32_t pos[2] = {-1, -1}, nrows = 0, row0 = 0, tok0 = 0, head = 0;   // the item
-    float o[kNt][4], m[2], l[2], ref = 0.f, inv_ref = 0.f;   // ref: 8-bit, the largest value scale so far
+    // This lane's rows are 8 x + 2 t and the one after, x < NR.
+    uint32_t qb[kRegQ ? kKs : 1][NR][2];
+    float rs[NR][2];
+    int32_t pos[NR][2], nrows = 0, row0 = 0, tok0 = 0, head = 0;   // the item
+    float o[NR][kDt][4], m[NR][2], l[NR][2], ref = 0.f, inv_ref = 0.f;   // ref: 8-bit, the largest value scale so far
     for (;;) {
         const bool ok = __all_sync(0xFFFFFFFFu, wait_bar(&full[stage], phase, err));
         if (!ok) {
@@ -413,25 +423,32 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
                 uint32_t z[NT];
                 split2<FMT, NT>(x[i], x[i + 1], z);
 #pragma unroll
-                for (int n = 0; n < NT; ++n) qfrag[((n * kKs + k) * 32 + row % 8 * 4 + tt) * 4 + row / 8 + 2 * half] = z[n];
+                for (int n = 0; n < NT; ++n)
+                    if (row < 8 * NR) qfrag[(((n * kKs + k) * NR + row / 8) * 32 + row % 8 * 4 + tt) * 2 + half] = z[n];
             }
             meet();
             if constexpr (kRegQ) {
 #pragma unroll
-                for (int k = 0; k < kKs; ++k) {
-                    const uint4 u = *reinterpret_cast<const uint4 *>(qfrag + (k * 32 + lane) * 4);
-                    qa[k][0] = u.x, qa[k][1] = u.y, qa[k][2] = u.z, qa[k][3] = u.w;
-                }
+                for (int k = 0; k < kKs; ++k)
+#pragma unroll
+                    for (int x = 0; x < NR; ++x) {
+                        const uint2 u = *reinterpret_cast<const uint2 *>(qfrag + ((k * NR + x) * 32 + lane) * 2);
+                        qb[k][x][0] = u.x, qb[k][x][1] = u.y;
+                    }
             }
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                rs[r] = qs[g + 8 * r];
-                pos[r] = g + 8 * r < nrows ? jb.base + (row0 + g + 8 * r) / a.G : -1;
-                m[r] = -INFINITY, l[r] = 0.f;
+            for (int x = 0; x < NR; ++x) {
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const int row = 8 * x + 2 * t + r;
+                    rs[x][r] = qs[row];
+                    pos[x][r] = row < nrows ? jb.base + (row0 + row) / a.G : -1;
+                    m[x][r] = -INFINITY, l[x][r] = 0.f;
+                }
+#pragma unroll
+                for (int j = 0; j < kDt; ++j) o[x][j][0] = o[x][j][1] = o[x][j][2] = o[x][j][3] = 0.f;
             }
             ref = inv_ref = 0.f;
-#pragma unroll
-            for (int j = 0; j < kNt; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
         }
         const uint32_t there = jb.live >> (warp * kGr) & ((1u << kGr) - 1u);
         if (there) {
@@ -439,168 +456,180 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
             const uint8_t *buf = ring + stage * S::stage;
             uint32_t kb = ptx::smem_u32(buf);
             asm volatile("" : "+r"(kb)::"memory");
-            float sc[kGr][2], vs[kGr];   // a group's score factors (by row half, all > 0) and value scale
-            bool strange = false;        // a scale that is no number: what a row does not see must stay 0
+            float ks[kGr], vs[kGr];   // a group's scales; the key's goes into the score factors, which are > 0
+            bool strange = false;     // a scale that is no number: what a row does not see must stay 0
 #pragma unroll
             for (int y = 0; y < kGr; ++y) {
-                sc[y][0] = rs[0], sc[y][1] = rs[1], vs[y] = 0.f;
-                if (FMT == KDA_KV_I8) {
+                ks[y] = 1.f, vs[y] = 0.f;
+                if (FMT == KDA_KV_I8 && (there >> y & 1u)) {
                     const float2 f = *reinterpret_cast<const float2 *>(buf + 2 * S::tile +
                                                                        16 * (jb.lead >> (4 * (warp * kGr + y)) & 15u));
-                    if (there >> y & 1u) {
-                        const float ks = f.x == 0.f ? 1e-30f : fabsf(f.x);   // 0: the codes are 0, too
-                        sc[y][0] *= ks, sc[y][1] *= ks, vs[y] = fabsf(f.y);
-                        strange |= !(ks < INFINITY && vs[y] < INFINITY);
-                    }
+                    ks[y] = f.x == 0.f ? 1e-30f : fabsf(f.x);   // 0: the codes are 0, too
+                    vs[y] = fabsf(f.y);
+                    strange |= !(ks[y] < INFINITY && vs[y] < INFINITY);
                 }
             }
-            // ---- scores: c[n] of tokens j0 + 8 n ..
-            float c[2 * kGr][4] = {};
-            auto slice = [&](float (&d)[4], int k, uint32_t b0, uint32_t b1) {
-                if constexpr (kRegQ) {
-                    mma<FMT>(d, qa[k], b0, b1);
-                } else {
+            // ---- scores: c[y][x][e] is token j0 + 16 y + g + 8 (e / 2), row 8 x + 2 t + e % 2
+            float c[kGr][NR][4] = {};
+            auto slice = [&](int y, int k, const uint32_t (&af)[4]) {
 #pragma unroll
-                    for (int z = NT - 1; z >= 0; --z) {
-                        const uint4 f = *reinterpret_cast<const uint4 *>(qfrag + ((z * kKs + k) * 32 + lane) * 4);
-                        const uint32_t qf[4] = {f.x, f.y, f.z, f.w};
-                        mma<FMT>(d, qf, b0, b1);
+                for (int x = 0; x < NR; ++x) {
+                    if constexpr (kRegQ) {
+                        mma<FMT>(c[y][x], af, qb[k][x][0], qb[k][x][1]);
+                    } else {
+#pragma unroll
+                        for (int z = NT - 1; z >= 0; --z) {
+                            const uint2 f = *reinterpret_cast<const uint2 *>(qfrag + (((z * kKs + k) * NR + x) * 32 + lane) * 2);
+                            mma<FMT>(c[y][x], af, f.x, f.y);
+                        }
                     }
                 }
             };
-            // a slice of every tile in turn, so that products that follow one another add to different sums
 #pragma unroll
-            for (int i = 0; i < S::row / 64; ++i) {
-                uint32_t w[2 * kGr][4];   // 16-byte units 4 i .. of each tile's keys
+            for (int i = 0; i < S::row / 32; ++i) {
+                uint32_t w[kGr][4];   // 16-byte units 2 i and 2 i + 1 of tokens 0-7 and 8-15
 #pragma unroll
-                for (int n = 0; n < 2 * kGr; ++n) ldsm4(w[n], kb + unit(k_at, 4 * i) + n * 8 * kLine);
+                for (int y = 0; y < kGr; ++y) ldsm4(w[y], kb + unit(k_at, 2 * i) + y * 16 * kLine);
                 if constexpr (FMT == KDA_KV_I8) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-#pragma unroll
-                        for (int n = 0; n < 2 * kGr; ++n) {
-                            const uint32_t b = w[n][k] ^ 0x80808080u;
-                            slice(c[n], 4 * i + k, half2_of<0x4140>(b), half2_of<0x4342>(b));
-                        }
-                } else {
 #pragma unroll
                     for (int k = 0; k < 2; ++k)
 #pragma unroll
-                        for (int n = 0; n < 2 * kGr; ++n) slice(c[n], 2 * i + k, w[n][2 * k], w[n][2 * k + 1]);
+                        for (int y = 0; y < kGr; ++y) {
+                            const uint32_t b0 = w[y][2 * k] ^ 0x80808080u, b1 = w[y][2 * k + 1] ^ 0x80808080u;
+                            const uint32_t af[4] = {half2_of<0x4140>(b0), half2_of<0x4140>(b1), half2_of<0x4342>(b0), half2_of<0x4342>(b1)};
+                            slice(y, 2 * i + k, af);
+                        }
+                } else {
+#pragma unroll
+                    for (int y = 0; y < kGr; ++y) slice(y, i, w[y]);
                 }
             }
-            // ---- softmax: element (n, e) is row g + 8 (e / 2), token j0 + 8 n + 2 t + e % 2
+            // ---- softmax
             const bool whole = there == (1u << kGr) - 1u && (jb.whole >> warp & 1u);
             if (!whole)   // rows not in use may see what they like
 #pragma unroll
-                for (int n = 0; n < 2 * kGr; ++n)
+                for (int y = 0; y < kGr; ++y)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (!(there >> (n >> 1) & 1u) || !sees(a, pos[e >> 1], j0 + 8 * n + 2 * t + (e & 1)))
-                            c[n][e] = -INFINITY;
-            // m lags: it only follows a row's maximum when that has grown by more than 2^8, which this
-            // lane's own scores tell well enough; so do ref and the value scales, by a factor of two.
-            float top[2] = {-INFINITY, -INFINITY}, vmax = 0.f;
+                    for (int x = 0; x < NR; ++x)
 #pragma unroll
-            for (int y = 0; y < kGr; ++y) {
+                        for (int e = 0; e < 4; ++e)
+                            if (!(there >> y & 1u) || !sees(a, pos[x][e & 1], j0 + 16 * y + g + 8 * (e >> 1))) c[y][x][e] = -INFINITY;
+            // m lags: it only follows a row's maximum when that has grown by more than 2^8, which the
+            // lanes' own scores tell well enough; so do ref and the value scales, by a factor of two.
+            float top[NR][2], vmax = 0.f;
+            bool grown = false;
+#pragma unroll
+            for (int x = 0; x < NR; ++x)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    const float x = fmaxf(fmaxf(c[2 * y][2 * r], c[2 * y][2 * r + 1]), fmaxf(c[2 * y + 1][2 * r], c[2 * y + 1][2 * r + 1]));
-                    top[r] = fmaxf(top[r], x * sc[y][r]);
+                    top[x][r] = -INFINITY;
+#pragma unroll
+                    for (int y = 0; y < kGr; ++y) top[x][r] = fmaxf(top[x][r], fmaxf(c[y][x][r], c[y][x][r + 2]) * ks[y]);
+                    top[x][r] *= rs[x][r];
+                    grown |= top[x][r] > m[x][r] + kGrow;
                 }
+#pragma unroll
+            for (int y = 0; y < kGr; ++y)
                 if (FMT == KDA_KV_I8 && vs[y] < INFINITY) vmax = fmaxf(vmax, vs[y]);
-            }
             const bool scaled = FMT == KDA_KV_I8 && vmax > 2.f * ref;
-            if (__any_sync(0xFFFFFFFFu, top[0] > m[0] + kGrow || top[1] > m[1] + kGrow || scaled)) {
-                float f[2];
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    top[r] = fmaxf(top[r], __shfl_xor_sync(0xFFFFFFFFu, top[r], 1));
-                    top[r] = fmaxf(top[r], __shfl_xor_sync(0xFFFFFFFFu, top[r], 2));
-                    const float mn = fmaxf(m[r], top[r]);
-                    f[r] = mn == -INFINITY ? 1.f : ex2(m[r] - mn);
-                    l[r] *= f[r];
-                    m[r] = mn;
-                }
+            if (__any_sync(0xFFFFFFFFu, grown || scaled)) {
+                float k = 1.f;
                 if (scaled) {
-                    const float rn = fmaxf(vmax, kMinRef), k = ref / rn;
-                    f[0] *= k, f[1] *= k;
+                    const float rn = fmaxf(vmax, kMinRef);
+                    k = ref / rn;
                     ref = rn;
                     inv_ref = kPScale / rn;
                 }
 #pragma unroll
-                for (int j = 0; j < kNt; ++j) o[j][0] *= f[0], o[j][1] *= f[0], o[j][2] *= f[1], o[j][3] *= f[1];
-            }
-            const float mx[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
-            uint32_t pa[kGr][4][NT];
+                for (int x = 0; x < NR; ++x) {
+                    float f[2];
 #pragma unroll
-            for (int n = 0; n < 2 * kGr; ++n) {
-                // probabilities, and what of them is rounded: 8-bit, p vs / ref 2^6
-                const float pv = FMT == KDA_KV_I8 ? (vs[n >> 1] < INFINITY ? vs[n >> 1] * inv_ref : NAN) : 1.f;
-                float p[4];
+                    for (int r = 0; r < 2; ++r) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    p[e] = ex2(fmaf(c[n][e], sc[n >> 1][e >> 1], -mx[e >> 1]));
-                    if (FMT == KDA_KV_I8 && strange && c[n][e] == -INFINITY) p[e] = 0.f;
-                    l[e >> 1] += p[e];
-                    if (FMT == KDA_KV_I8) p[e] = strange && p[e] == 0.f ? 0.f : p[e] * pv;
+                        for (int i = 4; i < 32; i <<= 1) top[x][r] = fmaxf(top[x][r], __shfl_xor_sync(0xFFFFFFFFu, top[x][r], i));
+                        const float mn = fmaxf(m[x][r], top[x][r]);
+                        f[r] = mn == -INFINITY ? 1.f : ex2(m[x][r] - mn);
+                        l[x][r] *= f[r];
+                        m[x][r] = mn;
+                        f[r] *= k;
+                    }
+#pragma unroll
+                    for (int j = 0; j < kDt; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[x][j][e] *= f[e & 1];
                 }
-                split2<FMT, NT>(p[0], p[1], pa[n >> 1][2 * (n & 1)]);
-                split2<FMT, NT>(p[2], p[3], pa[n >> 1][2 * (n & 1) + 1]);
             }
-            // ---- values
-            auto values = [&]() {
+            uint32_t pb[kGr][NR][2][NT];
 #pragma unroll
-                for (int y = 0; y < kGr; ++y) {
+            for (int y = 0; y < kGr; ++y) {
+                // probabilities, and what of them is rounded: 8-bit, p vs / ref 2^6
+                const float pv = FMT == KDA_KV_I8 ? (vs[y] < INFINITY ? vs[y] * inv_ref : NAN) : 1.f;
 #pragma unroll
-                    for (int i = 0; i < S::row / 32; ++i) {
-                        uint32_t w[4];   // (tokens 0-7, 8-15) of 16-byte units 2 i and 2 i + 1
-                        ldsm4t(w, kb + unit(v_at, 2 * i) + y * 16 * kLine);
+                for (int x = 0; x < NR; ++x) {
+                    float p[4];
 #pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            if constexpr (FMT == KDA_KV_I8) {
-                                // a register holds columns 2 g, 2 g + 1 of two tokens: the even ones
-                                // make one output tile, the odd ones the next
-                                const uint32_t b0 = w[2 * x] ^ 0x80808080u, b1 = w[2 * x + 1] ^ 0x80808080u;
+                    for (int e = 0; e < 4; ++e) {
+                        const int r = e & 1;
+                        p[e] = ex2(fmaf(c[y][x][e], rs[x][r] * ks[y], m[x][r] == -INFINITY ? 0.f : -m[x][r]));
+                        if (FMT == KDA_KV_I8 && strange && c[y][x][e] == -INFINITY) p[e] = 0.f;
+                        l[x][r] += p[e];
+                        if (FMT == KDA_KV_I8) p[e] = strange && p[e] == 0.f ? 0.f : p[e] * pv;
+                    }
 #pragma unroll
-                                for (int z = NT - 1; z >= 0; --z) {
-                                    const uint32_t f[4] = {pa[y][0][z], pa[y][1][z], pa[y][2][z], pa[y][3][z]};
-                                    mma<FMT>(o[2 * (2 * i + x)], f, half2_of<0x4240>(b0), half2_of<0x4240>(b1));
-                                    mma<FMT>(o[2 * (2 * i + x) + 1], f, half2_of<0x4341>(b0), half2_of<0x4341>(b1));
-                                }
-                            } else {
+                    for (int h = 0; h < 2; ++h) {   // tokens 0-7, 8-15: rows of the transposed operand
+                        split2<FMT, NT>(p[2 * h], p[2 * h + 1], pb[y][x][h]);
 #pragma unroll
-                                for (int z = NT - 1; z >= 0; --z) {
-                                    const uint32_t f[4] = {pa[y][0][z], pa[y][1][z], pa[y][2][z], pa[y][3][z]};
-                                    mma<FMT>(o[2 * i + x], f, w[2 * x], w[2 * x + 1]);
-                                }
-                            }
-                        }
+                        for (int z = 0; z < NT; ++z) pb[y][x][h][z] = transpose8(pb[y][x][h][z]);
                     }
                 }
-            };
+            }
+            // ---- values
             bool odd = false;
             if constexpr (FMT == KDA_KV_BF16) {
-                // A token that a row does not see has probability 0, but 0 times an infinity or a
-                // NaN is not 0 (stale slots past the end, or a value the row must not know of).
-                // Where a step is not seen whole, look for such a value first.
+                // A token that a row does not see has probability 0, but 0 times an infinity or a NaN is
+                // not 0 (stale slots past the end, or a value the row must not know of).  Where a step is
+                // not seen whole, look for such a value first.
                 if (!whole) {
                     uint32_t bad = 0;
                     for (int i = lane; i < S::step * S::blocks * 8; i += 32) {   // 16-byte units of the warp's rows
-                        const int b = i / (S::step * 8);
-                        const uint4 x = *reinterpret_cast<const uint4 *>(buf + S::tile + b * S::unit * 128 + warp * S::step * 128 +
-                                                                         16 * (i % (S::step * 8)));
-                        for (uint32_t y : {x.x, x.y, x.z, x.w})
+                        const uint4 v = *reinterpret_cast<const uint4 *>(buf + S::tile + i / (S::step * 8) * S::unit * 128 +
+                                                                         warp * S::step * 128 + 16 * (i % (S::step * 8)));
+                        for (uint32_t y : {v.x, v.y, v.z, v.w})
                             bad |= (uint32_t)((y & 0x7F80u) == 0x7F80u) | (uint32_t)((y & 0x7F800000u) == 0x7F800000u);
                     }
                     odd = __any_sync(0xFFFFFFFFu, bad != 0);
                 }
             }
             if (!odd) {
-                values();
+#pragma unroll
+                for (int y = 0; y < kGr; ++y)
+#pragma unroll
+                    for (int i = 0; i < S::row / 32; ++i) {
+                        uint32_t w[4];   // 16-byte units 2 i and 2 i + 1 of tokens 0-7 and 8-15
+                        ldsm4t(w, kb + unit(v_at, 2 * i) + y * 16 * kLine);
+                        auto columns = [&](int j, const uint32_t (&af)[4]) {
+#pragma unroll
+                            for (int x = 0; x < NR; ++x)
+#pragma unroll
+                                for (int z = NT - 1; z >= 0; --z) mma<FMT>(o[x][j], af, pb[y][x][0][z], pb[y][x][1][z]);
+                        };
+                        if constexpr (FMT == KDA_KV_I8) {
+                            // a register holds columns 2 g, 2 g + 1 of two tokens: output tile j has the even
+                            // columns of its 16 in rows 0-7 and the odd ones in rows 8-15
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const uint32_t b0 = w[2 * k] ^ 0x80808080u, b1 = w[2 * k + 1] ^ 0x80808080u;
+                                const uint32_t af[4] = {half2_of<0x4240>(b0), half2_of<0x4341>(b0), half2_of<0x4240>(b1), half2_of<0x4341>(b1)};
+                                columns(2 * i + k, af);
+                            }
+                        } else {
+                            columns(i, w);
+                        }
+                    }
             } else if constexpr (FMT == KDA_KV_BF16) {
-                // one product for each query token, without the tokens it does not see, of which
-                // only that token's rows are kept
+                // one product for each query token, without the tokens it does not see, of which only
+                // that token's rows are kept
+#pragma unroll 1
                 for (int32_t q = jb.pmin; q <= jb.pmax; ++q) {
                     uint32_t keep[2];
 #pragma unroll
@@ -609,23 +638,25 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
                         keep[i] = (sees(a, q, j) ? 0xFFFFu : 0u) | (sees(a, q, j + 1) ? 0xFFFF0000u : 0u);
                     }
 #pragma unroll
-                    for (int i = 0; i < kNt; ++i) {
+                    for (int i = 0; i < kDt; ++i) {
                         uint32_t w[4];
-                        ldsm4t(w, kb + S::tile + kv_tile_off<S::row>(S::unit, warp * S::step + 8 * (mm & 1) + mr, 16 * i));
-                        float d[4] = {};
+                        ldsm4t(w, kb + unit(v_at, 2 * i));
+                        w[0] &= keep[0], w[1] &= keep[0], w[2] &= keep[1], w[3] &= keep[1];
 #pragma unroll
-                        for (int z = NT - 1; z >= 0; --z) {
-                            const uint32_t f[4] = {pa[0][0][z], pa[0][1][z], pa[0][2][z], pa[0][3][z]};
-                            mma<FMT>(d, f, w[0] & keep[0], w[1] & keep[1]);
+                        for (int x = 0; x < NR; ++x) {
+                            float d[4] = {};
+#pragma unroll
+                            for (int z = NT - 1; z >= 0; --z) mma<FMT>(d, w, pb[0][x][0][z], pb[0][x][1][z]);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (pos[x][e & 1] == q) o[x][i][e] += d[e];
                         }
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (pos[e >> 1] == q) o[i][e] += d[e];
                     }
                 }
             }
-            }
-        pin(o);
+        }
+#pragma unroll
+        for (int x = 0; x < NR; ++x) pin(o[x]);
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&empty[stage]);
         if (++stage == stages) stage = 0, phase ^= 1;
@@ -633,42 +664,49 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
 
         // ---- the warps' results together
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], 1);
-            l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], 2);
-            if (t == 0) {
-                ml[(warp * 16 + g + 8 * r) * 2] = m[r];
-                ml[(warp * 16 + g + 8 * r) * 2 + 1] = l[r];
+        for (int x = 0; x < NR; ++x)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+#pragma unroll
+                for (int i = 4; i < 32; i <<= 1) l[x][r] += __shfl_xor_sync(0xFFFFFFFFu, l[x][r], i);
+                if (g == 0) {
+                    ml[(warp * 16 + 8 * x + 2 * t + r) * 2] = m[x][r];
+                    ml[(warp * 16 + 8 * x + 2 * t + r) * 2 + 1] = l[x][r];
+                }
             }
-        }
         meet();
         // four rows at a time, so that the ring has the room
         const bool starts = flags & kStarts, ends = flags & kEnds;
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int my_row = g + 8 * r;
-            float mt = -INFINITY;
+        for (int x = 0; x < NR; ++x) {
+            float f[2];
 #pragma unroll
-            for (int i = 0; i < kWarps; ++i) mt = fmaxf(mt, ml[(i * 16 + my_row) * 2]);
-            float f = mt == -INFINITY ? 1.f : ex2(m[r] - mt);
-            if (FMT == KDA_KV_I8) f *= ref * (1.f / kPScale);
+            for (int r = 0; r < 2; ++r) {
+                float mt = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < kWarps; ++i) mt = fmaxf(mt, ml[(i * 16 + 8 * x + 2 * t + r) * 2]);
+                f[r] = mt == -INFINITY ? 1.f : ex2(m[x][r] - mt);
+                if (FMT == KDA_KV_I8) f[r] *= ref * (1.f / kPScale);
+            }
 #pragma unroll 1
             for (int half = 0; half < 2; ++half) {
-                const int base = 8 * r + 4 * half;
+                const int base = 8 * x + 4 * half;
                 if (base >= nrows) break;
-                if (g >> 2 == half) {
-                    float *dst = acc + (warp * 4 + (my_row & 3)) * D;
-                    if constexpr (FMT == KDA_KV_I8) {
+                if (t >> 1 == half) {
 #pragma unroll
-                        for (int i = 0; i < kNt / 2; ++i)   // columns 16 i + 4 t ..: even and odd ones from two tiles
-                            *reinterpret_cast<float4 *>(dst + 4 * acc_unit<FMT, D>(my_row, 4 * i + t)) =
-                                make_float4(o[2 * i][2 * r] * f, o[2 * i + 1][2 * r] * f, o[2 * i][2 * r + 1] * f,
-                                            o[2 * i + 1][2 * r + 1] * f);
-                    } else {
+                    for (int r = 0; r < 2; ++r) {
+                        const int row = 2 * (t & 1) + r;
+                        float *dst = acc + (warp * 4 + row) * D;
 #pragma unroll
-                        for (int j = 0; j < kNt; ++j)
-                            *reinterpret_cast<float2 *>(dst + 4 * acc_unit<FMT, D>(my_row, 2 * j + (t >> 1)) + 2 * (t & 1)) =
-                                make_float2(o[j][2 * r] * f, o[j][2 * r + 1] * f);
+                        for (int j = 0; j < kDt; ++j) {
+                            const float v0 = o[x][j][r] * f[r], v1 = o[x][j][r + 2] * f[r];
+                            if constexpr (FMT == KDA_KV_I8) {   // columns 16 j + 2 g, 2 g + 1
+                                *reinterpret_cast<float2 *>(dst + 4 * acc_unit(base + row, 4 * j + (g >> 1)) + 2 * (g & 1)) = make_float2(v0, v1);
+                            } else {                            // columns 16 j + g, 16 j + 8 + g
+                                dst[4 * acc_unit(base + row, 4 * j + (g >> 2)) + (g & 3)] = v0;
+                                dst[4 * acc_unit(base + row, 4 * j + 2 + (g >> 2)) + (g & 3)] = v1;
+                            }
+                        }
                     }
                 }
                 meet();
@@ -684,7 +722,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
                         const float lw = ml[(w * 16 + sum_row) * 2 + 1];
                         lt += top == -INFINITY ? lw : lw * ex2(ml[(w * 16 + sum_row) * 2] - top);
                         const float4 x = *reinterpret_cast<const float4 *>(acc + (w * 4 + (sum_row & 3)) * D +
-                                                                           4 * acc_unit<FMT, D>(sum_row, unit4));
+                                                                           4 * acc_unit(sum_row, unit4));
                         v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
                     }
                     if (starts && ends) {
@@ -709,14 +747,14 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
     }
 }
 
-template <int FMT, int D, int NT>
-cudaError_t run(const AttnArgs &a, cudaStream_t st) {
-    using M = Smem<FMT, D, NT>;
+template <int FMT, int D, int NT, int NR>
+cudaError_t run_rows(const AttnArgs &a, cudaStream_t st) {
+    using M = Smem<FMT, D, NT, NR>;
     static_assert(M::total(Shape<FMT, D>::deep_stages) + 1024 <= 227 * 1024, "shared memory");
     // (the split terms of float32 queries leave room for one stage less beside another CTA)
     static_assert(NT > 1 || 2 * (M::total(Shape<FMT, D>::stages) + 2048) <= 228 * 1024, "two CTAs an SM");
     const int smem = M::total(a.deep ? Shape<FMT, D>::deep_stages : Shape<FMT, D>::stages - (NT > 1)) + 1024;
-    auto kern = attn_decode_kernel<FMT, D, NT>;
+    auto kern = attn_decode_kernel<FMT, D, NT, NR>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     kern<<<a.ctas, (kWarps + 1) * 32, smem, st>>>(a);
@@ -733,6 +771,15 @@ cudaError_t run(const AttnArgs &a, cudaStream_t st) {
     cfg.attrs = &at;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, attn_join_kernel<D, kAttnDecodeRows>, a);
+}
+
+// Up to eight rows a sequence take one tile of rows; the split products of float32 queries, which are
+// not bound by bytes, have one form for both.
+template <int FMT, int D, int NT>
+cudaError_t run(const AttnArgs &a, cudaStream_t st) {
+    if constexpr (NT == 1)
+        if ((int64_t)a.max_q * a.G <= 8) return run_rows<FMT, D, NT, 1>(a, st);
+    return run_rows<FMT, D, NT, 2>(a, st);
 }
 
 }  // namespace
