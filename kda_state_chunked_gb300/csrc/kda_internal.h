@@ -183,7 +183,7 @@ struct KvAppendArgs {
 struct KvGatherArgs {
     KvView kv;
     int32_t dtype, nseq;
-    int64_t T_out;
+    int64_t T_out, row0;          // rows; first one of this launch
     const int32_t *cu_out, *begin;
     void *k_out, *v_out;          // [T_out][Hkv][d]
 };

@@ -267,9 +267,8 @@ constexpr int kGatherRows = 4;
 template <int FMT, int D, class TOUT>
 __global__ void __launch_bounds__(256) kv_gather_kernel(KvGatherArgs a) {
     constexpr int kTpr = D / 16, kRow = kKvRow<FMT, D>;
-    const int per_row = a.kv.Hkv * kTpr;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t row0 = i / per_row * kGatherRows;
+    const uint32_t per_row = a.kv.Hkv * kTpr, i = blockIdx.x * 256u + threadIdx.x;   // below 2^31 threads a launch
+    const int64_t row0 = a.row0 + (int64_t)(i / per_row) * kGatherRows;
     const int c = (int)(i % kTpr), head = (int)(i % per_row) / kTpr, pt = a.kv.page_tokens;
     // the warp's first row's sequence; a thread steps on from there
     int s = kv_find(a.nseq, __shfl_sync(0xFFFFFFFFu, row0, 0), [&](int m) { return (int64_t)__ldg(a.cu_out + m); });
@@ -352,19 +351,27 @@ cudaError_t append(const KvAppendArgs &a, cudaStream_t st) {
 }
 
 // Few new tokens a sequence leave all but one row of a block's threads idle, so small CTAs take
-// them; a CTA of 256 holds a whole block of 128 new rows.
+// them; a CTA of 256 holds a whole block of new rows, and one made for blocks of up to 64 tokens
+// needs half the registers of the largest, so that more of them have loads under way on an SM
+// (keys and values of 4 x 8192 tokens in 64-token blocks: 186 us with the largest's registers).
 template <int FMT, int D, class TIN>
 cudaError_t append_sized(const KvAppendArgs &a, cudaStream_t st) {
+    constexpr int kMost = kKvMaxPageTokens * (D / 16) / 256;
     if (a.max_q <= 8) return append<FMT, D, TIN, 64, 1>(a, st);
-    return append<FMT, D, TIN, 256, kKvMaxPageTokens * (D / 16) / 256>(a, st);
+    if (a.kv.page_tokens <= kKvMaxPageTokens / 2) return append<FMT, D, TIN, 256, kMost / 2>(a, st);
+    return append<FMT, D, TIN, 256, kMost>(a, st);
 }
 
 template <int FMT, int D>
 cudaError_t gather(const KvGatherArgs &a, cudaStream_t st) {
-    const int64_t n = (a.T_out + kGatherRows - 1) / kGatherRows * a.kv.Hkv * (D / 16), grid = (n + 255) / 256;
-    if (grid > INT32_MAX) return cudaErrorInvalidValue;
-    if (a.dtype == KDA_F32) kv_gather_kernel<FMT, D, float><<<(unsigned)grid, 256, 0, st>>>(a);
-    else kv_gather_kernel<FMT, D, __nv_bfloat16><<<(unsigned)grid, 256, 0, st>>>(a);
+    KvGatherArgs part = a;
+    const int64_t per_row = (int64_t)a.kv.Hkv * (D / 16), most = ((int64_t)1 << 30) / per_row * kGatherRows;   // rows a launch
+    for (part.row0 = 0; part.row0 < a.T_out; part.row0 += most) {
+        const int64_t rows = min(most, a.T_out - part.row0);
+        const unsigned grid = (unsigned)(((rows + kGatherRows - 1) / kGatherRows * per_row + 255) / 256);
+        if (a.dtype == KDA_F32) kv_gather_kernel<FMT, D, float><<<grid, 256, 0, st>>>(part);
+        else kv_gather_kernel<FMT, D, __nv_bfloat16><<<grid, 256, 0, st>>>(part);
+    }
     return cudaGetLastError();
 }
 
