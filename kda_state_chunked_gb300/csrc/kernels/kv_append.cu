@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(NT) kv_append_kernel(KvAppendArgs a, int32_t q
 // Cached ranges as values.  A thread takes 16 elements of K and of V of one head, in kGatherRows rows
 // whose loads are under way together; neighbours take the next elements and heads, so a warp writes
 // whole lines of both outputs.
-constexpr int kGatherRows = 4;
+constexpr int kGatherRows = 2;
 template <int FMT, int D, class TOUT>
 __global__ void __launch_bounds__(256) kv_gather_kernel(KvGatherArgs a) {
     constexpr int kTpr = D / 16, kRow = kKvRow<FMT, D>;
