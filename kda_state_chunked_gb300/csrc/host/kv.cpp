@@ -153,6 +153,7 @@ int kda_attn_paged(const kda_pool *pool, int32_t Hq, int32_t Hkv, int32_t d, int
         !aligned16(workspace) || ws_bytes < need)
         return KDA_EINVAL;
     a.Hq = Hq; a.G = Hq / Hkv; a.dtype = dtype; a.nseq = nseq; a.max_q = max_q; a.T_tot = T_tot;
+    a.g_magic = a.G > 1 ? (uint32_t)(((1ull << 32) + a.G - 1) / a.G) : 0u;
     a.cu_q = cu_q; a.kv_len = kv_len;
     a.q = q; a.q_stride = q_stride;
     // a window (or sinks) as long as a sequence can be is none (are all of it)

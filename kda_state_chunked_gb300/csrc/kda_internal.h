@@ -208,6 +208,7 @@ struct AttnSplit {
 struct AttnArgs {
     KvView kv;
     int32_t Hq, G, dtype, nseq, max_q;
+    uint32_t g_magic;             // ceil(2^32 / G) (0 for G = 1): rows to tokens without a division
     int64_t T_tot;
     const int32_t *cu_q, *kv_len;
     const void *q;

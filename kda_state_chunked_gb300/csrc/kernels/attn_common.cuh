@@ -26,6 +26,13 @@ struct Tile {
     int32_t first, sinks, units;  // unit where its window begins, sink units before that, units in all
 };
 
+// Token r / G of row r of a sequence (r < 2^31): the high half of r ceil(2^32 / G) is that or one more.
+__device__ __forceinline__ int32_t token_of(const AttnArgs &a, int32_t r) {
+    if (a.G == 1) return r;
+    const uint32_t q = __umulhi((uint32_t)r, a.g_magic);
+    return (int32_t)(q * (uint32_t)a.G > (uint32_t)r ? q - 1 : q);
+}
+
 template <int ROWS>
 __device__ __forceinline__ int32_t tiles_of(const AttnArgs &a, const KvSeq &q) {
     return (int32_t)(((int64_t)q.n * a.G + ROWS - 1) / ROWS);
@@ -41,8 +48,8 @@ __device__ __forceinline__ Tile make_tile(const AttnArgs &a, int32_t s, const Kv
     t.row0 = rt * ROWS;
     t.nrows = min(ROWS, q.n * a.G - t.row0);
     const int32_t base = q.len - q.n;
-    t.pmin = base + t.row0 / a.G;
-    t.pmax = base + (t.row0 + t.nrows - 1) / a.G;
+    t.pmin = base + token_of(a, t.row0);
+    t.pmax = base + token_of(a, t.row0 + t.nrows - 1);
     t.first = t.sinks = 0;
     if (t.pmax < 0) {             // more new tokens than the cache holds: these rows see nothing
         t.units = 1;
@@ -175,7 +182,8 @@ __global__ void __launch_bounds__(128) attn_join_kernel(AttnArgs a) {
             for (int j = 0; j < kCols; ++j) o[j] += w * p[lane * kCols + j];
         }
         const int row = sp.row0 + r;
-        const int64_t at = (int64_t)(sp.row_tok + row / a.G) * a.Hq + sp.head * a.G + row % a.G;
+        const int32_t tok = token_of(a, row);
+        const int64_t at = (int64_t)(sp.row_tok + tok) * a.Hq + sp.head * a.G + row - tok * a.G;
         const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
         for (int j = 0; j < kCols; ++j) {

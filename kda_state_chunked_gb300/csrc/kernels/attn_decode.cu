@@ -378,7 +378,8 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
 #pragma unroll
             for (int i = 0; i < kCols; ++i) x[i] = 0.f;
             if (row < nrows) {
-                const int64_t off = (int64_t)(tok0 + at / a.G) * a.q_stride + (int64_t)(head * a.G + at % a.G) * D + c0;
+                const int32_t tok = token_of(a, at);
+                const int64_t off = (int64_t)(tok0 + tok) * a.q_stride + (int64_t)(head * a.G + at - tok * a.G) * D + c0;
 #pragma unroll
                 for (int i = 0; i < kCols; i += 8) {
                     if (NT > 1) {
@@ -442,7 +443,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
                 for (int r = 0; r < 2; ++r) {
                     const int row = 8 * x + 2 * t + r;
                     rs[x][r] = qs[row];
-                    pos[x][r] = row < nrows ? jb.base + (row0 + row) / a.G : -1;
+                    pos[x][r] = row < nrows ? jb.base + token_of(a, row0 + row) : -1;
                     m[x][r] = -INFINITY, l[x][r] = 0.f;
                 }
 #pragma unroll
@@ -726,8 +727,8 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
                         v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
                     }
                     if (starts && ends) {
-                        const int at_row = row0 + sum_row;
-                        const int64_t at = (int64_t)(tok0 + at_row / a.G) * a.Hq + head * a.G + at_row % a.G;
+                        const int32_t at_row = row0 + sum_row, tok = token_of(a, at_row);
+                        const int64_t at = (int64_t)(tok0 + tok) * a.Hq + head * a.G + at_row - tok * a.G;
                         const float inv = 1.f / lt;
                         if (lt == 0.f) v = make_float4(0.f, 0.f, 0.f, 0.f);
                         else v.x *= inv, v.y *= inv, v.z *= inv, v.w *= inv;

@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
         float *pair = reinterpret_cast<float *>(sm + L::pair);
         auto meet = [&]() { tcx::named_bar(1 + half * 4 + warp % 4, 64); };    // the two warps of these rows
         uint32_t n_s = 0, n_item = 0;   // units of this half, items so far: the barriers' parities
-        int32_t pos = -1;
+        int32_t pos = -1, p_lo = 0, p_hi = 0;   // positions of this row, of the warp's rows
         bool in = false, ok = true;
         float m = -INFINITY, l = 0.f, f_row = 0.f;
         for (uint32_t n = 0;; ++n) {
@@ -304,7 +304,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
             const int32_t at = jb.row0 + row;
             if (flags & kBegin) {
                 in = row < nrows;
-                pos = in ? jb.base + at / a.G : -1;
+                pos = in ? jb.base + token_of(a, at) : -1;
+                p_lo = __reduce_min_sync(0xFFFFFFFFu, in ? pos : INT32_MAX);
+                p_hi = __reduce_max_sync(0xFFFFFFFFu, pos);
                 m = -INFINITY, l = 0.f;
                 float z[16];
 #pragma unroll
@@ -316,13 +318,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
             if (!ok) break;
             ptx::tc_fence_after();
             if (flags & kBegin) f_row = qs[(n_item & 1) * kRows + row];
-            // columns of group c (16 tokens) that this row sees
+            // Of group c (16 tokens): the columns that this row sees, and whether every row of the warp sees
+            // all of them or none any.  A warp's rows are few neighbouring tokens, so in a unit that a mask
+            // cuts most groups still are the one or the other.
             auto seen = [&](int c) -> uint32_t {
                 auto low = [](int32_t k) -> uint32_t { return k <= 0 ? 0u : k >= 16 ? 0xFFFFu : (1u << k) - 1u; };
                 const int32_t b = j0 + 64 * side + 16 * c;
                 uint32_t x = low(pos + 1 - b);
                 if (a.window > 0) x &= ~low(pos - a.window + 1 - b) | low(a.sinks - b);
-                return jb.live >> (4 * side + c) & 1u ? x : 0u;
+                return x;
+            };
+            enum { kNone, kSome, kEvery };
+            auto kind = [&](int c) -> int {
+                const int32_t b = j0 + 64 * side + 16 * c;
+                if (!(jb.live >> (4 * side + c) & 1u) || b > p_hi || (a.window > 0 && b + 15 <= p_lo - a.window && b >= a.sinks)) return kNone;
+                return b + 15 <= p_lo && (a.window <= 0 || b > p_hi - a.window || b + 16 <= a.sinks) ? kEvery : kSome;
             };
             // 16 scores at a time, the next on their way from tensor memory
             auto groups = [&](auto step) {
@@ -342,13 +352,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
             float top = -INFINITY;
             auto most = [&](auto all) {
                 groups([&](const float (&x)[16], int c) {
-                    constexpr bool kAll = decltype(all)::value;
-                    const uint32_t see = kAll ? ~0u : seen(c);
+                    const int k = decltype(all)::value ? kEvery : kind(c);
                     float gt = -INFINITY;
+                    if (k == kEvery) {
 #pragma unroll
-                    for (int i = 0; i < 16; i += 2)
-                        gt = fmaxf(gt, fmaxf(kAll || (see >> i & 1u) ? x[i] : -INFINITY,
-                                             kAll || (see >> (i + 1) & 1u) ? x[i + 1] : -INFINITY));
+                        for (int i = 0; i < 16; i += 2) gt = fmaxf(gt, fmaxf(x[i], x[i + 1]));
+                    } else if (k == kSome) {
+                        const uint32_t see = seen(c);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) gt = fmaxf(gt, see & 1u << i ? x[i] : -INFINITY);
+                    }
                     // f >= 0: the product keeps the order
                     const float fk = FMT == KDA_KV_I8 ? f_row * jb.ks[4 * side + c] : f_row;
                     top = fmaxf(top, gt == -INFINITY ? gt : gt * fk);
@@ -427,29 +440,34 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
             // what an earlier group has read
             auto weigh = [&](auto all) {
                 groups([&](const float (&x)[16], int c) {
-                    constexpr bool kAll = decltype(all)::value;
-                    const uint32_t see = kAll ? ~0u : seen(c);
+                    const int k = decltype(all)::value ? kEvery : kind(c);
                     float p[8];
-                    float fk = f_row, bias = -ms, back = 1.f;
-                    if (FMT == KDA_KV_I8) {
-                        fk *= jb.ks[4 * side + c];
-                        bias += jb.lg[4 * side + c];
-                        back = jb.back[4 * side + c];
-                    }
-                    const float2 ff = make_float2(fk, fk), bb = make_float2(bias, bias);
-                    float2 part = make_float2(0.f, 0.f);
+                    if (k == kNone) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        float2 y = tcx::ffma2(make_float2(x[2 * i], x[2 * i + 1]), ff, bb);
-                        y.x = ex2(y.x), y.y = ex2(y.y);
-                        if (!kAll) {
-                            y.x = see >> (2 * i) & 1u ? y.x : 0.f;
-                            y.y = see >> (2 * i + 1) & 1u ? y.y : 0.f;
+                        for (int i = 0; i < 8; ++i) p[i] = 0.f;
+                    } else {
+                        const uint32_t see = k == kEvery ? ~0u : seen(c);
+                        float fk = f_row, bias = -ms, back = 1.f;
+                        if (FMT == KDA_KV_I8) {
+                            fk *= jb.ks[4 * side + c];
+                            bias += jb.lg[4 * side + c];
+                            back = jb.back[4 * side + c];
                         }
-                        part = tcx::fadd2(part, y);
-                        p[i] = __uint_as_float(pack2<FMT>(y.x, y.y));
+                        const float2 ff = make_float2(fk, fk), bb = make_float2(bias, bias);
+                        float2 part = make_float2(0.f, 0.f);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            float2 y = tcx::ffma2(make_float2(x[2 * i], x[2 * i + 1]), ff, bb);
+                            y.x = ex2(y.x), y.y = ex2(y.y);
+                            if (k == kSome) {
+                                y.x = see & 1u << 2 * i ? y.x : 0.f;
+                                y.y = see & 2u << 2 * i ? y.y : 0.f;
+                            }
+                            part = tcx::fadd2(part, y);
+                            p[i] = __uint_as_float(pack2<FMT>(y.x, y.y));
+                        }
+                        l += (part.x + part.y) * back;
                     }
-                    l += (part.x + part.y) * back;
                     ptx::tmem_st8(tS + 8 * c, p);
                 });
             };
@@ -472,29 +490,35 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                 if (!ok) break;
                 ptx::tc_fence_after();
                 const bool all = (flags & kStarts) && (flags & kEnds);
-                const int64_t orow = ((int64_t)jb.tok0 + at / a.G) * a.Hq + jb.head * a.G + at % a.G;
+                const int32_t tok = token_of(a, at);
+                const int64_t orow = ((int64_t)jb.tok0 + tok) * a.Hq + jb.head * a.G + at - tok * a.G;
                 const float unscale = FMT == KDA_KV_I8 ? exp2f(jb.lref - kPBits) : 1.f;
                 const float f = all ? (l == 0.f ? 0.f : unscale / l) : unscale;
                 float *part = a.part + ((int64_t)(blockIdx.x * 2 + (flags & kStarts ? 1 : 0)) * kRows + row) * kPartRow<D>;
 #pragma unroll 1
-                for (int c = 0; c < D / 32; ++c) {
-                    float o[16];
-                    tmem_ld16(tO + 16 * c, o);
-                    wait_ld(o);
+                for (int c = 0; c < D / 32; c += 2) {
+                    float o[2][16];
+                    tmem_ld16(tO + 16 * c, o[0]);
+                    tmem_ld16(tO + 16 * c + 16, o[1]);
+                    wait_ld(o[0]);
+                    wait_ld(o[1]);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) o[i] = all && l == 0.f ? 0.f : o[i] * f;
-                    const int col = side * (D / 2) + 16 * c;
-                    if (in && all) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o) + orow * D + col);
+                    for (int y = 0; y < 2; ++y) {
 #pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            dst[i] = make_uint4(tcx::f2_to_bf2(o[8 * i], o[8 * i + 1]), tcx::f2_to_bf2(o[8 * i + 2], o[8 * i + 3]),
-                                                tcx::f2_to_bf2(o[8 * i + 4], o[8 * i + 5]), tcx::f2_to_bf2(o[8 * i + 6], o[8 * i + 7]));
-                    } else if (in) {
+                        for (int i = 0; i < 16; ++i) o[y][i] = all && l == 0.f ? 0.f : o[y][i] * f;
+                        const int col = side * (D / 2) + 16 * (c + y);
+                        if (in && all) {
+                            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o) + orow * D + col);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            reinterpret_cast<float4 *>(part + col)[i] =
-                                make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                            for (int i = 0; i < 2; ++i)
+                                dst[i] = make_uint4(tcx::f2_to_bf2(o[y][8 * i], o[y][8 * i + 1]), tcx::f2_to_bf2(o[y][8 * i + 2], o[y][8 * i + 3]),
+                                                    tcx::f2_to_bf2(o[y][8 * i + 4], o[y][8 * i + 5]), tcx::f2_to_bf2(o[y][8 * i + 6], o[y][8 * i + 7]));
+                        } else if (in) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                reinterpret_cast<float4 *>(part + col)[i] =
+                                    make_float4(o[y][4 * i], o[y][4 * i + 1], o[y][4 * i + 2], o[y][4 * i + 3]);
+                        }
                     }
                     __syncwarp();
                 }
@@ -564,12 +588,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
             for (int r0 = lt / kTpr; r0 < rows; r0 += kBatch * kRpp) {
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i) {
-                    const int r = r0 + i * kRpp, at = jb.row0 + r;
+                    const int r = r0 + i * kRpp, at = jb.row0 + r, tok = token_of(a, at);
                     x[i][0] = x[i][1] = make_uint4(0, 0, 0, 0);
                     if (r < nrows) {
                         const uint4 *src = reinterpret_cast<const uint4 *>(
-                            static_cast<const __nv_bfloat16 *>(a.q) + ((int64_t)jb.tok0 + at / a.G) * a.q_stride +
-                            (int64_t)(jb.head * a.G + at % a.G) * D + 16 * c);
+                            static_cast<const __nv_bfloat16 *>(a.q) + ((int64_t)jb.tok0 + tok) * a.q_stride +
+                            (int64_t)(jb.head * a.G + at - tok * a.G) * D + 16 * c);
                         x[i][0] = src[0], x[i][1] = src[1];
                     }
                 }
@@ -579,16 +603,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                     const int r = r0 + i * kRpp;
                     if (r >= rows) break;
                     float f = a.scale * sign * kLog2e;
-                    float e[16];
-                    const uint32_t xw[8] = {x[i][0].x, x[i][0].y, x[i][0].z, x[i][0].w, x[i][1].x, x[i][1].y, x[i][1].z, x[i][1].w};
+                    uint32_t y[8] = {x[i][0].x, x[i][0].y, x[i][0].z, x[i][0].w, x[i][1].x, x[i][1].y, x[i][1].z, x[i][1].w};
+                    if (sign < 0.f)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float2 p = tcx::bf2_to_f2(xw[j]);
-                        e[2 * j] = p.x * sign, e[2 * j + 1] = p.y * sign;
-                    }
+                        for (int j = 0; j < 8; ++j) y[j] ^= 0x80008000u;
                     if (FMT == KDA_KV_I8) {
                         // a power of two that brings the row's largest magnitude to [2^10, 2^11)
-                        float top = 0.f;
+                        float e[16], top = 0.f;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const float2 v = tcx::bf2_to_f2(y[j]);
+                            e[2 * j] = v.x, e[2 * j + 1] = v.y;
+                        }
 #pragma unroll
                         for (int j = 0; j < 16; ++j) top = fmaxf(top, fabsf(e[j]));
 #pragma unroll
@@ -596,13 +622,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                         const int b = (int)(__float_as_uint(top) >> 23);
                         const int shift = b == 0 || b == 255 ? 0 : min(max(137 - b, -120), 120);
                         const float up = __uint_as_float((uint32_t)(127 + shift) << 23);
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) e[j] *= up;
                         f *= __uint_as_float((uint32_t)(127 - shift) << 23);
-                    }
-                    uint32_t y[8];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) y[j] = pack2<FMT>(e[2 * j], e[2 * j + 1]);
+                        for (int j = 0; j < 8; ++j) y[j] = pack2<FMT>(e[2 * j] * up, e[2 * j + 1] * up);
+                    }
                     uint8_t *dst = sm + L::q + (r / kHalf) * L::half_q + (c >> 2) * (kHalf * 128);
                     const int rr = r % kHalf;
                     *reinterpret_cast<uint4 *>(dst + ptx::sw128_off(rr, 32 * (c & 3))) = make_uint4(y[0], y[1], y[2], y[3]);
