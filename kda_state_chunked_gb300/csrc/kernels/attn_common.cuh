@@ -93,15 +93,31 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // ptx::mbar_wait with its loop kept rolled: these kernels wait in many places, and the unrolled
-// loops alone came to 85 KB of code.
+// loops alone came to 85 KB of code.  NS: nanoseconds between looks, for warps that run ahead and so
+// mostly wait; a warp that looks all the time takes a third of its scheduler's issue slots.
+template <int NS = 0>
 __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatile int *err) {
 #pragma unroll 1
-    for (uint32_t i = 0; i < ptx::kSpinLimit; ++i) {
+    for (uint32_t i = 0; i < ptx::kSpinLimit >> (NS ? 4 : 0); ++i) {
         if (ptx::mbar_try_wait(bar, parity)) return true;
         if (err && *err) return false;
+        if (NS) __nanosleep(NS);
     }
     if (err) *err = 1;
     return false;
+}
+
+// The same for a group of warps of which one looks and the others stand at named barrier `id`.
+template <int ID_THREADS>
+__device__ __forceinline__ bool wait_together(uint64_t *bar, uint32_t parity, volatile int *err, bool looks, int id) {
+    uint32_t ok = 1;
+    if (looks) ok = wait_bar(bar, parity, err);
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %0, 0;\n\tbarrier.cta.red.and.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "+r"(ok)
+        : "r"(id), "n"(ID_THREADS)
+        : "memory");
+    return ok != 0;
 }
 
 // What a warp that walks the list of units says of each (bits of a job's flags): first, last unit of

@@ -121,6 +121,12 @@ __device__ __forceinline__ float tmem_ld1(uint32_t addr) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(r)::"memory");
     return __uint_as_float(r);
 }
+__device__ __forceinline__ float max3(float x, float y, float z) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+    return r;
+}
+
 // True in one lane of a converged warp.
 __device__ __forceinline__ bool elect() {
     uint32_t p;
@@ -272,6 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
     // Waits of a whole warp, of one thread; the next job, and being done with one.
     auto wait1 = [&](int b, uint32_t parity) { return wait_bar(&bars[b], parity, err); };
     auto wait = [&](int b, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait1(b, parity)) != 0; };
+    auto wait_slow = [&](int b, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait_bar<64>(&bars[b], parity, err)) != 0; };
     auto job = [&](uint32_t n) -> const Job & { return jobs[n % kJobs]; };
     auto wait_job = [&](uint32_t n) { return wait(JFULL + n % kJobs, n / kJobs & 1); };
     auto done = [&](uint32_t n) { tcx::warp_arrive(&bars[JEMPTY + n % kJobs]); };
@@ -286,6 +293,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
         const uint32_t tO = tm + lanes + 256 + half * 128 + side * (D / 2);   // and its half of the output
         float *pair = reinterpret_cast<float *>(sm + L::pair);
         auto meet = [&]() { tcx::named_bar(1 + half * 4 + warp % 4, 64); };    // the two warps of these rows
+        auto wait_half = [&](int b, uint32_t parity) {                         // the half's eight warps
+            return wait_together<kSoftWarps / 2 * 32>(&bars[b], parity, err, warp % 8 == 0, 9 + half);
+        };
         uint32_t n_s = 0, n_item = 0;   // units of this half, items so far: the barriers' parities
         int32_t pos = -1, p_lo = 0, p_hi = 0;   // positions of this row, of the warp's rows
         bool in = false, ok = true;
@@ -314,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) ptx::tmem_st16(tO + 16 * c, z);
             }
-            ok = wait(SFULL + half, n_s & 1);
+            ok = wait_half(SFULL + half, n_s & 1);
             if (!ok) break;
             ptx::tc_fence_after();
             if (flags & kBegin) f_row = qs[(n_item & 1) * kRows + row];
@@ -353,22 +363,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
             auto most = [&](auto all) {
                 groups([&](const float (&x)[16], int c) {
                     const int k = decltype(all)::value ? kEvery : kind(c);
-                    float gt = -INFINITY;
+                    float gt = FMT == KDA_KV_I8 ? -INFINITY : top;
                     if (k == kEvery) {
 #pragma unroll
-                        for (int i = 0; i < 16; i += 2) gt = fmaxf(gt, fmaxf(x[i], x[i + 1]));
+                        for (int i = 0; i < 16; i += 2) gt = max3(gt, x[i], x[i + 1]);
                     } else if (k == kSome) {
                         const uint32_t see = seen(c);
 #pragma unroll
                         for (int i = 0; i < 16; ++i) gt = fmaxf(gt, see & 1u << i ? x[i] : -INFINITY);
                     }
-                    // f >= 0: the product keeps the order
-                    const float fk = FMT == KDA_KV_I8 ? f_row * jb.ks[4 * side + c] : f_row;
-                    top = fmaxf(top, gt == -INFINITY ? gt : gt * fk);
+                    // a group's factor is >= 0, and so is the row's, which the end brings in
+                    if (FMT == KDA_KV_I8) top = fmaxf(top, k == kNone ? -INFINITY : gt * jb.ks[4 * side + c]);
+                    else top = gt;
                 });
             };
             if (flags & kWhole) most(std::true_type{});
             else most(std::false_type{});
+            if (top != -INFINITY) top *= f_row;
             {
                 float *mine = pair + ((n_s & 1) * 2 + side) * kRows, *other = pair + ((n_s & 1) * 2 + (side ^ 1)) * kRows;
                 mine[row] = top;
@@ -387,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
             // ---- tokens whose values were taken out of the product (16-bit cache)
             bool odd = false;
             if (FMT == KDA_KV_BF16 && !(flags & kWhole)) {
-                ok = wait(VFULL + (n & 1), n >> 1 & 1);
+                ok = wait_half(VFULL + (n & 1), n >> 1 & 1);
                 if (!ok) break;
                 const volatile uint32_t *out = bad + (n & 1) * 4;
                 odd = (out[0] | out[1] | out[2] | out[3]) != 0;
@@ -486,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                     l += other[row];
                     meet();              // the next item's first maxima go to the same place
                 }
-                ok = wait(OFULL + half, (n_s - 1) & 1);
+                ok = wait_half(OFULL + half, (n_s - 1) & 1);
                 if (!ok) break;
                 ptx::tc_fence_after();
                 const bool all = (flags & kStarts) && (flags & kEnds);
@@ -496,14 +507,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                 const float f = all ? (l == 0.f ? 0.f : unscale / l) : unscale;
                 float *part = a.part + ((int64_t)(blockIdx.x * 2 + (flags & kStarts ? 1 : 0)) * kRows + row) * kPartRow<D>;
 #pragma unroll 1
-                for (int c = 0; c < D / 32; c += 2) {
-                    float o[2][16];
+                for (int c = 0; c < D / 32; ++c) {
+                    float o[1][16];
                     tmem_ld16(tO + 16 * c, o[0]);
-                    tmem_ld16(tO + 16 * c + 16, o[1]);
                     wait_ld(o[0]);
-                    wait_ld(o[1]);
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) {
+                    for (int y = 0; y < 1; ++y) {
 #pragma unroll
                         for (int i = 0; i < 16; ++i) o[y][i] = all && l == 0.f ? 0.f : o[y][i] * f;
                         const int col = side * (D / 2) + 16 * (c + y);
@@ -544,6 +553,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
     } else if (warp < kSoftWarps + kLoadWarps) {
         // ====================================================== queries, and keys and values
         const int lw = warp - kSoftWarps, lt = tid - kSoftWarps * 32;
+        auto wait_all = [&](int b, uint32_t parity) {             // the eight warps
+            return wait_together<kLoadWarps * 32>(&bars[b], parity, err, lw == 0, 11);
+        };
         uint32_t n_item = 0;
         // 8-bit: the units' codes are read one unit ahead into registers.  A warp takes 16 tokens;
         // eight lanes take four units of token r and of token r ^ 5, which keeps both their reads
@@ -597,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                         x[i][0] = src[0], x[i][1] = src[1];
                     }
                 }
-                if (r0 == lt / kTpr && !wait(QEMPTY, (n_item & 1) ^ 1)) return false;
+                if (r0 == lt / kTpr && !wait_all(QEMPTY, (n_item & 1) ^ 1)) return false;
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i) {
                     const int r = r0 + i * kRpp;
@@ -659,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                 // keys, then values: kc goes out, vc moves up, the same of the next unit is fetched
 #pragma unroll 1
                 for (int v = 0; v < 2; ++v) {
-                    ok = wait((v ? VEMPTY : KEMPTY) + st, par);
+                    ok = wait_all((v ? VEMPTY : KEMPTY) + st, par);
                     if (!ok) break;
                     put(kc, sm + (v ? L::v : L::k) + st * L::tile);
                     ptx::fence_proxy_async_smem();
@@ -678,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                 // values that not every row sees: a token that no row sees is cleared (0 times what a
                 // stale slot holds need not be 0), and one with an infinity or a NaN is taken out and
                 // left to the rows that see it
-                ok = wait(VRAW + st, n >> 1 & 1);
+                ok = wait_all(VRAW + st, n >> 1 & 1);
                 if (!ok) break;
                 if (!(jb.flags & kWhole) && lt < kUnit) {
                     uint8_t *line = sm + L::v + st * L::tile + lt * 128;
@@ -808,10 +820,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                         for (int b = 0; b < kBlks; ++b)
                             ptx::bulk_load(dst + b * L::blk + lane * 2048, from + b * pt * 128, 2048, &bars[bar]);
                 };
-                if (!wait(KEMPTY + st, par)) break;
+                if (!wait_slow(KEMPTY + st, par)) break;
                 copy(KFULL + st, sm + L::k + st * L::tile, src);
                 ++n_k;
-                if (!wait(VEMPTY + st, par)) break;
+                if (!wait_slow(VEMPTY + st, par)) break;
                 copy(VRAW + st, sm + L::v + st * L::tile, src + pt * kRow);
                 ++n_v;
             }
@@ -827,7 +839,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
             int32_t u_first = w.u;
             float lref = -INFINITY;
             for (uint32_t n = 0;; ++n) {
-                if (!wait(JEMPTY + n % kJobs, (n / kJobs & 1) ^ 1)) break;
+                if (!wait_slow(JEMPTY + n % kJobs, (n / kJobs & 1) ^ 1)) break;
                 Job &jb = jobs[n % kJobs];
                 if (w.left <= 0) {
                     if (lane == 0) {
@@ -862,7 +874,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                         lref = top;
                     }
                     lg = x == 0.f ? kPBits : x < INFINITY ? fmaxf(lg - lref, -100.f) + kPBits : NAN;
-                    if (lane < 8) jb.ks[lane] = fabsf(sc.x), jb.lg[lane] = lg, jb.back[lane] = exp2f(-lg);
+                    if (lane < 8) jb.ks[lane] = sc.x == 0.f ? 1e-30f : fabsf(sc.x), jb.lg[lane] = lg, jb.back[lane] = exp2f(-lg);
                     if (lane == 0) jb.lref = lref, jb.shift = shift;
                 }
                 if (lane == 0) {
