@@ -57,7 +57,7 @@ struct __align__(16) Job {
     int32_t base;                       // position of the sequence's first query
     int32_t row0, nrows, tok0, head;    // the row tile
     uint32_t live;                      // groups of 16 tokens that are there
-    int32_t s, last_cta, pmin, pmax;
+    int32_t last_cta, pmin, pmax, pad0;
     int32_t slot[8];                    // of each group: first token's slot in its page,
     int64_t rec[8];                     // its record's place in the pool (the pool's first where it is not there),
     float ks[8];                        // 8-bit: key scale, log2 of what the probabilities are scaled by,
@@ -833,69 +833,111 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
             for (uint32_t i = n_v > 2 ? n_v - 2 : 0; i < n_v; ++i) wait_bar(&bars[VRAW + (i & 1)], i >> 1 & 1, nullptr);
         } else if (warp == kWalkWarp) {
             // ================================================== the list of units
-            Walk w = start;
+            // Units go in batches of up to four of one item: lane i has group i % 8 of the batch's unit i / 8.
+            // A batch's pages are read two batches ahead and its scales one ahead: one unit at a time, the
+            // two reads one behind the other took 5,000 cycles a unit and held everything else up.
+            struct Batch {
+                Walk w;               // at its first unit
+                int32_t n, page, slot;
+                bool want;
+            };
+            auto look = [&](const Walk &x) {
+                Batch r;
+                r.w = x;
+                r.n = x.left > 0 ? (int32_t)min((int64_t)min(4, x.t.units - x.u), x.left) : 0;
+                r.page = r.slot = 0;
+                r.want = false;
+                if (r.n > 0) {
+                    const int32_t j = unit_token<kUnit>(x.t, x.u + lane / 8) + lane % 8 * 16, b = j / pt;
+                    r.slot = j - b * pt;
+                    r.want = lane / 8 < r.n && any_sees(a, x.t, j, 16);
+                    if (r.want) r.page = __ldg(a.kv.table + (int64_t)x.t.s * a.kv.max_pages + b);
+                }
+                return r;
+            };
+            auto after = [&](const Batch &x) {
+                Walk w = x.w;
+                w.left -= x.n;
+                w.u += x.n;
+                if (w.left > 0 && w.u == w.t.units) next_item<kRows, kUnit>(a, w);
+                return w;
+            };
+            auto record = [&](const Batch &x) { return x.want ? kv_record(a.kv, x.page, x.w.h) : nullptr; };
+            auto scales = [&](const uint8_t *rec) {
+                return FMT == KDA_KV_I8 && rec ? __ldg(reinterpret_cast<const float2 *>(rec + 2 * pt * kRow)) : make_float2(0.f, 0.f);
+            };
             if (lane == 0) a.split[blockIdx.x].last_cta = -1;
             const int64_t end = C > 0 ? (int64_t)(blockIdx.x + 1) * W / C : 0;
-            int32_t u_first = w.u;
+            Batch now = look(start), next = look(after(now));
+            const uint8_t *rec = record(now);
+            float2 sc = scales(rec);
+            int32_t u_first = start.u;
             float lref = -INFINITY;
-            for (uint32_t n = 0;; ++n) {
-                if (!wait_slow(JEMPTY + n % kJobs, (n / kJobs & 1) ^ 1)) break;
-                Job &jb = jobs[n % kJobs];
-                if (w.left <= 0) {
-                    if (lane == 0) {
-                        jb.flags = kStop;
-                        ptx::mbar_arrive(&bars[JFULL + n % kJobs]);
-                    }
-                    break;
-                }
-                const Tile &t = w.t;
-                const int32_t j0 = unit_token<kUnit>(t, w.u), j = j0 + 16 * lane;
-                const uint8_t *rec = nullptr;
-                if (lane < 8 && any_sees(a, t, j, 16))
-                    rec = kv_record(a.kv, __ldg(a.kv.table + (int64_t)t.s * a.kv.max_pages + j / pt), w.h);
-                const uint32_t live = __ballot_sync(0xFFFFFFFFu, rec != nullptr);
-                if (lane < 8) {
-                    jb.slot[lane] = j % pt;
-                    jb.rec[lane] = rec ? rec - a.kv.base : 0;
-                }
+            uint32_t n = 0;
+            bool ok = true;
+            while (ok && now.n > 0) {
+                const uint8_t *next_rec = record(next);
+                const float2 next_sc = scales(next_rec);
+                const Batch then = look(after(next));
+                const Tile &t = now.w.t;
+                const int32_t k = lane / 8, u = now.w.u + k, j0 = unit_token<kUnit>(t, u);
+                const int64_t left = now.w.left - k;
+                const uint32_t live = __ballot_sync(0xFFFFFFFFu, rec != nullptr) >> (8 * k) & 0xFFu;
+                if (now.w.u == u_first) lref = -INFINITY;
+                // 8-bit: ref moves up to a unit's largest value scale when that has doubled.  A scale of 0 stands
+                // for codes of 0: any factor does.
+                float lg = 0.f, shift = 1.f, my_ref = 0.f;
+                const float x = fabsf(sc.y);
                 if (FMT == KDA_KV_I8) {
-                    // ref moves up to the unit's largest value scale when that has doubled.  A scale of 0
-                    // stands for codes of 0: any factor does, so the largest other.
-                    const float2 sc = rec ? __ldg(reinterpret_cast<const float2 *>(rec + 2 * pt * kRow)) : make_float2(0.f, 0.f);
-                    const float x = fabsf(sc.y);
-                    float lg = x > 0.f && x < INFINITY ? log2f(x) : -INFINITY, top = lg;
+                    lg = x > 0.f && x < INFINITY ? log2f(x) : -INFINITY;
+                    float top = lg;
 #pragma unroll
                     for (int i = 1; i < 8; i <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, i));
-                    top = fmaxf(__shfl_sync(0xFFFFFFFFu, top, 0), -100.f);
-                    if (w.u == u_first) lref = -INFINITY;
-                    float shift = 1.f;
-                    if (top > lref + 1.f) {
-                        shift = exp2f(lref - top);
-                        lref = top;
+                    top = fmaxf(top, -100.f);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float ti = __shfl_sync(0xFFFFFFFFu, top, 8 * i);
+                        float si = 1.f;
+                        if (i < now.n && ti > lref + 1.f) {
+                            si = exp2f(lref - ti);
+                            lref = ti;
+                        }
+                        if (i == k) shift = si, my_ref = lref;
                     }
-                    lg = x == 0.f ? kPBits : x < INFINITY ? fmaxf(lg - lref, -100.f) + kPBits : NAN;
-                    if (lane < 8) jb.ks[lane] = sc.x == 0.f ? 1e-30f : fabsf(sc.x), jb.lg[lane] = lg, jb.back[lane] = exp2f(-lg);
-                    if (lane == 0) jb.lref = lref, jb.shift = shift;
+                    lg = x == 0.f ? kPBits : x < INFINITY ? fmaxf(lg - my_ref, -100.f) + kPBits : NAN;
                 }
-                if (lane == 0) {
-                    const bool ends = w.left >= t.units - w.u;   // the item's last unit is in this share
-                    jb.j0 = j0;
-                    jb.flags = (w.u == u_first ? kBegin : 0) | (w.u + 1 == t.units || w.left == 1 ? kEnd : 0) |
-                               (all_see(a, t, j0, kUnit) && live == 0xFFu ? kWhole : 0) | (u_first == 0 ? kStarts : 0) |
-                               (ends ? kEnds : 0);
-                    jb.base = t.q.len - t.q.n;
-                    jb.row0 = t.row0, jb.nrows = t.nrows, jb.tok0 = t.q.tok0, jb.head = w.h;
-                    jb.live = live;
-                    jb.s = t.s;
-                    jb.last_cta = ends ? (int32_t)blockIdx.x : cta_of(end - w.left + (t.units - 1 - w.u), W, C);
-                    jb.pmin = t.pmin, jb.pmax = t.pmax;
+                for (int i = 0; ok && i < now.n; ++i) ok = wait_slow(JEMPTY + (n + i) % kJobs, ((n + i) / kJobs & 1) ^ 1);
+                if (!ok) break;
+                if (k < now.n) {
+                    Job &jb = jobs[(n + k) % kJobs];
+                    const int i = lane % 8;
+                    jb.slot[i] = now.slot;
+                    jb.rec[i] = rec ? rec - a.kv.base : 0;
+                    if (FMT == KDA_KV_I8) jb.ks[i] = sc.x == 0.f ? 1e-30f : fabsf(sc.x), jb.lg[i] = lg, jb.back[i] = exp2f(-lg);
+                    if (i == 0) {
+                        const bool ends = left >= t.units - u;   // the item's last unit is in this share
+                        jb.j0 = j0;
+                        jb.flags = (u == u_first ? kBegin : 0) | (u + 1 == t.units || left == 1 ? kEnd : 0) |
+                                   (all_see(a, t, j0, kUnit) && live == 0xFFu ? kWhole : 0) | (u_first == 0 ? kStarts : 0) |
+                                   (ends ? kEnds : 0);
+                        jb.base = t.q.len - t.q.n;
+                        jb.row0 = t.row0, jb.nrows = t.nrows, jb.tok0 = t.q.tok0, jb.head = now.w.h;
+                        jb.live = live;
+                        jb.last_cta = ends ? (int32_t)blockIdx.x : cta_of(end - left + (t.units - 1 - u), W, C);
+                        jb.pmin = t.pmin, jb.pmax = t.pmax;
+                        if (FMT == KDA_KV_I8) jb.lref = my_ref, jb.shift = shift;
+                    }
                 }
-                tcx::warp_arrive(&bars[JFULL + n % kJobs]);
-                --w.left;
-                if (++w.u == w.t.units) {
-                    if (w.left > 0) next_item<kRows, kUnit>(a, w);
-                    u_first = 0;
-                }
+                __syncwarp();
+                if (lane % 8 == 0 && k < now.n) ptx::mbar_arrive(&bars[JFULL + (n + k) % kJobs]);
+                n += now.n;
+                if (next.w.u == 0) u_first = 0;
+                now = next, next = then;
+                rec = next_rec, sc = next_sc;
+            }
+            if (ok && wait_slow(JEMPTY + n % kJobs, (n / kJobs & 1) ^ 1) && lane == 0) {
+                jobs[n % kJobs].flags = kStop;
+                ptx::mbar_arrive(&bars[JFULL + n % kJobs]);
             }
         }
     }
