@@ -48,6 +48,9 @@ constexpr int kRows = kAttnPrefillRows, kHalf = 128, kUnit = 128;
 constexpr int kSoftWarps = 16, kLoadWarps = 8, kMmaWarp = 24, kCopyWarp = 25, kWalkWarp = 26, kThreads = 28 * 32;
 constexpr float kGrow = 8.f;            // bits that a row's maximum may grow before O is rescaled
 constexpr float kPBits = 6.f;           // 8-bit: bits that a probability is scaled up in fp16
+// What an item (a row tile of a head) costs beyond its units, in units: the share of a CTA counts it.
+// Its end stays in the pipe's way for one to two units' time, and its masked units take longer.
+constexpr int kItem = 2;
 constexpr int kJobs = 8;                // units handed out and not yet done with
 
 // A unit of work.
@@ -153,13 +156,13 @@ __device__ __forceinline__ void codes_to_half(uint4 c, uint4 &lo, uint4 &hi) {
     hi = make_uint4(r[4], r[5], r[6], r[7]);
 }
 
-// Units of sequence s over all heads, summed by a warp.
+// Units of sequence s over all heads and what its items add, summed by a warp.
 __device__ __forceinline__ int64_t seq_units(const AttnArgs &a, int s, int lane) {
     const KvSeq q = seq_of(a, s);
     const int n = tiles_of<kRows>(a, q);
     int64_t w = 0;
 #pragma unroll 1
-    for (int i = lane; i < n; i += 32) w += make_tile<kRows, kUnit>(a, s, q, i).units;
+    for (int i = lane; i < n; i += 32) w += make_tile<kRows, kUnit>(a, s, q, i).units + kItem;
     for (int i = 16; i; i >>= 1) w += __shfl_xor_sync(0xFFFFFFFFu, w, i);
     return w * a.kv.Hkv;
 }
@@ -195,7 +198,7 @@ __device__ __forceinline__ void find_share(const AttnArgs &a, int64_t *sums, Wal
 #pragma unroll 1
             for (int base = 0;; base += 32) {           // the tile: prefix sums over 32 tiles at a time
                 const int rt = base + lane, n = tiles_of<kRows>(a, q);
-                const int64_t mine = rt < n ? (int64_t)make_tile<kRows, kUnit>(a, s, q, rt).units * a.kv.Hkv : 0;
+                const int64_t mine = rt < n ? (int64_t)(make_tile<kRows, kUnit>(a, s, q, rt).units + kItem) * a.kv.Hkv : 0;
                 int64_t x = mine;
                 for (int j = 1; j < 32; j <<= 1) {
                     const int64_t y = __shfl_up_sync(0xFFFFFFFFu, x, j);
@@ -210,9 +213,13 @@ __device__ __forceinline__ void find_share(const AttnArgs &a, int64_t *sums, Wal
                 }
                 at -= __shfl_sync(0xFFFFFFFFu, x, 31);
             }
-            w.h = (int32_t)(at / w.t.units);
-            w.u = (int32_t)(at % w.t.units);
+            w.h = (int32_t)(at / (w.t.units + kItem));
+            w.u = (int32_t)(at % (w.t.units + kItem));
             w.left = end - begin;
+            if (w.u >= w.t.units) {                     // behind the units of an item: on to the next one
+                w.left -= w.t.units + kItem - w.u;
+                if (w.left > 0) next_item<kRows, kUnit>(a, w);
+            }
         }
         __syncwarp();
         if (lane == 0) {
@@ -296,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
         auto wait_half = [&](int b, uint32_t parity) {                         // the half's eight warps
             return wait_together<kSoftWarps / 2 * 32>(&bars[b], parity, err, warp % 8 == 0, 9 + half);
         };
-        uint32_t n_s = 0, n_item = 0;   // units of this half, items so far: the barriers' parities
+        uint32_t n_s = 0, n_item = 0, n_o = 0;   // units of this half, items so far, of this half: the barriers' parities
         int32_t pos = -1, p_lo = 0, p_hi = 0;   // positions of this row, of the warp's rows
         bool in = false, ok = true;
         float m = -INFINITY, l = 0.f, f_row = 0.f;
@@ -405,13 +412,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
             }
             // ---- O to the new references
             if (__any_sync(0xFFFFFFFFu, grown != 1.f || odd)) {
-                if (!(flags & kBegin)) {
-                    ok = wait(OFULL + half, (n_s - 1) & 1);
-                    if (!ok) break;
-                    ptx::tc_fence_after();
-                } else {
-                    ptx::tmem_wait_st();
-                }
+                // the products of the last unit are done, for the scores of this one came after them
+                if (flags & kBegin) ptx::tmem_wait_st();
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
                     float o[16];
@@ -497,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                     l += other[row];
                     meet();              // the next item's first maxima go to the same place
                 }
-                ok = wait_half(OFULL + half, (n_s - 1) & 1);
+                ok = wait_half(OFULL + half, n_o++ & 1);
                 if (!ok) break;
                 ptx::tc_fence_after();
                 const bool all = (flags & kStarts) && (flags & kEnds);
@@ -748,58 +750,72 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                 for (int s = 0; s < kUnit / 16; ++s)   // probabilities: 32 columns in each half of the scores
                     ptx::mma_bf16_ta(tu + 256 + half * 128, tu + half * 128 + (s >> 2) * 64 + (s & 3) * 8, vd + (s * 2048 >> 4),
                                      idesc<FMT>(128, D, 1), 1u);
-                ptx::mma_commit(&bars[OFULL + half]);
             };
-            auto commit = [&](int b) {
-                if (elect()) ptx::mma_commit(&bars[b]);
+            // Wait for up to four barriers at once, lane i for the i-th: beside the other warps' work a wait
+            // costs this one 250 cycles even where the barrier's phase is over, four of them a quarter of a unit.
+            auto wait_set = [&](int count, int b0, uint32_t p0, int b1, uint32_t p1, int b2, uint32_t p2, int b3, uint32_t p3) {
+                const int b = lane == 0 ? b0 : lane == 1 ? b1 : lane == 2 ? b2 : b3;
+                const uint32_t par = (lane == 0 ? p0 : lane == 1 ? p1 : lane == 2 ? p2 : p3) & 1;
+                bool there = lane >= count;
+#pragma unroll 1
+                for (uint32_t i = 0; i < ptx::kSpinLimit; ++i) {
+                    if (!there) there = ptx::mbar_try_wait(&bars[b], par);
+                    if (__all_sync(0xFFFFFFFFu, there)) return true;
+                    if (__any_sync(0xFFFFFFFFu, *err != 0)) return false;
+                }
+                *err = 1;
+                return false;
+            };
+            // a half's outputs of unit n, and its scores of the next, whose completion says both
+            auto issue = [&](uint32_t n, int h, bool more, bool unit_done, bool item_done) {
+                const int st = n & 1, nx = st ^ 1;
+                ptx::tc_fence_after();
+                if (elect()) {
+                    outputs(h, st);
+                    if (more) scores(h, nx);
+                    else ptx::mma_commit(&bars[OFULL + h]);
+                    if (unit_done) {
+                        ptx::mma_commit(&bars[VEMPTY + st]);
+                        if (more) ptx::mma_commit(&bars[KEMPTY + nx]);
+                        if (item_done) ptx::mma_commit(&bars[QEMPTY]);
+                    }
+                }
                 __syncwarp();
             };
-            bool ok = true;
-            for (uint32_t n = 0; ok; ++n) {
-                ok = wait_job(n);
-                if (!ok) break;
-                const int32_t flags = job(n).flags;
-                if (flags & kStop) break;
-                const int halves = job(n).nrows > kHalf ? 2 : 1, st = n & 1, nx = st ^ 1;
-                done(n);
+            bool ok = wait_job(0);
+            int32_t flags = ok ? job(0).flags : kStop, nrows = job(0).nrows;
+            for (uint32_t n = 0; !(flags & kStop); ++n) {
+                const int st = n & 1, nx = st ^ 1;
+                const bool two = nrows > kHalf, more = !(flags & kEnd);
                 // the scores of an item's first unit; those of the next follow each half's outputs
                 if (flags & kBegin) {
-                    ok = wait(QFULL, n_item & 1) && wait(KFULL + st, n >> 1 & 1);
-                    if (!ok) break;
+                    if (!wait_set(2, QFULL, n_item, KFULL + st, n >> 1, 0, 0, 0, 0)) break;
                     ptx::tc_fence_after();
                     if (elect()) {
-                        for (int h = 0; h < halves; ++h) scores(h, st);
+                        scores(0, st);
+                        if (two) scores(1, st);
                         ptx::mma_commit(&bars[KEMPTY + st]);
                         if (flags & kEnd) ptx::mma_commit(&bars[QEMPTY]);
                     }
                     __syncwarp();
                     ++n_item;
                 }
-                const bool more = !(flags & kEnd);
-                ok = wait(VFULL + st, n >> 1 & 1) && (!more || (wait(KFULL + nx, (n + 1) >> 1 & 1) && wait_job(n + 1)));
-                if (!ok) break;
-                // the item's last scores: its queries may go when they are done
-                const bool last = more && (job(n + 1).flags & kEnd);
-#pragma unroll 1
-                for (int h = 0; h < halves; ++h) {
-                    ok = wait(PFULL + h, n_p[h] & 1);
-                    if (!ok) break;
-                    if (h) ++n_p[1];
-                    else ++n_p[0];
-                    ptx::tc_fence_after();
-                    if (elect()) {
-                        outputs(h, st);
-                        if (more) scores(h, nx);
-                        if (h + 1 == halves) {
-                            ptx::mma_commit(&bars[VEMPTY + st]);
-                            if (more) ptx::mma_commit(&bars[KEMPTY + nx]);
-                            if (last) ptx::mma_commit(&bars[QEMPTY]);
-                        }
-                    }
-                    __syncwarp();
+                if (!wait_set(more ? 4 : 3, PFULL, n_p[0]++, VFULL + st, n >> 1, JFULL + (n + 1) % kJobs, (n + 1) / kJobs,
+                              KFULL + nx, (n + 1) >> 1))
+                    break;
+                // with the scores of an item's last unit done its queries may go
+                const int32_t next_flags = job(n + 1).flags, next_nrows = job(n + 1).nrows;
+                const bool last = more && (next_flags & kEnd);
+                issue(n, 0, more, !two, last);
+                if (two) {
+                    if (!wait(PFULL + 1, n_p[1]++ & 1)) break;
+                    issue(n, 1, more, true, last);
                 }
+                done(n);
+                flags = next_flags, nrows = next_nrows;
             }
-            commit(DRAIN);
+            if (elect()) ptx::mma_commit(&bars[DRAIN]);
+            __syncwarp();
             wait_bar(&bars[DRAIN], 0, nullptr);
         } else if (FMT == KDA_KV_BF16 && warp == kCopyWarp) {
             // ================================================== copies (16-bit cache)
@@ -834,8 +850,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
         } else if (warp == kWalkWarp) {
             // ================================================== the list of units
             // Units go in batches of up to four of one item: lane i has group i % 8 of the batch's unit i / 8.
-            // A batch's pages are read two batches ahead and its scales one ahead: one unit at a time, the
-            // two reads one behind the other took 5,000 cycles a unit and held everything else up.
+            // A batch's pages are read two batches ahead and its scales one ahead, so that the walk waits for
+            // memory once in four units and not twice in each.
             struct Batch {
                 Walk w;               // at its first unit
                 int32_t n, page, slot;
@@ -859,7 +875,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                 Walk w = x.w;
                 w.left -= x.n;
                 w.u += x.n;
-                if (w.left > 0 && w.u == w.t.units) next_item<kRows, kUnit>(a, w);
+                if (w.left > 0 && w.u == w.t.units) {
+                    w.left -= kItem;
+                    if (w.left > 0) next_item<kRows, kUnit>(a, w);
+                }
                 return w;
             };
             auto record = [&](const Batch &x) { return x.want ? kv_record(a.kv, x.page, x.w.h) : nullptr; };
