@@ -450,7 +450,7 @@ int kda_ckpt_restore_q8(kda_pool *pool, int32_t H, int32_t d, int32_t dtype, int
  *
  * Token tensors q, k, v are [T_tot][H][d] in dtype with token rows `stride` elements apart (at
  * least H * d: the parts of one fused projection will do); pointers are 16-byte aligned and
- * strides multiples of 16 bytes.  d is 64 or 128. */
+ * strides multiples of 16 bytes.  d is 64 or 128.  max_pages * page_tokens is at most 2^30. */
 #define KDA_KV_BF16 0
 #define KDA_KV_I8 1
 
@@ -504,7 +504,8 @@ int64_t kda_attn_workspace_bytes(int32_t Hq, int32_t Hkv, int32_t d, int32_t dty
  * lse = -infinity.  What a query does not see never changes its result, a NaN or an infinity
  * included; pages that no query of the call sees are not read, and their table entries may hold
  * anything.  Sums, maxima and accumulators are fp32; KDA_F32 calls keep fp32 accuracy throughout.
- * Results do not depend on timing: the same call gives the same bits. */
+ * KDA_KV_I8: a block whose value scale is 2^30 times smaller than an earlier one's of its sequence
+ * may add nothing to o.  Results do not depend on timing: the same call gives the same bits. */
 int kda_attn_paged(const kda_pool *pool, int32_t Hq, int32_t Hkv, int32_t d, int32_t dtype, int32_t fmt,
                    int32_t page_tokens, int32_t nseq, int64_t T_tot, int32_t max_q, const int32_t *cu_q,
                    const int32_t *kv_len, const int32_t *page_table, int32_t max_pages, const void *q,

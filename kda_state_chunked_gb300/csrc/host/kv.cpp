@@ -9,7 +9,7 @@
 
 namespace {
 
-constexpr int64_t kWholeTokens = 384;      // visible tokens up to which an item is not split
+constexpr int64_t kWholeUnits = 6;         // units up to which an item of the register kernel is not split
 constexpr int64_t kMaxTokens = 1 << 30;   // of a sequence: the kernels' positions and their differences fit int32
 
 int64_t elem_size(int32_t dtype) { return dtype == KDA_BF16 ? 2 : 4; }
@@ -58,11 +58,15 @@ bool valid_batch(int32_t nseq, int64_t T_tot, int32_t max_q, int32_t dtype) {
 
 int status_of(cudaError_t e) { return e == cudaSuccess ? KDA_OK : KDA_ECUDA; }
 
-// Rows of a tile.  The register kernel holds 16 rows and is bound by the cache's bytes; with more
-// rows a sequence it would read the cache again for every 16, so the tensor-memory kernel takes
-// them.  float32 calls stay on the register kernel: its products split an operand into terms.
-int32_t attn_rows(int32_t dtype, int32_t max_q, int32_t G) {
-    return dtype == KDA_F32 || (int64_t)max_q * G <= kda::kAttnDecodeRows ? kda::kAttnDecodeRows : kda::kAttnPrefillRows;
+// Rows of a tile.  The register kernel holds 16 rows; with more rows a sequence it reads the cache
+// again for every 16, while a tile of the tensor-memory kernel takes 256 of them in the same time.  32
+// sequences of 4096 tokens and 8 heads of 128, with 16, 32 and 64 rows a head: 8-bit cache 74, 127 and
+// 237 us by the first, 165, 166 and 169 by the second; 16-bit cache with 16 and 32 rows 102 and 185
+// against 117 and 118.  float32 calls stay on the register kernel: its products split an operand into
+// terms.
+int32_t attn_rows(int32_t dtype, int32_t fmt, int32_t max_q, int32_t G) {
+    const int64_t most = fmt == KDA_KV_I8 ? 2 * kda::kAttnDecodeRows : kda::kAttnDecodeRows;
+    return dtype == KDA_F32 || (int64_t)max_q * G <= most ? kda::kAttnDecodeRows : kda::kAttnPrefillRows;
 }
 
 // Workspace of an attention call: [AttnSplit per CTA][partial results].
@@ -133,7 +137,8 @@ int64_t kda_attn_workspace_bytes(int32_t Hq, int32_t Hkv, int32_t d, int32_t dty
                                  int32_t max_q) {
     if (Hkv <= 0 || Hq <= 0 || Hq > 4096 || Hq % Hkv || (d != 64 && d != 128) || !valid_batch(nseq, T_tot, max_q, dtype))
         return KDA_EINVAL;
-    return attn_ws(d, attn_rows(dtype, max_q, Hq / Hkv)).total;
+    return std::max(attn_ws(d, attn_rows(dtype, KDA_KV_BF16, max_q, Hq / Hkv)).total,
+                    attn_ws(d, attn_rows(dtype, KDA_KV_I8, max_q, Hq / Hkv)).total);   // serves either format
 }
 
 int kda_attn_paged(const kda_pool *pool, int32_t Hq, int32_t Hkv, int32_t d, int32_t dtype, int32_t fmt,
@@ -160,7 +165,7 @@ int kda_attn_paged(const kda_pool *pool, int32_t Hq, int32_t Hkv, int32_t d, int
     const int32_t longest = max_pages * page_tokens;
     a.scale = scale; a.window = window >= longest ? 0 : window; a.sinks = std::min(sinks, longest);
     a.o = o; a.lse = lse;
-    const int32_t rows = attn_rows(dtype, max_q, a.G);
+    const int32_t rows = attn_rows(dtype, fmt, max_q, a.G);
     const AttnWs w = attn_ws(d, rows);
     // the most units that the call can have bounds the CTAs worth launching
     const int64_t tiles = T_tot * a.G / rows + nseq;
@@ -168,12 +173,13 @@ int kda_attn_paged(const kda_pool *pool, int32_t Hq, int32_t Hkv, int32_t d, int
     if (a.window) tokens = std::min<int64_t>(tokens, (int64_t)a.window + a.sinks + max_q + 3 * kda::kAttnMinUnit);
     const int64_t units = std::max<int64_t>(1, (tokens + kda::kAttnMinUnit - 1) / kda::kAttnMinUnit);
     a.ctas = (int32_t)std::min<int64_t>(attn_ctas(rows), std::max<int64_t>(1, tiles * Hkv * units));
-    // Few, short items: a CTA each, which then takes all of its loads ahead; splitting them would cost
-    // another launch to join the parts.
+    // Few, short items: a CTA each; splitting them costs another launch to join the parts.  64 items of
+    // 256, 640 and 1000 tokens of an 8-bit cache (2, 5 and 8 units): 6.7, 9.6 and 12.4 us whole, 10.0,
+    // 12.7 and 14.0 split; of 384 tokens of a 16-bit one (6 units) 7.8 and 11.0; but 4 items of 8 units
+    // 12.1 and 11.0.
     a.whole = rows == kda::kAttnDecodeRows && (int64_t)max_q * a.G <= rows && (int64_t)nseq * Hkv <= kda::kAttnSms &&
-              tokens <= kWholeTokens;
+              tokens <= kWholeUnits * (fmt == KDA_KV_I8 ? 128 : 64);
     if (a.whole) a.ctas = nseq * Hkv;
-    a.deep = rows == kda::kAttnDecodeRows && a.ctas <= kda::kAttnSms;
     a.split = static_cast<kda::AttnSplit *>(workspace);
     a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + w.o_part);
     return status_of(rows == kda::kAttnDecodeRows ? kda::launch_attn_decode(a, static_cast<cudaStream_t>(stream))

@@ -219,7 +219,6 @@ struct AttnArgs {
     float *lse;                   // [T_tot][Hq] or null
     int32_t ctas;                 // CTAs the units are shared out over
     int32_t whole;                // register kernel: a CTA takes one whole item instead, and nothing is joined
-    int32_t deep;                 // register kernel: an SM has one CTA, with a longer ring of loads
     float *part;                  // [ctas][2][rows][d + 2]: m, l and unnormalised o of partial items
     AttnSplit *split;             // [ctas]
 };
