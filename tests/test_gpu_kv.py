@@ -147,6 +147,26 @@ def test_long_context_is_joined_from_many_parts(fmt):
     Case([(1, 40000)], Hkv=1, G=8, fmt=fmt, seed=7).on_gpu().check()
 
 
+@pytest.mark.parametrize("fmt,d", [(f, d) for f in (ref.I8, ref.BF16) for d in (64, 128)])
+@pytest.mark.parametrize("n", [4, 5, 8, 9])
+def test_rows_around_a_tile(fmt, d, n):
+    # 16, 20, 32 and 36 rows a head: either side of where the kernels change over
+    Case([(n, 300), (n, n), (1, 77), (0, 5), (n, 1500)], fmt=fmt, d=d, Hkv=2, G=4, seed=31 + n).on_gpu().check(120, 3)
+
+
+@pytest.mark.parametrize("fmt", [ref.I8, ref.BF16])
+def test_short_items_beside_a_long_one(fmt):
+    # items of one unit, several to a share, and a long one that many shares take
+    lens = [(1 + 7 * i % 40, 41 + 5 * i) for i in range(60)]
+    Case(lens + [(40, 6000)] + lens[:20], fmt=fmt, Hkv=4, G=2, seed=41).on_gpu().check()
+
+
+@pytest.mark.parametrize("fmt", [ref.I8, ref.BF16])
+@pytest.mark.parametrize("tokens", [383, 385, 640, 767, 769])
+def test_lengths_around_unsplit_items(fmt, tokens):
+    Case([(1, tokens), (1, 5), (2, tokens - 1)], fmt=fmt, Hkv=2, G=4, seed=51).on_gpu().check()
+
+
 def test_wide_value_scales():
     """Blocks whose scales lie many powers of ten apart keep their precision."""
     Case([(1, 900), (2, 500)], fmt=ref.I8, dtype="f32", spread=6.0, qscale=1e-3, seed=8).on_gpu().check()
