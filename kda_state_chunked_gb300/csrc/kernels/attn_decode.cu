@@ -614,9 +614,19 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
                         ldsm4t(w, kb + unit(v_at, 2 * i) + y * 16 * kLine);
                         auto columns = [&](int j, const uint32_t (&af)[4]) {
 #pragma unroll
-                            for (int x = 0; x < NR; ++x)
+                            for (int x = 0; x < NR; ++x) {
+                                if constexpr (NT == 1) {
+                                    mma<FMT>(o[x][j], af, pb[y][x][0][0], pb[y][x][1][0]);
+                                } else {
+                                    // the matrix unit's sums are cut, not rounded: over a long context their
+                                    // bias came to 2e-6 of a float32 result, so each group's is added here
+                                    float d[4] = {};
 #pragma unroll
-                                for (int z = NT - 1; z >= 0; --z) mma<FMT>(o[x][j], af, pb[y][x][0][z], pb[y][x][1][z]);
+                                    for (int z = NT - 1; z >= 0; --z) mma<FMT>(d, af, pb[y][x][0][z], pb[y][x][1][z]);
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) o[x][j][e] += d[e];
+                                }
+                            }
                         };
                         if constexpr (FMT == KDA_KV_I8) {
                             // a register holds columns 2 g, 2 g + 1 of two tokens: output tile j has the even

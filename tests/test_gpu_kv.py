@@ -167,6 +167,34 @@ def test_lengths_around_unsplit_items(fmt, tokens):
     Case([(1, tokens), (1, 5), (2, tokens - 1)], fmt=fmt, Hkv=2, G=4, seed=51).on_gpu().check()
 
 
+# A score of up to 8 kept to 23 bits is off by 5e-7 at most, and so is its probability; the exponential
+# adds 2 ulp (2.4e-7), and sums of some 50 rounded terms a warp 2e-7: under 1e-6 of the result's size,
+# taken one and a half times.
+@pytest.mark.parametrize("fmt", [ref.I8, ref.BF16])
+def test_float32_sums_over_long_contexts_keep_their_bits(fmt):
+    nseq, L, G, d, pt = 40, 40000, 8, 64, 64
+    g = torch.Generator(device=DEV).manual_seed(61)
+    blocks = L // pt
+    pool = kda.Pool(kda.kda_kv_page_bytes(1, d, FMT[fmt], pt), nseq * blocks, DEV)
+    table = torch.randperm(nseq * blocks, generator=g, device=DEV).to(torch.int32).reshape(nseq, blocks)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    k, v = (torch.randn(nseq * L, 1, d, generator=g, device=DEV) for _ in range(2))
+    lens, begin = i32([L] * nseq), i32([0] * nseq)
+    kda.kda_kv_append(pool, FMT[fmt], pt, i32(np.arange(nseq + 1) * L), lens, table, L, None, k, v, None, None, status)
+    kda.kda_kv_gather(pool, FMT[fmt], pt, i32(np.arange(nseq + 1) * L), begin, table, k, v, status)
+    q = torch.randn(nseq, G, d, generator=g, device=DEV)
+    o = torch.empty_like(q)
+    kda.kda_attn_paged(pool, 1, FMT[fmt], pt, i32(np.arange(nseq + 1)), lens, table, 1, q, o, kda.attn_workspace(q, 1, nseq, 1),
+                       status)
+    assert kda.kda_sync_status(status) == (kda.KDA_OK, 0)
+    wrong = size = 0.0
+    for s in range(nseq):
+        ks, vs = k[s * L:(s + 1) * L, 0].double(), v[s * L:(s + 1) * L, 0].double()
+        e = torch.softmax(q[s].double() @ ks.T * d ** -0.5, dim=1) @ vs
+        wrong, size = wrong + float((o[s].double() - e).pow(2).sum()), size + float(e.pow(2).sum())
+    assert (wrong / size) ** 0.5 <= 1.5e-6
+
+
 def test_wide_value_scales():
     """Blocks whose scales lie many powers of ten apart keep their precision."""
     Case([(1, 900), (2, 500)], fmt=ref.I8, dtype="f32", spread=6.0, qscale=1e-3, seed=8).on_gpu().check()
