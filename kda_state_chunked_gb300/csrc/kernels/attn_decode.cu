@@ -19,7 +19,7 @@
 //
 // Measured (d = 128): 32 contexts of 512 to 32768 tokens, 8-bit: 200 us, 6.1 TB/s, 91% of the copy
 // rate; one of 1,048,576 tokens: 186 us, 86%; 256 requests through a window of 1024, 16-bit: 172 us,
-// 87%.  4 float32 drafts of 24 requests, 8-bit, d = 64: 28.6 us, where the products count (two or four
+// 87%.  4 float32 drafts of 24 requests, 8-bit, d = 64: 28.8 us, where the products count (two or four
 // for each of the 16-bit forms' one) and the split leaves 1.5 steps a warp.
 //
 // 8-bit cache: codes c become fp16 exactly (the byte under the exponent of 1024, less 1152), a
