@@ -75,7 +75,8 @@ struct __align__(16) Job {
     float ks[8];                        // 8-bit: key scale, log2 of what the probabilities are scaled by,
     float lg[8], back[8];               // and the inverse of that
     float lref, shift;                  // log2 of ref, and by what O follows its last move
-    int32_t pad[2];
+    uint32_t nans;                      // groups whose value scale is no number
+    int32_t pad;
 };
 
 template <int D>
@@ -489,6 +490,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                             p[i] = __uint_as_float(pack2<FMT>(y.x, y.y));
                         }
                         l += (part.x + part.y) * back;
+                        if (FMT == KDA_KV_I8 && (jb.nans >> (4 * side + c) & 1u)) {   // fp16 NaN where the row sees it
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                p[i] = __uint_as_float((see & 1u << 2 * i ? 0x7E00u : 0u) | (see & 2u << 2 * i ? 0x7E000000u : 0u));
+                        }
                     }
                     ptx::tmem_st8(tS + 8 * c, p);
                 });
@@ -913,7 +919,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                 const uint32_t live = __ballot_sync(0xFFFFFFFFu, rec != nullptr) >> (8 * k) & 0xFFu;
                 if (now.w.u == u_first) lref = -INFINITY;
                 // 8-bit: ref moves up to a unit's largest value scale when that has doubled.  A scale of 0 stands
-                // for codes of 0: any factor does.
+                // for codes of 0: any factor does.  So it does for one that is no number: the softmax makes the
+                // probabilities NaN where they are seen, and the sums, which have no part in the values, stay.
                 float lg = 0.f, shift = 1.f, my_ref = 0.f;
                 const float x = fabsf(sc.y);
                 if (FMT == KDA_KV_I8) {
@@ -932,8 +939,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                         }
                         if (i == k) shift = si, my_ref = lref;
                     }
-                    lg = x == 0.f ? kPBits : x < INFINITY ? fmaxf(lg - my_ref, -100.f) + kPBits : NAN;
+                    lg = x > 0.f && x < INFINITY ? fmaxf(lg - my_ref, -100.f) + kPBits : kPBits;
                 }
+                const uint32_t nans = __ballot_sync(0xFFFFFFFFu, !(x < INFINITY)) >> (8 * k) & 0xFFu;
                 for (int i = 0; ok && i < now.n; ++i) ok = wait_slow(JEMPTY + (n + i) % kJobs, ((n + i) / kJobs & 1) ^ 1);
                 if (!ok) break;
                 if (k < now.n) {
@@ -953,7 +961,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                         jb.live = live;
                         jb.last_cta = ends ? (int32_t)blockIdx.x : cta_of(end - left + (t.units - 1 - u), W, C);
                         jb.pmin = t.pmin, jb.pmax = t.pmax;
-                        if (FMT == KDA_KV_I8) jb.lref = my_ref, jb.shift = shift;
+                        if (FMT == KDA_KV_I8) jb.lref = my_ref, jb.shift = shift, jb.nans = nans;
                     }
                 }
                 __syncwarp();

@@ -1,0 +1,101 @@
+"""Edges of the paged attention and the append, each query row by itself.
+
+A row's error is taken over its own columns (root mean square) and held against that row's own
+answer e = sum_j p_j v_j, not against the largest of the call:
+
+    rms(o - e) <= u_o rms(e) + u_p sqrt(sum_j p_j^2 mean_c v_jc^2)
+
+u_o: the output's rounding, 2^-8 of bf16 (8 bits); u_p: the probabilities', 2^-8 where they enter
+the product as bf16 (16-bit cache), 2^-11 as fp16 (8-bit cache), independent from token to token.
+Either gets 1e-5 for fp32 scores: sums of |scale q k log2 e| up to 30 in eight steps, each cut at
+2^-24 of that, times ln 2; float32 calls have nothing else.  A log-sum-exp is held to
+1e-5 (1 + |lse|)."""
+import numpy as np
+import pytest
+import torch
+
+import kda_state_chunked_gb300 as kda
+import kv_ref as ref
+from test_gpu_kv import Case
+
+pytestmark = pytest.mark.gpu
+
+U_O = {"bf16": 2.0 ** -8 + 1e-5, "f32": 1e-5}
+
+
+def u_p(c):
+    return 1e-5 + (0 if c.dtype == "f32" else 2.0 ** -11 if c.fmt == ref.I8 else 2.0 ** -8)
+
+
+def exact(c, window=0, sinks=0, scale=None, lose=None):
+    """o, lse and the probabilities' root sum of squares of every row in 64 bits.  A token whose key
+    or value is no number makes the rows that see it NaN and reaches no other.  lose: positions to
+    leave out (a planted mistake)."""
+    vals, G, d = ref.values(c.stored, c.scales), c.G, c.d
+    scale = d ** -0.5 if scale is None else scale
+    o = np.zeros((c.T, G * c.Hkv, d))
+    lse, noise = np.full(o.shape[:2], -np.inf), np.zeros(o.shape[:2])
+    for s, (n, L) in enumerate(zip(np.diff(c.cu), c.kv_len)):
+        if not n or not L:
+            continue
+        j, p = np.arange(L), L - n + np.arange(n)[:, None]
+        see = j <= p
+        if window:
+            see &= (j > p - window) | (j < sinks)
+        if lose is not None:
+            see &= ~np.isin(j, lose)
+        page, slot = np.asarray(c.table[s])[j // c.pt], j % c.pt
+        for h in range(G * c.Hkv):
+            k, v = vals[page, h // G, 0, slot], vals[page, h // G, 1, slot]
+            bad_k, bad_v = ~np.isfinite(k).all(1), ~np.isfinite(v).all(1)
+            k, v = np.where(bad_k[:, None], 0, k), np.where(bad_v[:, None], 0, v)
+            x = np.where(see, scale * (c.q[c.cu[s]:c.cu[s] + n, h].astype(np.float64) @ k.T), -np.inf)
+            m = x.max(1, keepdims=True)
+            e = np.exp(x - np.where(np.isfinite(m), m, 0))
+            l = e.sum(1, keepdims=True)
+            w = e / np.where(l > 0, l, 1)
+            rows = slice(c.cu[s], c.cu[s] + n)
+            with np.errstate(divide="ignore"):
+                z = m + np.log(l)
+            poisoned = (see & bad_k).any(1, keepdims=True)
+            lse[rows, h] = np.where(poisoned, np.nan, np.where(l > 0, z, -np.inf))[:, 0]
+            o[rows, h] = np.where(poisoned | (see & bad_v).any(1, keepdims=True), np.nan, w @ v)
+            noise[rows, h] = np.sqrt(w ** 2 @ (v ** 2).mean(1))
+    return o, lse, noise
+
+
+def hold(c, o, lse, want):
+    e, el, noise = want
+    o, lse = o.double().cpu().numpy(), lse.double().cpu().numpy()
+    assert np.array_equal(np.isnan(o), np.isnan(e)) and np.array_equal(np.isnan(lse), np.isnan(el))
+    assert np.array_equal(np.isneginf(lse), np.isneginf(el))
+    fine = ~np.isnan(e).any(-1)
+    rms = lambda x: np.sqrt((x[fine] ** 2).mean(-1))  # noqa: E731
+    over = rms(o - e) / np.maximum(U_O[c.dtype] * rms(e) + u_p(c) * noise[fine], 1e-300)
+    assert over.size == 0 or over.max() <= 1, over.max()
+    fine = np.isfinite(el)
+    assert (np.abs(lse - el)[fine] <= 1e-5 * (1 + np.abs(el[fine]))).all()
+
+
+def check(c, window=0, sinks=0, **kw):
+    o, lse = c.on_gpu().attend(window, sinks, **kw)
+    assert kda.kda_sync_status(c.status) == (kda.KDA_OK, 0)
+    hold(c, o, lse, exact(c, window, sinks, kw.get("scale")))
+    return o, lse
+
+
+# ------------------------------------------------------------------ scales that are no numbers
+@pytest.mark.parametrize("which,bad", [(0, np.nan), (1, np.nan), (1, np.inf)])
+@pytest.mark.parametrize("G,n,pt", [(1, 40, 16), (1, 150, 48), (5, 40, 16), (2, 3, 16)])
+def test_rows_before_a_block_that_is_no_number_keep_their_results(which, bad, G, n, pt):
+    # block 12 begins in the middle of a warp's rows: those before it do not see it
+    c = Case([(n, 12 * pt + n // 2 + 1), (n, n + 7)], fmt=ref.I8, Hkv=2, G=G, pt=pt, seed=101)
+    c.scales[c.table[0, 12], :, which] = bad
+    c.scales[c.table[1, (n + 6) // pt], :, which] = bad
+    o, _ = check(c)
+    assert torch.isfinite(o).any() and torch.isnan(o).any()
+    # and the rows whose window has left it
+    c = Case([(n, 200), (n, n + 90)], fmt=ref.I8, Hkv=2, G=G, pt=pt, seed=102)
+    for s, (_, L) in enumerate(c.lens):
+        c.scales[c.table[s, (L - n // 2 - 40) // pt], :, which] = bad
+    check(c, window=41)
