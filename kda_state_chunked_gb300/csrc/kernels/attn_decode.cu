@@ -510,6 +510,12 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
                 }
             }
             // ---- softmax
+            // A score's factor.  A product too small for a number of its own becomes a small one, for a masked
+            // score, -infinity, has to stay that; |c| < 2^25 there, so a seen score is 0 by either.
+            auto factor = [&](int y, int x, int r) {
+                const float f = rs[x][r] * ks[y];
+                return FMT == KDA_KV_I8 && f < 1e-37f ? 1e-37f : f;
+            };
             const bool whole = there == (1u << kGr) - 1u && (jb.whole >> warp & 1u);
             if (!whole)   // rows not in use may see what they like
 #pragma unroll
@@ -529,8 +535,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
                 for (int r = 0; r < 2; ++r) {
                     top[x][r] = -INFINITY;
 #pragma unroll
-                    for (int y = 0; y < kGr; ++y) top[x][r] = fmaxf(top[x][r], fmaxf(c[y][x][r], c[y][x][r + 2]) * ks[y]);
-                    top[x][r] *= rs[x][r];
+                    for (int y = 0; y < kGr; ++y) top[x][r] = fmaxf(top[x][r], fmaxf(c[y][x][r], c[y][x][r + 2]) * factor(y, x, r));
                     grown |= top[x][r] > m[x][r] + kGrow;
                 }
 #pragma unroll
@@ -575,7 +580,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int r = e & 1;
-                        p[e] = ex2(fmaf(c[y][x][e], rs[x][r] * ks[y], m[x][r] == -INFINITY ? 0.f : -m[x][r]));
+                        p[e] = ex2(fmaf(c[y][x][e], factor(y, x, r), m[x][r] == -INFINITY ? 0.f : -m[x][r]));
                         if (FMT == KDA_KV_I8 && strange && c[y][x][e] == -INFINITY) p[e] = 0.f;
                         l[x][r] += p[e];
                         if (FMT == KDA_KV_I8) p[e] = strange && p[e] == 0.f ? 0.f : p[e] * pv;

@@ -16,7 +16,7 @@ import torch
 
 import kda_state_chunked_gb300 as kda
 import kv_ref as ref
-from test_gpu_kv import Case
+from test_gpu_kv import KINDS, Case
 
 pytestmark = pytest.mark.gpu
 
@@ -99,3 +99,16 @@ def test_rows_before_a_block_that_is_no_number_keep_their_results(which, bad, G,
     for s, (_, L) in enumerate(c.lens):
         c.scales[c.table[s, (L - n // 2 - 40) // pt], :, which] = bad
     check(c, window=41)
+
+
+# ------------------------------------------------------------------ blocks of zero keys, scale 0
+@pytest.mark.parametrize("fmt,dtype,d", KINDS)
+@pytest.mark.parametrize("n", [1, 3, 40])
+@pytest.mark.parametrize("qscale,scale", [(5e-12, None), (1e-30, None), (2.0, 0.0), (1e30, 0.0)])
+def test_equal_scores_at_the_ends_of_the_range(fmt, dtype, d, n, qscale, scale):
+    c = Case([(n, 300), (n, 45)], fmt=fmt, dtype=dtype, d=d, qscale=qscale, seed=103)
+    c.stored[:, :, 0] = 0
+    if fmt == ref.I8:
+        c.scales[:, :, 0] = 0
+    check(c, scale=scale)
+    check(c, window=50, sinks=3, scale=scale)
