@@ -42,6 +42,7 @@ constexpr int kWarps = 4;                             // that compute; one more 
 constexpr float kPScale = 64.f;                       // probabilities' scale in fp16
 constexpr float kGrow = 8.f;                          // bits that a row's maximum may grow before O is rescaled
 constexpr float kMinRef = 0x1p-100f;
+constexpr float kTiny = 0x1p-149f;                    // stands for a score's factor of 0
 
 template <int FMT, int D>
 struct Shape {
@@ -403,7 +404,8 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
                 }
             }
             const float sign = a.scale < 0.f ? -1.f : 1.f;   // goes to the query: factors are positive
-            float f = fmaxf(a.scale * sign * kLog2e, 1e-30f);
+            float f = a.scale * sign * kLog2e;
+            if (FMT == KDA_KV_BF16 && f == 0.f) f = kTiny;
 #pragma unroll
             for (int i = 0; i < kCols; ++i) x[i] *= sign;
             if (FMT == KDA_KV_I8) {
@@ -510,11 +512,10 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
                 }
             }
             // ---- softmax
-            // A score's factor.  A product too small for a number of its own becomes a small one, for a masked
-            // score, -infinity, has to stay that; |c| < 2^25 there, so a seen score is 0 by either.
+            // A score's factor.  It is never 0, for a masked score, -infinity, has to stay that.
             auto factor = [&](int y, int x, int r) {
                 const float f = rs[x][r] * ks[y];
-                return FMT == KDA_KV_I8 && f < 1e-37f ? 1e-37f : f;
+                return FMT == KDA_KV_I8 && f == 0.f ? kTiny : f;
             };
             const bool whole = there == (1u << kGr) - 1u && (jb.whole >> warp & 1u);
             if (!whole)   // rows not in use may see what they like

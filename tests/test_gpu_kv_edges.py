@@ -112,3 +112,19 @@ def test_equal_scores_at_the_ends_of_the_range(fmt, dtype, d, n, qscale, scale):
         c.scales[:, :, 0] = 0
     check(c, scale=scale)
     check(c, window=50, sinks=3, scale=scale)
+
+
+# ------------------------------------------------------------------ factors beyond the usual range
+@pytest.mark.parametrize("fmt,dtype,d", KINDS)
+@pytest.mark.parametrize("n", [1, 40])
+def test_small_scale_over_large_queries(fmt, dtype, d, n):
+    c = Case([(n, 200)], fmt=fmt, dtype=dtype, d=d, qscale=1e32, seed=109, spread=0.1)
+    check(c, scale=0.5e-33)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [1, 40])
+def test_large_keys_under_small_queries(dtype, n):
+    c = Case([(n, 200)], fmt=ref.I8, dtype=dtype, qscale=1e-35, seed=110, spread=0.1)
+    c.scales[:, :, 0] *= np.float32(1e35)
+    check(c)
