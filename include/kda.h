@@ -496,7 +496,7 @@ int64_t kda_attn_workspace_bytes(int32_t Hq, int32_t Hkv, int32_t d, int32_t dty
  *     window == 0  or  j > p - window  or  j < sinks
  * (causal; with a window, the last `window` tokens and the first `sinks` ones).
  *   q             [T_tot][Hq][d] as rotated by kda_kv_append, its tokens already in the cache
- *   scale         factor of q . k, commonly 1 / sqrt(d)
+ *   scale         factor of q . k, commonly 1 / sqrt(d); finite
  *   o             [T_tot][Hq][d] contiguous, dtype: softmax(scale q k) v
  *   lse           device fp32 [T_tot][Hq] or NULL: the log of the sum of the exponentials
  *   workspace     device, 16-byte aligned, kda_attn_workspace_bytes(); one call at a time uses it

@@ -2,6 +2,7 @@
 // stream-ordered, allocates nothing and never waits for the device; lengths and page tables stay
 // on the device and are checked there.
 #include <algorithm>
+#include <cmath>
 
 #include "kda.h"
 #include "pool.h"
@@ -149,7 +150,8 @@ int kda_attn_paged(const kda_pool *pool, int32_t Hq, int32_t Hkv, int32_t d, int
     kda::AttnArgs a{};
     if (!cache_view(pool, Hkv, d, fmt, page_tokens, const_cast<void *>(pool_base), page_table, max_pages, status_dev,
                     a.kv) ||
-        !valid_batch(nseq, T_tot, max_q, dtype) || Hq <= 0 || Hq > 4096 || Hq % Hkv || window < 0 || sinks < 0)
+        !valid_batch(nseq, T_tot, max_q, dtype) || Hq <= 0 || Hq > 4096 || Hq % Hkv || !std::isfinite(scale) ||
+        window < 0 || sinks < 0)
         return KDA_EINVAL;
     if ((int64_t)max_q * (Hq / Hkv) > INT32_MAX - 1024) return KDA_EINVAL;
     if (T_tot == 0 || max_q == 0) return KDA_OK;
