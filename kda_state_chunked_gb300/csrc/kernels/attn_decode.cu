@@ -25,9 +25,11 @@
 // 8-bit cache: codes c become fp16 exactly (the byte under the exponent of 1024, less 1152), a
 // query row is scaled by a power of two into fp16's range, so q . c carries no rounding beyond
 // fp32 sums, and the block's key scale multiplies the score.  The value scale goes into the
-// probabilities: p (vs / ref) 2^6 in fp16, ref the largest value scale so far to within a factor of two.  float32 queries
-// are split into 2 fp16 terms (3 bf16 terms over the 16-bit cache), and so are the probabilities:
-// the products then keep 22 to 24 bits.
+// probabilities: p (vs / ref) 2^6 in fp16, ref the largest value scale so far to within a factor of two.
+//
+// float32 calls: queries and probabilities are split into three bf16 terms, which keep all 24 bits over
+// fp32's range; codes are exact in bf16.  (Two fp16 terms hold 22, and fewer the further a
+// probability times its value scale lies below the largest.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -97,9 +99,9 @@ __device__ __forceinline__ void pin(float (&o)[N][4]) {
 }
 
 // D (16x8) += A (16x16) B (16x8), fp32 sums.
-template <int FMT>
+template <bool F16>
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    if constexpr (FMT == KDA_KV_I8)
+    if constexpr (F16)
         asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
             "{%0,%1,%2,%3};"
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -111,21 +113,29 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Two biased bytes (selected by SEL, under the exponent byte 0x64) as fp16: 1024 + b - 1152 = code.
-template <uint32_t SEL>
-__device__ __forceinline__ uint32_t half2_of(uint32_t biased) {
-    const uint32_t u = __byte_perm(biased, 0x64646464u, SEL);
-    const uint32_t k = 0x64806480u;   // 1152, 1152
-    const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&u), *reinterpret_cast<const __half2 *>(&k));
-    return *reinterpret_cast<const uint32_t *>(&r);
+// Two codes (bytes selected by SEL) as the product's type, both exact.  fp16: under the exponent byte 0x64
+// a biased code, b = code + 128, is 1024 + b, less 1152.  bf16: under 0x43 a code's low seven bits are
+// 128 + those, less 128 or, where the sign bit is set, 256.
+template <bool F16, uint32_t SEL>
+__device__ __forceinline__ uint32_t codes2(uint32_t c) {
+    if constexpr (F16) {
+        const uint32_t u = __byte_perm(c, 0x64646464u, SEL);
+        const uint32_t k = 0x64806480u;   // 1152, 1152
+        const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&u), *reinterpret_cast<const __half2 *>(&k));
+        return *reinterpret_cast<const uint32_t *>(&r);
+    } else {
+        const uint32_t x = __byte_perm(c, 0x43434343u, SEL), u = x & 0xFF7FFF7Fu, k = x & 0xFF80FF80u;
+        const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&u), *reinterpret_cast<const __nv_bfloat162 *>(&k));
+        return *reinterpret_cast<const uint32_t *>(&r);
+    }
 }
 
 // x (already in range) as NT packed terms of the product's type whose sum is x to NT times its bits.
-template <int FMT, int NT>
+template <bool F16, int NT>
 __device__ __forceinline__ void split2(float x, float y, uint32_t (&out)[NT]) {
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-        if constexpr (FMT == KDA_KV_I8) {
+        if constexpr (F16) {
             const __half2 h = __floats2half2_rn(x, y);
             out[i] = *reinterpret_cast<const uint32_t *>(&h);
             if (i + 1 < NT) x -= __low2float(h), y -= __high2float(h);
@@ -207,6 +217,8 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
     constexpr int kDt = D / 16;   // 16-column output tiles
     constexpr int kGr = S::groups;
     constexpr bool kRegQ = NT == 1;   // query fragments stay in registers
+    constexpr bool kF16 = FMT == KDA_KV_I8 && NT == 1;   // the products' type: fp16, or bf16
+    constexpr uint32_t kBias = kF16 ? 0x80808080u : 0u;  // of a code that codes2() takes
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = ptx::smem_align1024(smem_raw);
     constexpr int stages = S::stages - (NT > 1);
@@ -428,7 +440,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
                 const int c = (c0 + i) % 16, k = (c0 + i) / 16;
                 const int tt = FMT == KDA_KV_I8 ? c / 4 : c % 8 / 2, half = FMT == KDA_KV_I8 ? c / 2 % 2 : c / 8;
                 uint32_t z[NT];
-                split2<FMT, NT>(x[i], x[i + 1], z);
+                split2<kF16, NT>(x[i], x[i + 1], z);
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
                     if (row < 8 * NR) qfrag[(((n * kKs + k) * NR + row / 8) * 32 + row % 8 * 4 + tt) * 2 + half] = z[n];
@@ -482,12 +494,12 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
 #pragma unroll
                 for (int x = 0; x < NR; ++x) {
                     if constexpr (kRegQ) {
-                        mma<FMT>(c[y][x], af, qb[k][x][0], qb[k][x][1]);
+                        mma<kF16>(c[y][x], af, qb[k][x][0], qb[k][x][1]);
                     } else {
 #pragma unroll
                         for (int z = NT - 1; z >= 0; --z) {
                             const uint2 f = *reinterpret_cast<const uint2 *>(qfrag + (((z * kKs + k) * NR + x) * 32 + lane) * 2);
-                            mma<FMT>(c[y][x], af, f.x, f.y);
+                            mma<kF16>(c[y][x], af, f.x, f.y);
                         }
                     }
                 }
@@ -502,8 +514,9 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
                     for (int k = 0; k < 2; ++k)
 #pragma unroll
                         for (int y = 0; y < kGr; ++y) {
-                            const uint32_t b0 = w[y][2 * k] ^ 0x80808080u, b1 = w[y][2 * k + 1] ^ 0x80808080u;
-                            const uint32_t af[4] = {half2_of<0x4140>(b0), half2_of<0x4140>(b1), half2_of<0x4342>(b0), half2_of<0x4342>(b1)};
+                            const uint32_t b0 = w[y][2 * k] ^ kBias, b1 = w[y][2 * k + 1] ^ kBias;
+                            const uint32_t af[4] = {codes2<kF16, 0x4140>(b0), codes2<kF16, 0x4140>(b1), codes2<kF16, 0x4342>(b0),
+                                                    codes2<kF16, 0x4342>(b1)};
                             slice(y, 2 * i + k, af);
                         }
                 } else {
@@ -588,7 +601,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
                     }
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {   // tokens 0-7, 8-15: rows of the transposed operand
-                        split2<FMT, NT>(p[2 * h], p[2 * h + 1], pb[y][x][h]);
+                        split2<kF16, NT>(p[2 * h], p[2 * h + 1], pb[y][x][h]);
 #pragma unroll
                         for (int z = 0; z < NT; ++z) pb[y][x][h][z] = transpose8(pb[y][x][h][z]);
                     }
@@ -622,13 +635,13 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
 #pragma unroll
                             for (int x = 0; x < NR; ++x) {
                                 if constexpr (NT == 1) {
-                                    mma<FMT>(o[x][j], af, pb[y][x][0][0], pb[y][x][1][0]);
+                                    mma<kF16>(o[x][j], af, pb[y][x][0][0], pb[y][x][1][0]);
                                 } else {
                                     // the matrix unit's sums are cut, not rounded: over a long context their
                                     // bias came to 2e-6 of a float32 result, so each group's is added here
                                     float d[4] = {};
 #pragma unroll
-                                    for (int z = NT - 1; z >= 0; --z) mma<FMT>(d, af, pb[y][x][0][z], pb[y][x][1][z]);
+                                    for (int z = NT - 1; z >= 0; --z) mma<kF16>(d, af, pb[y][x][0][z], pb[y][x][1][z]);
 #pragma unroll
                                     for (int e = 0; e < 4; ++e) o[x][j][e] += d[e];
                                 }
@@ -639,8 +652,9 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
                             // columns of its 16 in rows 0-7 and the odd ones in rows 8-15
 #pragma unroll
                             for (int k = 0; k < 2; ++k) {
-                                const uint32_t b0 = w[2 * k] ^ 0x80808080u, b1 = w[2 * k + 1] ^ 0x80808080u;
-                                const uint32_t af[4] = {half2_of<0x4240>(b0), half2_of<0x4341>(b0), half2_of<0x4240>(b1), half2_of<0x4341>(b1)};
+                                const uint32_t b0 = w[2 * k] ^ kBias, b1 = w[2 * k + 1] ^ kBias;
+                                const uint32_t af[4] = {codes2<kF16, 0x4240>(b0), codes2<kF16, 0x4341>(b0), codes2<kF16, 0x4240>(b1),
+                                                        codes2<kF16, 0x4341>(b1)};
                                 columns(2 * i + k, af);
                             }
                         } else {
@@ -667,7 +681,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
                         for (int x = 0; x < NR; ++x) {
                             float d[4] = {};
 #pragma unroll
-                            for (int z = NT - 1; z >= 0; --z) mma<FMT>(d, w, pb[0][x][0][z], pb[0][x][1][z]);
+                            for (int z = NT - 1; z >= 0; --z) mma<kF16>(d, w, pb[0][x][0][z], pb[0][x][1][z]);
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
                                 if (pos[x][e & 1] == q) o[x][i][e] += d[e];
@@ -807,10 +821,10 @@ cudaError_t run(const AttnArgs &a, cudaStream_t st) {
 cudaError_t launch_attn_decode(const AttnArgs &a, cudaStream_t s) {
     const bool i8 = a.kv.fmt == KDA_KV_I8, f32 = a.dtype == KDA_F32;
     if (a.kv.d == 128) {
-        if (i8) return f32 ? run<KDA_KV_I8, 128, 2>(a, s) : run<KDA_KV_I8, 128, 1>(a, s);
+        if (i8) return f32 ? run<KDA_KV_I8, 128, 3>(a, s) : run<KDA_KV_I8, 128, 1>(a, s);
         return f32 ? run<KDA_KV_BF16, 128, 3>(a, s) : run<KDA_KV_BF16, 128, 1>(a, s);
     }
-    if (i8) return f32 ? run<KDA_KV_I8, 64, 2>(a, s) : run<KDA_KV_I8, 64, 1>(a, s);
+    if (i8) return f32 ? run<KDA_KV_I8, 64, 3>(a, s) : run<KDA_KV_I8, 64, 1>(a, s);
     return f32 ? run<KDA_KV_BF16, 64, 3>(a, s) : run<KDA_KV_BF16, 64, 1>(a, s);
 }
 

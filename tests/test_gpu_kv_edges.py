@@ -128,3 +128,57 @@ def test_large_keys_under_small_queries(dtype, n):
     c = Case([(n, 200)], fmt=ref.I8, dtype=dtype, qscale=1e-35, seed=110, spread=0.1)
     c.scales[:, :, 0] *= np.float32(1e35)
     check(c)
+
+
+# ------------------------------------------------------------------ value scales far apart
+def far_apart(c, block, bits, quiet):
+    """Blocks `block(s)` get values 2^bits times larger; quiet: and keys that give them 2^-41 of the others'
+    weights (a query's first element is 32, and a key's -10 there and 0 elsewhere)."""
+    for s in range(len(c.lens)):
+        for b in block(s):
+            p = c.table[s, b]
+            c.scales[p, :, 1] *= 2.0 ** bits
+            if quiet:
+                c.scales[p, :, 0] = 10 / 127
+                c.stored[p, :, 0] = 0
+    if quiet:
+        c.q[..., 0] = 32
+        c.stored[:, :, 0, :, 0] = 0
+        for s in range(len(c.lens)):
+            for b in block(s):
+                c.stored[c.table[s, b], :, 0, :, 0] = -127
+    return c
+
+
+@pytest.mark.parametrize("dtype,bits", [("f32", 16), ("f32", 28), ("f32", 60)])
+@pytest.mark.parametrize("n,many", [(1, 1), (4, 1), (40, 1), (2, 40), (40, 40)])
+def test_large_values_without_weight_cost_the_others_nothing(dtype, bits, n, many):
+    # first in each sequence, and behind others; `many` sequences: a share takes several units
+    lens = [(n, 700 - 13 * (i % 7)) for i in range(many)]
+    c = Case(lens, fmt=ref.I8, dtype=dtype, Hkv=2, G=2, pt=16, seed=104, qscale=0.5)
+    check(far_apart(c, lambda s: [0, 9], bits, True))
+
+
+@pytest.mark.parametrize("dtype", ["f32"])
+@pytest.mark.parametrize("bits", [28, 60])
+@pytest.mark.parametrize("n,L", [(4, 50), (4, 402), (40, 300), (40, 55)])
+def test_large_values_that_a_row_does_not_see_cost_it_nothing(dtype, bits, n, L):
+    c = Case([(n, L), (n, L + 32)], fmt=ref.I8, dtype=dtype, Hkv=2, G=2, pt=16, seed=105, qscale=0.5)
+    far_apart(c, lambda s: [(int(c.kv_len[s]) - 1) // 16], bits, False)
+    check(c)
+    c = Case([(n, 300), (n, 340)], fmt=ref.I8, dtype=dtype, Hkv=2, G=2, pt=16, seed=106, qscale=0.5)
+    check(far_apart(c, lambda s: [0, 12], bits, False), window=100)
+
+
+@pytest.mark.parametrize("n", [1, 4])
+def test_float32_weights_far_below_the_largest_count(n):
+    """A first token with 2^30 times the others' weight and a value of 0: all that comes out is theirs."""
+    c = Case([(n, 700)], fmt=ref.I8, dtype="f32", Hkv=2, G=4, pt=16, seed=107, qscale=0.25)
+    c.q[..., 0] = 32
+    c.stored[:, :, 0, :, 0] = 0
+    p = c.table[0, 0]
+    c.stored[p, :, :, 0] = 0
+    c.scales[p, :, 0] = 7.35 / 127
+    c.stored[p, :, 0, 1:] = 0
+    c.stored[p, :, 0, 0, 0] = 127
+    check(c)
