@@ -504,8 +504,11 @@ int64_t kda_attn_workspace_bytes(int32_t Hq, int32_t Hkv, int32_t d, int32_t dty
  * lse = -infinity.  What a query does not see never changes its result, a NaN or an infinity
  * included; pages that no query of the call sees are not read, and their table entries may hold
  * anything.  Sums, maxima and accumulators are fp32; KDA_F32 calls keep fp32 accuracy throughout.
- * KDA_KV_I8: a block whose value scale is 2^30 times smaller than an earlier one's of its sequence
- * may add nothing to o.  Results do not depend on timing: the same call gives the same bits. */
+ * KDA_BF16 calls round each probability before its product with the value: to bf16 over KDA_KV_BF16;
+ * over KDA_KV_I8, times the block's value scale, to fp16 with a range that follows the query's own
+ * tokens: a product of probability and value scale 2^19 times below the largest that the query sees
+ * loses bits, one 2^30 below may add nothing to o.  Results do not depend on timing: the same call
+ * gives the same bits. */
 int kda_attn_paged(const kda_pool *pool, int32_t Hq, int32_t Hkv, int32_t d, int32_t dtype, int32_t fmt,
                    int32_t page_tokens, int32_t nseq, int64_t T_tot, int32_t max_q, const int32_t *cu_q,
                    const int32_t *kv_len, const int32_t *page_table, int32_t max_pages, const void *q,

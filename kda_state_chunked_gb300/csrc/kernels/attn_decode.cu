@@ -25,7 +25,9 @@
 // 8-bit cache: codes c become fp16 exactly (the byte under the exponent of 1024, less 1152), a
 // query row is scaled by a power of two into fp16's range, so q . c carries no rounding beyond
 // fp32 sums, and the block's key scale multiplies the score.  The value scale goes into the
-// probabilities: p (vs / ref) 2^6 in fp16, ref the largest value scale so far to within a factor of two.
+// probabilities: p vs 2^6 in fp16, relative to the largest p vs that the row has seen (to within 2^8).
+// A token 2^19 times below that loses bits and one 2^30 below adds nothing; what a row does not see, or
+// sees without weight, costs it none.
 //
 // float32 calls: queries and probabilities are split into three bf16 terms, which keep all 24 bits over
 // fp32's range; codes are exact in bf16.  (Two fp16 terms hold 22, and fewer the further a
@@ -41,9 +43,8 @@ namespace {
 using namespace attn;
 
 constexpr int kWarps = 4;                             // that compute; one more walks and copies
-constexpr float kPScale = 64.f;                       // probabilities' scale in fp16
+constexpr float kPBits = 6.f;                         // bits that a probability is scaled up in fp16
 constexpr float kGrow = 8.f;                          // bits that a row's maximum may grow before O is rescaled
-constexpr float kMinRef = 0x1p-100f;
 constexpr float kTiny = 0x1p-149f;                    // stands for a score's factor of 0
 
 template <int FMT, int D>
@@ -375,7 +376,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
     uint32_t qb[kRegQ ? kKs : 1][NR][2];
     float rs[NR][2];
     int32_t pos[NR][2], nrows = 0, row0 = 0, tok0 = 0, head = 0;   // the item
-    float o[NR][kDt][4], m[NR][2], l[NR][2], ref = 0.f, inv_ref = 0.f;   // ref: 8-bit, the largest value scale so far
+    float o[NR][kDt][4], m[NR][2], l[NR][2], big[NR][2];   // big: 8-bit, the reference of probability times value scale
     for (;;) {
         const bool ok = __all_sync(0xFFFFFFFFu, wait_bar(&full[stage], phase, err));
         if (!ok) {
@@ -462,12 +463,11 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
                     const int row = 8 * x + 2 * t + r;
                     rs[x][r] = qs[row];
                     pos[x][r] = row < nrows ? jb.base + token_of(a, row0 + row) : -1;
-                    m[x][r] = -INFINITY, l[x][r] = 0.f;
+                    m[x][r] = big[x][r] = -INFINITY, l[x][r] = 0.f;
                 }
 #pragma unroll
                 for (int j = 0; j < kDt; ++j) o[x][j][0] = o[x][j][1] = o[x][j][2] = o[x][j][3] = 0.f;
             }
-            ref = inv_ref = 0.f;
         }
         const uint32_t there = jb.live >> (warp * kGr) & ((1u << kGr) - 1u);
         if (there) {
@@ -539,43 +539,54 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             if (!(there >> y & 1u) || !sees(a, pos[x][e & 1], j0 + 16 * y + g + 8 * (e >> 1))) c[y][x][e] = -INFINITY;
-            // m lags: it only follows a row's maximum when that has grown by more than 2^8, which the
-            // lanes' own scores tell well enough; so do ref and the value scales, by a factor of two.
-            float top[NR][2], vmax = 0.f;
+            // m lags: it only follows a row's maximum when that has grown by more than 2^8.  So does big, which
+            // is the same for the scores with log2 of the value scales added: what enters the product stays in
+            // fp16's range by what the row itself sees, whatever scales its other blocks have.  Either is a whole
+            // number, so that moving it rounds nothing, and moves by the row's own scores alone.
+            float top[NR][2], topv[NR][2], lv[kGr];
             bool grown = false;
+#pragma unroll
+            for (int y = 0; y < kGr; ++y) lv[y] = vs[y] > 0.f && vs[y] < INFINITY ? fmaxf(__log2f(vs[y]), -100.f) : -INFINITY;
 #pragma unroll
             for (int x = 0; x < NR; ++x)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    top[x][r] = -INFINITY;
+                    top[x][r] = topv[x][r] = -INFINITY;
 #pragma unroll
-                    for (int y = 0; y < kGr; ++y) top[x][r] = fmaxf(top[x][r], fmaxf(c[y][x][r], c[y][x][r + 2]) * factor(y, x, r));
+                    for (int y = 0; y < kGr; ++y) {
+                        const float s = fmaxf(c[y][x][r], c[y][x][r + 2]) * factor(y, x, r);
+                        top[x][r] = fmaxf(top[x][r], s);
+                        if (FMT == KDA_KV_I8) topv[x][r] = fmaxf(topv[x][r], s + lv[y]);
+                    }
                     grown |= top[x][r] > m[x][r] + kGrow;
+                    if (FMT == KDA_KV_I8) grown |= topv[x][r] > big[x][r] + kGrow;
                 }
-#pragma unroll
-            for (int y = 0; y < kGr; ++y)
-                if (FMT == KDA_KV_I8 && vs[y] < INFINITY) vmax = fmaxf(vmax, vs[y]);
-            const bool scaled = FMT == KDA_KV_I8 && vmax > 2.f * ref;
-            if (__any_sync(0xFFFFFFFFu, grown || scaled)) {
-                float k = 1.f;
-                if (scaled) {
-                    const float rn = fmaxf(vmax, kMinRef);
-                    k = ref / rn;
-                    ref = rn;
-                    inv_ref = kPScale / rn;
-                }
+            if (__any_sync(0xFFFFFFFFu, grown)) {
 #pragma unroll
                 for (int x = 0; x < NR; ++x) {
                     float f[2];
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
 #pragma unroll
-                        for (int i = 4; i < 32; i <<= 1) top[x][r] = fmaxf(top[x][r], __shfl_xor_sync(0xFFFFFFFFu, top[x][r], i));
-                        const float mn = fmaxf(m[x][r], top[x][r]);
-                        f[r] = mn == -INFINITY ? 1.f : ex2(m[x][r] - mn);
-                        l[x][r] *= f[r];
-                        m[x][r] = mn;
-                        f[r] *= k;
+                        for (int i = 4; i < 32; i <<= 1) {
+                            top[x][r] = fmaxf(top[x][r], __shfl_xor_sync(0xFFFFFFFFu, top[x][r], i));
+                            if (FMT == KDA_KV_I8) topv[x][r] = fmaxf(topv[x][r], __shfl_xor_sync(0xFFFFFFFFu, topv[x][r], i));
+                        }
+                        f[r] = 1.f;
+                        if (top[x][r] > m[x][r] + kGrow) {
+                            const float mn = ceilf(top[x][r]);
+                            f[r] = ex2(m[x][r] - mn);
+                            l[x][r] *= f[r];
+                            m[x][r] = mn;
+                        }
+                        if (FMT == KDA_KV_I8) {
+                            f[r] = 1.f;
+                            if (topv[x][r] > big[x][r] + kGrow) {
+                                const float bn = ceilf(topv[x][r]);
+                                f[r] = ex2(big[x][r] - bn);
+                                big[x][r] = bn;
+                            }
+                        }
                     }
 #pragma unroll
                     for (int j = 0; j < kDt; ++j)
@@ -583,21 +594,30 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
                         for (int e = 0; e < 4; ++e) o[x][j][e] *= f[e & 1];
                 }
             }
+            // 8-bit: what a probability is multiplied by beside its value scale
+            float up[NR][2];
+#pragma unroll
+            for (int x = 0; x < NR; ++x)
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+                    up[x][r] = FMT == KDA_KV_I8 && big[x][r] != -INFINITY ? ex2(m[x][r] - big[x][r] + kPBits) : 0.f;
             uint32_t pb[kGr][NR][2][NT];
 #pragma unroll
             for (int y = 0; y < kGr; ++y) {
-                // probabilities, and what of them is rounded: 8-bit, p vs / ref 2^6
-                const float pv = FMT == KDA_KV_I8 ? (vs[y] < INFINITY ? vs[y] * inv_ref : NAN) : 1.f;
+                // probabilities, and what of them is rounded: 8-bit, p vs 2^(m - big + 6).  (Where vs 2^(m - big)
+                // is beyond fp32, p is 0.)
 #pragma unroll
                 for (int x = 0; x < NR; ++x) {
-                    float p[4];
+                    float p[4], pv[2];
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) pv[r] = vs[y] < INFINITY ? fminf(vs[y] * up[x][r], 0x1p127f) : NAN;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int r = e & 1;
                         p[e] = ex2(fmaf(c[y][x][e], factor(y, x, r), m[x][r] == -INFINITY ? 0.f : -m[x][r]));
                         if (FMT == KDA_KV_I8 && strange && c[y][x][e] == -INFINITY) p[e] = 0.f;
                         l[x][r] += p[e];
-                        if (FMT == KDA_KV_I8) p[e] = strange && p[e] == 0.f ? 0.f : p[e] * pv;
+                        if (FMT == KDA_KV_I8) p[e] = strange && c[y][x][e] == -INFINITY ? 0.f : p[e] * pv[r];
                     }
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {   // tokens 0-7, 8-15: rows of the transposed operand
@@ -721,7 +741,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
 #pragma unroll
                 for (int i = 0; i < kWarps; ++i) mt = fmaxf(mt, ml[(i * 16 + 8 * x + 2 * t + r) * 2]);
                 f[r] = mt == -INFINITY ? 1.f : ex2(m[x][r] - mt);
-                if (FMT == KDA_KV_I8) f[r] *= ref * (1.f / kPScale);
+                if (FMT == KDA_KV_I8) f[r] = big[x][r] == -INFINITY ? 0.f : ex2(big[x][r] - kPBits - mt);
             }
 #pragma unroll 1
             for (int half = 0; half < 2; ++half) {

@@ -37,8 +37,8 @@
 //
 // 8-bit cache: as in the register kernel codes are exact in fp16 and query rows scaled by a power
 // of two; the key scale of each 16 tokens multiplies f, the value scale goes into the exponent:
-// p' = 2^(f S - m + log2(vs / ref 2^6)), and a group's sum of p' divided by that factor is its sum
-// of p.  ref is the largest value scale so far, to within a factor of two.
+// p' = 2^(f S + log2 vs - b + 6), b a running bound of the row's own f S + log2 vs, and a group's sum
+// of p' divided by 2^(log2 vs - b + m + 6) is its sum of p.
 #include <type_traits>
 
 #include <cuda_bf16.h>
@@ -69,14 +69,11 @@ struct __align__(16) Job {
     int32_t base;                       // position of the sequence's first query
     int32_t row0, nrows, tok0, head;    // the row tile
     uint32_t live;                      // groups of 16 tokens that are there
-    int32_t last_cta, pmin, pmax, pad0;
+    int32_t last_cta, pmin, pmax;
+    uint32_t nans;                      // 8-bit: groups whose value scale is no number
     int32_t slot[8];                    // of each group: first token's slot in its page,
     int64_t rec[8];                     // its record's place in the pool (the pool's first where it is not there),
-    float ks[8];                        // 8-bit: key scale, log2 of what the probabilities are scaled by,
-    float lg[8], back[8];               // and the inverse of that
-    float lref, shift;                  // log2 of ref, and by what O follows its last move
-    uint32_t nans;                      // groups whose value scale is no number
-    int32_t pad;
+    float ks[8], lg[8];                 // 8-bit: key scale, log2 of the value scale (-infinity for 0 and for no number)
 };
 
 template <int D>
@@ -85,8 +82,8 @@ struct Lay {
     static constexpr int q = 0, k = 2 * half_q, v = k + 2 * tile, misc = v + 2 * tile;
     static constexpr int qs = misc;                        // [2][256] row factors
     static constexpr int jobs = qs + 2 * kRows * 4;        // [kJobs]
-    static constexpr int pair = jobs + kJobs * (int)sizeof(Job);  // [2][2][256] what a row's two threads tell each other
-    static constexpr int bad = pair + 2 * 2 * kRows * 4;   // [2][4] tokens taken out of a value tile
+    static constexpr int pair = jobs + kJobs * (int)sizeof(Job);  // [2][2][256][2] what a row's two threads tell each other
+    static constexpr int bad = pair + 2 * 2 * kRows * 8;   // [2][4] tokens taken out of a value tile
     static constexpr int plan = bad + 2 * 16;              // the split's scratch
     static constexpr int bar = plan + 4096;
     static constexpr int total = bar + 512;
@@ -308,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
         const uint32_t lanes = (uint32_t)((warp % 4) * 32) << 16;
         const uint32_t tS = tm + lanes + half * 128 + side * 64;           // this thread's 64 scores
         const uint32_t tO = tm + lanes + 256 + half * 128 + side * (D / 2);   // and its half of the output
-        float *pair = reinterpret_cast<float *>(sm + L::pair);
+        float2 *pair = reinterpret_cast<float2 *>(sm + L::pair);
         auto meet = [&]() { tcx::named_bar(1 + half * 4 + warp % 4, 64); };    // the two warps of these rows
         auto wait_half = [&](int b, uint32_t parity) {                         // the half's eight warps
             return wait_together<kSoftWarps / 2 * 32>(&bars[b], parity, err, warp % 8 == 0, 9 + half);
@@ -316,7 +313,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
         uint32_t n_s = 0, n_item = 0, n_o = 0;   // units of this half, items so far, of this half: the barriers' parities
         int32_t pos = -1, p_lo = 0, p_hi = 0;   // positions of this row, of the warp's rows
         bool in = false, ok = true;
-        float m = -INFINITY, l = 0.f, f_row = 0.f;
+        float m = -INFINITY, big = -INFINITY, l = 0.f, f_row = 0.f;   // big: 8-bit, the reference with value scales
+        auto lift = [&]() { return (big == -INFINITY ? 0.f : big - m) - kPBits; };
         for (uint32_t n = 0;; ++n) {
             ok = wait_job(n);
             if (!ok) break;
@@ -334,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                 pos = in ? jb.base + token_of(a, at) : -1;
                 p_lo = __reduce_min_sync(0xFFFFFFFFu, in ? pos : INT32_MAX);
                 p_hi = __reduce_max_sync(0xFFFFFFFFu, pos);
-                m = -INFINITY, l = 0.f;
+                m = big = -INFINITY, l = 0.f;
                 float z[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) z[i] = 0.f;
@@ -375,8 +373,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                     step(x[1], c + 1);
                 }
             };
-            // ---- the row's maximum
-            float top = -INFINITY;
+            // ---- the row's maximum, and (8-bit cache) that of its scores with log2 of their value scales added
+            float top = -INFINITY, topv = -INFINITY;
             auto most = [&](auto all) {
                 groups([&](const float (&x)[16], int c) {
                     const int k = decltype(all)::value ? kEvery : kind(c);
@@ -389,27 +387,39 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
 #pragma unroll
                         for (int i = 0; i < 16; ++i) gt = fmaxf(gt, see & 1u << i ? x[i] : -INFINITY);
                     }
-                    // a group's factor is >= 0, and so is the row's, which the end brings in
-                    if (FMT == KDA_KV_I8) top = fmaxf(top, k == kNone ? -INFINITY : gt * jb.ks[4 * side + c]);
-                    else top = gt;
+                    if constexpr (FMT == KDA_KV_I8) {
+                        if (k != kNone) {
+                            gt *= f_row * jb.ks[4 * side + c];   // factors are >= 0
+                            top = fmaxf(top, gt);
+                            topv = fmaxf(topv, gt + jb.lg[4 * side + c]);
+                        }
+                    } else {
+                        top = gt;
+                    }
                 });
             };
             if (flags & kWhole) most(std::true_type{});
             else most(std::false_type{});
-            if (top != -INFINITY) top *= f_row;
+            if (FMT == KDA_KV_BF16 && top != -INFINITY) top *= f_row;
             {
-                float *mine = pair + ((n_s & 1) * 2 + side) * kRows, *other = pair + ((n_s & 1) * 2 + (side ^ 1)) * kRows;
-                mine[row] = top;
+                float2 *mine = pair + ((n_s & 1) * 2 + side) * kRows, *other = pair + ((n_s & 1) * 2 + (side ^ 1)) * kRows;
+                mine[row] = make_float2(top, topv);
                 meet();
-                top = fmaxf(top, other[row]);
+                const float2 z = other[row];
+                top = fmaxf(top, z.x), topv = fmaxf(topv, z.y);
             }
-            // ---- the row's reference, which lags behind its maximum
-            float grown = FMT == KDA_KV_I8 ? jb.shift : 1.f;   // what O is to be multiplied by
-            if (top > m + kGrow) {        // also where m is still -infinity
-                const float f = m == -INFINITY ? 0.f : ex2(m - top);
-                grown *= f;
+            // ---- the row's references, which lag behind its maxima (also from -infinity)
+            float grown = 1.f;            // what O is to be multiplied by
+            if (top > m + kGrow) {
+                const float mn = FMT == KDA_KV_I8 ? ceilf(top) : top, f = ex2(m - mn);
+                if (FMT == KDA_KV_BF16) grown = f;
                 l *= f;
-                m = top;
+                m = mn;
+            }
+            if (FMT == KDA_KV_I8 && topv > big + kGrow) {
+                const float bn = ceilf(topv);
+                grown = ex2(big - bn);
+                big = bn;
             }
             const float ms = m == -INFINITY ? 0.f : m;
             // ---- tokens whose values were taken out of the product (16-bit cache)
@@ -461,6 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
             if (FMT == KDA_KV_BF16 && odd) meet();   // the other warp is done with these scores too
             // ---- the probabilities, over the scores that they come from: a group's 8 columns lie in
             // what an earlier group has read
+            const float lifted = FMT == KDA_KV_I8 ? lift() : 0.f;
             auto weigh = [&](auto all) {
                 groups([&](const float (&x)[16], int c) {
                     const int k = decltype(all)::value ? kEvery : kind(c);
@@ -472,9 +483,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                         const uint32_t see = k == kEvery ? ~0u : seen(c);
                         float fk = f_row, bias = -ms, back = 1.f;
                         if (FMT == KDA_KV_I8) {
+                            // (a scale of 0 gives a product of 0 in fp16, and still its share of the sum)
+                            const float e = fmaxf(jb.lg[4 * side + c] - lifted, -94.f);
                             fk *= jb.ks[4 * side + c];
-                            bias += jb.lg[4 * side + c];
-                            back = jb.back[4 * side + c];
+                            bias += e;
+                            back = ex2(-e);
                         }
                         const float2 ff = make_float2(fk, fk), bb = make_float2(bias, bias);
                         float2 part = make_float2(0.f, 0.f);
@@ -508,10 +521,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
             if (flags & kEnd) {
                 // ---- the item's output, or this CTA's part of it
                 {
-                    float *mine = pair + ((n_s & 1) * 2 + side) * kRows, *other = pair + ((n_s & 1) * 2 + (side ^ 1)) * kRows;
-                    mine[row] = l;
+                    float2 *mine = pair + ((n_s & 1) * 2 + side) * kRows, *other = pair + ((n_s & 1) * 2 + (side ^ 1)) * kRows;
+                    mine[row].x = l;
                     meet();
-                    l += other[row];
+                    l += other[row].x;
                     meet();              // the next item's first maxima go to the same place
                 }
                 ok = wait_half(OFULL + half, n_o++ & 1);
@@ -520,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                 const bool all = (flags & kStarts) && (flags & kEnds);
                 const int32_t tok = token_of(a, at);
                 const int64_t orow = ((int64_t)jb.tok0 + tok) * a.Hq + jb.head * a.G + at - tok * a.G;
-                const float unscale = FMT == KDA_KV_I8 ? exp2f(jb.lref - kPBits) : 1.f;
+                const float unscale = FMT == KDA_KV_I8 ? exp2f(lift()) : 1.f;
                 const float f = all ? (l == 0.f ? 0.f : unscale / l) : unscale;
                 float *part = a.part + ((int64_t)(blockIdx.x * 2 + (flags & kStarts ? 1 : 0)) * kRows + row) * kPartRow<D>;
 #pragma unroll 1
@@ -906,7 +919,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
             const uint8_t *rec = record(now);
             float2 sc = scales(rec);
             int32_t u_first = start.u;
-            float lref = -INFINITY;
             uint32_t n = 0;
             bool ok = true;
             while (ok && now.n > 0) {
@@ -917,30 +929,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                 const int32_t k = lane / 8, u = now.w.u + k, j0 = unit_token<kUnit>(t, u);
                 const int64_t left = now.w.left - k;
                 const uint32_t live = __ballot_sync(0xFFFFFFFFu, rec != nullptr) >> (8 * k) & 0xFFu;
-                if (now.w.u == u_first) lref = -INFINITY;
-                // 8-bit: ref moves up to a unit's largest value scale when that has doubled.  A scale of 0 stands
-                // for codes of 0: any factor does.  So it does for one that is no number: the softmax makes the
-                // probabilities NaN where they are seen, and the sums, which have no part in the values, stay.
-                float lg = 0.f, shift = 1.f, my_ref = 0.f;
                 const float x = fabsf(sc.y);
-                if (FMT == KDA_KV_I8) {
-                    lg = x > 0.f && x < INFINITY ? log2f(x) : -INFINITY;
-                    float top = lg;
-#pragma unroll
-                    for (int i = 1; i < 8; i <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, i));
-                    top = fmaxf(top, -100.f);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float ti = __shfl_sync(0xFFFFFFFFu, top, 8 * i);
-                        float si = 1.f;
-                        if (i < now.n && ti > lref + 1.f) {
-                            si = exp2f(lref - ti);
-                            lref = ti;
-                        }
-                        if (i == k) shift = si, my_ref = lref;
-                    }
-                    lg = x > 0.f && x < INFINITY ? fmaxf(lg - my_ref, -100.f) + kPBits : kPBits;
-                }
                 const uint32_t nans = __ballot_sync(0xFFFFFFFFu, !(x < INFINITY)) >> (8 * k) & 0xFFu;
                 for (int i = 0; ok && i < now.n; ++i) ok = wait_slow(JEMPTY + (n + i) % kJobs, ((n + i) / kJobs & 1) ^ 1);
                 if (!ok) break;
@@ -949,7 +938,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                     const int i = lane % 8;
                     jb.slot[i] = now.slot;
                     jb.rec[i] = rec ? rec - a.kv.base : 0;
-                    if (FMT == KDA_KV_I8) jb.ks[i] = sc.x == 0.f ? 1e-30f : fabsf(sc.x), jb.lg[i] = lg, jb.back[i] = exp2f(-lg);
+                    if (FMT == KDA_KV_I8) {
+                        // a value scale that is no number makes the probabilities NaN where they are seen; the sums,
+                        // which have no part in the values, stay
+                        jb.ks[i] = sc.x == 0.f ? 1e-30f : fabsf(sc.x);
+                        jb.lg[i] = x > 0.f && x < INFINITY ? fmaxf(log2f(x), -100.f) : -INFINITY;
+                    }
                     if (i == 0) {
                         const bool ends = left >= t.units - u;   // the item's last unit is in this share
                         jb.j0 = j0;
@@ -961,7 +955,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                         jb.live = live;
                         jb.last_cta = ends ? (int32_t)blockIdx.x : cta_of(end - left + (t.units - 1 - u), W, C);
                         jb.pmin = t.pmin, jb.pmax = t.pmax;
-                        if (FMT == KDA_KV_I8) jb.lref = my_ref, jb.shift = shift, jb.nans = nans;
+                        jb.nans = nans;
                     }
                 }
                 __syncwarp();

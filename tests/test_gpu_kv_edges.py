@@ -150,7 +150,7 @@ def far_apart(c, block, bits, quiet):
     return c
 
 
-@pytest.mark.parametrize("dtype,bits", [("f32", 16), ("f32", 28), ("f32", 60)])
+@pytest.mark.parametrize("dtype,bits", [("bf16", 28), ("bf16", 40), ("f32", 16), ("f32", 28), ("f32", 60)])
 @pytest.mark.parametrize("n,many", [(1, 1), (4, 1), (40, 1), (2, 40), (40, 40)])
 def test_large_values_without_weight_cost_the_others_nothing(dtype, bits, n, many):
     # first in each sequence, and behind others; `many` sequences: a share takes several units
@@ -159,7 +159,7 @@ def test_large_values_without_weight_cost_the_others_nothing(dtype, bits, n, man
     check(far_apart(c, lambda s: [0, 9], bits, True))
 
 
-@pytest.mark.parametrize("dtype", ["f32"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("bits", [28, 60])
 @pytest.mark.parametrize("n,L", [(4, 50), (4, 402), (40, 300), (40, 55)])
 def test_large_values_that_a_row_does_not_see_cost_it_nothing(dtype, bits, n, L):
@@ -182,3 +182,18 @@ def test_float32_weights_far_below_the_largest_count(n):
     c.stored[p, :, 0, 1:] = 0
     c.stored[p, :, 0, 0, 0] = 127
     check(c)
+
+
+# ------------------------------------------------------------------ scales of 0 over codes that are not
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [1, 4, 40])
+def test_codes_under_a_scale_of_zero_read_as_zeros(dtype, n):
+    c = Case([(n, 300), (n, 77)], fmt=ref.I8, dtype=dtype, G=2, pt=16, seed=108)
+    for s, (_, L) in enumerate(c.lens):
+        c.scales[c.table[s, 0]] = 0
+        c.scales[c.table[s, 2], :, 0] = 0
+        c.scales[c.table[s, 3], :, 1] = 0
+    check(c)
+    c.scales[:, :, 1] = 0
+    o, _ = check(c)
+    assert (o == 0).all()
