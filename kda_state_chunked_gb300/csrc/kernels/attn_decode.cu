@@ -475,7 +475,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
             const uint8_t *buf = ring + stage * S::stage;
             uint32_t kb = ptx::smem_u32(buf);
             asm volatile("" : "+r"(kb)::"memory");
-            float ks[kGr], vs[kGr];   // a group's scales; the key's goes into the score factors, which are > 0
+            float ks[kGr], vs[kGr];   // a group's scales; the key's goes into the score factors
             bool strange = false;     // a scale that is no number: what a row does not see must stay 0
 #pragma unroll
             for (int y = 0; y < kGr; ++y) {
@@ -483,7 +483,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
                 if (FMT == KDA_KV_I8 && (there >> y & 1u)) {
                     const float2 f = *reinterpret_cast<const float2 *>(buf + 2 * S::tile +
                                                                        16 * (jb.lead >> (4 * (warp * kGr + y)) & 15u));
-                    ks[y] = f.x == 0.f ? 1e-30f : fabsf(f.x);   // 0: the codes are 0, too
+                    ks[y] = fabsf(f.x) < INFINITY ? fabsf(f.x) : NAN;   // an infinity reads as NaN whatever the codes
                     vs[y] = fabsf(f.y);
                     strange |= !(ks[y] < INFINITY && vs[y] < INFINITY);
                 }

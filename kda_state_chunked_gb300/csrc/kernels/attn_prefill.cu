@@ -941,7 +941,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                     if (FMT == KDA_KV_I8) {
                         // a value scale that is no number makes the probabilities NaN where they are seen; the sums,
                         // which have no part in the values, stay
-                        jb.ks[i] = sc.x == 0.f ? 1e-30f : fabsf(sc.x);
+                        jb.ks[i] = fabsf(sc.x) < INFINITY ? fabsf(sc.x) : NAN;   // an infinity reads as NaN whatever the codes
                         jb.lg[i] = x > 0.f && x < INFINITY ? fmaxf(log2f(x), -100.f) : -INFINITY;
                     }
                     if (i == 0) {

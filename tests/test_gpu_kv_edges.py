@@ -130,6 +130,20 @@ def test_large_keys_under_small_queries(dtype, n):
     check(c)
 
 
+# ------------------------------------------------------------------ key scales of 0 and infinity over other codes
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [1, 3, 40])
+def test_key_scales_read_as_they_stand(dtype, n):
+    c = Case([(n, 300), (n, 45)], fmt=ref.I8, dtype=dtype, G=1, pt=16, qscale=1e30, seed=115)
+    c.scales[:, :, 0] = 0
+    check(c)                                  # zeros, however large the queries
+    c = Case([(n, 300), (n, 45)], fmt=ref.I8, dtype=dtype, G=1, pt=16, seed=116)
+    c.scales[c.table[0, 3], :, 0] = np.inf
+    c.scales[c.table[1, 2], :, 0] = np.inf    # some of whose rows see it
+    check(c)
+    check(c, window=40)
+
+
 # ------------------------------------------------------------------ value scales far apart
 def far_apart(c, block, bits, quiet):
     """Blocks `block(s)` get values 2^bits times larger; quiet: and keys that give them 2^-41 of the others'
