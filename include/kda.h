@@ -465,12 +465,13 @@ int64_t kda_kv_page_bytes(int32_t Hkv, int32_t d, int32_t fmt, int32_t page_toke
  *   k, v          new keys and values [T_tot][Hkv][d]
  *   cos_sin       device fp32 [max_pos][rot_dim]: row p holds the rot_dim / 2 cosines, then the
  *                 sines, of position p.  NULL (rot_dim 0): no rotation.  A sequence that
- *                 reaches past max_pos sets KDA_DEV_BAD_META and is skipped
+ *                 reaches past max_pos sets KDA_DEV_BAD_META and is skipped, its queries too
  *   rot_dim       leading elements of a head that rotate: a multiple of 16, at most d
  *   interleaved   0: element i turns with i + rot_dim / 2; else 2 i with 2 i + 1
  * The pages written must be private to their sequence (a shared prefix ends on a block's end, or
  * its last block is copied first).  A call whose kv_len < n for a sequence skips it
- * (KDA_DEV_BAD_META).  One launch. */
+ * (KDA_DEV_BAD_META).  Of a skipped sequence, and of rows that no sequence owns, q_out stays as it
+ * was.  One launch. */
 int kda_kv_append(const kda_pool *pool, int32_t Hq, int32_t Hkv, int32_t d, int32_t dtype, int32_t fmt,
                   int32_t page_tokens, int32_t nseq, int64_t T_tot, int32_t max_q, const int32_t *cu_q,
                   const int32_t *kv_len, const int32_t *page_table, int32_t max_pages, const void *q,

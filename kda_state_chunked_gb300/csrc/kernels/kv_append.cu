@@ -103,6 +103,11 @@ __device__ __forceinline__ uint2 codes8(const float *x, float s) {
 
 constexpr int kMaxToks = 128;   // tokens of a CTA that rotates queries
 
+// A sequence with no place, or no angle, for some of its new tokens: all of it is skipped, queries too.
+__device__ __forceinline__ bool no_place(const KvAppendArgs &a, const KvSeq &q) {
+    return q.len < q.n || (a.rot_dim > 0 && q.len > a.max_pos);
+}
+
 // NT threads; ROWS: new rows of a block that one thread may hold.
 template <int FMT, int D, class TIN, int NT, int ROWS>
 __global__ void __launch_bounds__(NT) kv_append_kernel(KvAppendArgs a, int32_t q_ctas, int32_t q_toks, int64_t items) {
@@ -114,40 +119,36 @@ __global__ void __launch_bounds__(NT) kv_append_kernel(KvAppendArgs a, int32_t q
     const int rot = a.rot_dim;
 
     if ((int)blockIdx.x < q_ctas) {
-        // a token's place in its sequence, by one warp a token
+        // a token's place in its sequence, by one warp a token; none where the sequence is skipped
         __shared__ int64_t place_of[kMaxToks];
         const int64_t t_lo = (int64_t)blockIdx.x * q_toks;
         const int per_tok = a.Hq * kTpr;
-        if (rot > 0) {
-            for (int i = tid / 32; i < q_toks; i += NT / 32) {
-                const int64_t tok = t_lo + i;
-                if (tok >= a.T_tot) break;
-                const int s = kv_find(a.nseq, tok, [&](int m) { return (int64_t)__ldg(a.cu_q + m); });
-                const KvSeq q = kv_seq(a.cu_q, a.kv_len, s, a.T_tot, a.max_q, a.kv);
-                int64_t pos = (int64_t)q.len - q.n + (tok - q.tok0);
-                if (tok < q.tok0 || tok >= (int64_t)q.tok0 + q.n) pos = -1;
-                else if (pos < 0 || pos >= a.max_pos) {
-                    flag_status(a.kv.status, KDA_DEV_BAD_META);
-                    pos = -1;
-                }
-                if (tid % 32 == 0) place_of[i] = pos;
+        for (int i = tid / 32; i < q_toks; i += NT / 32) {
+            const int64_t tok = t_lo + i;
+            if (tok >= a.T_tot) break;
+            const int s = kv_find(a.nseq, tok, [&](int m) { return (int64_t)__ldg(a.cu_q + m); });
+            const KvSeq q = kv_seq(a.cu_q, a.kv_len, s, a.T_tot, a.max_q, a.kv);
+            int64_t pos = (int64_t)q.len - q.n + (tok - q.tok0);
+            if (tok < q.tok0 || tok >= (int64_t)q.tok0 + q.n) pos = -1;
+            else if (no_place(a, q)) {
+                flag_status(a.kv.status, KDA_DEV_BAD_META);
+                pos = -1;
             }
-            __syncthreads();
+            if (tid % 32 == 0) place_of[i] = pos;
         }
+        __syncthreads();
         for (int i = tid; i < q_toks * per_tok; i += NT) {
             const int64_t tok = t_lo + i / per_tok;
             if (tok >= a.T_tot) break;
+            const int64_t pos = place_of[i / per_tok];
+            if (pos < 0) continue;
             const int h = (i % per_tok) / kTpr, c = i % kTpr;
             const Place p = place(c, rot, il);
             const TIN *src = static_cast<const TIN *>(a.q) + tok * a.q_stride + h * D;
             float x[16];
             load8(src + p.a, x);
             load8(src + p.b, x + 8);
-            if (p.turned) {
-                const int64_t pos = place_of[i / per_tok];
-                if (pos < 0) continue;
-                rotate(x, a.cos_sin + pos * rot, c, rot, il);
-            }
+            if (p.turned) rotate(x, a.cos_sin + pos * rot, c, rot, il);
             TIN *dst = static_cast<TIN *>(a.q_out) + (tok * a.Hq + h) * D;
             store8(dst + p.a, x);
             store8(dst + p.b, x + 8);
@@ -180,7 +181,7 @@ __global__ void __launch_bounds__(NT) kv_append_kernel(KvAppendArgs a, int32_t q
         block = (int)b;
     }
     const int old = q.len - q.n;
-    if (old < 0 || (rot > 0 && q.len > a.max_pos)) {   // no place, or no angle, for such a token
+    if (no_place(a, q)) {
         if (tid == 0) flag_status(a.kv.status, KDA_DEV_BAD_META);
         return;
     }

@@ -16,7 +16,7 @@ import torch
 
 import kda_state_chunked_gb300 as kda
 import kv_ref as ref
-from test_gpu_kv import KINDS, Case
+from test_gpu_kv import DEV, FMT, KINDS, Case
 
 pytestmark = pytest.mark.gpu
 
@@ -211,3 +211,59 @@ def test_codes_under_a_scale_of_zero_read_as_zeros(dtype, n):
     c.scales[:, :, 1] = 0
     o, _ = check(c)
     assert (o == 0).all()
+
+
+# ------------------------------------------------------------------ append: queries in place, refused sequences
+def angles(top, rot, r):
+    a = r.standard_normal((top, rot // 2))
+    return np.concatenate([np.cos(a), np.sin(a)], 1).astype(np.float32)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rot,pairs", [(32, False), (64, True), (128, False), (128, True)])
+@pytest.mark.parametrize("lens", [[(1, 30), (1, 1), (1, 64)], [(70, 200), (0, 9), (3, 3)]])
+def test_queries_rotate_in_place(dtype, rot, pairs, lens):
+    c = Case(lens, fmt=ref.I8, dtype=dtype, G=3, seed=112).on_gpu()
+    cs = angles(300, rot, c.r)
+    k = c.gpu(c.token(c.Hkv))
+    q = c.gpu(c.q)
+    kda.kda_kv_append(c.pool, FMT[c.fmt], c.pt, *c.meta, c.max_q, q, k, k, torch.from_numpy(cs).to(DEV), q, c.status,
+                      interleaved=pairs)
+    assert kda.kda_sync_status(c.status) == (kda.KDA_OK, 0)
+    for s, (n, L) in enumerate(c.lens):
+        a, b = int(c.cu[s]), int(c.cu[s + 1])
+        x = ref.rotate(c.q[a:b], cs[L - n:L], pairs)
+        assert np.array_equal(q[a:b].float().cpu().numpy(), x if dtype == "f32" else ref.to_bf16(x))
+
+
+@pytest.mark.parametrize("rot,what", [(r, w) for r in (0, 32, 128) for w in ("angles", "length", "table") if r or w != "angles"])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_queries_of_a_refused_sequence_stay(rot, what, in_place):
+    c = Case([(4, 70), (2, 20), (3, 70)], G=2, seed=113).on_gpu()
+    if what == "angles":
+        c.meta[1][2] = 40                      # only the first sequence reaches past the table
+    cs = torch.from_numpy(angles(69 if what == "angles" else 100, rot, c.r)).to(DEV) if rot else None
+    if what == "length":
+        c.meta[1][0] = 3
+    if what == "table":
+        c.meta[1][0] = c.maxp * c.pt + 1
+    k, q = c.gpu(c.token(c.Hkv)), c.gpu(c.q)
+    before = q.clone()
+    out = q if in_place else torch.full_like(q, 7.0)
+    stays = out[:4].clone()
+    kda.kda_kv_append(c.pool, FMT[c.fmt], c.pt, *c.meta, c.max_q, q, k, k, cs, out, c.status)
+    assert kda.kda_sync_status(c.status) == (kda.KDA_EDEVICE, kda.KDA_DEV_BAD_META)
+    assert torch.equal(out[:4], stays)
+    assert (rot == 0 and torch.equal(out[4:], before[4:])) or (rot and not torch.equal(out[4:], before[4:]) and (out[4:] != 7).any())
+
+
+@pytest.mark.parametrize("rot", [0, 32])
+def test_query_rows_that_no_sequence_owns_stay(rot):
+    c = Case([(2, 20), (9, 70)], G=2, seed=117).on_gpu()
+    q = torch.cat([c.gpu(c.q), c.gpu(c.q)])
+    k = q[:, :c.Hkv].contiguous()
+    out = torch.full_like(q, 7.0)
+    cs = torch.from_numpy(angles(100, rot, c.r)).to(DEV) if rot else None
+    kda.kda_kv_append(c.pool, FMT[c.fmt], c.pt, *c.meta, c.max_q, q, k, k, cs, out, c.status)
+    assert kda.kda_sync_status(c.status) == (kda.KDA_OK, 0)
+    assert (out[c.T:] == 7).all() and not (out[:c.T] == 7).all(-1).any()
