@@ -175,9 +175,9 @@ __global__ void __launch_bounds__(NT) kv_append_kernel(KvAppendArgs a, int32_t q
         auto start = [&](int m) { return (int64_t)(__ldg(a.cu_q + m) / pt) + 2 * (int64_t)m; };
         s = kv_find(a.nseq, item, start);
         q = kv_seq(a.cu_q, a.kv_len, s, a.T_tot, a.max_q, a.kv);
-        if (q.n == 0) return;
+        if (q.n == 0 || item < start(s)) return;
         const int64_t b = (int64_t)((q.len - q.n) / pt) + (item - start(s));
-        if (item < start(s) || b * pt >= q.len) return;
+        if (b * pt >= q.len && !no_place(a, q)) return;
         block = (int)b;
     }
     const int old = q.len - q.n;

@@ -267,3 +267,17 @@ def test_query_rows_that_no_sequence_owns_stay(rot):
     kda.kda_kv_append(c.pool, FMT[c.fmt], c.pt, *c.meta, c.max_q, q, k, k, cs, out, c.status)
     assert kda.kda_sync_status(c.status) == (kda.KDA_OK, 0)
     assert (out[c.T:] == 7).all() and not (out[:c.T] == 7).all(-1).any()
+
+
+@pytest.mark.parametrize("n", [1, 3, 20, 200])
+@pytest.mark.parametrize("rot", [0, 32])
+def test_new_tokens_of_a_sequence_without_length_are_reported(n, rot):
+    c = Case([(n, n), (2, 20)], seed=114).on_gpu()
+    c.meta[1][0] = 0
+    before = c.pool.base.clone()
+    k = c.gpu(c.token(c.Hkv))
+    cs = torch.from_numpy(angles(300, rot, c.r)).to(DEV) if rot else None
+    kda.kda_kv_append(c.pool, FMT[c.fmt], c.pt, *c.meta, c.max_q, None, k, k, cs, None, c.status)
+    assert kda.kda_sync_status(c.status) == (kda.KDA_EDEVICE, kda.KDA_DEV_BAD_META)
+    mine = torch.from_numpy(c.table[0][c.table[0] >= 0]).to(DEV)
+    assert torch.equal(c.pool.base[mine], before[mine]) and not torch.equal(c.pool.base, before)
