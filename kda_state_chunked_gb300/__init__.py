@@ -537,42 +537,51 @@ def kda_ckpt_restore_q8(pool: Pool, H: int, d: int, dtype: int, ckpt_pages, acti
 # A decode step makes these calls once a layer and runs for microseconds on the GPU, so their host
 # side is kept short: addresses go as plain integers, the library and the current stream are looked
 # up without locks or wrapper objects.
-def _address(t):
-    """Device address of a contiguous CUDA tensor (None: NULL)."""
+def _address(t, gpu: int):
+    """Device address of a contiguous tensor on that GPU (None: NULL)."""
     if t is None:
         return None
-    if not t.is_cuda or not t.is_contiguous():
-        raise ValueError("expected a contiguous CUDA tensor")
+    if t.get_device() != gpu or not t.is_contiguous():
+        raise ValueError("expected a contiguous tensor on the GPU of the call's tokens")
     return t.data_ptr()
 
 
-def _rows(t, H: int, d: int):
-    """(device address, token stride) of a [T, H, d] CUDA tensor whose token rows are whole: the
-    parts of a fused projection qualify."""
+def _rows(t, H: int, d: int, gpu: int):
+    """(device address, token stride) of a [T, H, d] tensor on that GPU whose token rows are whole:
+    the parts of a fused projection qualify."""
     T, h, w = t.shape
     row, head, elem = t.stride()
-    if not t.is_cuda or h != H or w != d or (T and (elem != 1 or (h > 1 and head != d))):
-        raise ValueError("expected a [T, H, d] CUDA tensor with contiguous heads")
+    if t.get_device() != gpu or h != H or w != d or (T and (elem != 1 or (h > 1 and head != d))):
+        raise ValueError("expected a [T, H, d] tensor with contiguous heads on the GPU of the call's tokens")
     return t.data_ptr(), (row if T > 1 else H * d)
 
 
-def _batch(cu, lens, page_table):
-    """(nseq, max_pages, addresses) of a batch's device int32 arrays."""
+def _batch(cu, lens, page_table, status, gpu: int):
+    """(nseq, max_pages, addresses) of a batch's device int32 arrays, the status word's last."""
     import torch
     nseq, max_pages = page_table.shape
     i32 = torch.int32
     if (cu.dtype != i32 or lens.dtype != i32 or page_table.dtype != i32 or cu.numel() != nseq + 1
             or lens.numel() != nseq):
         raise ValueError("expected int32 [nseq + 1], [nseq] and [nseq, max_pages] CUDA tensors")
-    return nseq, max_pages, _address(cu), _address(lens), _address(page_table)
+    if status.dtype != i32:
+        raise ValueError("status must be int32 [1]")
+    if gpu < 0:
+        raise ValueError("expected CUDA tensors")
+    return nseq, max_pages, _address(cu, gpu), _address(lens, gpu), _address(page_table, gpu), _address(status, gpu)
 
 
-def _raw_stream(t, stream) -> int:
-    """The given stream, or the current one of t's device, as an integer."""
+def _f32(t, what: str) -> None:
+    if t is not None and (t.element_size() != 4 or not t.is_floating_point()):
+        raise ValueError(f"{what} must be float32")
+
+
+def _raw_stream(gpu: int, stream) -> int:
+    """The given stream, or the current one of the GPU, as an integer."""
     if stream is not None:
         return stream.cuda_stream
     import torch
-    return torch._C._cuda_getCurrentRawStream(t.get_device())
+    return torch._C._cuda_getCurrentRawStream(gpu)
 
 
 def kda_kv_page_bytes(Hkv: int, d: int, fmt: int, page_tokens: int) -> int:
@@ -585,16 +594,17 @@ def kda_kv_append(pool: Pool, fmt: int, page_tokens: int, cu_q, kv_len, page_tab
     apart; cu_q, kv_len, page_table: int32 CUDA [nseq + 1], [nseq], [nseq, max_pages]; cos_sin:
     fp32 CUDA [max_pos, rot_dim] or None; q_out: [T, Hq, d] contiguous."""
     T, Hkv, d = k.shape
-    dtype = k.dtype
-    nseq, max_pages, cu, lens, table = _batch(cu_q, kv_len, page_table)
-    kp, ks = _rows(k, Hkv, d)
-    vp, vs = _rows(v, Hkv, d)
+    dtype, gpu = k.dtype, k.get_device()
+    _f32(cos_sin, "cos_sin")
+    nseq, max_pages, cu, lens, table, word = _batch(cu_q, kv_len, page_table, status, gpu)
+    kp, ks = _rows(k, Hkv, d, gpu)
+    vp, vs = _rows(v, Hkv, d, gpu)
     if v.shape[0] != T or v.dtype != dtype:
         raise ValueError("k and v differ in tokens or type")
     Hq, qp, qs = 0, None, 0
     if q is not None and q_out is not None:
         Hq = q.shape[1]
-        qp, qs = _rows(q, Hq, d)
+        qp, qs = _rows(q, Hq, d, gpu)
         if q.shape[0] != T or q_out.shape != q.shape or q.dtype != dtype or q_out.dtype != dtype:
             raise ValueError("q, q_out and k differ in tokens or type")
     elif q is not None or q_out is not None:
@@ -602,12 +612,10 @@ def kda_kv_append(pool: Pool, fmt: int, page_tokens: int, cu_q, kv_len, page_tab
     pos, rot = 0, 0
     if cos_sin is not None:
         pos, rot = cos_sin.shape
-        if cos_sin.element_size() != 4:
-            raise ValueError("cos_sin must be float32")
     rc = (_lib or lib()).kda_kv_append(
         pool.handle, Hq, Hkv, d, dtype_of(k), fmt, page_tokens, nseq, T, max_q, cu, lens, table, max_pages, qp, qs, kp,
-        ks, vp, vs, _address(cos_sin), pos, rot, bool(interleaved), _address(q_out), _address(pool.base),
-        _address(status), _raw_stream(k, stream))
+        ks, vp, vs, _address(cos_sin, gpu), pos, rot, bool(interleaved), _address(q_out, gpu),
+        _address(pool.base, gpu), word, _raw_stream(gpu, stream))
     if rc < 0:
         raise KdaError(rc, "kda_kv_append")
 
@@ -619,10 +627,11 @@ def kda_kv_gather(pool: Pool, fmt: int, page_tokens: int, cu_out, begin, page_ta
     T, Hkv, d = k_out.shape
     if v_out.shape != k_out.shape or v_out.dtype != k_out.dtype:
         raise ValueError("k_out and v_out differ")
-    nseq, max_pages, cu, lens, table = _batch(cu_out, begin, page_table)
+    gpu = k_out.get_device()
+    nseq, max_pages, cu, lens, table, word = _batch(cu_out, begin, page_table, status, gpu)
     rc = (_lib or lib()).kda_kv_gather(
-        pool.handle, Hkv, d, dtype_of(k_out), fmt, page_tokens, nseq, T, cu, lens, table, max_pages, _address(k_out),
-        _address(v_out), _address(pool.base), _address(status), _raw_stream(k_out, stream))
+        pool.handle, Hkv, d, dtype_of(k_out), fmt, page_tokens, nseq, T, cu, lens, table, max_pages,
+        _address(k_out, gpu), _address(v_out, gpu), _address(pool.base, gpu), word, _raw_stream(gpu, stream))
     if rc < 0:
         raise KdaError(rc, "kda_kv_gather")
 
@@ -647,14 +656,17 @@ def kda_attn_paged(pool: Pool, Hkv: int, fmt: int, page_tokens: int, cu_q, kv_le
     T, Hq, d = q.shape
     if o.shape != q.shape or o.dtype != q.dtype:
         raise ValueError("q and o differ in shape or type")
-    if lse is not None and (lse.element_size() != 4 or lse.numel() != T * Hq):
-        raise ValueError("lse must be float32 [T, Hq]")
-    nseq, max_pages, cu, lens, table = _batch(cu_q, kv_len, page_table)
-    qp, qs = _rows(q, Hq, d)
+    _f32(lse, "lse")
+    if lse is not None and lse.numel() != T * Hq:
+        raise ValueError("lse must be [T, Hq]")
+    gpu = q.get_device()
+    nseq, max_pages, cu, lens, table, word = _batch(cu_q, kv_len, page_table, status, gpu)
+    qp, qs = _rows(q, Hq, d, gpu)
     rc = (_lib or lib()).kda_attn_paged(
         pool.handle, Hq, Hkv, d, dtype_of(q), fmt, page_tokens, nseq, T, max_q, cu, lens, table, max_pages, qp, qs,
-        d ** -0.5 if scale is None else scale, window, sinks, _address(o), _address(lse), _address(pool.base),
-        _address(workspace), workspace.numel() * workspace.element_size(), _address(status), _raw_stream(q, stream))
+        d ** -0.5 if scale is None else scale, window, sinks, _address(o, gpu), _address(lse, gpu),
+        _address(pool.base, gpu), _address(workspace, gpu), workspace.numel() * workspace.element_size(), word,
+        _raw_stream(gpu, stream))
     if rc < 0:
         raise KdaError(rc, "kda_attn_paged")
 
