@@ -107,11 +107,13 @@ __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatil
     return false;
 }
 
-// The same for a group of warps of which one looks and the others stand at named barrier `id`.
-template <int ID_THREADS>
-__device__ __forceinline__ bool wait_together(uint64_t *bar, uint32_t parity, volatile int *err, bool looks, int id) {
+// A group of warps of which one looks, by look(), and the others stand at named barrier `id`.  All get
+// its answer, and a wait that runs out sends the whole group out of its loop: were one warp to leave by
+// itself, the others would stand at the group's next barrier for good.
+template <int ID_THREADS, class F>
+__device__ __forceinline__ bool wait_together(F look, bool looks, int id) {
     uint32_t ok = 1;
-    if (looks) ok = wait_bar(bar, parity, err);
+    if (looks) ok = look();
     asm volatile(
         "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %0, 0;\n\tbarrier.cta.red.and.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
         : "+r"(ok)

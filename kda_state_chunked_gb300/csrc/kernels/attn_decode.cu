@@ -279,6 +279,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
         Look now = look(w);
         int stage = 0;
         uint32_t phase = 1;
+        int64_t asked = 0;   // units whose copies were started
         bool ok = true;
         while (ok && now.n > 0) {
             Walk next = w;
@@ -341,15 +342,22 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
                     if (FMT == KDA_KV_I8)
                         ptx::bulk_load(ring + stage * S::stage + 2 * S::tile + 16 * lane, rec + 2 * pt * S::row, 16, &full[stage]);
                 }
+                ++asked;
                 if (++stage == stages) stage = 0, phase ^= 1;
             }
             if (next.u == 0) u_first = 0;
             w = next;
             now = then;
         }
-        if (ok && __all_sync(0xFFFFFFFFu, wait_bar(&empty[stage], phase, err)) && lane == 0) {
-            jobs[stage].flags = kStop;
-            ptx::mbar_arrive(&full[stage]);
+        ok = ok && __all_sync(0xFFFFFFFFu, wait_bar(&empty[stage], phase, err));
+        if (ok) {
+            if (lane == 0) {
+                jobs[stage].flags = kStop;
+                ptx::mbar_arrive(&full[stage]);
+            }
+        } else {   // the copies under way land before the block ends
+            for (int64_t i = max((int64_t)0, asked - stages); i < asked; ++i)
+                wait_bar(&full[i % stages], (uint32_t)(i / stages) & 1u, nullptr);
         }
         return;
     }
@@ -360,7 +368,14 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
     float *acc = reinterpret_cast<float *>(sm + M::o_acc);
     uint32_t *qfrag = reinterpret_cast<uint32_t *>(sm + M::o_q);
     float *qs = reinterpret_cast<float *>(sm + M::o_qs);
-    auto meet = [&]() { asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory"); };
+    // The four warps meet; false where one has left, or is about to.  A warp that leaves sets the error
+    // first and then arrives once more: the others, each at this meeting or on its way there, get through
+    // it and find the error, so that no barrier holds anyone for good.
+    auto meet = [&]() {
+        asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
+        return *err == 0;
+    };
+    bool ok = true;
     // Where a lane's addresses for the fragment loads lie in a stage.  Row mr of matrix mm: for the keys
     // of the 8-bit cache, tokens 8 (mm % 2) + mr and unit mm / 2 (two slices); of the 16-bit one, the
     // same (a slice is two units); for its values, tokens 8 (mm / 2) + mr and unit mm % 2; for those of
@@ -378,11 +393,8 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
     int32_t pos[NR][2], nrows = 0, row0 = 0, tok0 = 0, head = 0;   // the item
     float o[NR][kDt][4], m[NR][2], l[NR][2], big[NR][2];   // big: 8-bit, the reference of probability times value scale
     for (;;) {
-        const bool ok = __all_sync(0xFFFFFFFFu, wait_bar(&full[stage], phase, err));
-        if (!ok) {
-            if (lane == 0) flag_status(a.kv.status, KDA_DEV_TIMEOUT);
-            break;
-        }
+        ok = __all_sync(0xFFFFFFFFu, wait_bar(&full[stage], phase, err));
+        if (!ok) break;
         const Job &jb = jobs[stage];
         const int32_t flags = jb.flags;
         if (flags & kStop) break;
@@ -446,7 +458,8 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
                 for (int n = 0; n < NT; ++n)
                     if (row < 8 * NR) qfrag[(((n * kKs + k) * NR + row / 8) * 32 + row % 8 * 4 + tt) * 2 + half] = z[n];
             }
-            meet();
+            ok = meet();
+            if (!ok) break;
             if constexpr (kRegQ) {
 #pragma unroll
                 for (int k = 0; k < kKs; ++k)
@@ -729,7 +742,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
                     ml[(warp * 16 + 8 * x + 2 * t + r) * 2 + 1] = l[x][r];
                 }
             }
-        meet();
+        ok = meet();
         // four rows at a time, so that the ring has the room
         const bool starts = flags & kStarts, ends = flags & kEnds;
 #pragma unroll
@@ -744,7 +757,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
                 if (FMT == KDA_KV_I8) f[r] = big[x][r] == -INFINITY ? 0.f : ex2(big[x][r] - kPBits - mt);
             }
 #pragma unroll 1
-            for (int half = 0; half < 2; ++half) {
+            for (int half = 0; ok && half < 2; ++half) {
                 const int base = 8 * x + 4 * half;
                 if (base >= nrows) break;
                 if (t >> 1 == half) {
@@ -764,7 +777,8 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
                         }
                     }
                 }
-                meet();
+                ok = meet();
+                if (!ok) break;
                 // a thread sums 4 columns of a row: D / 4 threads a row
                 const int sum_row = base + tid / (D / 4), unit4 = tid % (D / 4);
                 if (sum_row < min(nrows, base + 4)) {
@@ -794,11 +808,17 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
                         if (unit4 == 0) dst[D] = top, dst[D + 1] = lt;
                     }
                 }
-                if (base + 4 < nrows) meet();
+                if (base + 4 < nrows) ok = meet();
             }
         }
+        if (!ok) break;
         ml += ml_next;
         ml_next = -ml_next;
+    }
+    if (!ok) {
+        if (lane == 0) flag_status(a.kv.status, KDA_DEV_TIMEOUT);
+        __syncwarp();
+        asm volatile("bar.arrive 1, %0;" ::"n"(kWarps * 32) : "memory");
     }
 }
 

@@ -307,23 +307,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
         const uint32_t tO = tm + lanes + 256 + half * 128 + side * (D / 2);   // and its half of the output
         float2 *pair = reinterpret_cast<float2 *>(sm + L::pair);
         auto meet = [&]() { tcx::named_bar(1 + half * 4 + warp % 4, 64); };    // the two warps of these rows
-        auto wait_half = [&](int b, uint32_t parity) {                         // the half's eight warps
-            return wait_together<kSoftWarps / 2 * 32>(&bars[b], parity, err, warp % 8 == 0, 9 + half);
+        auto together = [&](auto look) {                                       // the half's eight warps
+            return wait_together<kSoftWarps / 2 * 32>(look, warp % 8 == 0, 9 + half);
         };
+        auto wait_half = [&](int b, uint32_t parity) { return together([&]() { return wait1(b, parity); }); };
         uint32_t n_s = 0, n_item = 0, n_o = 0;   // units of this half, items so far, of this half: the barriers' parities
         int32_t pos = -1, p_lo = 0, p_hi = 0;   // positions of this row, of the warp's rows
         bool in = false, ok = true;
         float m = -INFINITY, big = -INFINITY, l = 0.f, f_row = 0.f;   // big: 8-bit, the reference with value scales
         auto lift = [&]() { return (big == -INFINITY ? 0.f : big - m) - kPBits; };
-        for (uint32_t n = 0;; ++n) {
-            ok = wait_job(n);
-            if (!ok) break;
+        auto next_job = [&](uint32_t n) { return wait1(JFULL + (n + 1) % kJobs, (n + 1) / kJobs & 1); };
+        ok = wait_half(JFULL, 0);
+        for (uint32_t n = 0; ok; ++n) {            // job n is there; the next is waited for beside its scores
             const Job &jb = job(n);
             const int32_t flags = jb.flags, nrows = jb.nrows, j0 = jb.j0;
             if (flags & kStop) break;
             if (half * kHalf >= nrows) {           // nothing in this half
                 n_item += (flags & kEnd) != 0;
                 done(n);
+                ok = together([&]() { return next_job(n); });
                 continue;
             }
             const int32_t at = jb.row0 + row;
@@ -339,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) ptx::tmem_st16(tO + 16 * c, z);
             }
-            ok = wait_half(SFULL + half, n_s & 1);
+            ok = together([&]() { return next_job(n) && wait1(SFULL + half, n_s & 1); });
             if (!ok) break;
             ptx::tc_fence_after();
             if (flags & kBegin) f_row = qs[(n_item & 1) * kRows + row];
@@ -583,8 +585,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
     } else if (warp < kSoftWarps + kLoadWarps) {
         // ====================================================== queries, and keys and values
         const int lw = warp - kSoftWarps, lt = tid - kSoftWarps * 32;
-        auto wait_all = [&](int b, uint32_t parity) {             // the eight warps
-            return wait_together<kLoadWarps * 32>(&bars[b], parity, err, lw == 0, 11);
+        auto together = [&](auto look) {                          // the eight warps
+            return wait_together<kLoadWarps * 32>(look, lw == 0, 11);
+        };
+        auto wait_all = [&](int b, uint32_t parity) { return together([&]() { return wait1(b, parity); }); };
+        auto with_next = [&](int b, uint32_t parity, uint32_t n) {   // and the job behind job n
+            return together([&]() { return wait1(b, parity) && wait1(JFULL + (n + 1) % kJobs, (n + 1) / kJobs & 1); });
         };
         uint32_t n_item = 0;
         // 8-bit: the units' codes are read one unit ahead into registers.  A warp takes 16 tokens;
@@ -679,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
             tcx::warp_arrive(&bars[QFULL]);
             return true;
         };
-        bool ok = wait_job(0), stop = ok && (job(0).flags & kStop);
+        bool ok = wait_all(JFULL, 0), stop = ok && (job(0).flags & kStop);
         if (FMT == KDA_KV_I8 && ok && !stop) {
 #pragma unroll 1
             for (int v = 0; v < 2; ++v) {
@@ -701,16 +707,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                 // keys, then values: kc goes out, vc moves up, the same of the next unit is fetched
 #pragma unroll 1
                 for (int v = 0; v < 2; ++v) {
-                    ok = wait_all((v ? VEMPTY : KEMPTY) + st, par);
+                    ok = v ? wait_all(VEMPTY + st, par) : with_next(KEMPTY + st, par, n);
                     if (!ok) break;
                     put(kc, sm + (v ? L::v : L::k) + st * L::tile);
                     ptx::fence_proxy_async_smem();
                     tcx::warp_arrive(&bars[(v ? VFULL : KFULL) + st]);
-                    if (v == 0) {
-                        ok = wait_job(n + 1);
-                        if (!ok) break;
-                        stop = job(n + 1).flags & kStop;
-                    }
+                    if (v == 0) stop = job(n + 1).flags & kStop;
 #pragma unroll
                     for (int i = 0; i < kRegs; ++i) kc[i] = vc[i];
                     if (!stop) fetch(job(n + 1), v, vc);
@@ -720,8 +722,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                 // values that not every row sees: a token that no row sees is cleared (0 times what a
                 // stale slot holds need not be 0), and one with an infinity or a NaN is taken out and
                 // left to the rows that see it
-                ok = wait_all(VRAW + st, n >> 1 & 1);
+                ok = with_next(VRAW + st, n >> 1 & 1, n);
                 if (!ok) break;
+                stop = job(n + 1).flags & kStop;
                 if (!(jb.flags & kWhole) && lt < kUnit) {
                     uint8_t *line = sm + L::v + st * L::tile + lt * 128;
                     const int32_t j = jb.j0 + lt;
@@ -749,8 +752,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                     ptx::fence_proxy_async_smem();
                 }
                 tcx::warp_arrive(&bars[VFULL + st]);
-                ok = wait_job(n + 1);
-                stop = ok && (job(n + 1).flags & kStop);
             }
             done(n);
         }
