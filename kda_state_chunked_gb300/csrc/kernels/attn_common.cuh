@@ -122,10 +122,23 @@ __device__ __forceinline__ bool wait_together(F look, bool looks, int id) {
     return ok != 0;
 }
 
-// What a warp that walks the list of units says of each (bits of a job's flags): first, last unit of
-// its item in this CTA; every row sees every token; the item's own first, last unit is in this CTA;
-// no unit, the end.
-enum : int32_t { kBegin = 1, kEnd = 2, kWhole = 4, kStop = 8, kStarts = 16, kEnds = 32 };
+// The matrix unit cuts its sums instead of rounding them: over 27,000 products on one accumulator (a context
+// of a million tokens, where an item has a CTA for itself) outputs came out 2.5e-3 too small, more than
+// half a bf16's step.  So an item is taken in pieces of that many units, whose results are added in
+// rounded fp32 in the CTA's partial result: at most 2,048 products a piece, 1e-4.
+constexpr int kPieceUnits = 256;
+
+// What a warp that walks the list of units says of each (bits of a job's flags): first, last unit of a
+// piece; every row sees every token; the item's own first, last unit is in this CTA; no unit, the end;
+// the CTA has a further piece of the item, had one before.
+enum : int32_t { kBegin = 1, kEnd = 2, kWhole = 4, kStop = 8, kStarts = 16, kEnds = 32, kMore = 64, kAgain = 128 };
+
+// The flags of a piece's ends, for the i-th unit of an item in this CTA; last: the last one.
+__device__ __forceinline__ int32_t piece_flags(int32_t i, bool last) {
+    const int32_t k = i % kPieceUnits;
+    return (k == 0 ? kBegin : 0) | (last || k + 1 == kPieceUnits ? kEnd : 0) | (!last && k + 1 == kPieceUnits ? kMore : 0) |
+           (i >= kPieceUnits ? kAgain : 0);
+}
 
 // A place in the list of units.
 struct Walk {

@@ -312,8 +312,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
                     Job &jb = jobs[stage];
                     const bool ends = left >= x.units - u;   // the item's last unit is in this share
                     jb.j0 = j0;
-                    jb.flags = (u == u_first ? kBegin : 0) | (u + 1 == x.units || left == 1 ? kEnd : 0) |
-                               (u_first == 0 ? kStarts : 0) | (ends ? kEnds : 0);
+                    jb.flags = piece_flags(u - u_first, u + 1 == x.units || left == 1) | (u_first == 0 ? kStarts : 0) | (ends ? kEnds : 0);
                     jb.base = x.q.len - x.q.n;
                     jb.row0 = x.row0, jb.nrows = x.nrows, jb.tok0 = x.q.tok0, jb.head = w.h;
                     jb.live = live, jb.whole = whole, jb.lead = lead;
@@ -782,6 +781,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
                 // a thread sums 4 columns of a row: D / 4 threads a row
                 const int sum_row = base + tid / (D / 4), unit4 = tid % (D / 4);
                 if (sum_row < min(nrows, base + 4)) {
+                    auto partial = [&]() { return a.part + ((int64_t)(blockIdx.x * 2 + (starts ? 1 : 0)) * 16 + sum_row) * kPartRow<D>; };
                     float top = -INFINITY, lt = 0.f;
 #pragma unroll
                     for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[(w * 16 + sum_row) * 2]);
@@ -794,7 +794,18 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
                                                                            4 * acc_unit(sum_row, unit4));
                         v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
                     }
-                    if (starts && ends) {
+                    if (flags & kAgain) {   // to an earlier piece's
+                        const float *was = partial();
+                        const float4 u = *reinterpret_cast<const float4 *>(was + 4 * unit4);
+                        const float both = fmaxf(top, was[D]), ref = both == -INFINITY ? 0.f : both;
+                        const float fv = ex2(top - ref), fu = ex2(was[D] - ref);
+                        v = make_float4(v.x * fv + u.x * fu, v.y * fv + u.y * fu, v.z * fv + u.z * fu, v.w * fv + u.w * fu);
+                        lt = lt * fv + was[D + 1] * fu;
+                        top = both;
+                        // a row's threads, of one warp, have read what one of them replaces
+                        __syncwarp(D == 128 ? ~0u : 0xFFFFu << (lane & 16));
+                    }
+                    if (starts && ends && !(flags & kMore)) {
                         const int32_t at_row = row0 + sum_row, tok = token_of(a, at_row);
                         const int64_t at = (int64_t)(tok0 + tok) * a.Hq + head * a.G + at_row - tok * a.G;
                         const float inv = 1.f / lt;
@@ -803,7 +814,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
                         store_row4(a.o, a.dtype, at * D + 4 * unit4, v);
                         if (a.lse && unit4 == 0) a.lse[at] = lse_of(top, lt);
                     } else {
-                        float *dst = a.part + ((int64_t)(blockIdx.x * 2 + (starts ? 1 : 0)) * 16 + sum_row) * kPartRow<D>;
+                        float *dst = partial();
                         *reinterpret_cast<float4 *>(dst + 4 * unit4) = v;
                         if (unit4 == 0) dst[D] = top, dst[D + 1] = lt;
                     }

@@ -521,23 +521,32 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
             tcx::warp_arrive(&bars[PFULL + half]);
             ++n_s;
             if (flags & kEnd) {
-                // ---- the item's output, or this CTA's part of it
+                // ---- the item's output, or this CTA's part of it, added to an earlier piece's
+                const bool all = (flags & kStarts) && (flags & kEnds) && !(flags & kMore);
+                float *part = a.part + ((int64_t)(blockIdx.x * 2 + (flags & kStarts ? 1 : 0)) * kRows + row) * kPartRow<D>;
+                float unscale = FMT == KDA_KV_I8 ? exp2f(lift()) : 1.f, again = 0.f, l_was = 0.f;
+                if (flags & kAgain) {
+                    const float was = part[D], both = fmaxf(m, was), ref = both == -INFINITY ? 0.f : both;
+                    const float f = ex2(m - ref);
+                    again = ex2(was - ref);
+                    l_was = part[D + 1] * again;
+                    unscale *= f, l *= f;
+                    m = both;
+                }
                 {
                     float2 *mine = pair + ((n_s & 1) * 2 + side) * kRows, *other = pair + ((n_s & 1) * 2 + (side ^ 1)) * kRows;
                     mine[row].x = l;
                     meet();
-                    l += other[row].x;
+                    l += other[row].x + l_was;
                     meet();              // the next item's first maxima go to the same place
                 }
                 ok = wait_half(OFULL + half, n_o++ & 1);
                 if (!ok) break;
                 ptx::tc_fence_after();
-                const bool all = (flags & kStarts) && (flags & kEnds);
                 const int32_t tok = token_of(a, at);
                 const int64_t orow = ((int64_t)jb.tok0 + tok) * a.Hq + jb.head * a.G + at - tok * a.G;
-                const float unscale = FMT == KDA_KV_I8 ? exp2f(lift()) : 1.f;
-                const float f = all ? (l == 0.f ? 0.f : unscale / l) : unscale;
-                float *part = a.part + ((int64_t)(blockIdx.x * 2 + (flags & kStarts ? 1 : 0)) * kRows + row) * kPartRow<D>;
+                const float norm = !all ? 1.f : l == 0.f ? 0.f : 1.f / l, f = unscale * norm;
+                again *= norm;
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
                     float o[1][16];
@@ -548,6 +557,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
 #pragma unroll
                         for (int i = 0; i < 16; ++i) o[y][i] = all && l == 0.f ? 0.f : o[y][i] * f;
                         const int col = side * (D / 2) + 16 * (c + y);
+                        if (flags & kAgain)
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) o[y][i] += part[col + i] * again;
                         if (in && all) {
                             uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.o) + orow * D + col);
 #pragma unroll
@@ -948,7 +960,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                     if (i == 0) {
                         const bool ends = left >= t.units - u;   // the item's last unit is in this share
                         jb.j0 = j0;
-                        jb.flags = (u == u_first ? kBegin : 0) | (u + 1 == t.units || left == 1 ? kEnd : 0) |
+                        jb.flags = piece_flags(u - u_first, u + 1 == t.units || left == 1) |
                                    (all_see(a, t, j0, kUnit) && live == 0xFFu ? kWhole : 0) | (u_first == 0 ? kStarts : 0) |
                                    (ends ? kEnds : 0);
                         jb.base = t.q.len - t.q.n;

@@ -16,7 +16,7 @@ import torch
 
 import kda_state_chunked_gb300 as kda
 import kv_ref as ref
-from test_gpu_kv import DEV, FMT, KINDS, Case
+from test_gpu_kv import DEV, FMT, KINDS, Case, i32
 
 pytestmark = pytest.mark.gpu
 
@@ -281,3 +281,51 @@ def test_new_tokens_of_a_sequence_without_length_are_reported(n, rot):
     assert kda.kda_sync_status(c.status) == (kda.KDA_EDEVICE, kda.KDA_DEV_BAD_META)
     mine = torch.from_numpy(c.table[0][c.table[0] >= 0]).to(DEV)
     assert torch.equal(c.pool.base[mine], before[mine]) and not torch.equal(c.pool.base, before)
+
+
+# ------------------------------------------------------------------ sums over long contexts
+def shared_context(L, Hkv, d, fmt, seed):
+    """One context of L tokens whose values lie around a mean of 1 to 2 a column: pool, its pages, and the
+    keys and values that the cache stands for."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    pt = 64
+    blocks = -(-L // pt)
+    pool = kda.Pool(kda.kda_kv_page_bytes(Hkv, d, FMT[fmt], pt), blocks, DEV)
+    pages = torch.randperm(blocks, generator=g, device=DEV).to(torch.int32).view(1, blocks)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    mean = 1 + torch.rand(Hkv, d, generator=g, device=DEV)
+    for a in range(0, L, 1 << 17):
+        b = min(L, a + (1 << 17))
+        k = 0.1 * torch.randn(b - a, Hkv, d, generator=g, device=DEV)
+        v = mean + 0.1 * torch.randn(b - a, Hkv, d, generator=g, device=DEV)
+        kda.kda_kv_append(pool, FMT[fmt], pt, i32([0, b - a]), i32([b]), pages, b - a, None, k, v, None, None, status)
+    k, v = (torch.empty(L, Hkv, d, device=DEV) for _ in range(2))
+    kda.kda_kv_gather(pool, FMT[fmt], pt, i32([0, L]), i32([0]), pages, k, v, status)
+    assert kda.kda_sync_status(status) == (kda.KDA_OK, 0)
+    return pool, pages, k, v, g
+
+
+# The mean error of a row set's 512 columns: a bf16's rounding, 1.7e-3 in each, leaves 3e-4 at four times its
+# deviation, and sums cut no more than 2,048 times 1e-4; of a single column, half a bf16's step and that.
+@pytest.mark.parametrize("fmt", [ref.I8, ref.BF16])
+@pytest.mark.parametrize("n,nseq,L", [(1, 512, 524288), (4, 160, 70001), (1024, 1, 524288), (300, 24, 70001)])
+def test_sums_over_long_contexts_are_not_cut(fmt, n, nseq, L):
+    Hkv, G, d = 4, 4, 128
+    pool, pages, k, v, g = shared_context(L, Hkv, d, fmt, 118)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    q = torch.randn(nseq * n, Hkv * G, d, generator=g, device=DEV).to(torch.bfloat16)
+    o, lse = torch.empty_like(q), torch.empty(nseq * n, Hkv * G, device=DEV)
+    kda.kda_attn_paged(pool, Hkv, FMT[fmt], 64, i32(np.arange(nseq + 1) * n), i32([L] * nseq),
+                       pages.expand(nseq, -1).contiguous(), n, q, o, kda.attn_workspace(q, Hkv, nseq, n), status, lse=lse)
+    assert kda.kda_sync_status(status) == (kda.KDA_OK, 0)
+    off = []
+    for t in np.linspace(0, nseq * n - 1, 6).astype(int):
+        for h in range(Hkv):
+            seen = L - n + t % n + 1
+            s = d ** -0.5 * (k[:seen, h].double() @ q[t, h * G].double())
+            e = torch.softmax(s, 0) @ v[:seen, h].double()
+            off.append((o[t, h * G].double() - e) / e)
+            assert abs(float(lse[t, h * G]) - float(torch.logsumexp(s, 0))) <= 1e-5 * (1 + 14)
+    off = torch.stack(off)
+    assert float(off.abs().max()) <= 2.0 ** -8 + 1e-4 and abs(float(off.mean())) <= 4e-4
+    pool.close()
