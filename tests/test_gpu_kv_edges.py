@@ -84,6 +84,20 @@ def check(c, window=0, sinks=0, **kw):
     return o, lse
 
 
+# ------------------------------------------------------------------ every group of tokens counts in its row
+@pytest.mark.parametrize("fmt,dtype,d", KINDS)
+@pytest.mark.parametrize("n", [1, 4, 40])
+def test_every_group_of_tokens_is_felt_by_its_rows(fmt, dtype, d, n):
+    """One short context beside long ones, each row against its own answer; the same check has to
+    notice a group of 16 tokens left out anywhere."""
+    c = Case([(n, n), (n, 700), (n, 1000)], fmt=fmt, dtype=dtype, d=d, Hkv=1, seed=111, qscale=0.5, spread=0.2)
+    o, lse = check(c)
+    _, el, noise = exact(c)
+    for first in range(0, 688, 48):
+        with pytest.raises(AssertionError):
+            hold(c, o, lse, (exact(c, lose=np.arange(first, first + 16))[0], el, noise))
+
+
 # ------------------------------------------------------------------ scales that are no numbers
 @pytest.mark.parametrize("which,bad", [(0, np.nan), (1, np.nan), (1, np.inf)])
 @pytest.mark.parametrize("G,n,pt", [(1, 40, 16), (1, 150, 48), (5, 40, 16), (2, 3, 16)])
