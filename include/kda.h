@@ -505,7 +505,8 @@ int64_t kda_attn_workspace_bytes(int32_t Hq, int32_t Hkv, int32_t d, int32_t dty
  * lse = -infinity.  What a query does not see never changes its result, a NaN or an infinity
  * included; pages that no query of the call sees are not read, and their table entries may hold
  * anything.  Sums, maxima and accumulators are fp32; KDA_F32 calls keep fp32 accuracy throughout.
- * KDA_BF16 calls round each probability before its product with the value: to bf16 over KDA_KV_BF16;
+ * KDA_BF16 calls round each probability before its product with the value: over KDA_KV_BF16 to bf16,
+ * or to 16 bits where max_q * Hq / Hkv is at most 16 (a caller who wants more passes KDA_F32 tokens);
  * over KDA_KV_I8, times the block's value scale, to fp16 with a range that follows the query's own
  * tokens: a product of probability and value scale 2^19 times below the largest that the query sees
  * loses bits, one 2^30 below may add nothing to o.  Results do not depend on timing: the same call

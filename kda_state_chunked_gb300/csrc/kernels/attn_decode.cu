@@ -219,6 +219,11 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
     constexpr int kGr = S::groups;
     constexpr bool kRegQ = NT == 1;   // query fragments stay in registers
     constexpr bool kF16 = FMT == KDA_KV_I8 && NT == 1;   // the products' type: fp16, or bf16
+    // Terms of a probability.  bf16 calls over the 16-bit cache split them in two, which keep 16 bits: one term
+    // of 8 took a third of the outputs off their nearest bf16 (2.2e-3 of their size instead of 1.66e-3) and
+    // saved nothing, as the bytes bound these calls (256 windowed requests 173.4 and 173.7 us; 16 rows a head
+    // 103 and 107).
+    constexpr int kPt = NT == 1 && !kF16 ? 2 : NT;
     constexpr uint32_t kBias = kF16 ? 0x80808080u : 0u;  // of a code that codes2() takes
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = ptx::smem_align1024(smem_raw);
@@ -613,7 +618,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
 #pragma unroll
                 for (int r = 0; r < 2; ++r)
                     up[x][r] = FMT == KDA_KV_I8 && big[x][r] != -INFINITY ? ex2(m[x][r] - big[x][r] + kPBits) : 0.f;
-            uint32_t pb[kGr][NR][2][NT];
+            uint32_t pb[kGr][NR][2][kPt];
 #pragma unroll
             for (int y = 0; y < kGr; ++y) {
                 // probabilities, and what of them is rounded: 8-bit, p vs 2^(m - big + 6).  (Where vs 2^(m - big)
@@ -633,9 +638,9 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
                     }
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {   // tokens 0-7, 8-15: rows of the transposed operand
-                        split2<kF16, NT>(p[2 * h], p[2 * h + 1], pb[y][x][h]);
+                        split2<kF16, kPt>(p[2 * h], p[2 * h + 1], pb[y][x][h]);
 #pragma unroll
-                        for (int z = 0; z < NT; ++z) pb[y][x][h][z] = transpose8(pb[y][x][h][z]);
+                        for (int z = 0; z < kPt; ++z) pb[y][x][h][z] = transpose8(pb[y][x][h][z]);
                     }
                 }
             }
@@ -667,13 +672,14 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
 #pragma unroll
                             for (int x = 0; x < NR; ++x) {
                                 if constexpr (NT == 1) {
-                                    mma<kF16>(o[x][j], af, pb[y][x][0][0], pb[y][x][1][0]);
+#pragma unroll
+                                    for (int z = kPt - 1; z >= 0; --z) mma<kF16>(o[x][j], af, pb[y][x][0][z], pb[y][x][1][z]);
                                 } else {
                                     // the matrix unit's sums are cut, not rounded: over a long context their
                                     // bias came to 2e-6 of a float32 result, so each group's is added here
                                     float d[4] = {};
 #pragma unroll
-                                    for (int z = NT - 1; z >= 0; --z) mma<kF16>(d, af, pb[y][x][0][z], pb[y][x][1][z]);
+                                    for (int z = kPt - 1; z >= 0; --z) mma<kF16>(d, af, pb[y][x][0][z], pb[y][x][1][z]);
 #pragma unroll
                                     for (int e = 0; e < 4; ++e) o[x][j][e] += d[e];
                                 }
@@ -713,7 +719,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
                         for (int x = 0; x < NR; ++x) {
                             float d[4] = {};
 #pragma unroll
-                            for (int z = NT - 1; z >= 0; --z) mma<kF16>(d, w, pb[0][x][0][z], pb[0][x][1][z]);
+                            for (int z = kPt - 1; z >= 0; --z) mma<kF16>(d, w, pb[0][x][0][z], pb[0][x][1][z]);
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
                                 if (pos[x][e & 1] == q) o[x][i][e] += d[e];
