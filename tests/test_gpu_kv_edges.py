@@ -357,3 +357,32 @@ def test_few_rows_over_the_16_bit_cache_round_only_the_output(d, n, G, window, s
     o, _ = check(c, window, sinks)
     nearest = ref.to_bf16(exact(c, window, sinks)[0].astype(np.float32))
     assert (o.float().cpu().numpy() != nearest).mean() <= 0.05
+
+
+# Contexts a little longer than the pieces that sums are taken in, so that some rows see nothing of the last one;
+# with a window, rows that see nothing of the first.  (Half a bf16's step, and 1e-4 as above.)
+@pytest.mark.parametrize("fmt", [ref.I8, ref.BF16])
+@pytest.mark.parametrize("n,nseq,L,window", [(200, 64, 32868, 0), (200, 64, 40000, 33000), (4, 160, 32770, 0), (4, 160, 16386, 0),
+                                             (1, 200, 33001, 33000)])
+def test_pieces_that_not_every_row_sees(fmt, n, nseq, L, window):
+    Hkv, G, d, sinks = 4, 1, 64, 3
+    pool, pages, k, v, g = shared_context(L, Hkv, d, fmt, 120)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    q = torch.randn(nseq * n, Hkv * G, d, generator=g, device=DEV).to(torch.bfloat16)
+    o, lse = torch.empty_like(q), torch.empty(nseq * n, Hkv * G, device=DEV)
+    kda.kda_attn_paged(pool, Hkv, FMT[fmt], 64, i32(np.arange(nseq + 1) * n), i32([L] * nseq),
+                       pages.expand(nseq, -1).contiguous(), n, q, o, kda.attn_workspace(q, Hkv, nseq, n), status, window=window,
+                       sinks=sinks, lse=lse)
+    assert kda.kda_sync_status(status) == (kda.KDA_OK, 0)
+    p, j = L - n + torch.arange(n, device=DEV)[:, None], torch.arange(L, device=DEV)
+    hide = j > p
+    if window:
+        hide |= (j <= p - window) & (j >= sinks)
+    for s in range(0, nseq, 3):
+        for h in range(Hkv):
+            x = d ** -0.5 * (q[s * n:s * n + n, h].double() @ k[:, h].double().T)
+            x.masked_fill_(hide, -np.inf)
+            e = torch.softmax(x, 1) @ v[:, h].double()
+            assert float(((o[s * n:s * n + n, h].double() - e) / e).abs().max()) <= 2.0 ** -8 + 1e-4
+            assert float((lse[s * n:s * n + n, h] - torch.logsumexp(x, 1)).abs().max()) <= 1e-5 * (1 + 11)
+    pool.close()
