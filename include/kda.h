@@ -425,7 +425,7 @@ int kda_ckpt_restore_q8(kda_pool *pool, int32_t H, int32_t d, int32_t dtype, int
  *
  * A page is one block of page_tokens tokens (a multiple of 16, 16 to 128) of all Hkv heads of one
  * layer: Hkv records in head order, each
- *     K tile | V tile | KDA_KV_I8 only: float K scale, float V scale, 8 zero bytes
+ *     K tile | V tile | KDA_KV_I8 only: float K scale, float V scale, 8 bytes that no call writes
  * A tile is page_tokens rows of d elements (bf16, or int8 codes), cut into lines of 128 bytes (64
  * where a row has only 64): line block c holds bytes [128 c, 128 c + 128) of every row, row after
  * row, and the 16-byte unit u of token slot t's line lies at place u ^ (t % 8) (64-byte lines:
@@ -437,7 +437,7 @@ int kda_ckpt_restore_q8(kda_pool *pool, int32_t H, int32_t d, int32_t dtype, int
  * scale = max(max |x| over the new tokens / 127, the block's scale if it holds older tokens) and
  * code = round-to-nearest-even(x / scale), both divisions IEEE fp32; when the scale grows, older
  * codes c become rne(c * old scale / scale).  A block with an infinity or a NaN in it reads as NaN
- * (that head's K or V); a scale of 0 reads as zeros.
+ * (that head's K or V); a scale of 0 reads as zeros.  Scales are not negative.
  *
  * Batches: cu_q (device int32 [nseq + 1], ascending) cuts the call's T_tot packed token rows into
  * sequences; kv_len (device int32 [nseq]) is each sequence's length in the cache with the call's

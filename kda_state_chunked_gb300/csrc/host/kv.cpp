@@ -61,9 +61,9 @@ int status_of(cudaError_t e) { return e == cudaSuccess ? KDA_OK : KDA_ECUDA; }
 
 // Rows of a tile.  The register kernel holds 16 rows; with more rows a sequence it reads the cache
 // again for every 16, while a tile of the tensor-memory kernel takes 256 of them in the same time.  32
-// sequences of 4096 tokens and 8 heads of 128, with 16, 32 and 64 rows a head: 8-bit cache 74, 127 and
-// 237 us by the first, 165, 166 and 169 by the second; 16-bit cache with 16 and 32 rows 102 and 185
-// against 117 and 118.  float32 calls stay on the register kernel: its products split an operand into
+// sequences of 4096 tokens and 8 heads of 128, with 16, 32 and 64 rows a head: 8-bit cache 78, 134 and
+// 253 us by the first, 167, 168 and 171 by the second; 16-bit cache with 16 and 32 rows 107 and 193
+// against 116 and 117.  float32 calls stay on the register kernel: its products split an operand into
 // terms.
 int32_t attn_rows(int32_t dtype, int32_t fmt, int32_t max_q, int32_t G) {
     const int64_t most = fmt == KDA_KV_I8 ? 2 * kda::kAttnDecodeRows : kda::kAttnDecodeRows;
@@ -176,9 +176,9 @@ int kda_attn_paged(const kda_pool *pool, int32_t Hq, int32_t Hkv, int32_t d, int
     const int64_t units = std::max<int64_t>(1, (tokens + kda::kAttnMinUnit - 1) / kda::kAttnMinUnit);
     a.ctas = (int32_t)std::min<int64_t>(attn_ctas(rows), std::max<int64_t>(1, tiles * Hkv * units));
     // Few, short items: a CTA each; splitting them costs another launch to join the parts.  64 items of
-    // 256, 640 and 1000 tokens of an 8-bit cache (2, 5 and 8 units): 6.7, 9.6 and 12.4 us whole, 10.0,
-    // 12.7 and 14.0 split; of 384 tokens of a 16-bit one (6 units) 7.8 and 11.0; but 4 items of 8 units
-    // 12.1 and 11.0.
+    // 256, 640 and 1000 tokens of an 8-bit cache (2, 5 and 8 units): 6.7, 10.0 and 13.0 us whole, 10.0,
+    // 12.9 and 14.2 split; of 384 tokens of a 16-bit one (6 units) 8.0 and 11.3; but 4 items of 8 units
+    // 12.7 and 10.7.
     a.whole = rows == kda::kAttnDecodeRows && (int64_t)max_q * a.G <= rows && (int64_t)nseq * Hkv <= kda::kAttnSms &&
               tokens <= kWholeUnits * (fmt == KDA_KV_I8 ? 128 : 64);
     if (a.whole) a.ctas = nseq * Hkv;

@@ -15,11 +15,11 @@
 // one page, and a page's rows are contiguous); with each warp aiming its own copies the bookkeeping
 // was 40% of the instructions.  The other four take a step of a unit's tokens each (32 of the 8-bit
 // cache, 16 of the 16-bit one) and run alone, with their own maxima, sums and 16 x D accumulators.
-// They meet only at an item's beginning, to split its queries, and at its end.
+// They meet only at a piece's beginning, to split its queries, and at its end.
 //
-// Measured (d = 128): 32 contexts of 512 to 32768 tokens, 8-bit: 200 us, 6.1 TB/s, 91% of the copy
-// rate; one of 1,048,576 tokens: 186 us, 86%; 256 requests through a window of 1024, 16-bit: 172 us,
-// 87%.  4 float32 drafts of 24 requests, 8-bit, d = 64: 28.8 us, where the products count (two or four
+// Measured (d = 128): 32 contexts of 512 to 32768 tokens, 8-bit: 202 us, 6.0 TB/s, 90% of the copy
+// rate; one of 1,048,576 tokens: 185 us, 87%; 256 requests through a window of 1024, 16-bit: 172 us,
+// 87%.  4 float32 drafts of 24 requests, 8-bit, d = 64: 33 us, where the products count (three or six
 // for each of the 16-bit forms' one) and the split leaves 1.5 steps a warp.
 //
 // 8-bit cache: codes c become fp16 exactly (the byte under the exponent of 1024, less 1152), a

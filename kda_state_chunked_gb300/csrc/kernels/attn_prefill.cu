@@ -27,12 +27,12 @@
 // in every role the kernel was 220 KB of code and stood waiting for instructions, 9,700 cycles a
 // unit instead of the 4,400 to 5,300 of now.
 //
-// Measured: 4096 queries of 32 heads of 128 behind 12288 tokens, 8-bit cache: 1,037 us, 930 TFLOP/s,
+// Measured: 4096 queries of 32 heads of 128 behind 12288 tokens, 8-bit cache: 1,034 us, 930 TFLOP/s,
 // 49% of the plain product's rate; four ragged prompts of up to 8192 tokens through a window of 1024:
-// 286 us, 0.30 of that rate.  The pipe is busy 2,100 of a unit's cycles.  What stands in its way is a
+// 283 us, 0.30 of that rate.  The pipe is busy 2,100 of a unit's cycles.  What stands in its way is a
 // half's way from its scores to its probabilities (2,700 cycles) with the pipe's own 1,000 and two
 // hand-overs behind it; the other half covers part of that only, as both use the same issue slots
-// (59% taken).  One pass over the scores instead of two wants 32 more registers than there are:
+// (63% taken).  One pass over the scores instead of two wants 32 more registers than there are:
 // 20% slower, and 15% with registers taken from the other warps.
 //
 // 8-bit cache: as in the register kernel codes are exact in fp16 and query rows scaled by a power
