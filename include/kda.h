@@ -446,7 +446,8 @@ int kda_ckpt_restore_q8(kda_pool *pool, int32_t H, int32_t d, int32_t dtype, int
  * sequence (host).  Nothing is read back to the host, so the calls can be captured in a graph and
  * replayed on new lengths.  Metadata out of range (n > max_q, kv_len beyond the table, cu_q beyond
  * T_tot) sets KDA_DEV_BAD_META and that sequence is skipped; a page id outside the pool sets
- * KDA_DEV_BAD_PAGE and that block is skipped.
+ * KDA_DEV_BAD_PAGE and that block is skipped.  Output rows of a skipped sequence, and those that no
+ * sequence owns, stay as they were.
  *
  * Token tensors q, k, v are [T_tot][H][d] in dtype with token rows `stride` elements apart (at
  * least H * d: the parts of one fused projection will do); pointers are 16-byte aligned and
@@ -470,8 +471,7 @@ int64_t kda_kv_page_bytes(int32_t Hkv, int32_t d, int32_t fmt, int32_t page_toke
  *   interleaved   0: element i turns with i + rot_dim / 2; else 2 i with 2 i + 1
  * The pages written must be private to their sequence (a shared prefix ends on a block's end, or
  * its last block is copied first).  A call whose kv_len < n for a sequence skips it
- * (KDA_DEV_BAD_META).  Of a skipped sequence, and of rows that no sequence owns, q_out stays as it
- * was.  One launch. */
+ * (KDA_DEV_BAD_META).  One launch. */
 int kda_kv_append(const kda_pool *pool, int32_t Hq, int32_t Hkv, int32_t d, int32_t dtype, int32_t fmt,
                   int32_t page_tokens, int32_t nseq, int64_t T_tot, int32_t max_q, const int32_t *cu_q,
                   const int32_t *kv_len, const int32_t *page_table, int32_t max_pages, const void *q,
