@@ -47,10 +47,12 @@ __device__ __forceinline__ uint8_t *obj_addr(const PoolView &pv, const int32_t *
 }
 
 // Base address of a run of accesses at off0 .. off0 + span of one object when the run is
-// contiguous in the pool (one page, or physically adjacent pages), so that every access in it
-// is base + (off - off0); nullptr otherwise (the caller then translates each access).
+// contiguous in the pool (one page, or two physically adjacent ones), so that every access in it
+// is base + (off - off0); nullptr otherwise (the caller then translates each access).  A run that
+// pages lie between the ends of counts as not contiguous: the two ends say nothing of those.
 __device__ __forceinline__ uint8_t *run_addr(const PoolView &pv, const int32_t *pages, uint64_t off0,
                                              uint64_t span, int32_t *status) {
+    if (span >= (uint64_t)pv.page_bytes) return nullptr;
     uint8_t *a = obj_addr(pv, pages, off0, status), *b = obj_addr(pv, pages, off0 + span, status);
     return (a && b && b - a == (int64_t)span) ? a : nullptr;
 }
