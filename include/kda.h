@@ -517,6 +517,115 @@ int kda_attn_paged(const kda_pool *pool, int32_t Hq, int32_t Hkv, int32_t d, int
                    int64_t q_stride, float scale, int32_t window, int32_t sinks, void *o, float *lse,
                    const void *pool_base, void *workspace, int64_t ws_bytes, int32_t *status_dev, void *stream);
 
+/* ---------------------------------------------------------------- trees of drafts ----- */
+
+/* Speculation with a tree of drafts: a draft model offers several continuations that share their
+ * beginnings, one pass answers for all of them, and one branch is kept.  A sequence's n <= KDA_TREE_MAX
+ * drafts are its n new tokens of the call, in the calls' packed rows (cu_q, kv_len and max_q as for the
+ * key/value cache); draft i's parent is an earlier draft, parent[cu_q[s] + i] in [0, i), or -1: it then
+ * follows the sequence's last accepted token.  One round of a hybrid model:
+ *     kda_tree_plan            masks and positions, once for all layers
+ *     kda_kv_append_at, kda_attn_tree       each layer with a cache
+ *     kda_verify_tree          each recurrent layer
+ *     (the caller compares the model's answers with the drafts and finds the accepted branch)
+ *     kda_kv_accept            each layer with a cache
+ *     kda_verify_tree_accept   each recurrent layer
+ * The accepted branch: path[cu_q[s] + i], i < accepted[s], the drafts kept, from the tree's root on and so
+ * ascending; 0 <= accepted[s] <= n.  Trees, branches and lengths stay on the device: a round can be captured
+ * in a graph and replayed on others of at most max_q drafts.  A sequence whose metadata is out of range (a
+ * parent at or behind its draft or below -1, a path that does not ascend or leaves the tree, a length below n,
+ * n > max_q) sets KDA_DEV_BAD_META and is skipped; what it owns stays as it was.  max_q is at most
+ * KDA_TREE_MAX (KDA_EINVAL). */
+#define KDA_TREE_MAX 64
+
+/* Masks and positions of the drafts: bit j of mask[t] (device uint64 [T_tot]) says that the draft of packed
+ * row t is draft j or descends from it; pos[t] (device int32 [T_tot]) is kv_len - n + its depth, the tree's
+ * roots having depth 0.  One launch. */
+int kda_tree_plan(int32_t nseq, int64_t T_tot, int32_t max_q, const int32_t *cu_q, const int32_t *kv_len,
+                  const int32_t *parent, uint64_t *mask, int32_t *pos, int32_t *status_dev, void *stream);
+
+/* kda_kv_append for tokens whose position is not their place in the cache: the drafts of a tree, or tokens
+ * of pictures and video with coordinates on several axes (time, height, width).  Also for more than
+ * KDA_TREE_MAX new tokens.
+ *   pos           device int32 [T_tot][axes]: each token's coordinates, in [0, max_pos)
+ *   axes          1 to KDA_MAX_AXES
+ *   sections      host int32 [axes]: of a head's rot_dim / 2 angles the first sections[0] go by a token's
+ *                 first coordinate, the next sections[1] by its second, and so on; positive multiples of 8
+ *                 whose sum is rot_dim / 2
+ *   cos_sin       as there, not NULL; row p serves coordinate p of any axis
+ * A coordinate outside [0, max_pos) sets KDA_DEV_BAD_META; the block that would hold the token is then
+ * skipped, keys and values, and that token's query.  Everything else is as kda_kv_append has it. */
+#define KDA_MAX_AXES 4
+int kda_kv_append_at(const kda_pool *pool, int32_t Hq, int32_t Hkv, int32_t d, int32_t dtype, int32_t fmt,
+                     int32_t page_tokens, int32_t nseq, int64_t T_tot, int32_t max_q, const int32_t *cu_q,
+                     const int32_t *kv_len, const int32_t *page_table, int32_t max_pages, const void *q,
+                     int64_t q_stride, const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                     const float *cos_sin, int32_t max_pos, int32_t rot_dim, int32_t interleaved, const int32_t *pos,
+                     int32_t axes, const int32_t *sections, void *q_out, void *pool_base, int32_t *status_dev,
+                     void *stream);
+
+/* Attention of a tree's drafts over the cache, their own keys and values in it: kda_attn_paged with another
+ * rule of who sees what.  With base = kv_len - n, draft i sees
+ *     the cached tokens j < base with window == 0 or j > pos[i] - window or j < sinks
+ *     the drafts j whose bit of mask[i] is set, whatever the window
+ *   mask          device uint64 [T_tot], as kda_tree_plan writes it; any other will do (bits from n on count
+ *                 for nothing, a draft need not see itself)
+ *   pos           device int32 [T_tot]; read with a window only (NULL without one).  A position before base
+ *                 or behind the last draft's place counts as that
+ * Sequences with kv_len < n are skipped (KDA_DEV_BAD_META); a draft that sees nothing gets o = 0 and
+ * lse = -infinity; one that sees an infinite value gets an infinity or NaN in that
+ * column, and one that sees an infinite key may get NaN.  Workspace, types,
+ * roundings, unseen infinities and NaN, and the same bits for the same call: as kda_attn_paged has them. */
+int64_t kda_attn_tree_workspace_bytes(int32_t Hq, int32_t Hkv, int32_t d, int32_t dtype, int32_t nseq, int64_t T_tot,
+                                      int32_t max_q);
+int kda_attn_tree(const kda_pool *pool, int32_t Hq, int32_t Hkv, int32_t d, int32_t dtype, int32_t fmt,
+                  int32_t page_tokens, int32_t nseq, int64_t T_tot, int32_t max_q, const int32_t *cu_q,
+                  const int32_t *kv_len, const int32_t *page_table, int32_t max_pages, const uint64_t *mask,
+                  const int32_t *pos, const void *q, int64_t q_stride, float scale, int32_t window, int32_t sinks,
+                  void *o, float *lse, const void *pool_base, void *workspace, int64_t ws_bytes, int32_t *status_dev,
+                  void *stream);
+
+/* Keep the accepted branch in the cache: the keys and values of token base + path[i] move to place base + i
+ * (base = kv_len - n, i < accepted), and kv_len_out (device int32 [nseq], apart from kv_len) receives base +
+ * accepted.  What stands behind it afterwards is left over and counts for nothing.  Rows of the 16-bit cache
+ * move as they are.  KDA_KV_I8: a block that takes in tokens of another block sets scale = max(max |x| / 127 over
+ * those, the block's scale if a token stays in it: an older one, or an accepted one that it held already) and
+ * codes as kda_kv_append does, x = code * scale in fp32; without such tokens its scale and codes stay.  The pages
+ * that hold the drafts must be private to their sequence.  A page id outside the pool among the blocks that rows
+ * move from or to (and those between) sets KDA_DEV_BAD_PAGE, and the sequence is skipped.  One launch. */
+int kda_kv_accept(const kda_pool *pool, int32_t Hkv, int32_t d, int32_t fmt, int32_t page_tokens, int32_t nseq,
+                  int64_t T_tot, int32_t max_q, const int32_t *cu_q, const int32_t *kv_len, const int32_t *page_table,
+                  int32_t max_pages, const int32_t *path, const int32_t *accepted, int32_t *kv_len_out,
+                  void *pool_base, int32_t *status_dev, void *stream);
+
+/* Verify a tree against recurrent states: o[t] is what kda_decode_step would answer for draft t after the
+ * drafts of its branch, starting from the request's state; convolution windows follow the branches too.  The
+ * state is read once and nothing but o is written: the state after draft t is
+ *     S_t = Diag(A_t) S_0 + sum over the branch of (r(t, i) k_i) u_i^T,
+ *     u_t = beta_t (v_t - S_0^T (A_t k_t) - sum over the branch before t of <k_t, r(t, i) k_i> u_i)
+ * with A_t the product of alpha over the branch and r(t, i) over the part behind i, and o_t = S_t^T q_t needs the
+ * products with S_0, the inner products and the u alone.  Any alpha in [0, 1] will do, 0 included.
+ *   q, k, v, alpha   device [T_tot][H][d] dtype, contiguous, 16-byte aligned; beta [T_tot][H]
+ *   cu_q             device int32 [B + 1]; a request may have no drafts
+ *   parent           device int32 [T_tot]
+ *   state_pages      device int32 [B * P], P = kda_object_pages(): read only
+ * Sums and the products' operands are fp32 for KDA_F32.  KDA_BF16: see kda_verify_tree_accept for the state, which
+ * keeps fp32; an answer's products with S_0 take either operand in two bf16 terms (16 bits), far below o's own
+ * rounding.  A page id outside the pool sets KDA_DEV_BAD_PAGE and the request is skipped.  One launch. */
+int kda_verify_tree(const kda_pool *pool, int32_t H, int32_t d, int32_t dtype, int32_t B, int64_t T_tot, int32_t max_q,
+                    const int32_t *cu_q, const int32_t *parent, const void *q, const void *k, const void *v,
+                    const void *alpha, const void *beta, const float *conv_w, void *o, const void *pool_base,
+                    const int32_t *state_pages, int32_t *status_dev, void *stream);
+
+/* Advance each request's state and convolution window over its accepted branch, in place (decode steps without the
+ * answers, the state read and written once; fp32 throughout).  The arguments are those of kda_verify_tree, the same
+ * tokens among them.  A request that accepts nothing is left as it is.  One launch. */
+int kda_verify_tree_accept(const kda_pool *pool, int32_t H, int32_t d, int32_t dtype, int32_t B, int64_t T_tot,
+                           int32_t max_q, const int32_t *cu_q, const int32_t *path, const int32_t *accepted,
+                           const void *q, const void *k, const void *v, const void *alpha, const void *beta,
+                           const float *conv_w, void *pool_base, const int32_t *state_pages, int32_t *status_dev,
+                           void *stream);
+
 /* ---------------------------------------------------------------- status -------------- */
 
 /* Wait for `stream`, read and clear *status_dev.  Returns KDA_OK, KDA_EDEVICE (bits in

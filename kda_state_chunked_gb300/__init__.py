@@ -26,6 +26,7 @@ KDA_OK, KDA_EINVAL, KDA_ENOPAGES, KDA_EREF, KDA_ECUDA, KDA_EDEVICE = 0, -1, -2, 
 KDA_F32, KDA_BF16 = 0, 1
 KDA_DEV_BAD_PAGE, KDA_DEV_BAD_META, KDA_DEV_TIMEOUT, KDA_DEV_RANGE = 1, 2, 4, 8
 KDA_KV_BF16, KDA_KV_I8 = 0, 1
+KDA_TREE_MAX, KDA_MAX_AXES = 64, 4
 DTYPES = {"f32": KDA_F32, "bf16": KDA_BF16}
 
 # Every symbol include/kda.h declares, with (restype, argtypes).
@@ -83,6 +84,18 @@ _SIGS = {
     "kda_attn_workspace_bytes": (_I64, [_I32, _I32, _I32, _I32, _I32, _I64, _I32]),
     "kda_attn_paged": (ctypes.c_int, [_P, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _I64, _I32, _P, _P, _P, _I32, _P,
                                       _I64, ctypes.c_float, _I32, _I32, _P, _P, _P, _P, _I64, _P, _P]),
+    "kda_tree_plan": (ctypes.c_int, [_I32, _I64, _I32, _P, _P, _P, _P, _P, _P, _P]),
+    "kda_kv_append_at": (ctypes.c_int, [_P, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _I64, _I32, _P, _P, _P, _I32, _P,
+                                        _I64, _P, _I64, _P, _I64, _P, _I32, _I32, _I32, _P, _I32, _P, _P, _P, _P, _P]),
+    "kda_attn_tree_workspace_bytes": (_I64, [_I32, _I32, _I32, _I32, _I32, _I64, _I32]),
+    "kda_attn_tree": (ctypes.c_int, [_P, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _I64, _I32, _P, _P, _P, _I32, _P, _P,
+                                     _P, _I64, ctypes.c_float, _I32, _I32, _P, _P, _P, _P, _I64, _P, _P]),
+    "kda_kv_accept": (ctypes.c_int, [_P, _I32, _I32, _I32, _I32, _I32, _I64, _I32, _P, _P, _P, _I32, _P, _P, _P, _P, _P,
+                                     _P]),
+    "kda_verify_tree": (ctypes.c_int, [_P, _I32, _I32, _I32, _I32, _I64, _I32, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
+                                       _P, _P]),
+    "kda_verify_tree_accept": (ctypes.c_int, [_P, _I32, _I32, _I32, _I32, _I64, _I32, _P, _P, _P, _P, _P, _P, _P, _P, _P,
+                                              _P, _P, _P, _P]),
     "kda_sync_status": (ctypes.c_int, [_P, _P, _P]),
     "kda_status_string": (ctypes.c_char_p, [ctypes.c_int]),
 }
@@ -588,11 +601,9 @@ def kda_kv_page_bytes(Hkv: int, d: int, fmt: int, page_tokens: int) -> int:
     return _check(lib().kda_kv_page_bytes(Hkv, d, fmt, page_tokens), "kda_kv_page_bytes")
 
 
-def kda_kv_append(pool: Pool, fmt: int, page_tokens: int, cu_q, kv_len, page_table, max_q: int, q, k, v, cos_sin,
-                  q_out, status, interleaved: bool = False, stream=None) -> None:
-    """k, v: [T, Hkv, d] and q: [T, Hq, d] (or None, with q_out None), token rows any stride
-    apart; cu_q, kv_len, page_table: int32 CUDA [nseq + 1], [nseq], [nseq, max_pages]; cos_sin:
-    fp32 CUDA [max_pos, rot_dim] or None; q_out: [T, Hq, d] contiguous."""
+def _append_call(name: str, pool: Pool, fmt: int, page_tokens: int, cu_q, kv_len, page_table, max_q: int, q, k, v, cos_sin,
+                 q_out, status, interleaved: bool, stream, at) -> None:
+    """at: what kda_kv_append_at has beside kda_kv_append's arguments (pos, axes, sections), checked."""
     T, Hkv, d = k.shape
     dtype, gpu = k.dtype, k.get_device()
     _f32(cos_sin, "cos_sin")
@@ -612,12 +623,21 @@ def kda_kv_append(pool: Pool, fmt: int, page_tokens: int, cu_q, kv_len, page_tab
     pos, rot = 0, 0
     if cos_sin is not None:
         pos, rot = cos_sin.shape
-    rc = (_lib or lib()).kda_kv_append(
+    rc = getattr(_lib or lib(), name)(
         pool.handle, Hq, Hkv, d, dtype_of(k), fmt, page_tokens, nseq, T, max_q, cu, lens, table, max_pages, qp, qs, kp,
-        ks, vp, vs, _address(cos_sin, gpu), pos, rot, bool(interleaved), _address(q_out, gpu),
+        ks, vp, vs, _address(cos_sin, gpu), pos, rot, bool(interleaved), *at, _address(q_out, gpu),
         _address(pool.base, gpu), word, _raw_stream(gpu, stream))
     if rc < 0:
-        raise KdaError(rc, "kda_kv_append")
+        raise KdaError(rc, name)
+
+
+def kda_kv_append(pool: Pool, fmt: int, page_tokens: int, cu_q, kv_len, page_table, max_q: int, q, k, v, cos_sin,
+                  q_out, status, interleaved: bool = False, stream=None) -> None:
+    """k, v: [T, Hkv, d] and q: [T, Hq, d] (or None, with q_out None), token rows any stride
+    apart; cu_q, kv_len, page_table: int32 CUDA [nseq + 1], [nseq], [nseq, max_pages]; cos_sin:
+    fp32 CUDA [max_pos, rot_dim] or None; q_out: [T, Hq, d] contiguous."""
+    _append_call("kda_kv_append", pool, fmt, page_tokens, cu_q, kv_len, page_table, max_q, q, k, v, cos_sin, q_out, status,
+                 interleaved, stream, ())
 
 
 def kda_kv_gather(pool: Pool, fmt: int, page_tokens: int, cu_out, begin, page_table, k_out, v_out, status,
@@ -669,6 +689,154 @@ def kda_attn_paged(pool: Pool, Hkv: int, fmt: int, page_tokens: int, cu_q, kv_le
         _raw_stream(gpu, stream))
     if rc < 0:
         raise KdaError(rc, "kda_attn_paged")
+
+
+# ------------------------------------------------------------------------------ trees of drafts
+def _ints(t, n: int, gpu: int, what: str):
+    """Device address of an int32 tensor of n elements."""
+    import torch
+    if t.dtype != torch.int32 or t.numel() != n:
+        raise ValueError(f"{what} must be int32 with {n} elements")
+    return _address(t, gpu)
+
+
+def kda_tree_plan(cu_q, kv_len, parent, max_q: int, mask, pos, status, stream=None) -> None:
+    """parent: int32 CUDA [T]; mask: int64 CUDA [T] (the bits of a uint64) and pos: int32 CUDA [T]
+    are written."""
+    import torch
+    T, gpu, nseq = parent.numel(), parent.get_device(), kv_len.numel()
+    if mask.dtype != torch.int64 or mask.numel() != T:
+        raise ValueError("mask must be int64 [T]")
+    if gpu < 0:
+        raise ValueError("expected CUDA tensors")
+    rc = (_lib or lib()).kda_tree_plan(
+        nseq, T, max_q, _ints(cu_q, nseq + 1, gpu, "cu_q"), _ints(kv_len, nseq, gpu, "kv_len"),
+        _ints(parent, T, gpu, "parent"), _address(mask, gpu), _ints(pos, T, gpu, "pos"), _ints(status, 1, gpu, "status"),
+        _raw_stream(gpu, stream))
+    if rc < 0:
+        raise KdaError(rc, "kda_tree_plan")
+
+
+def kda_kv_append_at(pool: Pool, fmt: int, page_tokens: int, cu_q, kv_len, page_table, max_q: int, q, k, v, cos_sin, pos,
+                     sections, q_out, status, interleaved: bool = False, stream=None) -> None:
+    """kda_kv_append of tokens with positions of their own.  pos: int32 CUDA [T, axes] (or [T] for one
+    axis); sections: how many of the rot_dim / 2 angles go by each axis."""
+    if cos_sin is None:
+        raise ValueError("positions need cos_sin")
+    sec = _i32(sections)
+    at = _ints(pos, k.shape[0] * len(sec), k.get_device(), "pos"), len(sec), sec.ctypes.data
+    _append_call("kda_kv_append_at", pool, fmt, page_tokens, cu_q, kv_len, page_table, max_q, q, k, v, cos_sin, q_out,
+                 status, interleaved, stream, at)
+
+
+def kda_attn_tree_workspace_bytes(Hq: int, Hkv: int, d: int, dtype: int, nseq: int, T_tot: int, max_q: int) -> int:
+    return _check(lib().kda_attn_tree_workspace_bytes(Hq, Hkv, d, dtype, nseq, T_tot, max_q),
+                  "kda_attn_tree_workspace_bytes")
+
+
+def attn_tree_workspace(q, Hkv: int, nseq: int, max_q: int):
+    """A device byte tensor sized for kda_attn_tree on queries q [T, Hq, d]."""
+    import torch
+    T, Hq, d = q.shape
+    nb = kda_attn_tree_workspace_bytes(Hq, Hkv, d, dtype_of(q), nseq, T, max_q)
+    return torch.empty(nb, dtype=torch.uint8, device=q.device)
+
+
+def kda_attn_tree(pool: Pool, Hkv: int, fmt: int, page_tokens: int, cu_q, kv_len, page_table, max_q: int, mask, q, o,
+                  workspace, status, scale: float | None = None, window: int = 0, sinks: int = 0, pos=None, lse=None,
+                  stream=None) -> None:
+    """mask: int64 CUDA [T] as kda_tree_plan writes it; pos: int32 CUDA [T], needed with a window;
+    the rest as kda_attn_paged."""
+    import torch
+    T, Hq, d = q.shape
+    if o.shape != q.shape or o.dtype != q.dtype:
+        raise ValueError("q and o differ in shape or type")
+    _f32(lse, "lse")
+    if lse is not None and lse.numel() != T * Hq:
+        raise ValueError("lse must be [T, Hq]")
+    if mask.dtype != torch.int64 or mask.numel() != T:
+        raise ValueError("mask must be int64 [T]")
+    gpu = q.get_device()
+    nseq, max_pages, cu, lens, table, word = _batch(cu_q, kv_len, page_table, status, gpu)
+    qp, qs = _rows(q, Hq, d, gpu)
+    rc = (_lib or lib()).kda_attn_tree(
+        pool.handle, Hq, Hkv, d, dtype_of(q), fmt, page_tokens, nseq, T, max_q, cu, lens, table, max_pages,
+        _address(mask, gpu), None if pos is None else _ints(pos, T, gpu, "pos"), qp, qs, d ** -0.5 if scale is None else scale,
+        window, sinks, _address(o, gpu), _address(lse, gpu), _address(pool.base, gpu), _address(workspace, gpu),
+        workspace.numel() * workspace.element_size(), word, _raw_stream(gpu, stream))
+    if rc < 0:
+        raise KdaError(rc, "kda_attn_tree")
+
+
+def kda_kv_accept(pool: Pool, Hkv: int, d: int, fmt: int, page_tokens: int, cu_q, kv_len, page_table, max_q: int, path,
+                  accepted, kv_len_out, status, stream=None) -> None:
+    """path: int32 CUDA [T], the accepted drafts of each sequence first in its rows; accepted and
+    kv_len_out: int32 CUDA [nseq], the latter written."""
+    gpu = path.get_device()
+    nseq, max_pages, cu, lens, table, word = _batch(cu_q, kv_len, page_table, status, gpu)
+    rc = (_lib or lib()).kda_kv_accept(
+        pool.handle, Hkv, d, fmt, page_tokens, nseq, path.numel(), max_q, cu, lens, table, max_pages,
+        _ints(path, path.numel(), gpu, "path"), _ints(accepted, nseq, gpu, "accepted"),
+        _ints(kv_len_out, nseq, gpu, "kv_len_out"), _address(pool.base, gpu), word, _raw_stream(gpu, stream))
+    if rc < 0:
+        raise KdaError(rc, "kda_kv_accept")
+
+
+def _tree_tokens(cu_q, max_q: int, q, k, v, alpha, beta, conv_w, state_pages, status):
+    """(leading arguments, addresses of the tokens, the state's) of the two calls on states."""
+    import torch
+    T, H, d = q.shape
+    gpu, dt = q.get_device(), q.dtype
+    if gpu < 0:
+        raise ValueError("expected CUDA tensors")
+    for x in (k, v, alpha):
+        if x.shape != q.shape or x.dtype != dt:
+            raise ValueError("q, k, v and alpha differ in shape or type")
+    if beta.shape != (T, H) or beta.dtype != dt:
+        raise ValueError("beta must be [T, H] of the tokens' type")
+    _f32(conv_w, "conv_w")
+    if conv_w.shape != (H, 3 * d, 4):
+        raise ValueError("conv_w must be [H, 3 d, 4]")
+    B = cu_q.numel() - 1
+    if state_pages.dtype != torch.int32 or state_pages.dim() != 2 or state_pages.shape[0] != B:
+        raise ValueError("state_pages must be int32 [B, P]")
+    return ((H, d, dtype_of(q), B, T, max_q, _ints(cu_q, B + 1, gpu, "cu_q")),
+            (*(_address(x, gpu) for x in (q, k, v, alpha, beta)), _address(conv_w, gpu)),
+            (_address(state_pages, gpu), _ints(status, 1, gpu, "status")))
+
+
+def _state_width(pool: Pool, state_pages, shape) -> None:
+    if state_pages.shape[1] != kda_object_pages(pool, shape[0], shape[1], shape[2]):
+        raise ValueError("state_pages must be [B, kda_object_pages()]")
+
+
+def kda_verify_tree(pool: Pool, cu_q, parent, max_q: int, q, k, v, alpha, beta, conv_w, o, state_pages, status,
+                    stream=None) -> None:
+    """q, k, v, alpha, o: [T, H, d]; beta: [T, H]; cu_q, parent: int32 CUDA [B + 1], [T]; state_pages:
+    int32 CUDA [B, P], read only."""
+    head, tokens, state = _tree_tokens(cu_q, max_q, q, k, v, alpha, beta, conv_w, state_pages, status)
+    _state_width(pool, state_pages, head)
+    if o.shape != q.shape or o.dtype != q.dtype:
+        raise ValueError("q and o differ in shape or type")
+    gpu = q.get_device()
+    rc = (_lib or lib()).kda_verify_tree(pool.handle, *head, _ints(parent, q.shape[0], gpu, "parent"), *tokens,
+                                         _address(o, gpu), _address(pool.base, gpu), *state, _raw_stream(gpu, stream))
+    if rc < 0:
+        raise KdaError(rc, "kda_verify_tree")
+
+
+def kda_verify_tree_accept(pool: Pool, cu_q, path, accepted, max_q: int, q, k, v, alpha, beta, conv_w, state_pages, status,
+                           stream=None) -> None:
+    """The tokens of kda_verify_tree; path: int32 CUDA [T], accepted: int32 CUDA [B].  The objects of
+    state_pages advance in place."""
+    head, tokens, state = _tree_tokens(cu_q, max_q, q, k, v, alpha, beta, conv_w, state_pages, status)
+    _state_width(pool, state_pages, head)
+    gpu = q.get_device()
+    rc = (_lib or lib()).kda_verify_tree_accept(
+        pool.handle, *head, _ints(path, q.shape[0], gpu, "path"), _ints(accepted, head[3], gpu, "accepted"), *tokens,
+        _address(pool.base, gpu), *state, _raw_stream(gpu, stream))
+    if rc < 0:
+        raise KdaError(rc, "kda_verify_tree_accept")
 
 
 # ------------------------------------------------------------------------------ status

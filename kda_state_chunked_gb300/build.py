@@ -24,9 +24,10 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CU_SOURCES = ["kernels/ckpt_copy.cu", "kernels/ckpt_q8.cu", "kernels/decode.cu", "kernels/prefill_simt.cu",
               "kernels/prefill_tc.cu", "kernels/prefill_split.cu", "host/tensor_map.cu",
               "host/prefill_noalloc.cu", "kernels/kv_append.cu", "kernels/attn_decode.cu",
-              "kernels/attn_prefill.cu"]
+              "kernels/attn_prefill.cu", "kernels/attn_tree_decode.cu", "kernels/attn_tree_prefill.cu",
+              "kernels/kv_tree.cu", "kernels/verify_tree.cu"]
 SELFTEST_CU = ["selftest/tc_selftest.cu"]
-CPP_SOURCES = ["host/pool.cpp", "host/split_plan.cpp", "host/api.cpp", "host/kv.cpp"]
+CPP_SOURCES = ["host/pool.cpp", "host/split_plan.cpp", "host/api.cpp", "host/kv.cpp", "host/tree.cpp"]
 
 
 def _cuda_home() -> str:

@@ -167,6 +167,7 @@ struct KvView {
     int32_t *status;
 };
 constexpr int kKvMaxPageTokens = 128;
+constexpr int kTreeMost = KDA_TREE_MAX;   // drafts of a tree: a draft's mask is one 64-bit word
 
 struct KvAppendArgs {
     KvView kv;
@@ -178,6 +179,9 @@ struct KvAppendArgs {
     const float *cos_sin;         // [max_pos][rot_dim]: cosines, then sines; null for no rotation
     int32_t max_pos, rot_dim, interleaved;
     void *q_out;                  // [T_tot][Hq][d]
+    const int32_t *pos;           // null: a token's position is its place; else [T_tot][axes]
+    int32_t axes;
+    int32_t section_end[KDA_MAX_AXES];   // angles up to which an axis goes (multiples of 8)
 };
 
 struct KvGatherArgs {
@@ -186,6 +190,40 @@ struct KvGatherArgs {
     int64_t T_out, row0;          // rows; first one of this launch
     const int32_t *cu_out, *begin;
     void *k_out, *v_out;          // [T_out][Hkv][d]
+};
+
+// Parents of drafts to masks and positions.
+struct TreePlanArgs {
+    int32_t nseq, max_q;
+    int64_t T_tot;
+    const int32_t *cu_q, *kv_len, *parent;
+    uint64_t *mask;
+    int32_t *pos;
+    int32_t *status;
+};
+
+// The accepted branch of each sequence's drafts moves to the places right behind its context.
+struct KvAcceptArgs {
+    KvView kv;
+    int32_t nseq, max_q;
+    int64_t T_tot;
+    const int32_t *cu_q, *kv_len, *path, *accepted;
+    int32_t *kv_len_out;
+};
+
+// A tree of drafts against recurrent states.
+struct VerifyTreeArgs {
+    int32_t H, d, dtype, B, max_q;
+    int64_t T_tot;
+    const int32_t *cu_q, *parent;        // parent: verify
+    const int32_t *path, *accepted;      // accept
+    const void *q, *k, *v, *alpha;       // [T_tot][H][d]
+    const void *beta;                    // [T_tot][H]
+    const float *conv_w;
+    void *o;                             // [T_tot][H][d], verify
+    PoolView pool;
+    const int32_t *state_pages;          // [B * P]
+    int32_t *status;
 };
 
 // Attention over a paged cache.  A row tile is a run of (token, head of the group) query rows of
@@ -215,6 +253,8 @@ struct AttnArgs {
     int64_t q_stride;
     float scale;
     int32_t window, sinks;
+    const uint64_t *mask;         // a tree's: [T_tot], what each draft sees of the drafts; null: causal
+    const int32_t *pos;           // a tree's, with a window: [T_tot] positions
     void *o;                      // [T_tot][Hq][d]
     float *lse;                   // [T_tot][Hq] or null
     int32_t ctas;                 // CTAs the units are shared out over
@@ -250,5 +290,11 @@ cudaError_t launch_kv_append(const KvAppendArgs &a, cudaStream_t s);
 cudaError_t launch_kv_gather(const KvGatherArgs &a, cudaStream_t s);
 cudaError_t launch_attn_decode(const AttnArgs &a, cudaStream_t s);
 cudaError_t launch_attn_prefill(const AttnArgs &a, cudaStream_t s);
+cudaError_t launch_attn_tree_decode(const AttnArgs &a, cudaStream_t s);    // the same two kernels for trees
+cudaError_t launch_attn_tree_prefill(const AttnArgs &a, cudaStream_t s);
+cudaError_t launch_tree_plan(const TreePlanArgs &a, cudaStream_t s);
+cudaError_t launch_kv_accept(const KvAcceptArgs &a, cudaStream_t s);
+cudaError_t launch_verify_tree(const VerifyTreeArgs &a, cudaStream_t s);
+cudaError_t launch_verify_tree_accept(const VerifyTreeArgs &a, cudaStream_t s);
 
 }  // namespace kda

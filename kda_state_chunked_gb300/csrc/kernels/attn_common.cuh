@@ -48,8 +48,13 @@ __device__ __forceinline__ Tile make_tile(const AttnArgs &a, int32_t s, const Kv
     t.row0 = rt * ROWS;
     t.nrows = min(ROWS, q.n * a.G - t.row0);
     const int32_t base = q.len - q.n;
-    t.pmin = base + token_of(a, t.row0);
-    t.pmax = base + token_of(a, t.row0 + t.nrows - 1);
+    if (a.mask) {                 // a tree's rows see what is before its drafts, and drafts by their own masks
+        t.pmin = base - 1;
+        t.pmax = base + q.n - 1;
+    } else {
+        t.pmin = base + token_of(a, t.row0);
+        t.pmax = base + token_of(a, t.row0 + t.nrows - 1);
+    }
     t.first = t.sinks = 0;
     if (t.pmax < 0) {             // more new tokens than the cache holds: these rows see nothing
         t.units = 1;
@@ -73,6 +78,23 @@ __device__ __forceinline__ int32_t unit_token(const Tile &t, int32_t u) {
 __device__ __forceinline__ bool sees(const AttnArgs &a, int32_t p, int32_t j) {
     return j <= p && (a.window <= 0 || j > p - a.window || j < a.sinks);
 }
+// A draft of a tree: what it sees of the drafts, and its position (between the first draft's place and the last's).
+struct Draft {
+    uint64_t mask;
+    int32_t pos;
+};
+__device__ __forceinline__ Draft draft_of(const AttnArgs &a, int32_t tok0, int32_t n, int32_t base, int32_t tok) {
+    Draft r;
+    r.mask = __ldg(a.mask + tok0 + tok) & (~0ull >> (kTreeMost - n));   // (1 <= n <= kTreeMost)
+    r.pos = a.window > 0 ? min(max(__ldg(a.pos + tok0 + tok), base), base + n - 1) : base;
+    return r;
+}
+// Whether it sees token j, base being the first draft's place.
+__device__ __forceinline__ bool draft_sees(const AttnArgs &a, const Draft &r, int32_t base, int32_t j) {
+    if (j < base) return a.window <= 0 || j > r.pos - a.window || j < a.sinks;
+    return j - base < kTreeMost && (r.mask >> (j - base) & 1u);
+}
+
 // Whether any / every row of the tile sees some / all of tokens [t0, t0 + n).
 __device__ __forceinline__ bool any_sees(const AttnArgs &a, const Tile &t, int32_t t0, int32_t n) {
     return t0 <= t.pmax && (a.window <= 0 || t0 + n - 1 > t.pmin - a.window || t0 < a.sinks);
@@ -148,7 +170,12 @@ struct Walk {
 };
 
 __device__ __forceinline__ KvSeq seq_of(const AttnArgs &a, int s) {
-    return kv_seq(a.cu_q, a.kv_len, s, a.T_tot, a.max_q, a.kv);
+    const KvSeq q = kv_seq(a.cu_q, a.kv_len, s, a.T_tot, a.max_q, a.kv);
+    if (a.mask && q.len < q.n) {  // drafts without a place
+        flag_status(a.kv.status, KDA_DEV_BAD_META);
+        return {0, 0, 0};
+    }
+    return q;
 }
 
 template <int ROWS, int UNIT>

@@ -42,6 +42,13 @@ namespace {
 
 using namespace attn;
 
+// Trees of drafts are this kernel compiled again (attn_tree_decode.cu), with masks in the place of the causal rule.
+#ifdef KDA_ATTN_TREE
+constexpr bool kTree = true;
+#else
+constexpr bool kTree = false;
+#endif
+
 constexpr int kWarps = 4;                             // that compute; one more walks and copies
 constexpr float kPBits = 6.f;                         // bits that a probability is scaled up in fp16
 constexpr float kGrow = 8.f;                          // bits that a row's maximum may grow before O is rescaled
@@ -72,7 +79,8 @@ struct Smem {
     static constexpr int o_ml = o_acc + kWarps * 4 * D * 4;             // [2][kWarps][16][2] fp32
     static constexpr int o_q = o_ml + 2 * kWarps * 16 * 8;               // fragments of the queries
     static constexpr int o_qs = o_q + NT * NR * (D / 16) * 256;          // [16] row factors
-    static constexpr int o_job = o_qs + 64;
+    static constexpr int o_drafts = o_qs + 64;                           // trees: [16] what each row sees
+    static constexpr int o_job = o_drafts + (kTree ? 16 * (int)sizeof(Draft) : 0);
     static constexpr int o_bar = o_job + Shape<FMT, D>::stages * (int)sizeof(Job);   // full, empty
     static constexpr int o_err = o_bar + 2 * Shape<FMT, D>::stages * 8;
     static constexpr int total(int stages) { return stages * Shape<FMT, D>::stage + o_err + 64; }
@@ -372,6 +380,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
     float *acc = reinterpret_cast<float *>(sm + M::o_acc);
     uint32_t *qfrag = reinterpret_cast<uint32_t *>(sm + M::o_q);
     float *qs = reinterpret_cast<float *>(sm + M::o_qs);
+    Draft *drafts = reinterpret_cast<Draft *>(sm + M::o_drafts);
     // The four warps meet; false where one has left, or is about to.  A warp that leaves sets the error
     // first and then arrives once more: the others, each at this meeting or on its way there, get through
     // it and find the error, so that no barrier holds anyone for good.
@@ -452,6 +461,8 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
                 f *= __uint_as_float((uint32_t)(127 - shift) << 23);
             }
             if (tid % 8 == 0) qs[row] = f;
+            if (kTree && tid % 8 == 1)
+                drafts[row] = row < nrows ? draft_of(a, tok0, jb.pmax + 1 - jb.base, jb.base, token_of(a, at)) : Draft{0, jb.base};
 #pragma unroll
             for (int i = 0; i < kCols; i += 2) {
                 const int c = (c0 + i) % 16, k = (c0 + i) / 16;
@@ -479,7 +490,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
                 for (int r = 0; r < 2; ++r) {
                     const int row = 8 * x + 2 * t + r;
                     rs[x][r] = qs[row];
-                    pos[x][r] = row < nrows ? jb.base + token_of(a, row0 + row) : -1;
+                    pos[x][r] = row < nrows ? (kTree ? 0 : jb.base) + token_of(a, row0 + row) : -1;   // trees: the draft
                     m[x][r] = big[x][r] = -INFINITY, l[x][r] = 0.f;
                 }
 #pragma unroll
@@ -554,8 +565,11 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
 #pragma unroll
                     for (int x = 0; x < NR; ++x)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (!(there >> y & 1u) || !sees(a, pos[x][e & 1], j0 + 16 * y + g + 8 * (e >> 1))) c[y][x][e] = -INFINITY;
+                        for (int e = 0; e < 4; ++e) {
+                            const int j = j0 + 16 * y + g + 8 * (e >> 1);
+                            const bool see = kTree ? draft_sees(a, drafts[8 * x + 2 * t + (e & 1)], jb.base, j) : sees(a, pos[x][e & 1], j);
+                            if (!(there >> y & 1u) || !see) c[y][x][e] = -INFINITY;
+                        }
             // m lags: it only follows a row's maximum when that has grown by more than 2^8.  So does big, which
             // is the same for the scores with log2 of the value scales added: what enters the product stays in
             // fp16's range by what the row itself sees, whatever scales its other blocks have.  Either is a whole
@@ -703,12 +717,15 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 2) attn_decode_kernel(const
                 // one product for each query token, without the tokens it does not see, of which only
                 // that token's rows are kept
 #pragma unroll 1
-                for (int32_t q = jb.pmin; q <= jb.pmax; ++q) {
+                for (int32_t q = kTree ? token_of(a, row0) : jb.pmin; q <= (kTree ? token_of(a, row0 + nrows - 1) : jb.pmax); ++q) {
                     uint32_t keep[2];
+                    Draft dr{};
+                    if (kTree) dr = draft_of(a, tok0, jb.pmax + 1 - jb.base, jb.base, q);
+                    auto sees_it = [&](int32_t j) { return kTree ? draft_sees(a, dr, jb.base, j) : sees(a, q, j); };
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const int j = j0 + 8 * i + 2 * t;
-                        keep[i] = (sees(a, q, j) ? 0xFFFFu : 0u) | (sees(a, q, j + 1) ? 0xFFFF0000u : 0u);
+                        keep[i] = (sees_it(j) ? 0xFFFFu : 0u) | (sees_it(j + 1) ? 0xFFFF0000u : 0u);
                     }
 #pragma unroll
                     for (int i = 0; i < kDt; ++i) {
@@ -875,7 +892,11 @@ cudaError_t run(const AttnArgs &a, cudaStream_t st) {
 
 }  // namespace
 
+#ifdef KDA_ATTN_TREE
+cudaError_t launch_attn_tree_decode(const AttnArgs &a, cudaStream_t s) {
+#else
 cudaError_t launch_attn_decode(const AttnArgs &a, cudaStream_t s) {
+#endif
     const bool i8 = a.kv.fmt == KDA_KV_I8, f32 = a.dtype == KDA_F32;
     if (a.kv.d == 128) {
         if (i8) return f32 ? run<KDA_KV_I8, 128, 3>(a, s) : run<KDA_KV_I8, 128, 1>(a, s);

@@ -52,6 +52,13 @@ namespace {
 
 using namespace attn;
 
+// Trees of drafts are this kernel compiled again (attn_tree_prefill.cu), with masks in the place of the causal rule.
+#ifdef KDA_ATTN_TREE
+constexpr bool kTree = true;
+#else
+constexpr bool kTree = false;
+#endif
+
 constexpr int kRows = kAttnPrefillRows, kHalf = 128, kUnit = 128;
 constexpr int kSoftWarps = 16, kLoadWarps = 8, kMmaWarp = 24, kCopyWarp = 25, kWalkWarp = 26, kThreads = 28 * 32;
 constexpr float kGrow = 8.f;            // bits that a row's maximum may grow before O is rescaled
@@ -332,8 +339,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
             if (flags & kBegin) {
                 in = row < nrows;
                 pos = in ? jb.base + token_of(a, at) : -1;
-                p_lo = __reduce_min_sync(0xFFFFFFFFu, in ? pos : INT32_MAX);
-                p_hi = __reduce_max_sync(0xFFFFFFFFu, pos);
+                if (kTree) {
+                    p_lo = jb.pmin, p_hi = jb.pmax;
+                } else {
+                    p_lo = __reduce_min_sync(0xFFFFFFFFu, in ? pos : INT32_MAX);
+                    p_hi = __reduce_max_sync(0xFFFFFFFFu, pos);
+                }
                 m = big = -INFINITY, l = 0.f;
                 float z[16];
 #pragma unroll
@@ -351,6 +362,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
             auto seen = [&](int c) -> uint32_t {
                 auto low = [](int32_t k) -> uint32_t { return k <= 0 ? 0u : k >= 16 ? 0xFFFFu : (1u << k) - 1u; };
                 const int32_t b = j0 + 64 * side + 16 * c;
+                if (kTree) {
+                    if (!in) return 0;
+                    const Draft r = draft_of(a, jb.tok0, jb.pmax + 1 - jb.base, jb.base, pos - jb.base);
+                    uint32_t x = low(jb.base - b);
+                    if (a.window > 0) x &= ~low(r.pos - a.window + 1 - b) | low(a.sinks - b);
+                    const int32_t first = b - jb.base;        // of the group's tokens, among the drafts
+                    if (first >= 0 && first < kTreeMost) x |= (uint32_t)(r.mask >> first) & 0xFFFFu;
+                    if (first < 0 && first > -16) x |= (uint32_t)(r.mask << -first) & 0xFFFFu;
+                    return x;
+                }
                 uint32_t x = low(pos + 1 - b);
                 if (a.window > 0) x &= ~low(pos - a.window + 1 - b) | low(a.sinks - b);
                 return x;
@@ -448,7 +469,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                         for (int j = 0; j < kUnit; ++j) {
                             if (!(bad[(n & 1) * 4 + (j >> 5)] >> (j & 31) & 1u)) continue;   // the same for all rows
                             const float x = tmem_ld1(tS - side * 64 + j);
-                            if (sees(a, pos, j0 + j)) {
+                            const bool see = kTree ? in && draft_sees(a, draft_of(a, jb.tok0, jb.pmax + 1 - jb.base, jb.base, pos - jb.base), jb.base, j0 + j)
+                                                   : sees(a, pos, j0 + j);
+                            if (see) {
                                 const float pj = ex2(x * f_row - ms);
                                 const uint8_t *line = a.kv.base + jb.rec[j >> 4] + pt * kRow;
 #pragma unroll
@@ -1012,7 +1035,11 @@ cudaError_t run(const AttnArgs &a, cudaStream_t st) {
 
 }  // namespace
 
+#ifdef KDA_ATTN_TREE
+cudaError_t launch_attn_tree_prefill(const AttnArgs &a, cudaStream_t s) {
+#else
 cudaError_t launch_attn_prefill(const AttnArgs &a, cudaStream_t s) {
+#endif
     if (a.kv.d == 128) return a.kv.fmt == KDA_KV_I8 ? run<KDA_KV_I8, 128>(a, s) : run<KDA_KV_BF16, 128>(a, s);
     return a.kv.fmt == KDA_KV_I8 ? run<KDA_KV_I8, 64>(a, s) : run<KDA_KV_BF16, 64>(a, s);
 }

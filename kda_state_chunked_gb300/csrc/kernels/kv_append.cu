@@ -87,30 +87,31 @@ __device__ __forceinline__ void rotate(float (&x)[16], const float *cs, int c, i
     }
 }
 
-__device__ __forceinline__ int8_t code_of(float x, float s) {
-    const int c = __float2int_rn(__fdiv_rn(x, s));
-    return (int8_t)max(-127, min(127, c));
-}
-// Eight codes of values x at scale s; all zero where the scale is (nothing but zeros, or so small
-// that a 127th of it is not a number of its own).
-__device__ __forceinline__ uint2 codes8(const float *x, float s) {
-    uint32_t w[2] = {0, 0};
-    if (s != 0.f)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i >> 2] |= (uint32_t)(uint8_t)code_of(x[i], s) << (8 * (i & 3));
-    return make_uint2(w[0], w[1]);
-}
-
 constexpr int kMaxToks = 128;   // tokens of a CTA that rotates queries
 
 // A sequence with no place, or no angle, for some of its new tokens: all of it is skipped, queries too.
+// (AT: tokens with positions of their own, kda_kv_append_at; those are looked at one by one.)
+template <bool AT>
 __device__ __forceinline__ bool no_place(const KvAppendArgs &a, const KvSeq &q) {
-    return q.len < q.n || (a.rot_dim > 0 && q.len > a.max_pos);
+    return q.len < q.n || (!AT && a.rot_dim > 0 && q.len > a.max_pos);
+}
+
+// AT: whether a packed token has a coordinate without an angle, and the coordinate by which thread c's
+// angles (8 c and up) go.
+__device__ __forceinline__ bool no_angle(const KvAppendArgs &a, int64_t tok) {
+    bool bad = false;
+    for (int i = 0; i < a.axes; ++i) bad |= (uint32_t)__ldg(a.pos + tok * a.axes + i) >= (uint32_t)a.max_pos;
+    return bad;
+}
+__device__ __forceinline__ int axis_of(const KvAppendArgs &a, int c) {
+    int axis = 0;
+    while (axis + 1 < a.axes && 8 * c >= a.section_end[axis]) ++axis;
+    return axis;
 }
 
 // NT threads; ROWS: new rows of a block that one thread may hold.
-template <int FMT, int D, class TIN, int NT, int ROWS>
-__global__ void __launch_bounds__(NT) kv_append_kernel(KvAppendArgs a, int32_t q_ctas, int32_t q_toks, int64_t items) {
+template <int FMT, int D, class TIN, int NT, int ROWS, bool AT>
+__global__ void __launch_bounds__(NT) kv_append_kernel(const __grid_constant__ KvAppendArgs a, int32_t q_ctas, int32_t q_toks, int64_t items) {
     constexpr int kTpr = D / 16;          // threads a row
     constexpr int kRpp = NT / kTpr;       // rows a pass
     constexpr int kRow = kKvRow<FMT, D>;
@@ -130,7 +131,7 @@ __global__ void __launch_bounds__(NT) kv_append_kernel(KvAppendArgs a, int32_t q
             const KvSeq q = kv_seq(a.cu_q, a.kv_len, s, a.T_tot, a.max_q, a.kv);
             int64_t pos = (int64_t)q.len - q.n + (tok - q.tok0);
             if (tok < q.tok0 || tok >= (int64_t)q.tok0 + q.n) pos = -1;
-            else if (no_place(a, q)) {
+            else if (no_place<AT>(a, q) || (AT && no_angle(a, tok))) {
                 flag_status(a.kv.status, KDA_DEV_BAD_META);
                 pos = -1;
             }
@@ -144,11 +145,12 @@ __global__ void __launch_bounds__(NT) kv_append_kernel(KvAppendArgs a, int32_t q
             if (pos < 0) continue;
             const int h = (i % per_tok) / kTpr, c = i % kTpr;
             const Place p = place(c, rot, il);
+            const int64_t angle = AT && p.turned ? __ldg(a.pos + tok * a.axes + axis_of(a, c)) : pos;
             const TIN *src = static_cast<const TIN *>(a.q) + tok * a.q_stride + h * D;
             float x[16];
             load8(src + p.a, x);
             load8(src + p.b, x + 8);
-            if (p.turned) rotate(x, a.cos_sin + pos * rot, c, rot, il);
+            if (p.turned) rotate(x, a.cos_sin + angle * rot, c, rot, il);
             TIN *dst = static_cast<TIN *>(a.q_out) + (tok * a.Hq + h) * D;
             store8(dst + p.a, x);
             store8(dst + p.b, x + 8);
@@ -177,11 +179,11 @@ __global__ void __launch_bounds__(NT) kv_append_kernel(KvAppendArgs a, int32_t q
         q = kv_seq(a.cu_q, a.kv_len, s, a.T_tot, a.max_q, a.kv);
         if (q.n == 0 || item < start(s)) return;
         const int64_t b = (int64_t)((q.len - q.n) / pt) + (item - start(s));
-        if (b * pt >= q.len && !no_place(a, q)) return;
+        if (b * pt >= q.len && !no_place<AT>(a, q)) return;
         block = (int)b;
     }
     const int old = q.len - q.n;
-    if (no_place(a, q)) {
+    if (no_place<AT>(a, q)) {
         if (tid == 0) flag_status(a.kv.status, KDA_DEV_BAD_META);
         return;
     }
@@ -194,6 +196,9 @@ __global__ void __launch_bounds__(NT) kv_append_kernel(KvAppendArgs a, int32_t q
     const TIN *src = is_v ? static_cast<const TIN *>(a.v) : static_cast<const TIN *>(a.k);
     const int64_t stride = is_v ? a.v_stride : a.k_stride;
     float x[ROWS][16];
+    bool lost = false;   // AT: a token of the block that has no angle
+    if (AT)
+        for (int slot = lo + tid; slot < hi; slot += NT) lost |= no_angle(a, tok_of_slot0 + slot);
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
         const int slot = lo + i * kRpp + r0;
@@ -203,6 +208,10 @@ __global__ void __launch_bounds__(NT) kv_append_kernel(KvAppendArgs a, int32_t q
             load8(row + p.b, x[i] + 8);
         }
     }
+    if (AT && __syncthreads_or(lost)) {
+        if (tid == 0) flag_status(a.kv.status, KDA_DEV_BAD_META);
+        return;
+    }
     uint8_t *rec = kv_record(a.kv, page, head);
     if (!rec) return;
     uint8_t *tile = rec + (is_v ? pt * kRow : 0);
@@ -210,10 +219,13 @@ __global__ void __launch_bounds__(NT) kv_append_kernel(KvAppendArgs a, int32_t q
     uint32_t s_old = 0;
     if (FMT == KDA_KV_I8 && lo > 0) s_old = __float_as_uint(*scale_at) & 0x7FFFFFFFu;
     if (p.turned) {
+        const int axis = AT ? axis_of(a, c) : 0;
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) {
             const int slot = lo + i * kRpp + r0;
-            if (slot < hi) rotate(x[i], a.cos_sin + ((int64_t)block * pt + slot) * rot, c, rot, il);
+            if (slot >= hi) continue;
+            const int64_t angle = AT ? __ldg(a.pos + (tok_of_slot0 + slot) * a.axes + axis) : (int64_t)block * pt + slot;
+            rotate(x[i], a.cos_sin + angle * rot, c, rot, il);
         }
     }
     if constexpr (FMT == KDA_KV_BF16) {
@@ -344,7 +356,7 @@ __global__ void __launch_bounds__(256) kv_gather_kernel(KvGatherArgs a) {
     }
 }
 
-template <int FMT, int D, class TIN, int NT, int ROWS>
+template <int FMT, int D, class TIN, int NT, int ROWS, bool AT>
 cudaError_t append(const KvAppendArgs &a, cudaStream_t st) {
     // about four pairs of eights a thread for the queries' CTAs
     const int32_t q_toks = a.q ? min(kMaxToks, max(1, 4 * NT / (a.Hq * (D / 16)))) : 1;
@@ -352,7 +364,7 @@ cudaError_t append(const KvAppendArgs &a, cudaStream_t st) {
     const int64_t items = a.max_q == 1 ? a.T_tot : a.T_tot / a.kv.page_tokens + 2 * (int64_t)a.nseq;
     const int64_t grid = q_ctas + 2 * items * a.kv.Hkv;
     if (grid > INT32_MAX) return cudaErrorInvalidValue;
-    kv_append_kernel<FMT, D, TIN, NT, ROWS><<<(unsigned)grid, NT, 0, st>>>(a, (int32_t)q_ctas, q_toks, items);
+    kv_append_kernel<FMT, D, TIN, NT, ROWS, AT><<<(unsigned)grid, NT, 0, st>>>(a, (int32_t)q_ctas, q_toks, items);
     return cudaGetLastError();
 }
 
@@ -360,12 +372,24 @@ cudaError_t append(const KvAppendArgs &a, cudaStream_t st) {
 // them; a CTA of 256 holds a whole block of new rows, and one made for blocks of up to 64 tokens
 // needs half the registers of the largest, so that more of them have loads under way on an SM
 // (4 x 8192 tokens in 64-token blocks: 162 us, and 263 us with the largest's registers).
-template <int FMT, int D, class TIN>
+template <int FMT, int D, class TIN, bool AT>
 cudaError_t append_sized(const KvAppendArgs &a, cudaStream_t st) {
     constexpr int kMost = kKvMaxPageTokens * (D / 16) / 256;
-    if (a.max_q <= 8) return append<FMT, D, TIN, 64, 1>(a, st);
-    if (a.kv.page_tokens <= kKvMaxPageTokens / 2) return append<FMT, D, TIN, 256, kMost / 2>(a, st);
-    return append<FMT, D, TIN, 256, kMost>(a, st);
+    if (a.max_q <= 8) return append<FMT, D, TIN, 64, 1, AT>(a, st);
+    if (a.kv.page_tokens <= kKvMaxPageTokens / 2) return append<FMT, D, TIN, 256, kMost / 2, AT>(a, st);
+    return append<FMT, D, TIN, 256, kMost, AT>(a, st);
+}
+
+template <bool AT>
+cudaError_t append_kind(const KvAppendArgs &a, cudaStream_t s) {
+    using bf16 = __nv_bfloat16;
+    const bool i8 = a.kv.fmt == KDA_KV_I8, f32 = a.dtype == KDA_F32;
+    if (a.kv.d == 128) {
+        if (i8) return f32 ? append_sized<KDA_KV_I8, 128, float, AT>(a, s) : append_sized<KDA_KV_I8, 128, bf16, AT>(a, s);
+        return f32 ? append_sized<KDA_KV_BF16, 128, float, AT>(a, s) : append_sized<KDA_KV_BF16, 128, bf16, AT>(a, s);
+    }
+    if (i8) return f32 ? append_sized<KDA_KV_I8, 64, float, AT>(a, s) : append_sized<KDA_KV_I8, 64, bf16, AT>(a, s);
+    return f32 ? append_sized<KDA_KV_BF16, 64, float, AT>(a, s) : append_sized<KDA_KV_BF16, 64, bf16, AT>(a, s);
 }
 
 template <int FMT, int D>
@@ -384,13 +408,7 @@ cudaError_t gather(const KvGatherArgs &a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_kv_append(const KvAppendArgs &a, cudaStream_t s) {
-    const bool i8 = a.kv.fmt == KDA_KV_I8, f32 = a.dtype == KDA_F32;
-    if (a.kv.d == 128) {
-        if (i8) return f32 ? append_sized<KDA_KV_I8, 128, float>(a, s) : append_sized<KDA_KV_I8, 128, __nv_bfloat16>(a, s);
-        return f32 ? append_sized<KDA_KV_BF16, 128, float>(a, s) : append_sized<KDA_KV_BF16, 128, __nv_bfloat16>(a, s);
-    }
-    if (i8) return f32 ? append_sized<KDA_KV_I8, 64, float>(a, s) : append_sized<KDA_KV_I8, 64, __nv_bfloat16>(a, s);
-    return f32 ? append_sized<KDA_KV_BF16, 64, float>(a, s) : append_sized<KDA_KV_BF16, 64, __nv_bfloat16>(a, s);
+    return a.pos ? append_kind<true>(a, s) : append_kind<false>(a, s);
 }
 
 cudaError_t launch_kv_gather(const KvGatherArgs &a, cudaStream_t s) {

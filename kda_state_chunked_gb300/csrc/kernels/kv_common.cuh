@@ -46,6 +46,20 @@ __device__ __forceinline__ KvSeq kv_seq(const int32_t *cu, const int32_t *kv_len
     return {a, (int32_t)n, len};
 }
 
+__device__ __forceinline__ int8_t code_of(float x, float s) {
+    const int c = __float2int_rn(__fdiv_rn(x, s));
+    return (int8_t)max(-127, min(127, c));
+}
+// Eight codes of values x at scale s; all zero where the scale is (nothing but zeros, or so small
+// that a 127th of it is not a number of its own).
+__device__ __forceinline__ uint2 codes8(const float *x, float s) {
+    uint32_t w[2] = {0, 0};
+    if (s != 0.f)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i >> 2] |= (uint32_t)(uint8_t)code_of(x[i], s) << (8 * (i & 3));
+    return make_uint2(w[0], w[1]);
+}
+
 // The last s in [0, nseq) with start(s) <= x, for a start() that does not fall; 0 if there is none.
 // The whole warp calls it with one x: 32 places are looked at a time, so that 1,024 sequences take
 // two reads one behind the other and not ten.
