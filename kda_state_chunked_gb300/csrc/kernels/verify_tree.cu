@@ -15,6 +15,8 @@
 //   a warp a draft walks its branch towards the root: c_ti, e_ti, A_t k_t, A_t q_t;
 //   the products with S_0;  then a thread a column solves for u, and all add up o.
 #include "common.cuh"
+#include "sm100_ptx.cuh"
+#include "tc_common.cuh"
 
 namespace kda {
 namespace {
@@ -62,81 +64,118 @@ __device__ __forceinline__ const uint8_t *raw_at(const VerifyTreeArgs &a, const 
     return static_cast<const uint8_t *>(x) + ((row * a.H + h) * d + c) * es;
 }
 
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kUnit = 256;   // bytes of a record that lie in one page: pages and records are multiples of it
+
+// Shared memory for trees of up to N drafts (a multiple of 8), in bytes.
 template <int D>
 struct Lay {
-    // floats, n: drafts rounded up to a multiple of 8
-    static __host__ __device__ int64_t bytes(int n) {
-        return ((int64_t)5 * n * D + 2 * (int64_t)n * n + 8 * D) * 4 + kMost * (8 + 4 + 4);
+    int N, kb, al, xq, u, ck, cq, xy, part, unit, mask, beta, up, total;
+    __host__ __device__ explicit Lay(int n) {
+        int at = 0;
+        auto take = [&](int bytes) {
+            const int was = at;
+            at += (bytes + 15) / 16 * 16;
+            return was;
+        };
+        N = n;
+        kb = take(N * D * 4), al = take(N * D * 4), xq = take(N * D * 4), u = take(N * D * 4);   // u: v until solved
+        ck = take(N * (N + 1) / 2 * 4), cq = take(N * (N + 1) / 2 * 4);                          // row t: i <= t
+        xy = take(2 * N * (D + 8) * 4);        // [A k | A q] in two bf16 terms or in fp32, then their products with S_0
+        part = take((kThreads / D - 1) * 8 * D * 4);
+        unit = take(D * D * 4 / kUnit * 8);    // addresses of S_0
+        mask = take(N * 8), beta = take(N * 4), up = take(N * 4);
+        total = at;
     }
 };
 
-// Threads: two groups of D.
-template <int D, class T>
-__global__ void __launch_bounds__(2 * D) verify_tree_kernel(const __grid_constant__ VerifyTreeArgs a, int N) {
-    constexpr int NT = 2 * D, kWarps = NT / 32, V = kVec<T>;
-    extern __shared__ __align__(16) float sm[];
-    float *kb = sm, *xk = kb + N * D, *xq = xk + N * D, *al = xq + N * D, *u = al + N * D;   // u: v until solved
-    float *ck = u + N * D, *cq = ck + N * N, *part = cq + N * N;                            // part: [8][D]
-    uint64_t *mask = reinterpret_cast<uint64_t *>(part + 8 * D);
-    float *beta = reinterpret_cast<float *>(mask + kMost);
-    int32_t *up = reinterpret_cast<int32_t *>(beta + kMost);
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// x, y as packed bf16: the nearest ones, and those of what is left.
+__device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t &lo) {
+    hi = tcx::f2_to_bf2(x, y);
+    const float2 h = tcx::bf2_to_f2(hi);
+    lo = tcx::f2_to_bf2(x - h.x, y - h.y);
+}
+
+// MT: tiles of 16 rows of [A k | A q], of up to 8 MT drafts.
+template <int D, class T, int MT>
+__global__ void __launch_bounds__(kThreads, MT <= 2 ? 3 : MT == 4 ? 2 : 1) verify_tree_kernel(const __grid_constant__ VerifyTreeArgs a) {
+    constexpr int V = kVec<T>, N = 8 * MT, kPitch = D + 8;   // of a row in bf16: rows 16 bytes apart in their banks
+    constexpr bool kMma = sizeof(T) == 2;
+    extern __shared__ __align__(16) uint8_t sm[];
+    const Lay<D> L(N);
+    float *kb = reinterpret_cast<float *>(sm + L.kb), *al = reinterpret_cast<float *>(sm + L.al);
+    float *xq = reinterpret_cast<float *>(sm + L.xq), *u = reinterpret_cast<float *>(sm + L.u);
+    float *ck = reinterpret_cast<float *>(sm + L.ck), *cq = reinterpret_cast<float *>(sm + L.cq);
+    float *xy = reinterpret_cast<float *>(sm + L.xy), *part = reinterpret_cast<float *>(sm + L.part);
+    __nv_bfloat16 *xh = reinterpret_cast<__nv_bfloat16 *>(xy), *xl = xh + 2 * N * kPitch;
+    const uint8_t **unit = reinterpret_cast<const uint8_t **>(sm + L.unit);
+    uint64_t *mask = reinterpret_cast<uint64_t *>(sm + L.mask);
+    float *beta = reinterpret_cast<float *>(sm + L.beta);
+    int32_t *up = reinterpret_cast<int32_t *>(sm + L.up);
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int b = blockIdx.x / a.H, h = blockIdx.x % a.H;
+    const int32_t *pages = a.state_pages + (int64_t)b * a.pool.pages_per_object;
     const Request r = request_of(a, b);
     if (r.n <= 0) {
         if (r.n < 0 && h == 0 && tid == 0) flag_status(a.status, KDA_DEV_BAD_META);
         return;
     }
     const int n = r.n;
-    const int32_t *pages = a.state_pages + (int64_t)b * a.pool.pages_per_object;
+    int32_t p = -1;
+    if (tid < n) p = __ldg(a.parent + r.first + tid);
     if (pages_lost(a.pool, pages)) {
         if (h == 0 && tid == 0) flag_status(a.status, KDA_DEV_BAD_PAGE);
         return;
     }
-    // ---- S_0: a thread takes a column and D / 2 rows
+    // ---- S_0 is asked into L2; its addresses
     const uint64_t rec = (uint64_t)h * (uint64_t)a.pool.rec_bytes, win_off = rec + (uint64_t)D * D * 4;
-    const int j = tid % D, half = tid / D;
-    float s[D / 2];
-    {
-        const uint64_t off = rec + ((uint64_t)(half * (D / 2)) * D + j) * 4, span = (uint64_t)(D / 2 - 1) * D * 4;
-        const uint8_t *run = run_addr(a.pool, pages, off, span, a.status);
-#pragma unroll
-        for (int i = 0; i < D / 2; ++i)
-            s[i] = __ldcs(reinterpret_cast<const float *>(run ? run + i * D * 4 : obj_addr(a.pool, pages, off + (uint64_t)i * D * 4, a.status)));
+    for (int i = tid; i < D * D * 4 / kUnit; i += kThreads) {
+        const uint8_t *at = obj_addr(a.pool, pages, rec + (uint64_t)i * kUnit, a.status);
+        unit[i] = at;
+        ptx::prefetch_l2(at);
+        ptx::prefetch_l2(at + 128);
     }
-    // ---- parents, branches
-    int32_t p = -1;
-    if (tid < n) p = __ldg(a.parent + r.first + tid);
+    // ---- parents, branches: by pointer doubling, as in the plan
     if (__syncthreads_or(p < -1 || (tid < n && p >= tid))) {
         if (h == 0 && tid == 0) flag_status(a.status, KDA_DEV_BAD_META);
         return;
     }
     {
-        uint64_t m = tid < kMost ? 1ull << tid : 0;
+        uint64_t m = tid < N ? 1ull << tid : 0;
         int32_t q = p;
 #pragma unroll 1
-        for (int k = 1; k < kMost; k *= 2) {
-            if (tid < kMost) mask[tid] = m, up[tid] = q;
+        for (int k = 1; k < N; k *= 2) {
+            if (tid < N) mask[tid] = m, up[tid] = q;
             if (!__syncthreads_or(q >= 0)) break;
             if (q >= 0) m |= mask[q], q = up[q];
             __syncthreads();
         }
-        __syncthreads();
-        if (tid < kMost) mask[tid] = m, up[tid] = p;
+        if (tid < N) mask[tid] = m, up[tid] = p;
         if (tid < n) beta[tid] = ld_elem(static_cast<const T *>(a.beta) + (r.first + tid) * a.H + h);
     }
     __syncthreads();
     // ---- convolutions along the branches; alpha
     {
-        constexpr int kGroups = 3 * D / V, kAt = NT / kGroups;   // drafts at a time
-        const int g = tid % kGroups, c = g * V % D, part3 = g * V / D;
-        const void *src = part3 == 0 ? a.q : part3 == 1 ? a.k : a.v;
-        float *dst = part3 == 0 ? xq : part3 == 1 ? kb : u;
+        constexpr int kGroups = 3 * D / V, kAt = kThreads / kGroups;   // drafts at a time
+        const int g = tid % kGroups, c = g * V % D, which = g * V / D;
+        const void *src = which == 0 ? a.q : which == 1 ? a.k : a.v;
+        float *dst = which == 0 ? xq : which == 1 ? kb : u;
         if (tid / kGroups < kAt) {
             float w[V][4];
 #pragma unroll
             for (int x = 0; x < V; ++x) {
-                const float4 f = *reinterpret_cast<const float4 *>(a.conv_w + ((int64_t)h * 3 * D + part3 * D + c + x) * 4);
+                const float4 f = __ldg(reinterpret_cast<const float4 *>(a.conv_w + ((int64_t)h * 3 * D + which * D + c + x) * 4));
                 w[x][0] = f.x, w[x][1] = f.y, w[x][2] = f.z, w[x][3] = f.w;
             }
             for (int t = tid / kGroups; t < n; t += kAt) {
@@ -147,107 +186,196 @@ __global__ void __launch_bounds__(2 * D) verify_tree_kernel(const __grid_constan
 #pragma unroll
                 for (int tap = 3; tap >= 0; --tap) {
                     const T *at = i >= 0 ? reinterpret_cast<const T *>(raw_at(a, src, r.first + i, h, D, c, sizeof(T)))
-                                         : reinterpret_cast<const T *>(obj_addr(a.pool, pages, win_off + ((uint64_t)(2 - back) * 3 * D + part3 * D + c) * sizeof(T), a.status));
-                    float x4[V];
-                    load_vec(at, x4);
+                                         : reinterpret_cast<const T *>(obj_addr(a.pool, pages, win_off + ((uint64_t)(2 - back) * 3 * D + which * D + c) * sizeof(T), a.status));
+                    float z[V];
+                    load_vec(at, z);
 #pragma unroll
-                    for (int x = 0; x < V; ++x) y[x] = fmaf(w[x][tap], x4[x], y[x]);
+                    for (int x = 0; x < V; ++x) y[x] = fmaf(w[x][tap], z[x], y[x]);
                     if (i >= 0) i = up[i];
                     else ++back;
                 }
 #pragma unroll
-                for (int x = 0; x < V; ++x) dst[t * D + c + x] = y[x];
+                for (int x = 0; x < V; x += 4) *reinterpret_cast<float4 *>(dst + t * D + c + x) = make_float4(y[x], y[x + 1], y[x + 2], y[x + 3]);
             }
         }
-        for (int i = tid; i < n * (D / V); i += NT) {
+        for (int i = tid; i < n * (D / V); i += kThreads) {
             const int t = i / (D / V), ch = i % (D / V) * V;
             float x[V];
             load_vec(reinterpret_cast<const T *>(raw_at(a, a.alpha, r.first + t, h, D, ch, sizeof(T))), x);
 #pragma unroll
-            for (int y = 0; y < V; ++y) al[t * D + ch + y] = x[y];
+            for (int y = 0; y < V; y += 4) *reinterpret_cast<float4 *>(al + t * D + ch + y) = make_float4(x[y], x[y + 1], x[y + 2], x[y + 3]);
         }
     }
     __syncthreads();
-    // ---- a warp a draft: up its branch, a lane D / 32 channels
-    constexpr int C = D / 32;
+    // ---- up the branches: sixteen lanes a draft, a lane 4 or 8 channels
+    {
+        constexpr int C = D / 16;
+        const int l16 = lane % 16;
+        auto get = [&](const float *row, float2 (&x)[C / 2]) {
+#pragma unroll
+            for (int i = 0; i < C; i += 4) {
+                const float4 f = *reinterpret_cast<const float4 *>(row + 16 * i + 4 * l16);
+                x[i / 2] = make_float2(f.x, f.y), x[i / 2 + 1] = make_float2(f.z, f.w);
+            }
+        };
 #pragma unroll 1
-    for (int t = warp; t < n; t += kWarps) {
-        float kr[C], qr[C];
+        for (int t0 = 2 * warp; t0 < n; t0 += 2 * kWarps) {
+            const int t = min(t0 + lane / 16, n - 1);           // (the last one twice where they are odd)
+            float2 kr[C / 2], qr[C / 2];
+            get(kb + t * D, kr);
+            get(xq + t * D, qr);
+            uint64_t m = mask[t];
+            int i = t;
+            while (__any_sync(0xFFFFFFFFu, m != 0)) {
+                float2 ki[C / 2], f[C / 2], dk = make_float2(0.f, 0.f), dq = dk;
+                get(kb + i * D, ki);
+                get(al + i * D, f);
 #pragma unroll
-        for (int x = 0; x < C; ++x) kr[x] = kb[t * D + lane + 32 * x], qr[x] = xq[t * D + lane + 32 * x];
-        uint64_t m = mask[t];
-        int i = t;
-        for (;;) {
-            float dk = 0.f, dq = 0.f;
+                for (int x = 0; x < C / 2; ++x) dk = tcx::ffma2(kr[x], ki[x], dk), dq = tcx::ffma2(qr[x], ki[x], dq);
+                // even lanes sum for k, odd ones for q
+                const float mine = lane & 1 ? dq.x + dq.y : dk.x + dk.y, other = lane & 1 ? dk.x + dk.y : dq.x + dq.y;
+                float sum = mine + __shfl_xor_sync(0xFFFFFFFFu, other, 1);
 #pragma unroll
-            for (int x = 0; x < C; ++x) {
-                const float ki = kb[i * D + lane + 32 * x];
-                dk = fmaf(kr[x], ki, dk), dq = fmaf(qr[x], ki, dq);
+                for (int y = 2; y < 16; y <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, y);
+                if (m) {
+                    if (l16 < 2) (l16 ? cq : ck)[t * (t + 1) / 2 + i] = sum;
+#pragma unroll
+                    for (int x = 0; x < C / 2; ++x) kr[x] = tcx::fmul2(kr[x], f[x]), qr[x] = tcx::fmul2(qr[x], f[x]);
+                    m &= ~(1ull << i);
+                    if (m) i = 63 - __clzll((long long)m);
+                }
             }
+            // A k and A q
 #pragma unroll
-            for (int y = 16; y; y >>= 1) dk += __shfl_xor_sync(0xFFFFFFFFu, dk, y), dq += __shfl_xor_sync(0xFFFFFFFFu, dq, y);
-            if (lane == 0) ck[t * N + i] = dk, cq[t * N + i] = dq;
+            for (int row = 0; row < 2; ++row) {
+                const int at = row * N + t;
 #pragma unroll
-            for (int x = 0; x < C; ++x) {
-                const float f = al[i * D + lane + 32 * x];
-                kr[x] *= f, qr[x] *= f;
+                for (int x = 0; x < C; x += 4) {
+                    const float2 y = row ? qr[x / 2] : kr[x / 2], z = row ? qr[x / 2 + 1] : kr[x / 2 + 1];
+                    if constexpr (kMma) {
+                        uint2 hi, lo;
+                        split2(y.x, y.y, hi.x, lo.x), split2(z.x, z.y, hi.y, lo.y);
+                        *reinterpret_cast<uint2 *>(xh + at * kPitch + 16 * x + 4 * l16) = hi;
+                        *reinterpret_cast<uint2 *>(xl + at * kPitch + 16 * x + 4 * l16) = lo;
+                    } else {
+                        *reinterpret_cast<float4 *>(xy + at * D + 16 * x + 4 * l16) = make_float4(y.x, y.y, z.x, z.y);
+                    }
+                }
             }
-            m &= ~(1ull << i);
-            if (!m) break;
-            i = 63 - __clzll((long long)m);
         }
-#pragma unroll
-        for (int x = 0; x < C; ++x) xk[t * D + lane + 32 * x] = kr[x], xq[t * D + lane + 32 * x] = qr[x];
     }
-    __syncthreads();
-    // ---- rows of [A k | A q] times S_0, in their places, eight at a time: each group sums its half of the channels
-    for (int r0 = 0; r0 < 2 * n; r0 += 8) {
-        float y[8];
+    // ---- their products with S_0, over them: row r of [A k | A q], column j at xy[r D + j]
+    if constexpr (kMma) {
+        // A warp takes 16 columns (two tiles of 8, their columns in turn).  Both operands in two bf16 terms, three of
+        // the four products: 16 bits of either, 2^-8 of an output's own rounding.
+        constexpr int kCols = D / 16, kHalves = kWarps / kCols;   // d = 64: two warps a 16 columns, each half of the rows
+        const int w = warp % kCols, g = lane / 4, t4 = lane % 4;
+        constexpr int kMine = MT >= kHalves ? MT / kHalves : 1;   // tiles of rows
+        const int mt0 = MT >= kHalves ? warp / kCols * kMine : 0;
+        const bool works = MT >= kHalves || warp / kCols == 0;
+        float acc[kMine][2][4] = {};
+        __syncthreads();
+        if (works) {
+            const uint32_t at = ptx::smem_u32(xh + (mt0 * 16 + lane % 16) * kPitch + lane / 16 * 8);
+            constexpr uint32_t kLow = 2 * N * kPitch * 2;   // bytes from the upper terms to the lower ones
 #pragma unroll
-        for (int x = 0; x < 8; ++x) {
-            y[x] = 0.f;
-            const int row = r0 + x;
-            if (row < 2 * n) {
-                const float4 *v = reinterpret_cast<const float4 *>((row < n ? xk + row * D : xq + (row - n) * D) + half * (D / 2));
+            for (int s = 0; s < D / 16; ++s) {
+                // rows 16 s + 2 t4, + 1, + 8, + 9 of S_0, columns 16 w + 2 g and the next
+                float2 f[4];
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
+                for (int x = 0; x < 4; ++x) {
+                    const int byte = (16 * s + 2 * t4 + (x & 1) + 8 * (x >> 1)) * D * 4 + (16 * w + 2 * g) * 4;
+                    f[x] = __ldcs(reinterpret_cast<const float2 *>(unit[byte / kUnit] + byte % kUnit));
+                }
+                uint32_t hi[2][2], lo[2][2];                 // [tile][register]
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    split2(f[2 * x].x, f[2 * x + 1].x, hi[0][x], lo[0][x]);
+                    split2(f[2 * x].y, f[2 * x + 1].y, hi[1][x], lo[1][x]);
+                }
+#pragma unroll
+                for (int mt = 0; mt < kMine; ++mt) {
+                    uint32_t ah[4], as[4];
+                    ldsm4(ah, at + (mt * 16 * kPitch + 16 * s) * 2);
+                    ldsm4(as, at + (mt * 16 * kPitch + 16 * s) * 2 + kLow);
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        mma(acc[mt][y], as, hi[y][0], hi[y][1]);
+                        mma(acc[mt][y], ah, lo[y][0], lo[y][1]);
+                        mma(acc[mt][y], ah, hi[y][0], hi[y][1]);
+                    }
+                }
+            }
+        }
+        __syncthreads();
+        if (works)
+#pragma unroll
+            for (int mt = 0; mt < kMine; ++mt)
+#pragma unroll
+                for (int x = 0; x < 2; ++x)   // columns 16 w + 4 t4 and up: tiles 0, 1, 0, 1
+                    *reinterpret_cast<float4 *>(xy + ((mt0 + mt) * 16 + g + 8 * x) * D + 16 * w + 4 * t4) =
+                        make_float4(acc[mt][0][2 * x], acc[mt][1][2 * x], acc[mt][0][2 * x + 1], acc[mt][1][2 * x + 1]);
+        __syncthreads();
+    } else {
+        // a thread takes a column of S_0 and a part of its rows; eight rows of the products at a time
+        constexpr int G = kThreads / D, R = D / G;
+        const int j = tid % D, grp = tid / D;
+        float s[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int byte = ((grp * R + i) * D + j) * 4;
+            s[i] = __ldcs(reinterpret_cast<const float *>(unit[byte / kUnit] + byte % kUnit));
+        }
+        __syncthreads();
+#pragma unroll 1
+        for (int r0 = 0; r0 < 2 * N; r0 += 8) {
+            if (r0 % N >= n) continue;                       // rows of no draft
+            float y[8];
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                y[x] = 0.f;
+                const float4 *v = reinterpret_cast<const float4 *>(xy + (r0 + x) * D + grp * R);
+#pragma unroll
+                for (int i = 0; i < R / 4; ++i) {
                     const float4 f = v[i];
                     y[x] = fmaf(f.x, s[4 * i], y[x]), y[x] = fmaf(f.y, s[4 * i + 1], y[x]);
                     y[x] = fmaf(f.z, s[4 * i + 2], y[x]), y[x] = fmaf(f.w, s[4 * i + 3], y[x]);
                 }
+                if (grp) part[((grp - 1) * 8 + x) * D + j] = y[x];
             }
+            __syncthreads();
+            if (grp == 0)
+#pragma unroll
+                for (int x = 0; x < 8; ++x) {
+#pragma unroll
+                    for (int i = 0; i < G - 1; ++i) y[x] += part[(i * 8 + x) * D + j];
+                    xy[(r0 + x) * D + j] = y[x];
+                }
+            __syncthreads();
         }
-        if (half)
-#pragma unroll
-            for (int x = 0; x < 8; ++x) part[x * D + j] = y[x];
-        __syncthreads();
-        if (!half)
-#pragma unroll
-            for (int x = 0; x < 8; ++x) {
-                const int row = r0 + x;
-                if (row < 2 * n) (row < n ? xk + row * D : xq + (row - n) * D)[j] = y[x] + part[x * D + j];
-            }
-        __syncthreads();
     }
     // ---- u, column by column
-    if (!half) {
+    const int j = tid % D, grp = tid / D;
+    if (grp == 0) {
 #pragma unroll 1
         for (int t = 0; t < n; ++t) {
-            float acc = xk[t * D + j];
+            float acc = xy[t * D + j];
+            const float *c = ck + t * (t + 1) / 2;
             for (uint64_t m = mask[t] & ~(1ull << t); m; m &= m - 1) {
                 const int i = __ffsll((long long)m) - 1;
-                acc = fmaf(ck[t * N + i], u[i * D + j], acc);
+                acc = fmaf(c[i], u[i * D + j], acc);
             }
             u[t * D + j] = beta[t] * (u[t * D + j] - acc);
         }
     }
     __syncthreads();
 #pragma unroll 1
-    for (int t = half; t < n; t += 2) {
-        float acc = xq[t * D + j];
+    for (int t = grp; t < n; t += kThreads / D) {
+        float acc = xy[(N + t) * D + j];
+        const float *c = cq + t * (t + 1) / 2;
         for (uint64_t m = mask[t]; m; m &= m - 1) {
             const int i = __ffsll((long long)m) - 1;
-            acc = fmaf(cq[t * N + i], u[i * D + j], acc);
+            acc = fmaf(c[i], u[i * D + j], acc);
         }
         st_elem(static_cast<T *>(a.o) + ((r.first + t) * a.H + h) * D + j, acc);
     }
@@ -260,8 +388,8 @@ constexpr int kAccThreads = 512, kAccWarps = 16;
 template <int D, class T>
 __global__ void __launch_bounds__(kAccThreads) verify_tree_accept_kernel(const __grid_constant__ VerifyTreeArgs a, int N) {
     constexpr int V = kVec<T>, C3 = 3 * D, R = D / kAccWarps, C = D / 32;
-    extern __shared__ __align__(16) float sm[];
-    float *kb = sm, *vb = kb + N * D, *al = vb + N * D, *red = al + N * D, *w = red + kAccWarps * D;
+    extern __shared__ __align__(16) uint8_t sm[];
+    float *kb = reinterpret_cast<float *>(sm), *vb = kb + N * D, *al = vb + N * D, *red = al + N * D, *w = red + kAccWarps * D;
     float *beta = w + D;
     int32_t *path = reinterpret_cast<int32_t *>(beta + kMost);
     T *win = reinterpret_cast<T *>(path + kMost);   // the window before, [3][3D]
@@ -377,25 +505,32 @@ __global__ void __launch_bounds__(kAccThreads) verify_tree_accept_kernel(const _
     }
 }
 
-template <class K>
-cudaError_t launch(K kern, const VerifyTreeArgs &a, int threads, int64_t smem, int N, cudaStream_t st) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+template <int D, class T, int MT>
+cudaError_t verify_of(const VerifyTreeArgs &a, cudaStream_t st) {
+    auto kern = verify_tree_kernel<D, T, MT>;
+    const int smem = Lay<D>(8 * MT).total;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    kern<<<(unsigned)(a.B * a.H), threads, (size_t)smem, st>>>(a, N);
+    kern<<<(unsigned)(a.B * a.H), kThreads, smem, st>>>(a);
     return cudaGetLastError();
 }
-
 template <int D, class T>
 cudaError_t verify(const VerifyTreeArgs &a, cudaStream_t st) {
-    const int N = (a.max_q + 7) / 8 * 8;
-    return launch(verify_tree_kernel<D, T>, a, 2 * D, Lay<D>::bytes(N), N, st);
+    if (a.max_q <= 8) return verify_of<D, T, 1>(a, st);
+    if (a.max_q <= 16) return verify_of<D, T, 2>(a, st);
+    if (a.max_q <= 32) return verify_of<D, T, 4>(a, st);
+    return verify_of<D, T, 8>(a, st);
 }
 
 template <int D, class T>
 cudaError_t accept(const VerifyTreeArgs &a, cudaStream_t st) {
     const int N = (a.max_q + 7) / 8 * 8;
     const int64_t smem = ((int64_t)3 * N * D + kAccWarps * D + D + 2 * kMost) * 4 + 9 * D * (int64_t)sizeof(T);
-    return launch(verify_tree_accept_kernel<D, T>, a, kAccThreads, smem, N, st);
+    auto kern = verify_tree_accept_kernel<D, T>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    kern<<<(unsigned)(a.B * a.H), kAccThreads, (size_t)smem, st>>>(a, N);
+    return cudaGetLastError();
 }
 
 }  // namespace
