@@ -70,21 +70,22 @@ constexpr int kUnit = 256;   // bytes of a record that lie in one page: pages an
 // Shared memory for trees of up to N drafts (a multiple of 8), in bytes.
 template <int D>
 struct Lay {
-    int N, kb, al, xq, u, ck, cq, xy, part, unit, mask, beta, up, total;
-    __host__ __device__ explicit Lay(int n) {
+    static constexpr int P = D * 4;   // of a draft's row
+    int kb, al, xk, xq, v, ck, cq, part, unit, tab, mask, beta, total;
+    __host__ __device__ explicit Lay(int N) {
         int at = 0;
         auto take = [&](int bytes) {
             const int was = at;
             at += (bytes + 15) / 16 * 16;
             return was;
         };
-        N = n;
-        kb = take(N * D * 4), al = take(N * D * 4), xq = take(N * D * 4), u = take(N * D * 4);   // u: v until solved
-        ck = take(N * (N + 1) / 2 * 4), cq = take(N * (N + 1) / 2 * 4);                          // row t: i <= t
-        xy = take(2 * N * (D + 8) * 4);        // [A k | A q] in two bf16 terms or in fp32, then their products with S_0
+        kb = take(N * P), al = take(N * P);       // k and alpha; when the branches are walked, the products with S_0
+        xk = take(N * P), xq = take(N * P);       // A k and A q: two bf16 terms or fp32; xk then holds u, xq held q
+        v = take(N * P);
+        ck = take(N * N * 4), cq = take(N * N * 4);   // c_ti at [i][t], 0 where i is not on t's branch
         part = take((kThreads / D - 1) * 8 * D * 4);
-        unit = take(D * D * 4 / kUnit * 8);    // addresses of S_0
-        mask = take(N * 8), beta = take(N * 4), up = take(N * 4);
+        unit = take(D * D * 4 / kUnit * 8);       // addresses of S_0
+        tab = take(N * 16), mask = take(N * 8), beta = take(N * 4);
         total = at;
     }
 };
@@ -106,23 +107,32 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t 
     const float2 h = tcx::bf2_to_f2(hi);
     lo = tcx::f2_to_bf2(x - h.x, y - h.y);
 }
+// The elements of a 16-byte unit, in pairs.
+__device__ __forceinline__ void pairs_of(const uint4 &u, float2 (&x)[2]) {
+    x[0] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
+    x[1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
+}
+__device__ __forceinline__ void pairs_of(const uint4 &u, float2 (&x)[4]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = tcx::bf2_to_f2(w[i]);
+}
 
 // MT: tiles of 16 rows of [A k | A q], of up to 8 MT drafts.
 template <int D, class T, int MT>
 __global__ void __launch_bounds__(kThreads, MT <= 2 ? 3 : MT == 4 ? 2 : 1) verify_tree_kernel(const __grid_constant__ VerifyTreeArgs a) {
-    constexpr int V = kVec<T>, N = 8 * MT, kPitch = D + 8;   // of a row in bf16: rows 16 bytes apart in their banks
+    constexpr int V = kVec<T>, N = 8 * MT, P = Lay<D>::P;
     constexpr bool kMma = sizeof(T) == 2;
     extern __shared__ __align__(16) uint8_t sm[];
     const Lay<D> L(N);
     float *kb = reinterpret_cast<float *>(sm + L.kb), *al = reinterpret_cast<float *>(sm + L.al);
-    float *xq = reinterpret_cast<float *>(sm + L.xq), *u = reinterpret_cast<float *>(sm + L.u);
+    float *xk = reinterpret_cast<float *>(sm + L.xk), *xq = reinterpret_cast<float *>(sm + L.xq);
+    float *vb = reinterpret_cast<float *>(sm + L.v), *part = reinterpret_cast<float *>(sm + L.part);
     float *ck = reinterpret_cast<float *>(sm + L.ck), *cq = reinterpret_cast<float *>(sm + L.cq);
-    float *xy = reinterpret_cast<float *>(sm + L.xy), *part = reinterpret_cast<float *>(sm + L.part);
-    __nv_bfloat16 *xh = reinterpret_cast<__nv_bfloat16 *>(xy), *xl = xh + 2 * N * kPitch;
     const uint8_t **unit = reinterpret_cast<const uint8_t **>(sm + L.unit);
+    int4 *tab = reinterpret_cast<int4 *>(sm + L.tab);
     uint64_t *mask = reinterpret_cast<uint64_t *>(sm + L.mask);
     float *beta = reinterpret_cast<float *>(sm + L.beta);
-    int32_t *up = reinterpret_cast<int32_t *>(sm + L.up);
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int b = blockIdx.x / a.H, h = blockIdx.x % a.H;
     const int32_t *pages = a.state_pages + (int64_t)b * a.pool.pages_per_object;
@@ -132,78 +142,121 @@ __global__ void __launch_bounds__(kThreads, MT <= 2 ? 3 : MT == 4 ? 2 : 1) verif
         return;
     }
     const int n = r.n;
-    int32_t p = -1;
-    if (tid < n) p = __ldg(a.parent + r.first + tid);
-    if (pages_lost(a.pool, pages)) {
-        if (h == 0 && tid == 0) flag_status(a.status, KDA_DEV_BAD_PAGE);
-        return;
-    }
-    // ---- S_0 is asked into L2; its addresses
+    const int64_t row0 = (r.first * a.H + h) * D;      // the first draft's row of a token tensor
+    // ---- pages; S_0 is asked into L2, its addresses are kept
     const uint64_t rec = (uint64_t)h * (uint64_t)a.pool.rec_bytes, win_off = rec + (uint64_t)D * D * 4;
+    int32_t wrong = 0;
+    for (int i = tid; i < a.pool.pages_per_object; i += kThreads)
+        if ((uint32_t)__ldg(pages + i) >= (uint32_t)a.pool.num_pages) wrong = KDA_DEV_BAD_PAGE;
     for (int i = tid; i < D * D * 4 / kUnit; i += kThreads) {
-        const uint8_t *at = obj_addr(a.pool, pages, rec + (uint64_t)i * kUnit, a.status);
+        const uint8_t *at = obj_addr(a.pool, pages, rec + (uint64_t)i * kUnit, nullptr);
         unit[i] = at;
-        ptx::prefetch_l2(at);
-        ptx::prefetch_l2(at + 128);
+        if (at) ptx::prefetch_l2(at), ptx::prefetch_l2(at + 128);
     }
-    // ---- parents, branches: by pointer doubling, as in the plan
-    if (__syncthreads_or(p < -1 || (tid < n && p >= tid))) {
-        if (h == 0 && tid == 0) flag_status(a.status, KDA_DEV_BAD_META);
-        return;
-    }
-    {
-        uint64_t m = tid < N ? 1ull << tid : 0;
-        int32_t q = p;
+    for (int i = tid; i < N * N / 2; i += kThreads) reinterpret_cast<float4 *>(ck)[i] = make_float4(0.f, 0.f, 0.f, 0.f);   // cq too
+    // ---- by the last warp: branches, by pointer doubling as in the plan, and the rows that a convolution reads: the
+    // draft's own and the three before it, in bytes from the first draft's; ~w for the window's row w
+    if (warp == kWarps - 1) {
+        uint64_t m[2];
+        int32_t p[2], q[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int i = lane + 32 * x;
+            p[x] = i < n ? __ldg(a.parent + r.first + i) : -1;
+            if (p[x] < -1 || (i < n && p[x] >= i)) wrong |= KDA_DEV_BAD_META, p[x] = -1;
+            q[x] = p[x], m[x] = 1ull << i;
+            if (i < n) beta[i] = ld_elem(static_cast<const T *>(a.beta) + (r.first + i) * a.H + h);
+        }
+        int32_t *up = reinterpret_cast<int32_t *>(tab);   // [N] for now
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+            if (lane + 32 * x < N) up[lane + 32 * x] = p[x];
+        __syncwarp();
+        int4 rows[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            int i = lane + 32 * x < N ? lane + 32 * x : 0, back = 3;
+            int32_t o[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                o[y] = i >= 0 ? i * a.H * D * (int)sizeof(T) : ~--back;
+                if (i >= 0) i = up[i];
+            }
+            rows[x] = make_int4(o[0], o[1], o[2], o[3]);
+        }
+        __syncwarp();
 #pragma unroll 1
         for (int k = 1; k < N; k *= 2) {
-            if (tid < N) mask[tid] = m, up[tid] = q;
-            if (!__syncthreads_or(q >= 0)) break;
-            if (q >= 0) m |= mask[q], q = up[q];
-            __syncthreads();
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+                if (lane + 32 * x < N) mask[lane + 32 * x] = m[x], up[lane + 32 * x] = q[x];
+            __syncwarp();
+            if (!__any_sync(0xFFFFFFFFu, q[0] >= 0 || q[1] >= 0)) break;
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+                if (q[x] >= 0) m[x] |= mask[q[x]], q[x] = up[q[x]];
+            __syncwarp();
         }
-        if (tid < N) mask[tid] = m, up[tid] = p;
-        if (tid < n) beta[tid] = ld_elem(static_cast<const T *>(a.beta) + (r.first + tid) * a.H + h);
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+            if (lane + 32 * x < N) mask[lane + 32 * x] = m[x], tab[lane + 32 * x] = rows[x];
     }
-    __syncthreads();
+    if (__syncthreads_or(wrong)) {
+        if (wrong && h == 0) flag_status(a.status, wrong);
+        return;
+    }
     // ---- convolutions along the branches; alpha
     {
         constexpr int kGroups = 3 * D / V, kAt = kThreads / kGroups;   // drafts at a time
         const int g = tid % kGroups, c = g * V % D, which = g * V / D;
-        const void *src = which == 0 ? a.q : which == 1 ? a.k : a.v;
-        float *dst = which == 0 ? xq : which == 1 ? kb : u;
+        const void *tensor = which == 0 ? a.q : which == 1 ? a.k : a.v;
+        const uint8_t *src = static_cast<const uint8_t *>(tensor) + (row0 + c) * (int)sizeof(T);
+        float *dst = (which == 0 ? xq : which == 1 ? kb : vb) + c;
         if (tid / kGroups < kAt) {
-            float w[V][4];
+            float2 w[4][V / 2];
+            uint4 win[3];
 #pragma unroll
-            for (int x = 0; x < V; ++x) {
-                const float4 f = __ldg(reinterpret_cast<const float4 *>(a.conv_w + ((int64_t)h * 3 * D + which * D + c + x) * 4));
-                w[x][0] = f.x, w[x][1] = f.y, w[x][2] = f.z, w[x][3] = f.w;
+            for (int x = 0; x < V; x += 2) {
+                const float4 *f = reinterpret_cast<const float4 *>(a.conv_w + ((int64_t)h * 3 * D + which * D + c + x) * 4);
+                const float4 y = __ldg(f), z = __ldg(f + 1);
+                w[0][x / 2] = make_float2(y.x, z.x), w[1][x / 2] = make_float2(y.y, z.y);
+                w[2][x / 2] = make_float2(y.z, z.z), w[3][x / 2] = make_float2(y.w, z.w);
             }
-            for (int t = tid / kGroups; t < n; t += kAt) {
-                float y[V];
 #pragma unroll
-                for (int x = 0; x < V; ++x) y[x] = 0.f;
-                int i = t, back = 0;                             // draft, or rows into the window
+            for (int x = 0; x < 3; ++x)
+                win[x] = *reinterpret_cast<const uint4 *>(obj_addr(a.pool, pages, win_off + ((uint64_t)x * 3 * D + which * D + c) * sizeof(T), nullptr));
+            for (int t = tid / kGroups; t < n; t += kAt) {
+                const int4 rows = tab[t];
+                const int32_t o[4] = {rows.w, rows.z, rows.y, rows.x};
+                uint4 z[4];
+#pragma unroll
+                for (int tap = 0; tap < 4; ++tap) {
+                    if (o[tap] >= 0) z[tap] = __ldg(reinterpret_cast<const uint4 *>(src + o[tap]));
+                    else z[tap] = o[tap] == ~2 ? win[2] : o[tap] == ~1 ? win[1] : win[0];
+                }
+                float2 y[V / 2];
+#pragma unroll
+                for (int x = 0; x < V / 2; ++x) y[x] = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int tap = 3; tap >= 0; --tap) {
-                    const T *at = i >= 0 ? reinterpret_cast<const T *>(raw_at(a, src, r.first + i, h, D, c, sizeof(T)))
-                                         : reinterpret_cast<const T *>(obj_addr(a.pool, pages, win_off + ((uint64_t)(2 - back) * 3 * D + which * D + c) * sizeof(T), a.status));
-                    float z[V];
-                    load_vec(at, z);
+                    float2 f[V / 2];
+                    pairs_of(z[tap], f);
 #pragma unroll
-                    for (int x = 0; x < V; ++x) y[x] = fmaf(w[x][tap], z[x], y[x]);
-                    if (i >= 0) i = up[i];
-                    else ++back;
+                    for (int x = 0; x < V / 2; ++x) y[x] = tcx::ffma2(w[tap][x], f[x], y[x]);
                 }
 #pragma unroll
-                for (int x = 0; x < V; x += 4) *reinterpret_cast<float4 *>(dst + t * D + c + x) = make_float4(y[x], y[x + 1], y[x + 2], y[x + 3]);
+                for (int x = 0; x < V; x += 4)
+                    *reinterpret_cast<float4 *>(dst + t * D + x) = make_float4(y[x / 2].x, y[x / 2].y, y[x / 2 + 1].x, y[x / 2 + 1].y);
             }
         }
+        const uint8_t *alpha = static_cast<const uint8_t *>(a.alpha) + row0 * (int)sizeof(T);
         for (int i = tid; i < n * (D / V); i += kThreads) {
             const int t = i / (D / V), ch = i % (D / V) * V;
-            float x[V];
-            load_vec(reinterpret_cast<const T *>(raw_at(a, a.alpha, r.first + t, h, D, ch, sizeof(T))), x);
+            float2 f[V / 2];
+            pairs_of(__ldg(reinterpret_cast<const uint4 *>(alpha + (t * a.H * D + ch) * (int)sizeof(T))), f);
 #pragma unroll
-            for (int y = 0; y < V; y += 4) *reinterpret_cast<float4 *>(al + t * D + ch + y) = make_float4(x[y], x[y + 1], x[y + 2], x[y + 3]);
+            for (int x = 0; x < V; x += 4)
+                *reinterpret_cast<float4 *>(al + t * D + ch + x) = make_float4(f[x / 2].x, f[x / 2].y, f[x / 2 + 1].x, f[x / 2 + 1].y);
         }
     }
     __syncthreads();
@@ -220,10 +273,12 @@ __global__ void __launch_bounds__(kThreads, MT <= 2 ? 3 : MT == 4 ? 2 : 1) verif
         };
 #pragma unroll 1
         for (int t0 = 2 * warp; t0 < n; t0 += 2 * kWarps) {
-            const int t = min(t0 + lane / 16, n - 1);           // (the last one twice where they are odd)
+            const bool mine = t0 + lane / 16 < n;               // (where they are odd the last one goes along twice)
+            const int t = mine ? t0 + lane / 16 : n - 1;
             float2 kr[C / 2], qr[C / 2];
             get(kb + t * D, kr);
             get(xq + t * D, qr);
+            __syncwarp();
             uint64_t m = mask[t];
             int i = t;
             while (__any_sync(0xFFFFFFFFu, m != 0)) {
@@ -233,51 +288,52 @@ __global__ void __launch_bounds__(kThreads, MT <= 2 ? 3 : MT == 4 ? 2 : 1) verif
 #pragma unroll
                 for (int x = 0; x < C / 2; ++x) dk = tcx::ffma2(kr[x], ki[x], dk), dq = tcx::ffma2(qr[x], ki[x], dq);
                 // even lanes sum for k, odd ones for q
-                const float mine = lane & 1 ? dq.x + dq.y : dk.x + dk.y, other = lane & 1 ? dk.x + dk.y : dq.x + dq.y;
-                float sum = mine + __shfl_xor_sync(0xFFFFFFFFu, other, 1);
+                const float sk = dk.x + dk.y, sq = dq.x + dq.y;
+                float sum = (lane & 1 ? sq : sk) + __shfl_xor_sync(0xFFFFFFFFu, lane & 1 ? sk : sq, 1);
 #pragma unroll
                 for (int y = 2; y < 16; y <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, y);
                 if (m) {
-                    if (l16 < 2) (l16 ? cq : ck)[t * (t + 1) / 2 + i] = sum;
+                    if (l16 < 2) (l16 ? cq : ck)[i * N + t] = sum;
 #pragma unroll
                     for (int x = 0; x < C / 2; ++x) kr[x] = tcx::fmul2(kr[x], f[x]), qr[x] = tcx::fmul2(qr[x], f[x]);
                     m &= ~(1ull << i);
                     if (m) i = 63 - __clzll((long long)m);
                 }
             }
-            // A k and A q
+            // A k, and A q in q's place (nobody else reads it).  Two bf16 terms: a row's 16-byte units are exchanged
+            // by the row's number, so that eight rows' units of one column lie in different banks.
+            if (mine)
 #pragma unroll
-            for (int row = 0; row < 2; ++row) {
-                const int at = row * N + t;
+                for (int row = 0; row < 2; ++row) {
+                    uint8_t *at = reinterpret_cast<uint8_t *>(row ? xq : xk) + t * P;
 #pragma unroll
-                for (int x = 0; x < C; x += 4) {
-                    const float2 y = row ? qr[x / 2] : kr[x / 2], z = row ? qr[x / 2 + 1] : kr[x / 2 + 1];
-                    if constexpr (kMma) {
-                        uint2 hi, lo;
-                        split2(y.x, y.y, hi.x, lo.x), split2(z.x, z.y, hi.y, lo.y);
-                        *reinterpret_cast<uint2 *>(xh + at * kPitch + 16 * x + 4 * l16) = hi;
-                        *reinterpret_cast<uint2 *>(xl + at * kPitch + 16 * x + 4 * l16) = lo;
-                    } else {
-                        *reinterpret_cast<float4 *>(xy + at * D + 16 * x + 4 * l16) = make_float4(y.x, y.y, z.x, z.y);
+                    for (int x = 0; x < C; x += 4) {
+                        const float2 y = row ? qr[x / 2] : kr[x / 2], z = row ? qr[x / 2 + 1] : kr[x / 2 + 1];
+                        if constexpr (kMma) {
+                            uint2 hi, lo;
+                            split2(y.x, y.y, hi.x, lo.x), split2(z.x, z.y, hi.y, lo.y);
+                            const int to = (((2 * x + l16 / 2) ^ (t & 7)) << 4) + l16 % 2 * 8;   // channels 16 x + 4 l16 and up
+                            *reinterpret_cast<uint2 *>(at + to) = hi;
+                            *reinterpret_cast<uint2 *>(at + P / 2 + to) = lo;
+                        } else {
+                            *reinterpret_cast<float4 *>(at + (16 * x + 4 * l16) * 4) = make_float4(y.x, y.y, z.x, z.y);
+                        }
                     }
                 }
-            }
         }
     }
-    // ---- their products with S_0, over them: row r of [A k | A q], column j at xy[r D + j]
+    __syncthreads();
+    // ---- their products with S_0: of A k over k, of A q over alpha
     if constexpr (kMma) {
         // A warp takes 16 columns (two tiles of 8, their columns in turn).  Both operands in two bf16 terms, three of
         // the four products: 16 bits of either, 2^-8 of an output's own rounding.
-        constexpr int kCols = D / 16, kHalves = kWarps / kCols;   // d = 64: two warps a 16 columns, each half of the rows
+        constexpr int kCols = D / 16, kSplit = kWarps / kCols;    // d = 64: two warps a 16 columns, each half of the rows
+        constexpr int kMine = MT >= kSplit ? MT / kSplit : 1;     // tiles of rows
         const int w = warp % kCols, g = lane / 4, t4 = lane % 4;
-        constexpr int kMine = MT >= kHalves ? MT / kHalves : 1;   // tiles of rows
-        const int mt0 = MT >= kHalves ? warp / kCols * kMine : 0;
-        const bool works = MT >= kHalves || warp / kCols == 0;
-        float acc[kMine][2][4] = {};
-        __syncthreads();
-        if (works) {
-            const uint32_t at = ptx::smem_u32(xh + (mt0 * 16 + lane % 16) * kPitch + lane / 16 * 8);
-            constexpr uint32_t kLow = 2 * N * kPitch * 2;   // bytes from the upper terms to the lower ones
+        const int mt0 = MT >= kSplit ? warp / kCols * kMine : 0;
+        if (MT >= kSplit || warp < kCols) {
+            float acc[kMine][2][4] = {};
+            const uint32_t at = ptx::smem_u32(sm + L.xk) + (mt0 * 16 + lane % 16) * P;   // (xq follows xk)
 #pragma unroll
             for (int s = 0; s < D / 16; ++s) {
                 // rows 16 s + 2 t4, + 1, + 8, + 9 of S_0, columns 16 w + 2 g and the next
@@ -287,17 +343,18 @@ __global__ void __launch_bounds__(kThreads, MT <= 2 ? 3 : MT == 4 ? 2 : 1) verif
                     const int byte = (16 * s + 2 * t4 + (x & 1) + 8 * (x >> 1)) * D * 4 + (16 * w + 2 * g) * 4;
                     f[x] = __ldcs(reinterpret_cast<const float2 *>(unit[byte / kUnit] + byte % kUnit));
                 }
-                uint32_t hi[2][2], lo[2][2];                 // [tile][register]
+                uint32_t hi[2][2], lo[2][2];                      // [tile][register]
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     split2(f[2 * x].x, f[2 * x + 1].x, hi[0][x], lo[0][x]);
                     split2(f[2 * x].y, f[2 * x + 1].y, hi[1][x], lo[1][x]);
                 }
+                const uint32_t to = at + (((2 * s + lane / 16) ^ (lane & 7)) << 4);
 #pragma unroll
                 for (int mt = 0; mt < kMine; ++mt) {
                     uint32_t ah[4], as[4];
-                    ldsm4(ah, at + (mt * 16 * kPitch + 16 * s) * 2);
-                    ldsm4(as, at + (mt * 16 * kPitch + 16 * s) * 2 + kLow);
+                    ldsm4(ah, to + mt * 16 * P);
+                    ldsm4(as, to + mt * 16 * P + P / 2);
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
                         mma(acc[mt][y], as, hi[y][0], hi[y][1]);
@@ -306,15 +363,13 @@ __global__ void __launch_bounds__(kThreads, MT <= 2 ? 3 : MT == 4 ? 2 : 1) verif
                     }
                 }
             }
-        }
-        __syncthreads();
-        if (works)
 #pragma unroll
             for (int mt = 0; mt < kMine; ++mt)
 #pragma unroll
-                for (int x = 0; x < 2; ++x)   // columns 16 w + 4 t4 and up: tiles 0, 1, 0, 1
-                    *reinterpret_cast<float4 *>(xy + ((mt0 + mt) * 16 + g + 8 * x) * D + 16 * w + 4 * t4) =
+                for (int x = 0; x < 2; ++x)   // columns 16 w + 4 t4 and up: tiles 0, 1, 0, 1 (al follows kb)
+                    *reinterpret_cast<float4 *>(kb + ((mt0 + mt) * 16 + g + 8 * x) * D + 16 * w + 4 * t4) =
                         make_float4(acc[mt][0][2 * x], acc[mt][1][2 * x], acc[mt][0][2 * x + 1], acc[mt][1][2 * x + 1]);
+        }
         __syncthreads();
     } else {
         // a thread takes a column of S_0 and a part of its rows; eight rows of the products at a time
@@ -326,7 +381,6 @@ __global__ void __launch_bounds__(kThreads, MT <= 2 ? 3 : MT == 4 ? 2 : 1) verif
             const int byte = ((grp * R + i) * D + j) * 4;
             s[i] = __ldcs(reinterpret_cast<const float *>(unit[byte / kUnit] + byte % kUnit));
         }
-        __syncthreads();
 #pragma unroll 1
         for (int r0 = 0; r0 < 2 * N; r0 += 8) {
             if (r0 % N >= n) continue;                       // rows of no draft
@@ -334,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, MT <= 2 ? 3 : MT == 4 ? 2 : 1) verif
 #pragma unroll
             for (int x = 0; x < 8; ++x) {
                 y[x] = 0.f;
-                const float4 *v = reinterpret_cast<const float4 *>(xy + (r0 + x) * D + grp * R);
+                const float4 *v = reinterpret_cast<const float4 *>(xk + (r0 + x) * D + grp * R);
 #pragma unroll
                 for (int i = 0; i < R / 4; ++i) {
                     const float4 f = v[i];
@@ -349,36 +403,81 @@ __global__ void __launch_bounds__(kThreads, MT <= 2 ? 3 : MT == 4 ? 2 : 1) verif
                 for (int x = 0; x < 8; ++x) {
 #pragma unroll
                     for (int i = 0; i < G - 1; ++i) y[x] += part[(i * 8 + x) * D + j];
-                    xy[(r0 + x) * D + j] = y[x];
+                    kb[(r0 + x) * D + j] = y[x];
                 }
             __syncthreads();
         }
     }
-    // ---- u, column by column
+    // ---- u, column by column, eight drafts at a time; every draft before counts, with 0 where it is not on the branch.
+    // 0 times what is no number is none: a column with such a u is taken again, along the branches alone.
+    float *u = xk;
     const int j = tid % D, grp = tid / D;
+    auto add8 = [&](float2 (&acc)[4], const float *c, float x) {
+        const float4 c0 = *reinterpret_cast<const float4 *>(c), c1 = *reinterpret_cast<const float4 *>(c + 4);
+        const float2 xx = make_float2(x, x);
+        acc[0] = tcx::ffma2(make_float2(c0.x, c0.y), xx, acc[0]), acc[1] = tcx::ffma2(make_float2(c0.z, c0.w), xx, acc[1]);
+        acc[2] = tcx::ffma2(make_float2(c1.x, c1.y), xx, acc[2]), acc[3] = tcx::ffma2(make_float2(c1.z, c1.w), xx, acc[3]);
+    };
     if (grp == 0) {
+        bool strange = false;
 #pragma unroll 1
-        for (int t = 0; t < n; ++t) {
-            float acc = xy[t * D + j];
-            const float *c = ck + t * (t + 1) / 2;
-            for (uint64_t m = mask[t] & ~(1ull << t); m; m &= m - 1) {
-                const int i = __ffsll((long long)m) - 1;
-                acc = fmaf(c[i], u[i * D + j], acc);
+        for (int t0 = 0; t0 < n; t0 += 8) {
+            float2 acc[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) acc[x] = make_float2(kb[(t0 + 2 * x) * D + j], kb[(t0 + 2 * x + 1) * D + j]);
+#pragma unroll 4
+            for (int i = 0; i < t0; ++i) add8(acc, ck + i * N + t0, u[i * D + j]);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                if (t0 + x >= n) break;
+                const float y = beta[t0 + x] * (vb[(t0 + x) * D + j] - (x & 1 ? acc[x / 2].y : acc[x / 2].x));
+                u[(t0 + x) * D + j] = y;
+                strange |= !(fabsf(y) < INFINITY);
+                if (x < 7) add8(acc, ck + (t0 + x) * N + t0, y);
             }
-            u[t * D + j] = beta[t] * (u[t * D + j] - acc);
         }
+        if (strange)
+#pragma unroll 1
+            for (int t = 0; t < n; ++t) {
+                float acc = kb[t * D + j];
+                for (uint64_t m = mask[t] & ~(1ull << t); m; m &= m - 1) {
+                    const int i = __ffsll((long long)m) - 1;
+                    acc = fmaf(ck[i * N + t], u[i * D + j], acc);
+                }
+                u[t * D + j] = beta[t] * (vb[t * D + j] - acc);
+            }
     }
     __syncthreads();
+    // ---- and o
+    T *o = static_cast<T *>(a.o) + row0 + j;
+    bool strange = false;
 #pragma unroll 1
-    for (int t = grp; t < n; t += kThreads / D) {
-        float acc = xy[(N + t) * D + j];
-        const float *c = cq + t * (t + 1) / 2;
-        for (uint64_t m = mask[t]; m; m &= m - 1) {
-            const int i = __ffsll((long long)m) - 1;
-            acc = fmaf(c[i], u[i * D + j], acc);
+    for (int t0 = 8 * grp; t0 < n; t0 += 8 * (kThreads / D)) {
+        float2 acc[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) acc[x] = make_float2(al[(t0 + 2 * x) * D + j], al[(t0 + 2 * x + 1) * D + j]);
+        const int end = min(t0 + 8, n);
+#pragma unroll 4
+        for (int i = 0; i < end; ++i) {
+            const float y = u[i * D + j];
+            strange |= !(fabsf(y) < INFINITY);
+            add8(acc, cq + i * N + t0, y);
         }
-        st_elem(static_cast<T *>(a.o) + ((r.first + t) * a.H + h) * D + j, acc);
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+            if (t0 + x < n) st_elem(o + (t0 + x) * a.H * D, x & 1 ? acc[x / 2].y : acc[x / 2].x);
     }
+    if (strange)
+#pragma unroll 1
+        for (int t = 0; t < n; ++t) {
+            if (t / 8 % (kThreads / D) != grp) continue;
+            float acc = al[t * D + j];
+            for (uint64_t m = mask[t]; m; m &= m - 1) {
+                const int i = __ffsll((long long)m) - 1;
+                acc = fmaf(cq[i * N + t], u[i * D + j], acc);
+            }
+            st_elem(o + t * a.H * D, acc);
+        }
 }
 
 // The state after the accepted branch: decode steps of its drafts one after another with the state in registers,
