@@ -64,6 +64,11 @@ __device__ __forceinline__ const uint8_t *raw_at(const VerifyTreeArgs &a, const 
     return static_cast<const uint8_t *>(x) + ((row * a.H + h) * d + c) * es;
 }
 
+// Ask a run of memory into L2: 16-byte aligned, bytes a multiple of 16.
+__device__ __forceinline__ void prefetch_bulk(const void *p, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(reinterpret_cast<uint64_t>(p)), "r"(bytes) : "memory");
+}
+
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kUnit = 256;   // bytes of a record that lie in one page: pages and records are multiples of it
 
@@ -71,6 +76,7 @@ constexpr int kUnit = 256;   // bytes of a record that lie in one page: pages an
 template <int D>
 struct Lay {
     static constexpr int P = D * 4;   // of a draft's row
+
     int kb, al, xk, xq, v, ck, cq, part, unit, tab, mask, beta, total;
     __host__ __device__ explicit Lay(int N) {
         int at = 0;
@@ -83,7 +89,7 @@ struct Lay {
         xk = take(N * P), xq = take(N * P);       // A k and A q: two bf16 terms or fp32; xk then holds u, xq held q
         v = take(N * P);
         ck = take(N * N * 4), cq = take(N * N * 4);   // c_ti at [i][t], 0 where i is not on t's branch
-        part = take((kThreads / D - 1) * 8 * D * 4);
+        part = take(6144);                // the convolution's weights, then (fp32) sums of the products' parts
         unit = take(D * D * 4 / kUnit * 8);       // addresses of S_0
         tab = take(N * 16), mask = take(N * 8), beta = take(N * 4);
         total = at;
@@ -107,21 +113,31 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t 
     const float2 h = tcx::bf2_to_f2(hi);
     lo = tcx::f2_to_bf2(x - h.x, y - h.y);
 }
-// The elements of a 16-byte unit, in pairs.
-__device__ __forceinline__ void pairs_of(const uint4 &u, float2 (&x)[2]) {
-    x[0] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
-    x[1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
-}
-__device__ __forceinline__ void pairs_of(const uint4 &u, float2 (&x)[4]) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// W elements as they lie in memory, and in pairs.
+template <int BYTES>
+struct Bits {
+    using type = uint4;
+};
+template <>
+struct Bits<8> {
+    using type = uint2;
+};
+template <class T, int W>
+__device__ __forceinline__ void pairs_of(const typename Bits<W * sizeof(T)>::type &u, float2 (&x)[W / 2]) {
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(&u);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = tcx::bf2_to_f2(w[i]);
+    for (int i = 0; i < W / 2; ++i)
+        x[i] = sizeof(T) == 2 ? tcx::bf2_to_f2(w[i]) : make_float2(__uint_as_float(w[2 * i % (W * sizeof(T) / 4)]), __uint_as_float(w[(2 * i + 1) % (W * sizeof(T) / 4)]));
 }
+
+// CTAs an SM: a CTA's chain of loads and steps is long, and others' work covers it.
+template <int D, class T, int MT>
+constexpr int kPerSm = MT == 8 ? 1 : MT == 4 || (D == 128 && sizeof(T) == 4) ? 2 : 4;
 
 // MT: tiles of 16 rows of [A k | A q], of up to 8 MT drafts.
 template <int D, class T, int MT>
-__global__ void __launch_bounds__(kThreads, MT <= 2 ? 3 : MT == 4 ? 2 : 1) verify_tree_kernel(const __grid_constant__ VerifyTreeArgs a) {
-    constexpr int V = kVec<T>, N = 8 * MT, P = Lay<D>::P;
+__global__ void __launch_bounds__(kThreads, kPerSm<D, T, MT>) verify_tree_kernel(const __grid_constant__ VerifyTreeArgs a) {
+    constexpr int N = 8 * MT, P = Lay<D>::P;
     constexpr bool kMma = sizeof(T) == 2;
     extern __shared__ __align__(16) uint8_t sm[];
     const Lay<D> L(N);
@@ -151,8 +167,17 @@ __global__ void __launch_bounds__(kThreads, MT <= 2 ? 3 : MT == 4 ? 2 : 1) verif
     for (int i = tid; i < D * D * 4 / kUnit; i += kThreads) {
         const uint8_t *at = obj_addr(a.pool, pages, rec + (uint64_t)i * kUnit, nullptr);
         unit[i] = at;
-        if (at) ptx::prefetch_l2(at), ptx::prefetch_l2(at + 128);
     }
+    {   // page by page
+        const uint64_t pb = (uint64_t)a.pool.page_bytes, end = rec + (uint64_t)D * D * 4;
+        for (uint64_t i = rec / pb + tid; i * pb < end; i += kThreads) {
+            const int32_t id = __ldg(pages + i);
+            const uint64_t from = i * pb > rec ? i * pb : rec, to = (i + 1) * pb < end ? (i + 1) * pb : end;
+            if ((uint32_t)id < (uint32_t)a.pool.num_pages) prefetch_bulk(a.pool.base + (uint64_t)id * pb + (from - i * pb), (uint32_t)(to - from));
+        }
+    }
+    for (int i = tid; i < 3 * D; i += kThreads)   // a channel's four taps; eight channels' places in other banks for each eight
+        reinterpret_cast<float4 *>(part)[i ^ (i >> 3 & 7)] = __ldg(reinterpret_cast<const float4 *>(a.conv_w) + (int64_t)h * 3 * D + i);
     for (int i = tid; i < N * N / 2; i += kThreads) reinterpret_cast<float4 *>(ck)[i] = make_float4(0.f, 0.f, 0.f, 0.f);   // cq too
     // ---- by the last warp: branches, by pointer doubling as in the plan, and the rows that a convolution reads: the
     // draft's own and the three before it, in bytes from the first draft's; ~w for the window's row w
@@ -207,55 +232,60 @@ __global__ void __launch_bounds__(kThreads, MT <= 2 ? 3 : MT == 4 ? 2 : 1) verif
     }
     // ---- convolutions along the branches; alpha
     {
-        constexpr int kGroups = 3 * D / V, kAt = kThreads / kGroups;   // drafts at a time
-        const int g = tid % kGroups, c = g * V % D, which = g * V / D;
+        // W channels a thread: few where the registers are for other CTAs (16 drafts 338 us with 8, 308 with 4), many
+        // where there are many drafts (64 x 64 drafts: 550 and 688)
+        constexpr int W = MT >= 4 ? 16 / (int)sizeof(T) : 4;
+        using Q = typename Bits<W * sizeof(T)>::type;
+        constexpr int kGroups = 3 * D / W, kAt = kThreads / kGroups;   // drafts at a time
+        const int g = tid % kGroups, c = g * W % D, which = g * W / D;
         const void *tensor = which == 0 ? a.q : which == 1 ? a.k : a.v;
         const uint8_t *src = static_cast<const uint8_t *>(tensor) + (row0 + c) * (int)sizeof(T);
         float *dst = (which == 0 ? xq : which == 1 ? kb : vb) + c;
         if (tid / kGroups < kAt) {
-            float2 w[4][V / 2];
-            uint4 win[3];
-#pragma unroll
-            for (int x = 0; x < V; x += 2) {
-                const float4 *f = reinterpret_cast<const float4 *>(a.conv_w + ((int64_t)h * 3 * D + which * D + c + x) * 4);
-                const float4 y = __ldg(f), z = __ldg(f + 1);
-                w[0][x / 2] = make_float2(y.x, z.x), w[1][x / 2] = make_float2(y.y, z.y);
-                w[2][x / 2] = make_float2(y.z, z.z), w[3][x / 2] = make_float2(y.w, z.w);
-            }
+            Q win[3];
 #pragma unroll
             for (int x = 0; x < 3; ++x)
-                win[x] = *reinterpret_cast<const uint4 *>(obj_addr(a.pool, pages, win_off + ((uint64_t)x * 3 * D + which * D + c) * sizeof(T), nullptr));
+                win[x] = *reinterpret_cast<const Q *>(obj_addr(a.pool, pages, win_off + ((uint64_t)x * 3 * D + W * g) * sizeof(T), nullptr));
+            float2 w[4][W / 2];
+#pragma unroll
+            for (int x = 0; x < W / 2; ++x) {
+                const int i = W * g + 2 * x;
+                const float4 y = reinterpret_cast<const float4 *>(part)[i ^ (i >> 3 & 7)];
+                const float4 z = reinterpret_cast<const float4 *>(part)[(i + 1) ^ (i >> 3 & 7)];
+                w[0][x] = make_float2(y.x, z.x), w[1][x] = make_float2(y.y, z.y);
+                w[2][x] = make_float2(y.z, z.z), w[3][x] = make_float2(y.w, z.w);
+            }
             for (int t = tid / kGroups; t < n; t += kAt) {
                 const int4 rows = tab[t];
                 const int32_t o[4] = {rows.w, rows.z, rows.y, rows.x};
-                uint4 z[4];
+                Q z[4];
 #pragma unroll
                 for (int tap = 0; tap < 4; ++tap) {
-                    if (o[tap] >= 0) z[tap] = __ldg(reinterpret_cast<const uint4 *>(src + o[tap]));
+                    if (o[tap] >= 0) z[tap] = __ldg(reinterpret_cast<const Q *>(src + o[tap]));
                     else z[tap] = o[tap] == ~2 ? win[2] : o[tap] == ~1 ? win[1] : win[0];
                 }
-                float2 y[V / 2];
+                float2 y[W / 2];
 #pragma unroll
-                for (int x = 0; x < V / 2; ++x) y[x] = make_float2(0.f, 0.f);
+                for (int x = 0; x < W / 2; ++x) y[x] = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int tap = 3; tap >= 0; --tap) {
-                    float2 f[V / 2];
-                    pairs_of(z[tap], f);
+                    float2 f[W / 2];
+                    pairs_of<T, W>(z[tap], f);
 #pragma unroll
-                    for (int x = 0; x < V / 2; ++x) y[x] = tcx::ffma2(w[tap][x], f[x], y[x]);
+                    for (int x = 0; x < W / 2; ++x) y[x] = tcx::ffma2(w[tap][x], f[x], y[x]);
                 }
 #pragma unroll
-                for (int x = 0; x < V; x += 4)
+                for (int x = 0; x < W; x += 4)
                     *reinterpret_cast<float4 *>(dst + t * D + x) = make_float4(y[x / 2].x, y[x / 2].y, y[x / 2 + 1].x, y[x / 2 + 1].y);
             }
         }
         const uint8_t *alpha = static_cast<const uint8_t *>(a.alpha) + row0 * (int)sizeof(T);
-        for (int i = tid; i < n * (D / V); i += kThreads) {
-            const int t = i / (D / V), ch = i % (D / V) * V;
-            float2 f[V / 2];
-            pairs_of(__ldg(reinterpret_cast<const uint4 *>(alpha + (t * a.H * D + ch) * (int)sizeof(T))), f);
+        for (int i = tid; i < n * (D / W); i += kThreads) {
+            const int t = i / (D / W), ch = i % (D / W) * W;
+            float2 f[W / 2];
+            pairs_of<T, W>(__ldg(reinterpret_cast<const Q *>(alpha + (t * a.H * D + ch) * (int)sizeof(T))), f);
 #pragma unroll
-            for (int x = 0; x < V; x += 4)
+            for (int x = 0; x < W; x += 4)
                 *reinterpret_cast<float4 *>(al + t * D + ch + x) = make_float4(f[x / 2].x, f[x / 2].y, f[x / 2 + 1].x, f[x / 2 + 1].y);
         }
     }
@@ -485,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, MT <= 2 ? 3 : MT == 4 ? 2 : 1) verif
 constexpr int kAccThreads = 512, kAccWarps = 16;
 
 template <int D, class T>
-__global__ void __launch_bounds__(kAccThreads) verify_tree_accept_kernel(const __grid_constant__ VerifyTreeArgs a, int N) {
+__global__ void __launch_bounds__(kAccThreads, 2) verify_tree_accept_kernel(const __grid_constant__ VerifyTreeArgs a, int N) {
     constexpr int V = kVec<T>, C3 = 3 * D, R = D / kAccWarps, C = D / 32;
     extern __shared__ __align__(16) uint8_t sm[];
     float *kb = reinterpret_cast<float *>(sm), *vb = kb + N * D, *al = vb + N * D, *red = al + N * D, *w = red + kAccWarps * D;
