@@ -634,6 +634,217 @@ __global__ void __launch_bounds__(kAccThreads, 2) verify_tree_accept_kernel(cons
     }
 }
 
+// The same for bf16 records of d = 128 in pages of at least 64 KiB, as a pipeline of bulk copies: one CTA an SM, three
+// slots of a record and its tokens; a warp looks branches up and copies records in and out, sixteen warps advance the
+// state of the one between, a thread 32 rows of a column in registers over the whole branch.
+constexpr int kPipeItems = 256;                       // (request, head) pairs from which it is taken
+constexpr int kPipe = 512, kPipeThreads = kPipe + 32, kSlots = 3;
+constexpr int kSlotTokens = 4;                        // a branch's tokens that come with the record; others are fetched
+constexpr uint32_t kRecBytes = 67840, kSlotBytes = kRecBytes + kSlotTokens * 1024;
+struct PipeJob {
+    int32_t item, m;                                  // m < 0: the end
+    int64_t first;
+    int32_t path[kMost];
+    float beta[kMost];
+};
+constexpr uint32_t kPipeRed = kSlots * kSlotBytes, kPipeX = kPipeRed + 2 * 4 * 128 * 4, kPipeA = kPipeX + 2 * 256 * 4,
+                   kPipeJobs = kPipeA + 2 * 128 * 4, kPipeMisc = kPipeJobs + kSlots * sizeof(PipeJob), kPipeSmem = kPipeMisc + 128;
+static_assert(kSlotBytes % 128 == 0 && kPipeSmem <= 227 * 1024, "shared memory");
+
+__global__ void __launch_bounds__(kPipeThreads, 1) verify_tree_accept_pipe_kernel(const __grid_constant__ VerifyTreeArgs a) {
+    using bf16 = __nv_bfloat16;
+    constexpr int D = 128, C3 = 3 * D;
+    extern __shared__ __align__(128) uint8_t sm[];
+    float *red = reinterpret_cast<float *>(sm + kPipeRed), *xb = reinterpret_cast<float *>(sm + kPipeX);
+    float *al = reinterpret_cast<float *>(sm + kPipeA);
+    PipeJob *jobs = reinterpret_cast<PipeJob *>(sm + kPipeJobs);
+    uint64_t *full = reinterpret_cast<uint64_t *>(sm + kPipeMisc), *done = full + kSlots;
+    volatile int *err = reinterpret_cast<volatile int *>(sm + kPipeMisc + 64), *go = err + 1;
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, total = a.B * a.H;
+    if (tid == 0) {
+        for (int i = 0; i < kSlots; ++i) {
+            ptx::mbar_init(&full[i], 1);
+            ptx::mbar_init(&done[i], 1);
+        }
+        *err = 0;
+        ptx::fence_mbar_init();
+    }
+    __syncthreads();
+    if (warp == kPipe / 32) {
+        // ------------------------------------------------------------------ branches and copies
+        auto pieces = [&](int item, auto &&fn) {      // of an item's record, at most one a page
+            const int32_t *pages = a.state_pages + (int64_t)(item / a.H) * a.pool.pages_per_object;
+            int64_t off = (int64_t)(item % a.H) * a.pool.rec_bytes;
+            for (uint32_t at = 0; at < kRecBytes;) {
+                const int64_t pi = off / a.pool.page_bytes, in = off - pi * a.pool.page_bytes;
+                const uint32_t len = (uint32_t)min((int64_t)(kRecBytes - at), a.pool.page_bytes - in);
+                fn(a.pool.base + (int64_t)__ldg(pages + pi) * a.pool.page_bytes + in, at, len);
+                off += len, at += len;
+            }
+        };
+        auto store = [&](int n) {                     // job n's record back to its pages, by lane 0
+            const int s = n % kSlots;
+            pieces(jobs[s].item, [&](uint8_t *p, uint32_t at, uint32_t len) { ptx::bulk_store(p, sm + s * kSlotBytes + at, len); });
+            ptx::bulk_commit();
+        };
+        int n = 0;                                    // jobs
+        bool ok = true;
+        // a slot for job n: the record that used it goes back first
+        auto slot = [&]() {
+            int stop = 0;
+            if (lane == 0 && n >= kSlots) {
+                if (!ptx::mbar_wait(&done[n % kSlots], (uint32_t)((n / kSlots - 1) & 1), err)) stop = 1;
+                else {
+                    store(n - kSlots);
+                    ptx::bulk_wait_read0();
+                }
+            }
+            return __shfl_sync(0xFFFFFFFFu, stop, 0) == 0;
+        };
+        for (int item = blockIdx.x; item < total; item += gridDim.x) {
+            const int b = item / a.H, h = item % a.H;
+            const Request r = request_of(a, b);
+            const int32_t m = __ldg(a.accepted + b);
+            bool lost = false;
+            for (int i = lane; i < a.pool.pages_per_object; i += 32)
+                lost |= (uint32_t)__ldg(a.state_pages + (int64_t)b * a.pool.pages_per_object + i) >= (uint32_t)a.pool.num_pages;
+            lost = __any_sync(0xFFFFFFFFu, lost);
+            int32_t p[2] = {-1, -1};
+            bool wrong = r.n < 0 || m < 0 || m > r.n;
+            if (!wrong) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    if (lane + 32 * x < m) p[x] = __ldg(a.path + r.first + lane + 32 * x);
+                const int32_t before = __shfl_up_sync(0xFFFFFFFFu, p[0], 1), half = __shfl_sync(0xFFFFFFFFu, p[0], 31);
+                const int32_t behind = __shfl_up_sync(0xFFFFFFFFu, p[1], 1);
+                bool off = lane < m && (p[0] < 0 || p[0] >= r.n || (lane && p[0] <= before));
+                off |= lane + 32 < m && (p[1] < 0 || p[1] >= r.n || p[1] <= (lane ? behind : half));
+                wrong = __any_sync(0xFFFFFFFFu, off);
+            }
+            if (wrong || (lost && m)) {
+                if (lane == 0 && h == 0) flag_status(a.status, wrong ? KDA_DEV_BAD_META : KDA_DEV_BAD_PAGE);
+                continue;
+            }
+            if (m == 0) continue;
+            float be[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+                be[x] = lane + 32 * x < m ? ld_elem(static_cast<const bf16 *>(a.beta) + (r.first + p[x]) * a.H + h) : 0.f;
+            ok = slot();
+            if (!ok) break;
+            PipeJob &jb = jobs[n % kSlots];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) jb.path[lane + 32 * x] = p[x], jb.beta[lane + 32 * x] = be[x];
+            if (lane == 0) jb.item = item, jb.m = m, jb.first = r.first;
+            __syncwarp();
+            if (lane == 0) {
+                uint64_t *bar = &full[n % kSlots];
+                uint8_t *dst = sm + n % kSlots * kSlotBytes;
+                const int toks = min(m, kSlotTokens);
+                ptx::mbar_arrive_expect_tx(bar, kRecBytes + toks * 1024);
+                pieces(item, [&](uint8_t *q, uint32_t at, uint32_t len) { ptx::bulk_load(dst + at, q, len, bar); });
+                for (int t = 0; t < toks; ++t) {
+                    const int64_t row = ((r.first + jb.path[t]) * a.H + h) * D;
+                    const void *src[4] = {a.q, a.k, a.v, a.alpha};
+                    for (int x = 0; x < 4; ++x)
+                        ptx::bulk_load(dst + kRecBytes + t * 1024 + x * 256, static_cast<const bf16 *>(src[x]) + row, 256, bar);
+                }
+            }
+            __syncwarp();
+            ++n;
+        }
+        if (ok && slot()) {                           // the end, and the last records back
+            if (lane == 0) {
+                jobs[n % kSlots].m = -1;
+                ptx::mbar_arrive(&full[n % kSlots]);
+                for (int i = max(0, n + 1 - kSlots); i < n; ++i) {
+                    if (!ptx::mbar_wait(&done[i % kSlots], (uint32_t)(i / kSlots & 1), err)) break;
+                    store(i);
+                }
+            }
+        }
+        if (lane == 0) {
+            ptx::bulk_wait0();
+            if (*err)                                 // leave no copy in flight
+                for (int i = max(0, n - kSlots); i < n; ++i)
+                    for (uint32_t k = 0; k < ptx::kSpinLimit && !ptx::mbar_try_wait(&full[i % kSlots], (uint32_t)(i / kSlots & 1)); ++k) {
+                    }
+        }
+    } else {
+        // ------------------------------------------------------------------ the states
+        const int j = tid % D, rq = tid / D;
+        auto meet = [&]() { tcx::named_bar(1, kPipe); };
+        for (int n = 0;; ++n) {
+            const int s = n % kSlots;
+            if (tid == 0) *go = ptx::mbar_wait(&full[s], (uint32_t)(n / kSlots & 1), err) && !*err;
+            meet();
+            if (!*go) break;
+            const PipeJob &jb = jobs[s];
+            const int m = jb.m;
+            if (m < 0) break;
+            uint8_t *slot = sm + s * kSlotBytes;
+            float *S = reinterpret_cast<float *>(slot);
+            bf16 *win = reinterpret_cast<bf16 *>(slot + D * D * 4);
+            const bf16 *tok = reinterpret_cast<const bf16 *>(slot + kRecBytes);
+            const int h = jb.item % a.H;
+            float sv[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) sv[i] = S[(rq * 32 + i) * D + j];
+            // a thread a channel of q | k | v: the last three raw values; the others have alpha
+            const int c = tid;
+            bf16 p0{}, p1{}, p2{};
+            float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (c < C3) {
+                p0 = win[c], p1 = win[C3 + c], p2 = win[2 * C3 + c];
+                if (c >= D) w = __ldg(reinterpret_cast<const float4 *>(a.conv_w) + (int64_t)h * C3 + c);
+            }
+            const bf16 *mine = static_cast<const bf16 *>(rq == 0 ? a.q : rq == 1 ? a.k : rq == 2 ? a.v : a.alpha);
+#pragma unroll 1
+            for (int t = 0; t < m; ++t) {
+                const int par = t & 1;
+                const bf16 x = t < kSlotTokens ? tok[t * 512 + c] : mine[((jb.first + jb.path[t]) * a.H + h) * D + j];
+                if (c >= C3) {
+                    al[par * D + j] = __bfloat162float(x);
+                } else {
+                    if (c >= D)
+                        xb[par * 256 + c - D] = w.x * __bfloat162float(p0) + w.y * __bfloat162float(p1) + w.z * __bfloat162float(p2) +
+                                                w.w * __bfloat162float(x);
+                    p0 = p1, p1 = p2, p2 = x;
+                }
+                meet();
+                const float4 *k4 = reinterpret_cast<const float4 *>(xb + par * 256 + rq * 32), *a4 = reinterpret_cast<const float4 *>(al + par * D + rq * 32);
+                float acc = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float4 k = k4[i], f = a4[i];
+                    sv[4 * i] *= f.x, sv[4 * i + 1] *= f.y, sv[4 * i + 2] *= f.z, sv[4 * i + 3] *= f.w;
+                    acc = fmaf(k.x, sv[4 * i], acc), acc = fmaf(k.y, sv[4 * i + 1], acc);
+                    acc = fmaf(k.z, sv[4 * i + 2], acc), acc = fmaf(k.w, sv[4 * i + 3], acc);
+                }
+                float *sum = red + par * 4 * D;
+                sum[rq * D + j] = acc;
+                meet();
+                const float u = (sum[j] + sum[D + j]) + (sum[2 * D + j] + sum[3 * D + j]);
+                const float wj = jb.beta[t] * (xb[par * 256 + D + j] - u);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float4 k = k4[i];
+                    sv[4 * i] = fmaf(k.x, wj, sv[4 * i]), sv[4 * i + 1] = fmaf(k.y, wj, sv[4 * i + 1]);
+                    sv[4 * i + 2] = fmaf(k.z, wj, sv[4 * i + 2]), sv[4 * i + 3] = fmaf(k.w, wj, sv[4 * i + 3]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 32; ++i) S[(rq * 32 + i) * D + j] = sv[i];
+            if (c < C3) win[c] = p0, win[C3 + c] = p1, win[2 * C3 + c] = p2;
+            ptx::fence_proxy_async_smem();
+            meet();
+            if (tid == 0) ptx::mbar_arrive(&done[s]);
+        }
+    }
+    __syncthreads();
+    if (*err && tid == 0) flag_status(a.status, KDA_DEV_TIMEOUT);
+}
+
 template <int D, class T, int MT>
 cudaError_t verify_of(const VerifyTreeArgs &a, cudaStream_t st) {
     auto kern = verify_tree_kernel<D, T, MT>;
@@ -653,6 +864,13 @@ cudaError_t verify(const VerifyTreeArgs &a, cudaStream_t st) {
 
 template <int D, class T>
 cudaError_t accept(const VerifyTreeArgs &a, cudaStream_t st) {
+    if constexpr (D == 128 && sizeof(T) == 2)
+        if (a.pool.page_bytes >= 65536 && a.B * a.H >= kPipeItems) {
+            const cudaError_t e = cudaFuncSetAttribute(verify_tree_accept_pipe_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPipeSmem);
+            if (e != cudaSuccess) return e;
+            verify_tree_accept_pipe_kernel<<<(unsigned)min(a.B * a.H, kAttnSms), kPipeThreads, kPipeSmem, st>>>(a);
+            return cudaGetLastError();
+        }
     const int N = (a.max_q + 7) / 8 * 8;
     const int64_t smem = ((int64_t)3 * N * D + kAccWarps * D + D + 2 * kMost) * 4 + 9 * D * (int64_t)sizeof(T);
     auto kern = verify_tree_accept_kernel<D, T>;

@@ -620,6 +620,28 @@ def test_many_requests_and_heads():
             c.check_state(b, path)
 
 
+@pytest.mark.parametrize("page_bytes", [65536, 260 * 256, 1 << 20])
+def test_many_branches_beside_bad_ones(page_bytes):
+    """More (request, head) pairs than SMs: long and empty branches, requests without drafts, branches that are none and lost pages."""
+    c = States([(5 * b) % 23 + (40 if b == 7 else 0) for b in range(80)], H=4, d=128, chain=0.9, seed=49, page_bytes=page_bytes)
+    paths = [tree.random_path(c.r, p, 0.95) if b % 3 else [] for b, p in enumerate(c.parents)]
+    bad = [b for b in range(80) if c.sizes[b] > 3][4:8]
+    paths[bad[0]], paths[bad[1]] = [1, 0], [0, c.sizes[bad[1]]]
+    paths[bad[2]] = paths[bad[3]] = [0]
+    pages = c.pages.copy()
+    pages[bad[2], -1], pages[bad[3], 0] = c.pool.num_pages, -1
+    before = c.objects()
+    c.accept(paths, pages=pages)
+    assert kda.kda_sync_status(c.status) == (kda.KDA_EDEVICE, kda.KDA_DEV_BAD_META | kda.KDA_DEV_BAD_PAGE)
+    after = c.objects()
+    assert max(len(p) for p in paths) > 8
+    for b, path in enumerate(paths):
+        if path and b not in bad:
+            c.check_state(b, path)
+        else:
+            assert after[b] == before[b], b
+
+
 @pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f32", 64)])
 def test_a_chain_is_the_verify_step(dtype, d):
     K = 5
