@@ -198,6 +198,7 @@ class Pool:
         self.handle = h
         self.page_bytes = page_bytes
         self.num_pages = num_pages
+        self.widths = {}     # pages of an object, by (H, d, dtype)
         self.base = None
         if device is not None:
             import torch
@@ -692,20 +693,31 @@ def kda_attn_paged(pool: Pool, Hkv: int, fmt: int, page_tokens: int, cu_q, kv_le
 
 
 # ------------------------------------------------------------------------------ trees of drafts
+_int_types = ()      # (torch.int32, torch.int64), once a call has needed them
+
+
+def _types():
+    global _int_types
+    if not _int_types:
+        import torch
+        _int_types = torch.int32, torch.int64
+    return _int_types
+
+
 def _ints(t, n: int, gpu: int, what: str):
     """Device address of an int32 tensor of n elements."""
-    import torch
-    if t.dtype != torch.int32 or t.numel() != n:
+    if t.dtype is not (_int_types or _types())[0] or t.numel() != n:
         raise ValueError(f"{what} must be int32 with {n} elements")
-    return _address(t, gpu)
+    if t.get_device() != gpu or not t.is_contiguous():
+        raise ValueError("expected a contiguous tensor on the GPU of the call's tokens")
+    return t.data_ptr()
 
 
 def kda_tree_plan(cu_q, kv_len, parent, max_q: int, mask, pos, status, stream=None) -> None:
     """parent: int32 CUDA [T]; mask: int64 CUDA [T] (the bits of a uint64) and pos: int32 CUDA [T]
     are written."""
-    import torch
     T, gpu, nseq = parent.numel(), parent.get_device(), kv_len.numel()
-    if mask.dtype != torch.int64 or mask.numel() != T:
+    if mask.dtype is not _types()[1] or mask.numel() != T:
         raise ValueError("mask must be int64 [T]")
     if gpu < 0:
         raise ValueError("expected CUDA tensors")
@@ -747,14 +759,13 @@ def kda_attn_tree(pool: Pool, Hkv: int, fmt: int, page_tokens: int, cu_q, kv_len
                   stream=None) -> None:
     """mask: int64 CUDA [T] as kda_tree_plan writes it; pos: int32 CUDA [T], needed with a window;
     the rest as kda_attn_paged."""
-    import torch
     T, Hq, d = q.shape
     if o.shape != q.shape or o.dtype != q.dtype:
         raise ValueError("q and o differ in shape or type")
     _f32(lse, "lse")
     if lse is not None and lse.numel() != T * Hq:
         raise ValueError("lse must be [T, Hq]")
-    if mask.dtype != torch.int64 or mask.numel() != T:
+    if mask.dtype is not _types()[1] or mask.numel() != T:
         raise ValueError("mask must be int64 [T]")
     gpu = q.get_device()
     nseq, max_pages, cu, lens, table, word = _batch(cu_q, kv_len, page_table, status, gpu)
@@ -782,40 +793,37 @@ def kda_kv_accept(pool: Pool, Hkv: int, d: int, fmt: int, page_tokens: int, cu_q
         raise KdaError(rc, "kda_kv_accept")
 
 
-def _tree_tokens(cu_q, max_q: int, q, k, v, alpha, beta, conv_w, state_pages, status):
+def _tree_tokens(pool: Pool, cu_q, max_q: int, q, k, v, alpha, beta, conv_w, state_pages, status):
     """(leading arguments, addresses of the tokens, the state's) of the two calls on states."""
-    import torch
-    T, H, d = q.shape
-    gpu, dt = q.get_device(), q.dtype
+    shape, gpu, dt = q.shape, q.get_device(), q.dtype
+    T, H, d = shape
     if gpu < 0:
         raise ValueError("expected CUDA tensors")
-    for x in (k, v, alpha):
-        if x.shape != q.shape or x.dtype != dt:
-            raise ValueError("q, k, v and alpha differ in shape or type")
-    if beta.shape != (T, H) or beta.dtype != dt:
+    if (k.shape != shape or v.shape != shape or alpha.shape != shape or k.dtype is not dt or v.dtype is not dt
+            or alpha.dtype is not dt):
+        raise ValueError("q, k, v and alpha differ in shape or type")
+    if beta.shape != (T, H) or beta.dtype is not dt:
         raise ValueError("beta must be [T, H] of the tokens' type")
     _f32(conv_w, "conv_w")
     if conv_w.shape != (H, 3 * d, 4):
         raise ValueError("conv_w must be [H, 3 d, 4]")
-    B = cu_q.numel() - 1
-    if state_pages.dtype != torch.int32 or state_pages.dim() != 2 or state_pages.shape[0] != B:
-        raise ValueError("state_pages must be int32 [B, P]")
-    return ((H, d, dtype_of(q), B, T, max_q, _ints(cu_q, B + 1, gpu, "cu_q")),
-            (*(_address(x, gpu) for x in (q, k, v, alpha, beta)), _address(conv_w, gpu)),
-            (_address(state_pages, gpu), _ints(status, 1, gpu, "status")))
-
-
-def _state_width(pool: Pool, state_pages, shape) -> None:
-    if state_pages.shape[1] != kda_object_pages(pool, shape[0], shape[1], shape[2]):
-        raise ValueError("state_pages must be [B, kda_object_pages()]")
+    B, kind = cu_q.numel() - 1, dtype_of(q)
+    width = pool.widths.get((H, d, kind))
+    if width is None:
+        width = pool.widths[H, d, kind] = kda_object_pages(pool, H, d, kind)
+    if state_pages.dim() != 2 or state_pages.shape[0] != B or state_pages.shape[1] != width:
+        raise ValueError("state_pages must be int32 [B, kda_object_pages()]")
+    return ((H, d, kind, B, T, max_q, _ints(cu_q, B + 1, gpu, "cu_q")),
+            (_address(q, gpu), _address(k, gpu), _address(v, gpu), _address(alpha, gpu), _address(beta, gpu),
+             _address(conv_w, gpu)),
+            (_ints(state_pages, B * width, gpu, "state_pages"), _ints(status, 1, gpu, "status")))
 
 
 def kda_verify_tree(pool: Pool, cu_q, parent, max_q: int, q, k, v, alpha, beta, conv_w, o, state_pages, status,
                     stream=None) -> None:
     """q, k, v, alpha, o: [T, H, d]; beta: [T, H]; cu_q, parent: int32 CUDA [B + 1], [T]; state_pages:
     int32 CUDA [B, P], read only."""
-    head, tokens, state = _tree_tokens(cu_q, max_q, q, k, v, alpha, beta, conv_w, state_pages, status)
-    _state_width(pool, state_pages, head)
+    head, tokens, state = _tree_tokens(pool, cu_q, max_q, q, k, v, alpha, beta, conv_w, state_pages, status)
     if o.shape != q.shape or o.dtype != q.dtype:
         raise ValueError("q and o differ in shape or type")
     gpu = q.get_device()
@@ -829,8 +837,7 @@ def kda_verify_tree_accept(pool: Pool, cu_q, path, accepted, max_q: int, q, k, v
                            stream=None) -> None:
     """The tokens of kda_verify_tree; path: int32 CUDA [T], accepted: int32 CUDA [B].  The objects of
     state_pages advance in place."""
-    head, tokens, state = _tree_tokens(cu_q, max_q, q, k, v, alpha, beta, conv_w, state_pages, status)
-    _state_width(pool, state_pages, head)
+    head, tokens, state = _tree_tokens(pool, cu_q, max_q, q, k, v, alpha, beta, conv_w, state_pages, status)
     gpu = q.get_device()
     rc = (_lib or lib()).kda_verify_tree_accept(
         pool.handle, *head, _ints(path, q.shape[0], gpu, "path"), _ints(accepted, head[3], gpu, "accepted"), *tokens,

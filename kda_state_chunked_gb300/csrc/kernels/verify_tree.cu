@@ -168,9 +168,9 @@ __global__ void __launch_bounds__(kThreads, kPerSm<D, T, MT>) verify_tree_kernel
         const uint8_t *at = obj_addr(a.pool, pages, rec + (uint64_t)i * kUnit, nullptr);
         unit[i] = at;
     }
-    {   // page by page
+    if (warp == 0) {   // page by page
         const uint64_t pb = (uint64_t)a.pool.page_bytes, end = rec + (uint64_t)D * D * 4;
-        for (uint64_t i = rec / pb + tid; i * pb < end; i += kThreads) {
+        for (uint64_t i = rec / pb + lane; i * pb < end; i += 32) {
             const int32_t id = __ldg(pages + i);
             const uint64_t from = i * pb > rec ? i * pb : rec, to = (i + 1) * pb < end ? (i + 1) * pb : end;
             if ((uint32_t)id < (uint32_t)a.pool.num_pages) prefetch_bulk(a.pool.base + (uint64_t)id * pb + (from - i * pb), (uint32_t)(to - from));
@@ -352,7 +352,6 @@ __global__ void __launch_bounds__(kThreads, kPerSm<D, T, MT>) verify_tree_kernel
                 }
         }
     }
-    __syncthreads();
     // ---- their products with S_0: of A k over k, of A q over alpha
     if constexpr (kMma) {
         // A warp takes 16 columns (two tiles of 8, their columns in turn).  Both operands in two bf16 terms, three of
@@ -361,24 +360,31 @@ __global__ void __launch_bounds__(kThreads, kPerSm<D, T, MT>) verify_tree_kernel
         constexpr int kMine = MT >= kSplit ? MT / kSplit : 1;     // tiles of rows
         const int w = warp % kCols, g = lane / 4, t4 = lane % 4;
         const int mt0 = MT >= kSplit ? warp / kCols * kMine : 0;
-        if (MT >= kSplit || warp < kCols) {
+        const bool works = MT >= kSplit || warp < kCols;
+        // rows 16 s + 2 t4, + 1, + 8, + 9 of S_0, columns 16 w + 2 g and the next; two steps s are under way, the first
+        // ones while the other warps still walk
+        float2 f[2][4];
+        auto fetch = [&](int s, float2 (&y)[4]) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const int byte = (16 * s + 2 * t4 + (x & 1) + 8 * (x >> 1)) * D * 4 + (16 * w + 2 * g) * 4;
+                y[x] = __ldcs(reinterpret_cast<const float2 *>(unit[byte / kUnit] + byte % kUnit));
+            }
+        };
+        if (works) fetch(0, f[0]), fetch(1, f[1]);
+        __syncthreads();
+        if (works) {
             float acc[kMine][2][4] = {};
             const uint32_t at = ptx::smem_u32(sm + L.xk) + (mt0 * 16 + lane % 16) * P;   // (xq follows xk)
 #pragma unroll
             for (int s = 0; s < D / 16; ++s) {
-                // rows 16 s + 2 t4, + 1, + 8, + 9 of S_0, columns 16 w + 2 g and the next
-                float2 f[4];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const int byte = (16 * s + 2 * t4 + (x & 1) + 8 * (x >> 1)) * D * 4 + (16 * w + 2 * g) * 4;
-                    f[x] = __ldcs(reinterpret_cast<const float2 *>(unit[byte / kUnit] + byte % kUnit));
-                }
                 uint32_t hi[2][2], lo[2][2];                      // [tile][register]
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    split2(f[2 * x].x, f[2 * x + 1].x, hi[0][x], lo[0][x]);
-                    split2(f[2 * x].y, f[2 * x + 1].y, hi[1][x], lo[1][x]);
+                    split2(f[s & 1][2 * x].x, f[s & 1][2 * x + 1].x, hi[0][x], lo[0][x]);
+                    split2(f[s & 1][2 * x].y, f[s & 1][2 * x + 1].y, hi[1][x], lo[1][x]);
                 }
+                if (s + 2 < D / 16) fetch(s + 2, f[s & 1]);
                 const uint32_t to = at + (((2 * s + lane / 16) ^ (lane & 7)) << 4);
 #pragma unroll
                 for (int mt = 0; mt < kMine; ++mt) {
@@ -411,6 +417,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm<D, T, MT>) verify_tree_kernel
             const int byte = ((grp * R + i) * D + j) * 4;
             s[i] = __ldcs(reinterpret_cast<const float *>(unit[byte / kUnit] + byte % kUnit));
         }
+        __syncthreads();
 #pragma unroll 1
         for (int r0 = 0; r0 < 2 * N; r0 += 8) {
             if (r0 % N >= n) continue;                       // rows of no draft
