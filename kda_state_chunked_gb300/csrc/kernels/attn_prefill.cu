@@ -144,6 +144,11 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
     return r;
 }
 
+// Ask a run of memory into L2: 16-byte aligned, bytes a multiple of 16.
+__device__ __forceinline__ void prefetch_bulk(const void *p, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(reinterpret_cast<uint64_t>(p)), "r"(bytes) : "memory");
+}
+
 // True in one lane of a converged warp.
 __device__ __forceinline__ bool elect() {
     uint32_t p;
@@ -993,6 +998,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                         jb.pmin = t.pmin, jb.pmax = t.pmax;
                         jb.nans = nans;
                     }
+                }
+                if (kTree && rec && k < now.n) {
+                    // Few rows leave little time a unit, and a unit's copies are under way for one unit's time alone: what
+                    // a job handed on needs is asked into L2, up to eight units before it is copied.
+                    constexpr int kLine = kRow < 128 ? kRow : 128;
+#pragma unroll
+                    for (int v = 0; v < 2; ++v)
+#pragma unroll
+                        for (int y = 0; y < kRow / kLine; ++y)
+                            prefetch_bulk(rec + v * pt * kRow + y * pt * kLine + now.slot * kLine, 16 * kLine);
                 }
                 __syncwarp();
                 if (lane % 8 == 0 && k < now.n) ptx::mbar_arrive(&bars[JFULL + (n + k) % kJobs]);
