@@ -726,7 +726,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
             return true;
         };
         bool ok = wait_all(JFULL, 0), stop = ok && (job(0).flags & kStop);
-        if (FMT == KDA_KV_I8 && ok && !stop) {
+        if (kTree && FMT == KDA_KV_I8 && ok && !stop) {
+            fetch(job(0), false, kc);
+            fetch(job(0), true, vc);
+        } else if (FMT == KDA_KV_I8 && ok && !stop) {
 #pragma unroll 1
             for (int v = 0; v < 2; ++v) {
 #pragma unroll
@@ -743,7 +746,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                 if (!ok) break;
                 ++n_item;
             }
-            if (FMT == KDA_KV_I8) {
+            if (kTree && FMT == KDA_KV_I8) {
+                // Few rows: keys and values in registers of their own.  Moving one up, as below, waits for it to land,
+                // which the time of a unit of a prompt hides.
+                ok = with_next(KEMPTY + st, par, n);
+                if (!ok) break;
+                put(kc, sm + L::k + st * L::tile);
+                ptx::fence_proxy_async_smem();
+                tcx::warp_arrive(&bars[KFULL + st]);
+                stop = job(n + 1).flags & kStop;
+                if (!stop) fetch(job(n + 1), false, kc);
+                ok = wait_all(VEMPTY + st, par);
+                if (!ok) break;
+                put(vc, sm + L::v + st * L::tile);
+                ptx::fence_proxy_async_smem();
+                tcx::warp_arrive(&bars[VFULL + st]);
+                if (!stop) fetch(job(n + 1), true, vc);
+            } else if (FMT == KDA_KV_I8) {
                 // keys, then values: kc goes out, vc moves up, the same of the next unit is fetched
 #pragma unroll 1
                 for (int v = 0; v < 2; ++v) {
