@@ -255,6 +255,9 @@ template <int FMT, int D>
 __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_constant__ AttnArgs a) {
     using L = Lay<D>;
     constexpr int kBlks = D / 64, kRow = kKvRow<FMT, D>;
+    // Trees over the 16-bit cache: probabilities in two bf16 terms, 16 bits, side by side in the columns of the scores
+    // that they come from (one term took the outputs from 1.7e-3 off to 2.3e-3; bytes and not products bound these).
+    constexpr bool kTwo = kTree && FMT == KDA_KV_BF16;
     static_assert(NBAR * 8 <= 512, "barriers");
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = ptx::smem_align1024(smem_raw);
@@ -505,10 +508,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
             auto weigh = [&](auto all) {
                 groups([&](const float (&x)[16], int c) {
                     const int k = decltype(all)::value ? kEvery : kind(c);
-                    float p[8];
+                    float p[8], low[8];
                     if (k == kNone) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) p[i] = 0.f;
+                        for (int i = 0; i < 8; ++i) p[i] = low[i] = 0.f;
                     } else {
                         const uint32_t see = k == kEvery ? ~0u : seen(c);
                         float fk = f_row, bias = -ms, back = 1.f;
@@ -531,6 +534,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                             }
                             part = tcx::fadd2(part, y);
                             p[i] = __uint_as_float(pack2<FMT>(y.x, y.y));
+                            if (kTwo) {
+                                const float2 z = tcx::bf2_to_f2(__float_as_uint(p[i]));
+                                low[i] = __uint_as_float(pack2<FMT>(y.x - z.x, y.y - z.y));
+                            }
                         }
                         l += (part.x + part.y) * back;
                         if (FMT == KDA_KV_I8 && (jb.nans >> (4 * side + c) & 1u)) {   // fp16 NaN where the row sees it
@@ -539,7 +546,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                                 p[i] = __uint_as_float((see & 1u << 2 * i ? 0x7E00u : 0u) | (see & 2u << 2 * i ? 0x7E000000u : 0u));
                         }
                     }
-                    ptx::tmem_st8(tS + 8 * c, p);
+                    ptx::tmem_st8(tS + (kTwo ? 16 : 8) * c, p);
+                    if (kTwo) ptx::tmem_st8(tS + 16 * c + 8, low);
                 });
             };
             if (flags & kWhole) weigh(std::true_type{});
@@ -835,9 +843,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
             auto outputs = [&](int half, int st) {
                 const uint64_t vd = ptx::sdesc_sw128(sb + L::v + st * L::tile, L::blk, 1024);
 #pragma unroll
-                for (int s = 0; s < kUnit / 16; ++s)   // probabilities: 32 columns in each half of the scores
-                    ptx::mma_bf16_ta(tu + 256 + half * 128, tu + half * 128 + (s >> 2) * 64 + (s & 3) * 8, vd + (s * 2048 >> 4),
-                                     idesc<FMT>(128, D, 1), 1u);
+                for (int s = 0; s < kUnit / 16; ++s) {   // probabilities: 32 columns (two terms: 64) in each half of the scores
+                    const uint32_t from = tu + half * 128 + (s >> 2) * 64 + (s & 3) * (kTwo ? 16 : 8);
+                    if (kTwo) ptx::mma_bf16_ta(tu + 256 + half * 128, from + 8, vd + (s * 2048 >> 4), idesc<FMT>(128, D, 1), 1u);
+                    ptx::mma_bf16_ta(tu + 256 + half * 128, from, vd + (s * 2048 >> 4), idesc<FMT>(128, D, 1), 1u);
+                }
             };
             // Wait for up to four barriers at once, lane i for the i-th: beside the other warps' work a wait
             // costs this one 250 cycles even where the barrier's phase is over, four of them a quarter of a unit.
