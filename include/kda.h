@@ -573,9 +573,10 @@ int kda_kv_append_at(const kda_pool *pool, int32_t Hq, int32_t Hkv, int32_t d, i
  *   pos           device int32 [T_tot]; read with a window only (NULL without one).  A position before base
  *                 or behind the last draft's place counts as that
  * Sequences with kv_len < n are skipped (KDA_DEV_BAD_META); a draft that sees nothing gets o = 0 and
- * lse = -infinity; one that sees an infinite value gets an infinity or NaN in that
- * column, and one that sees an infinite key may get NaN.  Workspace, types,
- * roundings, unseen infinities and NaN, and the same bits for the same call: as kda_attn_paged has them. */
+ * lse = -infinity; one that sees an infinite value gets an infinity or NaN in that column, and one that
+ * sees an infinite key may get NaN.  KDA_BF16 calls over KDA_KV_BF16 keep 16 bits of each probability.
+ * Workspace, types, other roundings, unseen infinities and NaN, and the same bits for the same call: as
+ * kda_attn_paged has them. */
 int64_t kda_attn_tree_workspace_bytes(int32_t Hq, int32_t Hkv, int32_t d, int32_t dtype, int32_t nseq, int64_t T_tot,
                                       int32_t max_q);
 int kda_attn_tree(const kda_pool *pool, int32_t Hq, int32_t Hkv, int32_t d, int32_t dtype, int32_t fmt,
@@ -586,8 +587,8 @@ int kda_attn_tree(const kda_pool *pool, int32_t Hq, int32_t Hkv, int32_t d, int3
                   void *stream);
 
 /* Keep the accepted branch in the cache: the keys and values of token base + path[i] move to place base + i
- * (base = kv_len - n, i < accepted), and kv_len_out (device int32 [nseq], apart from kv_len) receives base +
- * accepted.  What stands behind it afterwards is left over and counts for nothing.  Rows of the 16-bit cache
+ * (base = kv_len - n, i < accepted), and kv_len_out (device int32 [nseq], apart from kv_len and accepted) receives
+ * base + accepted.  What stands behind it afterwards is left over and counts for nothing.  Rows of the 16-bit cache
  * move as they are.  KDA_KV_I8: a block that takes in tokens of another block sets scale = max(max |x| / 127 over
  * those, the block's scale if a token stays in it: an older one, or an accepted one that it held already) and
  * codes as kda_kv_append does, x = code * scale in fp32; without such tokens its scale and codes stay.  The pages
@@ -609,9 +610,8 @@ int kda_kv_accept(const kda_pool *pool, int32_t Hkv, int32_t d, int32_t fmt, int
  *   cu_q             device int32 [B + 1]; a request may have no drafts
  *   parent           device int32 [T_tot]
  *   state_pages      device int32 [B * P], P = kda_object_pages(): read only
- * Sums and the products' operands are fp32 for KDA_F32.  KDA_BF16: see kda_verify_tree_accept for the state, which
- * keeps fp32; an answer's products with S_0 take either operand in two bf16 terms (16 bits), far below o's own
- * rounding.  A page id outside the pool sets KDA_DEV_BAD_PAGE and the request is skipped.  One launch. */
+ * Sums and the products' operands are fp32 for KDA_F32.  KDA_BF16: the products with S_0 take either operand in two
+ * bf16 terms (16 bits), far below o's own rounding; nothing of that enters a state (kda_verify_tree_accept).  A page id outside the pool sets KDA_DEV_BAD_PAGE and the request is skipped.  One launch. */
 int kda_verify_tree(const kda_pool *pool, int32_t H, int32_t d, int32_t dtype, int32_t B, int64_t T_tot, int32_t max_q,
                     const int32_t *cu_q, const int32_t *parent, const void *q, const void *k, const void *v,
                     const void *alpha, const void *beta, const float *conv_w, void *o, const void *pool_base,
@@ -619,7 +619,8 @@ int kda_verify_tree(const kda_pool *pool, int32_t H, int32_t d, int32_t dtype, i
 
 /* Advance each request's state and convolution window over its accepted branch, in place (decode steps without the
  * answers, the state read and written once; fp32 throughout).  The arguments are those of kda_verify_tree, the same
- * tokens among them.  A request that accepts nothing is left as it is.  One launch. */
+ * tokens among them; the objects of state_pages are private, each in the call once.  A request that accepts nothing is
+ * left as it is.  One launch. */
 int kda_verify_tree_accept(const kda_pool *pool, int32_t H, int32_t d, int32_t dtype, int32_t B, int64_t T_tot,
                            int32_t max_q, const int32_t *cu_q, const int32_t *path, const int32_t *accepted,
                            const void *q, const void *k, const void *v, const void *alpha, const void *beta,

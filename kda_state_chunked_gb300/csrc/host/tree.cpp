@@ -60,7 +60,7 @@ int kda_kv_accept(const kda_pool *pool, int32_t Hkv, int32_t d, int32_t fmt, int
     kda::KvAcceptArgs a{};
     if (!cache_view(pool, Hkv, d, fmt, page_tokens, pool_base, page_table, max_pages, status_dev, a.kv) ||
         !valid_trees(nseq, T_tot, max_q) || !cu_q || !kv_len || !accepted || !kv_len_out || (T_tot > 0 && !path) ||
-        overlap(kv_len, kv_len_out, (int64_t)nseq * 4) || 2 * (int64_t)nseq * Hkv > INT32_MAX)
+        overlap(kv_len, kv_len_out, (int64_t)nseq * 4) || overlap(accepted, kv_len_out, (int64_t)nseq * 4) || 2 * (int64_t)nseq * Hkv > INT32_MAX)
         return KDA_EINVAL;
     a.nseq = nseq; a.max_q = max_q; a.T_tot = T_tot;
     a.cu_q = cu_q; a.kv_len = kv_len; a.path = path; a.accepted = accepted; a.kv_len_out = kv_len_out;

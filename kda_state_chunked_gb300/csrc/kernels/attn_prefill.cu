@@ -35,6 +35,12 @@
 // (63% taken).  One pass over the scores instead of two wants 32 more registers than there are:
 // 20% slower, and 15% with registers taken from the other warps.
 //
+// Trees of drafts (compiled again, kTree): a job's pages are asked into L2 when it is handed on, keys and values of the
+// 8-bit cache have registers of their own, probabilities over the 16-bit cache two terms.  32 ragged contexts of 512 to
+// 32768 tokens, 32 heads (8 key/value), 16 drafts: 8-bit 512 us (618 without the first two), 16-bit 504 us (404 with one
+// term); 16 trees of 33 to 64 drafts behind 4096 to 16384 tokens, 16-bit: 205 us.  For up to 128 rows a form was built in
+// which the two halves take alternate units and join at an item's end: 608 us for the first, and not kept.
+//
 // 8-bit cache: as in the register kernel codes are exact in fp16 and query rows scaled by a power
 // of two; the key scale of each 16 tokens multiplies f, the value scale goes into the exponent:
 // p' = 2^(f S + log2 vs - b + 6), b a running bound of the row's own f S + log2 vs, and a group's sum

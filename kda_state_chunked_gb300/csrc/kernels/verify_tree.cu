@@ -11,9 +11,17 @@
 // tokens' bytes and the arithmetic alone, where a state a draft would be written and read again: 2 x 64 KiB a head.
 //
 // A CTA takes one (request, head):
-//   loads of S_0 are started;  masks of the branches, convolutions along them;
-//   a warp a draft walks its branch towards the root: c_ti, e_ti, A_t k_t, A_t q_t;
-//   the products with S_0;  then a thread a column solves for u, and all add up o.
+//   S_0 is asked into L2;  masks of the branches, convolutions along them;
+//   sixteen lanes a draft walk its branch towards the root: c_ti, e_ti, A_t k_t, A_t q_t;
+//   the products with S_0 (bf16 calls: warp-level matrix products, whose 16 rows fit 8 drafts' k and q; fp32 calls: FMA);
+//   then a thread a column solves for u, eight drafts at a time, and all add up o.
+//
+// Bound: the states' bytes for small trees, the walk and the solve (n^2) for large ones.  Measured, 256 requests x 32
+// heads of 128, bf16: trees of 16 drafts 302 us (floor 107: 36%), of 8 222 us, of 4 185 us; 64 requests x 64 drafts
+// 547 us.  fp32: 16 drafts 605 us; 48 requests x 16 heads of 64, 1 to 64 drafts, 101 us.  A CTA's chain of dependent
+// steps takes some 20 us and four a SM cover each other to 38% of the issue slots.  A thread a state element with
+// FMA took 1,462 us for the 16 drafts; branches as bit lists in the solve 478; asking the state of the item one wave
+// ahead into L2 cost 45 us and hid nothing.
 #include "common.cuh"
 #include "sm100_ptx.cuh"
 #include "tc_common.cuh"
@@ -518,7 +526,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm<D, T, MT>) verify_tree_kernel
 }
 
 // The state after the accepted branch: decode steps of its drafts one after another with the state in registers,
-// read and written once.  Warp w of 16 has D / 16 rows of S, a lane D / 32 columns.
+// read and written once.  Warp w of 16 has D / 16 rows of S, a lane D / 32 columns.  (The form for fp32, d = 64, small
+// pages and few items: 256 x 32 heads of 128, 2.5 tokens a branch, fp32: 269 us.)
 constexpr int kAccThreads = 512, kAccWarps = 16;
 
 template <int D, class T>
@@ -643,8 +652,11 @@ __global__ void __launch_bounds__(kAccThreads, 2) verify_tree_accept_kernel(cons
 
 // The same for bf16 records of d = 128 in pages of at least 64 KiB, as a pipeline of bulk copies: one CTA an SM, three
 // slots of a record and its tokens; a warp looks branches up and copies records in and out, sixteen warps advance the
-// state of the one between, a thread 32 rows of a column in registers over the whole branch.
-constexpr int kPipeItems = 256;                       // (request, head) pairs from which it is taken
+// state of the one between, a thread 32 rows of a column in registers over the whole branch.  Measured: 256 x 32 heads,
+// branches of 2.5 tokens: 216 us, 1.1 GB, 76% of the copy rate (339 us by the kernel above).
+// (request, head) pairs from which it is taken: with fewer there is nothing to copy beside the one at hand (16 pairs:
+// 10.8 us by the other, which has a CTA for each)
+constexpr int kPipeItems = 256;
 constexpr int kPipe = 512, kPipeThreads = kPipe + 32, kSlots = 3;
 constexpr int kSlotTokens = 4;                        // a branch's tokens that come with the record; others are fetched
 constexpr uint32_t kRecBytes = 67840, kSlotBytes = kRecBytes + kSlotTokens * 1024;

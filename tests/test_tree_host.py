@@ -79,7 +79,7 @@ def accept_args(**kw):
 
 @pytest.mark.parametrize("bad", [dict(pool=None), dict(Hkv=3), dict(d=96), dict(fmt=2), dict(pt=40), dict(nseq=0), dict(T=-1),
                                  dict(max_q=65), dict(cu=None), dict(kv_len=None), dict(table=None), dict(path=None),
-                                 dict(accepted=None), dict(out=None), dict(out=A), dict(out=A + 4), dict(kv_len=A + 4100),
+                                 dict(accepted=None), dict(out=None), dict(out=A), dict(out=A + 4), dict(kv_len=A + 4100), dict(accepted=A + 4092),
                                  dict(base=None), dict(base=A + 8), dict(status=None), dict(max_pages=-1)], ids=named)
 def test_accept_refuses(bad):
     pool, args = accept_args(**bad)
