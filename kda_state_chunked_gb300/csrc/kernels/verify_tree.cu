@@ -18,7 +18,7 @@
 //
 // Bound: the states' bytes for small trees, the walk and the solve (n^2) for large ones.  Measured, 256 requests x 32
 // heads of 128, bf16: trees of 16 drafts 302 us (floor 107: 36%), of 8 222 us, of 4 185 us; 64 requests x 64 drafts
-// 547 us.  fp32: 16 drafts 605 us; 48 requests x 16 heads of 64, 1 to 64 drafts, 101 us.  A CTA's chain of dependent
+// 547 us.  fp32: 16 drafts 605 us; 48 requests x 16 heads of 64, 1 to 64 drafts, 80 us.  A CTA's chain of dependent
 // steps takes some 20 us and four a SM cover each other to 38% of the issue slots.  A thread a state element with
 // FMA took 1,462 us for the 16 drafts; branches as bit lists in the solve 478; asking the state of the item one wave
 // ahead into L2 cost 45 us and hid nothing.
@@ -86,6 +86,13 @@ struct Lay {
     static constexpr int P = D * 4;   // of a draft's row
 
     int kb, al, xk, xq, v, ck, cq, part, unit, tab, mask, beta, total;
+    // c_ti, e_ti at row_at(N, i) + t, 0 where i is not on t's branch.  64 drafts at d = 64: only t from i's eight on, which
+    // makes room for a second CTA (48 fp32 trees of up to 64 drafts 101 -> 80 us); elsewhere it would cost 2 to 9%.
+    static __host__ __device__ constexpr bool packed(int N) { return D == 64 && N == 64; }
+    static __host__ __device__ constexpr int row_at(int N, int i) {
+        return packed(N) ? 8 * (N * (i / 8) - 4 * (i / 8) * (i / 8 - 1)) + i % 8 * (N - i / 8 * 8) - i / 8 * 8 : i * N;
+    }
+    static __host__ __device__ constexpr int coefs(int N) { return packed(N) ? 4 * N * (N / 8 + 1) : N * N; }
     __host__ __device__ explicit Lay(int N) {
         int at = 0;
         auto take = [&](int bytes) {
@@ -96,7 +103,7 @@ struct Lay {
         kb = take(N * P), al = take(N * P);       // k and alpha; when the branches are walked, the products with S_0
         xk = take(N * P), xq = take(N * P);       // A k and A q: two bf16 terms or fp32; xk then holds u, xq held q
         v = take(N * P);
-        ck = take(N * N * 4), cq = take(N * N * 4);   // c_ti at [i][t], 0 where i is not on t's branch
+        ck = take(coefs(N) * 4), cq = take(coefs(N) * 4);
         part = take(6144);                // the convolution's weights, then (fp32) sums of the products' parts
         unit = take(D * D * 4 / kUnit * 8);       // addresses of S_0
         tab = take(N * 16), mask = take(N * 8), beta = take(N * 4);
@@ -140,7 +147,7 @@ __device__ __forceinline__ void pairs_of(const typename Bits<W * sizeof(T)>::typ
 
 // CTAs an SM: a CTA's chain of loads and steps is long, and others' work covers it.
 template <int D, class T, int MT>
-constexpr int kPerSm = MT == 8 ? 1 : MT == 4 || (D == 128 && sizeof(T) == 4) ? 2 : 4;
+constexpr int kPerSm = MT == 8 ? D == 64 ? 2 : 1 : MT == 4 || (D == 128 && sizeof(T) == 4) ? 2 : 4;
 
 // MT: tiles of 16 rows of [A k | A q], of up to 8 MT drafts.
 template <int D, class T, int MT>
@@ -186,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm<D, T, MT>) verify_tree_kernel
     }
     for (int i = tid; i < 3 * D; i += kThreads)   // a channel's four taps; eight channels' places in other banks for each eight
         reinterpret_cast<float4 *>(part)[i ^ (i >> 3 & 7)] = __ldg(reinterpret_cast<const float4 *>(a.conv_w) + (int64_t)h * 3 * D + i);
-    for (int i = tid; i < N * N / 2; i += kThreads) reinterpret_cast<float4 *>(ck)[i] = make_float4(0.f, 0.f, 0.f, 0.f);   // cq too
+    for (int i = tid; i < Lay<D>::coefs(N) / 2; i += kThreads) reinterpret_cast<float4 *>(ck)[i] = make_float4(0.f, 0.f, 0.f, 0.f);   // cq too
     // ---- by the last warp: branches, by pointer doubling as in the plan, and the rows that a convolution reads: the
     // draft's own and the three before it, in bytes from the first draft's; ~w for the window's row w
     if (warp == kWarps - 1) {
@@ -331,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm<D, T, MT>) verify_tree_kernel
 #pragma unroll
                 for (int y = 2; y < 16; y <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, y);
                 if (m) {
-                    if (l16 < 2) (l16 ? cq : ck)[i * N + t] = sum;
+                    if (l16 < 2) (l16 ? cq : ck)[Lay<D>::row_at(N, i) + t] = sum;
 #pragma unroll
                     for (int x = 0; x < C / 2; ++x) kr[x] = tcx::fmul2(kr[x], f[x]), qr[x] = tcx::fmul2(qr[x], f[x]);
                     m &= ~(1ull << i);
@@ -471,14 +478,14 @@ __global__ void __launch_bounds__(kThreads, kPerSm<D, T, MT>) verify_tree_kernel
 #pragma unroll
             for (int x = 0; x < 4; ++x) acc[x] = make_float2(kb[(t0 + 2 * x) * D + j], kb[(t0 + 2 * x + 1) * D + j]);
 #pragma unroll 4
-            for (int i = 0; i < t0; ++i) add8(acc, ck + i * N + t0, u[i * D + j]);
+            for (int i = 0; i < t0; ++i) add8(acc, ck + Lay<D>::row_at(N, i) + t0, u[i * D + j]);
 #pragma unroll
             for (int x = 0; x < 8; ++x) {
                 if (t0 + x >= n) break;
                 const float y = beta[t0 + x] * (vb[(t0 + x) * D + j] - (x & 1 ? acc[x / 2].y : acc[x / 2].x));
                 u[(t0 + x) * D + j] = y;
                 strange |= !(fabsf(y) < INFINITY);
-                if (x < 7) add8(acc, ck + (t0 + x) * N + t0, y);
+                if (x < 7) add8(acc, ck + Lay<D>::row_at(N, t0 + x) + t0, y);
             }
         }
         if (strange)
@@ -487,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm<D, T, MT>) verify_tree_kernel
                 float acc = kb[t * D + j];
                 for (uint64_t m = mask[t] & ~(1ull << t); m; m &= m - 1) {
                     const int i = __ffsll((long long)m) - 1;
-                    acc = fmaf(ck[i * N + t], u[i * D + j], acc);
+                    acc = fmaf(ck[Lay<D>::row_at(N, i) + t], u[i * D + j], acc);
                 }
                 u[t * D + j] = beta[t] * (vb[t * D + j] - acc);
             }
@@ -506,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm<D, T, MT>) verify_tree_kernel
         for (int i = 0; i < end; ++i) {
             const float y = u[i * D + j];
             strange |= !(fabsf(y) < INFINITY);
-            add8(acc, cq + i * N + t0, y);
+            add8(acc, cq + Lay<D>::row_at(N, i) + t0, y);
         }
 #pragma unroll
         for (int x = 0; x < 8; ++x)
@@ -519,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm<D, T, MT>) verify_tree_kernel
             float acc = al[t * D + j];
             for (uint64_t m = mask[t]; m; m &= m - 1) {
                 const int i = __ffsll((long long)m) - 1;
-                acc = fmaf(cq[i * N + t], u[i * D + j], acc);
+                acc = fmaf(cq[Lay<D>::row_at(N, i) + t], u[i * D + j], acc);
             }
             st_elem(o + t * a.H * D, acc);
         }
