@@ -15,6 +15,15 @@
 namespace kda {
 namespace attn {
 
+// Trees of drafts are these kernels compiled again (attn_tree_decode.cu, attn_tree_prefill.cu), with masks in the place of
+// the causal rule.  Known when compiling: a branch on the call's mask in what follows, taken by the warp that walks the units,
+// cost the prompts' kernel registers (8-bit cache, 4096 tokens behind 12288: 1,103 us, 1,029 without).
+#ifdef KDA_ATTN_TREE
+constexpr bool kTree = true;
+#else
+constexpr bool kTree = false;
+#endif
+
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // Row tile rt of sequence s.  Row r of a sequence is (token r / G, head r % G of the group).
@@ -48,7 +57,7 @@ __device__ __forceinline__ Tile make_tile(const AttnArgs &a, int32_t s, const Kv
     t.row0 = rt * ROWS;
     t.nrows = min(ROWS, q.n * a.G - t.row0);
     const int32_t base = q.len - q.n;
-    if (a.mask) {                 // a tree's rows see what is before its drafts, and drafts by their own masks
+    if (kTree) {                  // a tree's rows see what is before its drafts, and drafts by their own masks
         t.pmin = base - 1;
         t.pmax = base + q.n - 1;
     } else {
@@ -171,7 +180,7 @@ struct Walk {
 
 __device__ __forceinline__ KvSeq seq_of(const AttnArgs &a, int s) {
     const KvSeq q = kv_seq(a.cu_q, a.kv_len, s, a.T_tot, a.max_q, a.kv);
-    if (a.mask && q.len < q.n) {  // drafts without a place
+    if (kTree && q.len < q.n) {   // drafts without a place
         flag_status(a.kv.status, KDA_DEV_BAD_META);
         return {0, 0, 0};
     }

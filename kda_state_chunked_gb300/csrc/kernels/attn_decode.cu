@@ -42,13 +42,6 @@ namespace {
 
 using namespace attn;
 
-// Trees of drafts are this kernel compiled again (attn_tree_decode.cu), with masks in the place of the causal rule.
-#ifdef KDA_ATTN_TREE
-constexpr bool kTree = true;
-#else
-constexpr bool kTree = false;
-#endif
-
 constexpr int kWarps = 4;                             // that compute; one more walks and copies
 constexpr float kPBits = 6.f;                         // bits that a probability is scaled up in fp16
 constexpr float kGrow = 8.f;                          // bits that a row's maximum may grow before O is rescaled

@@ -58,13 +58,6 @@ namespace {
 
 using namespace attn;
 
-// Trees of drafts are this kernel compiled again (attn_tree_prefill.cu), with masks in the place of the causal rule.
-#ifdef KDA_ATTN_TREE
-constexpr bool kTree = true;
-#else
-constexpr bool kTree = false;
-#endif
-
 constexpr int kRows = kAttnPrefillRows, kHalf = 128, kUnit = 128;
 constexpr int kSoftWarps = 16, kLoadWarps = 8, kMmaWarp = 24, kCopyWarp = 25, kWalkWarp = 26, kThreads = 28 * 32;
 constexpr float kGrow = 8.f;            // bits that a row's maximum may grow before O is rescaled
