@@ -534,13 +534,17 @@ int kda_attn_paged(const kda_pool *pool, int32_t Hq, int32_t Hkv, int32_t d, int
  * ascending; 0 <= accepted[s] <= n.  Trees, branches and lengths stay on the device: a round can be captured
  * in a graph and replayed on others of at most max_q drafts.  A sequence whose metadata is out of range (a
  * parent at or behind its draft or below -1, a path that does not ascend or leaves the tree, a length below n,
- * n > max_q) sets KDA_DEV_BAD_META and is skipped; what it owns stays as it was.  max_q is at most
- * KDA_TREE_MAX (KDA_EINVAL). */
+ * n > max_q) sets KDA_DEV_BAD_META and is skipped by every call that is given that metadata; what it owns stays
+ * as it was.  Parents are given to kda_tree_plan and kda_verify_tree alone: the plan of a tree with such a parent
+ * has no positions (below), so that kda_kv_append_at skips its tokens too, and kda_attn_tree's answers for it
+ * count for nothing.  Neither kda_kv_accept nor kda_verify_tree_accept sees parents: 0 accepted drafts leave such
+ * a sequence's cache and state as they were.  max_q is at most KDA_TREE_MAX (KDA_EINVAL). */
 #define KDA_TREE_MAX 64
 
 /* Masks and positions of the drafts: bit j of mask[t] (device uint64 [T_tot]) says that the draft of packed
  * row t is draft j or descends from it; pos[t] (device int32 [T_tot]) is kv_len - n + its depth, the tree's
- * roots having depth 0.  One launch. */
+ * roots having depth 0.  A tree with a parent that is none gets pos[t] = -1 and mask[t] = 0 in its rows, but for
+ * those whose pos is negative already, which are left as they are.  One launch. */
 int kda_tree_plan(int32_t nseq, int64_t T_tot, int32_t max_q, const int32_t *cu_q, const int32_t *kv_len,
                   const int32_t *parent, uint64_t *mask, int32_t *pos, int32_t *status_dev, void *stream);
 

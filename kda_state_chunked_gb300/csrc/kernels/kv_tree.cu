@@ -23,6 +23,8 @@ __global__ void __launch_bounds__(kTreeMost) tree_plan_kernel(TreePlanArgs a) {
     if (i < n) p = __ldg(a.parent + first + i);
     if (__syncthreads_or(p < -1 || (i < n && p >= i))) {
         if (i == 0) flag_status(a.status, KDA_DEV_BAD_META);
+        // the calls behind see no parents: what an earlier plan (or nobody) wrote here must not pass for this tree's
+        if (i < n && a.pos[first + i] >= 0) a.mask[first + i] = 0, a.pos[first + i] = -1;
         return;
     }
     uint64_t m = 1ull << i;

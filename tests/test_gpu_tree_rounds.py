@@ -1,0 +1,59 @@
+"""Rounds on trees of drafts through all calls: a tree that is none, and answers from the 8-bit cache."""
+import numpy as np
+import pytest
+import torch
+
+import kda_state_chunked_gb300 as kda
+from test_gpu_kv import DEV, i32
+from test_gpu_tree import OK, Round
+
+pytestmark = pytest.mark.gpu
+FMTS = [kda.KDA_KV_BF16, kda.KDA_KV_I8]
+
+
+def filled(fmt, starts, seed):
+    """A round's tensors behind contexts of `starts` tokens."""
+    c = Round(fmt, starts, seed=seed)
+    cu = np.concatenate([[0], np.cumsum(starts)])
+    x = torch.from_numpy(np.random.default_rng(seed).standard_normal((2, int(cu[-1]), c.Hkv, c.d)).astype(np.float32)).to(DEV, torch.bfloat16)
+    kda.kda_kv_append(c.pool, fmt, c.pt, i32(cu), i32(starts), c.table, max(starts), None, x[0], x[1], c.cs, None, c.status)
+    assert kda.kda_sync_status(c.status) == OK
+    return c
+
+
+def owned(c, s):
+    """Bytes of a sequence's pages: its cache and its state."""
+    return torch.cat([c.pool.page_view(int(p)) for p in list(c.table[s].cpu()) + list(c.pages[s])]).clone()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("bad", [0, 1, -2])          # draft 0's parent: itself, one behind it, none at all
+@pytest.mark.parametrize("left", ["another round's", "nobody's"])
+def test_a_tree_that_is_none_leaves_its_cache_and_state(fmt, bad, left):
+    """The append and the attention see masks and positions alone: what an earlier round left in them, or a buffer that
+    nobody wrote, must not pass for this tree's."""
+    starts = [3, 21, 33]
+    c, e = filled(fmt, starts, 53), filled(fmt, starts, 53)
+    for x in (c, e):
+        x.draft(74, starts)
+        x.accepted[1] = 0
+    if left == "nobody's":
+        c.mask.fill_(-1)
+        c.pos.fill_(5)
+    else:
+        base = c.pool.base.clone()
+        c.calls()
+        assert kda.kda_sync_status(c.status) == OK
+        c.pool.base.copy_(base)
+    first, end = int(c.cu_host[1]), int(c.cu_host[2])
+    c.parent[first] = bad
+    before = owned(c, 1)
+    c.calls()
+    e.calls()
+    assert kda.kda_sync_status(c.status) == (kda.KDA_EDEVICE, kda.KDA_DEV_BAD_META) and kda.kda_sync_status(e.status) == OK
+    assert torch.equal(owned(c, 1), before) and torch.equal(c.new_lens, e.new_lens) and int(c.new_lens[1]) == starts[1]
+    assert (c.pos[first:end] == -1).all() and (c.mask[first:end] == 0).all()
+    for s in (0, 2):
+        rows = slice(int(c.cu_host[s]), int(c.cu_host[s + 1]))
+        assert torch.equal(owned(c, s), owned(e, s))
+        assert torch.equal(c.o[rows], e.o[rows]) and torch.equal(c.o_rec[rows], e.o_rec[rows])
