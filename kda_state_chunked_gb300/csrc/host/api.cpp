@@ -46,6 +46,14 @@ int check_allocated(const kda_pool *p, const int32_t *ids, int64_t n) {
     return KDA_OK;
 }
 
+// Whether each of the n objects' lists of P pages is one stretch of the pool.
+bool pages_in_order(const int32_t *ids, int64_t n, int32_t P) {
+    for (int64_t i = 0; i < n; ++i)
+        for (int32_t p = 1; p < P; ++p)
+            if (ids[i * P + p] != ids[i * P] + p) return false;
+    return true;
+}
+
 // Workspace: [SeqMeta][CkptMeta][pages][split items][wave offsets] (the uploaded metadata),
 // then for the split path [operand images: 2 slots][wave state scratch][final windows].
 struct WsLayout {
@@ -114,6 +122,7 @@ PoolView pool_view(const kda_pool *p, void *base, int32_t H, int32_t d, int32_t 
     v.page_magic = p->page_bytes < ((int64_t)1 << 32)
                        ? (uint32_t)((((uint64_t)1 << 32) + (uint64_t)p->page_bytes - 1) / (uint64_t)p->page_bytes)
                        : 0u;
+    v.run_bytes = p->page_bytes;
     return v;
 }
 
@@ -324,6 +333,7 @@ int kda_prefill_varlen(kda_pool *pool, int32_t H, int32_t d, int32_t dtype, int3
     a.T_tot = T_tot;
     a.q = q; a.k = k; a.v = v; a.alpha = alpha; a.beta = beta; a.conv_w = conv_w; a.o = o;
     a.pool = kda::pool_view(pool, pool_base, H, d, dtype);
+    if (pages_in_order(pages.data(), nseq + (int64_t)n_ckpt, P)) a.pool.run_bytes = INT64_MAX;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     a.seqs = reinterpret_cast<const SeqMeta *>(ws);
     a.ckpts = reinterpret_cast<const CkptMeta *>(ws + L.o_ck);

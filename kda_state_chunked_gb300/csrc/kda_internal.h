@@ -47,6 +47,7 @@ struct PoolView {
     int64_t rec_bytes;   // bytes of one head record (multiple of 256)
     int32_t page_shift;  // log2(page_bytes) when that is a power of two, else -1
     uint32_t page_magic; // ceil(2^32 / page_bytes) for other sizes below 4 GiB, else 0
+    int64_t run_bytes;   // run_addr: a run of that many bytes or more has pages between its ends of which nothing is known
 };
 
 struct PrefillArgs {

@@ -43,3 +43,42 @@ def test_resumed_prefill_reads_and_writes_every_page_in_its_place():
         kda.kda_page_decref(pool, act)
         kda.kda_page_decref(pool, ck)
     assert torch.equal(got[0][0], got[1][0]) and got[0][1:] == got[1][1:]
+
+
+def shuffles(P, first, rng):
+    """Page lists of one object: in order, back to front, any order, and in order but for one page in the middle of every
+    three, four and seven, which is another's of those."""
+    whole = np.arange(first, first + P, dtype=np.int32)
+    out = [whole, whole[::-1].copy(), rng.permutation(whole)]
+    for step in (3, 4, 7):
+        at = np.arange(step // 2, P, step)
+        some = whole.copy()
+        some[at] = np.roll(whole[at], 1)
+        out.append(some)
+    return out
+
+
+@pytest.mark.parametrize("page", [256, 768, 1024, 2560, 8192, 16384, 20480])
+def test_any_order_of_pages_of_any_size(page):
+    P = policy.object_pages(H, D, "bf16", page)
+    pool = kda.Pool(page, 2 * P, DEV)
+    T = 200
+    tok = {k: v.to(DEV) for k, v in workloads.make_tokens(T, H, D, "bf16", 10, "cpu").items()}
+    S, win = random_state(H, D, "bf16", torch.Generator().manual_seed(10))
+    nb, want = policy.object_bytes(H, D, "bf16"), None
+    rng = np.random.default_rng(page)
+    for act, ck in zip(shuffles(P, 0, rng), shuffles(P, P, rng)):
+        kda.kda_page_claim(pool, act)
+        kda.kda_page_claim(pool, ck)
+        write_object(pool, act, S, win, "bf16")
+        ws = kda.prefill_workspace(tok["q"], [0, T], [512], 1, P)
+        st = torch.zeros(1, dtype=torch.int32, device=DEV)
+        o = torch.empty_like(tok["q"])
+        kda.kda_prefill_varlen(pool, [0, T], [512], [1], tok["q"], tok["k"], tok["v"], tok["alpha"], tok["beta"], tok["conv_w"], o, act,
+                               [0], [640], ck, ws, st)
+        assert kda.kda_sync_status(st) == (kda.KDA_OK, 0)
+        got = o, read_object_bytes(pool, act, nb), read_object_bytes(pool, ck, nb)
+        want = want or got
+        assert torch.equal(got[0], want[0]) and got[1:] == want[1:]
+        kda.kda_page_decref(pool, act)
+        kda.kda_page_decref(pool, ck)
