@@ -659,8 +659,10 @@ __global__ void __launch_bounds__(kAccThreads, 2) verify_tree_accept_kernel(cons
 
 // The same for bf16 records of d = 128 in pages of at least 64 KiB, as a pipeline of bulk copies: one CTA an SM, three
 // slots of a record and its tokens; a warp looks branches up and copies records in and out, sixteen warps advance the
-// state of the one between, a thread 32 rows of a column in registers over the whole branch.  Measured: 256 x 32 heads,
-// branches of 2.5 tokens: 216 us, 1.1 GB, 76% of the copy rate (339 us by the kernel above).
+// state of the one between, a thread 32 rows of a column in registers over the whole branch.  Measured: 256 requests x 32
+// heads, branches of 2.5 tokens (214 requests accept some): 216 us, 0.95 GB moved, 65% of the copy rate (339 us by the
+// kernel above); a job's meetings of sixteen warps, two a token, bound it.  8192 branches of 1, 4, 8, 16 and 64 tokens each:
+// 229, 270, 428, 860 and 3504 us (kernel above: 300, 461, 655, 1038 and 3619).
 // (request, head) pairs from which it is taken: with fewer there is nothing to copy beside the one at hand (16 pairs:
 // 10.8 us by the other, which has a CTA for each)
 constexpr int kPipeItems = 256;
@@ -776,6 +778,10 @@ __global__ void __launch_bounds__(kPipeThreads, 1) verify_tree_accept_pipe_kerne
                         ptx::bulk_load(dst + kRecBytes + t * 1024 + x * 256, static_cast<const bf16 *>(src[x]) + row, 256, bar);
                 }
             }
+            for (int i = 4 * kSlotTokens + lane; i < 4 * m; i += 32) {   // the other tokens are asked into L2
+                const void *src = i % 4 == 0 ? a.q : i % 4 == 1 ? a.k : i % 4 == 2 ? a.v : a.alpha;
+                prefetch_bulk(static_cast<const bf16 *>(src) + ((r.first + jb.path[i / 4]) * a.H + h) * D, 256);
+            }
             __syncwarp();
             ++n;
         }
@@ -825,10 +831,16 @@ __global__ void __launch_bounds__(kPipeThreads, 1) verify_tree_accept_pipe_kerne
                 if (c >= D) w = __ldg(reinterpret_cast<const float4 *>(a.conv_w) + (int64_t)h * C3 + c);
             }
             const bf16 *mine = static_cast<const bf16 *>(rq == 0 ? a.q : rq == 1 ? a.k : rq == 2 ? a.v : a.alpha);
+            // tokens two steps ahead: those that did not come with the record come from L2, which takes longer than a step
+            // (read where they are used, 8192 branches of 16 and 64 tokens take 995 and 3964 us, not 860 and 3504)
+            auto token = [&](int t) { return t < kSlotTokens ? tok[t * 512 + c] : __ldg(mine + ((jb.first + jb.path[t]) * a.H + h) * D + j); };
+            bf16 x1 = token(0), x2 = m > 1 ? token(1) : x1;
 #pragma unroll 1
             for (int t = 0; t < m; ++t) {
                 const int par = t & 1;
-                const bf16 x = t < kSlotTokens ? tok[t * 512 + c] : mine[((jb.first + jb.path[t]) * a.H + h) * D + j];
+                const bf16 x = x1;
+                x1 = x2;
+                if (t + 2 < m) x2 = token(t + 2);
                 if (c >= C3) {
                     al[par * D + j] = __bfloat162float(x);
                 } else {

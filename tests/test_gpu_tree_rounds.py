@@ -1,11 +1,12 @@
-"""Rounds on trees of drafts through all calls: a tree that is none, and answers from the 8-bit cache."""
+"""Rounds on trees of drafts through all calls, a tree that is none among them, and the largest calls of single ones."""
 import numpy as np
 import pytest
 import torch
 
 import kda_state_chunked_gb300 as kda
+import tree_ref as tree
 from test_gpu_kv import DEV, i32
-from test_gpu_tree import OK, Round
+from test_gpu_tree import OK, Round, States
 
 pytestmark = pytest.mark.gpu
 FMTS = [kda.KDA_KV_BF16, kda.KDA_KV_I8]
@@ -57,3 +58,15 @@ def test_a_tree_that_is_none_leaves_its_cache_and_state(fmt, bad, left):
         rows = slice(int(c.cu_host[s]), int(c.cu_host[s + 1]))
         assert torch.equal(owned(c, s), owned(e, s))
         assert torch.equal(c.o[rows], e.o[rows]) and torch.equal(c.o_rec[rows], e.o_rec[rows])
+
+
+# ------------------------------------------------------------------ the state after long branches
+@pytest.mark.parametrize("page_bytes", [65536, 1 << 20])
+def test_branches_of_every_length(page_bytes):
+    """1 to 64 accepted tokens: those that come with a record, and those behind them."""
+    c = States(list(range(1, 65)), H=4, d=128, chain=1.0, seed=55, page_bytes=page_bytes)
+    paths = [list(range(n)) if b % 2 else tree.random_path(c.r, p, 1.0) for b, (n, p) in enumerate(zip(c.sizes, c.parents))]
+    c.accept(paths)
+    assert kda.kda_sync_status(c.status) == OK
+    for b, path in enumerate(paths):
+        c.check_state(b, path)
