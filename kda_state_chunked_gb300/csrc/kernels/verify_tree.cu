@@ -666,6 +666,9 @@ __global__ void __launch_bounds__(kAccThreads, 2) verify_tree_accept_kernel(cons
 // (request, head) pairs from which it is taken: with fewer there is nothing to copy beside the one at hand (16 pairs:
 // 10.8 us by the other, which has a CTA for each)
 constexpr int kPipeItems = 256;
+// ... and up to which: a CTA goes over its requests one by one, and the warps that wait for one that accepts something give
+// up after some seconds; near 2^31 the count itself would wrap.  More records than 2^24 no memory holds.
+constexpr int kPipeMost = 1 << 24;
 constexpr int kPipe = 512, kPipeThreads = kPipe + 32, kSlots = 3;
 constexpr int kSlotTokens = 4;                        // a branch's tokens that come with the record; others are fetched
 constexpr uint32_t kRecBytes = 67840, kSlotBytes = kRecBytes + kSlotTokens * 1024;
@@ -903,7 +906,7 @@ cudaError_t verify(const VerifyTreeArgs &a, cudaStream_t st) {
 template <int D, class T>
 cudaError_t accept(const VerifyTreeArgs &a, cudaStream_t st) {
     if constexpr (D == 128 && sizeof(T) == 2)
-        if (a.pool.page_bytes >= 65536 && a.B * a.H >= kPipeItems) {
+        if (a.pool.page_bytes >= 65536 && a.B * a.H >= kPipeItems && a.B * a.H <= kPipeMost) {
             const cudaError_t e = cudaFuncSetAttribute(verify_tree_accept_pipe_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPipeSmem);
             if (e != cudaSuccess) return e;
             verify_tree_accept_pipe_kernel<<<(unsigned)min(a.B * a.H, kAttnSms), kPipeThreads, kPipeSmem, st>>>(a);

@@ -70,3 +70,17 @@ def test_branches_of_every_length(page_bytes):
     assert kda.kda_sync_status(c.status) == OK
     for b, path in enumerate(paths):
         c.check_state(b, path)
+
+
+@pytest.mark.parametrize("B", [1 << 24, (1 << 24) + 1])
+def test_millions_of_requests_of_which_two_accept(B):
+    c = States([1, 2], H=1, d=128, chain=1.0, seed=56, page_bytes=1 << 20)
+    one = dict(dtype=torch.int32, device=DEV)
+    cu, accepted, pages = torch.ones(B + 1, **one), torch.zeros(B, **one), torch.zeros(B, 1, **one)
+    cu[0], cu[-1] = 0, 3
+    accepted[0], accepted[-1] = 1, 2
+    pages[0], pages[-1] = i32(c.pages[0]), i32(c.pages[1])
+    kda.kda_verify_tree_accept(c.pool, cu, i32([0, 0, 1]), accepted, 2, *c.tokens(), pages, c.status)
+    assert kda.kda_sync_status(c.status) == OK
+    c.check_state(0, [0])
+    c.check_state(1, [0, 1])
