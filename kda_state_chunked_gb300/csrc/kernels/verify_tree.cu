@@ -533,8 +533,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm<D, T, MT>) verify_tree_kernel
 }
 
 // The state after the accepted branch: decode steps of its drafts one after another with the state in registers,
-// read and written once.  Warp w of 16 has D / 16 rows of S, a lane D / 32 columns.  (The form for fp32, d = 64, small
-// pages and few items: 256 x 32 heads of 128, 2.5 tokens a branch, fp32: 269 us.)
+// read and written once.  Warp w of 16 has D / 16 rows of S, a lane D / 32 columns.  (The form for fp32, d = 64 and
+// pages below 64 KiB: 256 x 32 heads of 128, 2.5 tokens a branch, fp32: 269 us.)
 constexpr int kAccThreads = 512, kAccWarps = 16;
 
 template <int D, class T>
@@ -663,11 +663,11 @@ __global__ void __launch_bounds__(kAccThreads, 2) verify_tree_accept_kernel(cons
 // heads, branches of 2.5 tokens (214 requests accept some): 216 us, 0.95 GB moved, 65% of the copy rate (339 us by the
 // kernel above); a job's meetings of sixteen warps, two a token, bound it.  8192 branches of 1, 4, 8, 16 and 64 tokens each:
 // 229, 270, 428, 860 and 3504 us (kernel above: 300, 461, 655, 1038 and 3619).
-// (request, head) pairs from which it is taken: with fewer there is nothing to copy beside the one at hand (16 pairs:
-// 10.8 us by the other, which has a CTA for each)
-constexpr int kPipeItems = 256;
-// ... and up to which: a CTA goes over its requests one by one, and the warps that wait for one that accepts something give
-// up after some seconds; near 2^31 the count itself would wrap.  More records than 2^24 no memory holds.
+// Taken for any number of (request, head) pairs up to kPipeMost.  With few pairs it is the faster one too, a token's step
+// being shorter (16 pairs with 1, 4, 16, 64 tokens: 7.2, 9.6, 19.3, 57.1 us, and 9.5, 12.9, 25.0, 76.7 by the kernel above;
+// 256 pairs: 9.8, 13.7, 33.1, 109 and 11.9, 17.7, 40.8, 136).  But a CTA goes over its requests one by one, and the warps
+// that wait for one that accepts something give up after some seconds; near 2^31 the count itself would wrap.  More records
+// than 2^24 no memory holds.
 constexpr int kPipeMost = 1 << 24;
 constexpr int kPipe = 512, kPipeThreads = kPipe + 32, kSlots = 3;
 constexpr int kSlotTokens = 4;                        // a branch's tokens that come with the record; others are fetched
@@ -906,7 +906,7 @@ cudaError_t verify(const VerifyTreeArgs &a, cudaStream_t st) {
 template <int D, class T>
 cudaError_t accept(const VerifyTreeArgs &a, cudaStream_t st) {
     if constexpr (D == 128 && sizeof(T) == 2)
-        if (a.pool.page_bytes >= 65536 && a.B * a.H >= kPipeItems && a.B * a.H <= kPipeMost) {
+        if (a.pool.page_bytes >= 65536 && a.B * a.H <= kPipeMost) {
             const cudaError_t e = cudaFuncSetAttribute(verify_tree_accept_pipe_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPipeSmem);
             if (e != cudaSuccess) return e;
             verify_tree_accept_pipe_kernel<<<(unsigned)min(a.B * a.H, kAttnSms), kPipeThreads, kPipeSmem, st>>>(a);
