@@ -1,20 +1,22 @@
-"""Rounds on trees of drafts through all calls, a tree that is none among them, and the largest calls of single ones."""
+"""Rounds on trees of drafts through all calls, a tree that is none among them, and the largest calls of single ones.
+
+Attention has the tolerance of test_gpu_kv, states that of test_gpu_tree; everything else is equal."""
 import numpy as np
 import pytest
 import torch
 
 import kda_state_chunked_gb300 as kda
 import tree_ref as tree
-from test_gpu_kv import DEV, i32
+from test_gpu_kv import DEV, TOL, i32
 from test_gpu_tree import OK, Round, States
 
 pytestmark = pytest.mark.gpu
 FMTS = [kda.KDA_KV_BF16, kda.KDA_KV_I8]
 
 
-def filled(fmt, starts, seed):
+def filled(fmt, starts, seed, kind=Round):
     """A round's tensors behind contexts of `starts` tokens."""
-    c = Round(fmt, starts, seed=seed)
+    c = kind(fmt, starts, seed=seed)
     cu = np.concatenate([[0], np.cumsum(starts)])
     x = torch.from_numpy(np.random.default_rng(seed).standard_normal((2, int(cu[-1]), c.Hkv, c.d)).astype(np.float32)).to(DEV, torch.bfloat16)
     kda.kda_kv_append(c.pool, fmt, c.pt, i32(cu), i32(starts), c.table, max(starts), None, x[0], x[1], c.cs, None, c.status)
@@ -58,6 +60,76 @@ def test_a_tree_that_is_none_leaves_its_cache_and_state(fmt, bad, left):
         rows = slice(int(c.cu_host[s]), int(c.cu_host[s + 1]))
         assert torch.equal(owned(c, s), owned(e, s))
         assert torch.equal(c.o[rows], e.o[rows]) and torch.equal(c.o_rec[rows], e.o_rec[rows])
+
+
+class Seen(Round):
+    """A round that also looks at the cache between the attention and the kept branch."""
+
+    def calls(self):
+        Hq, Hkv = self.Hq, self.Hkv
+        x, meta = self.x, (self.cu, self.lens, self.table, self.max_q)
+        kda.kda_tree_plan(self.cu, self.lens, self.parent, self.max_q, self.mask, self.pos, self.status)
+        kda.kda_kv_append_at(self.pool, self.fmt, self.pt, *meta, x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], self.cs, self.pos,
+                             [self.d // 2], self.q, self.status)
+        kda.kda_attn_tree(self.pool, Hkv, self.fmt, self.pt, *meta, self.mask, self.q, self.o, self.ws, self.status)
+        lens = [int(n) for n in self.lens.cpu()]
+        self.there = lens, *(t.double().cpu().numpy() for t in self.cached(lens))
+
+    def check_answers(self):
+        """o against a softmax in 64 bits over the values that the cache holds, by the branches of the trees themselves."""
+        lens, k, v = self.there
+        q, o = self.q.double().cpu().numpy(), self.o.double().cpu().numpy()
+        G, off = self.Hq // self.Hkv, np.concatenate([[0], np.cumsum(lens)])
+        worst = top = 0.0
+        for s, parent in enumerate(self.trees):
+            base = lens[s] - len(parent)
+            for i in range(len(parent)):
+                rows = off[s] + np.array(list(range(base)) + [base + j for j in sorted(tree.branch(parent, i))])
+                for h in range(self.Hq):
+                    x = k[rows, h // G] @ q[self.cu_host[s] + i, h] / self.d ** 0.5
+                    e = np.exp(x - x.max())
+                    want = e @ v[rows, h // G] / e.sum()
+                    worst, top = max(worst, np.abs(o[self.cu_host[s] + i, h] - want).max()), max(top, np.abs(want).max())
+        assert worst <= TOL["bf16"] * top, worst / top
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("max_q", [3, 24])           # 6 and 48 rows a head: either attention kernel
+def test_answers_of_a_round(fmt, max_q, monkeypatch):
+    monkeypatch.setattr(Seen, "max_q", max_q)
+    starts = [0, 1, 15, 16, 40, 130]
+    c = filled(fmt, starts, 57, Seen)
+    for seed in (75, 76):
+        c.draft(seed, starts)
+        c.calls()
+        assert kda.kda_sync_status(c.status) == OK
+        c.check_answers()
+
+
+def test_a_captured_round_over_the_8_bit_cache():
+    starts = [3, 1, 33]
+    c, e = filled(kda.KDA_KV_I8, starts, 58), filled(kda.KDA_KV_I8, starts, 58)
+    c.draft(77, starts)
+    side, base = torch.cuda.Stream(), c.pool.base.clone()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        c.calls()
+    torch.cuda.current_stream().wait_stream(side)
+    c.pool.base.copy_(base)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.calls()
+    lens = starts
+    for seed in (78, 79, 80):
+        for x in (c, e):
+            x.draft(seed, lens)
+        graph.replay()
+        e.calls()
+        assert kda.kda_sync_status(c.status) == OK and kda.kda_sync_status(e.status) == OK
+        T = c.cu_host[-1]
+        assert torch.equal(c.pool.base, e.pool.base) and torch.equal(c.new_lens, e.new_lens)
+        assert torch.equal(c.o[:T], e.o[:T]) and torch.equal(c.o_rec[:T], e.o_rec[:T])
+        lens = c.new_lens.cpu().numpy()
 
 
 # ------------------------------------------------------------------ the state after long branches
