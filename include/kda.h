@@ -614,8 +614,10 @@ int kda_kv_accept(const kda_pool *pool, int32_t Hkv, int32_t d, int32_t fmt, int
  *   cu_q             device int32 [B + 1]; a request may have no drafts
  *   parent           device int32 [T_tot]
  *   state_pages      device int32 [B * P], P = kda_object_pages(): read only
- * Sums and the products' operands are fp32 for KDA_F32.  KDA_BF16: the products with S_0 take either operand in two
- * bf16 terms (16 bits), far below o's own rounding; nothing of that enters a state (kda_verify_tree_accept).  A page id outside the pool sets KDA_DEV_BAD_PAGE and the request is skipped.  One launch. */
+ * Sums and the products' operands are fp32 for KDA_F32.  KDA_BF16: the products with S_0 take either operand in
+ * two bf16 terms, and are off by 3 x 2^-16 of the absolute sum of their terms: below o's own rounding unless o
+ * cancels to a hundredth of those terms.  Nothing of that enters a state (kda_verify_tree_accept).  A page id
+ * outside the pool sets KDA_DEV_BAD_PAGE and the request is skipped.  One launch. */
 int kda_verify_tree(const kda_pool *pool, int32_t H, int32_t d, int32_t dtype, int32_t B, int64_t T_tot, int32_t max_q,
                     const int32_t *cu_q, const int32_t *parent, const void *q, const void *k, const void *v,
                     const void *alpha, const void *beta, const float *conv_w, void *o, const void *pool_base,

@@ -6,7 +6,9 @@ import pytest
 import torch
 
 import kda_state_chunked_gb300 as kda
+import kv_ref as ref
 import tree_ref as tree
+from kda_cases import write_object
 from test_gpu_kv import DEV, TOL, i32
 from test_gpu_tree import OK, Round, States
 
@@ -156,3 +158,36 @@ def test_millions_of_requests_of_which_two_accept(B):
     assert kda.kda_sync_status(c.status) == OK
     c.check_state(0, [0])
     c.check_state(1, [0, 1])
+
+
+# ------------------------------------------------------------------ products with a state that cancel
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_state_that_cancels(d):
+    """Keys and queries at right angles to what the state holds: the products with it are sums of large terms that come to
+    little.  Element by element, with |.| products of absolute values: bf16 calls take either operand in two bf16 terms (2^-16
+    of it each) and leave out the smallest product (2^-16), and their sums are cut at 2^-23 some 24 times: 4 x 2^-16 of
+    |S|^T |A k| and |S|^T |A q|, the former times beta <q, k>; o's rounding is 2^-8 of it."""
+    B, H, r = 6, 2, np.random.default_rng(59)
+    c = States([1] * B, H=H, d=d, seed=59)
+    c.w[:] = 0
+    c.w[:, :, 3] = 1                                      # the convolution hands the token on
+    bf = lambda x: ref.to_bf16(x.astype(np.float32)).astype(np.float64)  # noqa: E731
+    o = np.zeros((B, H, d))
+    room = np.zeros_like(o)
+    for b in range(B):
+        K, V = r.standard_normal((H, d // 2, d)), 8 * r.standard_normal((H, d // 2, d))
+        S = np.einsum("hmi,hmj->hij", K, V).astype(np.float32)
+        c.S[b][:] = S
+        write_object(c.pool, c.pages[b], c.S[b], c.win[b], "bf16")
+        for h in range(H):
+            free = np.linalg.svd(K[h])[2][d // 2:]        # right angles to all keys
+            c.q[b, h], c.k[b, h] = (bf(r.standard_normal(d // 2) @ free / d ** 0.5) for _ in range(2))
+            q, k, v, a = (x[b, h].astype(np.float64) for x in (c.q, c.k, c.v, c.alpha))
+            beta, S64 = float(c.beta[b, h]), S[h].astype(np.float64)
+            u = beta * (v - S64.T @ (a * k))
+            o[b, h] = S64.T @ (a * q) + (q @ k) * u
+            room[b, h] = (np.abs(S64).T @ np.abs(a * q) + abs(q @ k) * beta * (np.abs(S64).T @ np.abs(a * k))) * 4 * 2.0 ** -16
+    got = c.verify().double().cpu().numpy()
+    assert kda.kda_sync_status(c.status) == OK
+    assert np.abs(o - np.stack([c.expect(b)[0][0] for b in range(B)])).max() <= 1e-12 * np.abs(o).max()
+    assert (np.abs(got - o) <= room + (np.abs(o) + room) * 2.0 ** -8).all()
