@@ -143,11 +143,6 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
     return r;
 }
 
-// Ask a run of memory into L2: 16-byte aligned, bytes a multiple of 16.
-__device__ __forceinline__ void prefetch_bulk(const void *p, uint32_t bytes) {
-    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(reinterpret_cast<uint64_t>(p)), "r"(bytes) : "memory");
-}
-
 // True in one lane of a converged warp.
 __device__ __forceinline__ bool elect() {
     uint32_t p;
@@ -255,7 +250,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
     using L = Lay<D>;
     constexpr int kBlks = D / 64, kRow = kKvRow<FMT, D>;
     // Trees over the 16-bit cache: probabilities in two bf16 terms, 16 bits, side by side in the columns of the scores
-    // that they come from (one term took the outputs from 1.7e-3 off to 2.3e-3; bytes and not products bound these).
+    // that they come from.  A choice of accuracy against time: outputs are 1.7e-3 off, as fp32 probabilities give them, and
+    // 2.3e-3 with one term, which would take 404 us instead of 504 for the ragged contexts above and 177 instead of 205 for
+    // the large trees.
     constexpr bool kTwo = kTree && FMT == KDA_KV_BF16;
     static_assert(NBAR * 8 <= 512, "barriers");
     extern __shared__ uint8_t smem_raw[];
@@ -1035,7 +1032,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                     for (int v = 0; v < 2; ++v)
 #pragma unroll
                         for (int y = 0; y < kRow / kLine; ++y)
-                            prefetch_bulk(rec + v * pt * kRow + y * pt * kLine + now.slot * kLine, 16 * kLine);
+                            ptx::prefetch_bulk(rec + v * pt * kRow + y * pt * kLine + now.slot * kLine, 16 * kLine);
                 }
                 __syncwarp();
                 if (lane % 8 == 0 && k < now.n) ptx::mbar_arrive(&bars[JFULL + (n + k) % kJobs]);

@@ -101,6 +101,11 @@ __device__ __forceinline__ void tma_store_2d(const void *tmap, const void *src, 
                  : "memory");
 }
 
+// Ask a run of memory into L2: 16-byte aligned, bytes a multiple of 16.
+__device__ __forceinline__ void prefetch_bulk(const void *p, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(reinterpret_cast<uint64_t>(p)), "r"(bytes) : "memory");
+}
+
 // Contiguous global -> shared copy (untiled bulk copy), completion counted in bytes on *bar.
 // Both addresses 16-byte aligned, bytes a multiple of 16.
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {

@@ -66,15 +66,9 @@ __device__ __forceinline__ bool pages_lost(const PoolView &pv, const int32_t *pa
     return __syncthreads_or(lost) != 0;
 }
 
-// The convolution's inputs for one draft: packed rows of the three drafts before it on its branch, nearest first, or
-// (negative) window rows: -1 the newest.
+// Channel c of head h in a packed row of a token tensor, es bytes an element.
 __device__ __forceinline__ const uint8_t *raw_at(const VerifyTreeArgs &a, const void *x, int64_t row, int h, int d, int c, int es) {
     return static_cast<const uint8_t *>(x) + ((row * a.H + h) * d + c) * es;
-}
-
-// Ask a run of memory into L2: 16-byte aligned, bytes a multiple of 16.
-__device__ __forceinline__ void prefetch_bulk(const void *p, uint32_t bytes) {
-    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(reinterpret_cast<uint64_t>(p)), "r"(bytes) : "memory");
 }
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
@@ -188,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm<D, T, MT>) verify_tree_kernel
         for (uint64_t i = rec / pb + lane; i * pb < end; i += 32) {
             const int32_t id = __ldg(pages + i);
             const uint64_t from = i * pb > rec ? i * pb : rec, to = (i + 1) * pb < end ? (i + 1) * pb : end;
-            if ((uint32_t)id < (uint32_t)a.pool.num_pages) prefetch_bulk(a.pool.base + (uint64_t)id * pb + (from - i * pb), (uint32_t)(to - from));
+            if ((uint32_t)id < (uint32_t)a.pool.num_pages) ptx::prefetch_bulk(a.pool.base + (uint64_t)id * pb + (from - i * pb), (uint32_t)(to - from));
         }
     }
     for (int i = tid; i < 3 * D; i += kThreads)   // a channel's four taps; eight channels' places in other banks for each eight
@@ -370,7 +364,9 @@ __global__ void __launch_bounds__(kThreads, kPerSm<D, T, MT>) verify_tree_kernel
     // ---- their products with S_0: of A k over k, of A q over alpha
     if constexpr (kMma) {
         // A warp takes 16 columns (two tiles of 8, their columns in turn).  Both operands in two bf16 terms, three of
-        // the four products: 16 bits of either, 2^-8 of an output's own rounding.
+        // the four products: off by 3 x 2^-16 of the terms' absolute sum, below an output's own rounding of 2^-8 unless
+        // the sum cancels to some hundredth of its terms (64 keys in the state, q at right angles to all: outputs 2.2e-3
+        // off, 1.6e-3 by decode steps).  Three terms would be six products.
         constexpr int kCols = D / 16, kSplit = kWarps / kCols;    // d = 64: two warps a 16 columns, each half of the rows
         constexpr int kMine = MT >= kSplit ? MT / kSplit : 1;     // tiles of rows
         const int w = warp % kCols, g = lane / 4, t4 = lane % 4;
@@ -783,7 +779,7 @@ __global__ void __launch_bounds__(kPipeThreads, 1) verify_tree_accept_pipe_kerne
             }
             for (int i = 4 * kSlotTokens + lane; i < 4 * m; i += 32) {   // the other tokens are asked into L2
                 const void *src = i % 4 == 0 ? a.q : i % 4 == 1 ? a.k : i % 4 == 2 ? a.v : a.alpha;
-                prefetch_bulk(static_cast<const bf16 *>(src) + ((r.first + jb.path[i / 4]) * a.H + h) * D, 256);
+                ptx::prefetch_bulk(static_cast<const bf16 *>(src) + ((r.first + jb.path[i / 4]) * a.H + h) * D, 256);
             }
             __syncwarp();
             ++n;
