@@ -544,7 +544,9 @@ int kda_attn_paged(const kda_pool *pool, int32_t Hq, int32_t Hkv, int32_t d, int
 /* Masks and positions of the drafts: bit j of mask[t] (device uint64 [T_tot]) says that the draft of packed
  * row t is draft j or descends from it; pos[t] (device int32 [T_tot]) is kv_len - n + its depth, the tree's
  * roots having depth 0.  A tree with a parent that is none gets pos[t] = -1 and mask[t] = 0 in its rows, but for
- * those whose pos is negative already, which are left as they are.  One launch. */
+ * those whose pos is negative already, which are left as they are.  pos is a token's coordinate where coordinates
+ * are places in the cache.  Behind pictures, or on several axes, the caller forms kda_kv_append_at's [T_tot][axes]
+ * from the depth, pos[t] - (kv_len - n), and leaves a negative pos negative.  One launch. */
 int kda_tree_plan(int32_t nseq, int64_t T_tot, int32_t max_q, const int32_t *cu_q, const int32_t *kv_len,
                   const int32_t *parent, uint64_t *mask, int32_t *pos, int32_t *status_dev, void *stream);
 

@@ -134,6 +134,38 @@ def test_a_captured_round_over_the_8_bit_cache():
         lens = c.new_lens.cpu().numpy()
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+def test_drafts_on_three_axes_behind_pictures(fmt):
+    """Coordinates formed from the plan's depths: the kept branch is the accepted tokens placed by themselves."""
+    starts = [3, 16, 33]
+    c, e = filled(fmt, starts, 60), filled(fmt, starts, 60)
+    c.draft(81, starts)
+    next_free = torch.tensor([[50, 50, 50], [9, 9, 9], [120, 120, 120]], device=DEV)     # behind pictures: not the places
+    sections, x, Hq, Hkv = [c.d // 4, c.d // 8, c.d // 8], c.x, c.Hq, c.Hkv
+    meta, T = (c.cu, c.lens, c.table, c.max_q), int(c.cu_host[-1])
+    seq = torch.repeat_interleave(torch.arange(c.n, device=DEV), torch.tensor(np.diff(c.cu_host), device=DEV))
+    kda.kda_tree_plan(c.cu, c.lens, c.parent, c.max_q, c.mask, c.pos, c.status)
+    depth = c.pos[:T] - torch.tensor(starts, device=DEV)[seq]
+    coords = torch.zeros(c.T, 3, dtype=torch.int32, device=DEV)
+    coords[:T] = torch.where(c.pos[:T, None] < 0, -1, next_free[seq] + depth[:, None]).int()
+    kda.kda_kv_append_at(c.pool, fmt, c.pt, *meta, x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], c.cs, coords, sections, c.q, c.status)
+    kda.kda_kv_accept(c.pool, Hkv, c.d, fmt, c.pt, *meta, c.path, c.accepted, c.new_lens, c.status)
+    lens = [a + len(p) for a, p in zip(starts, c.paths)]
+    rows = torch.tensor([c.cu_host[s] + i for s, p in enumerate(c.paths) for i in p], device=DEV)
+    at = torch.tensor([[int(next_free[s, 0]) + i] * 3 for s, p in enumerate(c.paths) for i in range(len(p))], device=DEV)
+    y, q = x[rows], torch.empty(len(rows), Hq, c.d, dtype=x.dtype, device=DEV)
+    cu = i32(np.concatenate([[0], np.cumsum([len(p) for p in c.paths])]))
+    kda.kda_kv_append_at(e.pool, fmt, e.pt, cu, i32(lens), e.table, e.max_q, y[:, :Hq], y[:, Hq:Hq + Hkv], y[:, Hq + Hkv:], e.cs,
+                         at.int(), sections, q, e.status)
+    assert kda.kda_sync_status(c.status) == OK and kda.kda_sync_status(e.status) == OK
+    assert c.new_lens.tolist() == lens and torch.equal(c.q[rows], q)
+    for a, b in zip(c.cached(lens), e.cached(lens)):
+        if fmt == kda.KDA_KV_BF16:
+            assert torch.equal(a, b)
+        else:                          # each side codes a block anew at most twice: steps of max / 127, rounded by half
+            assert ((a - b).abs() <= 2 * b.abs().max() / 127).all()
+
+
 # ------------------------------------------------------------------ the state after long branches
 @pytest.mark.parametrize("page_bytes", [65536, 1 << 20])
 def test_branches_of_every_length(page_bytes):
