@@ -1,8 +1,8 @@
 // Trees of drafts in the key/value cache: the plan of a tree, and keeping its accepted branch.
 //
 // Both are bound by latency: a plan reads a word a draft, a branch is some rows of a few blocks.  Keeping the branches of
-// 256 requests (1 to 64 drafts, 8 heads of 128, 8-bit) and reading their blocks back takes 31 us, one request's 15 us, of
-// which the host side of the two calls is 14.
+// 256 requests (1 to 64 drafts, 8 heads of 128) takes 11.3 us over the 8-bit cache and 7.1 over the 16-bit one, one request's
+// 2.9 us; a plan 2.6 to 2.9.
 #include "kv_common.cuh"
 
 namespace kda {

@@ -656,7 +656,7 @@ __global__ void __launch_bounds__(kAccThreads, 2) verify_tree_accept_kernel(cons
 // The same for bf16 records of d = 128 in pages of at least 64 KiB, as a pipeline of bulk copies: one CTA an SM, three
 // slots of a record and its tokens; a warp looks branches up and copies records in and out, sixteen warps advance the
 // state of the one between, a thread 32 rows of a column in registers over the whole branch.  Measured: 256 requests x 32
-// heads, branches of 2.5 tokens (214 requests accept some): 216 us, 0.95 GB moved, 65% of the copy rate (339 us by the
+// heads, branches of 2.5 tokens (214 requests accept some): 211 us, 0.95 GB moved, 66% of the copy rate (339 us by the
 // kernel above); a job's meetings of sixteen warps, two a token, bound it.  8192 branches of 1, 4, 8, 16 and 64 tokens each:
 // 229, 270, 428, 860 and 3504 us (kernel above: 300, 461, 655, 1038 and 3619).
 // Taken for any number of (request, head) pairs up to kPipeMost.  With few pairs it is the faster one too, a token's step
